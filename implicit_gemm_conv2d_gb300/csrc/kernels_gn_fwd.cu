@@ -1,0 +1,492 @@
+// kernels_gn_fwd.cu -- group norm with an activation, forward:
+//   mean = sum x / M,  rstd = 1 / sqrt(sum (x - mean)^2 / M + eps),
+//   y = act((x - mean) * rstd * gamma[c] + beta[c]).
+//
+// About ten operations a value against 2 (bf16) or 4 bytes in and out: bound by memory, so what
+// counts is to read x once.  A group that fits a team of threads is held in its registers: the
+// sum, then the squares about the mean, then the result, one read and one write.  Larger groups
+// are cut into pieces whose (mean, sum of squares about it) partials are combined by Chan,
+// Golub & LeVeque's update ("Updating formulae and a pairwise algorithm for computing sample
+// variances", 1979), and a second pass applies them.  No path subtracts a squared mean from a
+// mean of squares, so a large common offset costs no digits.
+#include "gn_common.cuh"
+
+namespace igc {
+
+GnTeam gn_team(const GnParams& p, int dt, const DevInfo& d, bool bwd)
+{
+    GnTeam q = {};
+    const int es = dt == DT_F32 ? 4 : 2;
+    q.V = gn_vector_width(p, es);
+    const int64_t nvec = p.M / q.V;
+    if (p.M > int64_t(GN_TEAM_MAX) * GN_LANE_VALUES || (p.layout == CONV_LAYOUT_NHWC && p.M > 512 && p.Cg * es < 32))
+        return q;
+    // Lanes and vectors a lane: the fewest instructions a value, counting the idle lanes, the
+    // butterfly steps (two sums a group) and a fixed cost an iteration.
+    double best = 1e30;
+    for (int K = 1; K * q.V <= GN_LANE_VALUES; ++K) {
+        if (!gn_team_k(q.V, K)) continue;
+        const int64_t need = (nvec + K - 1) / K;
+        int L = 1, steps = 0;
+        while (L < need && L < 32) { L *= 2; ++steps; }
+        if (L < need) {
+            L = int((need + 31) / 32) * 32;
+            steps = 5 + 8;
+        }
+        if (L > GN_TEAM_MAX) continue;
+        const double cost = double(L) * (12.0 * K * q.V + 4.0 * steps + 20.0);
+        if (cost < best) { best = cost; q.K = K; q.L = L; }
+    }
+    if (best == 1e30) return q;
+    if (q.L > 32) {
+        q.gpc = q.spc = 1;
+        q.threads = q.L;
+    } else {
+        const int teams = GN_THREADS / q.L;
+        q.gpc = std::min(p.G, teams);
+        q.spc = std::max(1, std::min(teams / q.gpc, std::max(1, p.B)));
+        q.threads = round_up(q.gpc * q.spc * q.L, 32);
+    }
+    q.gsets = ceil_div(p.G, q.gpc);
+    const int per_sm = std::max(1, (bwd ? 768 : 1024) / q.threads);
+    const int want = std::max(1, d.sms * per_sm / q.gsets);
+    q.chunks = std::min(ceil_div(std::max(1, p.B), q.spc), want);
+    q.ok = true;
+    return q;
+}
+
+GnPieces gn_pieces(const GnParams& p, int dt, const DevInfo& d)
+{
+    GnPieces q = {};
+    const int es = dt == DT_F32 ? 4 : 2;
+    q.threads = 256;
+    int v = 16 / es;
+    const int n = p.layout == CONV_LAYOUT_NHWC ? p.C : p.P;
+    while (v > 1 && n % v != 0) v /= 2;
+    q.V = v;
+    const int U = 4;  // rows (vectors) a thread merges at a time
+    if (p.layout == CONV_LAYOUT_NHWC) {
+        const int ncv = p.C / v;
+        q.wins = ceil_div(ncv, q.threads);
+        q.cols = ceil_div(ncv, q.wins);
+        q.wins = ceil_div(ncv, q.cols);
+        const int lanes = std::max(1, q.threads / q.cols);
+        // four passes of U rows a lane while that leaves enough pieces for the SMs
+        int len = lanes * U * 4;
+        while (len > lanes * U && int64_t(p.B) * q.wins * ceil_div(p.P, len) < 4 * d.sms) len /= 2;
+        q.len = std::min(len, p.P);
+    } else {
+        q.wins = q.cols = 1;
+        int len = q.threads * U * v * 2;
+        while (len > q.threads * v && int64_t(p.B) * p.C * ceil_div(p.P, len) < 4 * d.sms) len /= 2;
+        q.len = std::min(len, p.P);
+        // rows of at most U vectors a lane of a warp: a warp each, eight rows a block
+        q.row_lanes = p.P <= 32 * U * v ? 32 : q.threads;
+        if (q.row_lanes == 32) q.len = p.P;
+    }
+    q.pieces = ceil_div(p.P, q.len);
+    q.blocks = p.layout == CONV_LAYOUT_NHWC
+                   ? int64_t(p.B) * q.pieces * q.wins
+                   : (int64_t(p.B) * p.C * q.pieces + q.threads / q.row_lanes - 1) / (q.threads / q.row_lanes);
+    return q;
+}
+
+namespace {
+
+// ---- small groups ----------------------------------------------------------------------------
+template <typename T, int V, int K, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? GN_TEAM_MAX : GN_THREADS, WIDE ? 1 : 2)
+gn_team_fwd(const GnParams p, const GnTeam q, const T* x, const T* gamma, const T* beta, T* y, float* mean_out,
+            float* rstd_out)
+{
+    __shared__ float sm[64];
+    int turn = 0;
+    const int L = q.L;
+    const int ti = WIDE ? 0 : int(threadIdx.x) / L, lane = WIDE ? int(threadIdx.x) : int(threadIdx.x) % L;
+    const int gi = ti % q.gpc, si = ti / q.gpc;
+    const int g = int(blockIdx.x) % q.gsets * q.gpc + gi, chunk = int(blockIdx.x) / q.gsets;
+    const bool active = si < q.spc && g < p.G;
+    const int nvec = int(p.M / V), cgv = p.Cg / V;
+    int off[K];
+    bool has[K];
+    float ga[K * V], be[K * V];
+    tc::grid_dep_wait();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int j = lane + k * L;
+        has[k] = active && j < nvec;
+        const int row = p.layout == CONV_LAYOUT_NHWC ? j / cgv : 0;
+        off[k] = p.layout == CONV_LAYOUT_NHWC ? row * p.C + g * p.Cg + (j - row * cgv) * V : int(g * p.M) + j * V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = g * p.Cg + (p.layout == CONV_LAYOUT_NHWC ? (j - row * cgv) * V + i : (j * V + i) / p.P);
+            ga[k * V + i] = has[k] && gamma ? Elem<T>::ldg(gamma + c) : 1.f;
+            be[k * V + i] = has[k] && beta ? Elem<T>::ldg(beta + c) : 0.f;
+        }
+    }
+    const int step = q.chunks * q.spc;
+    const int b0 = chunk * q.spc + si;
+    const int iters = ceil_div(p.B - chunk * q.spc, step);
+    Vec<T, V> cur[K], nxt[K];
+    auto fetch = [&](Vec<T, V>(&v)[K], int b) {
+        const T* px = x + int64_t(b) * p.N;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (has[k] && b < p.B) v[k].load(px + off[k]);
+            else v[k].zero();
+        }
+    };
+    fetch(cur, b0);
+    for (int it = 0; it < iters; ++it) {
+        const int b = b0 + it * step;
+        if (it + 1 < iters) fetch(nxt, b + step);
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) s += cur[k].get(i);
+        const float mean = __fdiv_rn(team_total<WIDE>(s, L, sm, turn), p.m);  // exact for equal values
+        float m2 = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (has[k])
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float dlt = cur[k].get(i) - mean;
+                    m2 += dlt * dlt;
+                }
+        const float rstd = rsqrtf(team_total<WIDE>(m2, L, sm, turn) * p.inv_m + p.eps);
+        if (active && b < p.B) {
+            T* py = y + int64_t(b) * p.N;
+            with_act(p.act, [&](auto act) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    float r[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        r[i] = act_value<act.value>(gn_z(gn_xhat(cur[k].get(i), mean, rstd), ga[k * V + i], be[k * V + i]));
+                    Vec<T, V> o;
+                    o.set(r);
+                    if (has[k]) o.store(py + off[k]);
+                }
+            });
+            if (lane == 0 && mean_out) {
+                mean_out[int64_t(b) * p.G + g] = mean;
+                rstd_out[int64_t(b) * p.G + g] = rstd;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) cur[k] = nxt[k];
+    }
+}
+
+// ---- large groups ----------------------------------------------------------------------------
+// A running (mean, M2) over n values, and the merge of another (n2, mean2, m22).
+__device__ __forceinline__ void chan_merge(float& n, float& mean, float& m2, float n2, float mean2, float m22)
+{
+    const float t = n + n2;
+    if (n2 == 0.f) return;
+    const float dlt = mean2 - mean, w = __fdividef(n2, t);
+    mean += dlt * w;
+    m2 += m22 + dlt * dlt * n * w;
+    n = t;
+}
+
+// NHWC: block (piece, sample, window); thread (row lane, column vector).  Each thread merges U
+// rows at a time into its V columns' statistics, the row lanes are merged in ascending order.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) gn_stats_nhwc(const GnParams p, const GnPieces q, const T* x, float* pmean,
+                                                     float* pm2)
+{
+    constexpr int U = 4;
+    __shared__ float sm_mean[256 * V], sm_m2[256 * V];
+    const GnTile t(p, q, V, blockIdx.x);
+    const int lanes = t.lanes, r0 = t.r0, r1 = t.r1;
+    float mean[V], m2[V], n = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) mean[i] = m2[i] = 0.f;
+    tc::grid_dep_wait();
+    if (t.in()) {
+        const T* px = x + int64_t(t.b) * p.N + int64_t(t.cv0 + t.col) * V;
+        for (int r = r0 + t.lane; r < r1; r += lanes * U) {
+            Vec<T, V> v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (r + u * lanes < r1) v[u].load(px + int64_t(r + u * lanes) * p.C);
+                else v[u].zero();
+            }
+            const int cnt = min(U, (r1 - r + lanes - 1) / lanes);
+            const float fc = float(cnt);
+            const float tot = n + fc, w = __fdividef(fc, tot), nw = n * w;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float s = 0.f, sq = 0.f;
+#pragma unroll
+                for (int u = 0; u < U; ++u) s += v[u].get(i);
+                const float mu = cnt == U ? s * (1.f / U) : __fdiv_rn(s, fc);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const float dlt = u < cnt ? v[u].get(i) - mu : 0.f;
+                    sq += dlt * dlt;
+                }
+                const float dm = mu - mean[i];
+                mean[i] += dm * w;
+                m2[i] += sq + dm * dm * nw;
+            }
+            n = tot;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            sm_mean[(t.lane * q.cols + t.col) * V + i] = mean[i];
+            sm_m2[(t.lane * q.cols + t.col) * V + i] = m2[i];
+        }
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < t.cols * V; c += blockDim.x) {
+        float an = 0.f, am = 0.f, aq = 0.f;
+        for (int l = 0; l < lanes; ++l) {
+            const int cnt = r1 - r0 > l ? (r1 - r0 - l + lanes - 1) / lanes : 0;
+            chan_merge(an, am, aq, float(cnt), sm_mean[l * q.cols * V + c], sm_m2[l * q.cols * V + c]);
+        }
+        const int64_t o = gn_part(p, q.pieces, t.b, t.cv0 * V + c, t.pc);
+        pmean[o] = am;
+        pm2[o] = aq;
+    }
+}
+
+// NCHW: a block (or a warp) a row's piece.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) gn_stats_nchw(const GnParams p, const GnPieces q, const T* x, float* pmean,
+                                                     float* pm2)
+{
+    constexpr int U = 4;
+    __shared__ float sm[8][3];
+    const GnRow t(p, q, V, blockIdx.x);
+    const T* px = x + t.row * p.P;
+    float n = 0.f, mean = 0.f, m2 = 0.f;
+    tc::grid_dep_wait();
+    for (int e = t.e0; e < t.e1; e += t.hop * U) {
+        Vec<T, V> v[U];
+        int cnt = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (e + u * t.hop < t.e1) { v[u].load(px + e + u * t.hop); cnt += V; }
+            else v[u].zero();
+        }
+        float s = 0.f, sq = 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < V; ++i) s += v[u].get(i);
+        const float mu = __fdiv_rn(s, float(cnt));
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float dlt = u * V < cnt ? v[u].get(i) - mu : 0.f;
+                sq += dlt * dlt;
+            }
+        chan_merge(n, mean, m2, float(cnt), mu, sq);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float n2 = __shfl_down_sync(0xFFFFFFFFu, n, o), mean2 = __shfl_down_sync(0xFFFFFFFFu, mean, o),
+                    m22 = __shfl_down_sync(0xFFFFFFFFu, m2, o);
+        chan_merge(n, mean, m2, n2, mean2, m22);
+    }
+    if (q.row_lanes > 32) {
+        if ((threadIdx.x & 31) == 0) {
+            sm[threadIdx.x >> 5][0] = n;
+            sm[threadIdx.x >> 5][1] = mean;
+            sm[threadIdx.x >> 5][2] = m2;
+        }
+        __syncthreads();
+        if (t.lane == 0)
+            for (int w = 1; w < q.row_lanes / 32; ++w) chan_merge(n, mean, m2, sm[w][0], sm[w][1], sm[w][2]);
+    }
+    if (t.lane == 0 && t.in) {
+        pmean[t.row * q.pieces + t.pc] = mean;
+        pm2[t.row * q.pieces + t.pc] = m2;
+    }
+}
+
+// One block a group: the mean from the pieces' means, then the squares about it.
+__global__ void __launch_bounds__(128) gn_combine(const GnParams p, const GnPieces q, const float* pmean,
+                                                  const float* pm2, float* mean, float* rstd, float* mean_out,
+                                                  float* rstd_out)
+{
+    __shared__ float sm[64];
+    int turn = 0;
+    const int b = int(blockIdx.x / p.G), g = int(blockIdx.x % p.G);
+    const int np = p.Cg * q.pieces;
+    tc::grid_dep_wait();
+    float s = 0.f;
+    auto at = [&](int i, int& cnt) {
+        const int cl = p.layout == CONV_LAYOUT_NHWC ? i % p.Cg : i / q.pieces;
+        const int pc = p.layout == CONV_LAYOUT_NHWC ? i / p.Cg : i % q.pieces;
+        cnt = min(q.len, p.P - pc * q.len);
+        return gn_part(p, q.pieces, b, g * p.Cg + cl, pc);
+    };
+    for (int i = threadIdx.x; i < np; i += blockDim.x) {
+        int cnt;
+        const int64_t o = at(i, cnt);
+        s += pmean[o] * float(cnt);
+    }
+    const float mu = __fdiv_rn(team_total<true>(s, blockDim.x, sm, turn), p.m);
+    float v = 0.f;
+    for (int i = threadIdx.x; i < np; i += blockDim.x) {
+        int cnt;
+        const int64_t o = at(i, cnt);
+        const float dlt = pmean[o] - mu;
+        v += pm2[o] + dlt * dlt * float(cnt);
+    }
+    const float r = rsqrtf(team_total<true>(v, blockDim.x, sm, turn) * p.inv_m + p.eps);
+    if (threadIdx.x == 0) {
+        mean[blockIdx.x] = mu;
+        rstd[blockIdx.x] = r;
+        if (mean_out) {
+            mean_out[blockIdx.x] = mu;
+            rstd_out[blockIdx.x] = r;
+        }
+    }
+}
+
+// The second pass walks the pieces backwards: the first pass's last pieces are still in L2.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) gn_apply_nhwc(const GnParams p, const GnPieces q, const T* x, const T* gamma,
+                                                     const T* beta, T* y, const float* mean, const float* rstd)
+{
+    constexpr int U = 4;
+    const GnTile t(p, q, V, q.blocks - 1 - blockIdx.x);
+    const int lanes = t.lanes, r1 = t.r1;
+    float mu[V], rs[V], ga[V], be[V];
+    tc::grid_dep_wait();
+    if (!t.in()) return;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = (t.cv0 + t.col) * V + i;
+        const int64_t o = int64_t(t.b) * p.G + c / p.Cg;
+        mu[i] = mean[o];
+        rs[i] = rstd[o];
+        ga[i] = gamma ? Elem<T>::ldg(gamma + c) : 1.f;
+        be[i] = beta ? Elem<T>::ldg(beta + c) : 0.f;
+    }
+    const int64_t base = int64_t(t.b) * p.N + int64_t(t.cv0 + t.col) * V;
+    with_act(p.act, [&](auto act) {
+        for (int r = t.r0 + t.lane; r < r1; r += lanes * U) {
+            Vec<T, V> v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (r + u * lanes < r1) v[u].load(x + base + int64_t(r + u * lanes) * p.C);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (r + u * lanes < r1) {
+                    float o[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        o[i] = act_value<act.value>(gn_z(gn_xhat(v[u].get(i), mu[i], rs[i]), ga[i], be[i]));
+                    v[u].set(o);
+                    v[u].store(y + base + int64_t(r + u * lanes) * p.C);
+                }
+        }
+    });
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(256) gn_apply_nchw(const GnParams p, const GnPieces q, const T* x, const T* gamma,
+                                                     const T* beta, T* y, const float* mean, const float* rstd)
+{
+    constexpr int U = 4;
+    const GnRow t(p, q, V, q.blocks - 1 - blockIdx.x);
+    tc::grid_dep_wait();
+    if (!t.in) return;
+    const int c = int(t.row % p.C);
+    const int64_t grp = t.row / p.C * p.G + c / p.Cg;
+    const float mu = mean[grp], rs = rstd[grp];
+    const float ga = gamma ? Elem<T>::ldg(gamma + c) : 1.f, be = beta ? Elem<T>::ldg(beta + c) : 0.f;
+    const T* px = x + t.row * p.P;
+    T* py = y + t.row * p.P;
+    with_act(p.act, [&](auto act) {
+        for (int e = t.e0; e < t.e1; e += t.hop * U) {
+            Vec<T, V> v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (e + u * t.hop < t.e1) v[u].load(px + e + u * t.hop);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (e + u * t.hop < t.e1) {
+                    float o[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) o[i] = act_value<act.value>(gn_z(gn_xhat(v[u].get(i), mu, rs), ga, be));
+                    v[u].set(o);
+                    v[u].store(py + e + u * t.hop);
+                }
+        }
+    });
+}
+
+template <typename T>
+cudaError_t fwd_t(const GnParams& p, int dt, const DevInfo& d, const T* x, const T* gamma, const T* beta, T* y,
+                  float* mean, float* rstd, void* ws, cudaStream_t s)
+{
+    cudaError_t e = cudaSuccess;
+    const GnTeam t = gn_team(p, dt, d, false);
+    if (t.ok) {
+        const GnTeam& q = t;
+        const dim3 grid(unsigned(q.gsets) * unsigned(q.chunks)), block(q.threads);
+#define GN_CALL(T_, V_, K_)                                                                                           \
+    e = q.L > 32 ? launch_ex(gn_team_fwd<T_, V_, K_, true>, grid, block, 0, s, 1, true, p, q, x, gamma, beta, y,       \
+                             mean, rstd)                                                                              \
+                 : launch_ex(gn_team_fwd<T_, V_, K_, false>, grid, block, 0, s, 1, true, p, q, x, gamma, beta, y,      \
+                             mean, rstd)
+        GN_DISPATCH_TEAM(T, GN_CALL);
+#undef GN_CALL
+        return e != cudaSuccess ? e : cudaGetLastError();
+    }
+    const GnPieces q = gn_pieces(p, dt, d);
+    const int64_t np = int64_t(p.B) * p.C * q.pieces;
+    float* pmean = static_cast<float*>(ws);
+    float* pm2 = pmean + np;
+    float* mu = pm2 + np;
+    float* rs = mu + int64_t(p.B) * p.G;
+    const bool nhwc = p.layout == CONV_LAYOUT_NHWC;
+    const dim3 grid(static_cast<unsigned>(q.blocks));
+#define GN_CALL(T_, V_)                                                                                               \
+    e = nhwc ? launch_ex(gn_stats_nhwc<T_, V_>, grid, dim3(q.threads), 0, s, 1, true, p, q, x, pmean, pm2)            \
+             : launch_ex(gn_stats_nchw<T_, V_>, grid, dim3(q.threads), 0, s, 1, true, p, q, x, pmean, pm2)
+    GN_DISPATCH_V(T, q.V, GN_CALL);
+#undef GN_CALL
+    if (e != cudaSuccess) return e;
+    e = launch_ex(gn_combine, dim3(unsigned(p.B) * unsigned(p.G)), dim3(128), 0, s, 1, true, p, q,
+                  static_cast<const float*>(pmean), static_cast<const float*>(pm2), mu, rs, mean, rstd);
+    if (e != cudaSuccess) return e;
+#define GN_CALL(T_, V_)                                                                                               \
+    e = nhwc ? launch_ex(gn_apply_nhwc<T_, V_>, grid, dim3(q.threads), 0, s, 1, true, p, q, x, gamma, beta, y,        \
+                         static_cast<const float*>(mu), static_cast<const float*>(rs))                                \
+             : launch_ex(gn_apply_nchw<T_, V_>, grid, dim3(q.threads), 0, s, 1, true, p, q, x, gamma, beta, y,        \
+                         static_cast<const float*>(mu), static_cast<const float*>(rs))
+    GN_DISPATCH_V(T, q.V, GN_CALL);
+#undef GN_CALL
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+size_t gn_fwd_workspace(const GnParams& p, int dt, const DevInfo& d)
+{
+    if (p.B == 0 || gn_team(p, dt, d, false).ok) return 0;
+    const GnPieces q = gn_pieces(p, dt, d);
+    return size_t(4) * (2 * size_t(p.B) * p.C * q.pieces + 2 * size_t(p.B) * p.G);
+}
+
+cudaError_t run_gn_fwd(const GnParams& p, int dt, const DevInfo& d, const void* x, const void* gamma,
+                       const void* beta, void* y, float* mean, float* rstd, void* ws, cudaStream_t s)
+{
+    if (dt == DT_F32)
+        return fwd_t<float>(p, dt, d, (const float*)x, (const float*)gamma, (const float*)beta, (float*)y, mean, rstd,
+                            ws, s);
+    using H = __nv_bfloat16;
+    return fwd_t<H>(p, dt, d, (const H*)x, (const H*)gamma, (const H*)beta, (H*)y, mean, rstd, ws, s);
+}
+
+}  // namespace igc
