@@ -40,10 +40,9 @@ __device__ __forceinline__ float gn_z(float xhat, float gamma, float beta)
 }
 
 // dz = dy * act'(z); a ReLU that is off passes nothing, whatever dy holds there.
-template <int ACT> __device__ __forceinline__ float gn_dz(float dy, float xhat, float gamma, float beta)
+template <int ACT> __device__ __forceinline__ float gn_dz(float dy, float z)
 {
     if constexpr (ACT == CONV_ACT_NONE) return dy;
-    const float z = gn_z(xhat, gamma, beta);
     if constexpr (ACT == CONV_ACT_RELU) return z > 0.f ? dy : 0.f;
     return dy * act_slope<ACT>(z);
 }
@@ -59,62 +58,116 @@ template <class F> __device__ __forceinline__ void with_act(int act, F&& f)
     }
 }
 
-// ---- small groups: a team of threads holds a group in registers ------------------------------
-// A team is L lanes (a power of two within a warp, or a whole block of 32*W threads); lane l
-// holds the group's vectors l, l + L, ... (K of V values).  A block has gpc teams side by side
-// on consecutive groups, spc such rows on consecutive samples, and walks the samples with its
-// groups fixed: a lane's offsets in the sample, its gamma and beta and (backward) its channel
-// sums stay in registers.
-constexpr int GN_THREADS = 256;       // block of sub-warp teams
-constexpr int GN_TEAM_MAX = 512;      // lanes of a block-wide team
-constexpr int GN_LANE_VALUES = 16;    // values a lane holds at most
+// ---- small groups: a team of lanes holds a group in registers --------------------------------
+// A team is L lanes of a warp (a power of two); lane l holds the group's vectors l, l + L, ...
+// (K of V values, E = K*V).  A block has gpc teams side by side on consecutive groups, spc such
+// rows on consecutive samples, and walks the samples with its groups fixed, so that a lane's
+// offsets in the sample and (backward) its channel sums stay in registers.  Gamma and beta lie
+// in shared memory by position, in the order the lanes read them.
+constexpr int GN_THREADS = 256;
+constexpr int GN_FWD_VALUES = 16;     // values a lane holds at most
+constexpr int GN_BWD_VALUES = 12;     // the backward also keeps two sums a value
 
 struct GnTeam {
     int V, K, L;
     int gpc, spc, gsets, chunks;      // grid = gsets * chunks
     int threads;
     bool ok;
+    FastDivmod dm_cgv, dm_p, dm_cg, dm_m;
 };
+GnTeam gn_team(const GnParams& p, int dt, const DevInfo& d, bool bwd);
 
-inline int gn_vector_width(const GnParams& p, int es)
-{
-    // the widest vector (16 bytes at most) that keeps every group's vectors aligned and whole
-    const int64_t n = p.layout == CONV_LAYOUT_NCHW ? p.M : p.Cg;
-    int v = 16 / es;
-    while (v > 1 && n % v != 0) v /= 2;
-    return v;
-}
-
-// K variants that are compiled for each V.
-inline bool gn_team_k(int V, int K)
+// Vectors a lane (K) that are compiled for each width.
+inline bool gn_team_k(int V, int K, bool bwd)
 {
     switch (V) {
-        case 8: return K == 1 || K == 2;
-        case 4: return K >= 1 && K <= 4;
-        case 2: return K == 2 || K == 4 || K == 8;
-        default: return K == 2 || K == 4 || K == 8 || K == 16;
+        case 8: return K == 1 || (K == 2 && !bwd);
+        case 4: return K >= 1 && K <= (bwd ? 3 : 4);
+        case 2: return K == 2 || K == 4 || (K == 8 && !bwd);
+        default: return K == 2 || K == 4 || K == 8;
     }
 }
 
-GnTeam gn_team(const GnParams& p, int dt, const DevInfo& d, bool bwd);
-
-// Sum over a block-wide team (or a sub-warp one), the same value in every lane.  `sm` holds 64
-// floats; `turn` alternates its halves so that one barrier a call is enough.
-template <bool WIDE> __device__ __forceinline__ float team_total(float v, int L, float* sm, int& turn)
+// Offset of the group's vector j in the sample.
+__device__ __forceinline__ int gn_offset(const GnParams& p, const GnTeam& q, int g, int j)
 {
-    if constexpr (!WIDE) return team_sum(v, L);
+    if (p.layout == CONV_LAYOUT_NCHW) return int(g * p.M) + j * q.V;
+    uint32_t row, cv;
+    q.dm_cgv.divmod(uint32_t(j), row, cv);
+    return int(row) * p.C + g * p.Cg + int(cv) * q.V;
+}
+// Channel (within the group) of the group's value e, counted in the order of the vectors.
+__device__ __forceinline__ int gn_channel(const GnParams& p, const GnTeam& q, int e)
+{
+    uint32_t a, b;
+    if (p.layout == CONV_LAYOUT_NCHW) return int(q.dm_p.div(uint32_t(e)));
+    q.dm_cg.divmod(uint32_t(e), a, b);
+    return int(b);
+}
+// Gamma and beta of the block's groups by position: gam[gpc * M], bet[gpc * M].
+template <typename T>
+__device__ __forceinline__ void gn_team_tables(const GnParams& p, const GnTeam& q, int g0, const T* gamma,
+                                               const T* beta, float* gam, float* bet)
+{
+    const int m = int(p.M), n = min(q.gpc, p.G - g0) * m;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        uint32_t gi, e;
+        q.dm_m.divmod(uint32_t(i), gi, e);
+        const int c = (g0 + int(gi)) * p.Cg + gn_channel(p, q, int(e));
+        gam[i] = gamma ? Elem<T>::ldg(gamma + c) : 1.f;
+        bet[i] = beta ? Elem<T>::ldg(beta + c) : 0.f;
+    }
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+// Value pair h of K vectors of V values.
+template <typename T, int V, int K> __device__ __forceinline__ float2 pair_of(const Vec<T, V> (&v)[K], int h)
+{
+    return make_float2(v[2 * h / V].get(2 * h % V), v[(2 * h + 1) / V].get((2 * h + 1) % V));
+}
+// Pair h of a lane's table entries; toff[k]: where vector k's V floats begin.
+template <int V, int K> __device__ __forceinline__ float2 table_pair(const float* tab, const int (&toff)[K], int h)
+{
+    if constexpr (V == 1) return make_float2(tab[toff[2 * h]], tab[toff[2 * h + 1]]);
+    else return *reinterpret_cast<const float2*>(tab + toff[2 * h / V] + 2 * h % V);
+}
+
+// Sum over the block, the same value in every thread.  `sm` holds 64 floats; `turn` alternates
+// its halves so that one barrier a call is enough.
+__device__ __forceinline__ float block_total(float v, float* sm, int& turn)
+{
     v = warp_sum(v);
     float* half = sm + (turn & 1) * 32;
     ++turn;
     if ((threadIdx.x & 31) == 0) half[threadIdx.x >> 5] = v;
     __syncthreads();
-    const int nw = L >> 5;
+    const int nw = int(blockDim.x) >> 5;
     float t = 0.f;
     for (int w = 0; w < nw; ++w) t += half[w];
     return t;
 }
 
-// ---- large groups: pieces of rows ------------------------------------------------------------
+// ---- large groups kept on chip by a cluster (kernels_gn_cluster.cu) --------------------------
+struct GnCluster {
+    int V, S, threads, K;        // vector width, blocks a cluster, threads, slots a thread
+    int W, cols, lanes, groups;  // NHWC: channels, vectors and groups of a window, rows side by side
+    int wins;                    // units a sample
+    int Cg, smem;
+    bool nhwc, ok;
+};
+GnCluster gn_cluster(const GnParams& p, int dt, const DevInfo& d, bool bwd);
+cudaError_t run_gn_cluster_fwd(const GnParams& p, const GnCluster& q, int dt, const void* x, const void* gamma,
+                               const void* beta, void* y, float* mean, float* rstd, cudaStream_t s);
+// part: (B, 2, C) channel sums (dgamma's, dbeta's), or NULL.
+cudaError_t run_gn_cluster_bwd(const GnParams& p, const GnCluster& q, int dt, const void* x, const void* dy,
+                               const void* gamma, const void* beta, const float* mean, const float* rstd, void* dx,
+                               float* part, cudaStream_t s);
+
+// ---- groups that no cluster holds: pieces of rows --------------------------------------------
 // NHWC: a piece is a range of a sample's positions, all channels of a column window; NCHW: a
 // range of one channel's positions.  `pieces` a sample (a channel), `len` positions each.
 struct GnPieces {
@@ -165,35 +218,37 @@ struct GnRow {
     }
 };
 
-// Index of the partial of (sample, channel, piece).
-__device__ __forceinline__ int64_t gn_part(const GnParams& p, int pieces, int b, int c, int pc)
+// Index of the partial of (sample, piece, channel).
+__device__ __forceinline__ int64_t gn_part(const GnParams& p, int pieces, int64_t b, int c, int pc)
 {
-    return p.layout == CONV_LAYOUT_NHWC ? (int64_t(b) * pieces + pc) * p.C + c
-                                        : (int64_t(b) * p.C + c) * pieces + pc;
+    return (b * pieces + pc) * p.C + c;
 }
 
-#define GN_DISPATCH_TEAM(T, CALL)                                      \
+// The compiled (V, K); MORE: those of the forward only.
+#define GN_DISPATCH_TEAM(T, MORE, CALL)                                \
     do {                                                               \
         if constexpr (sizeof(T) == 2)                                  \
             if (q.V == 8) {                                            \
-                if (q.K == 1) { CALL(T, 8, 1); }                       \
-                else { CALL(T, 8, 2); }                                \
+                if constexpr (MORE)                                    \
+                    if (q.K == 2) { CALL(T, 8, 2); break; }            \
+                CALL(T, 8, 1);                                         \
                 break;                                                 \
             }                                                          \
         if (q.V == 4) {                                                \
+            if constexpr (MORE)                                        \
+                if (q.K == 4) { CALL(T, 4, 4); break; }                \
             if (q.K == 1) { CALL(T, 4, 1); }                           \
             else if (q.K == 2) { CALL(T, 4, 2); }                      \
-            else if (q.K == 3) { CALL(T, 4, 3); }                      \
-            else { CALL(T, 4, 4); }                                    \
+            else { CALL(T, 4, 3); }                                    \
         } else if (q.V == 2) {                                         \
+            if constexpr (MORE)                                        \
+                if (q.K == 8) { CALL(T, 2, 8); break; }                \
             if (q.K == 2) { CALL(T, 2, 2); }                           \
-            else if (q.K == 4) { CALL(T, 2, 4); }                      \
-            else { CALL(T, 2, 8); }                                    \
+            else { CALL(T, 2, 4); }                                    \
         } else {                                                       \
             if (q.K == 2) { CALL(T, 1, 2); }                           \
             else if (q.K == 4) { CALL(T, 1, 4); }                      \
-            else if (q.K == 8) { CALL(T, 1, 8); }                      \
-            else { CALL(T, 1, 16); }                                   \
+            else { CALL(T, 1, 8); }                                    \
         }                                                              \
     } while (0)
 

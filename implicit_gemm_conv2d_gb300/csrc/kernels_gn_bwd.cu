@@ -6,7 +6,7 @@
 // x and dy in, dx out: bound by memory like the forward, and split the same way.  A group that
 // fits a team is read once into registers; a lane keeps the channel sums of its own positions
 // over all the samples its team walks, and a block adds them per channel once, at its end.
-// Larger groups take a pass for the channels' sums (which give the group's m1 and m2 too:
+// Larger groups are held by a cluster (kernels_gn_cluster.cu).  Groups beyond that take a pass for the channels' sums (which give the group's m1 and m2 too:
 // m1 = sum gamma*sum dz / M) and a pass for dx.  Channel sums over the batch are added in a
 // fixed order by a last small kernel.
 #include "gn_common.cuh"
@@ -15,161 +15,178 @@ namespace igc {
 
 namespace {
 
-template <typename T, int V, int K, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? GN_TEAM_MAX : GN_THREADS, WIDE ? 1 : 2)
+template <typename T, int V, int K>
+__global__ void __launch_bounds__(GN_THREADS, 2)
 gn_team_bwd(const GnParams p, const GnTeam q, const T* x, const T* dy, const T* gamma, const T* beta,
             const float* mean_in, const float* rstd_in, T* dx, float* part)
 {
-    constexpr int E = K * V;
-    extern __shared__ float dyn[];  // the block's channel sums by position, one kind at a time
-    __shared__ float sm[64];
-    int turn = 0;
-    const int L = q.L;
-    const int ti = WIDE ? 0 : int(threadIdx.x) / L, lane = WIDE ? int(threadIdx.x) : int(threadIdx.x) % L;
+    constexpr int H = K * V / 2;  // pairs of values
+    // gamma and beta by position; at the end the block's channel sums by position
+    extern __shared__ __align__(16) float tab[];
+    const int L = q.L, m = int(p.M);
+    const int ti = int(threadIdx.x) / L, lane = int(threadIdx.x) % L;
     const int gi = ti % q.gpc, si = ti / q.gpc;
-    const int gset = int(blockIdx.x) % q.gsets, chunk = int(blockIdx.x) / q.gsets;
-    const int g = gset * q.gpc + gi;
+    const int g0 = int(blockIdx.x) % q.gsets * q.gpc, g = g0 + gi, chunk = int(blockIdx.x) / q.gsets;
     const bool active = si < q.spc && g < p.G;
-    const int nvec = int(p.M / V), cgv = p.Cg / V;
-    const bool nhwc = p.layout == CONV_LAYOUT_NHWC;
-    int off[K];
+    const int nvec = m / V;
+    int off[K], toff[K];  // in the sample and in the tables; a lane's vectors beyond the group stay at its start
     bool has[K];
-    float ga[E], be[E], sb[E], sg[E];
-    tc::grid_dep_wait();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int j = lane + k * L;
-        has[k] = active && j < nvec;
-        const int row = nhwc ? j / cgv : 0;
-        off[k] = nhwc ? row * p.C + g * p.Cg + (j - row * cgv) * V : int(g * p.M) + j * V;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = g * p.Cg + (nhwc ? (j - row * cgv) * V + i : (j * V + i) / p.P);
-            ga[k * V + i] = !has[k] ? 0.f : gamma ? Elem<T>::ldg(gamma + c) : 1.f;
-            be[k * V + i] = has[k] && beta ? Elem<T>::ldg(beta + c) : 0.f;
-            sb[k * V + i] = sg[k * V + i] = 0.f;
-        }
+        has[k] = active && lane + k * L < nvec;
+        off[k] = has[k] ? gn_offset(p, q, g, lane + k * L) : 0;
+        toff[k] = has[k] ? (lane + k * L) * V : 0;
     }
-    const int step = q.chunks * q.spc;
-    const int b0 = chunk * q.spc + si;
-    const int iters = ceil_div(p.B - chunk * q.spc, step);
-    Vec<T, V> cx[K], cd[K], nx[K], nd[K];
-    float mu = 0.f, rs = 0.f, nmu = 0.f, nrs = 0.f;
-    auto fetch = [&](Vec<T, V>(&vx)[K], Vec<T, V>(&vd)[K], float& m, float& r, int b) {
-        const bool in = active && b < p.B;
-        m = in ? mean_in[int64_t(b) * p.G + g] : 0.f;
-        r = in ? rstd_in[int64_t(b) * p.G + g] : 0.f;
+    const int step = q.chunks * q.spc, iters = ceil_div(p.B - chunk * q.spc, step);
+    int b = chunk * q.spc + si;
+    Vec<T, V> rx[K], rd[K];
+    float nmu, nrs;
+    auto fetch = [&](int at) {
+        const bool in = active && at < p.B;
+        nmu = in ? mean_in[int64_t(at) * p.G + g] : 0.f;
+        nrs = in ? rstd_in[int64_t(at) * p.G + g] : 0.f;
+        const T *px = x + int64_t(at) * p.N, *pd = dy + int64_t(at) * p.N;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            if (has[k] && b < p.B) {
-                vx[k].load(x + int64_t(b) * p.N + off[k]);
-                vd[k].load(dy + int64_t(b) * p.N + off[k]);
+            if (has[k] && at < p.B) {
+                rx[k].load(px + off[k]);
+                rd[k].load(pd + off[k]);
             } else {
-                vx[k].zero();
-                vd[k].zero();
+                rx[k].zero();
+                rd[k].zero();
             }
         }
     };
-    fetch(cx, cd, mu, rs, b0);
-    for (int it = 0; it < iters; ++it) {
-        const int b = b0 + it * step;
-        if (it + 1 < iters) fetch(nx, nd, nmu, nrs, b + step);
-        float xh[E], dg[E], s1 = 0.f, s2 = 0.f;
-        with_act(p.act, [&](auto act) {
+    tc::grid_dep_wait();
+    fetch(b);
+    gn_team_tables(p, q, g0, gamma, beta, tab, tab + q.gpc * m);
+    __syncthreads();
+    const float *gam = tab + gi * m, *bet = gam + q.gpc * m;
+    float2 sb[H], sg[H];
 #pragma unroll
-            for (int k = 0; k < K; ++k)
+    for (int h = 0; h < H; ++h) sb[h] = sg[h] = both(0.f);
+#pragma unroll 1
+    for (int it = 0; it < iters; ++it, b += step) {
+        const float mu = nmu, rs = nrs;
+        float2 xh[H], dg[H], s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int e = k * V + i;
-                    xh[e] = gn_xhat(cx[k].get(i), mu, rs);
-                    const float dz = gn_dz<act.value>(cd[k].get(i), xh[e], ga[e], be[e]);
-                    sb[e] += dz;
-                    sg[e] += dz * xh[e];
-                    dg[e] = dz * ga[e];
-                    s1 += dg[e];
-                    s2 += dg[e] * xh[e];
+        for (int h = 0; h < H; ++h) {
+            xh[h] = mul2(add2(pair_of<T, V, K>(rx, h), both(-mu)), both(rs));
+            dg[h] = pair_of<T, V, K>(rd, h);
+        }
+        if (it + 1 < iters) fetch(b + step);
+        if (p.act != CONV_ACT_NONE)
+            with_act(p.act, [&](auto act) {
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    const float2 z = add2(mul2(xh[h], table_pair<V, K>(gam, toff, h)), table_pair<V, K>(bet, toff, h));
+                    dg[h] = make_float2(gn_dz<act.value>(dg[h].x, z.x), gn_dz<act.value>(dg[h].y, z.y));
                 }
-        });
-        const float m1 = team_total<WIDE>(s1, L, sm, turn) * p.inv_m;
-        const float m2 = team_total<WIDE>(s2, L, sm, turn) * p.inv_m;
+            });
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            dg[h].x = has[2 * h / V] ? dg[h].x : 0.f;
+            dg[h].y = has[(2 * h + 1) / V] ? dg[h].y : 0.f;
+            sb[h] = add2(sb[h], dg[h]);
+            sg[h] = fma2(dg[h], xh[h], sg[h]);
+            dg[h] = mul2(dg[h], table_pair<V, K>(gam, toff, h));
+            s1 = add2(s1, dg[h]);
+            s2 = fma2(dg[h], xh[h], s2);
+        }
+        const float m1 = team_sum(s1.x + s1.y, L) * p.inv_m, m2 = team_sum(s2.x + s2.y, L) * p.inv_m;
         if (b < p.B) {
             T* po = dx + int64_t(b) * p.N;
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+                dg[h] = mul2(both(rs), fma2(xh[h], both(-m2), add2(dg[h], both(-m1))));
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 float r[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i) r[i] = rs * (dg[k * V + i] - m1 - xh[k * V + i] * m2);
+                for (int i = 0; i < V; ++i) r[i] = (k * V + i) % 2 ? dg[(k * V + i) / 2].y : dg[(k * V + i) / 2].x;
                 Vec<T, V> o;
                 o.set(r);
                 if (has[k]) o.store(po + off[k]);
             }
         }
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            cx[k] = nx[k];
-            cd[k] = nd[k];
-        }
-        mu = nmu;
-        rs = nrs;
     }
     if (!part) return;
-    // Channel sums of the block: dgamma's, then dbeta's, by position in shared memory; a warp a
-    // channel adds its positions over the block's samples in a fixed order.
-    const int m = int(p.M), lane_w = int(threadIdx.x) & 31, nw = int(blockDim.x) >> 5;
+    // Channel sums of the block: dgamma's, then dbeta's, by position in shared memory; `lp` lanes
+    // a channel add its positions over the block's samples in a fixed order.
+    const int per = q.spc * p.P;
+    int lp = 1;
+    while (lp < 32 && lp * 2 < per) lp *= 2;
+    const int sub = int(threadIdx.x) / lp, sl = int(threadIdx.x) % lp, teams = int(blockDim.x) / lp;
+    const int nch = min(q.gpc, p.G - g0) * p.Cg;
 #pragma unroll 1
     for (int kind = 0; kind < 2; ++kind) {
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (has[k])
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    dyn[(si * q.gpc + gi) * m + (lane + k * L) * V + i] = kind ? sb[k * V + i] : sg[k * V + i];
+        for (int h = 0; h < H; ++h) {
+            const float2 v = kind ? sb[h] : sg[h];
+            const int k0 = 2 * h / V, k1 = (2 * h + 1) / V;
+            if (has[k0]) tab[ti * m + (lane + k0 * L) * V + 2 * h % V] = v.x;
+            if (has[k1]) tab[ti * m + (lane + k1 * L) * V + (2 * h + 1) % V] = v.y;
+        }
         __syncthreads();
-        for (int w = int(threadIdx.x) >> 5; w < q.gpc * p.Cg; w += nw) {
-            const int gj = w / p.Cg, cl = w - gj * p.Cg;
-            if (gset * q.gpc + gj >= p.G) break;
+#pragma unroll 1
+        for (int c0 = 0; c0 < nch; c0 += teams) {
+            const int c = c0 + sub;
             float t = 0.f;
-            for (int o = lane_w; o < q.spc * p.P; o += 32) {
-                const int s = o / p.P, pp = o - s * p.P;
-                t += dyn[(s * q.gpc + gj) * m + (nhwc ? pp * p.Cg + cl : cl * p.P + pp)];
+            if (c < nch) {
+                uint32_t gj, cl;
+                q.dm_cg.divmod(uint32_t(c), gj, cl);
+                const float* base = tab + gj * m + (p.layout == CONV_LAYOUT_NHWC ? cl : cl * p.P);
+                const int hop = p.layout == CONV_LAYOUT_NHWC ? p.Cg : 1;
+                for (int o = sl; o < per; o += lp) {
+                    uint32_t s, pp;
+                    q.dm_p.divmod(uint32_t(o), s, pp);
+                    t += base[int(s) * q.gpc * m + int(pp) * hop];
+                }
             }
-            t = warp_sum(t);
-            if (lane_w == 0)
-                part[(int64_t(chunk) * 2 + kind) * p.C + (gset * q.gpc + gj) * p.Cg + cl] = t;
+            t = team_sum(t, lp);
+            if (sl == 0 && c < nch) part[(int64_t(chunk) * 2 + kind) * p.C + g0 * p.Cg + c] = t;
         }
     }
 }
 
-// dgamma (y = 0) and dbeta (y = 1): the sum of the `n` partials of each channel.  Block: 32
-// channels by 32 lanes, each lane its partials in ascending order, the lanes in ascending order.
-// Partial i of (kind, channel) is part[i / inner * outer_stride + i % inner * inner_stride +
-// kind * kind_stride + channel * chan_stride].
-struct ChanSum {
-    int64_t n;
-    int inner;
-    int64_t outer_stride, inner_stride, kind_stride, chan_stride;
-};
+// dgamma (blockIdx.y = 0) and dbeta (1): the sums of each channel's `n` partials
+// part[i * stride + kind * kind_stride + c].  Block: 32 channels by 32 lanes; the S blocks of a
+// cluster take contiguous ranges of the partials, each lane its own in ascending order, then the
+// lanes and the blocks are added in ascending order.
 template <typename T>
-__global__ void __launch_bounds__(1024) gn_chan_sum(int C, const ChanSum q, const float* part, T* dgamma, T* dbeta)
+__global__ void __launch_bounds__(1024) gn_chan_sum(int C, int64_t n, int S, int64_t stride, int64_t kind_stride,
+                                                    const float* part, T* dgamma, T* dbeta)
 {
     __shared__ float sm[32][33];
-    const int c = int(blockIdx.x) * 32 + int(threadIdx.x & 31), l = int(threadIdx.x >> 5);
+    const int rank = S > 1 ? int(tc::cluster_rank()) : 0;
+    const int c = int(blockIdx.x) / S * 32 + int(threadIdx.x & 31), l = int(threadIdx.x >> 5);
+    const int64_t i1 = n * (rank + 1) / S;
     float t = 0.f;
     tc::grid_dep_wait();
-    if (c < C)
-        for (int64_t i = l; i < q.n; i += 32) {
-            const int64_t o = i / q.inner;
-            t += part[o * q.outer_stride + (i - o * q.inner) * q.inner_stride + blockIdx.y * q.kind_stride +
-                      c * q.chan_stride];
-        }
+    if (c < C) {
+        const float* at = part + blockIdx.y * kind_stride + c;
+#pragma unroll 8
+        for (int64_t i = n * rank / S + l; i < i1; i += 32) t += at[i * stride];
+    }
     sm[l][threadIdx.x & 31] = t;
     __syncthreads();
-    if (l == 0 && c < C) {
+    if (l == 0) {
         t = 0.f;
-        for (int i = 0; i < 32; ++i) t += sm[i][threadIdx.x & 31];
-        Elem<T>::st((blockIdx.y ? dbeta : dgamma) + c, t);
+        for (int i = 0; i < 32; ++i) t += sm[i][threadIdx.x];
+        sm[0][threadIdx.x] = t;
     }
+    if (S > 1) {
+        __syncthreads();
+        tc::cluster_sync();
+        if (l == 0 && rank == 0) {
+            t = 0.f;
+            for (int r = 0; r < S; ++r) t += tc::ld_dsmem_f32(tc::dsmem_addr(tc::smem_u32(&sm[0][threadIdx.x]), r));
+        }
+        __syncwarp();
+        tc::cluster_sync();
+    }
+    if (l == 0 && rank == 0 && c < C) Elem<T>::st((blockIdx.y ? dbeta : dgamma) + c, t);
 }
 
 // ---- large groups ----------------------------------------------------------------------------
@@ -215,7 +232,7 @@ __global__ void __launch_bounds__(256) gn_sums_nhwc(const GnParams p, const GnPi
 #pragma unroll
                         for (int i = 0; i < V; ++i) {
                             const float xh = gn_xhat(vx[u].get(i), mu[i], rs[i]);
-                            const float dz = gn_dz<act.value>(vd[u].get(i), xh, ga[i], be[i]);
+                            const float dz = gn_dz<act.value>(vd[u].get(i), gn_z(xh, ga[i], be[i]));
                             sb[i] += dz;
                             sg[i] += dz * xh;
                         }
@@ -271,7 +288,7 @@ __global__ void __launch_bounds__(256) gn_sums_nchw(const GnParams p, const GnPi
 #pragma unroll
                         for (int i = 0; i < V; ++i) {
                             const float xh = gn_xhat(vx[u].get(i), mu, rs);
-                            const float dz = gn_dz<act.value>(vd[u].get(i), xh, ga, be);
+                            const float dz = gn_dz<act.value>(vd[u].get(i), gn_z(xh, ga, be));
                             sb += dz;
                             sg += dz * xh;
                         }
@@ -293,8 +310,9 @@ __global__ void __launch_bounds__(256) gn_sums_nchw(const GnParams p, const GnPi
             }
     }
     if (t.lane == 0 && t.in) {
-        psg[t.row * q.pieces + t.pc] = sg;
-        psb[t.row * q.pieces + t.pc] = sb;
+        const int64_t b = t.row / p.C, o = gn_part(p, q.pieces, b, int(t.row - b * p.C), t.pc);
+        psg[o] = sg;
+        psb[o] = sb;
     }
 }
 
@@ -310,16 +328,14 @@ __global__ void __launch_bounds__(128) gn_group_sums(const GnParams p, const GnP
     tc::grid_dep_wait();
     float s1 = 0.f, s2 = 0.f;
     for (int i = threadIdx.x; i < np; i += blockDim.x) {
-        const int cl = p.layout == CONV_LAYOUT_NHWC ? i % p.Cg : i / q.pieces;
-        const int pc = p.layout == CONV_LAYOUT_NHWC ? i / p.Cg : i % q.pieces;
-        const int c = g * p.Cg + cl;
+        const int pc = i / p.Cg, c = g * p.Cg + i - pc * p.Cg;
         const float ga = gamma ? Elem<T>::ldg(gamma + c) : 1.f;
         const int64_t o = gn_part(p, q.pieces, b, c, pc);
         s1 += ga * psb[o];
         s2 += ga * psg[o];
     }
-    s1 = team_total<true>(s1, blockDim.x, sm, turn) * p.inv_m;
-    s2 = team_total<true>(s2, blockDim.x, sm, turn) * p.inv_m;
+    s1 = block_total(s1, sm, turn) * p.inv_m;
+    s2 = block_total(s2, sm, turn) * p.inv_m;
     if (threadIdx.x == 0) {
         m1[blockIdx.x] = s1;
         m2[blockIdx.x] = s2;
@@ -365,7 +381,7 @@ __global__ void __launch_bounds__(256) gn_dx_nhwc(const GnParams p, const GnPiec
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         const float xh = gn_xhat(vx[u].get(i), mu[i], rs[i]);
-                        const float dz = gn_dz<act.value>(vd[u].get(i), xh, ga[i], be[i]);
+                        const float dz = gn_dz<act.value>(vd[u].get(i), gn_z(xh, ga[i], be[i]));
                         o[i] = rs[i] * (dz * ga[i] - a1[i] - xh * a2[i]);
                     }
                     vx[u].set(o);
@@ -406,7 +422,7 @@ __global__ void __launch_bounds__(256) gn_dx_nchw(const GnParams p, const GnPiec
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         const float xh = gn_xhat(vx[u].get(i), mu, rs);
-                        const float dz = gn_dz<act.value>(vd[u].get(i), xh, ga, be);
+                        const float dz = gn_dz<act.value>(vd[u].get(i), gn_z(xh, ga, be));
                         o[i] = rs * (dz * ga - a1 - xh * a2);
                     }
                     vx[u].set(o);
@@ -417,9 +433,12 @@ __global__ void __launch_bounds__(256) gn_dx_nchw(const GnParams p, const GnPiec
 }
 
 template <typename T>
-cudaError_t chan_sum(const GnParams& p, const ChanSum& q, const float* part, T* dgamma, T* dbeta, cudaStream_t s)
+cudaError_t chan_sum(const GnParams& p, int64_t n, int64_t stride, int64_t kind_stride, const float* part, T* dgamma,
+                     T* dbeta, cudaStream_t s)
 {
-    return launch_ex(gn_chan_sum<T>, dim3(ceil_div(p.C, 32), 2), dim3(1024), 0, s, 1, true, p.C, q, part, dgamma, dbeta);
+    const int S = n > 512 ? kMaxCluster : 1;  // 32 lanes take up to 16 partials each
+    return launch_ex(gn_chan_sum<T>, dim3(ceil_div(p.C, 32) * S, 2), dim3(1024), 0, s, S, true, p.C, n, S, stride,
+                     kind_stride, part, dgamma, dbeta);
 }
 
 template <typename T>
@@ -437,18 +456,19 @@ cudaError_t bwd_t(const GnParams& p, int dt, const DevInfo& d, const T* x, const
     if (t.ok) {
         const GnTeam& q = t;
         const dim3 grid(unsigned(q.gsets) * unsigned(q.chunks)), block(q.threads);
-        const size_t smem = dgamma ? size_t(4) * q.gpc * q.spc * size_t(p.M) : 0;
-        if (!dgamma) part = nullptr;
-#define GN_CALL(T_, V_, K_)                                                                                           \
-    e = q.L > 32 ? launch_ex(gn_team_bwd<T_, V_, K_, true>, grid, block, smem, s, 1, true, p, q, x, dy, gamma, beta,  \
-                             mean, rstd, dx, part)                                                                    \
-                 : launch_ex(gn_team_bwd<T_, V_, K_, false>, grid, block, smem, s, 1, true, p, q, x, dy, gamma, beta, \
-                             mean, rstd, dx, part)
-        GN_DISPATCH_TEAM(T, GN_CALL);
+        const size_t smem = size_t(4) * std::max(2 * q.gpc, q.gpc * q.spc) * size_t(p.M);
+        float* out = dgamma ? part : nullptr;
+#define GN_CALL(T_, V_, K_)                                                                                          \
+    e = launch_ex(gn_team_bwd<T_, V_, K_>, grid, block, smem, s, 1, true, p, q, x, dy, gamma, beta, mean, rstd, dx, out)
+        GN_DISPATCH_TEAM(T, false, GN_CALL);
 #undef GN_CALL
-        if (e != cudaSuccess || !dgamma) return e != cudaSuccess ? e : cudaGetLastError();
-        const ChanSum cs = {q.chunks, q.chunks, 0, 2 * int64_t(p.C), p.C, 1};
-        e = chan_sum<T>(p, cs, part, dgamma, dbeta, s);
+        if (e == cudaSuccess && dgamma) e = chan_sum<T>(p, q.chunks, 2 * int64_t(p.C), p.C, part, dgamma, dbeta, s);
+        return e != cudaSuccess ? e : cudaGetLastError();
+    }
+    const GnCluster cl = gn_cluster(p, dt, d, true);
+    if (cl.ok) {
+        e = run_gn_cluster_bwd(p, cl, dt, x, dy, gamma, beta, mean, rstd, dx, dgamma ? part : nullptr, s);
+        if (e == cudaSuccess && dgamma) e = chan_sum<T>(p, p.B, 2 * int64_t(p.C), p.C, part, dgamma, dbeta, s);
         return e != cudaSuccess ? e : cudaGetLastError();
     }
     const GnPieces q = gn_pieces(p, dt, d);
@@ -472,9 +492,7 @@ cudaError_t bwd_t(const GnParams& p, int dt, const DevInfo& d, const T* x, const
                   m1, m2);
     if (e != cudaSuccess) return e;
     if (dgamma) {
-        const ChanSum cs = nhwc ? ChanSum{int64_t(p.B) * q.pieces, q.pieces, int64_t(q.pieces) * p.C, p.C, np, 1}
-                                : ChanSum{int64_t(p.B) * q.pieces, q.pieces, int64_t(p.C) * q.pieces, 1, np, q.pieces};
-        e = chan_sum<T>(p, cs, psg, dgamma, dbeta, s);
+        e = chan_sum<T>(p, int64_t(p.B) * q.pieces, p.C, np, psg, dgamma, dbeta, s);
         if (e != cudaSuccess) return e;
     }
 #define GN_CALL(T_, V_)                                                                                               \
@@ -494,6 +512,7 @@ size_t gn_bwd_workspace(const GnParams& p, int dt, const DevInfo& d)
     if (p.B == 0) return 0;
     const GnTeam t = gn_team(p, dt, d, true);
     if (t.ok) return size_t(8) * t.chunks * p.C;
+    if (gn_cluster(p, dt, d, true).ok) return size_t(8) * p.B * p.C;
     const GnPieces q = gn_pieces(p, dt, d);
     return size_t(4) * (2 * size_t(p.B) * p.C * q.pieces + 2 * size_t(p.B) * p.G);
 }

@@ -3,8 +3,9 @@
 //   y = act((x - mean) * rstd * gamma[c] + beta[c]).
 //
 // About ten operations a value against 2 (bf16) or 4 bytes in and out: bound by memory, so what
-// counts is to read x once.  A group that fits a team of threads is held in its registers: the
+// counts is to read x once.  A group that fits a team of lanes is held in its registers: the
 // sum, then the squares about the mean, then the result, one read and one write.  Larger groups
+// are held by a thread-block cluster (kernels_gn_cluster.cu).  Groups beyond that
 // are cut into pieces whose (mean, sum of squares about it) partials are combined by Chan,
 // Golub & LeVeque's update ("Updating formulae and a pairwise algorithm for computing sample
 // variances", 1979), and a second pass applies them.  No path subtracts a squared mean from a
@@ -16,41 +17,38 @@ namespace igc {
 GnTeam gn_team(const GnParams& p, int dt, const DevInfo& d, bool bwd)
 {
     GnTeam q = {};
-    const int es = dt == DT_F32 ? 4 : 2;
-    q.V = gn_vector_width(p, es);
-    const int64_t nvec = p.M / q.V;
-    if (p.M > int64_t(GN_TEAM_MAX) * GN_LANE_VALUES || (p.layout == CONV_LAYOUT_NHWC && p.M > 512 && p.Cg * es < 32))
-        return q;
-    // Lanes and vectors a lane: the fewest instructions a value, counting the idle lanes, the
-    // butterfly steps (two sums a group) and a fixed cost an iteration.
+    const int es = dt == DT_F32 ? 4 : 2, most = bwd ? GN_BWD_VALUES : GN_FWD_VALUES;
+    if (p.M > 32 * most) return q;
+    // Vector width, vectors a lane and lanes: the fewest instructions a value by this count of
+    // them -- a value's own, the team's butterflies (two sums of one word, two steps an
+    // instruction pair), a vector's address and access, and what every lane does once -- with
+    // idle lanes counted.
     double best = 1e30;
-    for (int K = 1; K * q.V <= GN_LANE_VALUES; ++K) {
-        if (!gn_team_k(q.V, K)) continue;
-        const int64_t need = (nvec + K - 1) / K;
-        int L = 1, steps = 0;
-        while (L < need && L < 32) { L *= 2; ++steps; }
-        if (L < need) {
-            L = int((need + 31) / 32) * 32;
-            steps = 5 + 8;
+    for (int V = 16 / es; V >= 1; V /= 2) {
+        if ((p.layout == CONV_LAYOUT_NCHW ? p.M : p.Cg) % V != 0) continue;
+        const int64_t nvec = p.M / V;
+        for (int K = 1; K * V <= most; ++K) {
+            if (!gn_team_k(V, K, bwd)) continue;
+            int L = 1, steps = 0;
+            while (int64_t(L) * K < nvec) { L *= 2; ++steps; }
+            if (L > 32) continue;
+            const double cost = double(L) * ((bwd ? 18.0 : 9.0) * K * V + 4.0 * steps + (bwd ? 9.0 : 6.0) * K + 25.0);
+            if (cost < best) { best = cost; q.V = V; q.K = K; q.L = L; }
         }
-        if (L > GN_TEAM_MAX) continue;
-        const double cost = double(L) * (12.0 * K * q.V + 4.0 * steps + 20.0);
-        if (cost < best) { best = cost; q.K = K; q.L = L; }
     }
     if (best == 1e30) return q;
-    if (q.L > 32) {
-        q.gpc = q.spc = 1;
-        q.threads = q.L;
-    } else {
-        const int teams = GN_THREADS / q.L;
-        q.gpc = std::min(p.G, teams);
-        q.spc = std::max(1, std::min(teams / q.gpc, std::max(1, p.B)));
-        q.threads = round_up(q.gpc * q.spc * q.L, 32);
-    }
+    const int teams = GN_THREADS / q.L;
+    q.gpc = std::min(p.G, teams);
+    q.spc = std::max(1, std::min(teams / q.gpc, std::max(1, p.B)));
+    q.threads = round_up(q.gpc * q.spc * q.L, 32);
     q.gsets = ceil_div(p.G, q.gpc);
-    const int per_sm = std::max(1, (bwd ? 768 : 1024) / q.threads);
+    const int per_sm = std::max(1, (bwd ? 512 : 1024) / q.threads);
     const int want = std::max(1, d.sms * per_sm / q.gsets);
     q.chunks = std::min(ceil_div(std::max(1, p.B), q.spc), want);
+    q.dm_cgv = FastDivmod(uint32_t(std::max(1, p.Cg / q.V)));
+    q.dm_p = FastDivmod(uint32_t(p.P));
+    q.dm_cg = FastDivmod(uint32_t(p.Cg));
+    q.dm_m = FastDivmod(uint32_t(p.M));
     q.ok = true;
     return q;
 }
@@ -94,89 +92,85 @@ GnPieces gn_pieces(const GnParams& p, int dt, const DevInfo& d)
 namespace {
 
 // ---- small groups ----------------------------------------------------------------------------
-template <typename T, int V, int K, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? GN_TEAM_MAX : GN_THREADS, WIDE ? 1 : 2)
+template <typename T, int V, int K>
+__global__ void __launch_bounds__(GN_THREADS, 4)
 gn_team_fwd(const GnParams p, const GnTeam q, const T* x, const T* gamma, const T* beta, T* y, float* mean_out,
             float* rstd_out)
 {
-    __shared__ float sm[64];
-    int turn = 0;
-    const int L = q.L;
-    const int ti = WIDE ? 0 : int(threadIdx.x) / L, lane = WIDE ? int(threadIdx.x) : int(threadIdx.x) % L;
+    constexpr int H = K * V / 2;  // pairs of values
+    extern __shared__ __align__(16) float tab[];
+    const int L = q.L, m = int(p.M);
+    const int ti = int(threadIdx.x) / L, lane = int(threadIdx.x) % L;
     const int gi = ti % q.gpc, si = ti / q.gpc;
-    const int g = int(blockIdx.x) % q.gsets * q.gpc + gi, chunk = int(blockIdx.x) / q.gsets;
+    const int g0 = int(blockIdx.x) % q.gsets * q.gpc, g = g0 + gi, chunk = int(blockIdx.x) / q.gsets;
     const bool active = si < q.spc && g < p.G;
-    const int nvec = int(p.M / V), cgv = p.Cg / V;
-    int off[K];
+    const int nvec = m / V;
+    int off[K], toff[K];  // in the sample and in the tables; a lane's vectors beyond the group stay at its start
     bool has[K];
-    float ga[K * V], be[K * V];
-    tc::grid_dep_wait();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int j = lane + k * L;
-        has[k] = active && j < nvec;
-        const int row = p.layout == CONV_LAYOUT_NHWC ? j / cgv : 0;
-        off[k] = p.layout == CONV_LAYOUT_NHWC ? row * p.C + g * p.Cg + (j - row * cgv) * V : int(g * p.M) + j * V;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = g * p.Cg + (p.layout == CONV_LAYOUT_NHWC ? (j - row * cgv) * V + i : (j * V + i) / p.P);
-            ga[k * V + i] = has[k] && gamma ? Elem<T>::ldg(gamma + c) : 1.f;
-            be[k * V + i] = has[k] && beta ? Elem<T>::ldg(beta + c) : 0.f;
-        }
+        has[k] = active && lane + k * L < nvec;
+        off[k] = has[k] ? gn_offset(p, q, g, lane + k * L) : 0;
+        toff[k] = has[k] ? (lane + k * L) * V : 0;
     }
-    const int step = q.chunks * q.spc;
-    const int b0 = chunk * q.spc + si;
-    const int iters = ceil_div(p.B - chunk * q.spc, step);
-    Vec<T, V> cur[K], nxt[K];
-    auto fetch = [&](Vec<T, V>(&v)[K], int b) {
-        const T* px = x + int64_t(b) * p.N;
+    const int step = q.chunks * q.spc, iters = ceil_div(p.B - chunk * q.spc, step);
+    int b = chunk * q.spc + si;
+    Vec<T, V> raw[K];
+    auto fetch = [&](int at) {
+        const T* px = x + int64_t(at) * p.N;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            if (has[k] && b < p.B) v[k].load(px + off[k]);
-            else v[k].zero();
+            if (has[k] && at < p.B) raw[k].load(px + off[k]);
+            else raw[k].zero();
         }
     };
-    fetch(cur, b0);
-    for (int it = 0; it < iters; ++it) {
-        const int b = b0 + it * step;
-        if (it + 1 < iters) fetch(nxt, b + step);
-        float s = 0.f;
+    tc::grid_dep_wait();
+    fetch(b);
+    gn_team_tables(p, q, g0, gamma, beta, tab, tab + q.gpc * m);
+    __syncthreads();
+    const float *gam = tab + gi * m, *bet = gam + q.gpc * m;
+#pragma unroll 1
+    for (int it = 0; it < iters; ++it, b += step) {
+        float2 v[H], s = both(0.f);
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+        for (int h = 0; h < H; ++h) {
+            v[h] = pair_of<T, V, K>(raw, h);
+            s = add2(s, v[h]);
+        }
+        if (it + 1 < iters) fetch(b + step);
+        const float mean = __fdiv_rn(team_sum(s.x + s.y, L), p.m);  // exact for equal values
+        s = both(0.f);
 #pragma unroll
-            for (int i = 0; i < V; ++i) s += cur[k].get(i);
-        const float mean = __fdiv_rn(team_total<WIDE>(s, L, sm, turn), p.m);  // exact for equal values
-        float m2 = 0.f;
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (has[k])
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float dlt = cur[k].get(i) - mean;
-                    m2 += dlt * dlt;
-                }
-        const float rstd = rsqrtf(team_total<WIDE>(m2, L, sm, turn) * p.inv_m + p.eps);
+        for (int h = 0; h < H; ++h) {
+            v[h] = add2(v[h], both(-mean));
+            const float2 w = make_float2(has[2 * h / V] ? v[h].x : 0.f, has[(2 * h + 1) / V] ? v[h].y : 0.f);
+            s = fma2(w, w, s);
+        }
+        const float rstd = rsqrtf(team_sum(s.x + s.y, L) * p.inv_m + p.eps);
         if (active && b < p.B) {
             T* py = y + int64_t(b) * p.N;
             with_act(p.act, [&](auto act) {
 #pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    float r[V];
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        r[i] = act_value<act.value>(gn_z(gn_xhat(cur[k].get(i), mean, rstd), ga[k * V + i], be[k * V + i]));
-                    Vec<T, V> o;
-                    o.set(r);
-                    if (has[k]) o.store(py + off[k]);
+                for (int h = 0; h < H; ++h) {  // x - mean, rounded, is in v already
+                    const float2 z = add2(mul2(mul2(v[h], both(rstd)), table_pair<V, K>(gam, toff, h)),
+                                          table_pair<V, K>(bet, toff, h));
+                    v[h] = make_float2(act_value<act.value>(z.x), act_value<act.value>(z.y));
                 }
             });
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float r[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) r[i] = (k * V + i) % 2 ? v[(k * V + i) / 2].y : v[(k * V + i) / 2].x;
+                Vec<T, V> o;
+                o.set(r);
+                if (has[k]) o.store(py + off[k]);
+            }
             if (lane == 0 && mean_out) {
                 mean_out[int64_t(b) * p.G + g] = mean;
                 rstd_out[int64_t(b) * p.G + g] = rstd;
             }
         }
-#pragma unroll
-        for (int k = 0; k < K; ++k) cur[k] = nxt[k];
     }
 }
 
@@ -305,8 +299,9 @@ __global__ void __launch_bounds__(256) gn_stats_nchw(const GnParams p, const GnP
             for (int w = 1; w < q.row_lanes / 32; ++w) chan_merge(n, mean, m2, sm[w][0], sm[w][1], sm[w][2]);
     }
     if (t.lane == 0 && t.in) {
-        pmean[t.row * q.pieces + t.pc] = mean;
-        pm2[t.row * q.pieces + t.pc] = m2;
+        const int64_t b = t.row / p.C, o = gn_part(p, q.pieces, b, int(t.row - b * p.C), t.pc);
+        pmean[o] = mean;
+        pm2[o] = m2;
     }
 }
 
@@ -322,8 +317,7 @@ __global__ void __launch_bounds__(128) gn_combine(const GnParams p, const GnPiec
     tc::grid_dep_wait();
     float s = 0.f;
     auto at = [&](int i, int& cnt) {
-        const int cl = p.layout == CONV_LAYOUT_NHWC ? i % p.Cg : i / q.pieces;
-        const int pc = p.layout == CONV_LAYOUT_NHWC ? i / p.Cg : i % q.pieces;
+        const int pc = i / p.Cg, cl = i - pc * p.Cg;
         cnt = min(q.len, p.P - pc * q.len);
         return gn_part(p, q.pieces, b, g * p.Cg + cl, pc);
     };
@@ -332,7 +326,7 @@ __global__ void __launch_bounds__(128) gn_combine(const GnParams p, const GnPiec
         const int64_t o = at(i, cnt);
         s += pmean[o] * float(cnt);
     }
-    const float mu = __fdiv_rn(team_total<true>(s, blockDim.x, sm, turn), p.m);
+    const float mu = __fdiv_rn(block_total(s, sm, turn), p.m);
     float v = 0.f;
     for (int i = threadIdx.x; i < np; i += blockDim.x) {
         int cnt;
@@ -340,7 +334,7 @@ __global__ void __launch_bounds__(128) gn_combine(const GnParams p, const GnPiec
         const float dlt = pmean[o] - mu;
         v += pm2[o] + dlt * dlt * float(cnt);
     }
-    const float r = rsqrtf(team_total<true>(v, blockDim.x, sm, turn) * p.inv_m + p.eps);
+    const float r = rsqrtf(block_total(v, sm, turn) * p.inv_m + p.eps);
     if (threadIdx.x == 0) {
         mean[blockIdx.x] = mu;
         rstd[blockIdx.x] = r;
@@ -434,15 +428,15 @@ cudaError_t fwd_t(const GnParams& p, int dt, const DevInfo& d, const T* x, const
     if (t.ok) {
         const GnTeam& q = t;
         const dim3 grid(unsigned(q.gsets) * unsigned(q.chunks)), block(q.threads);
-#define GN_CALL(T_, V_, K_)                                                                                           \
-    e = q.L > 32 ? launch_ex(gn_team_fwd<T_, V_, K_, true>, grid, block, 0, s, 1, true, p, q, x, gamma, beta, y,       \
-                             mean, rstd)                                                                              \
-                 : launch_ex(gn_team_fwd<T_, V_, K_, false>, grid, block, 0, s, 1, true, p, q, x, gamma, beta, y,      \
-                             mean, rstd)
-        GN_DISPATCH_TEAM(T, GN_CALL);
+        const size_t smem = size_t(8) * q.gpc * size_t(p.M);
+#define GN_CALL(T_, V_, K_) \
+    e = launch_ex(gn_team_fwd<T_, V_, K_>, grid, block, smem, s, 1, true, p, q, x, gamma, beta, y, mean, rstd)
+        GN_DISPATCH_TEAM(T, true, GN_CALL);
 #undef GN_CALL
         return e != cudaSuccess ? e : cudaGetLastError();
     }
+    const GnCluster cl = gn_cluster(p, dt, d, false);
+    if (cl.ok) return run_gn_cluster_fwd(p, cl, dt, x, gamma, beta, y, mean, rstd, s);
     const GnPieces q = gn_pieces(p, dt, d);
     const int64_t np = int64_t(p.B) * p.C * q.pieces;
     float* pmean = static_cast<float*>(ws);
@@ -474,7 +468,7 @@ cudaError_t fwd_t(const GnParams& p, int dt, const DevInfo& d, const T* x, const
 
 size_t gn_fwd_workspace(const GnParams& p, int dt, const DevInfo& d)
 {
-    if (p.B == 0 || gn_team(p, dt, d, false).ok) return 0;
+    if (p.B == 0 || gn_team(p, dt, d, false).ok || gn_cluster(p, dt, d, false).ok) return 0;
     const GnPieces q = gn_pieces(p, dt, d);
     return size_t(4) * (2 * size_t(p.B) * p.C * q.pieces + 2 * size_t(p.B) * p.G);
 }

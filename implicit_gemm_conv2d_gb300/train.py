@@ -11,8 +11,10 @@ ordered by the caller (``stream.wait_stream``), as for any torch operation.  Wha
 functions allocate belongs to the stream they run on."""
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
+import itertools
 import threading
 
 import torch
@@ -81,8 +83,27 @@ def _bytes(ws) -> int:
     return 0 if ws is None else ws.numel() * ws.element_size()
 
 
+# The allocating functions are called once or more a layer and step, and a small call's time is
+# the host's: they pass plain integers and take the stream's handle without building a Stream.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _addr(t):
+    """The address of a contiguous CUDA tensor (None: NULL)."""
+    if t is None:
+        return None
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError("tensors must be contiguous CUDA tensors")
+    return t.data_ptr()
+
+
 def _workspace(nbytes: int, device):
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    """A workspace, its address and size."""
+    if not nbytes:
+        return None, None, 0
+    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return t, t.data_ptr(), nbytes
 
 
 def _on_stream(f):
@@ -126,26 +147,28 @@ def conv_gn_bwd(desc: GnDesc, x, dy, gamma, beta, mean, rstd, dx, dgamma, dbeta,
 
 
 def _same(name, t, shape, dtype, device):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
+    if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on {device}, got {tuple(t.shape)} {t.dtype} "
                          f"on {t.device}")
 
 
 def _gn_desc_of(x, groups, gamma, beta, eps, act, layout) -> GnDesc:
-    if x.dtype not in _DT:
+    dt, a, lay = _DT.get(x.dtype), ACTS.get(act), LAYOUTS.get(layout)
+    if dt is None:
         raise ValueError(f"x: float32 or bfloat16, got {x.dtype}")
-    if act not in ACTS or layout not in LAYOUTS:
+    if a is None or lay is None:
         raise ValueError(f"act is one of {list(ACTS)} and layout of {list(LAYOUTS)}, got {act!r}, {layout!r}")
-    if x.dim() < 2:
+    shape = x.shape
+    if len(shape) < 2:
         raise ValueError("x: at least (batch, channels)")
-    C = x.shape[1] if layout == "nchw" else x.shape[-1]
-    P = 1
-    for n in (x.shape[2:] if layout == "nchw" else x.shape[1:-1]):
+    C, P = shape[1 - 2 * lay], 1  # (B, C, ...) or (B, ..., C)
+    for n in (shape[1:-1] if lay else shape[2:]):
         P *= n
-    for name, t in (("gamma", gamma), ("beta", beta)):
-        if t is not None:
-            _same(name, t, (C,), x.dtype, x.device)
-    return make_gn_desc(x.shape[0], C, P, int(groups), act, layout, x.dtype, eps)
+    if gamma is not None:
+        _same("gamma", gamma, (C,), x.dtype, x.device)
+    if beta is not None:
+        _same("beta", beta, (C,), x.dtype, x.device)
+    return GnDesc(shape[0], C, P, groups, a, lay, dt, eps)
 
 
 @_on_stream
@@ -154,12 +177,16 @@ def group_norm(x, groups: int, gamma=None, beta=None, eps: float = 1e-5, act: st
     """y, mean, rstd of x (B, C, ...) for "nchw" or (B, ..., C) for "nhwc", contiguous; mean and
     rstd (fp32, (B, groups)) are what the backward takes, None with stats=False."""
     desc = _gn_desc_of(x, groups, gamma, beta, eps, act, layout)
+    px, device = _addr(x), x.device
     y = torch.empty_like(x)
     mean = rstd = None
     if stats:
-        mean = torch.empty((desc.B, desc.G), dtype=torch.float32, device=x.device)
+        mean = torch.empty((desc.B, groups), dtype=torch.float32, device=device)
         rstd = torch.empty_like(mean)
-    conv_gn_fwd(desc, x, gamma, beta, y, mean, rstd, _workspace(conv_gn_fwd_workspace_size(desc), x.device))
+    L = lib()
+    ws, pw, nw = _workspace(L.conv_gn_fwd_workspace_size(_ref(desc)), device)
+    _check(L.conv_gn_fwd(_ref(desc), px, _addr(gamma), _addr(beta), y.data_ptr(), _addr(mean), _addr(rstd), pw, nw,
+                         _raw_stream(device.index)), "conv_gn_fwd")
     return y, mean, rstd
 
 
@@ -168,16 +195,22 @@ def group_norm_bwd(x, dy, groups: int, gamma, beta, mean, rstd, act: str = "none
                    param_grads: bool = True):
     """dx, dgamma, dbeta (None, None with param_grads=False) from group_norm's inputs and stats."""
     desc = _gn_desc_of(x, groups, gamma, beta, 0.0, act, layout)
-    _same("dy", dy, x.shape, x.dtype, x.device)
-    _same("mean", mean, (desc.B, desc.G), torch.float32, x.device)
-    _same("rstd", rstd, (desc.B, desc.G), torch.float32, x.device)
+    device, dtype = x.device, x.dtype
+    _same("dy", dy, x.shape, dtype, device)
+    stat = (desc.B, groups)
+    _same("mean", mean, stat, torch.float32, device)
+    _same("rstd", rstd, stat, torch.float32, device)
+    px = _addr(x)
     dx = torch.empty_like(x)
     dgamma = dbeta = None
     if param_grads:
-        dgamma = torch.empty((desc.C,), dtype=x.dtype, device=x.device)
+        dgamma = torch.empty((desc.C,), dtype=dtype, device=device)
         dbeta = torch.empty_like(dgamma)
-    conv_gn_bwd(desc, x, dy, gamma, beta, mean, rstd, dx, dgamma, dbeta,
-                _workspace(conv_gn_bwd_workspace_size(desc), x.device))
+    L = lib()
+    ws, pw, nw = _workspace(L.conv_gn_bwd_workspace_size(_ref(desc)), device)
+    _check(L.conv_gn_bwd(_ref(desc), px, _addr(dy), _addr(gamma), _addr(beta), _addr(mean), _addr(rstd),
+                         dx.data_ptr(), _addr(dgamma), _addr(dbeta), pw, nw, _raw_stream(device.index)),
+           "conv_gn_bwd")
     return dx, dgamma, dbeta
 
 
@@ -199,35 +232,41 @@ def conv_embed_bwd(desc: EmbedDesc, idx, dy, dtable, workspace, stream=None) -> 
                                 _stream(stream)), "conv_embed_bwd")
 
 
-def _embed_check(idx, t, name):
-    if idx.dtype not in _IDX or t.dtype not in _DT:
+def _embed_desc_of(idx, t, V, D, scale, padding_idx, name) -> EmbedDesc:
+    it, dt = _IDX.get(idx.dtype), _DT.get(t.dtype)
+    if it is None or dt is None:
         raise ValueError(f"idx: int32 or int64, {name}: float32 or bfloat16; got {idx.dtype}, {t.dtype}")
     if idx.device != t.device:
         raise ValueError(f"idx on {idx.device}, {name} on {t.device}")
+    return EmbedDesc(idx.numel(), V, D, padding_idx, it, dt, scale)
 
 
 @_on_stream
 def embed(idx, table, scale: float = 1.0, padding_idx: int = -1):
     """scale * table[idx], shape idx.shape + (D,); a token equal to padding_idx or outside the
     table gives zeros."""
-    _embed_check(idx, table, "table")
     if table.dim() != 2:
         raise ValueError("table: (rows, values)")
     V, D = table.shape
-    y = torch.empty(idx.shape + (D,), dtype=table.dtype, device=table.device)
-    conv_embed_fwd(make_embed_desc(idx.numel(), V, D, idx.dtype, table.dtype, scale, padding_idx), idx, table, y)
+    desc = _embed_desc_of(idx, table, V, D, scale, padding_idx, "table")
+    pi, pt, device = _addr(idx), _addr(table), table.device
+    y = torch.empty(idx.shape + (D,), dtype=table.dtype, device=device)
+    _check(lib().conv_embed_fwd(_ref(desc), pi, pt, y.data_ptr(), _raw_stream(device.index)), "conv_embed_fwd")
     return y
 
 
 @_on_stream
 def embed_bwd(idx, dy, V: int, scale: float = 1.0, padding_idx: int = -1):
     """The table's gradient (V, D) from dy of shape idx.shape + (D,)."""
-    _embed_check(idx, dy, "dy")
     D = dy.shape[-1]
-    _same("dy", dy, tuple(idx.shape) + (D,), dy.dtype, idx.device)
-    desc = make_embed_desc(idx.numel(), V, D, idx.dtype, dy.dtype, scale, padding_idx)
-    dtable = torch.empty((V, D), dtype=dy.dtype, device=dy.device)
-    conv_embed_bwd(desc, idx, dy, dtable, _workspace(conv_embed_bwd_workspace_size(desc), dy.device))
+    desc = _embed_desc_of(idx, dy, V, D, scale, padding_idx, "dy")
+    _same("dy", dy, idx.shape + (D,), dy.dtype, idx.device)
+    pi, pd, device = _addr(idx), _addr(dy), dy.device
+    dtable = torch.empty((V, D), dtype=dy.dtype, device=device)
+    L = lib()
+    ws, pw, nw = _workspace(L.conv_embed_bwd_workspace_size(_ref(desc)), device)
+    _check(L.conv_embed_bwd(_ref(desc), pi, pd, dtable.data_ptr(), pw, nw, _raw_stream(device.index)),
+           "conv_embed_bwd")
     return dtable
 
 
@@ -235,16 +274,26 @@ def embed_bwd(idx, dy, V: int, scale: float = 1.0, padding_idx: int = -1):
 def make_grads(grads, out=None):
     """The C array of a list of gradients (and outputs, default: in place).  It holds addresses,
     not references: keep the tensors alive while it is in use."""
-    flat = []
-    for g, o in zip(grads, grads if out is None else out):
-        if not g.is_cuda or not g.is_contiguous():
+    n = len(grads)
+    # column by column: a list of hundreds of tensors is most of the call's host time
+    for t in grads if out is None else itertools.chain(grads, out):
+        if not t.is_cuda or not t.is_contiguous():
             raise ValueError("tensors must be contiguous CUDA tensors")
-        if o is not g and (o.shape != g.shape or o.dtype != g.dtype or o.device != g.device or not o.is_contiguous()):
-            raise ValueError(f"out: expected a contiguous {tuple(g.shape)} {g.dtype} on {g.device}")
-        if g.dtype not in _DT:
-            raise ValueError(f"gradients are float32 or bfloat16, got {g.dtype}")
-        flat += (g.data_ptr(), o.data_ptr(), g.numel(), _DT[g.dtype])
-    return (Grad * max(1, len(flat) // 4)).from_buffer((ctypes.c_int64 * max(4, len(flat)))(*flat))
+    flat = array.array("q", bytes(32 * max(1, n)))
+    numels = array.array("q", [t.numel() for t in grads])
+    dtypes = [t.dtype for t in grads]
+    addrs = array.array("q", [t.data_ptr() for t in grads])
+    flat[0:4 * n:4] = flat[1:4 * n:4] = addrs
+    flat[2:4 * n:4] = numels
+    try:
+        flat[3:4 * n:4] = array.array("q", [_DT[d] for d in dtypes])
+    except KeyError as e:
+        raise ValueError(f"gradients are float32 or bfloat16, got {e.args[0]}") from None
+    if out is not None:
+        if [t.numel() for t in out] != numels.tolist() or [t.dtype for t in out] != dtypes:
+            raise ValueError("out: each tensor with its gradient's size and dtype")
+        flat[1:4 * n:4] = array.array("q", [t.data_ptr() for t in out])
+    return (Grad * max(1, n)).from_buffer(flat)
 
 
 def conv_grad_norm_workspace_size(grads, count: int) -> int:
@@ -261,28 +310,33 @@ def conv_grad_clip(grads, count: int, max_norm: float, norm, workspace, stream=N
                                 _bytes(workspace), _stream(stream)), "conv_grad_clip")
 
 
-@_on_stream
-def grad_norm(grads):
-    """The 2-norm over all gradients, a 0-dim fp32 tensor (nothing waits for it)."""
+def _grads_call(grads, out, max_norm):
     grads = list(grads)
     if not grads:
         raise ValueError("an empty list of gradients")
-    arr, dev = make_grads(grads), grads[0].device
-    norm = torch.empty((), dtype=torch.float32, device=dev)
-    conv_grad_norm(arr, len(grads), norm, _workspace(conv_grad_norm_workspace_size(arr, len(grads)), dev))
+    if out is not None and len(out) != len(grads):
+        raise ValueError(f"out: {len(out)} tensors for {len(grads)} gradients")
+    n, device = len(grads), grads[0].device
+    arr = make_grads(grads, out)
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    L, at = lib(), ctypes.addressof(arr)
+    ws, pw, nw = _workspace(L.conv_grad_norm_workspace_size(at, n), device)
+    if max_norm is None:
+        _check(L.conv_grad_norm(at, n, norm.data_ptr(), pw, nw, _raw_stream(device.index)), "conv_grad_norm")
+    else:
+        _check(L.conv_grad_clip(at, n, max_norm, norm.data_ptr(), pw, nw, _raw_stream(device.index)),
+               "conv_grad_clip")
     return norm
+
+
+@_on_stream
+def grad_norm(grads):
+    """The 2-norm over all gradients, a 0-dim fp32 tensor (nothing waits for it)."""
+    return _grads_call(grads, None, None)
 
 
 @_on_stream
 def clip_grads(grads, max_norm: float, out=None):
     """Scales the gradients by min(1, max_norm / (norm + 1e-6)), in place or into the tensors of
     ``out``; returns the norm before."""
-    grads = list(grads)
-    if not grads:
-        raise ValueError("an empty list of gradients")
-    if out is not None and len(out) != len(grads):
-        raise ValueError(f"out: {len(out)} tensors for {len(grads)} gradients")
-    arr, dev = make_grads(grads, out), grads[0].device
-    norm = torch.empty((), dtype=torch.float32, device=dev)
-    conv_grad_clip(arr, len(grads), max_norm, norm, _workspace(conv_grad_norm_workspace_size(arr, len(grads)), dev))
-    return norm
+    return _grads_call(grads, out, max_norm)
