@@ -9,22 +9,63 @@
 
 namespace igc {
 
+// 2^x and 1/x in one instruction each (2 and 1 units in the last place; results below 2^-126
+// are 0).  The general-range forms of exp and of the quotient take about four times the
+// instructions, and the activations are most of what these kernels compute.
+__device__ __forceinline__ float fast_exp2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float fast_rcp(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float sigmoid(float z) { return fast_rcp(1.f + fast_exp2(-kLog2e * z)); }
+
+// Phi(z) and exp(-z^2 / 2).  Phi from Abramowitz & Stegun 7.1.26, Handbook of Mathematical
+// Functions: erf(x) = 1 - (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), x >= 0,
+// to 1.5e-7 (so Phi to 0.75e-7, near fp32's own rounding); its exponential is the density's.
+__device__ __forceinline__ float normal_cdf(float z, float& e)
+{
+    const float x = fabsf(z) * 0.70710678118654752f;
+    const float t = fast_rcp(fmaf(0.3275911f, x, 1.f));
+    e = fast_exp2(-0.5f * kLog2e * z * z);
+    float w = fmaf(1.061405429f, t, -1.453152027f);
+    w = fmaf(w, t, 1.421413741f);
+    w = fmaf(w, t, -0.284496736f);
+    w = fmaf(w, t, 0.254829592f);
+    const float tail = 0.5f * w * t * e;
+    return z < 0.f ? tail : 1.f - tail;
+}
+
 template <int ACT> __device__ __forceinline__ float act_value(float z)
 {
     if constexpr (ACT == CONV_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
-    if constexpr (ACT == CONV_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
-    if constexpr (ACT == CONV_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    if constexpr (ACT == CONV_ACT_SILU) return z * sigmoid(z);
+    if constexpr (ACT == CONV_ACT_GELU) {
+        float e;
+        return z * normal_cdf(z, e);
+    }
     return z;
 }
 
 template <int ACT> __device__ __forceinline__ float act_slope(float z)
 {
     if constexpr (ACT == CONV_ACT_SILU) {
-        const float p = __fdividef(1.f, 1.f + __expf(-z));
-        return p * (1.f + z * (1.f - p));
+        const float p = sigmoid(z);
+        return fmaf(p * z, 1.f - p, p);
     }
-    if constexpr (ACT == CONV_ACT_GELU)
-        return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * __expf(-0.5f * z * z);
+    if constexpr (ACT == CONV_ACT_GELU) {
+        float e;
+        const float cdf = normal_cdf(z, e);
+        return fmaf(z * 0.39894228040143268f, e, cdf);
+    }
     return 1.f;
 }
 
@@ -136,6 +177,14 @@ template <int V, int K> __device__ __forceinline__ float2 table_pair(const float
     else return *reinterpret_cast<const float2*>(tab + toff[2 * h / V] + 2 * h % V);
 }
 
+// s / m for m = p.m with the correctly rounded quotient's bits (one Newton step on s * inv_m), so
+// that the mean of equal values is that value.
+__device__ __forceinline__ float div_m(const GnParams& p, float s)
+{
+    const float q = s * p.inv_m;
+    return fmaf(fmaf(-q, p.m, s), p.inv_m, q);
+}
+
 // Sum over the block, the same value in every thread.  `sm` holds 64 floats; `turn` alternates
 // its halves so that one barrier a call is enough.
 __device__ __forceinline__ float block_total(float v, float* sm, int& turn)
@@ -153,9 +202,10 @@ __device__ __forceinline__ float block_total(float v, float* sm, int& turn)
 
 // ---- large groups kept on chip by a cluster (kernels_gn_cluster.cu) --------------------------
 struct GnCluster {
-    int V, S, threads, K;        // vector width, blocks a cluster, threads, slots a thread
+    int V, S, log_s, threads, K; // vector width, blocks a cluster (and its log2), threads, slots a thread
     int W, cols, lanes, groups;  // NHWC: channels, vectors and groups of a window, rows side by side
     int wins;                    // units a sample
+    int vecs;                    // NCHW: vectors of a unit
     int Cg, smem;
     bool nhwc, ok;
 };

@@ -40,21 +40,26 @@ gn_team_bwd(const GnParams p, const GnTeam q, const T* x, const T* dy, const T* 
     const int step = q.chunks * q.spc, iters = ceil_div(p.B - chunk * q.spc, step);
     int b = chunk * q.spc + si;
     Vec<T, V> rx[K], rd[K];
-    float nmu, nrs;
-    auto fetch = [&](int at) {
-        const bool in = active && at < p.B;
-        nmu = in ? mean_in[int64_t(at) * p.G + g] : 0.f;
-        nrs = in ? rstd_in[int64_t(at) * p.G + g] : 0.f;
-        const T *px = x + int64_t(at) * p.N, *pd = dy + int64_t(at) * p.N;
+    float nmu = 0.f, nrs = 0.f;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (has[k] && at < p.B) {
-                rx[k].load(px + off[k]);
-                rd[k].load(pd + off[k]);
-            } else {
-                rx[k].zero();
-                rd[k].zero();
-            }
+    for (int k = 0; k < K; ++k) {
+        rx[k].zero();
+        rd[k].zero();
+    }
+    auto fetch = [&](int at) {
+        if (active && at < p.B) {
+            nmu = mean_in[int64_t(at) * p.G + g];
+            nrs = rstd_in[int64_t(at) * p.G + g];
+            const T *px = x + int64_t(at) * p.N, *pd = dy + int64_t(at) * p.N;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (has[k]) {
+                    rx[k].load(px + off[k]);
+                    rd[k].load(pd + off[k]);
+                }
+        } else {  // a sample beyond the batch adds nothing
+#pragma unroll
+            for (int k = 0; k < K; ++k) rd[k].zero();
         }
     };
     tc::grid_dep_wait();
@@ -83,10 +88,9 @@ gn_team_bwd(const GnParams p, const GnTeam q, const T* x, const T* dy, const T* 
                     dg[h] = make_float2(gn_dz<act.value>(dg[h].x, z.x), gn_dz<act.value>(dg[h].y, z.y));
                 }
             });
+        // a lane's vectors beyond the group have zeros for dy and add nothing
 #pragma unroll
         for (int h = 0; h < H; ++h) {
-            dg[h].x = has[2 * h / V] ? dg[h].x : 0.f;
-            dg[h].y = has[(2 * h + 1) / V] ? dg[h].y : 0.f;
             sb[h] = add2(sb[h], dg[h]);
             sg[h] = fma2(dg[h], xh[h], sg[h]);
             dg[h] = mul2(dg[h], table_pair<V, K>(gam, toff, h));

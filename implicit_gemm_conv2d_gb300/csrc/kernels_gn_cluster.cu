@@ -17,8 +17,8 @@ namespace {
 constexpr int GC_MAX_CG = 2048;            // channels of a group (NCHW: their gammas sit in shared memory)
 constexpr int GC_TWO = 110 * 1024;         // shared memory of a block when two share an SM
 constexpr int GC_ONE = 220 * 1024;
-constexpr int GC_VECS = 8;                 // vectors a thread, about
-constexpr int GC_FWD_THREADS = 512, GC_BWD_THREADS = 256;
+constexpr int GC_VECS = 16;                // vectors a thread, about
+constexpr int GC_THREADS = 512;
 
 }  // namespace
 
@@ -33,7 +33,7 @@ static int gc_extra(const GnCluster& q, bool bwd)
 GnCluster gn_cluster(const GnParams& p, int dt, const DevInfo& d, bool bwd)
 {
     GnCluster q = {};
-    const int es = dt == DT_F32 ? 4 : 2, most_threads = bwd ? GC_BWD_THREADS : GC_FWD_THREADS;
+    const int es = dt == DT_F32 ? 4 : 2;
     // one position: both layouts are the same, and channels last reads it in wide vectors
     const bool nhwc = p.layout == CONV_LAYOUT_NHWC || p.P == 1;
     q.nhwc = nhwc;
@@ -46,47 +46,49 @@ GnCluster gn_cluster(const GnParams& p, int dt, const DevInfo& d, bool bwd)
     if (p.Cg > GC_MAX_CG) return q;
     int lcm = p.Cg;
     while (lcm % q.V != 0) lcm += p.Cg;
-    // NHWC: windows of whole vectors and whole groups, 64 bytes of a row at least (two sectors),
-    // narrower ones when the unit would not fit otherwise.
-    int m = nhwc ? std::max(1, std::min(ceil_div(64, lcm * es), ceil_div(p.C, lcm))) : 1;
-    for (; m >= 1; --m) {
-        int64_t vecs;  // of the unit
-        if (nhwc) {
-            q.W = std::min(m * lcm, p.C);
-            q.cols = q.W / q.V;
-            q.groups = q.W / p.Cg;
-            q.wins = ceil_div(p.C, q.W);
-            if (q.cols > most_threads) continue;
-            vecs = int64_t(p.P) * q.cols;
-        } else {
-            q.wins = p.G;
-            vecs = p.M / q.V;
+    // NHWC: windows of whole vectors and whole groups, 64 bytes of a row (two sectors) or less.
+    // Two blocks an SM come before wide rows and small clusters: a block alone on its SM waits
+    // with it.
+    const int widest = nhwc ? std::max(1, std::min(ceil_div(64, lcm * es), ceil_div(p.C, lcm))) : 1;
+    for (const int limit : {GC_TWO, std::min(GC_ONE, d.smem_optin - 1024)})
+        for (int m = widest; m >= 1; --m) {
+            int64_t vecs;  // of the unit
+            if (nhwc) {
+                q.W = std::min(m * lcm, p.C);
+                q.cols = q.W / q.V;
+                q.groups = q.W / p.Cg;
+                q.wins = ceil_div(p.C, q.W);
+                if (q.cols > GC_THREADS) continue;
+                vecs = int64_t(p.P) * q.cols;
+            } else {
+                q.wins = p.G;
+                vecs = p.M / q.V;
+                q.vecs = int(vecs);
+            }
+            const int64_t units = int64_t(p.B) * q.wins;
+            if (units * kMaxCluster > 0x7FFFFFFF) return q;
+            const int most = int(std::min<int64_t>(kMaxCluster, nhwc ? p.P : vecs / 32 + 1));
+            for (int S = 1, log = 0; S <= most; S *= 2, ++log) {
+                const int64_t per = (vecs + S - 1) / S;
+                int T = 32;
+                while (T < (bwd && limit == GC_TWO ? 256 : GC_THREADS) && per > int64_t(T) * GC_VECS) T *= 2;
+                if (nhwc) while (T < q.cols) T *= 2;
+                q.S = S;
+                q.log_s = log;
+                q.threads = T;
+                q.lanes = nhwc ? T / q.cols : 1;
+                const int64_t K = nhwc ? (ceil_div(p.P, S) + q.lanes - 1) / q.lanes : (per + T - 1) / T;
+                if (K * T * vb * tiles > limit) continue;
+                q.K = int(K);
+                q.smem = q.K * T * vb * tiles + gc_extra(q, bwd);
+                if (q.smem > limit) continue;
+                // larger clusters while the SMs are not filled and the blocks still have a few
+                // kilobytes each
+                if (S * 2 <= most && units * S < 2 * d.sms && per * vb > 4096) continue;
+                q.ok = true;
+                return q;
+            }
         }
-        const int64_t units = int64_t(p.B) * q.wins;
-        if (units * 8 > 0x7FFFFFFF) return q;
-        const int most = int(std::min<int64_t>(8, nhwc ? p.P : vecs / 32 + 1));
-        for (int S = 1; S <= most; S *= 2) {
-            const int64_t per = (vecs + S - 1) / S;
-            int T = 32;
-            while (T < most_threads && per > int64_t(T) * GC_VECS) T *= 2;
-            if (nhwc) while (T < q.cols) T *= 2;
-            q.S = S;
-            q.threads = T;
-            q.lanes = nhwc ? T / q.cols : 1;
-            const int64_t K = nhwc ? (ceil_div(p.P, S) + q.lanes - 1) / q.lanes : (per + T - 1) / T;
-            if (K * T * vb * tiles > GC_ONE) continue;
-            q.K = int(K);
-            q.smem = q.K * T * vb * tiles + gc_extra(q, bwd);
-            if (q.smem > std::min(GC_ONE, d.smem_optin - 1024)) continue;
-            const bool more = S * 2 <= most;
-            // larger clusters while a block does not leave room for a second one on the SM, or
-            // while the SMs are not filled and the blocks still have a few kilobytes each
-            if (more && q.smem > GC_TWO) continue;
-            if (more && units * S < 2 * d.sms && per * vb > 4096) continue;
-            q.ok = true;
-            return q;
-        }
-    }
     return q;
 }
 
@@ -124,6 +126,9 @@ __device__ __forceinline__ void cluster_wait()
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// Where block r's part of n items begins (S is a power of two).
+__device__ __forceinline__ int gc_cut(int n, const GnCluster& q, int r) { return int((int64_t(n) * r) >> q.log_s); }
+
 // The unit of an NHWC block: rows [r0, r1) of its window; thread (lane, col) holds the vector
 // `col` of the rows r0 + lane, r0 + lane + lanes, ...
 struct GcTile {
@@ -142,16 +147,16 @@ struct GcTile {
         lane = int(threadIdx.x) / q.cols;
         col = int(threadIdx.x) - lane * q.cols;
         in = lane < q.lanes && col * V < W;
-        r0 = int(int64_t(p.P) * rank / q.S);
-        r1 = int(int64_t(p.P) * (rank + 1) / q.S);
+        r0 = gc_cut(p.P, q, rank);
+        r1 = gc_cut(p.P, q, rank + 1);
         mine = in ? max(0, (r1 - r0 - lane + q.lanes - 1) / q.lanes) : 0;
         g = in ? col * V / p.Cg : 0;
         split = in ? min(V, (g + 1) * p.Cg - col * V) : V;
     }
 };
-__device__ __forceinline__ float gc_rows(const GnParams& p, int S, int r)
+__device__ __forceinline__ float gc_rows(const GnParams& p, const GnCluster& q, int r)
 {
-    return float(int(int64_t(p.P) * (r + 1) / S) - int(int64_t(p.P) * r / S));
+    return float(gc_cut(p.P, q, r + 1) - gc_cut(p.P, q, r));
 }
 // A vector's values as pairs; one value: (value, 0).
 template <int V> constexpr int gc_pairs() { return (V + 1) / 2; }
@@ -170,7 +175,7 @@ template <typename T, int V> __device__ __forceinline__ void gc_pack(Vec<T, V>& 
 
 // ---- channels last ---------------------------------------------------------------------------
 template <typename T, int V>
-__global__ void __launch_bounds__(GC_FWD_THREADS, 2)
+__global__ void __launch_bounds__(GC_THREADS, 2)
 gn_cluster_fwd_nhwc(const GnParams p, const GnCluster q, const T* x, const T* gamma, const T* beta, T* y,
                     float* mean_out, float* rstd_out)
 {
@@ -238,23 +243,26 @@ gn_cluster_fwd_nhwc(const GnParams p, const GnCluster q, const T* x, const T* ga
     }
     __syncthreads();
     // A warp a group: the mean over its threads' means, then the squares about it.
+    const int full = (t.r1 - t.r0) / q.lanes, extra = (t.r1 - t.r0) - full * q.lanes;
     for (int g = int(threadIdx.x >> 5); g < t.groups; g += nt >> 5) {
-        const int ca = g * p.Cg, va = ca / V, nv = (ca + p.Cg - 1) / V - va + 1, cnt = nv * q.lanes;
+        const int ca = g * p.Cg, va = ca / V, vb = (ca + p.Cg - 1) / V;
         float mean = 0.f, m2 = 0.f;
 #pragma unroll 1
         for (int pass = 0; pass < 2; ++pass) {
             float s = 0.f;
-            for (int i = int(threadIdx.x & 31); i < cnt; i += 32) {
-                const int l = i / nv, cv = va + i - l * nv;
-                const int rows = max(0, (t.r1 - t.r0 - l + q.lanes - 1) / q.lanes);
-                const float4 r = rec[l * q.cols + cv];
+            for (int cv = va; cv <= vb; ++cv) {
                 const bool later = cv * V < ca;  // the vector begins in the group before
-                const float n = float(rows * (min(ca + p.Cg, cv * V + V) - max(ca, cv * V)));
-                const float mu = later ? r.z : r.x, dlt = mu - mean;
-                s += pass == 0 ? n * mu : (later ? r.w : r.y) + n * dlt * dlt;
+                const int width = min(ca + p.Cg, cv * V + V) - max(ca, cv * V);
+#pragma unroll 2
+                for (int l = int(threadIdx.x & 31); l < q.lanes; l += 32) {
+                    const float4 r = rec[l * q.cols + cv];
+                    const float n = float((full + (l < extra)) * width);
+                    const float mu = later ? r.z : r.x, dlt = mu - mean;
+                    s += pass == 0 ? n * mu : (later ? r.w : r.y) + n * dlt * dlt;
+                }
             }
             s = warp_sum(s);
-            if (pass == 0) mean = __fdiv_rn(s, gc_rows(p, q.S, t.rank) * float(p.Cg));
+            if (pass == 0) mean = __fdiv_rn(s, gc_rows(p, q, t.rank) * float(p.Cg));
             else m2 = s;
         }
         if ((threadIdx.x & 31) == 0) {
@@ -279,13 +287,13 @@ gn_cluster_fwd_nhwc(const GnParams p, const GnCluster q, const T* x, const T* ga
                 }
 #pragma unroll
             for (int r = 0; r < 8; ++r)
-                if (r < q.S) sum += mu[r] * (gc_rows(p, q.S, r) * float(p.Cg));
+                if (r < q.S) sum += mu[r] * (gc_rows(p, q, r) * float(p.Cg));
             const float m = __fdiv_rn(sum, p.m);
 #pragma unroll
             for (int r = 0; r < 8; ++r)
                 if (r < q.S) {
                     const float dlt = mu[r] - m;
-                    sq += m2[r] + dlt * dlt * (gc_rows(p, q.S, r) * float(p.Cg));
+                    sq += m2[r] + dlt * dlt * (gc_rows(p, q, r) * float(p.Cg));
                 }
             stat[2 * g] = m;
             stat[2 * g + 1] = rsqrtf(sq * p.inv_m + p.eps);
@@ -332,7 +340,7 @@ gn_cluster_fwd_nhwc(const GnParams p, const GnCluster q, const T* x, const T* ga
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(GC_BWD_THREADS, 3)
+__global__ void __launch_bounds__(GC_THREADS, 1)
 gn_cluster_bwd_nhwc(const GnParams p, const GnCluster q, const T* x, const T* dy, const T* gamma, const T* beta,
                     const float* mean, const float* rstd, T* dx, float* part)
 {
@@ -510,16 +518,14 @@ struct GcRange {
         const int unit = int(blockIdx.x) / q.S;
         b = unit / p.G;
         g = unit - b * p.G;
-        const int64_t n = p.M / V;
-        v0 = int(n * rank / q.S);
-        v1 = int(n * (rank + 1) / q.S);
+        v0 = gc_cut(q.vecs, q, rank);
+        v1 = gc_cut(q.vecs, q, rank + 1);
         base = int64_t(b) * p.N + int64_t(g) * p.M;
     }
 };
-__device__ __forceinline__ int gc_count(const GnParams& p, int V, int S, int r)
+__device__ __forceinline__ int gc_count(const GnCluster& q, int V, int r)
 {
-    const int64_t n = p.M / V;
-    return (int(n * (r + 1) / S) - int(n * r / S)) * V;
+    return (gc_cut(q.vecs, q, r + 1) - gc_cut(q.vecs, q, r)) * V;
 }
 
 // Gamma and beta of a vector's values: channel c up to value `split`, channel c + 1 from there.
@@ -546,7 +552,7 @@ __device__ __forceinline__ float block_sum(float v, float* sm)
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(GC_FWD_THREADS, 2)
+__global__ void __launch_bounds__(GC_THREADS, 2)
 gn_cluster_fwd_nchw(const GnParams p, const GnCluster q, const FastDivmod dmP, const T* x, const T* gamma,
                     const T* beta, T* y, float* mean_out, float* rstd_out)
 {
@@ -605,14 +611,14 @@ gn_cluster_fwd_nchw(const GnParams p, const GnCluster q, const FastDivmod dmP, c
             }
 #pragma unroll
         for (int r = 0; r < 8; ++r)
-            if (r < q.S) sum += m[r] * float(gc_count(p, V, q.S, r));
+            if (r < q.S) sum += m[r] * float(gc_count(q, V, r));
         mu = __fdiv_rn(sum, p.m);
         sq = 0.f;
 #pragma unroll
         for (int r = 0; r < 8; ++r)
             if (r < q.S) {
                 const float dlt = m[r] - mu;
-                sq += m2[r] + dlt * dlt * float(gc_count(p, V, q.S, r));
+                sq += m2[r] + dlt * dlt * float(gc_count(q, V, r));
             }
         cluster_arrive();
     }
@@ -645,7 +651,7 @@ gn_cluster_fwd_nchw(const GnParams p, const GnCluster q, const FastDivmod dmP, c
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(GC_BWD_THREADS, 3)
+__global__ void __launch_bounds__(GC_THREADS, 1)
 gn_cluster_bwd_nchw(const GnParams p, const GnCluster q, const FastDivmod dmP, const T* x, const T* dy,
                     const T* gamma, const T* beta, const float* mean, const float* rstd, T* dx, float* part)
 {
@@ -716,8 +722,8 @@ gn_cluster_bwd_nchw(const GnParams p, const GnCluster q, const FastDivmod dmP, c
         const bool thin = p.P < 8 * V;
         const int lane = thin ? 0 : int(threadIdx.x & 31), hop = thin ? 1 : 32;
         for (int c = thin ? int(threadIdx.x) : int(threadIdx.x >> 5); c < p.Cg; c += thin ? nt : nt >> 5) {
-            const int lo = max(t.v0, int((int64_t(c) * p.P + V - 1) / V));
-            const int hi = min(t.v1, int((int64_t(c + 1) * p.P + V - 1) / V));
+            const int lo = max(t.v0, int(unsigned(c * p.P + V - 1) / V));
+            const int hi = min(t.v1, int(unsigned((c + 1) * p.P + V - 1) / V));
             float2 s = make_float2(0.f, 0.f);
             for (int v = lo + lane; v < hi; v += hop) {
                 const float2 e = vs[v - t.v0];

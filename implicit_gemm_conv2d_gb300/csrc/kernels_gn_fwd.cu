@@ -116,13 +116,14 @@ gn_team_fwd(const GnParams p, const GnTeam q, const T* x, const T* gamma, const 
     const int step = q.chunks * q.spc, iters = ceil_div(p.B - chunk * q.spc, step);
     int b = chunk * q.spc + si;
     Vec<T, V> raw[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) raw[k].zero();
     auto fetch = [&](int at) {
+        if (at >= p.B) return;
         const T* px = x + int64_t(at) * p.N;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (has[k] && at < p.B) raw[k].load(px + off[k]);
-            else raw[k].zero();
-        }
+        for (int k = 0; k < K; ++k)
+            if (has[k]) raw[k].load(px + off[k]);
     };
     tc::grid_dep_wait();
     fetch(b);
@@ -138,13 +139,12 @@ gn_team_fwd(const GnParams p, const GnTeam q, const T* x, const T* gamma, const 
             s = add2(s, v[h]);
         }
         if (it + 1 < iters) fetch(b + step);
-        const float mean = __fdiv_rn(team_sum(s.x + s.y, L), p.m);  // exact for equal values
+        const float mean = div_m(p, team_sum(s.x + s.y, L));
         s = both(0.f);
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
-            v[h] = add2(v[h], both(-mean));
-            const float2 w = make_float2(has[2 * h / V] ? v[h].x : 0.f, has[(2 * h + 1) / V] ? v[h].y : 0.f);
-            s = fma2(w, w, s);
+        for (int h = 0; h < H; ++h) {  // a lane's vectors beyond the group stay zero
+            v[h] = add2(v[h], make_float2(has[2 * h / V] ? -mean : 0.f, has[(2 * h + 1) / V] ? -mean : 0.f));
+            s = fma2(v[h], v[h], s);
         }
         const float rstd = rsqrtf(team_sum(s.x + s.y, L) * p.inv_m + p.eps);
         if (active && b < p.B) {

@@ -69,7 +69,7 @@ template <typename T, int V> struct Vec {
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) {
                 const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                r.w[i] = uint32_t(__bfloat16_as_ushort(h.x)) | (uint32_t(__bfloat16_as_ushort(h.y)) << 16);
+                r.w[i] = *reinterpret_cast<const uint32_t*>(&h);
             }
         }
     }
@@ -79,7 +79,9 @@ template <typename T, int V> struct Vec {
 // fixed butterfly order; every lane of the warp takes part.
 __device__ __forceinline__ float team_sum(float v, int width)
 {
-    for (int o = width >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        if (o < width) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
 __device__ __forceinline__ float warp_sum(float v)
