@@ -26,48 +26,66 @@ __device__ __forceinline__ float fast_rcp(float x)
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float sigmoid(float z) { return fast_rcp(1.f + fast_exp2(-kLog2e * z)); }
+// The kernels compute on pairs of values: one instruction adds or multiplies both.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
-// Phi(z) and exp(-z^2 / 2).  Phi from Abramowitz & Stegun 7.1.26, Handbook of Mathematical
-// Functions: erf(x) = 1 - (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), x >= 0,
-// to 1.5e-7 (so Phi to 0.75e-7, near fp32's own rounding); its exponential is the density's.
-__device__ __forceinline__ float normal_cdf(float z, float& e)
+__device__ __forceinline__ float2 sigmoid2(float2 z)
 {
-    const float x = fabsf(z) * 0.70710678118654752f;
-    const float t = fast_rcp(fmaf(0.3275911f, x, 1.f));
-    e = fast_exp2(-0.5f * kLog2e * z * z);
-    float w = fmaf(1.061405429f, t, -1.453152027f);
-    w = fmaf(w, t, 1.421413741f);
-    w = fmaf(w, t, -0.284496736f);
-    w = fmaf(w, t, 0.254829592f);
-    const float tail = 0.5f * w * t * e;
-    return z < 0.f ? tail : 1.f - tail;
+    const float2 u = mul2(z, both(-kLog2e));
+    const float2 w = add2(make_float2(fast_exp2(u.x), fast_exp2(u.y)), both(1.f));
+    return make_float2(fast_rcp(w.x), fast_rcp(w.y));
 }
 
-template <int ACT> __device__ __forceinline__ float act_value(float z)
+// Phi(z) and e = exp(-z^2 / 2).  Phi from Abramowitz & Stegun 7.1.26, Handbook of Mathematical
+// Functions: erf(x) = 1 - (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), x >= 0,
+// to 1.5e-7 (so Phi to 0.75e-7, near fp32's own rounding); its exponential is the density's.
+__device__ __forceinline__ float2 normal_cdf2(float2 z, float2& e)
 {
-    if constexpr (ACT == CONV_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
-    if constexpr (ACT == CONV_ACT_SILU) return z * sigmoid(z);
+    constexpr float c = 0.3275911f * 0.70710678118654752f;
+    const float2 t = make_float2(fast_rcp(fmaf(fabsf(z.x), c, 1.f)), fast_rcp(fmaf(fabsf(z.y), c, 1.f)));
+    const float2 u = mul2(mul2(z, both(-0.5f * kLog2e)), z);
+    e = make_float2(fast_exp2(u.x), fast_exp2(u.y));
+    // half of the polynomial: Phi(-|z|) = 0.5 (a1 t + ...) e
+    float2 w = fma2(both(0.5f * 1.061405429f), t, both(0.5f * -1.453152027f));
+    w = fma2(w, t, both(0.5f * 1.421413741f));
+    w = fma2(w, t, both(0.5f * -0.284496736f));
+    w = fma2(w, t, both(0.5f * 0.254829592f));
+    const float2 tail = mul2(mul2(w, t), e);
+    return make_float2(z.x < 0.f ? tail.x : 1.f - tail.x, z.y < 0.f ? tail.y : 1.f - tail.y);
+}
+
+template <int ACT> __device__ __forceinline__ float2 act_value(float2 z)
+{
+    if constexpr (ACT == CONV_ACT_RELU)  // NaN stays
+        return make_float2(z.x < 0.f ? 0.f : z.x + 0.f, z.y < 0.f ? 0.f : z.y + 0.f);
+    if constexpr (ACT == CONV_ACT_SILU) return mul2(z, sigmoid2(z));
     if constexpr (ACT == CONV_ACT_GELU) {
-        float e;
-        return z * normal_cdf(z, e);
+        float2 e;
+        return mul2(z, normal_cdf2(z, e));
     }
     return z;
 }
+template <int ACT> __device__ __forceinline__ float act_value(float z) { return act_value<ACT>(both(z)).x; }
 
-template <int ACT> __device__ __forceinline__ float act_slope(float z)
+// dz = dy * act'(z); a ReLU that is off passes nothing, whatever dy holds there.
+template <int ACT> __device__ __forceinline__ float2 gn_dz(float2 dy, float2 z)
 {
-    if constexpr (ACT == CONV_ACT_SILU) {
-        const float p = sigmoid(z);
-        return fmaf(p * z, 1.f - p, p);
+    if constexpr (ACT == CONV_ACT_RELU) return make_float2(z.x > 0.f ? dy.x : 0.f, z.y > 0.f ? dy.y : 0.f);
+    if constexpr (ACT == CONV_ACT_SILU) {  // p + z p (1 - p)
+        const float2 p = sigmoid2(z);
+        return mul2(dy, fma2(mul2(p, z), add2(both(1.f), mul2(p, both(-1.f))), p));
     }
     if constexpr (ACT == CONV_ACT_GELU) {
-        float e;
-        const float cdf = normal_cdf(z, e);
-        return fmaf(z * 0.39894228040143268f, e, cdf);
+        float2 e;
+        const float2 cdf = normal_cdf2(z, e);
+        return mul2(dy, fma2(mul2(z, both(0.39894228040143268f)), e, cdf));
     }
-    return 1.f;
+    return dy;
 }
+template <int ACT> __device__ __forceinline__ float gn_dz(float dy, float z) { return gn_dz<ACT>(both(dy), both(z)).x; }
 
 // xhat and z by individually rounded operations (no contraction): the forward and the backward
 // then agree on every bit of z, so the backward's ReLU mask is the forward's.
@@ -80,12 +98,18 @@ __device__ __forceinline__ float gn_z(float xhat, float gamma, float beta)
     return __fadd_rn(__fmul_rn(xhat, gamma), beta);
 }
 
-// dz = dy * act'(z); a ReLU that is off passes nothing, whatever dy holds there.
-template <int ACT> __device__ __forceinline__ float gn_dz(float dy, float z)
+// y from d = x - mean, rounded.  The ReLU's forward and backward round z alike, operation by
+// operation, so that their masks agree; the smooth activations take rstd * gamma in one.
+template <int ACT> __device__ __forceinline__ float2 gn_out(float2 d, float2 rstd, float2 gamma_or_scale, float2 beta)
 {
-    if constexpr (ACT == CONV_ACT_NONE) return dy;
-    if constexpr (ACT == CONV_ACT_RELU) return z > 0.f ? dy : 0.f;
-    return dy * act_slope<ACT>(z);
+    if constexpr (ACT == CONV_ACT_RELU) return act_value<ACT>(add2(mul2(mul2(d, rstd), gamma_or_scale), beta));
+    return act_value<ACT>(fma2(d, gamma_or_scale, beta));
+}
+// dz from xhat.
+template <int ACT> __device__ __forceinline__ float2 gn_grad(float2 dy, float2 xhat, float2 gamma, float2 beta)
+{
+    if constexpr (ACT == CONV_ACT_RELU) return gn_dz<ACT>(dy, add2(mul2(xhat, gamma), beta));
+    return gn_dz<ACT>(dy, fma2(xhat, gamma, beta));
 }
 
 // Calls f(integral_constant<ACT>) for the runtime activation.
@@ -161,20 +185,31 @@ __device__ __forceinline__ void gn_team_tables(const GnParams& p, const GnTeam& 
     }
 }
 
-__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
-__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 // Value pair h of K vectors of V values.
 template <typename T, int V, int K> __device__ __forceinline__ float2 pair_of(const Vec<T, V> (&v)[K], int h)
 {
     return make_float2(v[2 * h / V].get(2 * h % V), v[(2 * h + 1) / V].get((2 * h + 1) % V));
 }
-// Pair h of a lane's table entries; toff[k]: where vector k's V floats begin.
-template <int V, int K> __device__ __forceinline__ float2 table_pair(const float* tab, const int (&toff)[K], int h)
+// A lane's table entries as pairs; toff[k]: where vector k's V floats begin.  Read 16 bytes at a
+// time where V allows: consecutive lanes then read consecutive 16 bytes and no bank twice.
+template <int V, int K>
+__device__ __forceinline__ void table_pairs(const float* tab, const int (&toff)[K], float2 (&f)[K * V / 2])
 {
-    if constexpr (V == 1) return make_float2(tab[toff[2 * h]], tab[toff[2 * h + 1]]);
-    else return *reinterpret_cast<const float2*>(tab + toff[2 * h / V] + 2 * h % V);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if constexpr (V >= 4) {
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                const float4 r = *reinterpret_cast<const float4*>(tab + toff[k] + i);
+                f[(k * V + i) / 2] = make_float2(r.x, r.y);
+                f[(k * V + i) / 2 + 1] = make_float2(r.z, r.w);
+            }
+        } else if constexpr (V == 2) {
+            f[k] = *reinterpret_cast<const float2*>(tab + toff[k]);
+        } else if (k % 2 == 0) {
+            f[k / 2] = make_float2(tab[toff[k]], tab[toff[k + 1]]);
+        }
+    }
 }
 
 // s / m for m = p.m with the correctly rounded quotient's bits (one Newton step on s * inv_m), so
@@ -203,19 +238,41 @@ __device__ __forceinline__ float block_total(float v, float* sm, int& turn)
 // ---- large groups kept on chip by a cluster (kernels_gn_cluster.cu) --------------------------
 struct GnCluster {
     int V, S, log_s, threads, K; // vector width, blocks a cluster (and its log2), threads, slots a thread
+    int bufs, chunks;            // tiles a block holds; clusters that share a unit's samples
     int W, cols, lanes, groups;  // NHWC: channels, vectors and groups of a window, rows side by side
     int wins;                    // units a sample
     int vecs;                    // NCHW: vectors of a unit
     int Cg, smem;
-    bool nhwc, ok;
+    bool nhwc, one, ok;          // one: NHWC, a vector lies in one group
+    FastDivmod dm_cols, dm_cg, dm_p, dm_wins;
 };
 GnCluster gn_cluster(const GnParams& p, int dt, const DevInfo& d, bool bwd);
 cudaError_t run_gn_cluster_fwd(const GnParams& p, const GnCluster& q, int dt, const void* x, const void* gamma,
                                const void* beta, void* y, float* mean, float* rstd, cudaStream_t s);
-// part: (B, 2, C) channel sums (dgamma's, dbeta's), or NULL.
+// part: (chunks * S, 2, C) channel sums (dgamma's, dbeta's), or NULL.
 cudaError_t run_gn_cluster_bwd(const GnParams& p, const GnCluster& q, int dt, const void* x, const void* dy,
                                const void* gamma, const void* beta, const float* mean, const float* rstd, void* dx,
                                float* part, cudaStream_t s);
+
+// ---- channels last, large groups: two passes over row tiles (kernels_gn_nhwc.cu) --------------
+struct GnRows {
+    int V, W, cols, wins;        // vector width; channels and vectors of a window, windows a sample
+    int per;                     // windows a group (1: a window holds whole groups)
+    int lanes, threads;          // rows side by side in a block
+    int len, pieces, parts;      // rows a tile, tiles of the sample's rows, partial results of a group
+    int64_t blocks;
+    FastDivmod dm_cols, dm_cg, dm_wins, dm_pieces, dm_per;
+};
+GnRows gn_rows(const GnParams& p, int dt, const DevInfo& d, bool bwd);
+// one position: both layouts are the same
+inline bool gn_by_rows(const GnParams& p) { return p.layout == CONV_LAYOUT_NHWC || p.P == 1; }
+// ws: B * G * parts float2
+cudaError_t run_gn_rows_fwd(const GnParams& p, const GnRows& q, int dt, const void* x, const void* gamma,
+                            const void* beta, void* y, float* mean, float* rstd, void* ws, cudaStream_t s);
+// part: (B * pieces, 2, C) channel sums (dgamma's, dbeta's), or NULL.
+cudaError_t run_gn_rows_bwd(const GnParams& p, const GnRows& q, int dt, const void* x, const void* dy,
+                            const void* gamma, const void* beta, const float* mean, const float* rstd, void* dx,
+                            float* part, void* ws, cudaStream_t s);
 
 // ---- groups that no cluster holds: pieces of rows --------------------------------------------
 // NHWC: a piece is a range of a sample's positions, all channels of a column window; NCHW: a

@@ -80,20 +80,22 @@ gn_team_bwd(const GnParams p, const GnTeam q, const T* x, const T* dy, const T* 
             dg[h] = pair_of<T, V, K>(rd, h);
         }
         if (it + 1 < iters) fetch(b + step);
-        if (p.act != CONV_ACT_NONE)
+        float2 ga[H];
+        table_pairs<V, K>(gam, toff, ga);
+        if (p.act != CONV_ACT_NONE) {
+            float2 be[H];
+            table_pairs<V, K>(bet, toff, be);
             with_act(p.act, [&](auto act) {
 #pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    const float2 z = add2(mul2(xh[h], table_pair<V, K>(gam, toff, h)), table_pair<V, K>(bet, toff, h));
-                    dg[h] = make_float2(gn_dz<act.value>(dg[h].x, z.x), gn_dz<act.value>(dg[h].y, z.y));
-                }
+                for (int h = 0; h < H; ++h) dg[h] = gn_dz<act.value>(dg[h], add2(mul2(xh[h], ga[h]), be[h]));
             });
+        }
         // a lane's vectors beyond the group have zeros for dy and add nothing
 #pragma unroll
         for (int h = 0; h < H; ++h) {
             sb[h] = add2(sb[h], dg[h]);
             sg[h] = fma2(dg[h], xh[h], sg[h]);
-            dg[h] = mul2(dg[h], table_pair<V, K>(gam, toff, h));
+            dg[h] = mul2(dg[h], ga[h]);
             s1 = add2(s1, dg[h]);
             s2 = fma2(dg[h], xh[h], s2);
         }
@@ -472,7 +474,15 @@ cudaError_t bwd_t(const GnParams& p, int dt, const DevInfo& d, const T* x, const
     const GnCluster cl = gn_cluster(p, dt, d, true);
     if (cl.ok) {
         e = run_gn_cluster_bwd(p, cl, dt, x, dy, gamma, beta, mean, rstd, dx, dgamma ? part : nullptr, s);
-        if (e == cudaSuccess && dgamma) e = chan_sum<T>(p, p.B, 2 * int64_t(p.C), p.C, part, dgamma, dbeta, s);
+        if (e == cudaSuccess && dgamma) e = chan_sum<T>(p, int64_t(cl.chunks) * cl.S, 2 * int64_t(p.C), p.C, part, dgamma, dbeta, s);
+        return e != cudaSuccess ? e : cudaGetLastError();
+    }
+    if (gn_by_rows(p)) {
+        const GnRows q = gn_rows(p, dt, d, true);
+        float* rows = part + 2 * int64_t(p.B) * p.G * q.parts;
+        e = run_gn_rows_bwd(p, q, dt, x, dy, gamma, beta, mean, rstd, dx, dgamma ? rows : nullptr, ws, s);
+        if (e == cudaSuccess && dgamma)
+            e = chan_sum<T>(p, int64_t(p.B) * q.pieces, 2 * int64_t(p.C), p.C, rows, dgamma, dbeta, s);
         return e != cudaSuccess ? e : cudaGetLastError();
     }
     const GnPieces q = gn_pieces(p, dt, d);
@@ -516,7 +526,12 @@ size_t gn_bwd_workspace(const GnParams& p, int dt, const DevInfo& d)
     if (p.B == 0) return 0;
     const GnTeam t = gn_team(p, dt, d, true);
     if (t.ok) return size_t(8) * t.chunks * p.C;
-    if (gn_cluster(p, dt, d, true).ok) return size_t(8) * p.B * p.C;
+    const GnCluster cl = gn_cluster(p, dt, d, true);
+    if (cl.ok) return size_t(8) * cl.chunks * cl.S * p.C;
+    if (gn_by_rows(p)) {
+        const GnRows q = gn_rows(p, dt, d, true);
+        return size_t(8) * (size_t(p.B) * p.G * q.parts + size_t(p.B) * q.pieces * p.C);
+    }
     const GnPieces q = gn_pieces(p, dt, d);
     return size_t(4) * (2 * size_t(p.B) * p.C * q.pieces + 2 * size_t(p.B) * p.G);
 }

@@ -2,32 +2,37 @@
 // thread-block cluster of S blocks holds a unit (NCHW: one group of a sample; NHWC: a sample's
 // positions of a window of whole groups) in its shared memory, so x (and dy) are read from
 // memory once.  A thread copies its own vectors asynchronously into its own slots and is the
-// only one to read them: the tile is an extension of its registers and needs no barrier.  The
-// blocks exchange their groups' partial results through distributed shared memory, once.
+// only one to read them: the tile is an extension of its registers and needs no barrier.
+//
+// A cluster walks the samples with its groups fixed.  Where two tiles fit, the next sample is
+// copied while this one is computed.  What is set up once -- indices, gamma and beta, the
+// backward's channel sums, kept per value's place and added up when the cluster ends -- is most
+// of the instructions of a small unit.  Per sample the blocks exchange their groups' partial
+// results through distributed shared memory, with one cluster barrier.
 //
 // Bound by memory: the tile is written once and read three times (forward: sum, squares, result)
 // or twice (backward: sums, result) at shared-memory speed, about a third of its rate when HBM
-// is saturated; two blocks an SM (where the unit allows) let one load while the other computes.
+// is saturated.
 #include "gn_common.cuh"
 
 namespace igc {
 
 namespace {
 
-constexpr int GC_MAX_CG = 2048;            // channels of a group (NCHW: their gammas sit in shared memory)
-constexpr int GC_TWO = 110 * 1024;         // shared memory of a block when two share an SM
-constexpr int GC_ONE = 220 * 1024;
-constexpr int GC_VECS = 16;                // vectors a thread, about
+constexpr int GC_MAX_CG = 2048;            // channels of a group (their gammas sit in shared memory)
+constexpr int GC_SMEM = 110 * 1024;        // of a block: two share an SM, or each waits with its SM
 constexpr int GC_THREADS = 512;
+constexpr int GC_SPAN_THREADS = 256;       // NHWC, vectors in two groups: more registers a thread
+constexpr int GC_WARPS = GC_THREADS / 32;
+constexpr int GC_FWD_BYTES = 256, GC_BWD_BYTES = 96;  // of x a thread holds, at most where the block can grow
 
 }  // namespace
 
-// Bytes of shared memory beside the tile.
+// Bytes of shared memory beside the tiles.
 static int gc_extra(const GnCluster& q, bool bwd)
 {
-    if (q.nhwc && bwd) return 8 * (q.threads * q.V + q.threads + q.W + 1) + 16 * q.W + 16 * q.groups;
-    if (q.nhwc) return 16 * q.threads + 8 * q.W + 16 * q.groups;
-    return 4 * (2 * q.Cg + 64) + (bwd ? 8 * (q.K * q.threads + 2 * q.Cg) : 0);
+    if (q.nhwc) return 16 * q.threads + 16 * GC_WARPS + 8 * q.W + 32 * q.groups + (bwd ? 8 * q.threads : 0);
+    return 4 * 2 * (q.Cg + 1) + 32 * GC_WARPS + 64 + (bwd ? 8 * (q.K * q.threads + q.Cg + 1) : 0);
 }
 
 GnCluster gn_cluster(const GnParams& p, int dt, const DevInfo& d, bool bwd)
@@ -39,56 +44,86 @@ GnCluster gn_cluster(const GnParams& p, int dt, const DevInfo& d, bool bwd)
     q.nhwc = nhwc;
     q.Cg = p.Cg;
     q.V = 16 / es;
-    // a vector lies in two groups (NHWC) or two channels (NCHW) at most
-    if (nhwc) while (p.C % q.V != 0 || q.V > p.Cg) q.V /= 2;
-    else while (p.M % q.V != 0 || q.V > p.P) q.V /= 2;
+    // A vector lies in two groups (NHWC) or two channels (NCHW) at most.  In the channels-last
+    // backward one of two groups has at most 4 values: its sums take registers by place.
+    if (nhwc) {
+        while (p.C % q.V != 0 || (p.Cg % q.V != 0 && q.V > std::min(bwd ? 4 : 8, p.Cg))) q.V /= 2;
+        q.one = p.Cg % q.V == 0;
+    } else {
+        while (p.M % q.V != 0 || q.V > p.P) q.V /= 2;
+    }
     const int tiles = bwd ? 2 : 1, vb = q.V * es;
     if (p.Cg > GC_MAX_CG) return q;
     int lcm = p.Cg;
     while (lcm % q.V != 0) lcm += p.Cg;
     // NHWC: windows of whole vectors and whole groups, 64 bytes of a row (two sectors) or less.
-    // Two blocks an SM come before wide rows and small clusters: a block alone on its SM waits
-    // with it.
     const int widest = nhwc ? std::max(1, std::min(ceil_div(64, lcm * es), ceil_div(p.C, lcm))) : 1;
-    for (const int limit : {GC_TWO, std::min(GC_ONE, d.smem_optin - 1024)})
-        for (int m = widest; m >= 1; --m) {
-            int64_t vecs;  // of the unit
-            if (nhwc) {
-                q.W = std::min(m * lcm, p.C);
-                q.cols = q.W / q.V;
-                q.groups = q.W / p.Cg;
-                q.wins = ceil_div(p.C, q.W);
-                if (q.cols > GC_THREADS) continue;
-                vecs = int64_t(p.P) * q.cols;
-            } else {
-                q.wins = p.G;
-                vecs = p.M / q.V;
-                q.vecs = int(vecs);
-            }
-            const int64_t units = int64_t(p.B) * q.wins;
-            if (units * kMaxCluster > 0x7FFFFFFF) return q;
-            const int most = int(std::min<int64_t>(kMaxCluster, nhwc ? p.P : vecs / 32 + 1));
-            for (int S = 1, log = 0; S <= most; S *= 2, ++log) {
-                const int64_t per = (vecs + S - 1) / S;
-                int T = 32;
-                while (T < (bwd && limit == GC_TWO ? 256 : GC_THREADS) && per > int64_t(T) * GC_VECS) T *= 2;
-                if (nhwc) while (T < q.cols) T *= 2;
-                q.S = S;
-                q.log_s = log;
-                q.threads = T;
-                q.lanes = nhwc ? T / q.cols : 1;
-                const int64_t K = nhwc ? (ceil_div(p.P, S) + q.lanes - 1) / q.lanes : (per + T - 1) / T;
-                if (K * T * vb * tiles > limit) continue;
-                q.K = int(K);
-                q.smem = q.K * T * vb * tiles + gc_extra(q, bwd);
-                if (q.smem > limit) continue;
-                // larger clusters while the SMs are not filled and the blocks still have a few
-                // kilobytes each
-                if (S * 2 <= most && units * S < 2 * d.sms && per * vb > 4096) continue;
-                q.ok = true;
-                return q;
-            }
+    const int most_threads = nhwc && !q.one ? GC_SPAN_THREADS : GC_THREADS;
+    for (int m = widest; m >= 1; --m) {
+        int64_t vecs;  // of the unit
+        if (nhwc) {
+            q.W = std::min(m * lcm, p.C);
+            q.cols = q.W / q.V;
+            q.groups = q.W / p.Cg;
+            q.wins = ceil_div(p.C, q.W);
+            if (q.cols > most_threads) continue;
+            vecs = int64_t(p.P) * q.cols;
+        } else {
+            q.wins = p.G;
+            vecs = p.M / q.V;
+            q.vecs = int(vecs);
         }
+        const int64_t units = int64_t(p.B) * q.wins;
+        if (units * kMaxCluster > 0x7FFFFFFF) return q;
+        const int most = int(std::min<int64_t>(kMaxCluster, nhwc ? p.P : vecs / 32 + 1));
+        for (int S = 1, log = 0; S <= most; S *= 2, ++log) {
+            const int64_t per = (vecs + S - 1) / S;
+            // Threads: so many that each holds about GC_*_BYTES; of those up to twice as many,
+            // the count that leaves the fewest slots empty.
+            auto slots = [&](int T) {
+                const int lanes = nhwc ? T / q.cols : 1;
+                return nhwc ? (int64_t(ceil_div(p.P, S)) + lanes - 1) / lanes : (per + T - 1) / T;
+            };
+            const int bytes = bwd ? GC_BWD_BYTES : GC_FWD_BYTES;
+            int lo = nhwc ? round_up(q.cols, 32) : 32;
+            lo = int(std::min<int64_t>(most_threads, std::max<int64_t>(lo, (per * vb + bytes * 32 - 1) / (bytes * 32) * 32)));
+            int T = lo;
+            for (int t = lo + 32; t <= std::min(most_threads, 2 * lo); t += 32)
+                if (slots(t) * t < slots(T) * T) T = t;
+            q.S = S;
+            q.log_s = log;
+            q.threads = T;
+            q.lanes = nhwc ? T / q.cols : 1;
+            const int64_t K = slots(T);
+            if (K * T * vb * tiles > GC_SMEM) continue;
+            q.K = int(K);
+            const int tile = q.K * T * vb * tiles;
+            q.smem = tile + gc_extra(q, bwd);
+            if (q.smem > GC_SMEM) continue;
+            // larger clusters while the SMs are not filled and the blocks still have a few
+            // kilobytes each
+            if (S * 2 <= most && units * S < 2 * d.sms && per * vb > 4096) continue;
+            // Blocks an SM by registers (64 a thread) and by shared memory.  A second tile only
+            // where the cluster walks several samples and the SM keeps its threads: a block
+            // that waits less is worth less than another block (24 x 72 x 72 x 320 bf16
+            // forward: 78 us with two tiles and 2 blocks of 256 an SM, 55 with one and 3).
+            const int by_regs = std::max(1, std::min(32, (nhwc && !q.one ? 768 : 1024) / T));
+            auto per_sm = [&](int smem) { return std::min(by_regs, (227 * 1024) / (smem + 1024)); };
+            q.bufs = 1;
+            int64_t want = std::max<int64_t>(1, int64_t(d.sms) * per_sm(q.smem) / (int64_t(q.wins) * S));
+            if (want < p.B && q.smem + tile <= GC_SMEM && per_sm(q.smem + tile) == per_sm(q.smem)) {
+                q.bufs = 2;
+                q.smem += tile;
+            }
+            q.chunks = int(std::min<int64_t>(p.B, want));
+            q.dm_cols = FastDivmod(uint32_t(std::max(1, q.cols)));
+            q.dm_cg = FastDivmod(uint32_t(p.Cg));
+            q.dm_p = FastDivmod(uint32_t(p.P));
+            q.dm_wins = FastDivmod(uint32_t(q.wins));
+            q.ok = true;
+            return q;
+        }
+    }
     return q;
 }
 
@@ -101,7 +136,8 @@ template <int BYTES> __device__ __forceinline__ void copy_async(uint32_t dst, co
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
 template <typename T, int V> __device__ __forceinline__ void fetch_vec(unsigned char* slot, const T* src)
 {
@@ -114,715 +150,855 @@ template <typename T, int V> __device__ __forceinline__ void fetch_vec(unsigned 
     }
 }
 
-// The cluster barrier in two halves (the warp has to be converged for each).
-__device__ __forceinline__ void cluster_arrive()
+// The cluster barrier (the warp has to be converged for it).
+__device__ __forceinline__ void cluster_barrier()
 {
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait()
-{
-    __syncwarp();
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    tc::cluster_sync();
 }
 
 // Where block r's part of n items begins (S is a power of two).
 __device__ __forceinline__ int gc_cut(int n, const GnCluster& q, int r) { return int((int64_t(n) * r) >> q.log_s); }
 
-// The unit of an NHWC block: rows [r0, r1) of its window; thread (lane, col) holds the vector
-// `col` of the rows r0 + lane, r0 + lane + lanes, ...
-struct GcTile {
-    int b, rank, c0, W, groups, g0, lane, col, r0, r1, mine;
-    int g, split;  // the group (in the window) of the vector's first channel, its channels in that group
-    bool in;
-    __device__ __forceinline__ GcTile(const GnParams& p, const GnCluster& q, int V)
-    {
-        rank = q.S > 1 ? int(tc::cluster_rank()) : 0;
-        const int unit = int(blockIdx.x) / q.S;
-        b = unit / q.wins;
-        c0 = (unit - b * q.wins) * q.W;
-        W = min(q.W, p.C - c0);
-        groups = W / p.Cg;
-        g0 = c0 / p.Cg;
-        lane = int(threadIdx.x) / q.cols;
-        col = int(threadIdx.x) - lane * q.cols;
-        in = lane < q.lanes && col * V < W;
-        r0 = gc_cut(p.P, q, rank);
-        r1 = gc_cut(p.P, q, rank + 1);
-        mine = in ? max(0, (r1 - r0 - lane + q.lanes - 1) / q.lanes) : 0;
-        g = in ? col * V / p.Cg : 0;
-        split = in ? min(V, (g + 1) * p.Cg - col * V) : V;
-    }
-};
-__device__ __forceinline__ float gc_rows(const GnParams& p, const GnCluster& q, int r)
-{
-    return float(gc_cut(p.P, q, r + 1) - gc_cut(p.P, q, r));
-}
 // A vector's values as pairs; one value: (value, 0).
 template <int V> constexpr int gc_pairs() { return (V + 1) / 2; }
-template <typename T, int V> __device__ __forceinline__ void gc_unpack(const Vec<T, V>& v, float2 (&f)[gc_pairs<V>()])
+template <typename T, int V>
+__device__ __forceinline__ void gc_load(const unsigned char* slot, float2 (&f)[gc_pairs<V>()])
 {
+    Vec<T, V> v;
+    v.load(reinterpret_cast<const T*>(slot));
 #pragma unroll
     for (int h = 0; h < gc_pairs<V>(); ++h) f[h] = make_float2(v.get(2 * h), 2 * h + 1 < V ? v.get(2 * h + 1) : 0.f);
 }
-template <typename T, int V> __device__ __forceinline__ void gc_pack(Vec<T, V>& v, const float2 (&f)[gc_pairs<V>()])
+template <typename T, int V> __device__ __forceinline__ void gc_store(T* p, const float2 (&f)[gc_pairs<V>()])
 {
     float r[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) r[i] = i % 2 ? f[i / 2].y : f[i / 2].x;
+    Vec<T, V> v;
     v.set(r);
+    v.store(p);
+}
+
+// n, mean and M2 of the values of two sets.
+struct Moments {
+    float n, mean, m2;
+    __device__ __forceinline__ void merge(float n2, float mean2, float m22)
+    {
+        if (n2 == 0.f) return;
+        const float t = n + n2, dlt = mean2 - mean, w = __fdividef(n2, t);
+        mean = n == 0.f ? mean2 : fmaf(dlt, w, mean);
+        m2 += m22 + dlt * dlt * n * w;
+        n = t;
+    }
+};
+
+// The blocks' results of one value each (mean, M2) merged over the cluster: the unit's mean and
+// rstd.  addr: the pair's shared address, the same in every block; count(r): block r's values.
+template <class F>
+__device__ __forceinline__ float2 gc_exchange(const GnParams& p, const GnCluster& q, uint32_t addr, F&& count)
+{
+    float mu[kMaxCluster], m2[kMaxCluster], sum = 0.f, sq = 0.f;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+        if (r < q.S) {
+            mu[r] = tc::ld_dsmem_f32(tc::dsmem_addr(addr, r));
+            m2[r] = tc::ld_dsmem_f32(tc::dsmem_addr(addr + 4, r));
+        }
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+        if (r < q.S) sum += mu[r] * count(r);
+    const float m = __fdiv_rn(sum, p.m);
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+        if (r < q.S) {
+            const float dlt = mu[r] - m;
+            sq += m2[r] + dlt * dlt * count(r);
+        }
+    return make_float2(m, rsqrtf(sq * p.inv_m + p.eps));
+}
+// The blocks' sums of a pair added up.
+__device__ __forceinline__ float2 gc_add(const GnCluster& q, uint32_t addr)
+{
+    float a[kMaxCluster], b[kMaxCluster];
+    float2 s = both(0.f);
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+        if (r < q.S) {
+            a[r] = tc::ld_dsmem_f32(tc::dsmem_addr(addr, r));
+            b[r] = tc::ld_dsmem_f32(tc::dsmem_addr(addr + 4, r));
+        }
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+        if (r < q.S) s = add2(s, make_float2(a[r], b[r]));
+    return s;
 }
 
 // ---- channels last ---------------------------------------------------------------------------
-template <typename T, int V>
-__global__ void __launch_bounds__(GC_THREADS, 2)
-gn_cluster_fwd_nhwc(const GnParams p, const GnCluster q, const T* x, const T* gamma, const T* beta, T* y,
-                    float* mean_out, float* rstd_out)
-{
-    extern __shared__ __align__(16) unsigned char dyn[];
-    constexpr int VB = V * int(sizeof(T)), H = gc_pairs<V>();
-    const GcTile t(p, q, V);
-    const int nt = int(blockDim.x), hop = nt * VB;
-    unsigned char* slot = dyn + threadIdx.x * VB;
-    float4* rec = reinterpret_cast<float4*>(dyn + size_t(q.K) * hop);  // threads x (mean, M2) of either group
-    float* gs = reinterpret_cast<float*>(rec + nt);   // groups x (mean, M2) of the block, read by the others
-    float* stat = gs + 2 * q.groups;                  // groups x (mean, rstd) of the unit
-    float* gb = stat + 2 * q.groups;                  // W gammas, W betas
-    const int64_t at = int64_t(t.b) * p.N + t.c0 + t.col * V;
-    tc::grid_dep_wait();
-    for (int k = 0, r = t.r0 + t.lane; k < t.mine; ++k, r += q.lanes)
-        fetch_vec<T, V>(slot + k * hop, x + at + int64_t(r) * p.C);
-    for (int c = threadIdx.x; c < t.W; c += nt) {
-        gb[c] = gamma ? Elem<T>::ldg(gamma + t.c0 + c) : 1.f;
-        gb[q.W + c] = beta ? Elem<T>::ldg(beta + t.c0 + c) : 0.f;
-    }
-    copy_wait();
-    // The thread's mean of its values of either group, then the squares about it.
+// Block `rank` of a cluster holds the rows [r0, r1) of a window of W channels; thread (lane, col)
+// the vector `col` of the rows r0 + lane, r0 + lane + lanes, ...
+struct GcTile {
+    int rank, chunk, c0, W, groups, g0, lane, col, r0, r1, mine, full, extra;
+    int g, split;  // the group (in the window) of the vector's first channel, its channels in that group
+    __device__ __forceinline__ GcTile(const GnParams& p, const GnCluster& q, int V)
     {
-        float2 s[H], mu[H];
-        float m0 = 0.f, m1 = 0.f;
-#pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {
-#pragma unroll
-            for (int h = 0; h < H; ++h) {
-                s[h] = both(0.f);
-                mu[h] = make_float2(2 * h < t.split ? -m0 : -m1, 2 * h + 1 < t.split ? -m0 : -m1);
-                if (V == 1) mu[h].y = 0.f;
-            }
-#pragma unroll 2
-            for (int k = 0; k < t.mine; ++k) {
-                Vec<T, V> v;
-                float2 f[H];
-                v.load(reinterpret_cast<const T*>(slot + k * hop));
-                gc_unpack<T, V>(v, f);
-                if (pass == 0) {
-#pragma unroll
-                    for (int h = 0; h < H; ++h) s[h] = add2(s[h], f[h]);
-                } else {
-#pragma unroll
-                    for (int h = 0; h < H; ++h) {
-                        f[h] = add2(f[h], mu[h]);
-                        s[h] = fma2(f[h], f[h], s[h]);
-                    }
-                }
-            }
-            float a = 0.f, b = 0.f;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float e = i % 2 ? s[i / 2].y : s[i / 2].x;
-                a += i < t.split ? e : 0.f;
-                b += i < t.split ? 0.f : e;
-            }
-            if (pass == 0) {
-                m0 = t.mine ? __fdiv_rn(a, float(t.mine * t.split)) : 0.f;
-                m1 = t.mine && t.split < V ? __fdiv_rn(b, float(t.mine * (V - t.split))) : 0.f;
-            } else {
-                rec[threadIdx.x] = make_float4(m0, a, m1, b);
-            }
-        }
+        uint32_t a, b;
+        rank = q.S > 1 ? int(tc::cluster_rank()) : 0;
+        q.dm_wins.divmod(blockIdx.x >> q.log_s, a, b);
+        chunk = int(a);
+        c0 = int(b) * q.W;
+        W = min(q.W, p.C - c0);
+        groups = int(q.dm_cg.div(uint32_t(W)));
+        g0 = int(q.dm_cg.div(uint32_t(c0)));
+        q.dm_cols.divmod(threadIdx.x, a, b);
+        lane = int(a);
+        col = int(b);
+        r0 = gc_cut(p.P, q, rank);
+        r1 = gc_cut(p.P, q, rank + 1);
+        full = (r1 - r0) / q.lanes;
+        extra = r1 - r0 - full * q.lanes;
+        const bool in = lane < q.lanes && col * V < W;
+        mine = in ? full + (lane < extra) : 0;
+        g = in ? int(q.dm_cg.div(uint32_t(col * V))) : 0;
+        split = in ? min(V, (g + 1) * p.Cg - col * V) : V;
     }
-    __syncthreads();
-    // A warp a group: the mean over its threads' means, then the squares about it.
-    const int full = (t.r1 - t.r0) / q.lanes, extra = (t.r1 - t.r0) - full * q.lanes;
-    for (int g = int(threadIdx.x >> 5); g < t.groups; g += nt >> 5) {
-        const int ca = g * p.Cg, va = ca / V, vb = (ca + p.Cg - 1) / V;
-        float mean = 0.f, m2 = 0.f;
-#pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {
-            float s = 0.f;
-            for (int cv = va; cv <= vb; ++cv) {
-                const bool later = cv * V < ca;  // the vector begins in the group before
-                const int width = min(ca + p.Cg, cv * V + V) - max(ca, cv * V);
-#pragma unroll 2
-                for (int l = int(threadIdx.x & 31); l < q.lanes; l += 32) {
-                    const float4 r = rec[l * q.cols + cv];
-                    const float n = float((full + (l < extra)) * width);
-                    const float mu = later ? r.z : r.x, dlt = mu - mean;
-                    s += pass == 0 ? n * mu : (later ? r.w : r.y) + n * dlt * dlt;
-                }
-            }
-            s = warp_sum(s);
-            if (pass == 0) mean = __fdiv_rn(s, gc_rows(p, q, t.rank) * float(p.Cg));
-            else m2 = s;
-        }
-        if ((threadIdx.x & 31) == 0) {
-            gs[2 * g] = mean;
-            gs[2 * g + 1] = m2;
-            if (q.S == 1) {
-                stat[2 * g] = mean;
-                stat[2 * g + 1] = rsqrtf(m2 * p.inv_m + p.eps);
-            }
-        }
+    __device__ __forceinline__ float rows(const GnParams& p, const GnCluster& q, int r) const
+    {
+        return float(gc_cut(p.P, q, r + 1) - gc_cut(p.P, q, r));
     }
-    if (q.S > 1) {
-        cluster_arrive(), cluster_wait();
-        const uint32_t base = tc::smem_u32(gs);
-        for (int g = threadIdx.x; g < t.groups; g += nt) {
-            float mu[8], m2[8], sum = 0.f, sq = 0.f;
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-                if (r < q.S) {
-                    mu[r] = tc::ld_dsmem_f32(tc::dsmem_addr(base + 8 * g, r));
-                    m2[r] = tc::ld_dsmem_f32(tc::dsmem_addr(base + 8 * g + 4, r));
-                }
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-                if (r < q.S) sum += mu[r] * (gc_rows(p, q, r) * float(p.Cg));
-            const float m = __fdiv_rn(sum, p.m);
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-                if (r < q.S) {
-                    const float dlt = mu[r] - m;
-                    sq += m2[r] + dlt * dlt * (gc_rows(p, q, r) * float(p.Cg));
-                }
-            stat[2 * g] = m;
-            stat[2 * g + 1] = rsqrtf(sq * p.inv_m + p.eps);
-        }
-        cluster_arrive();  // this block has read what it needs from the others
-    }
-    __syncthreads();
-    if (mean_out && t.rank == 0)
-        for (int g = threadIdx.x; g < t.groups; g += nt) {
-            mean_out[int64_t(t.b) * p.G + t.g0 + g] = stat[2 * g];
-            rstd_out[int64_t(t.b) * p.G + t.g0 + g] = stat[2 * g + 1];
-        }
-    if (t.mine) {
-        float2 mu[H], rs[H], ga[H], be[H];
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-            const int ca = t.col * V + 2 * h, cb = min(ca + 1, t.col * V + V - 1);
-            const int ka = t.g + (2 * h >= t.split), kb = t.g + (cb - t.col * V >= t.split);
-            mu[h] = make_float2(-stat[2 * ka], -stat[2 * kb]);
-            rs[h] = make_float2(stat[2 * ka + 1], stat[2 * kb + 1]);
-            ga[h] = make_float2(gb[ca], gb[cb]);
-            be[h] = make_float2(gb[q.W + ca], gb[q.W + cb]);
-        }
-        T* py = y + at + int64_t(t.r0 + t.lane) * p.C;
-        const int64_t row_hop = int64_t(q.lanes) * p.C;
-        with_act(p.act, [&](auto act) {
+};
+
+// Warps that share a group (a power of two).
+__device__ __forceinline__ int gc_subs(int groups)
+{
+    int subs = 1;
+    while (subs * 2 * groups <= int(blockDim.x) >> 5) subs *= 2;
+    return subs;
+}
+// Hands every warp its share of a group's vectors: f(group, sub, for_each), where for_each(e)
+// calls e(column vector, row lane) for the lane's part of the share.
+template <int V, class F>
+__device__ __forceinline__ void gc_group_warps(const GnParams& p, const GnCluster& q, const GcTile& t, int subs, F&& f)
+{
+    const int nw = int(blockDim.x) >> 5, lane = int(threadIdx.x & 31);
+    int lw = 1;  // row lanes side by side in the warp
+    while (lw < 32 && lw * 2 <= q.lanes) lw *= 2;
+    const int l0 = lane & (lw - 1), across = 32 / lw;
+    for (int i = int(threadIdx.x) >> 5; i < t.groups * subs; i += nw) {
+        const int g = i / subs, sub = i - g * subs;
+        const int v0 = g * p.Cg / V, v1 = (g * p.Cg + p.Cg - 1) / V;
+        f(g, sub, [&](auto&& e) {
+            for (int cv = v0 + sub * across + lane / lw; cv <= v1; cv += subs * across)
 #pragma unroll 2
-            for (int k = 0; k < t.mine; ++k) {
-                Vec<T, V> v;
-                float2 f[H];
-                v.load(reinterpret_cast<const T*>(slot + k * hop));
-                gc_unpack<T, V>(v, f);
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    f[h] = add2(mul2(mul2(add2(f[h], mu[h]), rs[h]), ga[h]), be[h]);
-                    f[h] = make_float2(act_value<act.value>(f[h].x), act_value<act.value>(f[h].y));
-                }
-                gc_pack<T, V>(v, f);
-                v.store(py + k * row_hop);
-            }
+                for (int l = l0; l < q.lanes; l += lw) e(cv, l);
         });
     }
-    if (q.S > 1) cluster_wait();  // no block leaves while another still reads its shared memory
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(GC_THREADS, 1)
-gn_cluster_bwd_nhwc(const GnParams p, const GnCluster q, const T* x, const T* dy, const T* gamma, const T* beta,
-                    const float* mean, const float* rstd, T* dx, float* part)
+template <typename T, int V, bool ONE>
+__global__ void __launch_bounds__(ONE ? GC_THREADS : GC_SPAN_THREADS, ONE ? 2 : 3)
+gn_cluster_fwd_nhwc(const GnParams p, const __grid_constant__ GnCluster q, const T* x, const T* gamma, const T* beta,
+                    T* y, float* mean_out, float* rstd_out)
 {
     extern __shared__ __align__(16) unsigned char dyn[];
     constexpr int VB = V * int(sizeof(T)), H = gc_pairs<V>();
     const GcTile t(p, q, V);
     const int nt = int(blockDim.x), hop = nt * VB, tile = q.K * hop;
     unsigned char* slot = dyn + threadIdx.x * VB;
-    float2* red = reinterpret_cast<float2*>(dyn + 2 * size_t(tile));  // lanes x W (sum dz*xhat, sum dz)
-    float2* red2 = red + nt * V;
-    float2* col = red2 + nt;                          // W: the block's channel sums, read by the others
-    float2* gs = col + q.W;                           // groups x (sum dz*gamma*xhat, sum dz*gamma), read by the others
-    float2* gt = gs + q.groups;                       // groups x (m2, m1) of the unit
-    float4* cp = reinterpret_cast<float4*>(gt + q.groups + (q.W & 1));  // W x (-mean, rstd, gamma, beta)
-    const int64_t at = int64_t(t.b) * p.N + t.c0 + t.col * V;
+    float4* rec = reinterpret_cast<float4*>(dyn + size_t(q.bufs) * tile);  // threads x (mean, M2) of either group
+    float4* wrec = rec + nt;                                   // warps x (n, mean, M2) of their share of a group
+    float2* gs = reinterpret_cast<float2*>(wrec + GC_WARPS);   // 2 x groups (mean, M2) of the block, read by the others
+    float2* stat = gs + 2 * q.groups;                          // groups x (mean, rstd) of the unit
+    const int64_t at = t.c0 + t.col * V + int64_t(t.r0 + t.lane) * p.C, row_hop = int64_t(q.lanes) * p.C;
+    auto issue = [&](int b, int buf) {
+        const T* src = x + int64_t(b) * p.N + at;
+        unsigned char* dst = slot + buf * tile;
+        for (int k = 0; k < t.mine; ++k, src += row_hop, dst += hop) fetch_vec<T, V>(dst, src);
+        copy_commit();
+    };
     tc::grid_dep_wait();
-    for (int k = 0, r = t.r0 + t.lane; k < t.mine; ++k, r += q.lanes) {
-        fetch_vec<T, V>(slot + k * hop, x + at + int64_t(r) * p.C);
-        fetch_vec<T, V>(slot + tile + k * hop, dy + at + int64_t(r) * p.C);
-    }
-    for (int c = threadIdx.x; c < t.W; c += nt) {
-        const int64_t g = int64_t(t.b) * p.G + t.g0 + c / p.Cg;
-        cp[c] = make_float4(-mean[g], rstd[g], gamma ? Elem<T>::ldg(gamma + t.c0 + c) : 1.f,
-                            beta ? Elem<T>::ldg(beta + t.c0 + c) : 0.f);
-    }
-    copy_wait();
-    __syncthreads();
-    float2 mu[H], rs[H], ga[H], be[H];
+    if (q.bufs == 2) issue(t.chunk, 0);
+    float2 ga[H], be[H];
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-        const int c = t.in ? t.col * V + 2 * h : 0;
-        const float4 a = cp[c], b = cp[2 * h + 1 < V ? c + 1 : c];
-        mu[h] = make_float2(a.x, b.x);
-        rs[h] = make_float2(a.y, b.y);
-        ga[h] = make_float2(a.z, b.z);
-        be[h] = make_float2(a.w, b.w);
+        const int a = t.c0 + (t.mine ? t.col * V : 0) + 2 * h, b = V > 1 ? a + 1 : a;
+        ga[h] = gamma ? make_float2(Elem<T>::ldg(gamma + a), Elem<T>::ldg(gamma + b)) : both(1.f);
+        be[h] = beta ? make_float2(Elem<T>::ldg(beta + a), Elem<T>::ldg(beta + b)) : both(0.f);
     }
-    {
-        float2 sg[H], sb[H];
-#pragma unroll
-        for (int h = 0; h < H; ++h) sg[h] = sb[h] = both(0.f);
-        with_act(p.act, [&](auto act) {
-#pragma unroll 2
-            for (int k = 0; k < t.mine; ++k) {
-                Vec<T, V> v;
-                float2 xh[H], dz[H];
-                v.load(reinterpret_cast<const T*>(slot + k * hop));
-                gc_unpack<T, V>(v, xh);
-                v.load(reinterpret_cast<const T*>(slot + tile + k * hop));
-                gc_unpack<T, V>(v, dz);
+    const int subs = gc_subs(t.groups);
+    int turn = 0;
+    for (int b = t.chunk; b < p.B; b += q.chunks, turn ^= 1) {
+        const unsigned char* my = slot;
+        if (q.bufs == 2) {
+            my += turn * tile;
+            if (b + q.chunks < p.B) {
+                issue(b + q.chunks, turn ^ 1);
+                copy_wait<1>();
+            } else {
+                copy_wait<0>();
+            }
+        } else {
+            issue(b, 0);
+            copy_wait<0>();
+        }
+        // The thread's mean of its values of either group, then the squares about it.
+        {
+            float m0 = 0.f, m1 = 0.f;
+#pragma unroll 1
+            for (int pass = 0; pass < 2; ++pass) {
+                float2 s[H], mu[H];
 #pragma unroll
                 for (int h = 0; h < H; ++h) {
-                    xh[h] = mul2(add2(xh[h], mu[h]), rs[h]);
-                    const float2 z = add2(mul2(xh[h], ga[h]), be[h]);
-                    dz[h] = make_float2(gn_dz<act.value>(dz[h].x, z.x), gn_dz<act.value>(dz[h].y, z.y));
-                    sb[h] = add2(sb[h], dz[h]);
-                    sg[h] = fma2(dz[h], xh[h], sg[h]);
+                    s[h] = both(0.f);
+                    mu[h] = ONE ? both(-m0)
+                                : make_float2(2 * h < t.split ? -m0 : -m1, 2 * h + 1 < t.split ? -m0 : -m1);
+                    if (V == 1) mu[h].y = 0.f;
+                }
+#pragma unroll 4
+                for (int k = 0; k < t.mine; ++k) {
+                    float2 f[H];
+                    gc_load<T, V>(my + k * hop, f);
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        if (pass == 0) {
+                            s[h] = add2(s[h], f[h]);
+                        } else {
+                            f[h] = add2(f[h], mu[h]);
+                            s[h] = fma2(f[h], f[h], s[h]);
+                        }
+                    }
+                }
+                float a = 0.f, c = 0.f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float e = i % 2 ? s[i / 2].y : s[i / 2].x;
+                    if (ONE) {
+                        a += e;
+                    } else {
+                        a += i < t.split ? e : 0.f;
+                        c += i < t.split ? 0.f : e;
+                    }
+                }
+                if (pass == 0) {
+                    m0 = t.mine ? __fdiv_rn(a, float(t.mine * t.split)) : 0.f;
+                    if (!ONE) m1 = t.mine && t.split < V ? __fdiv_rn(c, float(t.mine * (V - t.split))) : 0.f;
+                } else {
+                    rec[threadIdx.x] = make_float4(m0, a, m1, c);
                 }
             }
-        });
-        if (t.in)
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                red[t.lane * t.W + t.col * V + i] = i % 2 ? make_float2(sg[i / 2].y, sb[i / 2].y)
-                                                          : make_float2(sg[i / 2].x, sb[i / 2].x);
-    }
-    __syncthreads();
-    {  // the lanes' sums of each channel: `parts` subsets of the lanes side by side, then those
-        const int parts = max(1, min(nt / t.W, 16));
-        float2* first = parts > 1 ? red2 : col;
-        for (int i = threadIdx.x; i < t.W * parts; i += nt) {
-            const int pt = i / t.W, c = i - pt * t.W;
-            float2 s = both(0.f);
-            for (int l = pt; l < q.lanes; l += parts) s = add2(s, red[l * t.W + c]);
-            first[i] = s;
         }
         __syncthreads();
-        if (parts > 1) {
-            for (int c = threadIdx.x; c < t.W; c += nt) {
-                float2 s = both(0.f);
-                for (int pt = 0; pt < parts; ++pt) s = add2(s, red2[pt * t.W + c]);
-                col[c] = s;
-            }
-            __syncthreads();
-        }
-    }
-    for (int g = int(threadIdx.x >> 5); g < t.groups; g += nt >> 5) {
-        float2 s = both(0.f);
-        for (int c = g * p.Cg + int(threadIdx.x & 31); c < (g + 1) * p.Cg; c += 32) s = fma2(both(cp[c].z), col[c], s);
-        s = make_float2(warp_sum(s.x), warp_sum(s.y));
-        if ((threadIdx.x & 31) == 0) {
-            gs[g] = s;
-            if (q.S == 1) gt[g] = mul2(s, both(p.inv_m));
-        }
-    }
-    if (q.S > 1) {
-        cluster_arrive(), cluster_wait();
-        const uint32_t gbase = tc::smem_u32(gs);
-        for (int g = threadIdx.x; g < 2 * t.groups; g += nt) {
-            float v[8], s = 0.f;
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-                if (r < q.S) v[r] = tc::ld_dsmem_f32(tc::dsmem_addr(gbase + 4 * g, r));
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-                if (r < q.S) s += v[r];
-            reinterpret_cast<float*>(gt)[g] = s * p.inv_m;
-        }
-    }
-    if (part) {  // the unit's channel sums: block r of the cluster writes every S-th
-        const uint32_t cbase = tc::smem_u32(col);
-        for (int i = int(threadIdx.x) * q.S + t.rank; i < 2 * t.W; i += nt * q.S) {
-            const int kind = i >= t.W, c = i - kind * t.W;
-            float s = 0.f;
-            if (q.S > 1) {
-                float v[8];
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (r < q.S) v[r] = tc::ld_dsmem_f32(tc::dsmem_addr(cbase + 8 * c + 4 * kind, r));
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (r < q.S) s += v[r];
-            } else {
-                s = kind ? col[c].y : col[c].x;
-            }
-            part[(int64_t(t.b) * 2 + kind) * p.C + t.c0 + c] = s;
-        }
-    }
-    if (q.S > 1) cluster_arrive();
-    __syncthreads();
-    if (t.mine) {
-        float2 m1[H], m2[H];
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-            const int i1 = min(2 * h + 1, V - 1);
-            const float2 a = gt[t.g + (2 * h >= t.split)], b = gt[t.g + (i1 >= t.split)];
-            m2[h] = make_float2(-a.x, -b.x);
-            m1[h] = make_float2(-a.y, -b.y);
-        }
-        T* po = dx + at + int64_t(t.r0 + t.lane) * p.C;
-        const int64_t row_hop = int64_t(q.lanes) * p.C;
-        with_act(p.act, [&](auto act) {
+        // A group's mean over its threads' means, then the squares about it; first by warp.
+        gc_group_warps<V>(p, q, t, subs, [&](int g, int sub, auto&& for_each) {
+            Moments w = {0.f, 0.f, 0.f};
 #pragma unroll 1
-            for (int k = 0; k < t.mine; ++k) {
-                Vec<T, V> v;
-                float2 xh[H], dz[H];
-                v.load(reinterpret_cast<const T*>(slot + tile + k * hop));
-                gc_unpack<T, V>(v, dz);
-                v.load(reinterpret_cast<const T*>(slot + k * hop));
-                gc_unpack<T, V>(v, xh);
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    xh[h] = mul2(add2(xh[h], mu[h]), rs[h]);
-                    const float2 z = add2(mul2(xh[h], ga[h]), be[h]);
-                    dz[h] = make_float2(gn_dz<act.value>(dz[h].x, z.x), gn_dz<act.value>(dz[h].y, z.y));
-                    xh[h] = mul2(rs[h], fma2(xh[h], m2[h], fma2(dz[h], ga[h], m1[h])));
+            for (int pass = 0; pass < 2; ++pass) {
+                float s = 0.f, n = 0.f;
+                for_each([&](int cv, int l) {
+                    const bool later = !ONE && cv * V < g * p.Cg;  // the vector begins in the group before
+                    const int width = ONE ? V : min((g + 1) * p.Cg, cv * V + V) - max(g * p.Cg, cv * V);
+                    const float4 r = rec[l * q.cols + cv];
+                    const float c = float((t.full + (l < t.extra)) * width);
+                    const float mu = later ? r.z : r.x, dlt = mu - w.mean;
+                    s += pass == 0 ? c * mu : (later ? r.w : r.y) + c * dlt * dlt;
+                    n += c;
+                });
+                s = warp_sum(s);
+                if (pass == 0) {
+                    w.n = warp_sum(n);
+                    w.mean = w.n > 0.f ? __fdiv_rn(s, w.n) : 0.f;
+                } else {
+                    w.m2 = s;
                 }
-                gc_pack<T, V>(v, xh);
-                v.store(po + k * row_hop);
+            }
+            if ((threadIdx.x & 31) == 0) {
+                if (subs > 1) wrec[g * subs + sub] = make_float4(w.n, w.mean, w.m2, 0.f);
+                else if (q.S > 1) gs[turn * q.groups + g] = make_float2(w.mean, w.m2);
+                else stat[g] = make_float2(w.mean, rsqrtf(w.m2 * p.inv_m + p.eps));
             }
         });
+        if (subs > 1) {
+            __syncthreads();
+            if (int(threadIdx.x) < t.groups) {
+                Moments w = {0.f, 0.f, 0.f};
+                for (int i = 0; i < subs; ++i) {
+                    const float4 r = wrec[threadIdx.x * subs + i];
+                    w.merge(r.x, r.y, r.z);
+                }
+                if (q.S > 1) gs[turn * q.groups + threadIdx.x] = make_float2(w.mean, w.m2);
+                else stat[threadIdx.x] = make_float2(w.mean, rsqrtf(w.m2 * p.inv_m + p.eps));
+            }
+        }
+        if (q.S > 1) {
+            cluster_barrier();
+            for (int g = threadIdx.x; g < t.groups; g += nt)
+                stat[g] = gc_exchange(p, q, tc::smem_u32(gs + turn * q.groups + g),
+                                      [&](int r) { return t.rows(p, q, r) * float(p.Cg); });
+        }
+        __syncthreads();
+        if (mean_out && t.rank == 0)
+            for (int g = threadIdx.x; g < t.groups; g += nt) {
+                mean_out[int64_t(b) * p.G + t.g0 + g] = stat[g].x;
+                rstd_out[int64_t(b) * p.G + t.g0 + g] = stat[g].y;
+            }
+        if (t.mine) {
+            const float2 s0 = stat[t.g], s1 = ONE ? s0 : stat[min(t.g + 1, t.groups - 1)];
+            T* py = y + int64_t(b) * p.N + at;
+            with_act(p.act, [&](auto act) {
+#pragma unroll 2
+                for (int k = 0; k < t.mine; ++k, py += row_hop) {
+                    float2 f[H];
+                    gc_load<T, V>(my + k * hop, f);
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        const float2 mu = ONE ? both(-s0.x) : make_float2(2 * h < t.split ? -s0.x : -s1.x,
+                                                                          2 * h + 1 < t.split ? -s0.x : -s1.x);
+                        const float2 rs = ONE ? both(s0.y) : make_float2(2 * h < t.split ? s0.y : s1.y,
+                                                                         2 * h + 1 < t.split ? s0.y : s1.y);
+                        f[h] = act_value<act.value>(add2(mul2(mul2(add2(f[h], mu), rs), ga[h]), be[h]));
+                    }
+                    gc_store<T, V>(py, f);
+                }
+            });
+        }
     }
-    if (q.S > 1) cluster_wait();
+    if (q.S > 1) cluster_barrier();  // no block leaves while another still reads its shared memory
+}
+
+// part: chunks * S rows of (dgamma's, dbeta's) channel sums.
+template <typename T, int V, bool ONE>
+__global__ void __launch_bounds__(ONE ? GC_THREADS : GC_SPAN_THREADS, ONE ? 2 : 3)
+gn_cluster_bwd_nhwc(const GnParams p, const __grid_constant__ GnCluster q, const T* x, const T* dy, const T* gamma,
+                    const T* beta, const float* mean, const float* rstd, T* dx, float* part)
+{
+    extern __shared__ __align__(16) unsigned char dyn[];
+    constexpr int VB = V * int(sizeof(T)), H = gc_pairs<V>();
+    const GcTile t(p, q, V);
+    const int nt = int(blockDim.x), hop = nt * VB, tile = q.K * hop;
+    unsigned char* slot = dyn + threadIdx.x * VB;
+    // threads x (sum dz*gamma*xhat, sum dz*gamma) of either group
+    float4* rec = reinterpret_cast<float4*>(dyn + size_t(2 * q.bufs) * tile);
+    float2* wrec = reinterpret_cast<float2*>(rec + nt);        // warps x the same of their share of a group
+    float2* gs = wrec + GC_WARPS;                              // 2 x groups, the block's, read by the others
+    float2* gt = gs + 2 * q.groups;                            // groups x (m2, m1) of the unit
+    float* red = reinterpret_cast<float*>(rec);                // at the end: channel sums of the lanes
+    const int64_t at = t.c0 + t.col * V + int64_t(t.r0 + t.lane) * p.C, row_hop = int64_t(q.lanes) * p.C;
+    auto issue = [&](int b, int buf) {
+        int64_t src = int64_t(b) * p.N + at;
+        unsigned char* dst = slot + buf * 2 * tile;
+        for (int k = 0; k < t.mine; ++k, src += row_hop, dst += hop) {
+            fetch_vec<T, V>(dst, x + src);
+            fetch_vec<T, V>(dst + tile, dy + src);
+        }
+        copy_commit();
+    };
+    tc::grid_dep_wait();
+    if (q.bufs == 2) issue(t.chunk, 0);
+    float2 ga[H], be[H], sg[H], sb[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+        const int a = t.c0 + (t.mine ? t.col * V : 0) + 2 * h, b = V > 1 ? a + 1 : a;
+        ga[h] = gamma ? make_float2(Elem<T>::ldg(gamma + a), Elem<T>::ldg(gamma + b)) : both(1.f);
+        be[h] = beta ? make_float2(Elem<T>::ldg(beta + a), Elem<T>::ldg(beta + b)) : both(0.f);
+        sg[h] = sb[h] = both(0.f);
+    }
+    const int subs = gc_subs(t.groups);
+    int turn = 0;
+    for (int b = t.chunk; b < p.B; b += q.chunks, turn ^= 1) {
+        unsigned char* my = slot;
+        const int64_t g0 = int64_t(b) * p.G + t.g0 + t.g;
+        const float mu0 = -mean[g0], rs0 = rstd[g0];
+        const bool next = !ONE && t.split < V;
+        const float mu1 = next ? -mean[g0 + 1] : mu0, rs1 = next ? rstd[g0 + 1] : rs0;
+        if (q.bufs == 2) {
+            my += turn * 2 * tile;
+            if (b + q.chunks < p.B) {
+                issue(b + q.chunks, turn ^ 1);
+                copy_wait<1>();
+            } else {
+                copy_wait<0>();
+            }
+        } else {
+            issue(b, 0);
+            copy_wait<0>();
+        }
+        auto mu = [&](int h) {
+            return ONE ? both(mu0) : make_float2(2 * h < t.split ? mu0 : mu1, 2 * h + 1 < t.split ? mu0 : mu1);
+        };
+        auto rs = [&](int h) {
+            return ONE ? both(rs0) : make_float2(2 * h < t.split ? rs0 : rs1, 2 * h + 1 < t.split ? rs0 : rs1);
+        };
+        {
+            // This sample's sums of dz*xhat and dz: by place where a vector lies in two groups
+            // (and times gamma below), else of dz*gamma right away, which takes fewer registers.
+            float2 a[ONE ? 1 : H], c[ONE ? 1 : H];
+#pragma unroll
+            for (int h = 0; h < (ONE ? 1 : H); ++h) a[h] = c[h] = both(0.f);
+            with_act(p.act, [&](auto act) {
+#pragma unroll 1
+                for (int k = 0; k < t.mine; ++k) {
+                    float2 xh[H], dz[H];
+                    gc_load<T, V>(my + k * hop, xh);
+                    gc_load<T, V>(my + tile + k * hop, dz);
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        xh[h] = mul2(add2(xh[h], mu(h)), rs(h));
+                        dz[h] = gn_dz<act.value>(dz[h], add2(mul2(xh[h], ga[h]), be[h]));
+                        if constexpr (ONE) {
+                            sb[h] = add2(sb[h], dz[h]);
+                            sg[h] = fma2(dz[h], xh[h], sg[h]);
+                            const float2 e = mul2(dz[h], ga[h]);
+                            c[0] = add2(c[0], e);
+                            a[0] = fma2(e, xh[h], a[0]);
+                        } else {
+                            c[h] = add2(c[h], dz[h]);
+                            a[h] = fma2(dz[h], xh[h], a[h]);
+                        }
+                    }
+                    // dz in dy's place: exact in fp32, and not computed again
+                    if constexpr (sizeof(T) == 4) gc_store<T, V>(reinterpret_cast<T*>(my + tile + k * hop), dz);
+                }
+            });
+            float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+            if constexpr (ONE) {
+                r.x = a[0].x + a[0].y;
+                r.y = c[0].x + c[0].y;
+            } else {
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    sg[h] = add2(sg[h], a[h]);
+                    sb[h] = add2(sb[h], c[h]);
+                    a[h] = mul2(a[h], ga[h]);
+                    c[h] = mul2(c[h], ga[h]);
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float e = i % 2 ? a[i / 2].y : a[i / 2].x, f = i % 2 ? c[i / 2].y : c[i / 2].x;
+                    const bool first = i < t.split;
+                    r.x += first ? e : 0.f;
+                    r.y += first ? f : 0.f;
+                    r.z += first ? 0.f : e;
+                    r.w += first ? 0.f : f;
+                }
+            }
+            rec[threadIdx.x] = r;
+        }
+        __syncthreads();
+        gc_group_warps<V>(p, q, t, subs, [&](int g, int sub, auto&& for_each) {
+            float2 s = both(0.f);
+            for_each([&](int cv, int l) {
+                const bool later = !ONE && cv * V < g * p.Cg;  // the vector begins in the group before
+                const float4 r = rec[l * q.cols + cv];
+                s = add2(s, later ? make_float2(r.z, r.w) : make_float2(r.x, r.y));
+            });
+            s = make_float2(warp_sum(s.x), warp_sum(s.y));
+            if ((threadIdx.x & 31) == 0) {
+                if (subs > 1) wrec[g * subs + sub] = s;
+                else if (q.S > 1) gs[turn * q.groups + g] = s;
+                else gt[g] = mul2(s, both(p.inv_m));
+            }
+        });
+        if (subs > 1) {
+            __syncthreads();
+            if (int(threadIdx.x) < t.groups) {
+                float2 s = both(0.f);
+                for (int i = 0; i < subs; ++i) s = add2(s, wrec[threadIdx.x * subs + i]);
+                if (q.S > 1) gs[turn * q.groups + threadIdx.x] = s;
+                else gt[threadIdx.x] = mul2(s, both(p.inv_m));
+            }
+        }
+        if (q.S > 1) {
+            cluster_barrier();
+            for (int g = threadIdx.x; g < t.groups; g += nt)
+                gt[g] = mul2(gc_add(q, tc::smem_u32(gs + turn * q.groups + g)), both(p.inv_m));
+        }
+        __syncthreads();
+        if (t.mine) {
+            const float2 s0 = gt[t.g], s1 = ONE ? s0 : gt[min(t.g + 1, t.groups - 1)];
+            T* po = dx + int64_t(b) * p.N + at;
+            with_act(p.act, [&](auto act) {
+#pragma unroll 1
+                for (int k = 0; k < t.mine; ++k, po += row_hop) {
+                    float2 xh[H], dz[H];
+                    gc_load<T, V>(my + tile + k * hop, dz);
+                    gc_load<T, V>(my + k * hop, xh);
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        xh[h] = mul2(add2(xh[h], mu(h)), rs(h));
+                        if constexpr (sizeof(T) == 2) dz[h] = gn_dz<act.value>(dz[h], add2(mul2(xh[h], ga[h]), be[h]));
+                        const bool f0 = ONE || 2 * h < t.split, f1 = ONE || 2 * h + 1 < t.split;
+                        const float2 m2 = make_float2(f0 ? -s0.x : -s1.x, f1 ? -s0.x : -s1.x);
+                        const float2 m1 = make_float2(f0 ? -s0.y : -s1.y, f1 ? -s0.y : -s1.y);
+                        xh[h] = mul2(rs(h), fma2(xh[h], m2, fma2(dz[h], ga[h], m1)));
+                    }
+                    gc_store<T, V>(po, xh);
+                }
+            });
+        }
+    }
+    if (q.S > 1) cluster_barrier();  // no block leaves while another still reads its shared memory
+    if (!part) return;
+    // The lanes' channel sums, a kind and a few of a vector's values at a time (red holds four
+    // floats a thread).
+    const int64_t row = (int64_t(t.chunk) << q.log_s) + t.rank;
+    constexpr int Q = V < 4 ? V : 4;
+    int team = 1;  // lanes a channel
+    while (team < 32 && team * 2 <= q.lanes && team * 2 * (t.W / V * Q) <= nt) team *= 2;
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind)
+#pragma unroll
+        for (int v0 = 0; v0 < V; v0 += Q) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                const float2 e = kind ? sb[(v0 + i) / 2] : sg[(v0 + i) / 2];
+                red[i * nt + threadIdx.x] = (v0 + i) % 2 ? e.y : e.x;
+            }
+            __syncthreads();
+            for (int j0 = 0; j0 < t.W / V * Q * team; j0 += nt) {
+                const int j = j0 + int(threadIdx.x), c = j / team, cv = c / Q, i = c % Q;
+                float s = 0.f;
+                if (cv * V < t.W)
+                    for (int l = j & (team - 1); l < q.lanes; l += team) s += red[i * nt + l * q.cols + cv];
+                s = team_sum(s, team);
+                if (cv * V < t.W && (j & (team - 1)) == 0) part[(row * 2 + kind) * p.C + t.c0 + cv * V + v0 + i] = s;
+            }
+        }
 }
 
 // ---- NCHW ------------------------------------------------------------------------------------
 // A unit is a group's M consecutive values; block r holds the vectors [r*n/S, (r+1)*n/S), thread
 // t the vectors t, t + T, ... of them.  A vector lies in one channel or spans two (V <= P).
 struct GcRange {
-    int b, g, rank, v0, v1;
+    int g, chunk, rank, v0, v1, mine;
     int64_t base;
     __device__ __forceinline__ GcRange(const GnParams& p, const GnCluster& q, int V)
     {
+        uint32_t a, b;
         rank = q.S > 1 ? int(tc::cluster_rank()) : 0;
-        const int unit = int(blockIdx.x) / q.S;
-        b = unit / p.G;
-        g = unit - b * p.G;
+        q.dm_wins.divmod(blockIdx.x >> q.log_s, a, b);
+        chunk = int(a);
+        g = int(b);
         v0 = gc_cut(q.vecs, q, rank);
         v1 = gc_cut(q.vecs, q, rank + 1);
-        base = int64_t(b) * p.N + int64_t(g) * p.M;
+        const int left = v1 - v0 - int(threadIdx.x);
+        mine = left > 0 ? (left - 1) / int(blockDim.x) + 1 : 0;
+        base = int64_t(g) * p.M + int64_t(v0 + int(threadIdx.x)) * V;
+    }
+    __device__ __forceinline__ float count(const GnCluster& q, int V, int r) const
+    {
+        return float((gc_cut(q.vecs, q, r + 1) - gc_cut(q.vecs, q, r)) * V);
     }
 };
-__device__ __forceinline__ int gc_count(const GnCluster& q, int V, int r)
-{
-    return (gc_cut(q.vecs, q, r + 1) - gc_cut(q.vecs, q, r)) * V;
-}
 
-// Gamma and beta of a vector's values: channel c up to value `split`, channel c + 1 from there.
+// The channel of a vector's first value, and how many of its values lie before the next channel.
 struct GcChan {
     int c, split;
-    __device__ __forceinline__ GcChan(const GnParams& p, const FastDivmod& dmP, int v, int V)
+    __device__ __forceinline__ GcChan(const GnParams& p, const GnCluster& q, int v, int V)
     {
         uint32_t cc, r;
-        dmP.divmod(uint32_t(v) * uint32_t(V), cc, r);
+        q.dm_p.divmod(uint32_t(v) * uint32_t(V), cc, r);
         c = int(cc);
         split = p.P - int(r);
     }
 };
-
-__device__ __forceinline__ float block_sum(float v, float* sm)
+// Calls f(gamma pairs, beta pairs) for the vector; gb: (gamma, beta) of each channel.
+template <int V, class F> __device__ __forceinline__ void with_channels(const GcChan& ch, const float2* gb, F&& f)
 {
-    v = warp_sum(v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.f;
-    for (int w = 0; w < int(blockDim.x) / 32; ++w) v += sm[w];
-    return v;
+    constexpr int H = gc_pairs<V>();
+    const float2 a = gb[ch.c];
+    float2 ga[H], be[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+        ga[h] = both(a.x);
+        be[h] = both(a.y);
+    }
+    if (ch.split < V) {
+        const float2 b = gb[ch.c + 1];
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            if (2 * h >= ch.split) ga[h].x = b.x, be[h].x = b.y;
+            if (2 * h + 1 >= ch.split) ga[h].y = b.x, be[h].y = b.y;
+        }
+    }
+    f(ga, be);
 }
 
 template <typename T, int V>
 __global__ void __launch_bounds__(GC_THREADS, 2)
-gn_cluster_fwd_nchw(const GnParams p, const GnCluster q, const FastDivmod dmP, const T* x, const T* gamma,
-                    const T* beta, T* y, float* mean_out, float* rstd_out)
+gn_cluster_fwd_nchw(const GnParams p, const __grid_constant__ GnCluster q, const T* x, const T* gamma, const T* beta,
+                    T* y, float* mean_out, float* rstd_out)
 {
     extern __shared__ __align__(16) unsigned char dyn[];
-    constexpr int VB = V * int(sizeof(T));
+    constexpr int VB = V * int(sizeof(T)), H = gc_pairs<V>();
     const GcRange t(p, q, V);
-    const int nt = int(blockDim.x);
+    const int nt = int(blockDim.x), hop = nt * VB, tile = q.K * hop, nw = nt >> 5, lane = int(threadIdx.x & 31);
     unsigned char* slot = dyn + threadIdx.x * VB;
-    float* gb = reinterpret_cast<float*>(dyn + size_t(q.K) * nt * VB);  // Cg x (gamma, beta)
-    float* sm = gb + 2 * p.Cg;
-    float* ex = sm + 32;  // the block's mean and M2, read by the others
-    const T* px = x + t.base;
+    float4* wrec = reinterpret_cast<float4*>(dyn + size_t(q.bufs) * tile);  // 2 x warps (n, mean, M2)
+    float2* ex = reinterpret_cast<float2*>(wrec + 2 * GC_WARPS);  // 2: the block's mean and M2, read by the others
+    float2* gb = ex + 2;                                          // Cg x (gamma, beta)
+    auto issue = [&](int b, int buf) {
+        const T* src = x + int64_t(b) * p.N + t.base;
+        unsigned char* dst = slot + buf * tile;
+        for (int k = 0; k < t.mine; ++k, src += nt * V, dst += hop) fetch_vec<T, V>(dst, src);
+        copy_commit();
+    };
     tc::grid_dep_wait();
-    for (int v = t.v0 + int(threadIdx.x), k = 0; v < t.v1; v += nt, ++k)
-        fetch_vec<T, V>(slot + size_t(k) * nt * VB, px + int64_t(v) * V);
-    for (int c = threadIdx.x; c < p.Cg; c += nt) {
-        gb[2 * c] = gamma ? Elem<T>::ldg(gamma + t.g * p.Cg + c) : 1.f;
-        gb[2 * c + 1] = beta ? Elem<T>::ldg(beta + t.g * p.Cg + c) : 0.f;
-    }
-    copy_wait();
-    const int left = t.v1 - t.v0 - int(threadIdx.x), mine = left > 0 ? (left + nt - 1) / nt : 0;
-    float s = 0.f;
-#pragma unroll 2
-    for (int k = 0; k < mine; ++k) {
-        Vec<T, V> v;
-        v.load(reinterpret_cast<const T*>(slot + size_t(k) * nt * VB));
-#pragma unroll
-        for (int i = 0; i < V; ++i) s += v.get(i);
-    }
-    float mu = __fdiv_rn(block_sum(s, sm), float((t.v1 - t.v0) * V));
-    s = 0.f;
-#pragma unroll 2
-    for (int k = 0; k < mine; ++k) {
-        Vec<T, V> v;
-        v.load(reinterpret_cast<const T*>(slot + size_t(k) * nt * VB));
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float dlt = v.get(i) - mu;
-            s += dlt * dlt;
-        }
-    }
-    float sq = block_sum(s, sm);
-    if (q.S > 1) {
-        if (threadIdx.x == 0) {
-            ex[0] = mu;
-            ex[1] = sq;
-        }
-        cluster_arrive(), cluster_wait();
-        const uint32_t base = tc::smem_u32(ex);
-        float m[8], m2[8], sum = 0.f;
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-            if (r < q.S) {
-                m[r] = tc::ld_dsmem_f32(tc::dsmem_addr(base, r));
-                m2[r] = tc::ld_dsmem_f32(tc::dsmem_addr(base + 4, r));
+    if (q.bufs == 2) issue(t.chunk, 0);
+    for (int c = threadIdx.x; c < p.Cg; c += nt)
+        gb[c] = make_float2(gamma ? Elem<T>::ldg(gamma + t.g * p.Cg + c) : 1.f,
+                            beta ? Elem<T>::ldg(beta + t.g * p.Cg + c) : 0.f);
+    int turn = 0;
+    for (int b = t.chunk; b < p.B; b += q.chunks, turn ^= 1) {
+        const unsigned char* my = slot;
+        if (q.bufs == 2) {
+            my += turn * tile;
+            if (b + q.chunks < p.B) {
+                issue(b + q.chunks, turn ^ 1);
+                copy_wait<1>();
+            } else {
+                copy_wait<0>();
             }
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-            if (r < q.S) sum += m[r] * float(gc_count(q, V, r));
-        mu = __fdiv_rn(sum, p.m);
-        sq = 0.f;
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-            if (r < q.S) {
-                const float dlt = m[r] - mu;
-                sq += m2[r] + dlt * dlt * float(gc_count(q, V, r));
-            }
-        cluster_arrive();
-    }
-    const float rs = rsqrtf(sq * p.inv_m + p.eps);
-    if (mean_out && t.rank == 0 && threadIdx.x == 0) {
-        mean_out[int64_t(t.b) * p.G + t.g] = mu;
-        rstd_out[int64_t(t.b) * p.G + t.g] = rs;
-    }
-    T* py = y + t.base;
-    with_act(p.act, [&](auto act) {
-#pragma unroll 2
-        for (int k = 0; k < mine; ++k) {
-            const int at = t.v0 + int(threadIdx.x) + k * nt;
-            const GcChan ch(p, dmP, at, V);
-            const float2 a = *reinterpret_cast<const float2*>(gb + 2 * ch.c);
-            const float2 b = *reinterpret_cast<const float2*>(gb + 2 * min(ch.c + 1, p.Cg - 1));
-            Vec<T, V> v;
-            v.load(reinterpret_cast<const T*>(slot + size_t(k) * nt * VB));
-            float o[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const bool first = i < ch.split;
-                o[i] = act_value<act.value>(gn_z(gn_xhat(v.get(i), mu, rs), first ? a.x : b.x, first ? a.y : b.y));
-            }
-            v.set(o);
-            v.store(py + int64_t(at) * V);
+        } else {
+            issue(b, 0);
+            copy_wait<0>();
         }
-    });
-    if (q.S > 1) cluster_wait();
+        // the thread's mean, then the squares about it; then the warp's, the block's, the cluster's
+        Moments w = {float(t.mine * V), 0.f, 0.f};
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+            float2 s[2] = {both(0.f), both(0.f)};
+            const float2 neg = make_float2(-w.mean, V == 1 ? 0.f : -w.mean);
+#pragma unroll 2
+            for (int k = 0; k < t.mine; ++k) {
+                float2 f[H];
+                gc_load<T, V>(my + k * hop, f);
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    if (pass == 0) {
+                        s[h & 1] = add2(s[h & 1], f[h]);
+                    } else {
+                        f[h] = add2(f[h], neg);
+                        s[h & 1] = fma2(f[h], f[h], s[h & 1]);
+                    }
+                }
+            }
+            s[0] = add2(s[0], s[1]);
+            if (pass == 0) w.mean = t.mine ? __fdiv_rn(s[0].x + s[0].y, w.n) : 0.f;
+            else w.m2 = s[0].x + s[0].y;
+        }
+        {
+            const float n = warp_sum(w.n), m = n > 0.f ? __fdiv_rn(warp_sum(w.n * w.mean), n) : 0.f;
+            const float dlt = w.mean - m;
+            w = {n, m, warp_sum(w.m2 + w.n * dlt * dlt)};
+        }
+        if (nw > 1) {
+            if (lane == 0) wrec[turn * GC_WARPS + (threadIdx.x >> 5)] = make_float4(w.n, w.mean, w.m2, 0.f);
+            __syncthreads();
+            const float4 r = lane < nw ? wrec[turn * GC_WARPS + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float n = warp_sum(r.x), m = __fdiv_rn(warp_sum(r.x * r.y), n), dlt = r.y - m;
+            w = {n, m, warp_sum(r.z + r.x * dlt * dlt)};
+        } else {
+            __syncwarp();  // gb
+        }
+        float2 stat;
+        if (q.S > 1) {
+            if (threadIdx.x == 0) ex[turn] = make_float2(w.mean, w.m2);
+            cluster_barrier();
+            stat = gc_exchange(p, q, tc::smem_u32(ex + turn), [&](int r) { return t.count(q, V, r); });
+        } else {
+            stat = make_float2(w.mean, rsqrtf(w.m2 * p.inv_m + p.eps));
+        }
+        if (mean_out && t.rank == 0 && threadIdx.x == 0) {
+            mean_out[int64_t(b) * p.G + t.g] = stat.x;
+            rstd_out[int64_t(b) * p.G + t.g] = stat.y;
+        }
+        T* py = y + int64_t(b) * p.N + t.base;
+        with_act(p.act, [&](auto act) {
+#pragma unroll 1
+            for (int k = 0; k < t.mine; ++k, py += nt * V) {
+                const GcChan ch(p, q, t.v0 + int(threadIdx.x) + k * nt, V);
+                float2 f[H];
+                gc_load<T, V>(my + k * hop, f);
+                with_channels<V>(ch, gb, [&](const auto& ga, const auto& be) {
+#pragma unroll
+                    for (int h = 0; h < H; ++h)
+                        f[h] = act_value<act.value>(
+                            add2(mul2(mul2(add2(f[h], both(-stat.x)), both(stat.y)), ga[h]), be[h]));
+                });
+                gc_store<T, V>(py, f);
+            }
+        });
+    }
+    if (q.S > 1) cluster_barrier();  // no block leaves while another still reads its shared memory
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(GC_THREADS, 1)
-gn_cluster_bwd_nchw(const GnParams p, const GnCluster q, const FastDivmod dmP, const T* x, const T* dy,
-                    const T* gamma, const T* beta, const float* mean, const float* rstd, T* dx, float* part)
+__global__ void __launch_bounds__(GC_THREADS, 2)
+gn_cluster_bwd_nchw(const GnParams p, const __grid_constant__ GnCluster q, const T* x, const T* dy, const T* gamma,
+                    const T* beta, const float* mean, const float* rstd, T* dx, float* part)
 {
     extern __shared__ __align__(16) unsigned char dyn[];
-    constexpr int VB = V * int(sizeof(T));
+    constexpr int VB = V * int(sizeof(T)), H = gc_pairs<V>();
     const GcRange t(p, q, V);
-    const int nt = int(blockDim.x);
-    const size_t tile = size_t(q.K) * nt * VB;
+    const int nt = int(blockDim.x), hop = nt * VB, tile = q.K * hop, nw = nt >> 5, lane = int(threadIdx.x & 31);
     unsigned char* slot = dyn + threadIdx.x * VB;
-    float2* vs = reinterpret_cast<float2*>(dyn + 2 * tile);  // each vector's sums (its first channel's)
-    float2* over = vs + q.K * nt;                            // channel c: sums of the vector that enters c from c - 1
-    float2* chs = over + p.Cg;                               // channel sums of the block, read by the others
-    float* gb = reinterpret_cast<float*>(chs + p.Cg);
-    float* sm = gb + 2 * p.Cg;
-    float* ex = sm + 32;
-    const int64_t grp = int64_t(t.b) * p.G + t.g;
+    float2* vs = reinterpret_cast<float2*>(dyn + size_t(2 * q.bufs) * tile);  // (dz*xhat, dz) sums of each vector's
+                                                                              // values of its first channel,
+    float2* over = vs + q.K * nt;           // of those that enter channel c with the vector that begins in c - 1
+    float2* wrec = over + p.Cg + 1;         // 2 x warps
+    float2* ex = wrec + 2 * GC_WARPS;       // 2: the block's sums, read by the others
+    float2* gb = ex + 2;                    // Cg x (gamma, beta)
+    auto issue = [&](int b, int buf) {
+        int64_t src = int64_t(b) * p.N + t.base;
+        unsigned char* dst = slot + buf * 2 * tile;
+        for (int k = 0; k < t.mine; ++k, src += nt * V, dst += hop) {
+            fetch_vec<T, V>(dst, x + src);
+            fetch_vec<T, V>(dst + tile, dy + src);
+        }
+        copy_commit();
+    };
     tc::grid_dep_wait();
-    for (int v = t.v0 + int(threadIdx.x), k = 0; v < t.v1; v += nt, ++k) {
-        fetch_vec<T, V>(slot + size_t(k) * nt * VB, x + t.base + int64_t(v) * V);
-        fetch_vec<T, V>(slot + tile + size_t(k) * nt * VB, dy + t.base + int64_t(v) * V);
-    }
+    if (q.bufs == 2) issue(t.chunk, 0);
     for (int c = threadIdx.x; c < p.Cg; c += nt) {
-        gb[2 * c] = gamma ? Elem<T>::ldg(gamma + t.g * p.Cg + c) : 1.f;
-        gb[2 * c + 1] = beta ? Elem<T>::ldg(beta + t.g * p.Cg + c) : 0.f;
-        over[c] = make_float2(0.f, 0.f);
+        gb[c] = make_float2(gamma ? Elem<T>::ldg(gamma + t.g * p.Cg + c) : 1.f,
+                            beta ? Elem<T>::ldg(beta + t.g * p.Cg + c) : 0.f);
+        over[c] = both(0.f);
     }
-    const float mu = mean[grp], rs = rstd[grp];
-    copy_wait();
+    for (int k = 0; k < t.mine; ++k) vs[k * nt + threadIdx.x] = both(0.f);
     __syncthreads();
-    const int left = t.v1 - t.v0 - int(threadIdx.x), mine = left > 0 ? (left + nt - 1) / nt : 0;
-    float s1 = 0.f, s2 = 0.f;
-    with_act(p.act, [&](auto act) {
+    int turn = 0;
+    for (int b = t.chunk; b < p.B; b += q.chunks, turn ^= 1) {
+        unsigned char* my = slot;
+        const int64_t grp = int64_t(b) * p.G + t.g;
+        const float mu = -mean[grp], rs = rstd[grp];
+        if (q.bufs == 2) {
+            my += turn * 2 * tile;
+            if (b + q.chunks < p.B) {
+                issue(b + q.chunks, turn ^ 1);
+                copy_wait<1>();
+            } else {
+                copy_wait<0>();
+            }
+        } else {
+            issue(b, 0);
+            copy_wait<0>();
+        }
+        float2 s = both(0.f);  // sum dz*gamma*xhat, sum dz*gamma
+        with_act(p.act, [&](auto act) {
 #pragma unroll 1
-        for (int k = 0; k < mine; ++k) {
-            const GcChan ch(p, dmP, t.v0 + int(threadIdx.x) + k * nt, V);
-            const float2 a = *reinterpret_cast<const float2*>(gb + 2 * ch.c);
-            const float2 b = *reinterpret_cast<const float2*>(gb + 2 * min(ch.c + 1, p.Cg - 1));
-            Vec<T, V> vx, vd;
-            vx.load(reinterpret_cast<const T*>(slot + size_t(k) * nt * VB));
-            vd.load(reinterpret_cast<const T*>(slot + tile + size_t(k) * nt * VB));
-            float2 f = make_float2(0.f, 0.f), o = make_float2(0.f, 0.f);
+            for (int k = 0; k < t.mine; ++k) {
+                const GcChan ch(p, q, t.v0 + int(threadIdx.x) + k * nt, V);
+                float2 xh[H], dz[H];
+                gc_load<T, V>(my + k * hop, xh);
+                gc_load<T, V>(my + tile + k * hop, dz);
+                with_channels<V>(ch, gb, [&](const auto& ga, const auto& be) {
+                    float2 g = both(0.f), d = both(0.f);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const bool first = i < ch.split;
-                const float xh = gn_xhat(vx.get(i), mu, rs);
-                const float dz = gn_dz<act.value>(vd.get(i), gn_z(xh, first ? a.x : b.x, first ? a.y : b.y));
-                const float dg = dz * xh;
-                f.x += first ? dg : 0.f;
-                f.y += first ? dz : 0.f;
-                o.x += first ? 0.f : dg;
-                o.y += first ? 0.f : dz;
+                    for (int h = 0; h < H; ++h) {
+                        xh[h] = mul2(add2(xh[h], both(mu)), both(rs));
+                        dz[h] = gn_dz<act.value>(dz[h], add2(mul2(xh[h], ga[h]), be[h]));
+                        xh[h] = mul2(dz[h], xh[h]);
+                        g = add2(g, xh[h]);
+                        d = add2(d, dz[h]);
+                    }
+                    float2 first = V == 1 ? make_float2(g.x, d.x) : make_float2(g.x + g.y, d.x + d.y);
+                    if (ch.split < V) {  // the values of either channel apart
+                        float2 second = both(0.f);
+                        first = both(0.f);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            const float2 e = i % 2 ? make_float2(xh[i / 2].y, dz[i / 2].y)
+                                                   : make_float2(xh[i / 2].x, dz[i / 2].x);
+                            if (i < ch.split) first = add2(first, e);
+                            else second = add2(second, e);
+                        }
+                        over[ch.c + 1] = add2(over[ch.c + 1], second);
+                        s = fma2(second, both(ga[H - 1].y), s);
+                    }
+                    s = fma2(first, both(ga[0].x), s);
+                    vs[k * nt + threadIdx.x] = add2(vs[k * nt + threadIdx.x], first);
+                });
+                // dz in dy's place: exact in fp32, and not computed again
+                if constexpr (sizeof(T) == 4) gc_store<T, V>(reinterpret_cast<T*>(my + tile + k * hop), dz);
             }
-            s1 += f.y * a.x + o.y * b.x;
-            s2 += f.x * a.x + o.x * b.x;
-            vs[k * nt + threadIdx.x] = f;
-            if (ch.split < V) over[ch.c + 1] = o;
+        });
+        s = make_float2(warp_sum(s.x), warp_sum(s.y));
+        if (nw > 1) {
+            if (lane == 0) wrec[turn * GC_WARPS + (threadIdx.x >> 5)] = s;
+            __syncthreads();
+            s = lane < nw ? wrec[turn * GC_WARPS + lane] : both(0.f);
+            s = make_float2(warp_sum(s.x), warp_sum(s.y));
         }
-    });
-    s1 = block_sum(s1, sm);
-    s2 = block_sum(s2, sm);
-    if (q.S > 1 && threadIdx.x == 0) {
-        ex[0] = s1;
-        ex[1] = s2;
-    }
-    if (part) {
-        // channel c's vectors are those that start in it: [ceil(c*P/V), ceil((c+1)*P/V)), of
-        // which this block holds some; few vectors a channel: a thread a channel, else a warp
-        const bool thin = p.P < 8 * V;
-        const int lane = thin ? 0 : int(threadIdx.x & 31), hop = thin ? 1 : 32;
-        for (int c = thin ? int(threadIdx.x) : int(threadIdx.x >> 5); c < p.Cg; c += thin ? nt : nt >> 5) {
-            const int lo = max(t.v0, int(unsigned(c * p.P + V - 1) / V));
-            const int hi = min(t.v1, int(unsigned((c + 1) * p.P + V - 1) / V));
-            float2 s = make_float2(0.f, 0.f);
-            for (int v = lo + lane; v < hi; v += hop) {
-                const float2 e = vs[v - t.v0];
-                s.x += e.x;
-                s.y += e.y;
-            }
-            if (!thin) {
-                s.x = warp_sum(s.x);
-                s.y = warp_sum(s.y);
-            }
-            if (lane == 0) chs[c] = make_float2(s.x + over[c].x, s.y + over[c].y);
+        if (q.S > 1) {
+            if (threadIdx.x == 0) ex[turn] = s;
+            cluster_barrier();
+            s = gc_add(q, tc::smem_u32(ex + turn));
         }
-    }
-    if (q.S > 1) cluster_arrive(), cluster_wait();
-    else __syncthreads();
-    if (q.S > 1) {
-        const uint32_t base = tc::smem_u32(ex);
-        float a[8], b[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-            if (r < q.S) {
-                a[r] = tc::ld_dsmem_f32(tc::dsmem_addr(base, r));
-                b[r] = tc::ld_dsmem_f32(tc::dsmem_addr(base + 4, r));
-            }
-        s1 = s2 = 0.f;
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-            if (r < q.S) {
-                s1 += a[r];
-                s2 += b[r];
-            }
-    }
-    if (part) {
-        const uint32_t cbase = tc::smem_u32(chs);
-        for (int i = int(threadIdx.x) * q.S + t.rank; i < 2 * p.Cg; i += nt * q.S) {
-            const int c = i >> 1, kind = i & 1;
-            float v[8], s = 0.f;
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-                if (r < q.S)
-                    v[r] = q.S > 1 ? tc::ld_dsmem_f32(tc::dsmem_addr(cbase + 4 * i, r))
-                                   : reinterpret_cast<const float*>(chs)[i];
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-                if (r < q.S) s += v[r];
-            part[(int64_t(t.b) * 2 + kind) * p.C + t.g * p.Cg + c] = s;
-        }
-    }
-    if (q.S > 1) cluster_arrive();
-    const float m1 = s1 * p.inv_m, m2 = s2 * p.inv_m;
-    T* po = dx + t.base;
-    with_act(p.act, [&](auto act) {
+        const float2 m2 = both(-s.x * p.inv_m), m1 = both(-s.y * p.inv_m);
+        T* po = dx + int64_t(b) * p.N + t.base;
+        with_act(p.act, [&](auto act) {
 #pragma unroll 1
-        for (int k = 0; k < mine; ++k) {
-            const int at = t.v0 + int(threadIdx.x) + k * nt;
-            const GcChan ch(p, dmP, at, V);
-            const float2 a = *reinterpret_cast<const float2*>(gb + 2 * ch.c);
-            const float2 b = *reinterpret_cast<const float2*>(gb + 2 * min(ch.c + 1, p.Cg - 1));
-            Vec<T, V> vx, vd;
-            vx.load(reinterpret_cast<const T*>(slot + size_t(k) * nt * VB));
-            vd.load(reinterpret_cast<const T*>(slot + tile + size_t(k) * nt * VB));
-            float o[V];
+            for (int k = 0; k < t.mine; ++k, po += nt * V) {
+                const GcChan ch(p, q, t.v0 + int(threadIdx.x) + k * nt, V);
+                float2 xh[H], dz[H];
+                gc_load<T, V>(my + tile + k * hop, dz);
+                gc_load<T, V>(my + k * hop, xh);
+                with_channels<V>(ch, gb, [&](const auto& ga, const auto& be) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const bool first = i < ch.split;
-                const float xh = gn_xhat(vx.get(i), mu, rs);
-                const float dz = gn_dz<act.value>(vd.get(i), gn_z(xh, first ? a.x : b.x, first ? a.y : b.y));
-                o[i] = rs * (dz * (first ? a.x : b.x) - m1 - xh * m2);
+                    for (int h = 0; h < H; ++h) {
+                        xh[h] = mul2(add2(xh[h], both(mu)), both(rs));
+                        if constexpr (sizeof(T) == 2) dz[h] = gn_dz<act.value>(dz[h], add2(mul2(xh[h], ga[h]), be[h]));
+                        xh[h] = mul2(both(rs), fma2(xh[h], m2, fma2(dz[h], ga[h], m1)));
+                    }
+                });
+                gc_store<T, V>(po, xh);
             }
-            vx.set(o);
-            vx.store(po + int64_t(at) * V);
+        });
+    }
+    if (q.S > 1) cluster_barrier();  // no block leaves while another still reads its shared memory
+    if (!part) return;
+    __syncthreads();
+    // Channel c's vectors are those that begin in it: [ceil(c*P/V), ceil((c+1)*P/V)), of which
+    // this block holds some.  Few vectors a channel: a thread a channel, else a warp.
+    const int64_t row = (int64_t(t.chunk) << q.log_s) + t.rank;
+    const bool thin = p.P < 8 * V;
+    const int l0 = thin ? 0 : lane, step = thin ? 1 : 32;
+    for (int c = thin ? int(threadIdx.x) : int(threadIdx.x >> 5); c < p.Cg; c += thin ? nt : nw) {
+        const int lo = max(t.v0, int(unsigned(c * p.P + V - 1) / V));
+        const int hi = min(t.v1, int(unsigned((c + 1) * p.P + V - 1) / V));
+        float2 s = both(0.f);
+        for (int v = lo + l0; v < hi; v += step) s = add2(s, vs[v - t.v0]);
+        if (!thin) s = make_float2(warp_sum(s.x), warp_sum(s.y));
+        if (l0 == 0) {
+            s = add2(s, over[c]);
+            part[row * 2 * p.C + t.g * p.Cg + c] = s.x;
+            part[(row * 2 + 1) * p.C + t.g * p.Cg + c] = s.y;
         }
-    });
-    if (q.S > 1) cluster_wait();
+    }
 }
 
 template <typename T>
 cudaError_t cluster_fwd_t(const GnParams& p, const GnCluster& q, const T* x, const T* gamma, const T* beta, T* y,
                           float* mean, float* rstd, cudaStream_t s)
 {
-    const dim3 grid(unsigned(p.B) * unsigned(q.wins) * unsigned(q.S)), block(q.threads);
-    const FastDivmod dm{uint32_t(p.P)};
+    const dim3 grid(unsigned(q.chunks) * unsigned(q.wins) * unsigned(q.S)), block(q.threads);
     cudaError_t e = cudaSuccess;
-#define GN_CALL(T_, V_)                                                                                               \
-    do {                                                                                                              \
-        if (q.nhwc) {                                                                                                 \
-            e = ensure_smem<gn_cluster_fwd_nhwc<T_, V_>>(q.smem);                                                     \
-            if (e == cudaSuccess)                                                                                     \
-                e = launch_ex(gn_cluster_fwd_nhwc<T_, V_>, grid, block, q.smem, s, q.S, true, p, q, x, gamma, beta,   \
-                              y, mean, rstd);                                                                         \
-        } else {                                                                                                      \
-            e = ensure_smem<gn_cluster_fwd_nchw<T_, V_>>(q.smem);                                                     \
-            if (e == cudaSuccess)                                                                                     \
-                e = launch_ex(gn_cluster_fwd_nchw<T_, V_>, grid, block, q.smem, s, q.S, true, p, q, dm, x, gamma,     \
-                              beta, y, mean, rstd);                                                                   \
-        }                                                                                                             \
+#define GN_LAUNCH(...)                                                                                             \
+    do {                                                                                                           \
+        e = ensure_smem<__VA_ARGS__>(q.smem);                                                                      \
+        if (e == cudaSuccess)                                                                                      \
+            e = launch_ex(__VA_ARGS__, grid, block, q.smem, s, q.S, true, p, q, x, gamma, beta, y, mean, rstd);    \
+    } while (0)
+#define GN_CALL(T_, V_)                                                       \
+    do {                                                                      \
+        if (!q.nhwc) GN_LAUNCH(gn_cluster_fwd_nchw<T_, V_>);                  \
+        else if (q.one) GN_LAUNCH(gn_cluster_fwd_nhwc<T_, V_, true>);         \
+        else GN_LAUNCH(gn_cluster_fwd_nhwc<T_, V_, false>);                   \
     } while (0)
     GN_DISPATCH_V(T, q.V, GN_CALL);
 #undef GN_CALL
+#undef GN_LAUNCH
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -830,25 +1006,24 @@ template <typename T>
 cudaError_t cluster_bwd_t(const GnParams& p, const GnCluster& q, const T* x, const T* dy, const T* gamma,
                           const T* beta, const float* mean, const float* rstd, T* dx, float* part, cudaStream_t s)
 {
-    const dim3 grid(unsigned(p.B) * unsigned(q.wins) * unsigned(q.S)), block(q.threads);
-    const FastDivmod dm{uint32_t(p.P)};
+    const dim3 grid(unsigned(q.chunks) * unsigned(q.wins) * unsigned(q.S)), block(q.threads);
     cudaError_t e = cudaSuccess;
-#define GN_CALL(T_, V_)                                                                                               \
-    do {                                                                                                              \
-        if (q.nhwc) {                                                                                                 \
-            e = ensure_smem<gn_cluster_bwd_nhwc<T_, V_>>(q.smem);                                                     \
-            if (e == cudaSuccess)                                                                                     \
-                e = launch_ex(gn_cluster_bwd_nhwc<T_, V_>, grid, block, q.smem, s, q.S, true, p, q, x, dy, gamma,     \
-                              beta, mean, rstd, dx, part);                                                            \
-        } else {                                                                                                      \
-            e = ensure_smem<gn_cluster_bwd_nchw<T_, V_>>(q.smem);                                                     \
-            if (e == cudaSuccess)                                                                                     \
-                e = launch_ex(gn_cluster_bwd_nchw<T_, V_>, grid, block, q.smem, s, q.S, true, p, q, dm, x, dy, gamma, \
-                              beta, mean, rstd, dx, part);                                                            \
-        }                                                                                                             \
+#define GN_LAUNCH(...)                                                                                             \
+    do {                                                                                                           \
+        e = ensure_smem<__VA_ARGS__>(q.smem);                                                                      \
+        if (e == cudaSuccess)                                                                                      \
+            e = launch_ex(__VA_ARGS__, grid, block, q.smem, s, q.S, true, p, q, x, dy, gamma, beta, mean, rstd,    \
+                          dx, part);                                                                               \
+    } while (0)
+#define GN_CALL(T_, V_)                                                       \
+    do {                                                                      \
+        if (!q.nhwc) GN_LAUNCH(gn_cluster_bwd_nchw<T_, V_>);                  \
+        else if (q.one) GN_LAUNCH(gn_cluster_bwd_nhwc<T_, V_, true>);         \
+        else if constexpr (V_ <= 4) GN_LAUNCH(gn_cluster_bwd_nhwc<T_, V_, false>); \
     } while (0)
     GN_DISPATCH_V(T, q.V, GN_CALL);
 #undef GN_CALL
+#undef GN_LAUNCH
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -149,13 +149,14 @@ gn_team_fwd(const GnParams p, const GnTeam q, const T* x, const T* gamma, const 
         const float rstd = rsqrtf(team_sum(s.x + s.y, L) * p.inv_m + p.eps);
         if (active && b < p.B) {
             T* py = y + int64_t(b) * p.N;
+            float2 w[H];
+            table_pairs<V, K>(gam, toff, w);
+#pragma unroll
+            for (int h = 0; h < H; ++h) v[h] = mul2(mul2(v[h], both(rstd)), w[h]);  // x - mean, rounded, is in v
+            table_pairs<V, K>(bet, toff, w);
             with_act(p.act, [&](auto act) {
 #pragma unroll
-                for (int h = 0; h < H; ++h) {  // x - mean, rounded, is in v already
-                    const float2 z = add2(mul2(mul2(v[h], both(rstd)), table_pair<V, K>(gam, toff, h)),
-                                          table_pair<V, K>(bet, toff, h));
-                    v[h] = make_float2(act_value<act.value>(z.x), act_value<act.value>(z.y));
-                }
+                for (int h = 0; h < H; ++h) v[h] = act_value<act.value>(add2(v[h], w[h]));
             });
 #pragma unroll
             for (int k = 0; k < K; ++k) {
@@ -437,6 +438,7 @@ cudaError_t fwd_t(const GnParams& p, int dt, const DevInfo& d, const T* x, const
     }
     const GnCluster cl = gn_cluster(p, dt, d, false);
     if (cl.ok) return run_gn_cluster_fwd(p, cl, dt, x, gamma, beta, y, mean, rstd, s);
+    if (gn_by_rows(p)) return run_gn_rows_fwd(p, gn_rows(p, dt, d, false), dt, x, gamma, beta, y, mean, rstd, ws, s);
     const GnPieces q = gn_pieces(p, dt, d);
     const int64_t np = int64_t(p.B) * p.C * q.pieces;
     float* pmean = static_cast<float*>(ws);
@@ -469,6 +471,7 @@ cudaError_t fwd_t(const GnParams& p, int dt, const DevInfo& d, const T* x, const
 size_t gn_fwd_workspace(const GnParams& p, int dt, const DevInfo& d)
 {
     if (p.B == 0 || gn_team(p, dt, d, false).ok || gn_cluster(p, dt, d, false).ok) return 0;
+    if (gn_by_rows(p)) return size_t(8) * p.B * p.G * gn_rows(p, dt, d, false).parts;
     const GnPieces q = gn_pieces(p, dt, d);
     return size_t(4) * (2 * size_t(p.B) * p.C * q.pieces + 2 * size_t(p.B) * p.G);
 }
