@@ -3,12 +3,20 @@
 //
 // The lookup moves T*D values in and out with one multiply each: bound by memory.
 //
-// The gradient is a sum per row over the tokens that name it.  The tokens are sorted by row
-// (least significant digit first, a stable counting sort a digit), so a row's tokens are one run
-// of the sorted order in ascending t: dy is read once, row by row, and no atomic is needed.  The
-// sorted order is cut into chunks of equal length, so a row that holds a large share of the
-// tokens is spread over many thread groups; a run inside one chunk is written at once, a run
-// that crosses chunks leaves fp32 partial sums that a second kernel adds in chunk order.
+// The gradient is a sum per row over the tokens that name it, in one of two ways:
+//
+// A table of few rows: a block takes a range of the tokens and keeps the whole table's sums (of a
+// window of columns, a lane each) in its warps' registers.  Chunk by chunk the values come in as
+// they lie, copied ahead into shared memory, the block lists the chunk's tokens by row, and each
+// warp adds its rows' tokens.  The blocks' sums are added up at the end.
+//
+// Else the tokens are sorted by row (least significant digit first, a stable counting sort a
+// digit), so a row's tokens are one run of the sorted order in ascending t: dy is read once, row
+// by row, and no atomic is needed.  Up to 64 Ki tokens are sorted by one thread-block cluster in
+// its shared memory, while the other blocks of the launch fill dtable with zeros.  The sorted
+// order is cut into chunks; a run is summed by the group of the chunk it begins in, if it ends
+// by the end of the next one.  A longer run -- a row that holds a large share of the tokens --
+// leaves an fp32 partial sum in each chunk, which a last kernel adds in chunk order.
 #include <algorithm>
 
 #include "tc_ptx.cuh"
@@ -25,8 +33,19 @@ constexpr int SORT_MAX_BITS = 9;                           // digit
 constexpr int SORT_MAX_BINS = 1 << SORT_MAX_BITS;
 constexpr int SUM_THREADS = 256;
 constexpr int FIX_THREADS = 512;
+constexpr int FIX_CHUNKS = 8;                              // chunks a block of the last kernel looks at
+constexpr int CS_THREADS = 1024, CS_ITEMS = 8;             // sort by one cluster: a block's threads, tokens a thread
+constexpr int CS_TOKENS = CS_THREADS * CS_ITEMS;
+constexpr int CS_WARPS = CS_THREADS / 32;
+constexpr int TAB_COLS = 32;                               // columns of a table window: a lane each
+constexpr int TAB_THREADS = 256, TAB_WARPS = TAB_THREADS / 32;
+constexpr int TAB_MAX_ROWS = 512;                          // 64 a warp
+constexpr int TAB_BLOCKS_SM = 3;
 
 struct EmbedPlan {
+    bool table;           // sums of the whole table in shared memory
+    int regs, blocks;     // rows a warp, blocks a window of columns
+    int cluster;          // blocks of the one-cluster sort, 0: sort by kernels
     int bits, passes, digit_bits;
     int tiles;
     int V;                // vector width of a row
@@ -39,9 +58,29 @@ struct EmbedPlan {
 EmbedPlan embed_plan(const conv_embed_desc_t& e, const DevInfo& d)
 {
     EmbedPlan q = {};
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = o;
+        o += (bytes + 255) / 256 * 256;
+        return at;
+    };
+    // Whole-table sums where the tokens outnumber by far the rows that every block has to add up
+    // and write.
+    q.wins = ceil_div(e.D, TAB_COLS);
+    q.table = e.V <= TAB_MAX_ROWS && e.T >= int64_t(64) * e.V && e.T >= 8192;
+    if (q.table) {
+        for (q.regs = 4; q.regs * TAB_WARPS < e.V; q.regs *= 2) {}
+        const int64_t most = std::max(1, d.sms * (q.regs > 32 ? 2 : TAB_BLOCKS_SM) / q.wins);
+        q.blocks = int(std::min<int64_t>(most, (e.T + 4 * TAB_THREADS - 1) / (4 * TAB_THREADS)));
+        q.off_part = take(size_t(q.blocks) * e.V * e.D * 4);
+        q.bytes = o;
+        return q;
+    }
     while ((int64_t(1) << q.bits) <= e.V) ++q.bits;  // keys 0 .. V (V: no row)
     q.passes = std::max(1, ceil_div(q.bits, SORT_MAX_BITS));
     q.digit_bits = ceil_div(q.bits, q.passes);
+    while (q.cluster < kMaxCluster && e.T > int64_t(q.cluster) * CS_TOKENS) q.cluster = std::max(1, q.cluster * 2);
+    if (e.T > int64_t(q.cluster) * CS_TOKENS) q.cluster = 0;
     q.tiles = int((e.T + SORT_TILE - 1) / SORT_TILE);
     const int es = e.dtype == CONV_F32 ? 4 : 2;
     q.V = 16 / es;
@@ -49,22 +88,19 @@ EmbedPlan embed_plan(const conv_embed_desc_t& e, const DevInfo& d)
     q.nv = e.D / q.V;
     q.wins = ceil_div(q.nv, SUM_THREADS);
     q.cols = ceil_div(q.nv, q.wins);
-    // Chunks: long enough that few runs cross a boundary, short enough to fill the SMs.
-    const int64_t groups = std::max<int64_t>(1, int64_t(d.sms) * 2048 / std::max(1, q.nv));
-    q.chunk = int(std::min<int64_t>(256, std::max<int64_t>(16, (e.T + groups - 1) / groups)));
+    // Chunks: long, so that few runs are cut, while about 512 threads an SM (eight loads each in
+    // flight) have a part of them.
+    const int64_t groups = std::max<int64_t>(1, int64_t(d.sms) * 512 / std::max(1, q.nv));
+    q.chunk = int(std::min<int64_t>(512, std::max<int64_t>(16, (e.T + groups - 1) / groups)));
     q.chunks = int((e.T + q.chunk - 1) / q.chunk);
-    size_t o = 0;
-    auto take = [&](size_t bytes) {
-        const size_t at = o;
-        o += (bytes + 255) / 256 * 256;
-        return at;
-    };
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < (q.cluster ? 1 : 2); ++i) {
         q.off_keys[i] = take(size_t(e.T) * 4);
         q.off_pos[i] = take(size_t(e.T) * 4);
     }
-    q.off_counts = take(size_t(q.tiles) * SORT_MAX_BINS * 4);
-    q.off_totals = take(SORT_MAX_BINS * 4);
+    if (!q.cluster) {
+        q.off_counts = take(size_t(q.tiles) * SORT_MAX_BINS * 4);
+        q.off_totals = take(SORT_MAX_BINS * 4);
+    }
     q.off_part = take(size_t(q.chunks) * 2 * e.D * 4);
     q.bytes = o;
     return q;
@@ -136,6 +172,11 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_count(int n, int rows, int 
     }
     __syncthreads();
     for (int i = threadIdx.x; i < bins; i += SORT_THREADS) counts[size_t(i) * tiles + blockIdx.x] = hist[i];
+}
+
+__device__ __forceinline__ void st_dsmem(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // Inclusive scan over a block's threads.
@@ -253,10 +294,287 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_scatter(int n, int rows, in
         }
 }
 
+// The whole sort by one cluster of S blocks (blockIdx.x < S), which hold the tokens in order,
+// CS_TOKENS a block; the other blocks write zeros to dtable meanwhile.  A pass ranks the tokens of
+// a digit as sort_scatter does (16 bits hold a warp's counts), the blocks read each other's counts
+// of each digit, and every token goes straight to its place in the next order, in whichever block
+// that lies.
+template <typename I>
+__global__ void __launch_bounds__(CS_THREADS, 1)
+sort_cluster(int n, int rows, int padding, int S, int passes, int digit_bits, const I* idx, uint32_t* keys_out,
+             uint32_t* pos_out, uint4* fill, int64_t fill_vecs, unsigned char* fill_tail, int fill_rest)
+{
+    extern __shared__ __align__(16) uint32_t cs[];
+    if (int(blockIdx.x) >= S) {
+        const int64_t nb = int64_t(gridDim.x) - S, t = (int64_t(blockIdx.x) - S) * CS_THREADS + threadIdx.x;
+        tc::grid_dep_wait();
+#pragma unroll 4
+        for (int64_t i = t; i < fill_vecs; i += nb * CS_THREADS) fill[i] = make_uint4(0, 0, 0, 0);
+        if (t < fill_rest) fill_tail[t] = 0;
+        return;
+    }
+    const int bins = 1 << digit_bits;
+    uint32_t* kv = cs;                                       // 2 x CS_TOKENS keys, then 2 x CS_TOKENS positions
+    uint32_t* hist = cs + 4 * CS_TOKENS;                     // bins: the block's counts, read by the others
+    uint32_t* base = hist + SORT_MAX_BINS;                   // bins
+    uint32_t* sm = base + SORT_MAX_BINS;                     // CS_WARPS
+    uint16_t* cnt = reinterpret_cast<uint16_t*>(sm + CS_WARPS);  // warps x bins
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int rank = S > 1 ? int(tc::cluster_rank()) : 0;
+    const int here = max(0, min(CS_TOKENS, n - rank * CS_TOKENS));
+    const int first = w * (32 * CS_ITEMS) + lane;
+    uint32_t key[CS_ITEMS], p[CS_ITEMS], rk[CS_ITEMS];
+    tc::grid_dep_wait();
+#pragma unroll
+    for (int i = 0; i < CS_ITEMS; ++i) {
+        const int t = first + i * 32;
+        p[i] = uint32_t(rank * CS_TOKENS + t);
+        key[i] = 0xFFFFFFFFu;
+        if (t < here) {
+            const int r = token_row(idx, int64_t(p[i]), rows, padding);
+            key[i] = r >= 0 ? uint32_t(r) : uint32_t(rows);
+        }
+    }
+    for (int pass = 0; pass < passes; ++pass) {
+        const int shift = pass * digit_bits;
+        for (int i = threadIdx.x; i < CS_WARPS * bins / 2; i += CS_THREADS) reinterpret_cast<uint32_t*>(cnt)[i] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < CS_ITEMS; ++i) {
+            const bool in = first + i * 32 < here;
+            const uint32_t dg = in ? (key[i] >> shift) & uint32_t(bins - 1) : 0xFFFFFFFFu;
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, dg), below = same & ((1u << lane) - 1u);
+            const uint32_t before = in ? cnt[w * bins + dg] : 0u;
+            __syncwarp();
+            rk[i] = before + __popc(below);
+            if (in && below == 0) cnt[w * bins + dg] = uint16_t(before + __popc(same));
+            __syncwarp();
+        }
+        __syncthreads();
+        // a digit's counts of the warps to first ranks in the block, and its total
+        uint32_t total = 0;
+        if (int(threadIdx.x) < bins) {
+            for (int k = 0; k < CS_WARPS; ++k) {
+                const uint32_t c = cnt[k * bins + threadIdx.x];
+                cnt[k * bins + threadIdx.x] = uint16_t(total);
+                total += c;
+            }
+            hist[threadIdx.x] = total;
+        }
+        uint32_t all = total, before = 0;
+        if (S > 1) {
+            __syncwarp();
+            tc::cluster_sync();
+            if (int(threadIdx.x) < bins) {
+                uint32_t v[kMaxCluster];
+                all = 0;
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r)
+                    if (r < S)
+                        v[r] = __float_as_uint(
+                            tc::ld_dsmem_f32(tc::dsmem_addr(tc::smem_u32(hist + threadIdx.x), uint32_t(r))));
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r)
+                    if (r < S) {
+                        all += v[r];
+                        before += r < rank ? v[r] : 0u;
+                    }
+            }
+        }
+        // first place of each digit: the digits below it, then the blocks below this one
+        const uint32_t up = block_scan(int(threadIdx.x) < bins ? all : 0u, sm);
+        if (int(threadIdx.x) < bins) base[threadIdx.x] = up - all + before;
+        __syncthreads();
+        const bool last = pass + 1 == passes;
+        uint32_t* dk = kv + (pass & 1) * CS_TOKENS;
+        uint32_t* dp = kv + (2 + (pass & 1)) * CS_TOKENS;
+#pragma unroll
+        for (int i = 0; i < CS_ITEMS; ++i)
+            if (first + i * 32 < here) {
+                const uint32_t dg = (key[i] >> shift) & uint32_t(bins - 1);
+                const uint32_t at = base[dg] + cnt[w * bins + dg] + rk[i];
+                if (last) {
+                    keys_out[at] = key[i];
+                    pos_out[at] = p[i];
+                } else if (S == 1) {
+                    dk[at] = key[i];
+                    dp[at] = p[i];
+                } else {
+                    const uint32_t r = at / CS_TOKENS, slot = at % CS_TOKENS;
+                    st_dsmem(tc::dsmem_addr(tc::smem_u32(dk + slot), r), key[i]);
+                    st_dsmem(tc::dsmem_addr(tc::smem_u32(dp + slot), r), p[i]);
+                }
+            }
+        if (last) break;
+        if (S > 1) {
+            __syncwarp();
+            tc::cluster_sync();
+        } else {
+            __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < CS_ITEMS; ++i)
+            if (first + i * 32 < here) {
+                key[i] = dk[first + i * 32];
+                p[i] = dp[first + i * 32];
+            }
+    }
+    if (S > 1) {  // no block leaves while another still reads its counts
+        __syncwarp();
+        tc::cluster_sync();
+    }
+}
+
+// ---- whole-table sums ------------------------------------------------------------------------
+// Block (range, window): tokens [t0, t1), TAB_THREADS at a time, columns [c0, c0 + TAB_COLS).
+// Warp w keeps the sums of the rows w, w + TAB_WARPS, ... (R of them), a column a lane.  A chunk's
+// values are copied a chunk ahead into one of two tiles.  Its tokens are listed by row with
+// matches in the warps and a scan over the rows; the list keeps the tokens' order, so a row's sum
+// has one order.
+template <int BYTES> __device__ __forceinline__ void tab_copy(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+
+template <typename T, typename I, int R, int V>
+__global__ void __launch_bounds__(TAB_THREADS, R > 32 ? 2 : TAB_BLOCKS_SM)
+embed_table(int n, int rows, int padding, int D, int blocks, const I* idx, const T* dy, float* part)
+{
+    constexpr int SEG = TAB_COLS / V;                       // copies a token's segment
+    extern __shared__ __align__(16) unsigned char dynt[];
+    T* tile = reinterpret_cast<T*>(dynt);                   // 2 x TAB_THREADS x TAB_COLS
+    __shared__ uint16_t cnt[TAB_WARPS][R * TAB_WARPS];      // the warps' tokens of each row, then their places
+    __shared__ uint16_t off[R * TAB_WARPS + 1];             // where each row's list begins
+    __shared__ uint16_t list[TAB_THREADS];
+    __shared__ uint32_t sm[TAB_WARPS];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int range = int(blockIdx.x) % blocks, c0 = int(blockIdx.x) / blocks * TAB_COLS;
+    const int t0 = int(int64_t(n) * range / blocks), t1 = int(int64_t(n) * (range + 1) / blocks);
+    const int width = min(TAB_COLS, D - c0);
+    float acc[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) acc[j] = 0.f;
+    int next_row = -1;
+    auto load = [&](int t, int buf) {  // the chunk at t: its values, and this thread's token's row
+        const int here = min(TAB_THREADS, t1 - t);
+        next_row = int(threadIdx.x) < here ? token_row(idx, int64_t(t) + threadIdx.x, rows, padding) : -1;
+        for (int i = threadIdx.x; i < here * SEG; i += TAB_THREADS) {
+            const int tok = i / SEG, c = i % SEG * V;
+            if (c < width) {
+                T* dst = tile + (buf * TAB_THREADS + tok) * TAB_COLS + c;
+                const T* src = dy + int64_t(t + tok) * D + c0 + c;
+                if constexpr (sizeof(T) * V >= 4) tab_copy<int(sizeof(T)) * V>(tc::smem_u32(dst), src);
+                else *dst = *src;
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    tc::grid_dep_wait();
+    if (t0 < t1) load(t0, 0);
+    int buf = 0;
+    for (int t = t0; t < t1; t += TAB_THREADS, buf ^= 1) {
+        const int row = next_row;
+        if (t + TAB_THREADS < t1) load(t + TAB_THREADS, buf ^ 1);
+        for (int i = threadIdx.x; i < TAB_WARPS * R * TAB_WARPS / 2; i += TAB_THREADS)
+            reinterpret_cast<uint32_t*>(&cnt[0][0])[i] = 0;
+        __syncthreads();
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, row), below = same & ((1u << lane) - 1u);
+        if (row >= 0 && below == 0) cnt[w][row] = uint16_t(__popc(same));
+        __syncthreads();
+        // rows' totals over the warps, scanned: PER rows a thread
+        constexpr int PER = (R * TAB_WARPS + TAB_THREADS - 1) / TAB_THREADS;
+        uint32_t tot[PER], mine = 0;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int r = int(threadIdx.x) * PER + k;
+            tot[k] = 0;
+            if (r < R * TAB_WARPS)
+#pragma unroll
+                for (int x = 0; x < TAB_WARPS; ++x) {
+                    const uint32_t c = cnt[x][r];
+                    cnt[x][r] = uint16_t(tot[k]);
+                    tot[k] += c;
+                }
+            mine += tot[k];
+        }
+        uint32_t at = block_scan(mine, sm) - mine;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int r = int(threadIdx.x) * PER + k;
+            if (r <= R * TAB_WARPS) off[r] = uint16_t(at);
+            at += tot[k];
+        }
+        if (R * TAB_WARPS == PER * TAB_THREADS && threadIdx.x == TAB_THREADS - 1) off[R * TAB_WARPS] = uint16_t(at);
+        __syncthreads();
+        if (row >= 0) list[off[row] + cnt[w][row] + __popc(below)] = uint16_t(threadIdx.x);
+        if (t + TAB_THREADS < t1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        const T* src = tile + buf * TAB_THREADS * TAB_COLS + lane;
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            const int r = w + j * TAB_WARPS, e = off[r + 1];
+#pragma unroll 4
+            for (int k = off[r]; k < e; ++k) acc[j] += Elem<T>::ld(src + int(list[k]) * TAB_COLS);
+        }
+        __syncthreads();
+    }
+    if (lane < width)
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            const int r = w + j * TAB_WARPS;
+            if (r < rows) part[(int64_t(range) * rows + r) * D + c0 + lane] = acc[j];
+        }
+}
+
+// dtable = scale * the blocks' sums, added in order: eight lanes an element (an eighth of the
+// blocks each, then a fixed butterfly).
+template <typename T>
+__global__ void __launch_bounds__(256) embed_table_sum(int64_t values, int blocks, float scale, const float* part,
+                                                       T* dtable)
+{
+    __shared__ float sm[8][32];
+    const int64_t e = int64_t(blockIdx.x) * 32 + (threadIdx.x & 31);
+    const int l = threadIdx.x >> 5;
+    float s = 0.f;
+    tc::grid_dep_wait();
+    if (e < values)
+#pragma unroll 8
+        for (int b = l; b < blocks; b += 8) s += part[int64_t(b) * values + e];
+    sm[l][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (l == 0 && e < values) {
+        s = 0.f;
+        for (int k = 0; k < 8; ++k) s += sm[k][threadIdx.x];
+        Elem<T>::st(dtable + e, s * scale);
+    }
+}
+
 // ---- sums ------------------------------------------------------------------------------------
-// A group of `cols` threads sums the chunk's sorted tokens, each thread one vector of the row.
-// part[chunk][0]: the sum of a run that began in an earlier chunk; part[chunk][1]: of a run that
-// begins here and goes on in the next chunk.
+// A group of `cols` threads sums the runs that begin in its chunk of the sorted tokens, each
+// thread one vector of the row.  A run that goes on in the next chunk and ends there is summed to
+// its end.  A longer one leaves partial sums: part[chunk][1] where it begins, part[chunk][0] in
+// each chunk that it enters from before.
+struct ChunkRuns {
+    bool skip;       // the run that enters from before is another group's
+    bool head;       // it is a long one: its part of this chunk is a partial sum
+    int end;         // where the group stops
+    bool tail;       // the run at the end is a long one
+    __device__ __forceinline__ ChunkRuns(const uint32_t* keys, int n, int chunk, int i0, int i1)
+    {
+        const uint32_t k0 = keys[i0], k1 = keys[i1 - 1];
+        const bool enters = i0 > 0 && keys[i0 - 1] == k0, leaves = i1 < n && keys[i1] == k1;
+        const bool from_last = enters && (i0 - chunk <= 0 || keys[i0 - chunk - 1] != k0);  // began in the chunk before
+        skip = from_last && !(leaves && k0 == k1);
+        head = enters && !skip;
+        const bool one = enters && k0 == k1;  // a single run from before
+        const int i2 = min(n, i1 + chunk);
+        const bool ends_next = i2 >= n || keys[i2] != k1;
+        tail = leaves && !one && !ends_next;
+        end = leaves && !one && ends_next ? i2 : i1;
+    }
+};
+
 template <typename T, int V>
 __global__ void __launch_bounds__(SUM_THREADS) embed_sum(int n, int rows, int D, int cols, int wins, int chunk,
                                                          int chunks, float scale, const uint32_t* keys,
@@ -270,15 +588,16 @@ __global__ void __launch_bounds__(SUM_THREADS) embed_sum(int n, int rows, int D,
     tc::grid_dep_wait();
     if (sub >= per || ch >= chunks || c >= D) return;
     const int i0 = int(ch) * chunk, i1 = min(n, i0 + chunk);
-    const uint32_t prev = i0 > 0 ? keys[i0 - 1] : 0xFFFFFFFFu, next = i1 < n ? keys[i1] : 0xFFFFFFFFu;
+    const ChunkRuns run(keys, n, chunk, i0, i1);
     float acc[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] = 0.f;
     uint32_t cur = keys[i0];
-    bool head = cur == prev;  // the running run began before this chunk
-    auto flush = [&](bool goes_on) {
-        if (cur >= uint32_t(rows)) return;
-        if (head || goes_on) {
+    const uint32_t last = keys[i1 - 1];
+    bool head = run.head, skip = run.skip;
+    auto flush = [&](bool tail) {
+        if (cur >= uint32_t(rows) || skip) return;
+        if (head || tail) {
             float* o = part + (ch * 2 + (head ? 0 : 1)) * D + c;
 #pragma unroll
             for (int k = 0; k < V; ++k) o[k] = acc[k];
@@ -291,22 +610,24 @@ __global__ void __launch_bounds__(SUM_THREADS) embed_sum(int n, int rows, int D,
             v.store(dtable + int64_t(cur) * D + c);
         }
     };
-    for (int i = i0; i < i1; i += U) {
+    for (int i = i0; i < run.end; i += U) {
         uint32_t k[U];
         Vec<T, V> v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            k[u] = i + u < i1 ? keys[i + u] : 0xFFFFFFFFu;
+            // beyond the chunk only the run at its end counts
+            k[u] = i + u < run.end ? keys[i + u] : 0xFFFFFFFFu;
+            if (i + u >= i1 && k[u] != last) k[u] = 0xFFFFFFFFu;
             if (k[u] < uint32_t(rows)) v[u].load(dy + int64_t(pos[i + u]) * D + c);
             else v[u].zero();
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (i + u < i1) {
+            if (i + u < i1 || k[u] == last) {
                 if (k[u] != cur) {
                     flush(false);
                     cur = k[u];
-                    head = false;
+                    head = skip = false;
 #pragma unroll
                     for (int j = 0; j < V; ++j) acc[j] = 0.f;
                 }
@@ -314,58 +635,70 @@ __global__ void __launch_bounds__(SUM_THREADS) embed_sum(int n, int rows, int D,
                 for (int j = 0; j < V; ++j) acc[j] += v[u].get(j);
             }
     }
-    flush(cur == next);
+    flush(run.tail);
 }
 
-// Rows whose tokens cross chunks: block `ch` looks whether a run begins in chunk ch and goes on;
-// if so it adds the run's partials: lanes take chunks round robin, then the lanes are added in
-// order.
+// The long runs: a block looks at FIX_CHUNKS chunks, and for each that a long run begins in adds
+// the run's partials, lanes taking chunks round robin and then the lanes in order.
 template <typename T, int V>
 __global__ void __launch_bounds__(FIX_THREADS) embed_fix(int n, int rows, int D, int cols, int wins, int chunk,
                                                          int chunks, float scale, const uint32_t* keys, T* dtable,
                                                          const float* part)
 {
     __shared__ float sm[FIX_THREADS * V];
-    const int win = int(blockIdx.x % wins), ch = int(blockIdx.x / wins);
+    __shared__ int reach[FIX_CHUNKS];  // further chunks of the run that begins here, 0: none
+    const int win = int(blockIdx.x % wins), ch0 = int(blockIdx.x / wins) * FIX_CHUNKS;
     const int lanes = FIX_THREADS / cols, lane = int(threadIdx.x) / cols, col = int(threadIdx.x) - lane * cols;
     const int c = (win * cols + col) * V;
     tc::grid_dep_wait();
-    const int i0 = ch * chunk, i1 = min(n, i0 + chunk);
-    if (i1 >= n) return;
-    const uint32_t key = keys[i1 - 1];
-    if (key >= uint32_t(rows) || keys[i1] != key) return;
-    if (i0 > 0 && keys[i0 - 1] == key) return;  // began earlier
-    // the last chunk that the run reaches, by bisection over the chunks' first keys
-    int lo = ch + 1, hi = chunks - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (keys[mid * chunk] == key) lo = mid;
-        else hi = mid - 1;
-    }
-    const int cnt = lo - ch;  // further chunks
-    float acc[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] = 0.f;
-    if (lane < lanes && c < D)
-#pragma unroll 4
-        for (int j = lane; j <= cnt; j += lanes) {
-            const float* s = part + (int64_t(ch + j) * 2 + (j == 0 ? 1 : 0)) * D + c;
-#pragma unroll
-            for (int k = 0; k < V; ++k) acc[k] += s[k];
+    if (threadIdx.x < FIX_CHUNKS) {
+        const int ch = ch0 + int(threadIdx.x);
+        int cnt = 0;
+        if (ch < chunks) {
+            const int i0 = ch * chunk, i1 = min(n, i0 + chunk);
+            const uint32_t key = keys[i1 - 1];
+            if (key < uint32_t(rows) && ChunkRuns(keys, n, chunk, i0, i1).tail) {
+                // the last chunk that the run reaches, by bisection over the chunks' first keys
+                int lo = ch + 1, hi = chunks - 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) / 2;
+                    if (keys[mid * chunk] == key) lo = mid;
+                    else hi = mid - 1;
+                }
+                cnt = lo - ch;
+            }
         }
-    if (lane < lanes)
-#pragma unroll
-        for (int k = 0; k < V; ++k) sm[(lane * cols + col) * V + k] = acc[k];
+        reach[threadIdx.x] = cnt;
+    }
     __syncthreads();
-    if (lane == 0 && c < D) {
-        for (int l = 1; l < lanes; ++l)
+    for (int k = 0; k < FIX_CHUNKS; ++k) {
+        const int cnt = reach[k], ch = ch0 + k;
+        if (cnt == 0) continue;
+        float acc[V];
 #pragma unroll
-            for (int k = 0; k < V; ++k) acc[k] += sm[(l * cols + col) * V + k];
-        Vec<T, V> v;
+        for (int i = 0; i < V; ++i) acc[i] = 0.f;
+        if (lane < lanes && c < D)
+#pragma unroll 8
+            for (int j = lane; j <= cnt; j += lanes) {
+                const float* s = part + (int64_t(ch + j) * 2 + (j == 0 ? 1 : 0)) * D + c;
 #pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] *= scale;
-        v.set(acc);
-        v.store(dtable + int64_t(key) * D + c);
+                for (int i = 0; i < V; ++i) acc[i] += s[i];
+            }
+        if (lane < lanes)
+#pragma unroll
+            for (int i = 0; i < V; ++i) sm[(lane * cols + col) * V + i] = acc[i];
+        __syncthreads();
+        if (lane == 0 && c < D) {
+            for (int l = 1; l < lanes; ++l)
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] += sm[(l * cols + col) * V + i];
+            Vec<T, V> v;
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] *= scale;
+            v.set(acc);
+            v.store(dtable + int64_t(keys[min(n, (ch + 1) * chunk) - 1]) * D + c);
+        }
+        __syncthreads();
     }
 }
 
@@ -395,10 +728,28 @@ cudaError_t fwd_t(const conv_embed_desc_t& e, const DevInfo& d, const I* idx, co
 }
 
 template <typename I>
-cudaError_t sort_tokens(const conv_embed_desc_t& e, const EmbedPlan& q, const I* idx, unsigned char* ws, int& where,
-                        cudaStream_t s)
+cudaError_t sort_tokens(const conv_embed_desc_t& e, const EmbedPlan& q, const DevInfo& d, const I* idx,
+                        unsigned char* ws, void* dtable, int& where, cudaStream_t s)
 {
     const int n = int(e.T), bins = 1 << q.digit_bits;
+    const size_t bytes = size_t(e.V) * e.D * (e.dtype == CONV_F32 ? 4 : 2);
+    if (q.cluster) {
+        const int S = q.cluster;
+        constexpr int smem = 4 * (4 * CS_TOKENS + 2 * SORT_MAX_BINS + CS_WARPS) + 2 * CS_WARPS * SORT_MAX_BINS;
+        cudaError_t r = ensure_smem<sort_cluster<I>>(smem);
+        if (r != cudaSuccess) return r;
+        const int64_t vecs = int64_t(bytes / 16);
+        // the sorting cluster, and blocks to fill with (whole clusters)
+        const int64_t want = (vecs + int64_t(CS_THREADS) * 8 - 1) / (int64_t(CS_THREADS) * 8);
+        const int more = round_up(int(std::min<int64_t>(std::max<int64_t>(1, want), d.sms)), S);
+        where = 0;
+        return launch_ex(sort_cluster<I>, dim3(S + more), dim3(CS_THREADS), smem, s, S, true, n, e.V, e.padding_idx, S,
+                         q.passes, q.digit_bits, idx, reinterpret_cast<uint32_t*>(ws + q.off_keys[0]),
+                         reinterpret_cast<uint32_t*>(ws + q.off_pos[0]), static_cast<uint4*>(dtable), vecs,
+                         static_cast<unsigned char*>(dtable) + vecs * 16, int(bytes - vecs * 16));
+    }
+    cudaError_t z = cudaMemsetAsync(dtable, 0, bytes, s);
+    if (z != cudaSuccess) return z;
     uint32_t* counts = reinterpret_cast<uint32_t*>(ws + q.off_counts);
     uint32_t* totals = reinterpret_cast<uint32_t*>(ws + q.off_totals);
     for (int pass = 0; pass < q.passes; ++pass) {
@@ -422,12 +773,52 @@ cudaError_t sort_tokens(const conv_embed_desc_t& e, const EmbedPlan& q, const I*
     return cudaSuccess;
 }
 
+template <typename T, typename I, int R, int V>
+cudaError_t table_rv(const conv_embed_desc_t& e, const EmbedPlan& q, const I* idx, const T* dy, float* part,
+                     cudaStream_t s)
+{
+    constexpr int smem = 2 * TAB_THREADS * TAB_COLS * int(sizeof(T));
+    const cudaError_t r = ensure_smem<embed_table<T, I, R, V>>(smem);
+    if (r != cudaSuccess) return r;
+    return launch_ex(embed_table<T, I, R, V>, dim3(unsigned(q.blocks) * unsigned(q.wins)), dim3(TAB_THREADS), smem, s,
+                     1, true, int(e.T), e.V, e.padding_idx, e.D, q.blocks, idx, dy, part);
+}
+
+template <typename T, typename I>
+cudaError_t table_t(const conv_embed_desc_t& e, const EmbedPlan& q, const I* idx, const T* dy, T* dtable, float* part,
+                    cudaStream_t s)
+{
+    // copies of 16 bytes, or of 4 (bf16 of an odd width: 2) where the rows are not aligned for them
+    constexpr int W = 16 / int(sizeof(T)), N = 4 / int(sizeof(T));
+    const int V = e.D % W == 0 ? W : e.D % N == 0 ? N : 1;
+    cudaError_t r = cudaSuccess;
+#define EMB_CALL(R_)                                                        \
+    r = V == W   ? table_rv<T, I, R_, W>(e, q, idx, dy, part, s)            \
+        : V == N ? table_rv<T, I, R_, N>(e, q, idx, dy, part, s)            \
+                 : table_rv<T, I, R_, 1>(e, q, idx, dy, part, s)
+    switch (q.regs) {
+        case 4: EMB_CALL(4); break;
+        case 8: EMB_CALL(8); break;
+        case 16: EMB_CALL(16); break;
+        case 32: EMB_CALL(32); break;
+        default: EMB_CALL(64); break;
+    }
+#undef EMB_CALL
+    if (r != cudaSuccess) return r;
+    const int64_t values = int64_t(e.V) * e.D;
+    const float* cpart = part;
+    r = launch_ex(embed_table_sum<T>, dim3(unsigned((values + 31) / 32)), dim3(256), 0, s, 1, true, values, q.blocks,
+                  e.scale, cpart, dtable);
+    return r != cudaSuccess ? r : cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t sum_t(const conv_embed_desc_t& e, const EmbedPlan& q, const uint32_t* keys, const uint32_t* pos,
                   const T* dy, T* dtable, float* part, cudaStream_t s)
 {
     const int n = int(e.T), per = SUM_THREADS / q.cols;
-    const dim3 sgrid(unsigned(ceil_div(q.chunks, per)) * unsigned(q.wins)), fgrid(unsigned(q.chunks) * unsigned(q.wins));
+    const dim3 sgrid(unsigned(ceil_div(q.chunks, per)) * unsigned(q.wins));
+    const dim3 fgrid(unsigned(ceil_div(q.chunks, FIX_CHUNKS)) * unsigned(q.wins));
     cudaError_t r = cudaSuccess;
     const float* cpart = part;
 #define EMB_CALL(V_)                                                                                             \
@@ -470,16 +861,24 @@ cudaError_t run_embed_bwd(const conv_embed_desc_t& e, const DevInfo& d, const vo
 {
     using H = __nv_bfloat16;
     unsigned char* ws = static_cast<unsigned char*>(ws_);
-    cudaError_t r = cudaMemsetAsync(dtable, 0, size_t(e.V) * e.D * (e.dtype == CONV_F32 ? 4 : 2), s);
-    if (r != cudaSuccess || e.T == 0) return r;
+    if (e.T == 0) return cudaMemsetAsync(dtable, 0, size_t(e.V) * e.D * (e.dtype == CONV_F32 ? 4 : 2), s);
     const EmbedPlan q = embed_plan(e, d);
+    float* part = reinterpret_cast<float*>(ws + q.off_part);
+    if (q.table) {
+        if (e.dtype == CONV_F32)
+            return e.index_dtype == CONV_INDEX_I32
+                       ? table_t(e, q, (const int32_t*)idx, (const float*)dy, (float*)dtable, part, s)
+                       : table_t(e, q, (const int64_t*)idx, (const float*)dy, (float*)dtable, part, s);
+        return e.index_dtype == CONV_INDEX_I32 ? table_t(e, q, (const int32_t*)idx, (const H*)dy, (H*)dtable, part, s)
+                                               : table_t(e, q, (const int64_t*)idx, (const H*)dy, (H*)dtable, part, s);
+    }
     int where = 0;
-    r = e.index_dtype == CONV_INDEX_I32 ? sort_tokens(e, q, (const int32_t*)idx, ws, where, s)
-                                        : sort_tokens(e, q, (const int64_t*)idx, ws, where, s);
+    const cudaError_t r = e.index_dtype == CONV_INDEX_I32
+                              ? sort_tokens(e, q, d, (const int32_t*)idx, ws, dtable, where, s)
+                              : sort_tokens(e, q, d, (const int64_t*)idx, ws, dtable, where, s);
     if (r != cudaSuccess) return r;
     const uint32_t* keys = reinterpret_cast<const uint32_t*>(ws + q.off_keys[where]);
     const uint32_t* pos = reinterpret_cast<const uint32_t*>(ws + q.off_pos[where]);
-    float* part = reinterpret_cast<float*>(ws + q.off_part);
     return e.dtype == CONV_F32 ? sum_t(e, q, keys, pos, (const float*)dy, (float*)dtable, part, s)
                                : sum_t(e, q, keys, pos, (const H*)dy, (H*)dtable, part, s);
 }

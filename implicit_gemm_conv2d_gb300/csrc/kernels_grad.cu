@@ -16,20 +16,24 @@ namespace igc {
 namespace {
 
 constexpr int GRAD_THREADS = 512;
-constexpr int GRAD_TILE = 16384;   // elements
+constexpr int GRAD_TILE = 16384, GRAD_TILE_MIN = 2048;  // elements
 constexpr int GRAD_BLOCKS_SM = 4;
-constexpr int GRAD_LIST = 512;     // entries a launch
+constexpr int GRAD_LIST = 512, GRAD_SHORT = 48;         // entries a launch; of a short list's kernel
 
-struct GradList {
+// N entries: a launch copies its parameters, so a short list has a short type.
+template <int N> struct GradListOf {
     int count;
     int tiles;
-    int first[GRAD_LIST + 1];      // first tile of each entry
-    const void* grad[GRAD_LIST];
-    void* out[GRAD_LIST];
-    int64_t n[GRAD_LIST];          // elements; negative: bf16, -n of them
+    int tile;                      // elements
+    int first[N + 1];              // first tile of each entry
+    const void* grad[N];
+    void* out[N];
+    int64_t n[N];                  // elements; negative: bf16, -n of them
 };
+using GradList = GradListOf<GRAD_LIST>;
+using GradShort = GradListOf<GRAD_SHORT>;
 
-__device__ __forceinline__ int find_entry(const GradList& l, int tile)
+template <class L> __device__ __forceinline__ int find_entry(const L& l, int tile)
 {
     int lo = 0, hi = l.count - 1;
     while (lo < hi) {
@@ -128,15 +132,16 @@ __device__ __forceinline__ float block_total(float s, float* sm)
     return s;
 }
 
-__global__ void __launch_bounds__(GRAD_THREADS) grad_squares(const __grid_constant__ GradList l, float* part)
+template <class L>
+__global__ void __launch_bounds__(GRAD_THREADS) grad_squares(const __grid_constant__ L l, float* part)
 {
     __shared__ float sm[GRAD_THREADS / 32];
     float s = 0.f;
     tc::grid_dep_wait();
     for (int t = blockIdx.x; t < l.tiles; t += gridDim.x) {
         const int k = find_entry(l, t);
-        const int64_t n = l.n[k] < 0 ? -l.n[k] : l.n[k], at = int64_t(t - l.first[k]) * GRAD_TILE;
-        const int cnt = int(n - at < GRAD_TILE ? n - at : GRAD_TILE);
+        const int64_t n = l.n[k] < 0 ? -l.n[k] : l.n[k], at = int64_t(t - l.first[k]) * l.tile;
+        const int cnt = int(n - at < l.tile ? n - at : l.tile);
         s += l.n[k] < 0 ? tile_squares(static_cast<const __nv_bfloat16*>(l.grad[k]) + at, cnt)
                         : tile_squares(static_cast<const float*>(l.grad[k]) + at, cnt);
     }
@@ -159,8 +164,9 @@ __global__ void __launch_bounds__(GRAD_THREADS) grad_norm_kernel(const float* pa
     if (threadIdx.x == 0) *norm = v;
 }
 
-__global__ void __launch_bounds__(GRAD_THREADS) grad_scale(const __grid_constant__ GradList l, const float* part,
-                                                           int parts, float max_norm, float* norm)
+template <class L>
+__global__ void __launch_bounds__(GRAD_THREADS) grad_scale(const __grid_constant__ L l, const float* part, int parts,
+                                                           float max_norm, float* norm)
 {
     __shared__ float sm[GRAD_THREADS / 32];
     tc::grid_dep_wait();
@@ -170,8 +176,8 @@ __global__ void __launch_bounds__(GRAD_THREADS) grad_scale(const __grid_constant
     coef = coef > 1.f ? 1.f : coef;  // NaN stays
     for (int t = l.tiles - 1 - int(blockIdx.x); t >= 0; t -= int(gridDim.x)) {
         const int k = find_entry(l, t);
-        const int64_t n = l.n[k] < 0 ? -l.n[k] : l.n[k], at = int64_t(t - l.first[k]) * GRAD_TILE;
-        const int cnt = int(n - at < GRAD_TILE ? n - at : GRAD_TILE);
+        const int64_t n = l.n[k] < 0 ? -l.n[k] : l.n[k], at = int64_t(t - l.first[k]) * l.tile;
+        const int cnt = int(n - at < l.tile ? n - at : l.tile);
         if (l.n[k] < 0)
             tile_scale(static_cast<const __nv_bfloat16*>(l.grad[k]) + at, static_cast<__nv_bfloat16*>(l.out[k]) + at,
                        cnt, coef);
@@ -180,15 +186,27 @@ __global__ void __launch_bounds__(GRAD_THREADS) grad_scale(const __grid_constant
     }
 }
 
+// Elements a tile: GRAD_TILE where that gives every SM a few tiles, else down to GRAD_TILE_MIN
+// (four elements a thread).
+int tile_of(const conv_grad_t* g, int count, const DevInfo& d)
+{
+    int64_t total = 0;
+    for (int i = 0; i < count; ++i) total += g[i].n;
+    int tile = GRAD_TILE;
+    while (tile > GRAD_TILE_MIN && total < int64_t(tile) * d.sms * GRAD_BLOCKS_SM) tile /= 2;
+    return tile;
+}
+
 // Entries [i0, ...) that fit a launch; returns the next one.
-int fill_list(const conv_grad_t* g, int count, int i0, GradList& l)
+int fill_list(const conv_grad_t* g, int count, int i0, int tile, GradList& l)
 {
     l.count = 0;
+    l.tile = tile;
     int64_t tiles = 0;
     int i = i0;
     for (; i < count && l.count < GRAD_LIST; ++i) {
         if (g[i].n == 0) continue;
-        const int64_t t = (g[i].n + GRAD_TILE - 1) / GRAD_TILE;
+        const int64_t t = (g[i].n + tile - 1) / tile;
         if (tiles + t > (int64_t(1) << 30)) break;
         l.first[l.count] = int(tiles);
         l.grad[l.count] = g[i].grad;
@@ -202,7 +220,42 @@ int fill_list(const conv_grad_t* g, int count, int i0, GradList& l)
     return i;
 }
 
+void shorten(const GradList& l, GradShort& q)
+{
+    q.count = l.count;
+    q.tiles = l.tiles;
+    q.tile = l.tile;
+    for (int i = 0; i < l.count; ++i) {
+        q.first[i] = l.first[i];
+        q.grad[i] = l.grad[i];
+        q.out[i] = l.out[i];
+        q.n[i] = l.n[i];
+    }
+    q.first[l.count] = l.tiles;
+}
+
 int list_grid(const GradList& l, const DevInfo& d) { return std::max(1, std::min(l.tiles, d.sms * GRAD_BLOCKS_SM)); }
+
+cudaError_t launch_squares(const GradList& l, int grid, float* part, cudaStream_t s)
+{
+    if (l.count > GRAD_SHORT)
+        return launch_ex(grad_squares<GradList>, dim3(grid), dim3(GRAD_THREADS), 0, s, 1, true, l, part);
+    GradShort q;
+    shorten(l, q);
+    return launch_ex(grad_squares<GradShort>, dim3(grid), dim3(GRAD_THREADS), 0, s, 1, true, q, part);
+}
+
+cudaError_t launch_scale(const GradList& l, int grid, const float* part, int parts, float max_norm, float* norm,
+                         cudaStream_t s)
+{
+    if (l.count > GRAD_SHORT)
+        return launch_ex(grad_scale<GradList>, dim3(grid), dim3(GRAD_THREADS), 0, s, 1, true, l, part, parts, max_norm,
+                         norm);
+    GradShort q;
+    shorten(l, q);
+    return launch_ex(grad_scale<GradShort>, dim3(grid), dim3(GRAD_THREADS), 0, s, 1, true, q, part, parts, max_norm,
+                     norm);
+}
 
 }  // namespace
 
@@ -211,8 +264,9 @@ size_t grad_workspace(const conv_grad_t* g, int count, const DevInfo& d)
 {
     GradList l;
     size_t floats = 0;
+    const int tile = tile_of(g, count, d);
     for (int i = 0; i < count;) {
-        i = fill_list(g, count, i, l);
+        i = fill_list(g, count, i, tile, l);
         if (l.tiles > 0) floats += size_t(list_grid(l, d));
     }
     return floats * 4;
@@ -224,11 +278,12 @@ cudaError_t run_grad_norm(const conv_grad_t* g, int count, bool clip, float max_
     float* part = static_cast<float*>(ws);
     GradList l;
     int parts = 0;
+    const int tile = tile_of(g, count, d);
     for (int i = 0; i < count;) {
-        i = fill_list(g, count, i, l);
+        i = fill_list(g, count, i, tile, l);
         if (l.tiles == 0) continue;
         const int grid = list_grid(l, d);
-        const cudaError_t e = launch_ex(grad_squares, dim3(grid), dim3(GRAD_THREADS), 0, s, 1, true, l, part + parts);
+        const cudaError_t e = launch_squares(l, grid, part + parts, s);
         if (e != cudaSuccess) return e;
         parts += grid;
     }
@@ -238,10 +293,9 @@ cudaError_t run_grad_norm(const conv_grad_t* g, int count, bool clip, float max_
         return e != cudaSuccess ? e : cudaGetLastError();
     }
     for (int i = 0, first = 1; i < count;) {
-        i = fill_list(g, count, i, l);
+        i = fill_list(g, count, i, tile, l);
         if (l.tiles == 0) continue;
-        const cudaError_t e = launch_ex(grad_scale, dim3(list_grid(l, d)), dim3(GRAD_THREADS), 0, s, 1, true, l, cpart,
-                                        parts, max_norm, first ? norm : static_cast<float*>(nullptr));
+        const cudaError_t e = launch_scale(l, list_grid(l, d), cpart, parts, max_norm, first ? norm : nullptr, s);
         if (e != cudaSuccess) return e;
         first = 0;
     }
