@@ -5,10 +5,9 @@
 //
 // The gradient is a sum per row over the tokens that name it, in one of two ways:
 //
-// A table of few rows: a block takes a range of the tokens and keeps the whole table's sums (of a
-// window of columns, a lane each) in its warps' registers.  Chunk by chunk the values come in as
-// they lie, copied ahead into shared memory, the block lists the chunk's tokens by row, and each
-// warp adds its rows' tokens.  The blocks' sums are added up at the end.
+// A table of few rows: a warp keeps the sums of the whole table, a window of 32 columns, in its own
+// part of shared memory (a column a lane) and adds a contiguous share of the tokens to it, whose
+// values are copied ahead as they lie.  The copies are added up at the end.
 //
 // Else the tokens are sorted by row (least significant digit first, a stable counting sort a
 // digit), so a row's tokens are one run of the sorted order in ascending t: dy is read once, row
@@ -38,14 +37,16 @@ constexpr int CS_THREADS = 1024, CS_ITEMS = 8;             // sort by one cluste
 constexpr int CS_TOKENS = CS_THREADS * CS_ITEMS;
 constexpr int CS_WARPS = CS_THREADS / 32;
 constexpr int TAB_COLS = 32;                               // columns of a table window: a lane each
-constexpr int TAB_THREADS = 256, TAB_WARPS = TAB_THREADS / 32;
-constexpr int TAB_MAX_ROWS = 512;                          // 64 a warp
-constexpr int TAB_BLOCKS_SM = 3;
+constexpr int TAB_STEP = 32;                               // tokens a warp copies at a time
+constexpr int TAB_SMEM = 216 * 1024;
+constexpr int TAB_MAX_UNITS = 16, TAB_MIN_UNITS = 5;       // warps with a table each, a block (and SM)
 
 struct EmbedPlan {
     bool table;           // sums of the whole table in shared memory
-    int regs, blocks;     // rows a warp, blocks a window of columns
+    int units, blocks;    // copies a block; blocks a window of columns
+    int smem;
     int cluster;          // blocks of the one-cluster sort, 0: sort by kernels
+    int log_items;        // its tokens a thread: 2^log_items
     int bits, passes, digit_bits;
     int tiles;
     int V;                // vector width of a row
@@ -64,14 +65,16 @@ EmbedPlan embed_plan(const conv_embed_desc_t& e, const DevInfo& d)
         o += (bytes + 255) / 256 * 256;
         return at;
     };
-    // Whole-table sums where the tokens outnumber by far the rows that every block has to add up
-    // and write.
+    // Whole-table sums where the tokens outnumber by far the rows that every copy has to add up,
+    // and an SM holds enough copies (a copy takes a token in about 20 clocks).
+    const int unit = (e.V + 1) * TAB_COLS * 4 + 2 * TAB_STEP * TAB_COLS * (e.dtype == CONV_F32 ? 4 : 2);
     q.wins = ceil_div(e.D, TAB_COLS);
-    q.table = e.V <= TAB_MAX_ROWS && e.T >= int64_t(64) * e.V && e.T >= 8192;
+    q.units = e.V < TAB_SMEM / (TAB_COLS * 4) ? std::min(TAB_MAX_UNITS, TAB_SMEM / unit) : 0;
+    q.table = q.units >= TAB_MIN_UNITS && e.T >= int64_t(64) * e.V && e.T >= 8192;
     if (q.table) {
-        for (q.regs = 4; q.regs * TAB_WARPS < e.V; q.regs *= 2) {}
-        const int64_t most = std::max(1, d.sms * (q.regs > 32 ? 2 : TAB_BLOCKS_SM) / q.wins);
-        q.blocks = int(std::min<int64_t>(most, (e.T + 4 * TAB_THREADS - 1) / (4 * TAB_THREADS)));
+        q.smem = q.units * unit;
+        const int64_t most = std::max(1, d.sms / q.wins);
+        q.blocks = int(std::min<int64_t>(most, (e.T + q.units * 4 * TAB_STEP - 1) / (q.units * 4 * TAB_STEP)));
         q.off_part = take(size_t(q.blocks) * e.V * e.D * 4);
         q.bytes = o;
         return q;
@@ -79,8 +82,11 @@ EmbedPlan embed_plan(const conv_embed_desc_t& e, const DevInfo& d)
     while ((int64_t(1) << q.bits) <= e.V) ++q.bits;  // keys 0 .. V (V: no row)
     q.passes = std::max(1, ceil_div(q.bits, SORT_MAX_BITS));
     q.digit_bits = ceil_div(q.bits, q.passes);
-    while (q.cluster < kMaxCluster && e.T > int64_t(q.cluster) * CS_TOKENS) q.cluster = std::max(1, q.cluster * 2);
-    if (e.T > int64_t(q.cluster) * CS_TOKENS) q.cluster = 0;
+    if (e.T <= int64_t(kMaxCluster) * CS_TOKENS) {  // as many blocks as have a token a thread
+        q.cluster = 1;
+        while (q.cluster < kMaxCluster && e.T > int64_t(q.cluster) * CS_THREADS) q.cluster *= 2;
+        while (e.T > (int64_t(q.cluster) * CS_THREADS << q.log_items)) ++q.log_items;
+    }
     q.tiles = int((e.T + SORT_TILE - 1) / SORT_TILE);
     const int es = e.dtype == CONV_F32 ? 4 : 2;
     q.V = 16 / es;
@@ -88,9 +94,9 @@ EmbedPlan embed_plan(const conv_embed_desc_t& e, const DevInfo& d)
     q.nv = e.D / q.V;
     q.wins = ceil_div(q.nv, SUM_THREADS);
     q.cols = ceil_div(q.nv, q.wins);
-    // Chunks: long, so that few runs are cut, while about 512 threads an SM (eight loads each in
-    // flight) have a part of them.
-    const int64_t groups = std::max<int64_t>(1, int64_t(d.sms) * 512 / std::max(1, q.nv));
+    // Chunks: long, so that few runs are cut, while about 1024 threads an SM (eight loads each
+    // in flight) have a part of them.
+    const int64_t groups = std::max<int64_t>(1, int64_t(d.sms) * 1024 / std::max(1, q.nv));
     q.chunk = int(std::min<int64_t>(512, std::max<int64_t>(16, (e.T + groups - 1) / groups)));
     q.chunks = int((e.T + q.chunk - 1) / q.chunk);
     for (int i = 0; i < (q.cluster ? 1 : 2); ++i) {
@@ -179,21 +185,26 @@ __device__ __forceinline__ void st_dsmem(uint32_t addr, uint32_t v)
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// Inclusive scan over a block's threads.
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* sm)
+// Inclusive scan over a block's threads (up to 32 warps).
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v)
 {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
-        if (lane >= o) v += u;
+        if ((threadIdx.x & 31) >= unsigned(o)) v += u;
     }
+    return v;
+}
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* sm)
+{
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    v = warp_scan(v);
     if (lane == 31) sm[w] = v;
     __syncthreads();
-    uint32_t before = 0;
-    for (int i = 0; i < w; ++i) before += sm[i];
+    const uint32_t t = warp_scan(lane < int(blockDim.x >> 5) ? sm[lane] : 0u);
+    const uint32_t before = __shfl_sync(0xFFFFFFFFu, t, max(w, 1) - 1);
     __syncthreads();
-    return v + before;
+    return w ? v + before : v;
 }
 
 // Block b: the exclusive scan of bin b's counts over the tiles, and the bin's total.
@@ -295,13 +306,13 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_scatter(int n, int rows, in
 }
 
 // The whole sort by one cluster of S blocks (blockIdx.x < S), which hold the tokens in order,
-// CS_TOKENS a block; the other blocks write zeros to dtable meanwhile.  A pass ranks the tokens of
+// up to CS_TOKENS a block; the other blocks write zeros to dtable meanwhile.  A pass ranks the tokens of
 // a digit as sort_scatter does (16 bits hold a warp's counts), the blocks read each other's counts
 // of each digit, and every token goes straight to its place in the next order, in whichever block
 // that lies.
 template <typename I>
 __global__ void __launch_bounds__(CS_THREADS, 1)
-sort_cluster(int n, int rows, int padding, int S, int passes, int digit_bits, const I* idx, uint32_t* keys_out,
+sort_cluster(int n, int rows, int padding, int S, int log_items, int passes, int digit_bits, const I* idx, uint32_t* keys_out,
              uint32_t* pos_out, uint4* fill, int64_t fill_vecs, unsigned char* fill_tail, int fill_rest)
 {
     extern __shared__ __align__(16) uint32_t cs[];
@@ -321,16 +332,19 @@ sort_cluster(int n, int rows, int padding, int S, int passes, int digit_bits, co
     uint16_t* cnt = reinterpret_cast<uint16_t*>(sm + CS_WARPS);  // warps x bins
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int rank = S > 1 ? int(tc::cluster_rank()) : 0;
-    const int here = max(0, min(CS_TOKENS, n - rank * CS_TOKENS));
-    const int first = w * (32 * CS_ITEMS) + lane;
+    const int log_cap = log_items + 10;  // tokens a block: 2^log_cap
+    static_assert(CS_THREADS == 1 << 10, "a block's tokens");
+    const int here = max(0, min(1 << log_cap, n - (rank << log_cap)));
+    const int first = (w << (5 + log_items)) + lane;
+    const int items = 1 << log_items;
     uint32_t key[CS_ITEMS], p[CS_ITEMS], rk[CS_ITEMS];
     tc::grid_dep_wait();
 #pragma unroll
     for (int i = 0; i < CS_ITEMS; ++i) {
         const int t = first + i * 32;
-        p[i] = uint32_t(rank * CS_TOKENS + t);
+        p[i] = uint32_t((rank << log_cap) + t);
         key[i] = 0xFFFFFFFFu;
-        if (t < here) {
+        if (i < items && t < here) {
             const int r = token_row(idx, int64_t(p[i]), rows, padding);
             key[i] = r >= 0 ? uint32_t(r) : uint32_t(rows);
         }
@@ -341,6 +355,7 @@ sort_cluster(int n, int rows, int padding, int S, int passes, int digit_bits, co
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < CS_ITEMS; ++i) {
+            if (i >= items) break;
             const bool in = first + i * 32 < here;
             const uint32_t dg = in ? (key[i] >> shift) & uint32_t(bins - 1) : 0xFFFFFFFFu;
             const uint32_t same = __match_any_sync(0xFFFFFFFFu, dg), below = same & ((1u << lane) - 1u);
@@ -354,6 +369,7 @@ sort_cluster(int n, int rows, int padding, int S, int passes, int digit_bits, co
         // a digit's counts of the warps to first ranks in the block, and its total
         uint32_t total = 0;
         if (int(threadIdx.x) < bins) {
+#pragma unroll 8
             for (int k = 0; k < CS_WARPS; ++k) {
                 const uint32_t c = cnt[k * bins + threadIdx.x];
                 cnt[k * bins + threadIdx.x] = uint16_t(total);
@@ -390,7 +406,7 @@ sort_cluster(int n, int rows, int padding, int S, int passes, int digit_bits, co
         uint32_t* dp = kv + (2 + (pass & 1)) * CS_TOKENS;
 #pragma unroll
         for (int i = 0; i < CS_ITEMS; ++i)
-            if (first + i * 32 < here) {
+            if (i < items && first + i * 32 < here) {
                 const uint32_t dg = (key[i] >> shift) & uint32_t(bins - 1);
                 const uint32_t at = base[dg] + cnt[w * bins + dg] + rk[i];
                 if (last) {
@@ -400,7 +416,7 @@ sort_cluster(int n, int rows, int padding, int S, int passes, int digit_bits, co
                     dk[at] = key[i];
                     dp[at] = p[i];
                 } else {
-                    const uint32_t r = at / CS_TOKENS, slot = at % CS_TOKENS;
+                    const uint32_t r = at >> log_cap, slot = at & ((1u << log_cap) - 1u);
                     st_dsmem(tc::dsmem_addr(tc::smem_u32(dk + slot), r), key[i]);
                     st_dsmem(tc::dsmem_addr(tc::smem_u32(dp + slot), r), p[i]);
                 }
@@ -414,7 +430,7 @@ sort_cluster(int n, int rows, int padding, int S, int passes, int digit_bits, co
         }
 #pragma unroll
         for (int i = 0; i < CS_ITEMS; ++i)
-            if (first + i * 32 < here) {
+            if (i < items && first + i * 32 < here) {
                 key[i] = dk[first + i * 32];
                 p[i] = dp[first + i * 32];
             }
@@ -426,105 +442,96 @@ sort_cluster(int n, int rows, int padding, int S, int passes, int digit_bits, co
 }
 
 // ---- whole-table sums ------------------------------------------------------------------------
-// Block (range, window): tokens [t0, t1), TAB_THREADS at a time, columns [c0, c0 + TAB_COLS).
-// Warp w keeps the sums of the rows w, w + TAB_WARPS, ... (R of them), a column a lane.  A chunk's
-// values are copied a chunk ahead into one of two tiles.  Its tokens are listed by row with
-// matches in the warps and a scan over the rows; the list keeps the tokens' order, so a row's sum
-// has one order.
+// Block (range, window), warp u: its own table of rows + 1 rows (the last one takes the tokens that
+// name none) and two tiles of TAB_STEP tokens.  Four tokens at a time are added side by side where
+// their rows differ, else one after the other; either way a row's tokens are added in order.
 template <int BYTES> __device__ __forceinline__ void tab_copy(uint32_t dst, const void* src)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 
-template <typename T, typename I, int R, int V>
-__global__ void __launch_bounds__(TAB_THREADS, R > 32 ? 2 : TAB_BLOCKS_SM)
-embed_table(int n, int rows, int padding, int D, int blocks, const I* idx, const T* dy, float* part)
+template <typename T, typename I, int V>
+__global__ void __launch_bounds__(TAB_MAX_UNITS * 32, 1)
+embed_table(int n, int rows, int padding, int D, int blocks, int units, const I* idx, const T* dy, float* part)
 {
-    constexpr int SEG = TAB_COLS / V;                       // copies a token's segment
+    constexpr int COPIES = TAB_COLS / V, AT_ONCE = 32 / COPIES;  // copies a token, tokens a copy of the warp
     extern __shared__ __align__(16) unsigned char dynt[];
-    T* tile = reinterpret_cast<T*>(dynt);                   // 2 x TAB_THREADS x TAB_COLS
-    __shared__ uint16_t cnt[TAB_WARPS][R * TAB_WARPS];      // the warps' tokens of each row, then their places
-    __shared__ uint16_t off[R * TAB_WARPS + 1];             // where each row's list begins
-    __shared__ uint16_t list[TAB_THREADS];
-    __shared__ uint32_t sm[TAB_WARPS];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, u = threadIdx.x >> 5;
+    float* tab = reinterpret_cast<float*>(dynt);            // units x (rows + 1) x TAB_COLS
+    const int size = (rows + 1) * TAB_COLS;
+    float* my = tab + size_t(u) * size + lane;
+    T* tile = reinterpret_cast<T*>(tab + size_t(units) * size) + u * (2 * TAB_STEP * TAB_COLS);
     const int range = int(blockIdx.x) % blocks, c0 = int(blockIdx.x) / blocks * TAB_COLS;
-    const int t0 = int(int64_t(n) * range / blocks), t1 = int(int64_t(n) * (range + 1) / blocks);
+    const int64_t parts = int64_t(blocks) * units, at = int64_t(range) * units + u;
+    const int t0 = int(int64_t(n) * at / parts), t1 = int(int64_t(n) * (at + 1) / parts);
     const int width = min(TAB_COLS, D - c0);
-    float acc[R];
+    const int tok0 = lane / COPIES, col = lane % COPIES * V;  // this lane's part of a copy
+    for (int r = 0; r <= rows; ++r) my[r * TAB_COLS] = 0.f;
+    for (int i = lane; i < 2 * TAB_STEP * TAB_COLS; i += 32) Elem<T>::st(tile + i, 0.f);
+    __syncwarp();
+    int next = 0;
+    auto load = [&](int t, T* dst) {  // the step at t: its values, and lane l's token's row (a table offset)
+        const int r = t + lane < t1 ? token_row(idx, int64_t(t) + lane, rows, padding) : -1;
+        next = (r >= 0 ? r : rows) * TAB_COLS;
+        const T* src = dy + int64_t(t + tok0) * D + c0 + col;
+        dst += tok0 * TAB_COLS + col;
+        const int left = t1 - t - tok0;
+        if (col < width)
 #pragma unroll
-    for (int j = 0; j < R; ++j) acc[j] = 0.f;
-    int next_row = -1;
-    auto load = [&](int t, int buf) {  // the chunk at t: its values, and this thread's token's row
-        const int here = min(TAB_THREADS, t1 - t);
-        next_row = int(threadIdx.x) < here ? token_row(idx, int64_t(t) + threadIdx.x, rows, padding) : -1;
-        for (int i = threadIdx.x; i < here * SEG; i += TAB_THREADS) {
-            const int tok = i / SEG, c = i % SEG * V;
-            if (c < width) {
-                T* dst = tile + (buf * TAB_THREADS + tok) * TAB_COLS + c;
-                const T* src = dy + int64_t(t + tok) * D + c0 + c;
-                if constexpr (sizeof(T) * V >= 4) tab_copy<int(sizeof(T)) * V>(tc::smem_u32(dst), src);
-                else *dst = *src;
-            }
-        }
+            for (int i = 0; i < TAB_STEP; i += AT_ONCE, src += int64_t(AT_ONCE) * D, dst += AT_ONCE * TAB_COLS)
+                if (i < left) {
+                    if constexpr (sizeof(T) * V >= 4) tab_copy<int(sizeof(T)) * V>(tc::smem_u32(dst), src);
+                    else *dst = *src;
+                }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     tc::grid_dep_wait();
-    if (t0 < t1) load(t0, 0);
+    if (t0 < t1) load(t0, tile);
     int buf = 0;
-    for (int t = t0; t < t1; t += TAB_THREADS, buf ^= 1) {
-        const int row = next_row;
-        if (t + TAB_THREADS < t1) load(t + TAB_THREADS, buf ^ 1);
-        for (int i = threadIdx.x; i < TAB_WARPS * R * TAB_WARPS / 2; i += TAB_THREADS)
-            reinterpret_cast<uint32_t*>(&cnt[0][0])[i] = 0;
-        __syncthreads();
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, row), below = same & ((1u << lane) - 1u);
-        if (row >= 0 && below == 0) cnt[w][row] = uint16_t(__popc(same));
-        __syncthreads();
-        // rows' totals over the warps, scanned: PER rows a thread
-        constexpr int PER = (R * TAB_WARPS + TAB_THREADS - 1) / TAB_THREADS;
-        uint32_t tot[PER], mine = 0;
-#pragma unroll
-        for (int k = 0; k < PER; ++k) {
-            const int r = int(threadIdx.x) * PER + k;
-            tot[k] = 0;
-            if (r < R * TAB_WARPS)
-#pragma unroll
-                for (int x = 0; x < TAB_WARPS; ++x) {
-                    const uint32_t c = cnt[x][r];
-                    cnt[x][r] = uint16_t(tot[k]);
-                    tot[k] += c;
-                }
-            mine += tot[k];
+    for (int t = t0; t < t1; t += TAB_STEP, buf ^= 1) {
+        const int row = next;
+        if (t + TAB_STEP < t1) {
+            load(t + TAB_STEP, tile + (buf ^ 1) * (TAB_STEP * TAB_COLS));
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
         }
-        uint32_t at = block_scan(mine, sm) - mine;
+        // bit 4g + j: token j of group g has the row of one before it in the group
+        bool again = false;
 #pragma unroll
-        for (int k = 0; k < PER; ++k) {
-            const int r = int(threadIdx.x) * PER + k;
-            if (r <= R * TAB_WARPS) off[r] = uint16_t(at);
-            at += tot[k];
-        }
-        if (R * TAB_WARPS == PER * TAB_THREADS && threadIdx.x == TAB_THREADS - 1) off[R * TAB_WARPS] = uint16_t(at);
-        __syncthreads();
-        if (row >= 0) list[off[row] + cnt[w][row] + __popc(below)] = uint16_t(threadIdx.x);
-        if (t + TAB_THREADS < t1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-        else asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncthreads();
-        const T* src = tile + buf * TAB_THREADS * TAB_COLS + lane;
+        for (int k = 1; k < 4; ++k) again |= __shfl_up_sync(0xFFFFFFFFu, row, k) == row && (lane & 3) >= k;
+        const uint32_t dup = __ballot_sync(0xFFFFFFFFu, again);  // (the tile's copies are visible to the warp after it)
+        const T* v = tile + buf * (TAB_STEP * TAB_COLS) + lane;
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
-            const int r = w + j * TAB_WARPS, e = off[r + 1];
-#pragma unroll 4
-            for (int k = off[r]; k < e; ++k) acc[j] += Elem<T>::ld(src + int(list[k]) * TAB_COLS);
+        for (int g = 0; g < TAB_STEP / 4; ++g) {
+            float* o[4];
+            float f[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                o[j] = my + __shfl_sync(0xFFFFFFFFu, row, 4 * g + j);
+                f[j] = Elem<T>::ld(v + (4 * g + j) * TAB_COLS);
+            }
+            if ((dup >> (4 * g) & 0xFu) == 0) {
+                float s[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[j] = *o[j];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) *o[j] = s[j] + f[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) *o[j] += f[j];
+            }
         }
-        __syncthreads();
+        __syncwarp();
     }
-    if (lane < width)
-#pragma unroll
-        for (int j = 0; j < R; ++j) {
-            const int r = w + j * TAB_WARPS;
-            if (r < rows) part[(int64_t(range) * rows + r) * D + c0 + lane] = acc[j];
-        }
+    __syncthreads();
+    // the copies added in order
+    for (int i = threadIdx.x; i < rows * TAB_COLS; i += blockDim.x) {
+        float s = 0.f;
+        for (int k = 0; k < units; ++k) s += tab[size_t(k) * size + i];
+        const int r = i / TAB_COLS, c = i % TAB_COLS;
+        if (c < width) part[(int64_t(range) * rows + r) * D + c0 + c] = s;
+    }
 }
 
 // dtable = scale * the blocks' sums, added in order: eight lanes an element (an eighth of the
@@ -610,23 +617,33 @@ __global__ void __launch_bounds__(SUM_THREADS) embed_sum(int n, int rows, int D,
             v.store(dtable + int64_t(cur) * D + c);
         }
     };
-    for (int i = i0; i < run.end; i += U) {
-        uint32_t k[U];
-        Vec<T, V> v[U];
+    uint32_t k[U], p[U];  // of the next tokens, a step ahead of their values
+    auto names = [&](int i) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             // beyond the chunk only the run at its end counts
             k[u] = i + u < run.end ? keys[i + u] : 0xFFFFFFFFu;
+            p[u] = i + u < run.end ? pos[i + u] : 0u;
             if (i + u >= i1 && k[u] != last) k[u] = 0xFFFFFFFFu;
-            if (k[u] < uint32_t(rows)) v[u].load(dy + int64_t(pos[i + u]) * D + c);
+        }
+    };
+    names(i0);
+    for (int i = i0; i < run.end; i += U) {
+        uint32_t kc[U];
+        Vec<T, V> v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            kc[u] = k[u];
+            if (k[u] < uint32_t(rows)) v[u].load(dy + int64_t(p[u]) * D + c);
             else v[u].zero();
         }
+        if (i + U < run.end) names(i + U);
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (i + u < i1 || k[u] == last) {
-                if (k[u] != cur) {
+            if (i + u < i1 || kc[u] == last) {
+                if (kc[u] != cur) {
                     flush(false);
-                    cur = k[u];
+                    cur = kc[u];
                     head = skip = false;
 #pragma unroll
                     for (int j = 0; j < V; ++j) acc[j] = 0.f;
@@ -651,24 +668,27 @@ __global__ void __launch_bounds__(FIX_THREADS) embed_fix(int n, int rows, int D,
     const int lanes = FIX_THREADS / cols, lane = int(threadIdx.x) / cols, col = int(threadIdx.x) - lane * cols;
     const int c = (win * cols + col) * V;
     tc::grid_dep_wait();
-    if (threadIdx.x < FIX_CHUNKS) {
-        const int ch = ch0 + int(threadIdx.x);
+    static_assert(FIX_THREADS / 32 >= FIX_CHUNKS, "a warp a chunk");
+    if (int(threadIdx.x) < FIX_CHUNKS * 32) {
+        const int ch = ch0 + int(threadIdx.x >> 5), wl = int(threadIdx.x & 31);
         int cnt = 0;
         if (ch < chunks) {
             const int i0 = ch * chunk, i1 = min(n, i0 + chunk);
             const uint32_t key = keys[i1 - 1];
             if (key < uint32_t(rows) && ChunkRuns(keys, n, chunk, i0, i1).tail) {
-                // the last chunk that the run reaches, by bisection over the chunks' first keys
-                int lo = ch + 1, hi = chunks - 1;
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) / 2;
-                    if (keys[mid * chunk] == key) lo = mid;
-                    else hi = mid - 1;
+                // the last chunk that the run reaches (whose first key is the run's), 32 probes at a time
+                int lo = ch + 1, hi = chunks;  // lo: reached; hi: not
+                while (hi - lo > 1) {
+                    const int step = (hi - lo + 31) / 32, at = lo + (wl + 1) * step;
+                    const uint32_t in = __ballot_sync(0xFFFFFFFFu, at < hi && keys[int64_t(at) * chunk] == key);
+                    const int got = __popc(in);  // the first `got` probes
+                    hi = min(hi, lo + (got + 1) * step);
+                    lo += got * step;
                 }
                 cnt = lo - ch;
             }
         }
-        reach[threadIdx.x] = cnt;
+        if (wl == 0) reach[threadIdx.x >> 5] = cnt;
     }
     __syncthreads();
     for (int k = 0; k < FIX_CHUNKS; ++k) {
@@ -744,7 +764,7 @@ cudaError_t sort_tokens(const conv_embed_desc_t& e, const EmbedPlan& q, const De
         const int more = round_up(int(std::min<int64_t>(std::max<int64_t>(1, want), d.sms)), S);
         where = 0;
         return launch_ex(sort_cluster<I>, dim3(S + more), dim3(CS_THREADS), smem, s, S, true, n, e.V, e.padding_idx, S,
-                         q.passes, q.digit_bits, idx, reinterpret_cast<uint32_t*>(ws + q.off_keys[0]),
+                         q.log_items, q.passes, q.digit_bits, idx, reinterpret_cast<uint32_t*>(ws + q.off_keys[0]),
                          reinterpret_cast<uint32_t*>(ws + q.off_pos[0]), static_cast<uint4*>(dtable), vecs,
                          static_cast<unsigned char*>(dtable) + vecs * 16, int(bytes - vecs * 16));
     }
@@ -773,15 +793,14 @@ cudaError_t sort_tokens(const conv_embed_desc_t& e, const EmbedPlan& q, const De
     return cudaSuccess;
 }
 
-template <typename T, typename I, int R, int V>
-cudaError_t table_rv(const conv_embed_desc_t& e, const EmbedPlan& q, const I* idx, const T* dy, float* part,
-                     cudaStream_t s)
+template <typename T, typename I, int V>
+cudaError_t table_v(const conv_embed_desc_t& e, const EmbedPlan& q, const I* idx, const T* dy, float* part,
+                    cudaStream_t s)
 {
-    constexpr int smem = 2 * TAB_THREADS * TAB_COLS * int(sizeof(T));
-    const cudaError_t r = ensure_smem<embed_table<T, I, R, V>>(smem);
+    const cudaError_t r = ensure_smem<embed_table<T, I, V>>(q.smem);
     if (r != cudaSuccess) return r;
-    return launch_ex(embed_table<T, I, R, V>, dim3(unsigned(q.blocks) * unsigned(q.wins)), dim3(TAB_THREADS), smem, s,
-                     1, true, int(e.T), e.V, e.padding_idx, e.D, q.blocks, idx, dy, part);
+    return launch_ex(embed_table<T, I, V>, dim3(unsigned(q.blocks) * unsigned(q.wins)), dim3(q.units * 32), q.smem, s,
+                     1, true, int(e.T), e.V, e.padding_idx, e.D, q.blocks, q.units, idx, dy, part);
 }
 
 template <typename T, typename I>
@@ -790,20 +809,9 @@ cudaError_t table_t(const conv_embed_desc_t& e, const EmbedPlan& q, const I* idx
 {
     // copies of 16 bytes, or of 4 (bf16 of an odd width: 2) where the rows are not aligned for them
     constexpr int W = 16 / int(sizeof(T)), N = 4 / int(sizeof(T));
-    const int V = e.D % W == 0 ? W : e.D % N == 0 ? N : 1;
-    cudaError_t r = cudaSuccess;
-#define EMB_CALL(R_)                                                        \
-    r = V == W   ? table_rv<T, I, R_, W>(e, q, idx, dy, part, s)            \
-        : V == N ? table_rv<T, I, R_, N>(e, q, idx, dy, part, s)            \
-                 : table_rv<T, I, R_, 1>(e, q, idx, dy, part, s)
-    switch (q.regs) {
-        case 4: EMB_CALL(4); break;
-        case 8: EMB_CALL(8); break;
-        case 16: EMB_CALL(16); break;
-        case 32: EMB_CALL(32); break;
-        default: EMB_CALL(64); break;
-    }
-#undef EMB_CALL
+    cudaError_t r = e.D % W == 0   ? table_v<T, I, W>(e, q, idx, dy, part, s)
+                    : e.D % N == 0 ? table_v<T, I, N>(e, q, idx, dy, part, s)
+                                   : table_v<T, I, 1>(e, q, idx, dy, part, s);
     if (r != cudaSuccess) return r;
     const int64_t values = int64_t(e.V) * e.D;
     const float* cpart = part;

@@ -31,6 +31,9 @@ CASES = {
     "two_digits": (30000, 70001, 8, "zipf"),
     "three_digits": (6000, 700001, 4, "uniform"),
     "many_tokens": (200000, 130, 12, "zipf"),
+    "few_rows_two_windows": (20000, 100, 40, "zipf"),
+    "few_rows_equal": (9000, 3, 33, "equal"),
+    "few_rows_most": (40000, 512, 7, "zipf"),
     "bins_511": (10000, 511, 16, "uniform"),
     "bins_512": (10000, 512, 16, "uniform"),
     "tile_end": (2048, 60, 16, "uniform"),
