@@ -30,15 +30,15 @@ constexpr int SORT_ITEMS = 8;                              // a thread
 constexpr int SORT_TILE = SORT_THREADS * SORT_ITEMS;       // tokens a block sorts
 constexpr int SORT_MAX_BITS = 9;                           // digit
 constexpr int SORT_MAX_BINS = 1 << SORT_MAX_BITS;
-constexpr int SUM_THREADS = 256;
-constexpr int FIX_THREADS = 512;
-constexpr int FIX_CHUNKS = 8;                              // chunks a block of the last kernel looks at
+constexpr int SUM_THREADS = 256, SUM_BLOCKS_SM = 3;
+constexpr int FIX_THREADS = 1024;
+constexpr int FIX_CHUNKS = 16;                             // chunks a block of the last kernel looks at
 constexpr int CS_THREADS = 1024, CS_ITEMS = 8;             // sort by one cluster: a block's threads, tokens a thread
 constexpr int CS_TOKENS = CS_THREADS * CS_ITEMS;
 constexpr int CS_WARPS = CS_THREADS / 32;
 constexpr int TAB_COLS = 32;                               // columns of a table window: a lane each
 constexpr int TAB_STEP = 32;                               // tokens a warp copies at a time
-constexpr int TAB_SMEM = 216 * 1024;
+constexpr int TAB_SMEM = 225 * 1024;
 constexpr int TAB_MAX_UNITS = 16, TAB_MIN_UNITS = 5;       // warps with a table each, a block (and SM)
 
 struct EmbedPlan {
@@ -94,9 +94,8 @@ EmbedPlan embed_plan(const conv_embed_desc_t& e, const DevInfo& d)
     q.nv = e.D / q.V;
     q.wins = ceil_div(q.nv, SUM_THREADS);
     q.cols = ceil_div(q.nv, q.wins);
-    // Chunks: long, so that few runs are cut, while about 1024 threads an SM (eight loads each
-    // in flight) have a part of them.
-    const int64_t groups = std::max<int64_t>(1, int64_t(d.sms) * 1024 / std::max(1, q.nv));
+    // Chunks: long, so that few runs are cut, while the groups fill the SMs once.
+    const int64_t groups = std::max<int64_t>(1, int64_t(d.sms) * SUM_BLOCKS_SM * (SUM_THREADS / q.cols) / q.wins);
     q.chunk = int(std::min<int64_t>(512, std::max<int64_t>(16, (e.T + groups - 1) / groups)));
     q.chunks = int((e.T + q.chunk - 1) / q.chunk);
     for (int i = 0; i < (q.cluster ? 1 : 2); ++i) {
@@ -180,9 +179,9 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_count(int n, int rows, int 
     for (int i = threadIdx.x; i < bins; i += SORT_THREADS) counts[size_t(i) * tiles + blockIdx.x] = hist[i];
 }
 
-__device__ __forceinline__ void st_dsmem(uint32_t addr, uint32_t v)
+__device__ __forceinline__ void st_dsmem(uint32_t addr, uint2 v)
 {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
 }
 
 // Inclusive scan over a block's threads (up to 32 warps).
@@ -230,7 +229,8 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_scan(int tiles, uint32_t* c
 
 // Stable scatter by one digit.  Warp w holds the tile's tokens [w*256, (w+1)*256), 32 at a time
 // in order; lanes with equal digits find each other by a match, the lowest one advances the
-// warp's counter of the digit.
+// warp's counter of the digit.  The tile is put in the digit's order in shared memory first, so
+// that what goes to memory are runs of neighbours.
 template <typename I>
 __global__ void __launch_bounds__(SORT_THREADS) sort_scatter(int n, int rows, int padding, const I* idx,
                                                              const uint32_t* keys, const uint32_t* pos, int shift,
@@ -239,25 +239,16 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_scatter(int n, int rows, in
                                                              uint32_t* pos_out)
 {
     constexpr int WARPS = SORT_THREADS / 32;
-    __shared__ uint32_t cnt[WARPS][SORT_MAX_BINS];
-    __shared__ uint32_t base[SORT_MAX_BINS];
-    __shared__ uint32_t sm[WARPS];
+    __shared__ uint16_t cnt[WARPS][SORT_MAX_BINS];  // the warps' counts, then first places in the tile
+    __shared__ uint32_t base[SORT_MAX_BINS];        // first place of the tile's tokens of a digit, less that in the tile
+    __shared__ uint2 stage[SORT_TILE];
+    __shared__ uint32_t sm[WARPS], last[2];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    for (int i = threadIdx.x; i < WARPS * SORT_MAX_BINS; i += SORT_THREADS) (&cnt[0][0])[i] = 0;
+    for (int i = threadIdx.x; i < WARPS * SORT_MAX_BINS / 2; i += SORT_THREADS)
+        reinterpret_cast<uint32_t*>(&cnt[0][0])[i] = 0;
     tc::grid_dep_wait();
-    uint32_t carry = 0;
-    for (int i0 = 0; i0 < bins; i0 += SORT_THREADS) {  // first position of each bin
-        const int i = i0 + int(threadIdx.x);
-        const uint32_t v = i < bins ? totals[i] : 0u;
-        const uint32_t s = block_scan(v, sm);
-        if (i < bins) base[i] = carry + s - v + counts[size_t(i) * tiles + blockIdx.x];
-        __shared__ uint32_t last;
-        if (threadIdx.x == SORT_THREADS - 1) last = s;
-        __syncthreads();
-        carry += last;
-        __syncthreads();
-    }
     const int t0 = int(blockIdx.x) * SORT_TILE + w * (32 * SORT_ITEMS) + lane;
+    const int here = min(SORT_TILE, n - int(blockIdx.x) * SORT_TILE);
     uint32_t key[SORT_ITEMS], p[SORT_ITEMS], rank[SORT_ITEMS];
 #pragma unroll
     for (int i = 0; i < SORT_ITEMS; ++i) {
@@ -274,61 +265,90 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_scatter(int n, int rows, in
             }
         }
     }
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < SORT_ITEMS; ++i) {
         const bool in = t0 + i * 32 < n;
         const uint32_t dg = in ? (key[i] >> shift) & uint32_t(bins - 1) : 0xFFFFFFFFu;
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, dg);
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, dg), below = same & ((1u << lane) - 1u);
         const uint32_t before = in ? cnt[w][dg] : 0u;
         __syncwarp();
-        rank[i] = before + __popc(same & ((1u << lane) - 1u));
-        if (in && (same & ((1u << lane) - 1u)) == 0) cnt[w][dg] = before + __popc(same);
+        rank[i] = before + __popc(below);
+        if (in && below == 0) cnt[w][dg] = uint16_t(before + __popc(same));
         __syncwarp();
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < bins; i += SORT_THREADS) {  // the warps' counts to first positions
-        uint32_t at = base[i];
+    uint32_t carry = 0, local = 0;
+    for (int i0 = 0; i0 < bins; i0 += SORT_THREADS) {  // first place of each digit, in all and in the tile
+        const int i = i0 + int(threadIdx.x);
+        uint32_t mine = 0;
+        if (i < bins)
 #pragma unroll
-        for (int k = 0; k < WARPS; ++k) {
-            const uint32_t c = cnt[k][i];
-            cnt[k][i] = at;
-            at += c;
+            for (int k = 0; k < WARPS; ++k) {
+                const uint32_t c = cnt[k][i];
+                cnt[k][i] = uint16_t(mine);
+                mine += c;
+            }
+        const uint32_t v = i < bins ? totals[i] : 0u;
+        const uint32_t s = block_scan(v, sm), m = block_scan(mine, sm);
+        const uint32_t at = local + m - mine;
+        if (i < bins) {
+            base[i] = carry + s - v + counts[size_t(i) * tiles + blockIdx.x] - at;
+#pragma unroll
+            for (int k = 0; k < WARPS; ++k) cnt[k][i] = uint16_t(cnt[k][i] + at);
         }
+        if (threadIdx.x == SORT_THREADS - 1) {
+            last[0] = s;
+            last[1] = m;
+        }
+        __syncthreads();
+        carry += last[0];
+        local += last[1];
+        __syncthreads();
     }
-    __syncthreads();
 #pragma unroll
     for (int i = 0; i < SORT_ITEMS; ++i)
-        if (t0 + i * 32 < n) {
-            const uint32_t at = cnt[w][(key[i] >> shift) & uint32_t(bins - 1)] + rank[i];
-            keys_out[at] = key[i];
-            pos_out[at] = p[i];
+        if (t0 + i * 32 < n) stage[cnt[w][(key[i] >> shift) & uint32_t(bins - 1)] + rank[i]] = make_uint2(key[i], p[i]);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < SORT_ITEMS; ++i) {
+        const int s = i * SORT_THREADS + int(threadIdx.x);
+        if (s < here) {
+            const uint2 e = stage[s];
+            const uint32_t at = base[(e.x >> shift) & uint32_t(bins - 1)] + uint32_t(s);
+            keys_out[at] = e.x;
+            pos_out[at] = e.y;
         }
+    }
 }
 
 // The whole sort by one cluster of S blocks (blockIdx.x < S), which hold the tokens in order,
-// up to CS_TOKENS a block; the other blocks write zeros to dtable meanwhile.  A pass ranks the tokens of
-// a digit as sort_scatter does (16 bits hold a warp's counts), the blocks read each other's counts
-// of each digit, and every token goes straight to its place in the next order, in whichever block
-// that lies.
+// up to CS_TOKENS a block; the other blocks write zeros to dtable meanwhile.  A pass ranks the
+// tokens of a digit as sort_scatter does (16 bits hold a warp's counts), the blocks read each
+// other's counts of each digit, and the tokens, put in the digit's order in the block first, go in
+// runs to their places in the next order, in whichever block those lie.
 template <typename I>
 __global__ void __launch_bounds__(CS_THREADS, 1)
-sort_cluster(int n, int rows, int padding, int S, int log_items, int passes, int digit_bits, const I* idx, uint32_t* keys_out,
-             uint32_t* pos_out, uint4* fill, int64_t fill_vecs, unsigned char* fill_tail, int fill_rest)
+sort_cluster(int n, int rows, int padding, int S, int log_items, int passes, int digit_bits, const I* idx,
+             uint32_t* keys_out, uint32_t* pos_out, uint4* fill, int64_t fill_vecs, unsigned char* fill_tail,
+             int fill_rest)
 {
-    extern __shared__ __align__(16) uint32_t cs[];
+    extern __shared__ __align__(16) uint2 cs[];
     if (int(blockIdx.x) >= S) {
         const int64_t nb = int64_t(gridDim.x) - S, t = (int64_t(blockIdx.x) - S) * CS_THREADS + threadIdx.x;
         tc::grid_dep_wait();
+        tc::grid_dep_launch();
 #pragma unroll 4
         for (int64_t i = t; i < fill_vecs; i += nb * CS_THREADS) fill[i] = make_uint4(0, 0, 0, 0);
         if (t < fill_rest) fill_tail[t] = 0;
         return;
     }
     const int bins = 1 << digit_bits;
-    uint32_t* kv = cs;                                       // 2 x CS_TOKENS keys, then 2 x CS_TOKENS positions
-    uint32_t* hist = cs + 4 * CS_TOKENS;                     // bins: the block's counts, read by the others
-    uint32_t* base = hist + SORT_MAX_BINS;                   // bins
-    uint32_t* sm = base + SORT_MAX_BINS;                     // CS_WARPS
+    uint2* stage = cs;                                           // the block's tokens (key, position) by digit
+    uint2* next = cs + CS_TOKENS;                                // its part of the next order, written by all blocks
+    uint32_t* hist = reinterpret_cast<uint32_t*>(next + CS_TOKENS);  // bins: the block's counts, read by the others
+    uint32_t* base = hist + SORT_MAX_BINS;                       // bins: first place, less that in the block
+    uint32_t* sm = base + SORT_MAX_BINS;                         // CS_WARPS
     uint16_t* cnt = reinterpret_cast<uint16_t*>(sm + CS_WARPS);  // warps x bins
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int rank = S > 1 ? int(tc::cluster_rank()) : 0;
@@ -337,27 +357,29 @@ sort_cluster(int n, int rows, int padding, int S, int log_items, int passes, int
     const int here = max(0, min(1 << log_cap, n - (rank << log_cap)));
     const int first = (w << (5 + log_items)) + lane;
     const int items = 1 << log_items;
-    uint32_t key[CS_ITEMS], p[CS_ITEMS], rk[CS_ITEMS];
+    uint2 e[CS_ITEMS];  // key, position
+    uint32_t rk[CS_ITEMS];
     tc::grid_dep_wait();
+    tc::grid_dep_launch();
 #pragma unroll
     for (int i = 0; i < CS_ITEMS; ++i) {
         const int t = first + i * 32;
-        p[i] = uint32_t((rank << log_cap) + t);
-        key[i] = 0xFFFFFFFFu;
+        e[i] = make_uint2(0xFFFFFFFFu, uint32_t((rank << log_cap) + t));
         if (i < items && t < here) {
-            const int r = token_row(idx, int64_t(p[i]), rows, padding);
-            key[i] = r >= 0 ? uint32_t(r) : uint32_t(rows);
+            const int r = token_row(idx, int64_t(e[i].y), rows, padding);
+            e[i].x = r >= 0 ? uint32_t(r) : uint32_t(rows);
         }
     }
     for (int pass = 0; pass < passes; ++pass) {
         const int shift = pass * digit_bits;
+        const bool last = pass + 1 == passes;
         for (int i = threadIdx.x; i < CS_WARPS * bins / 2; i += CS_THREADS) reinterpret_cast<uint32_t*>(cnt)[i] = 0;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < CS_ITEMS; ++i) {
             if (i >= items) break;
             const bool in = first + i * 32 < here;
-            const uint32_t dg = in ? (key[i] >> shift) & uint32_t(bins - 1) : 0xFFFFFFFFu;
+            const uint32_t dg = in ? (e[i].x >> shift) & uint32_t(bins - 1) : 0xFFFFFFFFu;
             const uint32_t same = __match_any_sync(0xFFFFFFFFu, dg), below = same & ((1u << lane) - 1u);
             const uint32_t before = in ? cnt[w * bins + dg] : 0u;
             __syncwarp();
@@ -366,7 +388,7 @@ sort_cluster(int n, int rows, int padding, int S, int log_items, int passes, int
             __syncwarp();
         }
         __syncthreads();
-        // a digit's counts of the warps to first ranks in the block, and its total
+        // a digit's counts of the warps, and its total
         uint32_t total = 0;
         if (int(threadIdx.x) < bins) {
 #pragma unroll 8
@@ -397,30 +419,33 @@ sort_cluster(int n, int rows, int padding, int S, int log_items, int passes, int
                     }
             }
         }
-        // first place of each digit: the digits below it, then the blocks below this one
-        const uint32_t up = block_scan(int(threadIdx.x) < bins ? all : 0u, sm);
-        if (int(threadIdx.x) < bins) base[threadIdx.x] = up - all + before;
+        // first place of each digit: in all (the digits below it, then the blocks below this one),
+        // and in the block
+        const uint32_t up = block_scan(all, sm), here_up = block_scan(total, sm);
+        if (int(threadIdx.x) < bins) {
+            const uint32_t at = here_up - total;
+            base[threadIdx.x] = up - all + before - at;
+#pragma unroll 8
+            for (int k = 0; k < CS_WARPS; ++k) cnt[k * bins + threadIdx.x] += uint16_t(at);
+        }
         __syncthreads();
-        const bool last = pass + 1 == passes;
-        uint32_t* dk = kv + (pass & 1) * CS_TOKENS;
-        uint32_t* dp = kv + (2 + (pass & 1)) * CS_TOKENS;
 #pragma unroll
         for (int i = 0; i < CS_ITEMS; ++i)
-            if (i < items && first + i * 32 < here) {
-                const uint32_t dg = (key[i] >> shift) & uint32_t(bins - 1);
-                const uint32_t at = base[dg] + cnt[w * bins + dg] + rk[i];
-                if (last) {
-                    keys_out[at] = key[i];
-                    pos_out[at] = p[i];
-                } else if (S == 1) {
-                    dk[at] = key[i];
-                    dp[at] = p[i];
-                } else {
-                    const uint32_t r = at >> log_cap, slot = at & ((1u << log_cap) - 1u);
-                    st_dsmem(tc::dsmem_addr(tc::smem_u32(dk + slot), r), key[i]);
-                    st_dsmem(tc::dsmem_addr(tc::smem_u32(dp + slot), r), p[i]);
-                }
+            if (i < items && first + i * 32 < here)
+                stage[cnt[w * bins + ((e[i].x >> shift) & uint32_t(bins - 1))] + rk[i]] = e[i];
+        __syncthreads();
+        for (int s = threadIdx.x; s < here; s += CS_THREADS) {
+            const uint2 v = stage[s];
+            const uint32_t at = base[(v.x >> shift) & uint32_t(bins - 1)] + uint32_t(s);
+            if (last) {
+                keys_out[at] = v.x;
+                pos_out[at] = v.y;
+            } else if (S == 1) {
+                next[at] = v;
+            } else {
+                st_dsmem(tc::dsmem_addr(tc::smem_u32(next + (at & ((1u << log_cap) - 1u))), at >> log_cap), v);
             }
+        }
         if (last) break;
         if (S > 1) {
             __syncwarp();
@@ -430,10 +455,7 @@ sort_cluster(int n, int rows, int padding, int S, int log_items, int passes, int
         }
 #pragma unroll
         for (int i = 0; i < CS_ITEMS; ++i)
-            if (i < items && first + i * 32 < here) {
-                key[i] = dk[first + i * 32];
-                p[i] = dp[first + i * 32];
-            }
+            if (i < items && first + i * 32 < here) e[i] = next[first + i * 32];
     }
     if (S > 1) {  // no block leaves while another still reads its counts
         __syncwarp();
@@ -469,10 +491,9 @@ embed_table(int n, int rows, int padding, int D, int blocks, int units, const I*
     for (int r = 0; r <= rows; ++r) my[r * TAB_COLS] = 0.f;
     for (int i = lane; i < 2 * TAB_STEP * TAB_COLS; i += 32) Elem<T>::st(tile + i, 0.f);
     __syncwarp();
-    int next = 0;
-    auto load = [&](int t, T* dst) {  // the step at t: its values, and lane l's token's row (a table offset)
-        const int r = t + lane < t1 ? token_row(idx, int64_t(t) + lane, rows, padding) : -1;
-        next = (r >= 0 ? r : rows) * TAB_COLS;
+    I raw = 0;  // lane l's token of the next step, not looked at before that step
+    auto load = [&](int t, T* dst) {  // the step at t
+        raw = t + lane < t1 ? idx[t + lane] : I(-1);
         const T* src = dy + int64_t(t + tok0) * D + c0 + col;
         dst += tok0 * TAB_COLS + col;
         const int left = t1 - t - tok0;
@@ -489,7 +510,7 @@ embed_table(int n, int rows, int padding, int D, int blocks, int units, const I*
     if (t0 < t1) load(t0, tile);
     int buf = 0;
     for (int t = t0; t < t1; t += TAB_STEP, buf ^= 1) {
-        const int row = next;
+        const int row = (raw >= 0 && raw < rows && raw != padding ? int(raw) : rows) * TAB_COLS;
         if (t + TAB_STEP < t1) {
             load(t + TAB_STEP, tile + (buf ^ 1) * (TAB_STEP * TAB_COLS));
             asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -583,16 +604,17 @@ struct ChunkRuns {
 };
 
 template <typename T, int V>
-__global__ void __launch_bounds__(SUM_THREADS) embed_sum(int n, int rows, int D, int cols, int wins, int chunk,
+__global__ void __launch_bounds__(SUM_THREADS, SUM_BLOCKS_SM) embed_sum(int n, int rows, int D, int cols, int wins, int chunk,
                                                          int chunks, float scale, const uint32_t* keys,
                                                          const uint32_t* pos, const T* dy, T* dtable, float* part)
 {
-    constexpr int U = 8;
+    constexpr int U = 4;
     const int per = SUM_THREADS / cols, sub = int(threadIdx.x) / cols;
     const int win = int(blockIdx.x % wins);
     const int64_t ch = int64_t(blockIdx.x / wins) * per + sub;
     const int c = (win * cols + int(threadIdx.x) - sub * cols) * V;
     tc::grid_dep_wait();
+    tc::grid_dep_launch();
     if (sub >= per || ch >= chunks || c >= D) return;
     const int i0 = int(ch) * chunk, i1 = min(n, i0 + chunk);
     const ChunkRuns run(keys, n, chunk, i0, i1);
@@ -617,27 +639,36 @@ __global__ void __launch_bounds__(SUM_THREADS) embed_sum(int n, int rows, int D,
             v.store(dtable + int64_t(cur) * D + c);
         }
     };
-    uint32_t k[U], p[U];  // of the next tokens, a step ahead of their values
+    // Two steps ahead a token's name is read, one step ahead its value, and neither is looked at
+    // before its step.  Beyond the chunk only the run at its end counts.
+    uint32_t k[U], p[U], kn[U], kc[U];
+    Vec<T, V> v[U], vn[U];
     auto names = [&](int i) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            // beyond the chunk only the run at its end counts
             k[u] = i + u < run.end ? keys[i + u] : 0xFFFFFFFFu;
             p[u] = i + u < run.end ? pos[i + u] : 0u;
-            if (i + u >= i1 && k[u] != last) k[u] = 0xFFFFFFFFu;
+        }
+    };
+    auto values = [&](int i) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            kn[u] = i + u < i1 || k[u] == last ? k[u] : 0xFFFFFFFFu;
+            if (kn[u] < uint32_t(rows)) vn[u].load(dy + int64_t(p[u]) * D + c);
+            else vn[u].zero();
         }
     };
     names(i0);
+    values(i0);
+    names(i0 + U);
     for (int i = i0; i < run.end; i += U) {
-        uint32_t kc[U];
-        Vec<T, V> v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            kc[u] = k[u];
-            if (k[u] < uint32_t(rows)) v[u].load(dy + int64_t(p[u]) * D + c);
-            else v[u].zero();
+            kc[u] = kn[u];
+            v[u] = vn[u];
         }
-        if (i + U < run.end) names(i + U);
+        values(i + U);
+        names(i + 2 * U);
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (i + u < i1 || kc[u] == last) {
@@ -691,27 +722,38 @@ __global__ void __launch_bounds__(FIX_THREADS) embed_fix(int n, int rows, int D,
         if (wl == 0) reach[threadIdx.x >> 5] = cnt;
     }
     __syncthreads();
-    for (int k = 0; k < FIX_CHUNKS; ++k) {
-        const int cnt = reach[k], ch = ch0 + k;
-        if (cnt == 0) continue;
+    // the block's long runs side by side, as many as it has lanes, each with `per` lanes
+    int active = 0;
+    for (int k = 0; k < FIX_CHUNKS; ++k) active += reach[k] > 0;
+    if (active == 0) return;
+    const int per = max(1, min(32, lanes / active)), slots = lanes / per, slot = lane / per, sub = lane - slot * per;
+    for (int done = 0; done < active; done += slots) {
+        int k = -1;  // the chunk of this lane's run
+        if (slot < slots && done + slot < active) {
+            int left = done + slot;
+            while (reach[++k] == 0 || left-- > 0) {}
+        }
         float acc[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = 0.f;
-        if (lane < lanes && c < D)
+        const int ch = ch0 + k;
+        if (k >= 0 && c < D) {
+            const int cnt = reach[k];
 #pragma unroll 8
-            for (int j = lane; j <= cnt; j += lanes) {
+            for (int j = sub; j <= cnt; j += per) {
                 const float* s = part + (int64_t(ch + j) * 2 + (j == 0 ? 1 : 0)) * D + c;
 #pragma unroll
                 for (int i = 0; i < V; ++i) acc[i] += s[i];
             }
+        }
         if (lane < lanes)
 #pragma unroll
             for (int i = 0; i < V; ++i) sm[(lane * cols + col) * V + i] = acc[i];
         __syncthreads();
-        if (lane == 0 && c < D) {
-            for (int l = 1; l < lanes; ++l)
+        if (k >= 0 && sub == 0 && c < D) {
+            for (int l = 1; l < per; ++l)
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] += sm[(l * cols + col) * V + i];
+                for (int i = 0; i < V; ++i) acc[i] += sm[((lane + l) * cols + col) * V + i];
             Vec<T, V> v;
 #pragma unroll
             for (int i = 0; i < V; ++i) acc[i] *= scale;
