@@ -5,9 +5,9 @@
 //
 // The gradient is a sum per row over the tokens that name it, in one of two ways:
 //
-// A table of few rows: a warp keeps the sums of the whole table, a window of 32 columns, in its own
-// part of shared memory (a column a lane) and adds a contiguous share of the tokens to it, whose
-// values are copied ahead as they lie.  The copies are added up at the end.
+// A table of few rows: half a warp keeps the sums of the whole table, a window of 32 columns, in its
+// own part of shared memory (two columns a lane) and adds a contiguous share of the tokens to it,
+// whose values are copied ahead as they lie.  The copies are added up at the end.
 //
 // Else the tokens are sorted by row (least significant digit first, a stable counting sort a
 // digit), so a row's tokens are one run of the sorted order in ascending t: dy is read once, row
@@ -36,10 +36,10 @@ constexpr int FIX_CHUNKS = 16;                             // chunks a block of 
 constexpr int CS_THREADS = 1024, CS_ITEMS = 8;             // sort by one cluster: a block's threads, tokens a thread
 constexpr int CS_TOKENS = CS_THREADS * CS_ITEMS;
 constexpr int CS_WARPS = CS_THREADS / 32;
-constexpr int TAB_COLS = 32;                               // columns of a table window: a lane each
-constexpr int TAB_STEP = 32;                               // tokens a warp copies at a time
+constexpr int TAB_COLS = 32;                               // columns of a table window: two a lane of half a warp
+constexpr int TAB_STEP = 16, TAB_STAGES = 4;               // tokens copied at a time, copies under way and in use
 constexpr int TAB_SMEM = 225 * 1024;
-constexpr int TAB_MAX_UNITS = 16, TAB_MIN_UNITS = 5;       // warps with a table each, a block (and SM)
+constexpr int TAB_MAX_UNITS = 32, TAB_MIN_UNITS = 4;       // half warps with a table each, a block (and SM)
 
 struct EmbedPlan {
     bool table;           // sums of the whole table in shared memory
@@ -66,10 +66,12 @@ EmbedPlan embed_plan(const conv_embed_desc_t& e, const DevInfo& d)
         return at;
     };
     // Whole-table sums where the tokens outnumber by far the rows that every copy has to add up,
-    // and an SM holds enough copies (a copy takes a token in about 20 clocks).
-    const int unit = (e.V + 1) * TAB_COLS * 4 + 2 * TAB_STEP * TAB_COLS * (e.dtype == CONV_F32 ? 4 : 2);
+    // and an SM holds a few copies, whose reads ahead keep it busy.
+    const int unit = (e.V + 1) * TAB_COLS * 4 +
+                     TAB_STAGES * TAB_STEP * (TAB_COLS * (e.dtype == CONV_F32 ? 4 : 2) +
+                                              (e.index_dtype == CONV_INDEX_I32 ? 4 : 8));
     q.wins = ceil_div(e.D, TAB_COLS);
-    q.units = e.V < TAB_SMEM / (TAB_COLS * 4) ? std::min(TAB_MAX_UNITS, TAB_SMEM / unit) : 0;
+    q.units = e.V < TAB_SMEM / (TAB_COLS * 4) ? std::min(TAB_MAX_UNITS, TAB_SMEM / unit / 2 * 2) : 0;
     q.table = q.units >= TAB_MIN_UNITS && e.T >= int64_t(64) * e.V && e.T >= 8192;
     if (q.table) {
         q.smem = q.units * unit;
@@ -464,84 +466,92 @@ sort_cluster(int n, int rows, int padding, int S, int log_items, int passes, int
 }
 
 // ---- whole-table sums ------------------------------------------------------------------------
-// Block (range, window), warp u: its own table of rows + 1 rows (the last one takes the tokens that
-// name none) and two tiles of TAB_STEP tokens.  Four tokens at a time are added side by side where
-// their rows differ, else one after the other; either way a row's tokens are added in order.
+// Block (range, window), unit u (half a warp): its own table of rows + 1 rows (the last one takes
+// the tokens that name none) and a ring of TAB_STAGES tiles of TAB_STEP tokens.  Four tokens are
+// added at a time: their table rows are read together, and where a row comes again among the four
+// the sum so far takes the place of what was read.
 template <int BYTES> __device__ __forceinline__ void tab_copy(uint32_t dst, const void* src)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 
 template <typename T, typename I, int V>
-__global__ void __launch_bounds__(TAB_MAX_UNITS * 32, 1)
+__global__ void __launch_bounds__(TAB_MAX_UNITS * 16, 1)
 embed_table(int n, int rows, int padding, int D, int blocks, int units, const I* idx, const T* dy, float* part)
 {
-    constexpr int COPIES = TAB_COLS / V, AT_ONCE = 32 / COPIES;  // copies a token, tokens a copy of the warp
+    constexpr int COPIES = TAB_COLS / V, TILE = TAB_STEP * TAB_COLS;  // copies a token; values a tile
     extern __shared__ __align__(16) unsigned char dynt[];
-    const int lane = threadIdx.x & 31, u = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 15, u = threadIdx.x >> 4;
     float* tab = reinterpret_cast<float*>(dynt);            // units x (rows + 1) x TAB_COLS
     const int size = (rows + 1) * TAB_COLS;
-    float* my = tab + size_t(u) * size + lane;
-    T* tile = reinterpret_cast<T*>(tab + size_t(units) * size) + u * (2 * TAB_STEP * TAB_COLS);
+    float2* my = reinterpret_cast<float2*>(tab + size_t(u) * size) + lane;
+    T* tiles = reinterpret_cast<T*>(tab + size_t(units) * size);
+    T* tile = tiles + u * (TAB_STAGES * TILE);
+    I* names = reinterpret_cast<I*>(tiles + units * (TAB_STAGES * TILE)) + u * (TAB_STAGES * TAB_STEP);
     const int range = int(blockIdx.x) % blocks, c0 = int(blockIdx.x) / blocks * TAB_COLS;
+    const int width = min(TAB_COLS, D - c0);
     const int64_t parts = int64_t(blocks) * units, at = int64_t(range) * units + u;
     const int t0 = int(int64_t(n) * at / parts), t1 = int(int64_t(n) * (at + 1) / parts);
-    const int width = min(TAB_COLS, D - c0);
-    const int tok0 = lane / COPIES, col = lane % COPIES * V;  // this lane's part of a copy
-    for (int r = 0; r <= rows; ++r) my[r * TAB_COLS] = 0.f;
-    for (int i = lane; i < 2 * TAB_STEP * TAB_COLS; i += 32) Elem<T>::st(tile + i, 0.f);
+    // (both halves of a warp walk as many steps)
+    const int other = __shfl_xor_sync(0xFFFFFFFFu, t1 - t0, 16);
+    const int steps = (max(t1 - t0, other) + TAB_STEP - 1) / TAB_STEP;
+    for (int r = 0; r <= rows; ++r) my[r * (TAB_COLS / 2)] = make_float2(0.f, 0.f);
+    for (int i = lane; i < TAB_STAGES * TILE; i += 16) Elem<T>::st(tile + i, 0.f);
     __syncwarp();
-    I raw = 0;  // lane l's token of the next step, not looked at before that step
-    auto load = [&](int t, T* dst) {  // the step at t
-        raw = t + lane < t1 ? idx[t + lane] : I(-1);
-        const T* src = dy + int64_t(t + tok0) * D + c0 + col;
-        dst += tok0 * TAB_COLS + col;
-        const int left = t1 - t - tok0;
-        if (col < width)
+    // This lane's part of a step's copies: one in AT_ONCE tokens where a token is less than 16
+    // copies, else a sixteenth of every token.
+    constexpr int AT_ONCE = COPIES <= 16 ? 16 / COPIES : 1, EACH = COPIES <= 16 ? 1 : COPIES / 16;
+    const int tok0 = COPIES <= 16 ? lane / COPIES : 0, col0 = lane % (COPIES <= 16 ? COPIES : 16) * V;
+    const T* src0 = dy + int64_t(t0 + tok0) * D + c0 + col0;
+    auto load = [&](int step, int stage) {  // as far as there is such a step
+        const int left = t1 - t0 - step * TAB_STEP;
+        if (lane < left)
+            tab_copy<int(sizeof(I))>(tc::smem_u32(names + stage * TAB_STEP + lane), idx + t0 + step * TAB_STEP + lane);
+        const T* src = src0;
+        T* dst = tile + stage * TILE + tok0 * TAB_COLS + col0;
+        src0 += int64_t(TAB_STEP) * D;
 #pragma unroll
-            for (int i = 0; i < TAB_STEP; i += AT_ONCE, src += int64_t(AT_ONCE) * D, dst += AT_ONCE * TAB_COLS)
-                if (i < left) {
-                    if constexpr (sizeof(T) * V >= 4) tab_copy<int(sizeof(T)) * V>(tc::smem_u32(dst), src);
-                    else *dst = *src;
+        for (int i = 0; i < TAB_STEP; i += AT_ONCE, src += int64_t(AT_ONCE) * D, dst += AT_ONCE * TAB_COLS)
+#pragma unroll
+            for (int k = 0; k < EACH; ++k)
+                if (i + tok0 < left && col0 + 16 * k < width) {
+                    if constexpr (sizeof(T) * V >= 4) tab_copy<int(sizeof(T)) * V>(tc::smem_u32(dst + 16 * k), src + 16 * k);
+                    else dst[16 * k] = src[16 * k];
                 }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     tc::grid_dep_wait();
-    if (t0 < t1) load(t0, tile);
-    int buf = 0;
-    for (int t = t0; t < t1; t += TAB_STEP, buf ^= 1) {
-        const int row = (raw >= 0 && raw < rows && raw != padding ? int(raw) : rows) * TAB_COLS;
-        if (t + TAB_STEP < t1) {
-            load(t + TAB_STEP, tile + (buf ^ 1) * (TAB_STEP * TAB_COLS));
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-        } else {
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-        }
-        // bit 4g + j: token j of group g has the row of one before it in the group
-        bool again = false;
 #pragma unroll
-        for (int k = 1; k < 4; ++k) again |= __shfl_up_sync(0xFFFFFFFFu, row, k) == row && (lane & 3) >= k;
-        const uint32_t dup = __ballot_sync(0xFFFFFFFFu, again);  // (the tile's copies are visible to the warp after it)
-        const T* v = tile + buf * (TAB_STEP * TAB_COLS) + lane;
+    for (int k = 0; k + 1 < TAB_STAGES; ++k) load(k, k);
+    int stage = 0;
+    for (int k = 0; k < steps; ++k, stage = (stage + 1) % TAB_STAGES) {
+        load(k + TAB_STAGES - 1, (stage + TAB_STAGES - 1) % TAB_STAGES);
+        asm volatile("cp.async.wait_group %0;" ::"n"(TAB_STAGES - 1) : "memory");
+        __syncwarp();  // every lane's copies have arrived
+        const I name = t0 + k * TAB_STEP + lane < t1 ? names[stage * TAB_STEP + lane] : I(-1);
+        const int row = (name >= 0 && name < rows && name != padding ? int(name) : rows) * (TAB_COLS / 2);
+        const T* v = tile + stage * TILE + 2 * lane;
 #pragma unroll
-        for (int g = 0; g < TAB_STEP / 4; ++g) {
-            float* o[4];
-            float f[4];
+        for (int g = 0; g < TAB_STEP; g += 4) {
+            int r[4];
+            float2 f[4], s[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                o[j] = my + __shfl_sync(0xFFFFFFFFu, row, 4 * g + j);
-                f[j] = Elem<T>::ld(v + (4 * g + j) * TAB_COLS);
+                r[j] = __shfl_sync(0xFFFFFFFFu, row, g + j, 16);
+                Vec<T, 2> e;
+                e.load(v + (g + j) * TAB_COLS);
+                f[j] = make_float2(e.get(0), e.get(1));
+                s[j] = my[r[j]];
             }
-            if ((dup >> (4 * g) & 0xFu) == 0) {
-                float s[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[j] = *o[j];
+            for (int j = 0; j < 4; ++j) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) *o[j] = s[j] + f[j];
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) *o[j] += f[j];
+                for (int i = 0; i < j; ++i)
+                    if (r[i] == r[j]) s[j] = s[i];
+                s[j] = make_float2(s[j].x + f[j].x, s[j].y + f[j].y);
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) my[r[j]] = s[j];
         }
         __syncwarp();
     }
@@ -549,6 +559,7 @@ embed_table(int n, int rows, int padding, int D, int blocks, int units, const I*
     // the copies added in order
     for (int i = threadIdx.x; i < rows * TAB_COLS; i += blockDim.x) {
         float s = 0.f;
+#pragma unroll 4
         for (int k = 0; k < units; ++k) s += tab[size_t(k) * size + i];
         const int r = i / TAB_COLS, c = i % TAB_COLS;
         if (c < width) part[(int64_t(range) * rows + r) * D + c0 + c] = s;
@@ -841,7 +852,7 @@ cudaError_t table_v(const conv_embed_desc_t& e, const EmbedPlan& q, const I* idx
 {
     const cudaError_t r = ensure_smem<embed_table<T, I, V>>(q.smem);
     if (r != cudaSuccess) return r;
-    return launch_ex(embed_table<T, I, V>, dim3(unsigned(q.blocks) * unsigned(q.wins)), dim3(q.units * 32), q.smem, s,
+    return launch_ex(embed_table<T, I, V>, dim3(unsigned(q.blocks) * unsigned(q.wins)), dim3(q.units * 16), q.smem, s,
                      1, true, int(e.T), e.V, e.padding_idx, e.D, q.blocks, q.units, idx, dy, part);
 }
 
