@@ -274,39 +274,17 @@ cudaError_t run_gn_rows_bwd(const GnParams& p, const GnRows& q, int dt, const vo
                             const void* gamma, const void* beta, const float* mean, const float* rstd, void* dx,
                             float* part, void* ws, cudaStream_t s);
 
-// ---- groups that no cluster holds: pieces of rows --------------------------------------------
-// NHWC: a piece is a range of a sample's positions, all channels of a column window; NCHW: a
-// range of one channel's positions.  `pieces` a sample (a channel), `len` positions each.
+// ---- NCHW groups that no cluster holds: pieces of rows (one channel's positions) -------------
 struct GnPieces {
     int V;
-    int pieces, len;
-    int cols, wins;      // NHWC: column vectors a window, windows
-    int row_lanes;       // NCHW: threads a row (channel): the whole block, or a warp for short rows
+    int pieces, len;     // pieces a row, positions each
+    int row_lanes;       // threads a row: the whole block, or a warp for short rows
     int threads;
     int64_t blocks;      // grid of the passes over x
 };
 GnPieces gn_pieces(const GnParams& p, int dt, const DevInfo& d);
 
-// The NHWC passes' block: window fastest, then piece, then sample.
-struct GnTile {
-    int b, pc, cv0, cols, lanes, col, lane, r0, r1;
-    __device__ __forceinline__ GnTile(const GnParams& p, const GnPieces& q, int V, int64_t at)
-    {
-        const int per = q.pieces * q.wins;
-        b = int(at / per);
-        const int rest = int(at - int64_t(b) * per);
-        pc = rest / q.wins;
-        cv0 = (rest - pc * q.wins) * q.cols;
-        cols = min(q.cols, p.C / V - cv0);
-        lanes = max(1, int(blockDim.x) / q.cols);
-        lane = int(threadIdx.x) / q.cols;
-        col = int(threadIdx.x) - lane * q.cols;
-        r0 = pc * q.len;
-        r1 = min(p.P, r0 + q.len);
-    }
-    __device__ __forceinline__ bool in() const { return lane < lanes && col < cols; }
-};
-// The NCHW passes' rows: `sub` is the row within the block, `lane` the thread within the row.
+// A block's rows: `sub` is the row within the block, `lane` the thread within the row.
 struct GnRow {
     int64_t row;  // sample * C + channel
     int pc, lane, e0, e1, hop;

@@ -87,7 +87,7 @@ gn_team_bwd(const GnParams p, const GnTeam q, const T* x, const T* dy, const T* 
             table_pairs<V, K>(bet, toff, be);
             with_act(p.act, [&](auto act) {
 #pragma unroll
-                for (int h = 0; h < H; ++h) dg[h] = gn_dz<act.value>(dg[h], add2(mul2(xh[h], ga[h]), be[h]));
+                for (int h = 0; h < H; ++h) dg[h] = gn_grad<act.value>(dg[h], xh[h], ga[h], be[h]);
             });
         }
         // a lane's vectors beyond the group have zeros for dy and add nothing
@@ -197,74 +197,7 @@ __global__ void __launch_bounds__(1024) gn_chan_sum(int C, int64_t n, int S, int
 
 // ---- large groups ----------------------------------------------------------------------------
 template <typename T, int V>
-__global__ void __launch_bounds__(256) gn_sums_nhwc(const GnParams p, const GnPieces q, const T* x, const T* dy,
-                                                    const T* gamma, const T* beta, const float* mean,
-                                                    const float* rstd, float* psg, float* psb)
-{
-    constexpr int U = 2;
-    __shared__ float sm_g[256 * V], sm_b[256 * V];
-    const GnTile t(p, q, V, blockIdx.x);
-    const int lanes = t.lanes;
-    tc::grid_dep_wait();
-    if (t.in()) {
-        float mu[V], rs[V], ga[V], be[V], sg[V], sb[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = (t.cv0 + t.col) * V + i;
-            const int64_t o = int64_t(t.b) * p.G + c / p.Cg;
-            mu[i] = mean[o];
-            rs[i] = rstd[o];
-            ga[i] = gamma ? Elem<T>::ldg(gamma + c) : 1.f;
-            be[i] = beta ? Elem<T>::ldg(beta + c) : 0.f;
-            sg[i] = sb[i] = 0.f;
-        }
-        const int64_t base = int64_t(t.b) * p.N + int64_t(t.cv0 + t.col) * V;
-        with_act(p.act, [&](auto act) {
-            for (int r = t.r0 + t.lane; r < t.r1; r += lanes * U) {
-                Vec<T, V> vx[U], vd[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (r + u * lanes < t.r1) {
-                        vx[u].load(x + base + int64_t(r + u * lanes) * p.C);
-                        vd[u].load(dy + base + int64_t(r + u * lanes) * p.C);
-                    } else {
-                        vx[u].zero();
-                        vd[u].zero();
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (r + u * lanes < t.r1)
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            const float xh = gn_xhat(vx[u].get(i), mu[i], rs[i]);
-                            const float dz = gn_dz<act.value>(vd[u].get(i), gn_z(xh, ga[i], be[i]));
-                            sb[i] += dz;
-                            sg[i] += dz * xh;
-                        }
-            }
-        });
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            sm_g[(t.lane * q.cols + t.col) * V + i] = sg[i];
-            sm_b[(t.lane * q.cols + t.col) * V + i] = sb[i];
-        }
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < t.cols * V; c += blockDim.x) {
-        float a = 0.f, b = 0.f;
-        for (int l = 0; l < lanes; ++l) {
-            a += sm_g[l * q.cols * V + c];
-            b += sm_b[l * q.cols * V + c];
-        }
-        const int64_t o = gn_part(p, q.pieces, t.b, t.cv0 * V + c, t.pc);
-        psg[o] = a;
-        psb[o] = b;
-    }
-}
-
-template <typename T, int V>
-__global__ void __launch_bounds__(256) gn_sums_nchw(const GnParams p, const GnPieces q, const T* x, const T* dy,
+__global__ void __launch_bounds__(256) gn_sums(const GnParams p, const GnPieces q, const T* x, const T* dy,
                                                     const T* gamma, const T* beta, const float* mean,
                                                     const float* rstd, float* psg, float* psb)
 {
@@ -349,56 +282,7 @@ __global__ void __launch_bounds__(128) gn_group_sums(const GnParams p, const GnP
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(256) gn_dx_nhwc(const GnParams p, const GnPieces q, const T* x, const T* dy,
-                                                  const T* gamma, const T* beta, const float* mean, const float* rstd,
-                                                  const float* m1, const float* m2, T* dx)
-{
-    constexpr int U = 2;
-    const GnTile t(p, q, V, q.blocks - 1 - blockIdx.x);
-    const int lanes = t.lanes;
-    tc::grid_dep_wait();
-    if (!t.in()) return;
-    float mu[V], rs[V], ga[V], be[V], a1[V], a2[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int c = (t.cv0 + t.col) * V + i;
-        const int64_t o = int64_t(t.b) * p.G + c / p.Cg;
-        mu[i] = mean[o];
-        rs[i] = rstd[o];
-        a1[i] = m1[o];
-        a2[i] = m2[o];
-        ga[i] = gamma ? Elem<T>::ldg(gamma + c) : 1.f;
-        be[i] = beta ? Elem<T>::ldg(beta + c) : 0.f;
-    }
-    const int64_t base = int64_t(t.b) * p.N + int64_t(t.cv0 + t.col) * V;
-    with_act(p.act, [&](auto act) {
-        for (int r = t.r0 + t.lane; r < t.r1; r += lanes * U) {
-            Vec<T, V> vx[U], vd[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (r + u * lanes < t.r1) {
-                    vx[u].load(x + base + int64_t(r + u * lanes) * p.C);
-                    vd[u].load(dy + base + int64_t(r + u * lanes) * p.C);
-                }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (r + u * lanes < t.r1) {
-                    float o[V];
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float xh = gn_xhat(vx[u].get(i), mu[i], rs[i]);
-                        const float dz = gn_dz<act.value>(vd[u].get(i), gn_z(xh, ga[i], be[i]));
-                        o[i] = rs[i] * (dz * ga[i] - a1[i] - xh * a2[i]);
-                    }
-                    vx[u].set(o);
-                    vx[u].store(dx + base + int64_t(r + u * lanes) * p.C);
-                }
-        }
-    });
-}
-
-template <typename T, int V>
-__global__ void __launch_bounds__(256) gn_dx_nchw(const GnParams p, const GnPieces q, const T* x, const T* dy,
+__global__ void __launch_bounds__(256) gn_dx(const GnParams p, const GnPieces q, const T* x, const T* dy,
                                                   const T* gamma, const T* beta, const float* mean, const float* rstd,
                                                   const float* m1, const float* m2, T* dx)
 {
@@ -491,13 +375,10 @@ cudaError_t bwd_t(const GnParams& p, int dt, const DevInfo& d, const T* x, const
     float* psb = psg + np;
     float* m1 = psb + np;
     float* m2 = m1 + int64_t(p.B) * p.G;
-    const bool nhwc = p.layout == CONV_LAYOUT_NHWC;
     const dim3 grid(static_cast<unsigned>(q.blocks));
-#define GN_CALL(T_, V_)                                                                                            \
-    e = nhwc ? launch_ex(gn_sums_nhwc<T_, V_>, grid, dim3(q.threads), 0, s, 1, true, p, q, x, dy, gamma, beta,     \
-                         mean, rstd, psg, psb)                                                                     \
-             : launch_ex(gn_sums_nchw<T_, V_>, grid, dim3(q.threads), 0, s, 1, true, p, q, x, dy, gamma, beta,     \
-                         mean, rstd, psg, psb)
+#define GN_CALL(T_, V_)                                                                                       \
+    e = launch_ex(gn_sums<T_, V_>, grid, dim3(q.threads), 0, s, 1, true, p, q, x, dy, gamma, beta, mean, rstd, \
+                  psg, psb)
     GN_DISPATCH_V(T, q.V, GN_CALL);
 #undef GN_CALL
     if (e != cudaSuccess) return e;
@@ -509,11 +390,9 @@ cudaError_t bwd_t(const GnParams& p, int dt, const DevInfo& d, const T* x, const
         e = chan_sum<T>(p, int64_t(p.B) * q.pieces, p.C, np, psg, dgamma, dbeta, s);
         if (e != cudaSuccess) return e;
     }
-#define GN_CALL(T_, V_)                                                                                               \
-    e = nhwc ? launch_ex(gn_dx_nhwc<T_, V_>, grid, dim3(q.threads), 0, s, 1, true, p, q, x, dy, gamma, beta, mean,    \
-                         rstd, c1, c2, dx)                                                                            \
-             : launch_ex(gn_dx_nchw<T_, V_>, grid, dim3(q.threads), 0, s, 1, true, p, q, x, dy, gamma, beta, mean,    \
-                         rstd, c1, c2, dx)
+#define GN_CALL(T_, V_)                                                                                       \
+    e = launch_ex(gn_dx<T_, V_>, grid, dim3(q.threads), 0, s, 1, true, p, q, x, dy, gamma, beta, mean, rstd,  \
+                  c1, c2, dx)
     GN_DISPATCH_V(T, q.V, GN_CALL);
 #undef GN_CALL
     return e != cudaSuccess ? e : cudaGetLastError();

@@ -455,7 +455,7 @@ gn_cluster_fwd_nhwc(const GnParams p, const __grid_constant__ GnCluster q, const
                                                                           2 * h + 1 < t.split ? -s0.x : -s1.x);
                         const float2 rs = ONE ? both(s0.y) : make_float2(2 * h < t.split ? s0.y : s1.y,
                                                                          2 * h + 1 < t.split ? s0.y : s1.y);
-                        f[h] = act_value<act.value>(add2(mul2(mul2(add2(f[h], mu), rs), ga[h]), be[h]));
+                        f[h] = gn_out<act.value>(add2(f[h], mu), rs, act.value == CONV_ACT_RELU ? ga[h] : mul2(ga[h], rs), be[h]);
                     }
                     gc_store<T, V>(py, f);
                 }
@@ -543,7 +543,7 @@ gn_cluster_bwd_nhwc(const GnParams p, const __grid_constant__ GnCluster q, const
 #pragma unroll
                     for (int h = 0; h < H; ++h) {
                         xh[h] = mul2(add2(xh[h], mu(h)), rs(h));
-                        dz[h] = gn_dz<act.value>(dz[h], add2(mul2(xh[h], ga[h]), be[h]));
+                        dz[h] = gn_grad<act.value>(dz[h], xh[h], ga[h], be[h]);
                         if constexpr (ONE) {
                             sb[h] = add2(sb[h], dz[h]);
                             sg[h] = fma2(dz[h], xh[h], sg[h]);
@@ -625,7 +625,7 @@ gn_cluster_bwd_nhwc(const GnParams p, const __grid_constant__ GnCluster q, const
 #pragma unroll
                     for (int h = 0; h < H; ++h) {
                         xh[h] = mul2(add2(xh[h], mu(h)), rs(h));
-                        if constexpr (sizeof(T) == 2) dz[h] = gn_dz<act.value>(dz[h], add2(mul2(xh[h], ga[h]), be[h]));
+                        if constexpr (sizeof(T) == 2) dz[h] = gn_grad<act.value>(dz[h], xh[h], ga[h], be[h]);
                         const bool f0 = ONE || 2 * h < t.split, f1 = ONE || 2 * h + 1 < t.split;
                         const float2 m2 = make_float2(f0 ? -s0.x : -s1.x, f1 ? -s0.x : -s1.x);
                         const float2 m1 = make_float2(f0 ? -s0.y : -s1.y, f1 ? -s0.y : -s1.y);
@@ -823,8 +823,8 @@ gn_cluster_fwd_nchw(const GnParams p, const __grid_constant__ GnCluster q, const
                 with_channels<V>(ch, gb, [&](const auto& ga, const auto& be) {
 #pragma unroll
                     for (int h = 0; h < H; ++h)
-                        f[h] = act_value<act.value>(
-                            add2(mul2(mul2(add2(f[h], both(-stat.x)), both(stat.y)), ga[h]), be[h]));
+                        f[h] = gn_out<act.value>(add2(f[h], both(-stat.x)), both(stat.y),
+                                                 act.value == CONV_ACT_RELU ? ga[h] : mul2(ga[h], both(stat.y)), be[h]);
                 });
                 gc_store<T, V>(py, f);
             }
@@ -897,7 +897,7 @@ gn_cluster_bwd_nchw(const GnParams p, const __grid_constant__ GnCluster q, const
 #pragma unroll
                     for (int h = 0; h < H; ++h) {
                         xh[h] = mul2(add2(xh[h], both(mu)), both(rs));
-                        dz[h] = gn_dz<act.value>(dz[h], add2(mul2(xh[h], ga[h]), be[h]));
+                        dz[h] = gn_grad<act.value>(dz[h], xh[h], ga[h], be[h]);
                         xh[h] = mul2(dz[h], xh[h]);
                         g = add2(g, xh[h]);
                         d = add2(d, dz[h]);
@@ -948,7 +948,7 @@ gn_cluster_bwd_nchw(const GnParams p, const __grid_constant__ GnCluster q, const
 #pragma unroll
                     for (int h = 0; h < H; ++h) {
                         xh[h] = mul2(add2(xh[h], both(mu)), both(rs));
-                        if constexpr (sizeof(T) == 2) dz[h] = gn_dz<act.value>(dz[h], add2(mul2(xh[h], ga[h]), be[h]));
+                        if constexpr (sizeof(T) == 2) dz[h] = gn_grad<act.value>(dz[h], xh[h], ga[h], be[h]);
                         xh[h] = mul2(both(rs), fma2(xh[h], m2, fma2(dz[h], ga[h], m1)));
                     }
                 });

@@ -59,33 +59,19 @@ GnPieces gn_pieces(const GnParams& p, int dt, const DevInfo& d)
     const int es = dt == DT_F32 ? 4 : 2;
     q.threads = 256;
     int v = 16 / es;
-    const int n = p.layout == CONV_LAYOUT_NHWC ? p.C : p.P;
-    while (v > 1 && n % v != 0) v /= 2;
+    while (v > 1 && p.P % v != 0) v /= 2;
     q.V = v;
-    const int U = 4;  // rows (vectors) a thread merges at a time
-    if (p.layout == CONV_LAYOUT_NHWC) {
-        const int ncv = p.C / v;
-        q.wins = ceil_div(ncv, q.threads);
-        q.cols = ceil_div(ncv, q.wins);
-        q.wins = ceil_div(ncv, q.cols);
-        const int lanes = std::max(1, q.threads / q.cols);
-        // four passes of U rows a lane while that leaves enough pieces for the SMs
-        int len = lanes * U * 4;
-        while (len > lanes * U && int64_t(p.B) * q.wins * ceil_div(p.P, len) < 4 * d.sms) len /= 2;
-        q.len = std::min(len, p.P);
-    } else {
-        q.wins = q.cols = 1;
-        int len = q.threads * U * v * 2;
-        while (len > q.threads * v && int64_t(p.B) * p.C * ceil_div(p.P, len) < 4 * d.sms) len /= 2;
-        q.len = std::min(len, p.P);
-        // rows of at most U vectors a lane of a warp: a warp each, eight rows a block
-        q.row_lanes = p.P <= 32 * U * v ? 32 : q.threads;
-        if (q.row_lanes == 32) q.len = p.P;
-    }
+    const int U = 4;  // vectors a thread merges at a time
+    // two merges a thread while that leaves enough pieces for the SMs
+    int len = q.threads * U * v * 2;
+    while (len > q.threads * v && int64_t(p.B) * p.C * ceil_div(p.P, len) < 4 * d.sms) len /= 2;
+    q.len = std::min(len, p.P);
+    // rows of at most U vectors a lane of a warp: a warp each, eight rows a block
+    q.row_lanes = p.P <= 32 * U * v ? 32 : q.threads;
+    if (q.row_lanes == 32) q.len = p.P;
     q.pieces = ceil_div(p.P, q.len);
-    q.blocks = p.layout == CONV_LAYOUT_NHWC
-                   ? int64_t(p.B) * q.pieces * q.wins
-                   : (int64_t(p.B) * p.C * q.pieces + q.threads / q.row_lanes - 1) / (q.threads / q.row_lanes);
+    const int rows = q.threads / q.row_lanes;
+    q.blocks = (int64_t(p.B) * p.C * q.pieces + rows - 1) / rows;
     return q;
 }
 
@@ -187,71 +173,9 @@ __device__ __forceinline__ void chan_merge(float& n, float& mean, float& m2, flo
     n = t;
 }
 
-// NHWC: block (piece, sample, window); thread (row lane, column vector).  Each thread merges U
-// rows at a time into its V columns' statistics, the row lanes are merged in ascending order.
+// A block (or a warp) a row's piece.
 template <typename T, int V>
-__global__ void __launch_bounds__(256) gn_stats_nhwc(const GnParams p, const GnPieces q, const T* x, float* pmean,
-                                                     float* pm2)
-{
-    constexpr int U = 4;
-    __shared__ float sm_mean[256 * V], sm_m2[256 * V];
-    const GnTile t(p, q, V, blockIdx.x);
-    const int lanes = t.lanes, r0 = t.r0, r1 = t.r1;
-    float mean[V], m2[V], n = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) mean[i] = m2[i] = 0.f;
-    tc::grid_dep_wait();
-    if (t.in()) {
-        const T* px = x + int64_t(t.b) * p.N + int64_t(t.cv0 + t.col) * V;
-        for (int r = r0 + t.lane; r < r1; r += lanes * U) {
-            Vec<T, V> v[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (r + u * lanes < r1) v[u].load(px + int64_t(r + u * lanes) * p.C);
-                else v[u].zero();
-            }
-            const int cnt = min(U, (r1 - r + lanes - 1) / lanes);
-            const float fc = float(cnt);
-            const float tot = n + fc, w = __fdividef(fc, tot), nw = n * w;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float s = 0.f, sq = 0.f;
-#pragma unroll
-                for (int u = 0; u < U; ++u) s += v[u].get(i);
-                const float mu = cnt == U ? s * (1.f / U) : __fdiv_rn(s, fc);
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const float dlt = u < cnt ? v[u].get(i) - mu : 0.f;
-                    sq += dlt * dlt;
-                }
-                const float dm = mu - mean[i];
-                mean[i] += dm * w;
-                m2[i] += sq + dm * dm * nw;
-            }
-            n = tot;
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            sm_mean[(t.lane * q.cols + t.col) * V + i] = mean[i];
-            sm_m2[(t.lane * q.cols + t.col) * V + i] = m2[i];
-        }
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < t.cols * V; c += blockDim.x) {
-        float an = 0.f, am = 0.f, aq = 0.f;
-        for (int l = 0; l < lanes; ++l) {
-            const int cnt = r1 - r0 > l ? (r1 - r0 - l + lanes - 1) / lanes : 0;
-            chan_merge(an, am, aq, float(cnt), sm_mean[l * q.cols * V + c], sm_m2[l * q.cols * V + c]);
-        }
-        const int64_t o = gn_part(p, q.pieces, t.b, t.cv0 * V + c, t.pc);
-        pmean[o] = am;
-        pm2[o] = aq;
-    }
-}
-
-// NCHW: a block (or a warp) a row's piece.
-template <typename T, int V>
-__global__ void __launch_bounds__(256) gn_stats_nchw(const GnParams p, const GnPieces q, const T* x, float* pmean,
+__global__ void __launch_bounds__(256) gn_stats(const GnParams p, const GnPieces q, const T* x, float* pmean,
                                                      float* pm2)
 {
     constexpr int U = 4;
@@ -348,47 +272,7 @@ __global__ void __launch_bounds__(128) gn_combine(const GnParams p, const GnPiec
 
 // The second pass walks the pieces backwards: the first pass's last pieces are still in L2.
 template <typename T, int V>
-__global__ void __launch_bounds__(256) gn_apply_nhwc(const GnParams p, const GnPieces q, const T* x, const T* gamma,
-                                                     const T* beta, T* y, const float* mean, const float* rstd)
-{
-    constexpr int U = 4;
-    const GnTile t(p, q, V, q.blocks - 1 - blockIdx.x);
-    const int lanes = t.lanes, r1 = t.r1;
-    float mu[V], rs[V], ga[V], be[V];
-    tc::grid_dep_wait();
-    if (!t.in()) return;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int c = (t.cv0 + t.col) * V + i;
-        const int64_t o = int64_t(t.b) * p.G + c / p.Cg;
-        mu[i] = mean[o];
-        rs[i] = rstd[o];
-        ga[i] = gamma ? Elem<T>::ldg(gamma + c) : 1.f;
-        be[i] = beta ? Elem<T>::ldg(beta + c) : 0.f;
-    }
-    const int64_t base = int64_t(t.b) * p.N + int64_t(t.cv0 + t.col) * V;
-    with_act(p.act, [&](auto act) {
-        for (int r = t.r0 + t.lane; r < r1; r += lanes * U) {
-            Vec<T, V> v[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (r + u * lanes < r1) v[u].load(x + base + int64_t(r + u * lanes) * p.C);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (r + u * lanes < r1) {
-                    float o[V];
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        o[i] = act_value<act.value>(gn_z(gn_xhat(v[u].get(i), mu[i], rs[i]), ga[i], be[i]));
-                    v[u].set(o);
-                    v[u].store(y + base + int64_t(r + u * lanes) * p.C);
-                }
-        }
-    });
-}
-
-template <typename T, int V>
-__global__ void __launch_bounds__(256) gn_apply_nchw(const GnParams p, const GnPieces q, const T* x, const T* gamma,
+__global__ void __launch_bounds__(256) gn_apply(const GnParams p, const GnPieces q, const T* x, const T* gamma,
                                                      const T* beta, T* y, const float* mean, const float* rstd)
 {
     constexpr int U = 4;
@@ -445,22 +329,17 @@ cudaError_t fwd_t(const GnParams& p, int dt, const DevInfo& d, const T* x, const
     float* pm2 = pmean + np;
     float* mu = pm2 + np;
     float* rs = mu + int64_t(p.B) * p.G;
-    const bool nhwc = p.layout == CONV_LAYOUT_NHWC;
     const dim3 grid(static_cast<unsigned>(q.blocks));
-#define GN_CALL(T_, V_)                                                                                               \
-    e = nhwc ? launch_ex(gn_stats_nhwc<T_, V_>, grid, dim3(q.threads), 0, s, 1, true, p, q, x, pmean, pm2)            \
-             : launch_ex(gn_stats_nchw<T_, V_>, grid, dim3(q.threads), 0, s, 1, true, p, q, x, pmean, pm2)
+#define GN_CALL(T_, V_) e = launch_ex(gn_stats<T_, V_>, grid, dim3(q.threads), 0, s, 1, true, p, q, x, pmean, pm2)
     GN_DISPATCH_V(T, q.V, GN_CALL);
 #undef GN_CALL
     if (e != cudaSuccess) return e;
     e = launch_ex(gn_combine, dim3(unsigned(p.B) * unsigned(p.G)), dim3(128), 0, s, 1, true, p, q,
                   static_cast<const float*>(pmean), static_cast<const float*>(pm2), mu, rs, mean, rstd);
     if (e != cudaSuccess) return e;
-#define GN_CALL(T_, V_)                                                                                               \
-    e = nhwc ? launch_ex(gn_apply_nhwc<T_, V_>, grid, dim3(q.threads), 0, s, 1, true, p, q, x, gamma, beta, y,        \
-                         static_cast<const float*>(mu), static_cast<const float*>(rs))                                \
-             : launch_ex(gn_apply_nchw<T_, V_>, grid, dim3(q.threads), 0, s, 1, true, p, q, x, gamma, beta, y,        \
-                         static_cast<const float*>(mu), static_cast<const float*>(rs))
+#define GN_CALL(T_, V_)                                                                                      \
+    e = launch_ex(gn_apply<T_, V_>, grid, dim3(q.threads), 0, s, 1, true, p, q, x, gamma, beta, y,           \
+                  static_cast<const float*>(mu), static_cast<const float*>(rs))
     GN_DISPATCH_V(T, q.V, GN_CALL);
 #undef GN_CALL
     return e != cudaSuccess ? e : cudaGetLastError();
