@@ -112,6 +112,14 @@ template <int ACT> __device__ __forceinline__ float2 gn_grad(float2 dy, float2 x
     return gn_dz<ACT>(dy, fma2(xhat, gamma, beta));
 }
 
+// dz from d = x - mean like gn_out.
+template <int ACT>
+__device__ __forceinline__ float2 gn_dz_at(float2 dy, float2 d, float2 rstd, float2 gamma_or_scale, float2 beta)
+{
+    if constexpr (ACT == CONV_ACT_RELU) return gn_dz<ACT>(dy, add2(mul2(mul2(d, rstd), gamma_or_scale), beta));
+    return gn_dz<ACT>(dy, fma2(d, gamma_or_scale, beta));
+}
+
 // Calls f(integral_constant<ACT>) for the runtime activation.
 template <class F> __device__ __forceinline__ void with_act(int act, F&& f)
 {
@@ -238,7 +246,7 @@ __device__ __forceinline__ float block_total(float v, float* sm, int& turn)
 // ---- large groups kept on chip by a cluster (kernels_gn_cluster.cu) --------------------------
 struct GnCluster {
     int V, S, log_s, threads, K; // vector width, blocks a cluster (and its log2), threads, slots a thread
-    int bufs, chunks;            // tiles a block holds; clusters that share a unit's samples
+    int chunks;                  // clusters that share a unit's samples
     int W, cols, lanes, groups;  // NHWC: channels, vectors and groups of a window, rows side by side
     int wins;                    // units a sample
     int vecs;                    // NCHW: vectors of a unit

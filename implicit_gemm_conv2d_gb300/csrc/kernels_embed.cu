@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_count(int n, int rows, int 
     for (int i = threadIdx.x; i < bins; i += SORT_THREADS) hist[i] = 0;
     __syncthreads();
     tc::grid_dep_wait();
+    tc::grid_dep_launch();
     const int base = int(blockIdx.x) * SORT_TILE;
 #pragma unroll
     for (int i = 0; i < SORT_ITEMS; ++i) {
@@ -219,6 +220,7 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_scan(int tiles, uint32_t* c
     uint32_t carry = 0;
     __shared__ uint32_t last;
     tc::grid_dep_wait();
+    tc::grid_dep_launch();
     for (int i0 = 0; i0 < tiles; i0 += SORT_THREADS) {
         const int i = i0 + int(threadIdx.x);
         const uint32_t v = i < tiles ? row[i] : 0u;
@@ -252,6 +254,7 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_scatter(int n, int rows, in
     for (int i = threadIdx.x; i < WARPS * SORT_MAX_BINS / 2; i += SORT_THREADS)
         reinterpret_cast<uint32_t*>(&cnt[0][0])[i] = 0;
     tc::grid_dep_wait();
+    tc::grid_dep_launch();
     const int t0 = int(blockIdx.x) * SORT_TILE + w * (32 * SORT_ITEMS) + lane;
     const int here = min(SORT_TILE, n - int(blockIdx.x) * SORT_TILE);
     uint32_t key[SORT_ITEMS], p[SORT_ITEMS], rank[SORT_ITEMS];

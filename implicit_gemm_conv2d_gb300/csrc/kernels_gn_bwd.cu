@@ -63,6 +63,7 @@ gn_team_bwd(const GnParams p, const GnTeam q, const T* x, const T* dy, const T* 
         }
     };
     tc::grid_dep_wait();
+    if (part) tc::grid_dep_launch();
     fetch(b);
     gn_team_tables(p, q, g0, gamma, beta, tab, tab + q.gpc * m);
     __syncthreads();
@@ -159,12 +160,12 @@ gn_team_bwd(const GnParams p, const GnTeam q, const T* x, const T* dy, const T* 
 // dgamma (blockIdx.y = 0) and dbeta (1): the sums of each channel's `n` partials
 // part[i * stride + kind * kind_stride + c].  Block: 32 channels by 32 lanes; the S blocks of a
 // cluster take contiguous ranges of the partials, each lane its own in ascending order, then the
-// lanes and the blocks are added in ascending order.
+// lanes and the blocks are added by fixed butterflies.
 template <typename T>
 __global__ void __launch_bounds__(1024) gn_chan_sum(int C, int64_t n, int S, int64_t stride, int64_t kind_stride,
                                                     const float* part, T* dgamma, T* dbeta)
 {
-    __shared__ float sm[32][33];
+    __shared__ float sm[32][33], total[32];
     const int rank = S > 1 ? int(tc::cluster_rank()) : 0;
     const int c = int(blockIdx.x) / S * 32 + int(threadIdx.x & 31), l = int(threadIdx.x >> 5);
     const int64_t i1 = n * (rank + 1) / S;
@@ -177,22 +178,21 @@ __global__ void __launch_bounds__(1024) gn_chan_sum(int C, int64_t n, int S, int
     }
     sm[l][threadIdx.x & 31] = t;
     __syncthreads();
-    if (l == 0) {
-        t = 0.f;
-        for (int i = 0; i < 32; ++i) t += sm[i][threadIdx.x];
-        sm[0][threadIdx.x] = t;
-    }
+    // warp l adds channel l's lanes
+    t = warp_sum(sm[threadIdx.x & 31][l]);
+    const int out = int(blockIdx.x) / S * 32 + l;
     if (S > 1) {
+        if ((threadIdx.x & 31) == 0) total[l] = t;
         __syncthreads();
         tc::cluster_sync();
-        if (l == 0 && rank == 0) {
-            t = 0.f;
-            for (int r = 0; r < S; ++r) t += tc::ld_dsmem_f32(tc::dsmem_addr(tc::smem_u32(&sm[0][threadIdx.x]), r));
+        if (rank == 0) {
+            t = int(threadIdx.x & 31) < S ? tc::ld_dsmem_f32(tc::dsmem_addr(tc::smem_u32(total + l), threadIdx.x & 31)) : 0.f;
+            t = warp_sum(t);
         }
         __syncwarp();
         tc::cluster_sync();
     }
-    if (l == 0 && rank == 0 && c < C) Elem<T>::st((blockIdx.y ? dbeta : dgamma) + c, t);
+    if ((threadIdx.x & 31) == 0 && rank == 0 && out < C) Elem<T>::st((blockIdx.y ? dbeta : dgamma) + out, t);
 }
 
 // ---- large groups ----------------------------------------------------------------------------
@@ -205,6 +205,7 @@ __global__ void __launch_bounds__(256) gn_sums(const GnParams p, const GnPieces 
     __shared__ float sm[8][2];
     const GnRow t(p, q, V, blockIdx.x);
     tc::grid_dep_wait();
+    tc::grid_dep_launch();
     float sg = 0.f, sb = 0.f;
     if (t.in) {
         const int c = int(t.row % p.C);
@@ -265,6 +266,7 @@ __global__ void __launch_bounds__(128) gn_group_sums(const GnParams p, const GnP
     const int b = int(blockIdx.x / p.G), g = int(blockIdx.x % p.G);
     const int np = p.Cg * q.pieces;
     tc::grid_dep_wait();
+    tc::grid_dep_launch();
     float s1 = 0.f, s2 = 0.f;
     for (int i = threadIdx.x; i < np; i += blockDim.x) {
         const int pc = i / p.Cg, c = g * p.Cg + i - pc * p.Cg;

@@ -22,6 +22,7 @@ namespace {
 constexpr int GC_MAX_CG = 2048;            // channels of a group (their gammas sit in shared memory)
 constexpr int GC_SMEM = 110 * 1024;        // of a block: two share an SM, or each waits with its SM
 constexpr int GC_THREADS = 512;
+constexpr int GC_ROW_THREADS = 384;
 constexpr int GC_SPAN_THREADS = 256;       // NHWC, vectors in two groups: more registers a thread
 constexpr int GC_WARPS = GC_THREADS / 32;
 constexpr int GC_FWD_BYTES = 256, GC_BWD_BYTES = 96;  // of x a thread holds, at most where the block can grow
@@ -58,7 +59,7 @@ GnCluster gn_cluster(const GnParams& p, int dt, const DevInfo& d, bool bwd)
     while (lcm % q.V != 0) lcm += p.Cg;
     // NHWC: windows of whole vectors and whole groups, 64 bytes of a row (two sectors) or less.
     const int widest = nhwc ? std::max(1, std::min(ceil_div(64, lcm * es), ceil_div(p.C, lcm))) : 1;
-    const int most_threads = nhwc && !q.one ? GC_SPAN_THREADS : GC_THREADS;
+    const int most_threads = !nhwc ? GC_THREADS : q.one ? GC_ROW_THREADS : GC_SPAN_THREADS;
     for (int m = widest; m >= 1; --m) {
         int64_t vecs;  // of the unit
         if (nhwc) {
@@ -103,18 +104,10 @@ GnCluster gn_cluster(const GnParams& p, int dt, const DevInfo& d, bool bwd)
             // larger clusters while the SMs are not filled and the blocks still have a few
             // kilobytes each
             if (S * 2 <= most && units * S < 2 * d.sms && per * vb > 4096) continue;
-            // Blocks an SM by registers (64 a thread) and by shared memory.  A second tile only
-            // where the cluster walks several samples and the SM keeps its threads: a block
-            // that waits less is worth less than another block (24 x 72 x 72 x 320 bf16
-            // forward: 78 us with two tiles and 2 blocks of 256 an SM, 55 with one and 3).
-            const int by_regs = std::max(1, std::min(32, (nhwc && !q.one ? 768 : 1024) / T));
-            auto per_sm = [&](int smem) { return std::min(by_regs, (227 * 1024) / (smem + 1024)); };
-            q.bufs = 1;
-            int64_t want = std::max<int64_t>(1, int64_t(d.sms) * per_sm(q.smem) / (int64_t(q.wins) * S));
-            if (want < p.B && q.smem + tile <= GC_SMEM && per_sm(q.smem + tile) == per_sm(q.smem)) {
-                q.bufs = 2;
-                q.smem += tile;
-            }
+            // Blocks an SM by registers (64 or 80 a thread) and by shared memory.
+            const int by_regs = std::max(1, std::min(32, (nhwc ? 768 : 1024) / T));
+            const int per_sm = std::min(by_regs, (227 * 1024) / (q.smem + 1024));
+            const int64_t want = std::max<int64_t>(1, int64_t(d.sms) * per_sm / (int64_t(q.wins) * S));
             q.chunks = int(std::min<int64_t>(p.B, want));
             q.dm_cols = FastDivmod(uint32_t(std::max(1, q.cols)));
             q.dm_cg = FastDivmod(uint32_t(p.Cg));
@@ -178,6 +171,94 @@ template <typename T, int V> __device__ __forceinline__ void gc_store(T* p, cons
     Vec<T, V> v;
     v.set(r);
     v.store(p);
+}
+
+// A thread's statistics in one pass: each place of its vectors has sums about a pivot, the place's
+// first value.  The pivot is one of the n values, so the squares about it are at most n times
+// those about the mean, and the subtraction at the end costs at most log2 n bits (n <= 128)
+// whatever the values' offset; equal values give zeros.
+template <int V> struct PivotSums {
+    static constexpr int H = gc_pairs<V>();
+    float2 c[H], s[H], s2[H];  // minus the pivot; sums of the differences and of their squares
+    __device__ __forceinline__ void start(const float2 (&f)[H])
+    {
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            c[h] = mul2(f[h], both(-1.f));
+            s[h] = s2[h] = both(0.f);
+        }
+    }
+    __device__ __forceinline__ void add(const float2 (&f)[H])
+    {
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const float2 e = add2(f[h], c[h]);
+            s[h] = add2(s[h], e);
+            s2[h] = fma2(e, e, s2[h]);
+        }
+    }
+    // (mean, M2) of the values in the places [0, split) and in [split, V), n a place: the places'
+    // results joined about one of their means.
+    template <bool ONE> __device__ __forceinline__ float4 finish(int n, int split) const
+    {
+        const float inv = __fdiv_rn(1.f, float(n));
+        float mu[V], m2[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float ci = i % 2 ? c[i / 2].y : c[i / 2].x, si = i % 2 ? s[i / 2].y : s[i / 2].x;
+            mu[i] = fmaf(si, inv, -ci);
+            m2[i] = fmaf(-si * inv, si, i % 2 ? s2[i / 2].y : s2[i / 2].x);
+        }
+        float a[3] = {0.f, 0.f, 0.f}, b[3] = {0.f, 0.f, 0.f};  // M2; sum and squares of the means' differences
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const bool first = ONE || i < split;
+            const float e = mu[i] - (first ? mu[0] : mu[V - 1]);
+            a[0] += first ? m2[i] : 0.f;
+            a[1] += first ? e : 0.f;
+            a[2] = first ? fmaf(e, e, a[2]) : a[2];
+            if (!ONE) {
+                b[0] += first ? 0.f : m2[i];
+                b[1] += first ? 0.f : e;
+                b[2] = first ? b[2] : fmaf(e, e, b[2]);
+            }
+        }
+        const float ia = ONE ? 1.f / V : __fdiv_rn(1.f, float(split));
+        float4 r = make_float4(fmaf(a[1], ia, mu[0]), fmaf(float(n), fmaf(-a[1] * ia, a[1], a[2]), a[0]), 0.f, 0.f);
+        if (!ONE && split < V) {
+            const float ib = __fdiv_rn(1.f, float(V - split));
+            r.z = fmaf(b[1], ib, mu[V - 1]);
+            r.w = fmaf(float(n), fmaf(-b[1] * ib, b[1], b[2]), b[0]);
+        }
+        return r;
+    }
+};
+
+// The statistics of a thread's n > 0 slots, read as their copies arrive (the first half is one
+// group of copies, the rest another).
+template <typename T, int V, bool ONE>
+__device__ __forceinline__ float4 gc_stats(const unsigned char* slot, int hop, int n, int split)
+{
+    PivotSums<V> w;
+    float2 f[gc_pairs<V>()];
+    const int half = n / 2;
+    if (half > 0) copy_wait<1>();
+    else copy_wait<0>();
+    gc_load<T, V>(slot, f);
+    w.start(f);
+    int k = 1;
+#pragma unroll 4
+    for (; k < half; ++k) {
+        gc_load<T, V>(slot + k * hop, f);
+        w.add(f);
+    }
+    copy_wait<0>();
+#pragma unroll 4
+    for (; k < n; ++k) {
+        gc_load<T, V>(slot + k * hop, f);
+        w.add(f);
+    }
+    return w.template finish<ONE>(n, split);
 }
 
 // n, mean and M2 of the values of two sets.
@@ -268,6 +349,15 @@ struct GcTile {
     }
 };
 
+// Calls f(integral_constant<n>, k) for the slots in order, two at a time and a last one.
+template <class F> __device__ __forceinline__ void gc_pairwise(int slots, F&& f)
+{
+    int k = 0;
+#pragma unroll 1
+    for (; k + 1 < slots; k += 2) f(std::integral_constant<int, 2>(), k);
+    if (k < slots) f(std::integral_constant<int, 1>(), k);
+}
+
 // Warps that share a group (a power of two).
 __device__ __forceinline__ int gc_subs(int groups)
 {
@@ -296,7 +386,7 @@ __device__ __forceinline__ void gc_group_warps(const GnParams& p, const GnCluste
 }
 
 template <typename T, int V, bool ONE>
-__global__ void __launch_bounds__(ONE ? GC_THREADS : GC_SPAN_THREADS, ONE ? 2 : 3)
+__global__ void __launch_bounds__(ONE ? GC_ROW_THREADS : GC_SPAN_THREADS, ONE ? 2 : 3)
 gn_cluster_fwd_nhwc(const GnParams p, const __grid_constant__ GnCluster q, const T* x, const T* gamma, const T* beta,
                     T* y, float* mean_out, float* rstd_out)
 {
@@ -305,19 +395,20 @@ gn_cluster_fwd_nhwc(const GnParams p, const __grid_constant__ GnCluster q, const
     const GcTile t(p, q, V);
     const int nt = int(blockDim.x), hop = nt * VB, tile = q.K * hop;
     unsigned char* slot = dyn + threadIdx.x * VB;
-    float4* rec = reinterpret_cast<float4*>(dyn + size_t(q.bufs) * tile);  // threads x (mean, M2) of either group
+    float4* rec = reinterpret_cast<float4*>(dyn + tile);  // threads x (mean, M2) of either group
     float4* wrec = rec + nt;                                   // warps x (n, mean, M2) of their share of a group
     float2* gs = reinterpret_cast<float2*>(wrec + GC_WARPS);   // 2 x groups (mean, M2) of the block, read by the others
     float2* stat = gs + 2 * q.groups;                          // groups x (mean, rstd) of the unit
     const int64_t at = t.c0 + t.col * V + int64_t(t.r0 + t.lane) * p.C, row_hop = int64_t(q.lanes) * p.C;
-    auto issue = [&](int b, int buf) {
-        const T* src = x + int64_t(b) * p.N + at;
-        unsigned char* dst = slot + buf * tile;
-        for (int k = 0; k < t.mine; ++k, src += row_hop, dst += hop) fetch_vec<T, V>(dst, src);
-        copy_commit();
-    };
     tc::grid_dep_wait();
-    if (q.bufs == 2) issue(t.chunk, 0);
+    {
+        const T* src = x + int64_t(t.chunk) * p.N + at;
+        for (int k = 0; k < t.mine; ++k, src += row_hop) {
+            fetch_vec<T, V>(slot + k * hop, src);
+            if (k == t.mine / 2 - 1) copy_commit();
+        }
+        copy_commit();
+    }
     float2 ga[H], be[H];
 #pragma unroll
     for (int h = 0; h < H; ++h) {
@@ -328,65 +419,8 @@ gn_cluster_fwd_nhwc(const GnParams p, const __grid_constant__ GnCluster q, const
     const int subs = gc_subs(t.groups);
     int turn = 0;
     for (int b = t.chunk; b < p.B; b += q.chunks, turn ^= 1) {
-        const unsigned char* my = slot;
-        if (q.bufs == 2) {
-            my += turn * tile;
-            if (b + q.chunks < p.B) {
-                issue(b + q.chunks, turn ^ 1);
-                copy_wait<1>();
-            } else {
-                copy_wait<0>();
-            }
-        } else {
-            issue(b, 0);
-            copy_wait<0>();
-        }
-        // The thread's mean of its values of either group, then the squares about it.
-        {
-            float m0 = 0.f, m1 = 0.f;
-#pragma unroll 1
-            for (int pass = 0; pass < 2; ++pass) {
-                float2 s[H], mu[H];
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    s[h] = both(0.f);
-                    mu[h] = ONE ? both(-m0)
-                                : make_float2(2 * h < t.split ? -m0 : -m1, 2 * h + 1 < t.split ? -m0 : -m1);
-                    if (V == 1) mu[h].y = 0.f;
-                }
-#pragma unroll 4
-                for (int k = 0; k < t.mine; ++k) {
-                    float2 f[H];
-                    gc_load<T, V>(my + k * hop, f);
-#pragma unroll
-                    for (int h = 0; h < H; ++h) {
-                        if (pass == 0) {
-                            s[h] = add2(s[h], f[h]);
-                        } else {
-                            f[h] = add2(f[h], mu[h]);
-                            s[h] = fma2(f[h], f[h], s[h]);
-                        }
-                    }
-                }
-                float a = 0.f, c = 0.f;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float e = i % 2 ? s[i / 2].y : s[i / 2].x;
-                    if (ONE) {
-                        a += e;
-                    } else {
-                        a += i < t.split ? e : 0.f;
-                        c += i < t.split ? 0.f : e;
-                    }
-                }
-                if (pass == 0) {
-                    m0 = t.mine ? __fdiv_rn(a, float(t.mine * t.split)) : 0.f;
-                    if (!ONE) m1 = t.mine && t.split < V ? __fdiv_rn(c, float(t.mine * (V - t.split))) : 0.f;
-                } else {
-                    rec[threadIdx.x] = make_float4(m0, a, m1, c);
-                }
-            }
-        }
+        const bool more = b + q.chunks < p.B;
+        rec[threadIdx.x] = t.mine ? gc_stats<T, V, ONE>(slot, hop, t.mine, t.split) : make_float4(0.f, 0.f, 0.f, 0.f);
         __syncthreads();
         // A group's mean over its threads' means, then the squares about it; first by warp.
         gc_group_warps<V>(p, q, t, subs, [&](int g, int sub, auto&& for_each) {
@@ -444,21 +478,34 @@ gn_cluster_fwd_nhwc(const GnParams p, const __grid_constant__ GnCluster q, const
         if (t.mine) {
             const float2 s0 = stat[t.g], s1 = ONE ? s0 : stat[min(t.g + 1, t.groups - 1)];
             T* py = y + int64_t(b) * p.N + at;
+            const T* px = x + int64_t(b + q.chunks) * p.N + at;
             with_act(p.act, [&](auto act) {
-#pragma unroll 2
-                for (int k = 0; k < t.mine; ++k, py += row_hop) {
-                    float2 f[H];
-                    gc_load<T, V>(my + k * hop, f);
+                float2 mu[H], rs[H], sc[H];
 #pragma unroll
-                    for (int h = 0; h < H; ++h) {
-                        const float2 mu = ONE ? both(-s0.x) : make_float2(2 * h < t.split ? -s0.x : -s1.x,
-                                                                          2 * h + 1 < t.split ? -s0.x : -s1.x);
-                        const float2 rs = ONE ? both(s0.y) : make_float2(2 * h < t.split ? s0.y : s1.y,
-                                                                         2 * h + 1 < t.split ? s0.y : s1.y);
-                        f[h] = gn_out<act.value>(add2(f[h], mu), rs, act.value == CONV_ACT_RELU ? ga[h] : mul2(ga[h], rs), be[h]);
-                    }
-                    gc_store<T, V>(py, f);
+                for (int h = 0; h < H; ++h) {
+                    const bool f0 = ONE || 2 * h < t.split, f1 = ONE || 2 * h + 1 < t.split;
+                    mu[h] = make_float2(f0 ? -s0.x : -s1.x, f1 ? -s0.x : -s1.x);
+                    rs[h] = make_float2(f0 ? s0.y : s1.y, f1 ? s0.y : s1.y);
+                    sc[h] = act.value == CONV_ACT_RELU ? ga[h] : mul2(ga[h], rs[h]);
                 }
+                gc_pairwise(t.mine, [&](auto n, int k) {
+                    constexpr int U = n.value;
+                    float2 f[U][H];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) gc_load<T, V>(slot + (k + u) * hop, f[u]);
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int h = 0; h < H; ++h)
+                            f[u][h] = gn_out<act.value>(add2(f[u][h], mu[h]), rs[h], sc[h], be[h]);
+#pragma unroll
+                    for (int u = 0; u < U; ++u, py += row_hop, px += row_hop) {
+                        gc_store<T, V>(py, f[u]);
+                        if (more) fetch_vec<T, V>(slot + (k + u) * hop, px);
+                        if (k + u == t.mine / 2 - 1) copy_commit();
+                    }
+                });
+                copy_commit();
             });
         }
     }
@@ -467,7 +514,7 @@ gn_cluster_fwd_nhwc(const GnParams p, const __grid_constant__ GnCluster q, const
 
 // part: chunks * S rows of (dgamma's, dbeta's) channel sums.
 template <typename T, int V, bool ONE>
-__global__ void __launch_bounds__(ONE ? GC_THREADS : GC_SPAN_THREADS, ONE ? 2 : 3)
+__global__ void __launch_bounds__(ONE ? GC_ROW_THREADS : GC_SPAN_THREADS, ONE ? 2 : 3)
 gn_cluster_bwd_nhwc(const GnParams p, const __grid_constant__ GnCluster q, const T* x, const T* dy, const T* gamma,
                     const T* beta, const float* mean, const float* rstd, T* dx, float* part)
 {
@@ -477,23 +524,23 @@ gn_cluster_bwd_nhwc(const GnParams p, const __grid_constant__ GnCluster q, const
     const int nt = int(blockDim.x), hop = nt * VB, tile = q.K * hop;
     unsigned char* slot = dyn + threadIdx.x * VB;
     // threads x (sum dz*gamma*xhat, sum dz*gamma) of either group
-    float4* rec = reinterpret_cast<float4*>(dyn + size_t(2 * q.bufs) * tile);
+    float4* rec = reinterpret_cast<float4*>(dyn + 2 * tile);
     float2* wrec = reinterpret_cast<float2*>(rec + nt);        // warps x the same of their share of a group
     float2* gs = wrec + GC_WARPS;                              // 2 x groups, the block's, read by the others
     float2* gt = gs + 2 * q.groups;                            // groups x (m2, m1) of the unit
     float* red = reinterpret_cast<float*>(rec);                // at the end: channel sums of the lanes
     const int64_t at = t.c0 + t.col * V + int64_t(t.r0 + t.lane) * p.C, row_hop = int64_t(q.lanes) * p.C;
-    auto issue = [&](int b, int buf) {
-        int64_t src = int64_t(b) * p.N + at;
-        unsigned char* dst = slot + buf * 2 * tile;
-        for (int k = 0; k < t.mine; ++k, src += row_hop, dst += hop) {
-            fetch_vec<T, V>(dst, x + src);
-            fetch_vec<T, V>(dst + tile, dy + src);
+    tc::grid_dep_wait();
+    if (part) tc::grid_dep_launch();
+    {
+        int64_t src = int64_t(t.chunk) * p.N + at;
+        for (int k = 0; k < t.mine; ++k, src += row_hop) {
+            fetch_vec<T, V>(slot + k * hop, x + src);
+            fetch_vec<T, V>(slot + tile + k * hop, dy + src);
+            if (k == t.mine / 2 - 1) copy_commit();
         }
         copy_commit();
-    };
-    tc::grid_dep_wait();
-    if (q.bufs == 2) issue(t.chunk, 0);
+    }
     float2 ga[H], be[H], sg[H], sb[H];
 #pragma unroll
     for (int h = 0; h < H; ++h) {
@@ -505,80 +552,62 @@ gn_cluster_bwd_nhwc(const GnParams p, const __grid_constant__ GnCluster q, const
     const int subs = gc_subs(t.groups);
     int turn = 0;
     for (int b = t.chunk; b < p.B; b += q.chunks, turn ^= 1) {
-        unsigned char* my = slot;
+        const bool more = b + q.chunks < p.B;
         const int64_t g0 = int64_t(b) * p.G + t.g0 + t.g;
         const float mu0 = -mean[g0], rs0 = rstd[g0];
         const bool next = !ONE && t.split < V;
         const float mu1 = next ? -mean[g0 + 1] : mu0, rs1 = next ? rstd[g0 + 1] : rs0;
-        if (q.bufs == 2) {
-            my += turn * 2 * tile;
-            if (b + q.chunks < p.B) {
-                issue(b + q.chunks, turn ^ 1);
-                copy_wait<1>();
-            } else {
-                copy_wait<0>();
-            }
-        } else {
-            issue(b, 0);
-            copy_wait<0>();
-        }
-        auto mu = [&](int h) {
-            return ONE ? both(mu0) : make_float2(2 * h < t.split ? mu0 : mu1, 2 * h + 1 < t.split ? mu0 : mu1);
-        };
-        auto rs = [&](int h) {
-            return ONE ? both(rs0) : make_float2(2 * h < t.split ? rs0 : rs1, 2 * h + 1 < t.split ? rs0 : rs1);
-        };
-        {
-            // This sample's sums of dz*xhat and dz: by place where a vector lies in two groups
-            // (and times gamma below), else of dz*gamma right away, which takes fewer registers.
-            float2 a[ONE ? 1 : H], c[ONE ? 1 : H];
+        // by place: minus the mean, rstd (this sample's)
+        float2 mu[H], rs[H];
 #pragma unroll
-            for (int h = 0; h < (ONE ? 1 : H); ++h) a[h] = c[h] = both(0.f);
+        for (int h = 0; h < H; ++h) {
+            mu[h] = ONE ? both(mu0) : make_float2(2 * h < t.split ? mu0 : mu1, 2 * h + 1 < t.split ? mu0 : mu1);
+            rs[h] = ONE ? both(rs0) : make_float2(2 * h < t.split ? rs0 : rs1, 2 * h + 1 < t.split ? rs0 : rs1);
+        }
+        {
+            float2 a[H], c[H];  // this sample's sums of dz * (x - mean) and dz by place
+#pragma unroll
+            for (int h = 0; h < H; ++h) a[h] = c[h] = both(0.f);
             with_act(p.act, [&](auto act) {
+                float2 sc[H];
+#pragma unroll
+                for (int h = 0; h < H; ++h) sc[h] = act.value == CONV_ACT_RELU ? ga[h] : mul2(ga[h], rs[h]);
+                copy_wait<1>();  // the first half's copies
 #pragma unroll 1
                 for (int k = 0; k < t.mine; ++k) {
-                    float2 xh[H], dz[H];
-                    gc_load<T, V>(my + k * hop, xh);
-                    gc_load<T, V>(my + tile + k * hop, dz);
+                    if (k == t.mine / 2) copy_wait<0>();
+                    float2 d[H], dz[H];
+                    gc_load<T, V>(slot + k * hop, d);
+                    gc_load<T, V>(slot + tile + k * hop, dz);
 #pragma unroll
                     for (int h = 0; h < H; ++h) {
-                        xh[h] = mul2(add2(xh[h], mu(h)), rs(h));
-                        dz[h] = gn_grad<act.value>(dz[h], xh[h], ga[h], be[h]);
-                        if constexpr (ONE) {
-                            sb[h] = add2(sb[h], dz[h]);
-                            sg[h] = fma2(dz[h], xh[h], sg[h]);
-                            const float2 e = mul2(dz[h], ga[h]);
-                            c[0] = add2(c[0], e);
-                            a[0] = fma2(e, xh[h], a[0]);
-                        } else {
-                            c[h] = add2(c[h], dz[h]);
-                            a[h] = fma2(dz[h], xh[h], a[h]);
-                        }
+                        d[h] = add2(d[h], mu[h]);
+                        dz[h] = gn_dz_at<act.value>(dz[h], d[h], rs[h], sc[h], be[h]);
+                        c[h] = add2(c[h], dz[h]);
+                        a[h] = fma2(dz[h], d[h], a[h]);
                     }
                     // dz in dy's place: exact in fp32, and not computed again
-                    if constexpr (sizeof(T) == 4) gc_store<T, V>(reinterpret_cast<T*>(my + tile + k * hop), dz);
+                    if constexpr (sizeof(T) == 4) gc_store<T, V>(reinterpret_cast<T*>(slot + tile + k * hop), dz);
                 }
             });
             float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-            if constexpr (ONE) {
-                r.x = a[0].x + a[0].y;
-                r.y = c[0].x + c[0].y;
-            } else {
 #pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    sg[h] = add2(sg[h], a[h]);
-                    sb[h] = add2(sb[h], c[h]);
-                    a[h] = mul2(a[h], ga[h]);
-                    c[h] = mul2(c[h], ga[h]);
-                }
+            for (int h = 0; h < H; ++h) {
+                a[h] = mul2(a[h], rs[h]);
+                sg[h] = add2(sg[h], a[h]);
+                sb[h] = add2(sb[h], c[h]);
+                a[h] = mul2(a[h], ga[h]);
+                c[h] = mul2(c[h], ga[h]);
+            }
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float e = i % 2 ? a[i / 2].y : a[i / 2].x, f = i % 2 ? c[i / 2].y : c[i / 2].x;
-                    const bool first = i < t.split;
-                    r.x += first ? e : 0.f;
-                    r.y += first ? f : 0.f;
+            for (int i = 0; i < V; ++i) {
+                const float e = i % 2 ? a[i / 2].y : a[i / 2].x, g = i % 2 ? c[i / 2].y : c[i / 2].x;
+                const bool first = ONE || i < t.split;
+                r.x += first ? e : 0.f;
+                r.y += first ? g : 0.f;
+                if (!ONE) {
                     r.z += first ? 0.f : e;
-                    r.w += first ? 0.f : f;
+                    r.w += first ? 0.f : g;
                 }
             }
             rec[threadIdx.x] = r;
@@ -616,23 +645,38 @@ gn_cluster_bwd_nhwc(const GnParams p, const __grid_constant__ GnCluster q, const
         if (t.mine) {
             const float2 s0 = gt[t.g], s1 = ONE ? s0 : gt[min(t.g + 1, t.groups - 1)];
             T* po = dx + int64_t(b) * p.N + at;
+            int64_t src = int64_t(b + q.chunks) * p.N + at;
             with_act(p.act, [&](auto act) {
+                // dx = dz * gamma * rstd - (x - mean) * rstd^2 * m2 - rstd * m1
+                float2 sc[H], k1[H], k2[H];
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    const bool f0 = ONE || 2 * h < t.split, f1 = ONE || 2 * h + 1 < t.split;
+                    sc[h] = mul2(ga[h], rs[h]);
+                    k1[h] = mul2(make_float2(f0 ? -s0.y : -s1.y, f1 ? -s0.y : -s1.y), rs[h]);
+                    k2[h] = mul2(make_float2(f0 ? -s0.x : -s1.x, f1 ? -s0.x : -s1.x), mul2(rs[h], rs[h]));
+                }
 #pragma unroll 1
-                for (int k = 0; k < t.mine; ++k, po += row_hop) {
-                    float2 xh[H], dz[H];
-                    gc_load<T, V>(my + tile + k * hop, dz);
-                    gc_load<T, V>(my + k * hop, xh);
+                for (int k = 0; k < t.mine; ++k, po += row_hop, src += row_hop) {
+                    float2 d[H], dz[H];
+                    gc_load<T, V>(slot + tile + k * hop, dz);
+                    gc_load<T, V>(slot + k * hop, d);
 #pragma unroll
                     for (int h = 0; h < H; ++h) {
-                        xh[h] = mul2(add2(xh[h], mu(h)), rs(h));
-                        if constexpr (sizeof(T) == 2) dz[h] = gn_grad<act.value>(dz[h], xh[h], ga[h], be[h]);
-                        const bool f0 = ONE || 2 * h < t.split, f1 = ONE || 2 * h + 1 < t.split;
-                        const float2 m2 = make_float2(f0 ? -s0.x : -s1.x, f1 ? -s0.x : -s1.x);
-                        const float2 m1 = make_float2(f0 ? -s0.y : -s1.y, f1 ? -s0.y : -s1.y);
-                        xh[h] = mul2(rs(h), fma2(xh[h], m2, fma2(dz[h], ga[h], m1)));
+                        d[h] = add2(d[h], mu[h]);
+                        if constexpr (sizeof(T) == 2)
+                            dz[h] = gn_dz_at<act.value>(dz[h], d[h], rs[h], act.value == CONV_ACT_RELU ? ga[h] : sc[h],
+                                                        be[h]);
+                        d[h] = fma2(dz[h], sc[h], fma2(d[h], k2[h], k1[h]));
                     }
-                    gc_store<T, V>(po, xh);
+                    gc_store<T, V>(po, d);
+                    if (more) {
+                        fetch_vec<T, V>(slot + k * hop, x + src);
+                        fetch_vec<T, V>(slot + tile + k * hop, dy + src);
+                    }
+                    if (k == t.mine / 2 - 1) copy_commit();
                 }
+                copy_commit();
             });
         }
     }
@@ -734,58 +778,30 @@ gn_cluster_fwd_nchw(const GnParams p, const __grid_constant__ GnCluster q, const
     const GcRange t(p, q, V);
     const int nt = int(blockDim.x), hop = nt * VB, tile = q.K * hop, nw = nt >> 5, lane = int(threadIdx.x & 31);
     unsigned char* slot = dyn + threadIdx.x * VB;
-    float4* wrec = reinterpret_cast<float4*>(dyn + size_t(q.bufs) * tile);  // 2 x warps (n, mean, M2)
+    float4* wrec = reinterpret_cast<float4*>(dyn + tile);  // 2 x warps (n, mean, M2)
     float2* ex = reinterpret_cast<float2*>(wrec + 2 * GC_WARPS);  // 2: the block's mean and M2, read by the others
     float2* gb = ex + 2;                                          // Cg x (gamma, beta)
-    auto issue = [&](int b, int buf) {
-        const T* src = x + int64_t(b) * p.N + t.base;
-        unsigned char* dst = slot + buf * tile;
-        for (int k = 0; k < t.mine; ++k, src += nt * V, dst += hop) fetch_vec<T, V>(dst, src);
-        copy_commit();
-    };
     tc::grid_dep_wait();
-    if (q.bufs == 2) issue(t.chunk, 0);
+    {
+        const T* src = x + int64_t(t.chunk) * p.N + t.base;
+        for (int k = 0; k < t.mine; ++k, src += nt * V) {
+            fetch_vec<T, V>(slot + k * hop, src);
+            if (k == t.mine / 2 - 1) copy_commit();
+        }
+        copy_commit();
+    }
     for (int c = threadIdx.x; c < p.Cg; c += nt)
         gb[c] = make_float2(gamma ? Elem<T>::ldg(gamma + t.g * p.Cg + c) : 1.f,
                             beta ? Elem<T>::ldg(beta + t.g * p.Cg + c) : 0.f);
     int turn = 0;
     for (int b = t.chunk; b < p.B; b += q.chunks, turn ^= 1) {
-        const unsigned char* my = slot;
-        if (q.bufs == 2) {
-            my += turn * tile;
-            if (b + q.chunks < p.B) {
-                issue(b + q.chunks, turn ^ 1);
-                copy_wait<1>();
-            } else {
-                copy_wait<0>();
-            }
-        } else {
-            issue(b, 0);
-            copy_wait<0>();
-        }
-        // the thread's mean, then the squares about it; then the warp's, the block's, the cluster's
+        const bool more = b + q.chunks < p.B;
+        // the thread's mean and the squares about it; then the warp's, the block's, the cluster's
         Moments w = {float(t.mine * V), 0.f, 0.f};
-#pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {
-            float2 s[2] = {both(0.f), both(0.f)};
-            const float2 neg = make_float2(-w.mean, V == 1 ? 0.f : -w.mean);
-#pragma unroll 2
-            for (int k = 0; k < t.mine; ++k) {
-                float2 f[H];
-                gc_load<T, V>(my + k * hop, f);
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    if (pass == 0) {
-                        s[h & 1] = add2(s[h & 1], f[h]);
-                    } else {
-                        f[h] = add2(f[h], neg);
-                        s[h & 1] = fma2(f[h], f[h], s[h & 1]);
-                    }
-                }
-            }
-            s[0] = add2(s[0], s[1]);
-            if (pass == 0) w.mean = t.mine ? __fdiv_rn(s[0].x + s[0].y, w.n) : 0.f;
-            else w.m2 = s[0].x + s[0].y;
+        if (t.mine) {
+            const float4 r = gc_stats<T, V, true>(slot, hop, t.mine, V);
+            w.mean = r.x;
+            w.m2 = r.y;
         }
         {
             const float n = warp_sum(w.n), m = n > 0.f ? __fdiv_rn(warp_sum(w.n * w.mean), n) : 0.f;
@@ -814,12 +830,13 @@ gn_cluster_fwd_nchw(const GnParams p, const __grid_constant__ GnCluster q, const
             rstd_out[int64_t(b) * p.G + t.g] = stat.y;
         }
         T* py = y + int64_t(b) * p.N + t.base;
+        const T* px = x + int64_t(b + q.chunks) * p.N + t.base;
         with_act(p.act, [&](auto act) {
 #pragma unroll 1
-            for (int k = 0; k < t.mine; ++k, py += nt * V) {
+            for (int k = 0; k < t.mine; ++k, py += nt * V, px += nt * V) {
                 const GcChan ch(p, q, t.v0 + int(threadIdx.x) + k * nt, V);
                 float2 f[H];
-                gc_load<T, V>(my + k * hop, f);
+                gc_load<T, V>(slot + k * hop, f);
                 with_channels<V>(ch, gb, [&](const auto& ga, const auto& be) {
 #pragma unroll
                     for (int h = 0; h < H; ++h)
@@ -827,7 +844,10 @@ gn_cluster_fwd_nchw(const GnParams p, const __grid_constant__ GnCluster q, const
                                                  act.value == CONV_ACT_RELU ? ga[h] : mul2(ga[h], both(stat.y)), be[h]);
                 });
                 gc_store<T, V>(py, f);
+                if (more) fetch_vec<T, V>(slot + k * hop, px);
+                if (k == t.mine / 2 - 1) copy_commit();
             }
+            copy_commit();
         });
     }
     if (q.S > 1) cluster_barrier();  // no block leaves while another still reads its shared memory
@@ -843,23 +863,23 @@ gn_cluster_bwd_nchw(const GnParams p, const __grid_constant__ GnCluster q, const
     const GcRange t(p, q, V);
     const int nt = int(blockDim.x), hop = nt * VB, tile = q.K * hop, nw = nt >> 5, lane = int(threadIdx.x & 31);
     unsigned char* slot = dyn + threadIdx.x * VB;
-    float2* vs = reinterpret_cast<float2*>(dyn + size_t(2 * q.bufs) * tile);  // (dz*xhat, dz) sums of each vector's
+    float2* vs = reinterpret_cast<float2*>(dyn + 2 * tile);  // (dz*xhat, dz) sums of each vector's
                                                                               // values of its first channel,
     float2* over = vs + q.K * nt;           // of those that enter channel c with the vector that begins in c - 1
     float2* wrec = over + p.Cg + 1;         // 2 x warps
     float2* ex = wrec + 2 * GC_WARPS;       // 2: the block's sums, read by the others
     float2* gb = ex + 2;                    // Cg x (gamma, beta)
-    auto issue = [&](int b, int buf) {
-        int64_t src = int64_t(b) * p.N + t.base;
-        unsigned char* dst = slot + buf * 2 * tile;
-        for (int k = 0; k < t.mine; ++k, src += nt * V, dst += hop) {
-            fetch_vec<T, V>(dst, x + src);
-            fetch_vec<T, V>(dst + tile, dy + src);
+    tc::grid_dep_wait();
+    if (part) tc::grid_dep_launch();
+    {
+        int64_t src = int64_t(t.chunk) * p.N + t.base;
+        for (int k = 0; k < t.mine; ++k, src += nt * V) {
+            fetch_vec<T, V>(slot + k * hop, x + src);
+            fetch_vec<T, V>(slot + tile + k * hop, dy + src);
+            if (k == t.mine / 2 - 1) copy_commit();
         }
         copy_commit();
-    };
-    tc::grid_dep_wait();
-    if (q.bufs == 2) issue(t.chunk, 0);
+    }
     for (int c = threadIdx.x; c < p.Cg; c += nt) {
         gb[c] = make_float2(gamma ? Elem<T>::ldg(gamma + t.g * p.Cg + c) : 1.f,
                             beta ? Elem<T>::ldg(beta + t.g * p.Cg + c) : 0.f);
@@ -869,58 +889,50 @@ gn_cluster_bwd_nchw(const GnParams p, const __grid_constant__ GnCluster q, const
     __syncthreads();
     int turn = 0;
     for (int b = t.chunk; b < p.B; b += q.chunks, turn ^= 1) {
-        unsigned char* my = slot;
+        const bool more = b + q.chunks < p.B;
         const int64_t grp = int64_t(b) * p.G + t.g;
         const float mu = -mean[grp], rs = rstd[grp];
-        if (q.bufs == 2) {
-            my += turn * 2 * tile;
-            if (b + q.chunks < p.B) {
-                issue(b + q.chunks, turn ^ 1);
-                copy_wait<1>();
-            } else {
-                copy_wait<0>();
-            }
-        } else {
-            issue(b, 0);
-            copy_wait<0>();
-        }
         float2 s = both(0.f);  // sum dz*gamma*xhat, sum dz*gamma
         with_act(p.act, [&](auto act) {
+            copy_wait<1>();  // the first half's copies
 #pragma unroll 1
             for (int k = 0; k < t.mine; ++k) {
+                if (k == t.mine / 2) copy_wait<0>();
                 const GcChan ch(p, q, t.v0 + int(threadIdx.x) + k * nt, V);
-                float2 xh[H], dz[H];
-                gc_load<T, V>(my + k * hop, xh);
-                gc_load<T, V>(my + tile + k * hop, dz);
+                float2 d[H], dz[H];
+                gc_load<T, V>(slot + k * hop, d);
+                gc_load<T, V>(slot + tile + k * hop, dz);
                 with_channels<V>(ch, gb, [&](const auto& ga, const auto& be) {
-                    float2 g = both(0.f), d = both(0.f);
+                    float2 g = both(0.f), e = both(0.f);
 #pragma unroll
                     for (int h = 0; h < H; ++h) {
-                        xh[h] = mul2(add2(xh[h], both(mu)), both(rs));
-                        dz[h] = gn_grad<act.value>(dz[h], xh[h], ga[h], be[h]);
-                        xh[h] = mul2(dz[h], xh[h]);
-                        g = add2(g, xh[h]);
-                        d = add2(d, dz[h]);
+                        d[h] = add2(d[h], both(mu));
+                        dz[h] = gn_dz_at<act.value>(dz[h], d[h], both(rs),
+                                                    act.value == CONV_ACT_RELU ? ga[h] : mul2(ga[h], both(rs)), be[h]);
+                        g = fma2(dz[h], d[h], g);
+                        e = add2(e, dz[h]);
                     }
-                    float2 first = V == 1 ? make_float2(g.x, d.x) : make_float2(g.x + g.y, d.x + d.y);
+                    float2 first = V == 1 ? make_float2(g.x, e.x) : make_float2(g.x + g.y, e.x + e.y);
                     if (ch.split < V) {  // the values of either channel apart
                         float2 second = both(0.f);
                         first = both(0.f);
 #pragma unroll
                         for (int i = 0; i < V; ++i) {
-                            const float2 e = i % 2 ? make_float2(xh[i / 2].y, dz[i / 2].y)
-                                                   : make_float2(xh[i / 2].x, dz[i / 2].x);
-                            if (i < ch.split) first = add2(first, e);
-                            else second = add2(second, e);
+                            const float di = i % 2 ? d[i / 2].y : d[i / 2].x, zi = i % 2 ? dz[i / 2].y : dz[i / 2].x;
+                            const float2 v = make_float2(di * zi, zi);
+                            if (i < ch.split) first = add2(first, v);
+                            else second = add2(second, v);
                         }
+                        second.x *= rs;
                         over[ch.c + 1] = add2(over[ch.c + 1], second);
                         s = fma2(second, both(ga[H - 1].y), s);
                     }
+                    first.x *= rs;
                     s = fma2(first, both(ga[0].x), s);
                     vs[k * nt + threadIdx.x] = add2(vs[k * nt + threadIdx.x], first);
                 });
                 // dz in dy's place: exact in fp32, and not computed again
-                if constexpr (sizeof(T) == 4) gc_store<T, V>(reinterpret_cast<T*>(my + tile + k * hop), dz);
+                if constexpr (sizeof(T) == 4) gc_store<T, V>(reinterpret_cast<T*>(slot + tile + k * hop), dz);
             }
         });
         s = make_float2(warp_sum(s.x), warp_sum(s.y));
@@ -935,25 +947,36 @@ gn_cluster_bwd_nchw(const GnParams p, const __grid_constant__ GnCluster q, const
             cluster_barrier();
             s = gc_add(q, tc::smem_u32(ex + turn));
         }
-        const float2 m2 = both(-s.x * p.inv_m), m1 = both(-s.y * p.inv_m);
+        // dx = dz * gamma * rstd - (x - mean) * rstd^2 * m2 - rstd * m1
+        const float2 k2 = both(-s.x * p.inv_m * rs * rs), k1 = both(-s.y * p.inv_m * rs);
         T* po = dx + int64_t(b) * p.N + t.base;
+        int64_t src = int64_t(b + q.chunks) * p.N + t.base;
         with_act(p.act, [&](auto act) {
 #pragma unroll 1
-            for (int k = 0; k < t.mine; ++k, po += nt * V) {
+            for (int k = 0; k < t.mine; ++k, po += nt * V, src += nt * V) {
                 const GcChan ch(p, q, t.v0 + int(threadIdx.x) + k * nt, V);
-                float2 xh[H], dz[H];
-                gc_load<T, V>(my + tile + k * hop, dz);
-                gc_load<T, V>(my + k * hop, xh);
+                float2 d[H], dz[H];
+                gc_load<T, V>(slot + tile + k * hop, dz);
+                gc_load<T, V>(slot + k * hop, d);
                 with_channels<V>(ch, gb, [&](const auto& ga, const auto& be) {
 #pragma unroll
                     for (int h = 0; h < H; ++h) {
-                        xh[h] = mul2(add2(xh[h], both(mu)), both(rs));
-                        if constexpr (sizeof(T) == 2) dz[h] = gn_grad<act.value>(dz[h], xh[h], ga[h], be[h]);
-                        xh[h] = mul2(both(rs), fma2(xh[h], m2, fma2(dz[h], ga[h], m1)));
+                        const float2 sc = mul2(ga[h], both(rs));
+                        d[h] = add2(d[h], both(mu));
+                        if constexpr (sizeof(T) == 2)
+                            dz[h] = gn_dz_at<act.value>(dz[h], d[h], both(rs), act.value == CONV_ACT_RELU ? ga[h] : sc,
+                                                        be[h]);
+                        d[h] = fma2(dz[h], sc, fma2(d[h], k2, k1));
                     }
                 });
-                gc_store<T, V>(po, xh);
+                gc_store<T, V>(po, d);
+                if (more) {
+                    fetch_vec<T, V>(slot + k * hop, x + src);
+                    fetch_vec<T, V>(slot + tile + k * hop, dy + src);
+                }
+                if (k == t.mine / 2 - 1) copy_commit();
             }
+            copy_commit();
         });
     }
     if (q.S > 1) cluster_barrier();  // no block leaves while another still reads its shared memory

@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(256) gn_stats(const GnParams p, const GnPieces
     const T* px = x + t.row * p.P;
     float n = 0.f, mean = 0.f, m2 = 0.f;
     tc::grid_dep_wait();
+    tc::grid_dep_launch();
     for (int e = t.e0; e < t.e1; e += t.hop * U) {
         Vec<T, V> v[U];
         int cnt = 0;
@@ -240,6 +241,7 @@ __global__ void __launch_bounds__(128) gn_combine(const GnParams p, const GnPiec
     const int b = int(blockIdx.x / p.G), g = int(blockIdx.x % p.G);
     const int np = p.Cg * q.pieces;
     tc::grid_dep_wait();
+    tc::grid_dep_launch();
     float s = 0.f;
     auto at = [&](int i, int& cnt) {
         const int pc = i / p.Cg, cl = i - pc * p.Cg;

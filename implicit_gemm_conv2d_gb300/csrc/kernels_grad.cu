@@ -138,6 +138,7 @@ __global__ void __launch_bounds__(GRAD_THREADS) grad_squares(const __grid_consta
     __shared__ float sm[GRAD_THREADS / 32];
     float s = 0.f;
     tc::grid_dep_wait();
+    tc::grid_dep_launch();
     for (int t = blockIdx.x; t < l.tiles; t += gridDim.x) {
         const int k = find_entry(l, t);
         const int64_t n = l.n[k] < 0 ? -l.n[k] : l.n[k], at = int64_t(t - l.first[k]) * l.tile;
