@@ -138,8 +138,10 @@ template <class F> __device__ __forceinline__ void with_act(int act, F&& f)
 // offsets in the sample and (backward) its channel sums stay in registers.  Gamma and beta lie
 // in shared memory by position, in the order the lanes read them.
 constexpr int GN_THREADS = 256;
-constexpr int GN_FWD_VALUES = 16;     // values a lane holds at most
-constexpr int GN_BWD_VALUES = 12;     // the backward also keeps two sums a value
+// Values a lane holds at most; larger groups go to a cluster.  The backward also keeps two sums a
+// value.  M = 512, forward, us, team / cluster: bf16 2048 x 512 x 16 21.7 / 24.4 (channels last
+// 22.5 / 32.8), fp32 32.2 / 27.5.
+constexpr int gn_team_values(int dt, bool bwd) { return bwd || dt == DT_F32 ? 12 : 16; }
 
 struct GnTeam {
     int V, K, L;
@@ -151,12 +153,12 @@ struct GnTeam {
 GnTeam gn_team(const GnParams& p, int dt, const DevInfo& d, bool bwd);
 
 // Vectors a lane (K) that are compiled for each width.
-inline bool gn_team_k(int V, int K, bool bwd)
+inline bool gn_team_k(int V, int K)
 {
     switch (V) {
-        case 8: return K == 1 || (K == 2 && !bwd);
-        case 4: return K >= 1 && K <= (bwd ? 3 : 4);
-        case 2: return K == 2 || K == 4 || (K == 8 && !bwd);
+        case 8: return K == 1 || K == 2;
+        case 4: return K >= 1 && K <= 4;
+        case 2: return K == 2 || K == 4 || K == 8;
         default: return K == 2 || K == 4 || K == 8;
     }
 }
@@ -317,9 +319,10 @@ __device__ __forceinline__ int64_t gn_part(const GnParams& p, int pieces, int64_
     return (b * pieces + pc) * p.C + c;
 }
 
-// The compiled (V, K); MORE: those of the forward only.
-#define GN_DISPATCH_TEAM(T, MORE, CALL)                                \
+// The compiled (V, K); MORE: those of the bf16 forward only.
+#define GN_DISPATCH_TEAM(T, FWD, CALL)                                 \
     do {                                                               \
+        constexpr bool MORE = (FWD) && sizeof(T) == 2;                 \
         if constexpr (sizeof(T) == 2)                                  \
             if (q.V == 8) {                                            \
                 if constexpr (MORE)                                    \

@@ -119,12 +119,12 @@ gn_team_bwd(const GnParams p, const GnTeam q, const T* x, const T* dy, const T* 
     }
     if (!part) return;
     // Channel sums of the block: dgamma's, then dbeta's, by position in shared memory; `lp` lanes
-    // a channel add its positions over the block's samples in a fixed order.
-    const int per = q.spc * p.P;
+    // a channel add its positions over the block's samples in a fixed order: as many as there are
+    // while every channel has its own.
+    const int per = q.spc * p.P, nch = min(q.gpc, p.G - g0) * p.Cg;
     int lp = 1;
-    while (lp < 32 && lp * 2 < per) lp *= 2;
+    while (lp < 32 && lp * 2 < per && lp * 2 * nch <= int(blockDim.x)) lp *= 2;
     const int sub = int(threadIdx.x) / lp, sl = int(threadIdx.x) % lp, teams = int(blockDim.x) / lp;
-    const int nch = min(q.gpc, p.G - g0) * p.Cg;
 #pragma unroll 1
     for (int kind = 0; kind < 2; ++kind) {
         __syncthreads();
@@ -145,6 +145,7 @@ gn_team_bwd(const GnParams p, const GnTeam q, const T* x, const T* dy, const T* 
                 q.dm_cg.divmod(uint32_t(c), gj, cl);
                 const float* base = tab + gj * m + (p.layout == CONV_LAYOUT_NHWC ? cl : cl * p.P);
                 const int hop = p.layout == CONV_LAYOUT_NHWC ? p.Cg : 1;
+#pragma unroll 4
                 for (int o = sl; o < per; o += lp) {
                     uint32_t s, pp;
                     q.dm_p.divmod(uint32_t(o), s, pp);

@@ -17,7 +17,7 @@ namespace igc {
 GnTeam gn_team(const GnParams& p, int dt, const DevInfo& d, bool bwd)
 {
     GnTeam q = {};
-    const int es = dt == DT_F32 ? 4 : 2, most = bwd ? GN_BWD_VALUES : GN_FWD_VALUES;
+    const int es = dt == DT_F32 ? 4 : 2, most = gn_team_values(dt, bwd);
     if (p.M > 32 * most) return q;
     // Vector width, vectors a lane and lanes: the fewest instructions a value by this count of
     // them -- a value's own, the team's butterflies (two sums of one word, two steps an
@@ -28,7 +28,7 @@ GnTeam gn_team(const GnParams& p, int dt, const DevInfo& d, bool bwd)
         if ((p.layout == CONV_LAYOUT_NCHW ? p.M : p.Cg) % V != 0) continue;
         const int64_t nvec = p.M / V;
         for (int K = 1; K * V <= most; ++K) {
-            if (!gn_team_k(V, K, bwd)) continue;
+            if (!gn_team_k(V, K)) continue;
             int L = 1, steps = 0;
             while (int64_t(L) * K < nvec) { L *= 2; ++steps; }
             if (L > 32) continue;

@@ -39,9 +39,10 @@ extern "C" {
  * Layouts (dense): CONV_LAYOUT_NCHW is (B, C, P), the conv layers' own; CONV_LAYOUT_NHWC is
  * (B, P, C), channels last.  x, y, dy, dx, gamma, beta, dgamma, dbeta have the descriptor's
  * dtype; mean and rstd are fp32, (B, G).
- * xhat and z are computed by separate, individually rounded fp32 operations in both
- * directions, so with the forward's mean and rstd the backward's z has the forward's bits and
- * its ReLU mask is exactly y > 0 of the fp32 forward.
+ * With CONV_ACT_RELU, xhat and z are computed by separate, individually rounded fp32 operations
+ * in both directions: with the forward's mean and rstd the backward's z has the forward's bits
+ * and its ReLU mask is exactly y > 0 of the fp32 forward.  The other activations, whose
+ * derivatives have no jump, take z = (x - mean) * (rstd * gamma) + beta with one rounding less.
  * A value that is infinite or NaN makes its whole group NaN and leaves the others alone. */
 typedef enum { CONV_LAYOUT_NCHW = 0, CONV_LAYOUT_NHWC = 1 } conv_layout_t;
 typedef enum { CONV_ACT_NONE = 0, CONV_ACT_RELU = 1, CONV_ACT_SILU = 2, CONV_ACT_GELU = 3 } conv_act_t;
@@ -75,8 +76,8 @@ int conv_gn_bwd(const conv_gn_desc_t* desc, const void* x, const void* dy, const
  * idx: (T), int32 or int64; table, dtable: (V, D); y, dy: (T, D).
  * A token equal to padding_idx, or outside [0, V), names no row: its y is zero and it adds to
  * no gradient (no row is read for it).  padding_idx < 0: no padding row.
- * The gradient sorts the tokens by row (stable), so every row is summed in one fixed order, and
- * rows that no token names are zeros. */
+ * The gradient adds a row's tokens in an order that the sizes fix (by parts of consecutive tokens,
+ * then the parts), and rows that no token names are zeros. */
 typedef enum { CONV_INDEX_I32 = 0, CONV_INDEX_I64 = 1 } conv_index_t;
 
 typedef struct {
