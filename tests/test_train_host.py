@@ -110,10 +110,14 @@ def test_grads_refused(L):
     def one(grad=OK, out=OK, n=10, dtype=0):
         return (train.Grad * 1)(train.Grad(grad, out, n, dtype))
 
-    def calls(a, count=1, norm=OK, max_norm=1.0):
+    # The addresses are made up: every call here has to be one that is refused.
+    def clip(a, count=1, norm=OK, max_norm=1.0):
         p = ctypes.addressof(a) if a is not None else None
-        return (L.conv_grad_norm(p, count, norm, OK, 1 << 40, None),
-                L.conv_grad_clip(p, count, max_norm, norm, OK, 1 << 40, None))
+        return L.conv_grad_clip(p, count, max_norm, norm, OK, 1 << 40, None)
+
+    def calls(a, count=1, norm=OK):
+        p = ctypes.addressof(a) if a is not None else None
+        return L.conv_grad_norm(p, count, norm, OK, 1 << 40, None), clip(a, count, norm)
 
     assert calls(one(n=-1)) == (-2, -2)
     assert calls(one(dtype=2)) == (-2, -2)
@@ -122,13 +126,13 @@ def test_grads_refused(L):
     assert calls(one(n=1 << 40)) == (-3, -3)
     assert calls(None) == (-1, -1)
     assert calls(one(grad=None)) == (-1, -1)
-    assert calls(one(out=None))[1] == -1
+    assert clip(one(out=None)) == -1
     assert calls(one(grad=0x1002)) == (-4, -4)          # fp32 off its element
-    assert calls(one(out=0x1002))[1] == -4
+    assert clip(one(out=0x1002)) == -4
     assert calls(one(grad=0x1001, dtype=1)) == (-4, -4)
     assert calls(one(), norm=None) == (-1, -1)
     for m in (-1.0, float("nan"), float("inf")):
-        assert calls(one(), max_norm=m)[1] == -2
+        assert clip(one(), max_norm=m) == -2
 
 
 def test_python_checks_before_the_library():
