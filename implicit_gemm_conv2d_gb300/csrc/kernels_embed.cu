@@ -3,7 +3,9 @@
 //
 // The lookup moves T*D values in and out with one multiply each: bound by memory.
 //
-// The gradient is a sum per row over the tokens that name it, in one of two ways:
+// The gradient is a sum per row over the tokens that name it, in one of three ways:
+//
+// Few tokens: one launch, in which a block a token finds the others of its row.
 //
 // A table of few rows: half a warp keeps the sums of the whole table, a window of 32 columns, in its
 // own part of shared memory (two columns a lane) and adds a contiguous share of the tokens to it,
@@ -39,11 +41,14 @@ constexpr int CS_WARPS = CS_THREADS / 32;
 constexpr int TAB_COLS = 32;                               // columns of a table window: two a lane of half a warp
 constexpr int TAB_STEP = 16, TAB_STAGES = 4;               // tokens copied at a time, copies under way and in use
 constexpr int TAB_SMEM = 225 * 1024;
+constexpr int FEW_THREADS = 256, FEW_WARPS = FEW_THREADS / 32;
+constexpr int FEW_TOKENS = 512, FEW_BLOCKS = 4096, FEW_ROWS = 1024;              // tokens at most; rows a filling block takes at most
 constexpr int TAB_MAX_UNITS = 32, TAB_MIN_UNITS = 4;       // half warps with a table each, a block (and SM)
 
 struct EmbedPlan {
+    bool few;             // few tokens: one launch
     bool table;           // sums of the whole table in shared memory
-    int units, blocks;    // copies a block; blocks a window of columns
+    int units, blocks;    // copies a block; blocks a window of columns (few: that fill)
     int smem;
     int cluster;          // blocks of the one-cluster sort, 0: sort by kernels
     int log_items;        // its tokens a thread: 2^log_items
@@ -65,6 +70,22 @@ EmbedPlan embed_plan(const conv_embed_desc_t& e, const DevInfo& d)
         o += (bytes + 255) / 256 * 256;
         return at;
     };
+    const int es = e.dtype == CONV_F32 ? 4 : 2;
+    q.V = 16 / es;
+    while (q.V > 1 && e.D % q.V != 0) q.V /= 2;
+    q.nv = e.D / q.V;
+    // Few tokens: one launch beside three (us): 300 tokens, 696 x 16 fp32 6 / 17, 4410 x 1088 bf16 10 / 18;
+    // 512 tokens, 60187 x 40 bf16 10 / 19, 20000 x 1024 fp32 (82 MB to write) 25 / 26.  Every block reads
+    // all names: at 1024 tokens 20000 x 1024 takes 28 us either way.
+    if (e.T <= FEW_TOKENS) {
+        q.wins = ceil_div(q.nv, 32);
+        q.cols = ceil_div(q.nv, q.wins);
+        q.blocks = int(std::max<int64_t>(ceil_div(e.V, FEW_ROWS), std::min<int64_t>(e.V, 2 * d.sms)));
+        if (e.T * q.wins <= FEW_BLOCKS) {
+            q.few = true;
+            return q;
+        }
+    }
     // Whole-table sums where the tokens outnumber by far the rows that every copy has to add up,
     // and an SM holds a few copies, whose reads ahead keep it busy.  Measured (Zipf tokens, us, whole
     // table against sort): 1540096 x 32 values, 128 rows, fp32 58 / 91; 60000 x 250 x 32 27 / 29;
@@ -93,10 +114,6 @@ EmbedPlan embed_plan(const conv_embed_desc_t& e, const DevInfo& d)
         while (e.T > (int64_t(q.cluster) * CS_THREADS << q.log_items)) ++q.log_items;
     }
     q.tiles = int((e.T + SORT_TILE - 1) / SORT_TILE);
-    const int es = e.dtype == CONV_F32 ? 4 : 2;
-    q.V = 16 / es;
-    while (q.V > 1 && e.D % q.V != 0) q.V /= 2;
-    q.nv = e.D / q.V;
     q.wins = ceil_div(q.nv, SUM_THREADS);
     q.cols = ceil_div(q.nv, q.wins);
     // Chunks: long, so that few runs are cut, while the groups fill the SMs once.
@@ -123,7 +140,9 @@ template <typename I> __device__ __forceinline__ int token_row(const I* idx, int
     return i >= 0 && i < V && i != padding ? int(i) : -1;
 }
 
-// A block takes `tokens` consecutive tokens, its threads their vectors in order.
+// A block takes `tokens` consecutive tokens, its threads their vectors in order.  1540096 tokens,
+// 128 x 32 bf16: 20 us, 5.1 TB/s of names in and values out, 76% of the measured copy's; 752
+// tokens: 4 us, a launch.  Bound by memory (the table's rows come from L1 and L2).
 template <typename T, typename I, int V>
 __global__ void __launch_bounds__(256) embed_fwd_kernel(int64_t n, int rows, int padding, FastDivmod nv, int tokens,
                                                         float scale, const I* idx, const T* table, T* y)
@@ -154,7 +173,104 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(int64_t n, int rows, int
     }
 }
 
+// ---- few tokens --------------------------------------------------------------------------------
+// One launch.  The first `fill` blocks write zeros to the rows that no token names.  Block (token,
+// window) after those: looks for the other tokens of its token's row; the row's first token sums them
+// all, groups of `cols` threads taking equal parts of them in order, the parts added in order.  6 to 12
+// us for up to 512 tokens: a launch, the names, and a few rounds of reads.
+template <typename T, typename I, int V>
+__global__ void __launch_bounds__(FEW_THREADS) embed_few(int n, int rows, int padding, int D, int cols, int wins,
+                                                         int fill, float scale, const I* idx, const T* dy, T* dtable)
+{
+    constexpr int U = 4;
+    __shared__ __align__(16) float sm[FEW_THREADS * V];
+    __shared__ int found[FEW_TOKENS], list[FEW_TOKENS], counts[FEW_WARPS];
+    const int w = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
+    tc::grid_dep_wait();
+    if (int(blockIdx.x) < fill) {
+        unsigned char* named = reinterpret_cast<unsigned char*>(sm);
+        static_assert(FEW_ROWS <= int(sizeof(float)) * FEW_THREADS, "a byte a row");
+        const int64_t f = blockIdx.x;
+        const int r0 = int(f * rows / fill), cnt = int((f + 1) * rows / fill) - r0;
+        for (int r = threadIdx.x; r < cnt; r += FEW_THREADS) named[r] = 0;
+        __syncthreads();
+        for (int t = threadIdx.x; t < n; t += FEW_THREADS) {
+            const int r = token_row(idx, t, rows, padding) - r0;
+            if (r >= 0 && r < cnt) named[r] = 1;
+        }
+        __syncthreads();
+        Vec<T, V> zero;
+        zero.zero();
+        for (int r = w; r < cnt; r += FEW_WARPS)
+            if (!named[r])
+                for (int c = lane * V; c < D; c += 32 * V) zero.store(dtable + int64_t(r0 + r) * D + c);
+        return;
+    }
+    const int t = (int(blockIdx.x) - fill) / wins, win = int(blockIdx.x) - fill - t * wins;
+    const int row = token_row(idx, t, rows, padding);
+    if (row < 0) return;
+    // the row's tokens: each warp those of its share, then all in order
+    const int share = (n + FEW_THREADS - 1) / FEW_THREADS * 32, t0 = w * share;
+    int mine = 0;
+    for (int i = t0; i < min(n, t0 + share); i += 32) {
+        const bool is = i + lane < n && token_row(idx, i + lane, rows, padding) == row;
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, is);
+        if (is) found[t0 + mine + __popc(m & ((1u << lane) - 1))] = i + lane;
+        mine += __popc(m);
+    }
+    if (lane == 0) counts[w] = mine;
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int i = 0; i < FEW_WARPS; ++i) {
+        before += i < w ? counts[i] : 0;
+        total += counts[i];
+    }
+    for (int i = lane; i < mine; i += 32) list[before + i] = found[t0 + i];
+    __syncthreads();
+    if (list[0] != t) return;  // an earlier token's block sums the row
+    const int groups = FEW_THREADS / cols, g = int(threadIdx.x) / cols, col = int(threadIdx.x) - g * cols;
+    const int c = (win * cols + col) * V;
+    if (g < groups) {
+        float acc[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = 0.f;
+        const int i1 = total * (g + 1) / groups;
+        if (c < D)
+            for (int i = total * g / groups; i < i1; i += U) {
+                Vec<T, V> v[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (i + u < i1) v[u].load(dy + int64_t(list[i + u]) * D + c);
+                    else v[u].zero();
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int k = 0; k < V; ++k) acc[k] += v[u].get(k);
+            }
+#pragma unroll
+        for (int k = 0; k < V; ++k) sm[k * FEW_THREADS + threadIdx.x] = acc[k];
+    }
+    __syncthreads();
+    if (g == 0 && c < D) {
+        float f[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) f[k] = sm[k * FEW_THREADS + col];
+        for (int j = 1; j < groups; ++j)
+#pragma unroll
+            for (int k = 0; k < V; ++k) f[k] += sm[k * FEW_THREADS + j * cols + col];
+        Vec<T, V> v;
+#pragma unroll
+        for (int k = 0; k < V; ++k) f[k] *= scale;
+        v.set(f);
+        v.store(dtable + int64_t(row) * D + c);
+    }
+}
+
 // ---- sort ------------------------------------------------------------------------------------
+// Three launches a digit for more tokens than a cluster holds: 887914 tokens, 13 bits in two digits:
+// 41 us, each pass reading and writing keys and places once (count 7, scan 4, scatter 10 us).
 // Counts of each digit in each tile: counts[bin][tile].
 template <typename I>
 __global__ void __launch_bounds__(SORT_THREADS) sort_count(int n, int rows, int padding, const I* idx,
@@ -334,7 +450,9 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_scatter(int n, int rows, in
 // up to CS_TOKENS a block; the other blocks write zeros to dtable meanwhile.  A pass ranks the
 // tokens of a digit as sort_scatter does (16 bits hold a warp's counts), the blocks read each
 // other's counts of each digit, and the tokens, put in the digit's order in the block first, go in
-// runs to their places in the next order, in whichever block those lie.
+// runs to their places in the next order, in whichever block those lie.  16384 tokens, 50021 rows of
+// 1024 bf16: 18 us, what the 102 MB of zeros take; the gradient as a whole takes 43 us so and 66
+// with a launch a step (65536 tokens, 50021 x 256: 56 and 63; 512 tokens, 1000 x 128: 19 and 23).
 template <typename I>
 __global__ void __launch_bounds__(CS_THREADS, 1)
 sort_cluster(int n, int rows, int padding, int S, int log_items, int passes, int digit_bits, const I* idx,
@@ -476,6 +594,8 @@ sort_cluster(int n, int rows, int padding, int S, int log_items, int passes, int
 // the tokens that name none) and a ring of TAB_STAGES tiles of TAB_STEP tokens.  Four tokens are
 // added at a time: their table rows are read together, and where a row comes again among the four
 // the sum so far takes the place of what was read.
+// 1540096 tokens, 128 x 32 fp32: 42 us and 5 for the copies' sum, 4.3 TB/s, 64% of the measured
+// copy's.  Bound by shared memory's latency: a step's sums wait for the step's before.
 template <int BYTES> __device__ __forceinline__ void tab_copy(uint32_t dst, const void* src)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
@@ -600,6 +720,9 @@ __global__ void __launch_bounds__(256) embed_table_sum(int64_t values, int block
 // thread one vector of the row.  A run that goes on in the next chunk and ends there is summed to
 // its end.  A longer one leaves partial sums: part[chunk][1] where it begins, part[chunk][0] in
 // each chunk that it enters from before.
+// 16384 tokens, rows of 1024 bf16: 13 us, 2.6 TB/s, bound by instructions (0.66 issued a slot: adds
+// and conversions at a few tokens a chunk); 887914 tokens, rows of 72 fp32: 74 us, 3.5 TB/s, by the
+// latency of rows that lie anywhere.
 struct ChunkRuns {
     bool skip;       // the run that enters from before is another group's
     bool head;       // it is a long one: its part of this chunk is a partial sum
@@ -713,7 +836,8 @@ template <int Q> __device__ __forceinline__ void put(float* to, const float* fro
 }
 
 // The long runs: a block looks at FIX_CHUNKS chunks, and for each that a long run begins in adds
-// the run's partials, lanes taking chunks round robin and then the lanes in order.
+// the run's partials, lanes taking chunks round robin and then the lanes in order.  A few
+// microseconds of latency: the ends of the runs are looked up while the sums still run.
 template <typename T, int V>
 __global__ void __launch_bounds__(FIX_THREADS) embed_fix(int n, int rows, int D, int cols, int wins, int chunk,
                                                          int chunks, float scale, const uint32_t* keys, T* dtable,
@@ -888,6 +1012,23 @@ cudaError_t table_v(const conv_embed_desc_t& e, const EmbedPlan& q, const I* idx
 }
 
 template <typename T, typename I>
+cudaError_t few_t(const conv_embed_desc_t& e, const EmbedPlan& q, const I* idx, const T* dy, T* dtable, cudaStream_t s)
+{
+    const dim3 grid(unsigned(e.T * q.wins + q.blocks));
+    cudaError_t r = cudaSuccess;
+#define EMB_CALL(V_)                                                                                              \
+    r = launch_ex(embed_few<T, I, V_>, grid, dim3(FEW_THREADS), 0, s, 1, true, int(e.T), e.V, e.padding_idx, e.D, \
+                  q.cols, q.wins, q.blocks, e.scale, idx, dy, dtable)
+    if (q.V == 8) {
+        if constexpr (sizeof(T) == 2) EMB_CALL(8);
+    } else if (q.V == 4) EMB_CALL(4);
+    else if (q.V == 2) EMB_CALL(2);
+    else EMB_CALL(1);
+#undef EMB_CALL
+    return r != cudaSuccess ? r : cudaGetLastError();
+}
+
+template <typename T, typename I>
 cudaError_t table_t(const conv_embed_desc_t& e, const EmbedPlan& q, const I* idx, const T* dy, T* dtable, float* part,
                     cudaStream_t s)
 {
@@ -956,6 +1097,14 @@ cudaError_t run_embed_bwd(const conv_embed_desc_t& e, const DevInfo& d, const vo
     if (e.T == 0) return cudaMemsetAsync(dtable, 0, size_t(e.V) * e.D * (e.dtype == CONV_F32 ? 4 : 2), s);
     const EmbedPlan q = embed_plan(e, d);
     float* part = reinterpret_cast<float*>(ws + q.off_part);
+    if (q.few) {
+        if (e.dtype == CONV_F32)
+            return e.index_dtype == CONV_INDEX_I32
+                       ? few_t(e, q, (const int32_t*)idx, (const float*)dy, (float*)dtable, s)
+                       : few_t(e, q, (const int64_t*)idx, (const float*)dy, (float*)dtable, s);
+        return e.index_dtype == CONV_INDEX_I32 ? few_t(e, q, (const int32_t*)idx, (const H*)dy, (H*)dtable, s)
+                                               : few_t(e, q, (const int64_t*)idx, (const H*)dy, (H*)dtable, s);
+    }
     if (q.table) {
         if (e.dtype == CONV_F32)
             return e.index_dtype == CONV_INDEX_I32

@@ -2,14 +2,14 @@
 //   mean = sum x / M,  rstd = 1 / sqrt(sum (x - mean)^2 / M + eps),
 //   y = act((x - mean) * rstd * gamma[c] + beta[c]).
 //
-// About ten operations a value against 2 (bf16) or 4 bytes in and out: bound by memory, so what
-// counts is to read x once.  A group that fits a team of lanes is held in its registers: the
+// About ten operations a value against 2 (bf16) or 4 bytes in and out: bound by memory in fp32, so
+// what counts is to read x once.  A group that fits a team of lanes is held in its registers: the
 // sum, then the squares about the mean, then the result, one read and one write.  Larger groups
-// are held by a thread-block cluster (kernels_gn_cluster.cu).  Groups beyond that
-// are cut into pieces whose (mean, sum of squares about it) partials are combined by Chan,
-// Golub & LeVeque's update ("Updating formulae and a pairwise algorithm for computing sample
-// variances", 1979), and a second pass applies them.  No path subtracts a squared mean from a
-// mean of squares, so a large common offset costs no digits.
+// are held by a thread-block cluster (kernels_gn_cluster.cu).  Groups beyond that are read twice:
+// channels last by row tiles (kernels_gn_nhwc.cu), NCHW here by pieces of rows whose (mean, sum of
+// squares about it) partials are combined by Chan, Golub & LeVeque's update ("Updating formulae
+// and a pairwise algorithm for computing sample variances", 1979).  No path subtracts a squared
+// mean from a mean of squares, so a large common offset costs no digits.
 #include "gn_common.cuh"
 
 namespace igc {
@@ -78,6 +78,11 @@ GnPieces gn_pieces(const GnParams& p, int dt, const DevInfo& d)
 namespace {
 
 // ---- small groups ----------------------------------------------------------------------------
+// 32768 x 128 x 12, 16 groups, bf16, SiLU: 45 us, 4.6 TB/s, 68% of the measured copy's; bound by
+// instructions (22 a value, of which the activation takes 4, at 0.71 an issue slot), as two
+// samples read ahead instead of one change nothing.  fp32, 8192 x 128 x 12: 22 us, 4.5 TB/s.
+// 256 x 128 x 2, 8 groups: 5 to 6 us, a launch.  Groups of up to 384 (bf16: 512) values; beside a
+// cluster's (us): 1024 x 256 x 36, 32 groups, 17 / 25 bf16 and 19 / 23 fp32.
 template <typename T, int V, int K>
 __global__ void __launch_bounds__(GN_THREADS, 4)
 gn_team_fwd(const GnParams p, const GnTeam q, const T* x, const T* gamma, const T* beta, T* y, float* mean_out,
@@ -161,7 +166,9 @@ gn_team_fwd(const GnParams p, const GnTeam q, const T* x, const T* gamma, const 
     }
 }
 
-// ---- large groups ----------------------------------------------------------------------------
+// ---- large groups, NCHW ------------------------------------------------------------------------
+// Two passes over x, the second out of L2 as far as it holds: 4 x 128 x 16384, 8 groups, SiLU: 16 us
+// in bf16 and 25 in fp32 (2.1 and 2.8 TB/s of one read and one write); three launches.
 // A running (mean, M2) over n values, and the merge of another (n2, mean2, m22).
 __device__ __forceinline__ void chan_merge(float& n, float& mean, float& m2, float n2, float mean2, float m22)
 {

@@ -76,8 +76,8 @@ int conv_gn_bwd(const conv_gn_desc_t* desc, const void* x, const void* dy, const
  * idx: (T), int32 or int64; table, dtable: (V, D); y, dy: (T, D).
  * A token equal to padding_idx, or outside [0, V), names no row: its y is zero and it adds to
  * no gradient (no row is read for it).  padding_idx < 0: no padding row.
- * The gradient adds a row's tokens in an order that the sizes fix (by parts of consecutive tokens,
- * then the parts), and rows that no token names are zeros. */
+ * The gradient adds a row's tokens in an order that the sizes and idx fix (by parts of consecutive
+ * tokens, then the parts), and rows that no token names are zeros. */
 typedef enum { CONV_INDEX_I32 = 0, CONV_INDEX_I64 = 1 } conv_index_t;
 
 typedef struct {
