@@ -160,3 +160,42 @@ def test_small_workspace_refused():
         with pytest.raises(train.binding.ConvError) as e:
             train.conv_embed_bwd(desc, idx, dy, dt, ws)
         assert e.value.status == -5
+
+
+# Around the one-launch path's limits: 512 tokens, 4096 blocks of a token and 32 vectors (513 x 40,
+# 128 x 8192 in fp32 and 512 x 257 are beyond them), tables of many rows a filling block, widths that
+# end inside a window.
+FEW = {
+    "most": (512, 60187, 40, "zipf"),
+    "most_plus": (513, 60187, 40, "zipf"),
+    "most_one_row": (512, 1, 136, "equal"),
+    "most_equal": (512, 90, 1032, "equal"),
+    "odd_width": (511, 400001, 3, "uniform"),
+    "many_rows": (40, 900000, 5, "uniform"),
+    "windows": (300, 4410, 1088, "zipf"),
+    "windows_most": (128, 700, 8192, "zipf"),
+    "windows_odd": (455, 100, 257, "zipf"),
+    "windows_odd_plus": (512, 512, 257, "permutation"),
+    "two": (2, 3, 33, "equal"),
+    "warp_shares": (257, 31, 64, "uniform"),
+}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("index", ["int32", "int64"])
+@pytest.mark.parametrize("case", list(FEW))
+def test_few_tokens(case, index, dtype):
+    T, V, D, dist = FEW[case]
+    rng = np.random.default_rng(9)
+    idx = tokens(T, V, dist, rng)
+    if T > 40 and V > 3:
+        idx[[3, 20, T - 1]] = [-1, V, V // 3]
+    didx = torch.from_numpy(idx).to("cuda", getattr(torch, index))
+    dy = to_dev(rng.normal(size=(T, D)), dtype)
+    padding = V // 3 if V > 3 else -1
+    dt = train.embed_bwd(didx, dy, V, 1.25, padding_idx=padding)
+    check_bwd(dt, idx, dy, V, 1.25, padding, dtype, f"{case} {index} {dtype}")
+    rows = np.zeros(V, dtype=bool)
+    rows[[i for i in idx if 0 <= i < V and i != padding]] = True
+    assert not dt[torch.from_numpy(~rows).cuda()].any()
+    assert torch.equal(dt, train.embed_bwd(didx, dy, V, 1.25, padding_idx=padding))
