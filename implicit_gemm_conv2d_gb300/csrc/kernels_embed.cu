@@ -34,7 +34,7 @@ constexpr int SORT_MAX_BITS = 9;                           // digit
 constexpr int SORT_MAX_BINS = 1 << SORT_MAX_BITS;
 constexpr int SUM_THREADS = 256, SUM_BLOCKS_SM = 3;
 constexpr int FIX_THREADS = 1024;
-constexpr int FIX_CHUNKS = 16;                             // chunks a block of the last kernel looks at
+constexpr int FIX_MIN = 16, FIX_MAX = 256;                 // chunks a block of the last kernel looks at
 constexpr int CS_THREADS = 1024, CS_ITEMS = 8;             // sort by one cluster: a block's threads, tokens a thread
 constexpr int CS_TOKENS = CS_THREADS * CS_ITEMS;
 constexpr int CS_WARPS = CS_THREADS / 32;
@@ -826,97 +826,87 @@ __global__ void __launch_bounds__(SUM_THREADS, SUM_BLOCKS_SM) embed_sum(int n, i
     flush(run.tail);
 }
 
-// Q floats in one access.
-template <int Q> __device__ __forceinline__ void put(float* to, const float* from)
-{
-    if constexpr (Q == 4) *reinterpret_cast<float4*>(to) = *reinterpret_cast<const float4*>(from);
-    else
-#pragma unroll
-        for (int i = 0; i < Q; ++i) to[i] = from[i];
-}
-
-// The long runs: a block looks at FIX_CHUNKS chunks, and for each that a long run begins in adds
-// the run's partials, lanes taking chunks round robin and then the lanes in order.  A few
-// microseconds of latency: the ends of the runs are looked up while the sums still run.
+// The long runs: a block looks at `look` chunks, and for each that a long run begins in adds the
+// run's partials, V <= 4 values a thread: lanes take chunks round robin while those go on with the
+// run, then the lanes are added in order.  So many chunks that the blocks are resident at once.  A
+// chain of latencies (a run's keys and partials are read together, four of a lane's at a time);
+// where its blocks find room the first of them pass while the sums still run.
 template <typename T, int V>
 __global__ void __launch_bounds__(FIX_THREADS) embed_fix(int n, int rows, int D, int cols, int wins, int chunk,
-                                                         int chunks, float scale, const uint32_t* keys, T* dtable,
-                                                         const float* part)
+                                                         int chunks, int look, float scale, const uint32_t* keys,
+                                                         T* dtable, const float* part)
 {
-    constexpr int Q = V < 4 ? V : 4;   // a lane's values in shared memory: Q together, so that no bank is met twice
-    __shared__ __align__(16) float sm[V / Q][FIX_THREADS][Q];
-    __shared__ int reach[FIX_CHUNKS];  // further chunks of the run that begins here, 0: none
-    __shared__ uint32_t name[FIX_CHUNKS];
-    const int win = int(blockIdx.x % wins), ch0 = int(blockIdx.x / wins) * FIX_CHUNKS;
+    constexpr int U = 4;
+    __shared__ __align__(16) float sm[FIX_THREADS][V];
+    __shared__ int begins[FIX_MAX];  // chunk that a long run begins in
+    __shared__ uint32_t name[FIX_MAX], sums[FIX_THREADS / 32];
+    const int win = int(blockIdx.x % wins), ch0 = int(blockIdx.x / wins) * look;
     const int lanes = FIX_THREADS / cols, lane = int(threadIdx.x) / cols, col = int(threadIdx.x) - lane * cols;
     const int c = (win * cols + col) * V;
     // The keys are the sort's: every block of the kernel before has waited for them, and this one
     // was launched after that.  Only the partials have to be waited for.
-    static_assert(FIX_THREADS / 32 >= FIX_CHUNKS, "a warp a chunk");
-    if (int(threadIdx.x) < FIX_CHUNKS * 32) {
-        const int ch = ch0 + int(threadIdx.x >> 5), wl = int(threadIdx.x & 31);
-        int cnt = 0;
+    static_assert(FIX_THREADS >= FIX_MAX, "a thread a chunk");
+    int active;
+    {
+        const int ch = ch0 + int(threadIdx.x);
         uint32_t key = 0;
-        if (ch < chunks) {
-            const int i0 = ch * chunk, i1 = min(n, i0 + chunk);
+        bool is = false;
+        if (int(threadIdx.x) < look && ch < chunks) {
+            const int i0 = ch * chunk, i1 = min(n, i0 + chunk), i2 = min(n, i1 + chunk);
+            // one round of reads: a run that goes on beyond the next chunk, and began in this one
+            const uint32_t before = i0 > 0 ? keys[i0 - 1] : 0xFFFFFFFFu, first = keys[i0];
+            const uint32_t after = i1 < n ? keys[i1] : 0xFFFFFFFFu, beyond = i2 < n ? keys[i2] : 0xFFFFFFFFu;
             key = keys[i1 - 1];
-            if (key < uint32_t(rows) && ChunkRuns(keys, n, chunk, i0, i1).tail) {
-                // the last chunk that the run reaches (whose first key is the run's), 32 probes at a time
-                int lo = ch + 1, hi = chunks;  // lo: reached; hi: not
-                while (hi - lo > 1) {
-                    const int step = (hi - lo + 31) / 32, at = lo + (wl + 1) * step;
-                    const uint32_t in = __ballot_sync(0xFFFFFFFFu, at < hi && keys[int64_t(at) * chunk] == key);
-                    const int got = __popc(in);  // the first `got` probes
-                    hi = min(hi, lo + (got + 1) * step);
-                    lo += got * step;
-                }
-                cnt = lo - ch;
-            }
+            is = key < uint32_t(rows) && after == key && beyond == key && !(before == first && first == key);
         }
-        if (wl == 0) {
-            reach[threadIdx.x >> 5] = cnt;
-            name[threadIdx.x >> 5] = key;
+        const int at = int(block_scan(is, sums));
+        if (is) {
+            begins[at - 1] = ch;
+            name[at - 1] = key;
         }
+        active = __syncthreads_count(is);
     }
-    __syncthreads();
-    // the block's long runs side by side, as many as it has lanes, each with `per` lanes
-    int active = 0;
-    for (int k = 0; k < FIX_CHUNKS; ++k) active += reach[k] > 0;
     tc::grid_dep_wait();
     if (active == 0) return;
+    // the block's long runs side by side, as many as it has lanes, each with `per` lanes
     const int per = max(1, min(32, lanes / active)), slots = lanes / per, slot = lane / per, sub = lane - slot * per;
     for (int done = 0; done < active; done += slots) {
-        int k = -1;  // the chunk of this lane's run
-        if (slot < slots && done + slot < active) {
-            int left = done + slot;
-            while (reach[++k] == 0 || left-- > 0) {}
-        }
-        __align__(16) float acc[V];
+        const int k = slot < slots && done + slot < active ? done + slot : -1;  // this lane's run
+        float acc[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = 0.f;
-        const int ch = ch0 + k;
         if (k >= 0 && c < D) {
-            const int cnt = reach[k];
-#pragma unroll 8
-            for (int j = sub; j <= cnt; j += per) {
-                const float* s = part + (int64_t(ch + j) * 2 + (j == 0 ? 1 : 0)) * D + c;
+            const int ch = begins[k];
+            const uint32_t key = name[k];
+            bool on = true;
+            for (int j = sub; on; j += per * U) {
+                uint32_t q[U];
+                Vec<float, V> v[U];
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] += s[i];
+                for (int u = 0; u < U; ++u) {
+                    const int at = ch + j + u * per;
+                    const bool in = at < chunks;
+                    q[u] = !in ? 0xFFFFFFFFu : at == ch ? key : keys[int64_t(at) * chunk];
+                    if (in) v[u].load(part + (int64_t(at) * 2 + (at == ch ? 1 : 0)) * D + c);
+                    else v[u].zero();
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    on = q[u] == key;  // beyond the run a partial is another's, or nothing
+                    if (on)
+#pragma unroll
+                        for (int i = 0; i < V; ++i) acc[i] += v[u].get(i);
+                }
             }
         }
         if (lane < lanes)
 #pragma unroll
-            for (int j = 0; j < V / Q; ++j) put<Q>(sm[j][lane * cols + col], acc + j * Q);
+            for (int i = 0; i < V; ++i) sm[lane * cols + col][i] = acc[i];
         __syncthreads();
         if (k >= 0 && sub == 0 && c < D) {
             for (int l = 1; l < per; ++l)
 #pragma unroll
-                for (int j = 0; j < V / Q; ++j) {
-                    __align__(16) float e[Q];
-                    put<Q>(e, sm[j][(lane + l) * cols + col]);
-#pragma unroll
-                    for (int i = 0; i < Q; ++i) acc[j * Q + i] += e[i];
-                }
+                for (int i = 0; i < V; ++i) acc[i] += sm[(lane + l) * cols + col][i];
             Vec<T, V> v;
 #pragma unroll
             for (int i = 0; i < V; ++i) acc[i] *= scale;
@@ -1046,21 +1036,24 @@ cudaError_t table_t(const conv_embed_desc_t& e, const EmbedPlan& q, const I* idx
 }
 
 template <typename T>
-cudaError_t sum_t(const conv_embed_desc_t& e, const EmbedPlan& q, const uint32_t* keys, const uint32_t* pos,
-                  const T* dy, T* dtable, float* part, cudaStream_t s)
+cudaError_t sum_t(const conv_embed_desc_t& e, const EmbedPlan& q, const DevInfo& d, const uint32_t* keys,
+                  const uint32_t* pos, const T* dy, T* dtable, float* part, cudaStream_t s)
 {
     const int n = int(e.T), per = SUM_THREADS / q.cols;
     const dim3 sgrid(unsigned(ceil_div(q.chunks, per)) * unsigned(q.wins));
-    const dim3 fgrid(unsigned(ceil_div(q.chunks, FIX_CHUNKS)) * unsigned(q.wins));
+    const int look = std::min(FIX_MAX, std::max(FIX_MIN, ceil_div(q.chunks, std::max(1, d.sms / q.wins))));
+    const dim3 fgrid(unsigned(ceil_div(q.chunks, look)) * unsigned(q.wins));
     cudaError_t r = cudaSuccess;
     const float* cpart = part;
 #define EMB_CALL(V_)                                                                                             \
     do {                                                                                                         \
         r = launch_ex(embed_sum<T, V_>, sgrid, dim3(SUM_THREADS), 0, s, 1, true, n, e.V, e.D, q.cols, q.wins,    \
                       q.chunk, q.chunks, e.scale, keys, pos, dy, dtable, part);                                  \
-        if (r == cudaSuccess)                                                                                    \
-            r = launch_ex(embed_fix<T, V_>, fgrid, dim3(FIX_THREADS), 0, s, 1, true, n, e.V, e.D, q.cols, q.wins,\
-                          q.chunk, q.chunks, e.scale, keys, dtable, cpart);                                      \
+        if (r == cudaSuccess) {                                                                                  \
+            constexpr int VF = V_ < 4 ? V_ : 4;                                                                  \
+            r = launch_ex(embed_fix<T, VF>, fgrid, dim3(FIX_THREADS), 0, s, 1, true, n, e.V, e.D,                \
+                          q.cols * (V_ / VF), q.wins, q.chunk, q.chunks, look, e.scale, keys, dtable, cpart);    \
+        }                                                                                                        \
     } while (0)
     if (q.V == 8) {
         if constexpr (sizeof(T) == 2) EMB_CALL(8);
@@ -1120,8 +1113,8 @@ cudaError_t run_embed_bwd(const conv_embed_desc_t& e, const DevInfo& d, const vo
     if (r != cudaSuccess) return r;
     const uint32_t* keys = reinterpret_cast<const uint32_t*>(ws + q.off_keys[where]);
     const uint32_t* pos = reinterpret_cast<const uint32_t*>(ws + q.off_pos[where]);
-    return e.dtype == CONV_F32 ? sum_t(e, q, keys, pos, (const float*)dy, (float*)dtable, part, s)
-                               : sum_t(e, q, keys, pos, (const H*)dy, (H*)dtable, part, s);
+    return e.dtype == CONV_F32 ? sum_t(e, q, d, keys, pos, (const float*)dy, (float*)dtable, part, s)
+                               : sum_t(e, q, d, keys, pos, (const H*)dy, (H*)dtable, part, s);
 }
 
 }  // namespace igc
