@@ -451,8 +451,8 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_scatter(int n, int rows, in
 // tokens of a digit as sort_scatter does (16 bits hold a warp's counts), the blocks read each
 // other's counts of each digit, and the tokens, put in the digit's order in the block first, go in
 // runs to their places in the next order, in whichever block those lie.  16384 tokens, 50021 rows of
-// 1024 bf16: 18 us, what the 102 MB of zeros take; the gradient as a whole takes 43 us so and 66
-// with a launch a step (65536 tokens, 50021 x 256: 56 and 63; 512 tokens, 1000 x 128: 19 and 23).
+// 1024 bf16: 18 us, what the 102 MB of zeros take; the gradient as a whole takes 24 us less than with
+// three launches a digit (65536 tokens, 50021 x 256: 7 us less; 4096 tokens, 1000 x 128 fp32: 6).
 template <typename I>
 __global__ void __launch_bounds__(CS_THREADS, 1)
 sort_cluster(int n, int rows, int padding, int S, int log_items, int passes, int digit_bits, const I* idx,
