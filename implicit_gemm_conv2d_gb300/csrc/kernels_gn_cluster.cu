@@ -12,15 +12,17 @@
 // results through distributed shared memory, with one cluster barrier.
 //
 // Measured (us; of the rate of the measured copy for one read of each input and one write):
-//   24 x 320 x 72x72 bf16, 32 groups of 10, SiLU, channels last, forward: 55, 43%; NCHW 43, 55%;
-//     fp32 84 and 61.
+//   24 x 320 x 72x72 bf16, 32 groups of 10, SiLU, channels last, forward: 53, 45%; NCHW 41, 58%;
+//     fp32 82 and 61.
 //   12 x 192 x 95x101 bf16, 24 groups of 8, GELU, channels last, backward: 65, 30% (ReLU 53).
 // Bound by latency: an instruction is issued in 0.44 (forward) to 0.49 slots, from 16 to 24 warps an
 // SM.  They wait for the activation's steps (its 2^x and 1/x), for shared memory and, a fifth of
 // the backward's time, at the barriers around a sample's sums.  In bf16 the backward's 48
 // instructions a value (the activation is computed twice) alone would take 28 us.
-// Beside two passes over memory (24 x 320 x 5184, SiLU): forward bf16 43 / 78, channels last 54 / 80,
-// fp32 61 / 98 and 84 / 139; backward bf16 107 / 144 and 107 / 152, fp32 135 / 157 and 188 / 188.
+// Beside two passes over memory (24 x 320 x 5184, SiLU): forward bf16 41 / 78, channels last 53 / 80,
+// fp32 61 / 98 and 82 / 139; backward bf16 102 / 144 and 108 / 152, fp32 141 / 157 and 149 / 188.
+#include <atomic>
+
 #include "gn_common.cuh"
 
 namespace igc {
@@ -28,11 +30,11 @@ namespace igc {
 namespace {
 
 constexpr int GC_MAX_CG = 2048;            // channels of a group (their gammas sit in shared memory)
-constexpr int GC_SMEM = 110 * 1024;        // of a block: two share an SM, or each waits with its SM
+constexpr int GC_SMEM = 113 * 1024;        // of a block: two share an SM, or each waits with its SM
 constexpr int GC_THREADS = 512;
 constexpr int GC_ROW_THREADS = 384;        // NHWC: 80 registers a thread, 64 spill (95x101 backward 75 -> 65 us)
-constexpr int GC_SPAN_THREADS = 256;       // NHWC, vectors in two groups: more registers a thread
 constexpr int GC_WARPS = GC_THREADS / 32;
+constexpr int GC_SLOTS = 128;              // of a thread: its one-pass statistics lose up to log2 of that in bits
 constexpr int GC_FWD_BYTES = 256, GC_BWD_BYTES = 96;  // of x a thread holds, at most where the block can grow
 
 }  // namespace
@@ -43,6 +45,45 @@ static int gc_extra(const GnCluster& q, bool bwd)
     if (q.nhwc) return 16 * q.threads + 16 * GC_WARPS + 8 * q.W + 32 * q.groups + (bwd ? 8 * q.threads : 0);
     return 4 * 2 * (q.Cg + 1) + 32 * GC_WARPS + 64 + (bwd ? 8 * (q.K * q.threads + q.Cg + 1) : 0);
 }
+
+namespace {
+
+__global__ void gc_probe() {}
+
+// Clusters of S blocks that the device holds at once with b blocks an SM (clusters lie within a
+// GPC, whose SMs do not divide evenly: 36 and not 38 of eight blocks, two an SM).  Asked for once a
+// device; without one, what the SMs alone allow.
+int gc_resident(const DevInfo& d, int S, int log_s, int b)
+{
+    constexpr int DEVICES = 16, BLOCKS = 32;
+    static std::atomic<int> known[DEVICES][4][BLOCKS + 1];
+    const int most = std::max(1, d.sms * b / S);
+    if (S == 1 || b > BLOCKS || d.device < 0 || d.device >= DEVICES) return most;
+    std::atomic<int>& k = known[d.device][log_s][b];
+    int n = k.load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaLaunchConfig_t c = {};
+        cudaLaunchAttribute a;
+        a.id = cudaLaunchAttributeClusterDimension;
+        a.val.clusterDim.x = S;
+        a.val.clusterDim.y = a.val.clusterDim.z = 1;
+        c.gridDim = dim3(S);
+        c.blockDim = dim3(32);
+        c.dynamicSmemBytes = size_t(227 * 1024) / b - 1024;
+        c.attrs = &a;
+        c.numAttrs = 1;
+        if (cudaFuncSetAttribute(gc_probe, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 1024) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, gc_probe, &c) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            n = most;
+        }
+        k.store(std::min(n, most), std::memory_order_relaxed);
+        n = std::min(n, most);
+    }
+    return n;
+}
+
+}  // namespace
 
 GnCluster gn_cluster(const GnParams& p, int dt, const DevInfo& d, bool bwd)
 {
@@ -67,7 +108,7 @@ GnCluster gn_cluster(const GnParams& p, int dt, const DevInfo& d, bool bwd)
     while (lcm % q.V != 0) lcm += p.Cg;
     // NHWC: windows of whole vectors and whole groups, 64 bytes of a row (two sectors) or less.
     const int widest = nhwc ? std::max(1, std::min(ceil_div(64, lcm * es), ceil_div(p.C, lcm))) : 1;
-    const int most_threads = !nhwc ? GC_THREADS : q.one ? GC_ROW_THREADS : GC_SPAN_THREADS;
+    const int most_threads = nhwc ? GC_ROW_THREADS : GC_THREADS;
     for (int m = widest; m >= 1; --m) {
         int64_t vecs;  // of the unit
         if (nhwc) {
@@ -87,45 +128,52 @@ GnCluster gn_cluster(const GnParams& p, int dt, const DevInfo& d, bool bwd)
         const int most = int(std::min<int64_t>(kMaxCluster, nhwc ? p.P : vecs / 32 + 1));
         for (int S = 1, log = 0; S <= most; S *= 2, ++log) {
             const int64_t per = (vecs + S - 1) / S;
-            // Threads: so many that each holds about GC_*_BYTES; of those up to twice as many,
-            // the count that leaves the fewest slots empty.
-            auto slots = [&](int T) {
-                const int lanes = nhwc ? T / q.cols : 1;
-                return nhwc ? (int64_t(ceil_div(p.P, S)) + lanes - 1) / lanes : (per + T - 1) / T;
-            };
-            const int bytes = bwd ? GC_BWD_BYTES : GC_FWD_BYTES;
-            int lo = nhwc ? round_up(q.cols, 32) : 32;
-            lo = int(std::min<int64_t>(most_threads, std::max<int64_t>(lo, (per * vb + bytes * 32 - 1) / (bytes * 32) * 32)));
-            int T = lo;
-            for (int t = lo + 32; t <= std::min(most_threads, 2 * lo); t += 32)
-                if (slots(t) * t < slots(T) * T) T = t;
-            q.S = S;
-            q.log_s = log;
-            q.threads = T;
-            q.lanes = nhwc ? T / q.cols : 1;
-            const int64_t K = slots(T);
-            if (K * T * vb * tiles > GC_SMEM) continue;
-            q.K = int(K);
-            const int tile = q.K * T * vb * tiles;
-            q.smem = tile + gc_extra(q, bwd);
-            if (q.smem > GC_SMEM) continue;
+            // Threads: about so many that each holds GC_*_BYTES.  Of the counts up to twice that (from
+            // half for large blocks) whose tiles fit, the one with the fewest slots a thread (and two
+            // for what a sample costs besides) for the blocks that an SM holds by registers (80 or 64
+            // a thread) and by shared memory (64 x 1024 x 256, 32 groups, channels last, fp32
+            // backward: 384 threads and two blocks 58 us, 256 and three 47).
+            const int bytes = bwd ? GC_BWD_BYTES : GC_FWD_BYTES, least = nhwc ? round_up(q.cols, 32) : 32;
+            const int about = int(std::min<int64_t>(
+                most_threads, std::max<int64_t>(least, (per * vb + bytes * 32 - 1) / (bytes * 32) * 32)));
+            GnCluster r = {};
+            int by_smem = 0, per_sm = 0;
+            for (int t = std::max(least, about > 128 ? about / 64 * 32 : about); t <= std::min(most_threads, 2 * about); t += 32) {
+                q.lanes = nhwc ? t / q.cols : 1;
+                const int64_t n = nhwc ? (int64_t(ceil_div(p.P, S)) + q.lanes - 1) / q.lanes : (per + t - 1) / t;
+                if (n > GC_SLOTS || n * t * vb * tiles > GC_SMEM) continue;
+                q.threads = t;
+                q.K = int(n);
+                q.smem = q.K * t * vb * tiles + gc_extra(q, bwd);
+                if (q.smem > GC_SMEM) continue;
+                const int by = (227 * 1024) / (q.smem + 1024);
+                const int blocks = std::min(std::max(1, std::min(32, (nhwc ? 768 : 1024) / t)), by);
+                if (per_sm == 0 || (n + 2) * per_sm < int64_t(r.K + 2) * blocks) r = q, per_sm = blocks, by_smem = by;
+            }
+            if (per_sm == 0) continue;
+            r.S = S;
+            r.log_s = log;
             // larger clusters while the SMs are not filled and the blocks still have a few
             // kilobytes each
             if (S * 2 <= most && units * S < 2 * d.sms && per * vb > 4096) continue;
-            // Blocks an SM by registers (64 or 80 a thread) and by shared memory.
-            const int by_regs = std::max(1, std::min(32, (nhwc ? 768 : 1024) / T));
-            const int per_sm = std::min(by_regs, (227 * 1024) / (q.smem + 1024));
-            const int64_t want = std::max<int64_t>(1, int64_t(d.sms) * per_sm / (int64_t(q.wins) * S));
-            q.chunks = int(std::min<int64_t>(p.B, want));
-            q.dm_cols = FastDivmod(uint32_t(std::max(1, q.cols)));
-            q.dm_cg = FastDivmod(uint32_t(p.Cg));
-            q.dm_p = FastDivmod(uint32_t(p.P));
-            q.dm_wins = FastDivmod(uint32_t(q.wins));
-            q.ok = true;
-            return q;
+            // A larger cluster or a narrower window where tiles of half an SM's shared memory leave it
+            // few threads that walk them long (24 x 320 x 5184 bf16, groups of 10, channels last,
+            // backward, us: windows of 40 channels, clusters of eight, 512 threads an SM 135; 20,
+            // four, 576 153; 20, eight, 768 107).
+            if (by_smem <= 2 && r.threads * per_sm < 700 && r.K > 16) {
+                if (S * 2 <= most) continue;
+                if (m > 1) break;
+            }
+            r.chunks = std::max(1, std::min(p.B, gc_resident(d, S, log, per_sm) / q.wins));
+            r.dm_cols = FastDivmod(uint32_t(std::max(1, q.cols)));
+            r.dm_cg = FastDivmod(uint32_t(p.Cg));
+            r.dm_p = FastDivmod(uint32_t(p.P));
+            r.dm_wins = FastDivmod(uint32_t(q.wins));
+            r.ok = true;
+            return r;
         }
     }
-    return q;
+    return GnCluster{};
 }
 
 namespace {
@@ -394,7 +442,7 @@ __device__ __forceinline__ void gc_group_warps(const GnParams& p, const GnCluste
 }
 
 template <typename T, int V, bool ONE>
-__global__ void __launch_bounds__(ONE ? GC_ROW_THREADS : GC_SPAN_THREADS, ONE ? 2 : 3)
+__global__ void __launch_bounds__(GC_ROW_THREADS, 2)
 gn_cluster_fwd_nhwc(const GnParams p, const __grid_constant__ GnCluster q, const T* x, const T* gamma, const T* beta,
                     T* y, float* mean_out, float* rstd_out)
 {
@@ -522,7 +570,7 @@ gn_cluster_fwd_nhwc(const GnParams p, const __grid_constant__ GnCluster q, const
 
 // part: chunks * S rows of (dgamma's, dbeta's) channel sums.
 template <typename T, int V, bool ONE>
-__global__ void __launch_bounds__(ONE ? GC_ROW_THREADS : GC_SPAN_THREADS, ONE ? 2 : 3)
+__global__ void __launch_bounds__(GC_ROW_THREADS, 2)
 gn_cluster_bwd_nhwc(const GnParams p, const __grid_constant__ GnCluster q, const T* x, const T* dy, const T* gamma,
                     const T* beta, const float* mean, const float* rstd, T* dx, float* part)
 {
