@@ -114,8 +114,9 @@ EmbedPlan embed_plan(const conv_embed_desc_t& e, const DevInfo& d)
         while (e.T > (int64_t(q.cluster) * CS_THREADS << q.log_items)) ++q.log_items;
     }
     q.tiles = int((e.T + SORT_TILE - 1) / SORT_TILE);
-    q.wins = ceil_div(q.nv, SUM_THREADS);
-    q.cols = ceil_div(q.nv, q.wins);
+    const int each = ceil_div(q.nv, q.V * es >= 16 ? 1 : q.V * es == 8 ? 2 : 4);  // a thread's vectors: sum_vectors()
+    q.wins = ceil_div(each, SUM_THREADS);
+    q.cols = ceil_div(each, q.wins);
     // Chunks: long, so that few runs are cut, while the groups fill the SMs once.
     const int64_t groups = std::max<int64_t>(1, int64_t(d.sms) * SUM_BLOCKS_SM * (SUM_THREADS / q.cols) / q.wins);
     q.chunk = int(std::min<int64_t>(512, std::max<int64_t>(16, (e.T + groups - 1) / groups)));
@@ -743,46 +744,72 @@ struct ChunkRuns {
     }
 };
 
+// Vectors of a thread: narrow ones (rows that are not a multiple of 16 bytes) share a token's
+// bookkeeping, 16 bytes of a row together (626078 tokens, 184423 rows of 37 fp32, bound by
+// instructions: 74 us with one of 4 bytes, 48 with four).
+template <typename T, int V> constexpr int sum_vectors()
+{
+    return int(sizeof(T)) * V >= 16 ? 1 : int(sizeof(T)) * V == 8 ? 2 : 4;
+}
+
 template <typename T, int V>
 __global__ void __launch_bounds__(SUM_THREADS, SUM_BLOCKS_SM) embed_sum(int n, int rows, int D, int cols, int wins, int chunk,
                                                          int chunks, float scale, const uint32_t* keys,
                                                          const uint32_t* pos, const T* dy, T* dtable, float* part)
 {
-    constexpr int U = 4;
+    constexpr int U = 4, E = sum_vectors<T, V>();
     const int per = SUM_THREADS / cols, sub = int(threadIdx.x) / cols;
     const int win = int(blockIdx.x % wins);
     const int64_t ch = int64_t(blockIdx.x / wins) * per + sub;
-    const int c = (win * cols + int(threadIdx.x) - sub * cols) * V;
+    int c[E];
+    bool in[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        c[e] = ((win * E + e) * cols + int(threadIdx.x) - sub * cols) * V;
+        in[e] = c[e] < D;
+    }
     tc::grid_dep_wait();
     tc::grid_dep_launch();
-    if (sub >= per || ch >= chunks || c >= D) return;
+    if (sub >= per || ch >= chunks || !in[0]) return;
     const int i0 = int(ch) * chunk, i1 = min(n, i0 + chunk);
     const ChunkRuns run(keys, n, chunk, i0, i1);
-    float acc[V];
+    float acc[E][V];
+    auto clear = [&]() {
 #pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] = 0.f;
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+            for (int k = 0; k < V; ++k) acc[e][k] = 0.f;
+    };
+    clear();
     uint32_t cur = keys[i0];
     const uint32_t last = keys[i1 - 1];
     bool head = run.head, skip = run.skip;
     auto flush = [&](bool tail) {
         if (cur >= uint32_t(rows) || skip) return;
         if (head || tail) {
-            float* o = part + (ch * 2 + (head ? 0 : 1)) * D + c;
+            float* o = part + (ch * 2 + (head ? 0 : 1)) * D;
 #pragma unroll
-            for (int k = 0; k < V; ++k) o[k] = acc[k];
+            for (int e = 0; e < E; ++e)
+                if (in[e])
+#pragma unroll
+                    for (int k = 0; k < V; ++k) o[c[e] + k] = acc[e][k];
         } else {
-            float f[V];
+            T* o = dtable + int64_t(cur) * D;
 #pragma unroll
-            for (int k = 0; k < V; ++k) f[k] = acc[k] * scale;
-            Vec<T, V> v;
-            v.set(f);
-            v.store(dtable + int64_t(cur) * D + c);
+            for (int e = 0; e < E; ++e) {
+                float f[V];
+#pragma unroll
+                for (int k = 0; k < V; ++k) f[k] = acc[e][k] * scale;
+                Vec<T, V> v;
+                v.set(f);
+                if (in[e]) v.store(o + c[e]);
+            }
         }
     };
     // Two steps ahead a token's name is read, one step ahead its value, and neither is looked at
     // before its step.  Beyond the chunk only the run at its end counts.
     uint32_t k[U], p[U], kn[U], kc[U];
-    Vec<T, V> v[U], vn[U];
+    Vec<T, V> v[U][E], vn[U][E];
     auto names = [&](int i) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -794,8 +821,12 @@ __global__ void __launch_bounds__(SUM_THREADS, SUM_BLOCKS_SM) embed_sum(int n, i
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             kn[u] = i + u < i1 || k[u] == last ? k[u] : 0xFFFFFFFFu;
-            if (kn[u] < uint32_t(rows)) vn[u].load(dy + int64_t(p[u]) * D + c);
-            else vn[u].zero();
+            const T* from = dy + int64_t(p[u]) * D;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if (in[e] && kn[u] < uint32_t(rows)) vn[u][e].load(from + c[e]);
+                else vn[u][e].zero();
+            }
         }
     };
     names(i0);
@@ -805,7 +836,8 @@ __global__ void __launch_bounds__(SUM_THREADS, SUM_BLOCKS_SM) embed_sum(int n, i
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             kc[u] = kn[u];
-            v[u] = vn[u];
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[u][e] = vn[u][e];
         }
         values(i + U);
         names(i + 2 * U);
@@ -816,11 +848,12 @@ __global__ void __launch_bounds__(SUM_THREADS, SUM_BLOCKS_SM) embed_sum(int n, i
                     flush(false);
                     cur = kc[u];
                     head = skip = false;
-#pragma unroll
-                    for (int j = 0; j < V; ++j) acc[j] = 0.f;
+                    clear();
                 }
 #pragma unroll
-                for (int j = 0; j < V; ++j) acc[j] += v[u].get(j);
+                for (int e = 0; e < E; ++e)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) acc[e][j] += v[u][e].get(j);
             }
     }
     flush(run.tail);
@@ -829,14 +862,14 @@ __global__ void __launch_bounds__(SUM_THREADS, SUM_BLOCKS_SM) embed_sum(int n, i
 // The long runs: a block looks at `look` chunks, and for each that a long run begins in adds the
 // run's partials, V <= 4 values a thread: lanes take chunks round robin while those go on with the
 // run, then the lanes are added in order.  So many chunks that the blocks are resident at once.  A
-// chain of latencies (a run's keys and partials are read together, four of a lane's at a time);
+// chain of latencies (a run's keys and partials are read together, eight of a lane's at a time);
 // where its blocks find room the first of them pass while the sums still run.
 template <typename T, int V>
 __global__ void __launch_bounds__(FIX_THREADS) embed_fix(int n, int rows, int D, int cols, int wins, int chunk,
                                                          int chunks, int look, float scale, const uint32_t* keys,
                                                          T* dtable, const float* part)
 {
-    constexpr int U = 4;
+    constexpr int U = 8;
     __shared__ __align__(16) float sm[FIX_THREADS][V];
     __shared__ int begins[FIX_MAX];  // chunk that a long run begins in
     __shared__ uint32_t name[FIX_MAX], sums[FIX_THREADS / 32];
@@ -1041,8 +1074,10 @@ cudaError_t sum_t(const conv_embed_desc_t& e, const EmbedPlan& q, const DevInfo&
 {
     const int n = int(e.T), per = SUM_THREADS / q.cols;
     const dim3 sgrid(unsigned(ceil_div(q.chunks, per)) * unsigned(q.wins));
-    const int look = std::min(FIX_MAX, std::max(FIX_MIN, ceil_div(q.chunks, std::max(1, d.sms / q.wins))));
-    const dim3 fgrid(unsigned(ceil_div(q.chunks, look)) * unsigned(q.wins));
+    // the last kernel's columns: vectors of at most four values
+    const int nvf = e.D / std::min(q.V, 4), fwins = ceil_div(nvf, SUM_THREADS), fcols = ceil_div(nvf, fwins);
+    const int look = std::min(FIX_MAX, std::max(FIX_MIN, ceil_div(q.chunks, std::max(1, d.sms / fwins))));
+    const dim3 fgrid(unsigned(ceil_div(q.chunks, look)) * unsigned(fwins));
     cudaError_t r = cudaSuccess;
     const float* cpart = part;
 #define EMB_CALL(V_)                                                                                             \
@@ -1052,7 +1087,7 @@ cudaError_t sum_t(const conv_embed_desc_t& e, const EmbedPlan& q, const DevInfo&
         if (r == cudaSuccess) {                                                                                  \
             constexpr int VF = V_ < 4 ? V_ : 4;                                                                  \
             r = launch_ex(embed_fix<T, VF>, fgrid, dim3(FIX_THREADS), 0, s, 1, true, n, e.V, e.D,                \
-                          q.cols * (V_ / VF), q.wins, q.chunk, q.chunks, look, e.scale, keys, dtable, cpart);    \
+                          fcols, fwins, q.chunk, q.chunks, look, e.scale, keys, dtable, cpart);                  \
         }                                                                                                        \
     } while (0)
     if (q.V == 8) {
