@@ -98,17 +98,23 @@ __device__ __forceinline__ float gn_z(float xhat, float gamma, float beta)
     return __fadd_rn(__fmul_rn(xhat, gamma), beta);
 }
 
+// a + b that no compiler merges with the product that a is (the pair's addition may be).
+__device__ __forceinline__ float2 add2_apart(float2 a, float2 b)
+{
+    return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+}
+
 // y from d = x - mean, rounded.  The ReLU's forward and backward round z alike, operation by
 // operation, so that their masks agree; the smooth activations take rstd * gamma in one.
 template <int ACT> __device__ __forceinline__ float2 gn_out(float2 d, float2 rstd, float2 gamma_or_scale, float2 beta)
 {
-    if constexpr (ACT == CONV_ACT_RELU) return act_value<ACT>(add2(mul2(mul2(d, rstd), gamma_or_scale), beta));
+    if constexpr (ACT == CONV_ACT_RELU) return act_value<ACT>(add2_apart(mul2(mul2(d, rstd), gamma_or_scale), beta));
     return act_value<ACT>(fma2(d, gamma_or_scale, beta));
 }
 // dz from xhat.
 template <int ACT> __device__ __forceinline__ float2 gn_grad(float2 dy, float2 xhat, float2 gamma, float2 beta)
 {
-    if constexpr (ACT == CONV_ACT_RELU) return gn_dz<ACT>(dy, add2(mul2(xhat, gamma), beta));
+    if constexpr (ACT == CONV_ACT_RELU) return gn_dz<ACT>(dy, add2_apart(mul2(xhat, gamma), beta));
     return gn_dz<ACT>(dy, fma2(xhat, gamma, beta));
 }
 
@@ -116,7 +122,7 @@ template <int ACT> __device__ __forceinline__ float2 gn_grad(float2 dy, float2 x
 template <int ACT>
 __device__ __forceinline__ float2 gn_dz_at(float2 dy, float2 d, float2 rstd, float2 gamma_or_scale, float2 beta)
 {
-    if constexpr (ACT == CONV_ACT_RELU) return gn_dz<ACT>(dy, add2(mul2(mul2(d, rstd), gamma_or_scale), beta));
+    if constexpr (ACT == CONV_ACT_RELU) return gn_dz<ACT>(dy, add2_apart(mul2(mul2(d, rstd), gamma_or_scale), beta));
     return gn_dz<ACT>(dy, fma2(d, gamma_or_scale, beta));
 }
 

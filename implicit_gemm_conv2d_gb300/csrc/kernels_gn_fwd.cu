@@ -147,7 +147,10 @@ gn_team_fwd(const GnParams p, const GnTeam q, const T* x, const T* gamma, const 
             table_pairs<V, K>(bet, toff, w);
             with_act(p.act, [&](auto act) {
 #pragma unroll
-                for (int h = 0; h < H; ++h) v[h] = act_value<act.value>(add2(v[h], w[h]));
+                for (int h = 0; h < H; ++h) {
+                    const float2 z = act.value == CONV_ACT_RELU ? add2_apart(v[h], w[h]) : add2(v[h], w[h]);
+                    v[h] = act_value<act.value>(z);
+                }
             });
 #pragma unroll
             for (int k = 0; k < K; ++k) {

@@ -254,3 +254,50 @@ def test_gradient_against_differences(shape, layout):
     ref = train_ref.gn_bwd(x, host["dy"], host["gamma"], host["beta"], to_np(mean), to_np(rstd), G, "silu", layout)
     den = sum((d * np.abs(t)).sum() for (_, d), t in zip(ref, (v, vg, vb)))
     assert abs(sum(t.sum() for t in terms) - want) <= 1e-5 * den
+
+
+# Sizes at which a team or a cluster walks several samples (its next one is read, or copied into the
+# slots of the last, while it works on this one), and tiles of many groups in two passes.
+MANY = {
+    "teams": ((6000, 32, 12, 4), "relu"),
+    "blocks": ((6000, 8, 131, 2), "gelu"),
+    "clusters": ((40, 64, 4096, 4), "relu"),
+    "vectors_of_two_groups": ((1500, 160, 60, 16), "silu"),
+    "many_groups_a_tile": ((1, 1088, 3860, 32), "relu"),
+    "long_tiles": ((2, 224, 13115, 8), "gelu"),
+}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("layout", ["nchw", "nhwc"])
+@pytest.mark.parametrize("case", list(MANY))
+def test_many_samples_and_long_tiles(case, layout, dtype):
+    shape, act = MANY[case]
+    both_ways(shape, layout, dtype, act, seed=11)
+
+
+@pytest.mark.parametrize("shape", ["block_team", (40, 64, 512, 4), (8192, 64, 12, 8)])
+@pytest.mark.parametrize("layout", ["nchw", "nhwc"])
+def test_relu_at_zero(shape, layout):
+    """beta = -fl(fl((x - mean) rstd) gamma) at one position of each channel and group: z is 0 there
+    when its product and its sum are rounded apart, and the product's rounding error when they are
+    not, so y and the gradient through that position show it."""
+    dev, host, G = inputs(shape, layout, "f32", 12)
+    x = host["x"].astype(np.float32)
+    C = host["gamma"].size
+    _, mean, rstd = train.group_norm(dev["x"], G, dev["gamma"], dev["beta"], EPS, "relu", layout)
+    m, r = to_np(mean).astype(np.float32), to_np(rstd).astype(np.float32)
+    at = (0, slice(None), 1) if layout == "nchw" else (0, 1, slice(None))  # sample 0, position 1, every channel
+    rep = C // G
+    xhat = (x[at] - np.repeat(m[0], rep)) * np.repeat(r[0], rep)
+    beta = -(xhat * host["gamma"].astype(np.float32))
+    assert beta.dtype == np.float32
+    dbeta_in = to_dev(beta, "f32")
+    y, mean2, rstd2 = train.group_norm(dev["x"], G, dev["gamma"], dbeta_in, EPS, "relu", layout)
+    assert torch.equal(mean, mean2) and torch.equal(rstd, rstd2)
+    assert not to_np(y)[at].any()
+    # a gradient at those positions only: the mask stops all of it
+    dy = torch.zeros_like(dev["x"])
+    dy[at] = 1.0
+    dx, dg, db = train.group_norm_bwd(dev["x"], dy, G, dev["gamma"], dbeta_in, mean, rstd, "relu", layout)
+    assert not dx.any() and not dg.any() and not db.any()
