@@ -139,6 +139,8 @@ def _ptr(t):
         return None
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError("tensors must be contiguous CUDA tensors")
+    if t.get_device() != torch.cuda.current_device():  # the library launches on the current device
+        raise ValueError(f"a tensor on {t.device}, which is not the current device: call under torch.cuda.device")
     return ctypes.c_void_p(t.data_ptr())
 
 

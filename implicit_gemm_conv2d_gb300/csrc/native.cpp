@@ -9,6 +9,7 @@
 #include <vector>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -52,6 +53,18 @@ const at::Tensor* optional(PyObject* o, const char* name) { return o == Py_None 
 void on_gpu(const at::Tensor& t)
 {
     if (!t.is_cuda() || !t.is_contiguous()) value_error("tensors must be contiguous CUDA tensors");
+}
+
+// A call runs on the current device (include/conv_train.h): on another device's tensors its kernels
+// would be given addresses that are not theirs.  Asked for one tensor of a call, before anything is
+// allocated; the others are on that one's device.
+void on_current(const at::Tensor& t)
+{
+    c10::DeviceIndex current = -1;
+    if (c10::cuda::GetDevice(&current) == cudaSuccess && current == t.device().index()) return;
+    PyErr_Format(PyExc_ValueError, "tensors on cuda:%d, which is not the current device: call under torch.cuda.device",
+                 int(t.device().index()));
+    throw Raised();
 }
 
 int dtype_code(const at::Tensor& t, const char* name)
@@ -138,6 +151,7 @@ conv_gn_desc_t gn_desc(const at::Tensor& x, PyObject* groups, double eps, PyObje
     d.eps = float(eps);
     if (x.dim() < 2) value_error("x: at least (batch, channels)");
     on_gpu(x);
+    on_current(x);
     const bool nhwc = d.layout == CONV_LAYOUT_NHWC;
     d.B = size32(x.size(0));
     d.C = size32(x.size(nhwc ? -1 : 1));
@@ -211,6 +225,7 @@ conv_embed_desc_t embed_desc(const at::Tensor& idx, const at::Tensor& t, const c
     if (idx.device() != t.device()) value_error("idx and its values are on different devices");
     on_gpu(idx);
     on_gpu(t);
+    on_current(t);
     d.T = idx.numel();
     d.V = size32(V);
     d.D = size32(D);
@@ -259,6 +274,8 @@ PyObject* grads_call(PyObject* const* a)
     PyObject** out = a[1] != Py_None ? PySequence_Fast_ITEMS(a[1]) : in;
     std::vector<conv_grad_t> list(static_cast<size_t>(n));
     const at::Tensor& first = tensor(in[0], "a gradient");
+    on_gpu(first);
+    on_current(first);
     for (Py_ssize_t i = 0; i < n; ++i) {
         const at::Tensor& g = tensor(in[i], "a gradient");
         on_gpu(g);

@@ -8,7 +8,8 @@ group_norm_bwd, embed, embed_bwd, grad_norm and clip_grads check shapes and type
 outputs and workspaces with torch first.  Everything is enqueued on the current torch stream (or
 the stream given) and nothing waits for the GPU; tensors made on another stream have to be
 ordered by the caller (``stream.wait_stream``), as for any torch operation.  What the allocating
-functions allocate belongs to the stream they run on."""
+functions allocate belongs to the stream they run on.  A call runs on the current device, and
+tensors on another one are refused (``with torch.cuda.device(x.device):``)."""
 from __future__ import annotations
 
 import ctypes
