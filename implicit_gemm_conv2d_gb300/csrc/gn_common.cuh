@@ -236,6 +236,23 @@ __device__ __forceinline__ float div_m(const GnParams& p, float s)
     return fmaf(fmaf(-q, p.m, s), p.inv_m, q);
 }
 
+// Sums s of n values less a pivot (c is minus the pivot) and sq of their squares, moved to another
+// pivot: the values' mean, rounded.  With D the step that the rounded pivot took, sum (x - p - D) is
+// s - n D and sum (x - p - D)^2 is sq - D (s + (s - n D)), so nothing depends on how D was rounded.
+template <int H> __device__ __forceinline__ void recentre(float2 (&c)[H], float2 (&s)[H], float2 (&sq)[H], float n)
+{
+    const float w = -fast_rcp(n);
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+        const float2 to = fma2(s[h], both(w), c[h]);
+        const float2 step = add2(to, mul2(c[h], both(-1.f)));  // -D
+        const float2 left = fma2(step, both(n), s[h]);
+        sq[h] = fma2(step, add2(s[h], left), sq[h]);
+        s[h] = left;
+        c[h] = to;
+    }
+}
+
 // Sum over the block, the same value in every thread.  `sm` holds 64 floats; `turn` alternates
 // its halves so that one barrier a call is enough.
 __device__ __forceinline__ float block_total(float v, float* sm, int& turn)
