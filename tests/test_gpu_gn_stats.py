@@ -16,6 +16,15 @@ TOL = 1e-5
 
 #                B,    C,      P,  G, layout
 SHAPES = {
+    # a cluster holds the group: up to 128 values a thread and place
+    "cluster_f32_single": (1, 5, 40000, 1, "nhwc", "f32"),
+    "cluster_bf16_single": (1, 5, 76000, 1, "nhwc", "bf16"),
+    "cluster_f32_pairs": (2, 6, 36000, 1, "nhwc", "f32"),
+    "cluster_bf16_pairs": (2, 6, 70000, 1, "nhwc", "bf16"),
+    "cluster_two_groups_a_vector": (1, 20, 22000, 4, "nhwc", "bf16"),
+    "cluster_rows_f32": (1, 1, 200001, 1, "nchw", "f32"),
+    "cluster_rows_bf16": (1, 1, 400001, 1, "nchw", "bf16"),
+    "cluster_wide_bf16": (2, 64, 5184, 2, "nhwc", "bf16"),
     # two passes over row tiles: 64 to 1024 rows a thread
     "tiles_f32": (1, 1024, 17000, 16, "nhwc", "f32"),
     "tiles_bf16": (1, 2048, 17000, 32, "nhwc", "bf16"),
