@@ -41,6 +41,8 @@ constexpr int CS_WARPS = CS_THREADS / 32;
 constexpr int TAB_COLS = 32;                               // columns of a table window: two a lane of half a warp
 constexpr int TAB_STEP = 16, TAB_STAGES = 4;               // tokens copied at a time, copies under way and in use
 constexpr int TAB_SMEM = 225 * 1024;
+constexpr int TAB_GROUP = 4;                               // tokens added at a time
+constexpr int TAB_TOKENS = 512 * TAB_GROUP;                // of a half warp's share at most: no chain of sums beyond 512
 constexpr int FEW_THREADS = 256, FEW_WARPS = FEW_THREADS / 32;
 constexpr int FEW_TOKENS = 512, FEW_BLOCKS = 4096, FEW_ROWS = 1024;              // tokens at most; rows a filling block takes at most
 constexpr int TAB_MAX_UNITS = 32, TAB_MIN_UNITS = 4;       // half warps with a table each, a block (and SM)
@@ -99,8 +101,10 @@ EmbedPlan embed_plan(const conv_embed_desc_t& e, const DevInfo& d)
               (e.D <= 256 || e.T <= int64_t(kMaxCluster) * CS_TOKENS);
     if (q.table) {
         q.smem = q.units * unit;
-        const int64_t most = std::max(1, d.sms / q.wins);
-        q.blocks = int(std::min<int64_t>(most, (e.T + q.units * 4 * TAB_STEP - 1) / (q.units * 4 * TAB_STEP)));
+        const int64_t most = std::max(1, d.sms / q.wins), share = int64_t(q.units) * TAB_TOKENS;
+        const int64_t waves = (e.T + most * share - 1) / (most * share);  // (whole ones)
+        q.blocks = int(waves > 1 ? waves * most
+                                 : std::min<int64_t>(most, (e.T + q.units * 4 * TAB_STEP - 1) / (q.units * 4 * TAB_STEP)));
         q.off_part = take(size_t(q.blocks) * e.V * e.D * 4);
         q.bytes = o;
         return q;
@@ -593,8 +597,12 @@ sort_cluster(int n, int rows, int padding, int S, int log_items, int passes, int
 // ---- whole-table sums ------------------------------------------------------------------------
 // Block (range, window), unit u (half a warp): its own table of rows + 1 rows (the last one takes
 // the tokens that name none) and a ring of TAB_STAGES tiles of TAB_STEP tokens.  Four tokens are
-// added at a time: their table rows are read together, and where a row comes again among the four
-// the sum so far takes the place of what was read.
+// added at a time: their table rows are read together; where a row comes again among the four, its
+// values are added to each other first, and the last of them stores the row.  A row thus gets one
+// addition in four tokens at most where it holds most of them, and a unit's share is at most
+// TAB_TOKENS: no chain of additions is longer than 512, which equal values keep within 8e-6 of their
+// sum (a chain of 4825, which one block a window had, lost 7e-5).  Eight tokens at a time are bound by
+// the comparisons: 1540096 tokens, 128 x 32 bf16 53 us against 47.
 // 1540096 tokens, 128 x 32 fp32: 42 us and 5 for the copies' sum, 4.3 TB/s, 64% of the measured
 // copy's.  Bound by shared memory's latency: a step's sums wait for the step's before.
 template <int BYTES> __device__ __forceinline__ void tab_copy(uint32_t dst, const void* src)
@@ -622,7 +630,8 @@ embed_table(int n, int rows, int padding, int D, int blocks, int units, const I*
     // (both halves of a warp walk as many steps)
     const int other = __shfl_xor_sync(0xFFFFFFFFu, t1 - t0, 16);
     const int steps = (max(t1 - t0, other) + TAB_STEP - 1) / TAB_STEP;
-    for (int r = 0; r <= rows; ++r) my[r * (TAB_COLS / 2)] = make_float2(0.f, 0.f);
+    for (int i = lane * 4; i < size; i += 64)
+        *reinterpret_cast<float4*>(tab + size_t(u) * size + i) = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i = lane; i < TAB_STAGES * TILE; i += 16) Elem<T>::st(tile + i, 0.f);
     __syncwarp();
     // This lane's part of a step's copies: one in AT_ONCE tokens where a token is less than 16
@@ -659,11 +668,11 @@ embed_table(int n, int rows, int padding, int D, int blocks, int units, const I*
         const int row = (name >= 0 && name < rows && name != padding ? int(name) : rows) * (TAB_COLS / 2);
         const T* v = tile + stage * TILE + 2 * lane;
 #pragma unroll
-        for (int g = 0; g < TAB_STEP; g += 4) {
-            int r[4];
-            float2 f[4], s[4];
+        for (int g = 0; g < TAB_STEP; g += TAB_GROUP) {
+            int r[TAB_GROUP];
+            float2 f[TAB_GROUP], s[TAB_GROUP];  // values, with those before them of the same row; the table's
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < TAB_GROUP; ++j) {
                 r[j] = __shfl_sync(0xFFFFFFFFu, row, g + j, 16);
                 Vec<T, 2> e;
                 e.load(v + (g + j) * TAB_COLS);
@@ -671,25 +680,38 @@ embed_table(int n, int rows, int padding, int D, int blocks, int units, const I*
                 s[j] = my[r[j]];
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < TAB_GROUP; ++j) {
+                float2 b = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < j; ++i)
-                    if (r[i] == r[j]) s[j] = s[i];
+                    if (r[i] == r[j]) b = f[i];
+                f[j] = make_float2(b.x + f[j].x, b.y + f[j].y);
                 s[j] = make_float2(s[j].x + f[j].x, s[j].y + f[j].y);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) my[r[j]] = s[j];
+            for (int j = 0; j < TAB_GROUP; ++j) my[r[j]] = s[j];
         }
         __syncwarp();
     }
     __syncthreads();
-    // the copies added in order
-    for (int i = threadIdx.x; i < rows * TAB_COLS; i += blockDim.x) {
-        float s = 0.f;
+    // the copies added in order, four columns at a time
+    for (int i = int(threadIdx.x) * 4; i < rows * TAB_COLS; i += int(blockDim.x) * 4) {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int k = 0; k < units; ++k) s += tab[size_t(k) * size + i];
+        for (int k = 0; k < units; ++k) {
+            const float4 e = *reinterpret_cast<const float4*>(tab + size_t(k) * size + i);
+            s = make_float4(s.x + e.x, s.y + e.y, s.z + e.z, s.w + e.w);
+        }
         const int r = i / TAB_COLS, c = i % TAB_COLS;
-        if (c < width) part[(int64_t(range) * rows + r) * D + c0 + c] = s;
+        float* o = part + (int64_t(range) * rows + r) * D + c0 + c;
+        if (D % 4 == 0) {
+            if (c < width) *reinterpret_cast<float4*>(o) = s;
+        } else {
+            if (c < width) o[0] = s.x;
+            if (c + 1 < width) o[1] = s.y;
+            if (c + 2 < width) o[2] = s.z;
+            if (c + 3 < width) o[3] = s.w;
+        }
     }
 }
 
@@ -705,8 +727,13 @@ __global__ void __launch_bounds__(256) embed_table_sum(int64_t values, int block
     float s = 0.f;
     tc::grid_dep_wait();
     if (e < values)
+        for (int b0 = l; b0 < blocks; b0 += 8 * 64) {  // 64 at a time, so that no chain is long
+            float part_sum = 0.f;
+            const int b1 = min(blocks, b0 + 8 * 64);
 #pragma unroll 8
-        for (int b = l; b < blocks; b += 8) s += part[int64_t(b) * values + e];
+            for (int b = b0; b < b1; b += 8) part_sum += part[int64_t(b) * values + e];
+            s += part_sum;
+        }
     sm[l][threadIdx.x & 31] = s;
     __syncthreads();
     if (l == 0 && e < values) {
