@@ -33,6 +33,7 @@ constexpr int SORT_TILE = SORT_THREADS * SORT_ITEMS;       // tokens a block sor
 constexpr int SORT_MAX_BITS = 9;                           // digit
 constexpr int SORT_MAX_BINS = 1 << SORT_MAX_BITS;
 constexpr int SUM_THREADS = 256, SUM_BLOCKS_SM = 3;
+constexpr int CHUNK_MAX = 256;                             // sorted tokens a group sums
 constexpr int FIX_THREADS = 1024;
 constexpr int FIX_MIN = 16, FIX_MAX = 256;                 // chunks a block of the last kernel looks at
 constexpr int CS_THREADS = 1024, CS_ITEMS = 8;             // sort by one cluster: a block's threads, tokens a thread
@@ -121,9 +122,10 @@ EmbedPlan embed_plan(const conv_embed_desc_t& e, const DevInfo& d)
     const int each = ceil_div(q.nv, q.V * es >= 16 ? 1 : q.V * es == 8 ? 2 : 4);  // a thread's vectors: sum_vectors()
     q.wins = ceil_div(each, SUM_THREADS);
     q.cols = ceil_div(each, q.wins);
-    // Chunks: long, so that few runs are cut, while the groups fill the SMs once.
+    // Chunks: long, so that few runs are cut, while the groups fill the SMs once; a run over two of
+    // them is one chain of additions (512 and 1023 of equal values lose up to 8e-6 and 1.5e-5).
     const int64_t groups = std::max<int64_t>(1, int64_t(d.sms) * SUM_BLOCKS_SM * (SUM_THREADS / q.cols) / q.wins);
-    q.chunk = int(std::min<int64_t>(512, std::max<int64_t>(16, (e.T + groups - 1) / groups)));
+    q.chunk = int(std::min<int64_t>(CHUNK_MAX, std::max<int64_t>(16, (e.T + groups - 1) / groups)));
     q.chunks = int((e.T + q.chunk - 1) / q.chunk);
     for (int i = 0; i < (q.cluster ? 1 : 2); ++i) {
         q.off_keys[i] = take(size_t(e.T) * 4);
@@ -933,12 +935,17 @@ __global__ void __launch_bounds__(FIX_THREADS) embed_fix(int n, int rows, int D,
     for (int done = 0; done < active; done += slots) {
         const int k = slot < slots && done + slot < active ? done + slot : -1;  // this lane's run
         float acc[V];
+        float* mine = sm[min(lane, lanes - 1) * cols + col];  // this lane's sum
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = 0.f;
+        for (int i = 0; i < V; ++i) {
+            acc[i] = 0.f;
+            if (lane < lanes) mine[i] = 0.f;
+        }
         if (k >= 0 && c < D) {
             const int ch = begins[k];
             const uint32_t key = name[k];
             bool on = true;
+            int stop = sub + 256 * per;  // 256 chunks at a time, so that no chain is long
             for (int j = sub; on; j += per * U) {
                 uint32_t q[U];
                 Vec<float, V> v[U];
@@ -949,6 +956,14 @@ __global__ void __launch_bounds__(FIX_THREADS) embed_fix(int n, int rows, int D,
                     q[u] = !in ? 0xFFFFFFFFu : at == ch ? key : keys[int64_t(at) * chunk];
                     if (in) v[u].load(part + (int64_t(at) * 2 + (at == ch ? 1 : 0)) * D + c);
                     else v[u].zero();
+                }
+                if (j == stop) {
+                    stop += 256 * per;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        mine[i] += acc[i];
+                        acc[i] = 0.f;
+                    }
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
@@ -961,9 +976,11 @@ __global__ void __launch_bounds__(FIX_THREADS) embed_fix(int n, int rows, int D,
         }
         if (lane < lanes)
 #pragma unroll
-            for (int i = 0; i < V; ++i) sm[lane * cols + col][i] = acc[i];
+            for (int i = 0; i < V; ++i) mine[i] += acc[i];
         __syncthreads();
         if (k >= 0 && sub == 0 && c < D) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = mine[i];
             for (int l = 1; l < per; ++l)
 #pragma unroll
                 for (int i = 0; i < V; ++i) acc[i] += sm[(lane + l) * cols + col][i];

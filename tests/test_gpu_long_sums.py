@@ -24,6 +24,7 @@ TOKENS = {
     "whole_table_long": (4_000_000, 128, 32),
     "sorted_in_a_cluster": (60000, 20000, 32),
     "sorted_by_kernels": (300000, 20000, 64),
+    "one_column": (1 << 25, 2000, 1),
 }
 
 
@@ -37,6 +38,20 @@ def test_table_gradient_of_one_row(name, value):
     off = rel(dt[V // 2], T * float(np.float32(value)))
     assert off <= TOL, f"{off:.2e}"
     assert torch.count_nonzero(dt).item() == D
+
+
+@pytest.mark.parametrize("value", VALUES)
+@pytest.mark.parametrize("length", [700, 1023])
+def test_table_gradient_of_runs_over_two_chunks(length, value):
+    """Every row the same number of tokens, so that runs begin at every place of a chunk."""
+    T, D = 240000, 1024
+    V = T // length + 1
+    idx = (torch.arange(T, device="cuda") // length).to(torch.int32)
+    dy = torch.full((T, D), value, device="cuda")
+    dt = train.embed_bwd(idx, dy, V)
+    count = torch.bincount(idx.long(), minlength=V).double()
+    off = rel(dt[count > 0], count[count > 0][:, None] * float(np.float32(value)))
+    assert off <= TOL, f"{off:.2e}"
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
