@@ -171,7 +171,7 @@ gn_team_bwd(const GnParams p, const GnTeam q, const T* x, const T* dy, const T* 
 // lanes and the blocks are added by fixed butterflies.  About 5 us of each backward, most of them
 // the launch behind the pass and one trip to memory.
 template <typename T>
-__global__ void __launch_bounds__(1024) gn_chan_sum(int C, int64_t n, int S, int64_t stride, int64_t kind_stride,
+__global__ void __launch_bounds__(1024, 2) gn_chan_sum(int C, int64_t n, int S, int64_t stride, int64_t kind_stride,
                                                     const float* part, T* dgamma, T* dbeta)
 {
     __shared__ float sm[32][33], total[32];
@@ -182,8 +182,13 @@ __global__ void __launch_bounds__(1024) gn_chan_sum(int C, int64_t n, int S, int
     tc::grid_dep_wait();
     if (c < C) {
         const float* at = part + blockIdx.y * kind_stride + c;
+        for (int64_t i = n * rank / S + l; i < i1;) {  // 128 at a time, so that no chain is long
+            float some = 0.f;
+            const int64_t stop = min(i1, i + 32 * 128);
 #pragma unroll 8
-        for (int64_t i = n * rank / S + l; i < i1; i += 32) t += at[i * stride];
+            for (; i < stop; i += 32) some += at[i * stride];
+            t += some;
+        }
     }
     sm[l][threadIdx.x & 31] = t;
     __syncthreads();

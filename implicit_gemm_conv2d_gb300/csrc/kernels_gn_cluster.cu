@@ -164,6 +164,7 @@ GnCluster gn_cluster(const GnParams& p, int dt, const DevInfo& d, bool bwd)
                 if (m > 1) break;
             }
             r.chunks = std::max(1, std::min(p.B, gc_resident(d, S, log, per_sm) / q.wins));
+            if (bwd) r.chunks = gn_bounded_chunks(r.chunks, std::max(1, p.B));
             r.dm_cols = FastDivmod(uint32_t(std::max(1, q.cols)));
             r.dm_cg = FastDivmod(uint32_t(p.Cg));
             r.dm_p = FastDivmod(uint32_t(p.P));

@@ -45,6 +45,7 @@ GnTeam gn_team(const GnParams& p, int dt, const DevInfo& d, bool bwd)
     const int per_sm = std::max(1, (bwd ? 512 : 1024) / q.threads);
     const int want = std::max(1, d.sms * per_sm / q.gsets);
     q.chunks = std::min(ceil_div(std::max(1, p.B), q.spc), want);
+    if (bwd) q.chunks = gn_bounded_chunks(q.chunks, ceil_div(std::max(1, p.B), q.spc));
     q.dm_cgv = FastDivmod(uint32_t(std::max(1, p.Cg / q.V)));
     q.dm_p = FastDivmod(uint32_t(p.P));
     q.dm_cg = FastDivmod(uint32_t(p.Cg));

@@ -50,17 +50,20 @@ GnRows gn_rows(const GnParams& p, int dt, const DevInfo& d, bool bwd)
     q.lanes = std::max(1, std::min(GR_THREADS / q.cols, p.P));
     q.threads = round_up(q.lanes * q.cols, 32);
     // Rows a thread: 16 where that fills the SMs, down to 4; more where a group would have more
-    // partial results than the second pass should merge.
+    // partial results than the second pass should merge.  The backward's sums over a thread's rows are
+    // one chain of additions each, so it takes GN_CHAIN rows at most (2048 rows of equal values lost
+    // 2.3e-5 of their sum; a second accumulator in the loop costs registers, and 3 to 12%).
     int R = 16;
+    const int most = bwd ? GN_CHAIN : INT32_MAX;
     while (R > 4 && int64_t(p.B) * q.wins * ceil_div(p.P, q.lanes * R) < 6 * d.sms) R /= 2;
-    while (int64_t(ceil_div(p.P, q.lanes * R)) * q.per > GR_MAX_PARTS && q.lanes * R < p.P) R *= 2;
+    while (int64_t(ceil_div(p.P, q.lanes * R)) * q.per > GR_MAX_PARTS && q.lanes * R < p.P && R < most) R *= 2;
     // A block of the second pass merges the partial results of all its window's groups: longer
     // tiles while those are more than a quarter of the tile's bytes (backward: half of one tensor's;
     // its merge is two additions) and the SMs stay filled (8 x 3860 x 1088 bf16, 32 groups a window,
     // forward: 16 rows 121 us, 64 rows 70; 6 x 13115 x 224 bf16, 8 groups, backward: 64 rows 72, 128 82).
     const int64_t groups = q.per == 1 ? q.W / p.Cg : 1;
     while (int64_t(ceil_div(p.P, q.lanes * R)) * q.per * groups * (bwd ? 16 : 32) > int64_t(q.lanes) * R * q.W * es &&
-           int64_t(p.B) * q.wins * ceil_div(p.P, q.lanes * R * 2) >= 2 * d.sms)
+           int64_t(p.B) * q.wins * ceil_div(p.P, q.lanes * R * 2) >= 2 * d.sms && R < most)
         R *= 2;
     q.len = int(std::min<int64_t>(p.P, int64_t(q.lanes) * R));
     q.pieces = ceil_div(p.P, q.len);

@@ -54,6 +54,43 @@ def test_table_gradient_of_runs_over_two_chunks(length, value):
     assert off <= TOL, f"{off:.2e}"
 
 
+#                B,      C,   P,      G, layout
+SHAPES = {
+    "teams": (160000, 1024, 2, 1024, "nchw"),
+    "teams_of_one_group": (400000, 16, 4, 1, "nchw"),
+    "clusters": (3000, 64, 64, 4, "nhwc"),
+    "tiles": (1, 1024, 280000, 16, "nhwc"),
+    "pieces": (1, 4, 2_000_000, 2, "nchw"),
+}
+
+
+@pytest.mark.parametrize("value", VALUES)
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_channel_sums(shape, value):
+    """dy constant and xhat 1 everywhere: dbeta and dgamma are both B * P * dy."""
+    B, C, P, G, layout = SHAPES[shape]
+    x = torch.ones((B, C, P) if layout == "nchw" else (B, P, C), device="cuda")
+    dy = torch.full_like(x, value)
+    mean, rstd = torch.zeros((B, G), device="cuda"), torch.ones((B, G), device="cuda")
+    dx, dgamma, dbeta = train.group_norm_bwd(x, dy, G, None, None, mean, rstd, "none", layout)
+    want = B * P * float(np.float32(value))
+    for name, out in (("dgamma", dgamma), ("dbeta", dbeta)):
+        off = rel(out, want)
+        assert off <= TOL, f"{name} {off:.2e}"
+
+
+@pytest.mark.parametrize("layout,C,P,G", [("nchw", 64, 16, 8), ("nchw", 64, 64, 8), ("nhwc", 64, 64, 8),
+                                          ("nchw", 4096, 400, 4096), ("nhwc", 4096, 64, 256)])
+def test_no_block_walks_more_than_256_samples(layout, C, P, G):
+    """A block adds up its samples' channel sums one after another and leaves one row of partial sums:
+    (2, C) fp32 a row of the workspace."""
+    for B in (1 << 17, min(1 << 20, (1 << 30) // G)):
+        d = train.make_gn_desc(B, C, P, G, "none", layout, torch.float32)
+        rows = train.conv_gn_bwd_workspace_size(d) // (8 * C)
+        per = 1 if C // G * P > 384 else max(1, 256 // G)  # teams: up to so many samples side by side
+        assert rows * 256 * per >= B, f"{B} samples, {rows} rows"
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("value", VALUES)
 def test_gradient_norm(value, dtype):
