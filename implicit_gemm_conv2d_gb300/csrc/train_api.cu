@@ -20,7 +20,9 @@ int gn_params(const conv_gn_desc_t* d, GnParams& p)
         d->act > CONV_ACT_GELU || (d->layout != CONV_LAYOUT_NCHW && d->layout != CONV_LAYOUT_NHWC) ||
         (d->dtype != CONV_F32 && d->dtype != CONV_BF16) || !std::isfinite(d->eps) || d->eps < 0.f)
         return CONV_ERR_DESC;
-    if (int64_t(d->C) * d->P > kMax32 - (1 << 20) || int64_t(d->B) * d->G > kMax32) return CONV_ERR_UNSUPPORTED;
+    // (B: the kernels step over samples in 32 bits, by B / 128 or some hundred thousand at most)
+    if (int64_t(d->C) * d->P > kMax32 - (1 << 20) || int64_t(d->B) * d->G > kMax32 || d->B > kMax32 - (1 << 25))
+        return CONV_ERR_UNSUPPORTED;
     p.B = d->B; p.C = d->C; p.P = d->P; p.G = d->G;
     p.Cg = d->C / d->G;
     p.act = d->act;

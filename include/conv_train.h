@@ -57,7 +57,8 @@ typedef struct {
 
 /* Forward.  gamma, beta: (C), or NULL (then 1 and 0).  mean, rstd: written, or both NULL (an
  * inference call).  y may be x (in place).
- * Limits: C*P < 2^31 - 2^20, B*G < 2^31 (CONV_ERR_UNSUPPORTED beyond).  B = 0 does nothing. */
+ * Limits: C*P < 2^31 - 2^20, B < 2^31 - 2^25, B*G < 2^31 (CONV_ERR_UNSUPPORTED beyond).  B = 0 does
+ * nothing. */
 size_t conv_gn_fwd_workspace_size(const conv_gn_desc_t* desc);
 int conv_gn_fwd(const conv_gn_desc_t* desc, const void* x, const void* gamma, const void* beta, void* y, float* mean,
                 float* rstd, void* workspace, size_t workspace_bytes, conv_stream_t stream);
