@@ -891,8 +891,7 @@ __global__ void __launch_bounds__(SUM_THREADS, SUM_BLOCKS_SM) embed_sum(int n, i
 // The long runs: a block looks at `look` chunks, and for each that a long run begins in adds the
 // run's partials, V <= 4 values a thread: lanes take chunks round robin while those go on with the
 // run, then the lanes are added in order.  So many chunks that the blocks are resident at once.  A
-// chain of latencies (a run's keys and partials are read together, eight of a lane's at a time);
-// where its blocks find room the first of them pass while the sums still run.
+// chain of latencies (a run's keys and partials are read together, eight of a lane's at a time).
 template <typename T, int V>
 __global__ void __launch_bounds__(FIX_THREADS) embed_fix(int n, int rows, int D, int cols, int wins, int chunk,
                                                          int chunks, int look, float scale, const uint32_t* keys,
@@ -905,10 +904,11 @@ __global__ void __launch_bounds__(FIX_THREADS) embed_fix(int n, int rows, int D,
     const int win = int(blockIdx.x % wins), ch0 = int(blockIdx.x / wins) * look;
     const int lanes = FIX_THREADS / cols, lane = int(threadIdx.x) / cols, col = int(threadIdx.x) - lane * cols;
     const int c = (win * cols + col) * V;
-    // The keys are the sort's: every block of the kernel before has waited for them, and this one
-    // was launched after that.  Only the partials have to be waited for.
+    // The keys, too, are read behind the wait: they are the sort's, which is done when any block of the
+    // kernel before runs on, but only the wait makes what earlier kernels wrote visible here.
     static_assert(FIX_THREADS >= FIX_MAX, "a thread a chunk");
     int active;
+    tc::grid_dep_wait();
     {
         const int ch = ch0 + int(threadIdx.x);
         uint32_t key = 0;
@@ -928,7 +928,6 @@ __global__ void __launch_bounds__(FIX_THREADS) embed_fix(int n, int rows, int D,
         }
         active = __syncthreads_count(is);
     }
-    tc::grid_dep_wait();
     if (active == 0) return;
     // the block's long runs side by side, as many as it has lanes, each with `per` lanes
     const int per = max(1, min(32, lanes / active)), slots = lanes / per, slot = lane / per, sub = lane - slot * per;
