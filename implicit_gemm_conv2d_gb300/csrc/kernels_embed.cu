@@ -93,15 +93,15 @@ EmbedPlan embed_plan(const conv_embed_desc_t& e, const DevInfo& d)
     // and an SM holds a few copies, whose reads ahead keep it busy.  Measured (Zipf tokens, us, whole
     // table against sort): 1540096 x 32 values, 128 rows, fp32 58 / 91; 60000 x 250 x 32 27 / 29;
     // 30000 x 16 x 1024 41 / 48; but 126925 x 102 x 504 102 / 71 (every window walks all tokens).
-    const int unit = (e.V + 1) * TAB_COLS * 4 +
-                     TAB_STAGES * TAB_STEP * (TAB_COLS * (e.dtype == CONV_F32 ? 4 : 2) +
-                                              (e.index_dtype == CONV_INDEX_I32 ? 4 : 8));
+    const int64_t unit = (int64_t(e.V) + 1) * TAB_COLS * 4 +
+                         TAB_STAGES * TAB_STEP * (TAB_COLS * (e.dtype == CONV_F32 ? 4 : 2) +
+                                                  (e.index_dtype == CONV_INDEX_I32 ? 4 : 8));
     q.wins = ceil_div(e.D, TAB_COLS);
-    q.units = e.V < TAB_SMEM / (TAB_COLS * 4) ? std::min(TAB_MAX_UNITS, TAB_SMEM / unit / 2 * 2) : 0;
+    q.units = int(std::min<int64_t>(TAB_MAX_UNITS, TAB_SMEM / unit / 2 * 2));
     q.table = q.units >= TAB_MIN_UNITS && e.T >= int64_t(64) * e.V && e.T >= 8192 &&
               (e.D <= 256 || e.T <= int64_t(kMaxCluster) * CS_TOKENS);
     if (q.table) {
-        q.smem = q.units * unit;
+        q.smem = q.units * int(unit);
         const int64_t most = std::max(1, d.sms / q.wins), share = int64_t(q.units) * TAB_TOKENS;
         const int64_t waves = (e.T + most * share - 1) / (most * share);  // (whole ones)
         q.blocks = int(waves > 1 ? waves * most
