@@ -187,6 +187,14 @@ cudaError_t run_wait_selftest(unsigned max_sleeps, cudaStream_t s);
 cudaError_t diag_read_status(unsigned* out, bool reset);
 
 __host__ __device__ inline int round_up(int a, int b) { return (a + b - 1) / b * b; }
-__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+// (on the host for every a >= 0, b > 0; on the device a + b stays below 2^31)
+__host__ __device__ inline int ceil_div(int a, int b)
+{
+#if defined(__CUDA_ARCH__)
+    return (a + b - 1) / b;
+#else
+    return int((int64_t(a) + b - 1) / b);
+#endif
+}
 
 }  // namespace igc

@@ -10,7 +10,8 @@ import pytest
 
 from implicit_gemm_conv2d_gb300 import build
 
-SOURCES = ["kernels_embed.cu", "kernels_grad.cu"]
+SOURCES = ["kernels_embed.cu", "kernels_gn_fwd.cu", "kernels_gn_bwd.cu", "kernels_gn_cluster.cu", "kernels_gn_nhwc.cu",
+           "kernels_grad.cu"]
 MAIN = r"""
 #include <cstdio>
 #include <vector>
@@ -25,7 +26,7 @@ int main()
     long plans = 0;
     for (int64_t T : {int64_t(1), int64_t(7), int64_t(512), int64_t(513), int64_t(65536), int64_t(65537),
                       int64_t(1540096), int64_t(100000003), most - (1 << 20)})
-        for (int64_t V : {int64_t(1), int64_t(128), int64_t(300), int64_t(1799), int64_t(50021), int64_t(1) << 25})
+        for (int64_t V : {int64_t(1), int64_t(128), int64_t(300), int64_t(1799), int64_t(50021), int64_t(1) << 25, most})
             for (int D : {1, 2, 3, 32, 37, 1024, 1088, 4096, 1 << 20, (1 << 24) - 1, 1 << 24})
                 for (int dt : {0, 1})
                     for (int it : {0, 1}) {
@@ -33,6 +34,25 @@ int main()
                         if (embed_bwd_workspace(e, d) > size_t(-1) / 2) return 1;
                         ++plans;
                     }
+    const int64_t last = most - (1 << 20);
+    for (int64_t C : {int64_t(1), int64_t(2), int64_t(27), int64_t(128), int64_t(320), int64_t(2051), int64_t(4096),
+                      int64_t(65536), last - 1, last})
+        for (int64_t P : {int64_t(1), int64_t(2), int64_t(12), int64_t(165), int64_t(5184), int64_t(1) << 20, last / C})
+            for (int64_t G : {int64_t(1), int64_t(2), int64_t(3), int64_t(16), int64_t(32), C})
+                for (int64_t B : {int64_t(1), int64_t(24), int64_t(32768), int64_t(100000007), most - (1 << 25)}) {
+                    if (P < 1 || C * P > last || C % G != 0 || B * G > most) continue;
+                    if (double(B) * double(C) * double(P) > 1.6e11) continue;  // no memory holds it
+                    for (int layout : {0, 1})
+                        for (int dt : {0, 1}) {
+                            GnParams p;
+                            p.B = int(B); p.C = int(C); p.P = int(P); p.G = int(G); p.Cg = int(C / G);
+                            p.act = 0; p.layout = layout; p.M = C / G * P; p.N = C * P;
+                            p.eps = 1e-5f; p.m = float(p.M); p.inv_m = float(1.0 / double(p.M));
+                            if (gn_fwd_workspace(p, dt, d) > size_t(-1) / 2) return 2;
+                            if (gn_bwd_workspace(p, dt, d) > size_t(-1) / 2) return 3;
+                            ++plans;
+                        }
+                }
     std::vector<conv_grad_t> g;
     for (int64_t n : {int64_t(0), int64_t(1), int64_t(16384), int64_t(400000000), (int64_t(1) << 40) - 1}) {
         g.push_back({nullptr, nullptr, n, 0});
@@ -74,4 +94,4 @@ def test_plans_do_not_overflow(tmp_path):
     assert r.returncode == 0, r.stderr
     r = subprocess.run([exe], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout + r.stderr
-    assert int(r.stdout.split()[0]) > 2000
+    assert int(r.stdout.split()[0]) > 3000
