@@ -109,7 +109,7 @@ struct GrTile {
         lane = int(x);
         col = int(a);
         r0 = pc * q.len;
-        r1 = min(p.P, r0 + q.len);
+        r1 = r0 + min(p.P - r0, q.len);  // (r0 + len may pass 2^31)
         full = (r1 - r0) / q.lanes;
         extra = r1 - r0 - full * q.lanes;
         in = lane < q.lanes && col * q.V < W;
