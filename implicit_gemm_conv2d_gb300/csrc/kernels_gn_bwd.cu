@@ -283,16 +283,16 @@ __global__ void __launch_bounds__(128) gn_group_sums(const GnParams p, const GnP
     const int np = p.Cg * q.pieces;
     tc::grid_dep_wait();
     tc::grid_dep_launch();
-    float s1 = 0.f, s2 = 0.f;
-    for (int i = threadIdx.x; i < np; i += blockDim.x) {
+    float2 s = both(0.f);
+    gn_stretches(np, s, [&](int i, float2& some) {
         const int pc = i / p.Cg, c = g * p.Cg + i - pc * p.Cg;
         const float ga = gamma ? Elem<T>::ldg(gamma + c) : 1.f;
         const int64_t o = gn_part(p, q.pieces, b, c, pc);
-        s1 += ga * psb[o];
-        s2 += ga * psg[o];
-    }
-    s1 = block_total(s1, sm, turn) * p.inv_m;
-    s2 = block_total(s2, sm, turn) * p.inv_m;
+        some.x += ga * psb[o];
+        some.y += ga * psg[o];
+    });
+    const float s1 = block_total(s.x, sm, turn) * p.inv_m;
+    const float s2 = block_total(s.y, sm, turn) * p.inv_m;
     if (threadIdx.x == 0) {
         m1[blockIdx.x] = s1;
         m2[blockIdx.x] = s2;

@@ -259,19 +259,19 @@ __global__ void __launch_bounds__(128) gn_combine(const GnParams p, const GnPiec
         cnt = min(q.len, p.P - pc * q.len);
         return gn_part(p, q.pieces, b, g * p.Cg + cl, pc);
     };
-    for (int i = threadIdx.x; i < np; i += blockDim.x) {
+    gn_stretches(np, s, [&](int i, float& some) {
         int cnt;
         const int64_t o = at(i, cnt);
-        s += pmean[o] * float(cnt);
-    }
+        some += pmean[o] * float(cnt);
+    });
     const float mu = __fdiv_rn(block_total(s, sm, turn), p.m);
     float v = 0.f;
-    for (int i = threadIdx.x; i < np; i += blockDim.x) {
+    gn_stretches(np, v, [&](int i, float& some) {
         int cnt;
         const int64_t o = at(i, cnt);
         const float dlt = pmean[o] - mu;
-        v += pm2[o] + dlt * dlt * float(cnt);
-    }
+        some += pm2[o] + dlt * dlt * float(cnt);
+    });
     const float r = rsqrtf(block_total(v, sm, turn) * p.inv_m + p.eps);
     if (threadIdx.x == 0) {
         mean[blockIdx.x] = mu;

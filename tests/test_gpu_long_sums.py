@@ -97,3 +97,14 @@ def test_gradient_norm(value, dtype):
     g = torch.full((300_000_000,), value, device="cuda").to(dtype)
     want = (300_000_000 * float(g[0]) ** 2) ** 0.5
     assert abs(float(train.grad_norm([g])) / want - 1.0) <= TOL
+
+
+@pytest.mark.parametrize("value", VALUES)
+def test_statistics_of_many_pieces(value):
+    """2^29 + 1 equal values of one channel, in 262145 pieces: mean is the value, y is 0."""
+    x = torch.full((1, 1, 2 ** 29 + 1), value, device="cuda")
+    y, mean, rstd = train.group_norm(x, 1, None, None, 1e-5, "none", "nchw")
+    assert abs(float(mean) / float(x[0, 0, 0]) - 1.0) <= TOL
+    dx, dg, db = train.group_norm_bwd(x, x, 1, None, None, torch.zeros_like(mean), torch.ones_like(rstd), "none")
+    v = float(x[0, 0, 0])  # xhat = dy = v: dx = v - v - v * v * v
+    assert float((dx.double() / -v ** 3 - 1.0).abs().max()) <= TOL
