@@ -91,19 +91,24 @@ EmbedPlan embed_plan(const conv_embed_desc_t& e, const DevInfo& d)
     }
     // Whole-table sums where the tokens outnumber by far the rows that every copy has to add up,
     // and an SM holds a few copies, whose reads ahead keep it busy.  Measured (Zipf tokens, us, whole
-    // table against sort): 1540096 x 32 values, 128 rows, fp32 58 / 91; 60000 x 250 x 32 27 / 29;
-    // 30000 x 16 x 1024 41 / 48; but 126925 x 102 x 504 102 / 71 (every window walks all tokens).
+    // table against sort): 1540096 x 32 values, 128 rows, fp32 45 / 83; 60000 x 250 x 32 16 / 28;
+    // 30000 x 16 x 1024 40 / 45; but 126925 x 102 x 504 98 / 87 (every window walks all tokens).
+    // Shares of TAB_TOKENS take several waves of blocks for many tokens, each of which zeroes its copies
+    // and adds them up: 4000000 x 128 x 32 fp32 106 / 214, 3000000 x 380 x 32 bf16 133 / 139 and 1000000
+    // x 100 x 128 fp32 128 / 156, but with several windows of narrow values or few copies 1000000 x 200 x
+    // 128 bf16 122 / 90, 1000000 x 380 x 128 bf16 176 / 93 and 19300 x 300 x 2500 fp32 104 / 78.
     const int64_t unit = (int64_t(e.V) + 1) * TAB_COLS * 4 +
                          TAB_STAGES * TAB_STEP * (TAB_COLS * (e.dtype == CONV_F32 ? 4 : 2) +
                                                   (e.index_dtype == CONV_INDEX_I32 ? 4 : 8));
     q.wins = ceil_div(e.D, TAB_COLS);
     q.units = int(std::min<int64_t>(TAB_MAX_UNITS, TAB_SMEM / unit / 2 * 2));
+    const int64_t most = std::max(1, d.sms / q.wins), wave = std::max<int64_t>(1, most * q.units * TAB_TOKENS);
+    const int64_t waves = (e.T + wave - 1) / wave;
     q.table = q.units >= TAB_MIN_UNITS && e.T >= int64_t(64) * e.V && e.T >= 8192 &&
-              (e.D <= 256 || e.T <= int64_t(kMaxCluster) * CS_TOKENS);
+              (e.D <= 256 || e.T <= int64_t(kMaxCluster) * CS_TOKENS) &&
+              (waves == 1 || q.wins == 1 || (e.dtype == CONV_F32 && q.units >= 8));
     if (q.table) {
         q.smem = q.units * int(unit);
-        const int64_t most = std::max(1, d.sms / q.wins), share = int64_t(q.units) * TAB_TOKENS;
-        const int64_t waves = (e.T + most * share - 1) / (most * share);  // (whole ones)
         q.blocks = int(waves > 1 ? waves * most
                                  : std::min<int64_t>(most, (e.T + q.units * 4 * TAB_STEP - 1) / (q.units * 4 * TAB_STEP)));
         q.off_part = take(size_t(q.blocks) * e.V * e.D * 4);
