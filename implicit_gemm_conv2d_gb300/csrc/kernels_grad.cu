@@ -7,9 +7,9 @@
 // the blocks' sums, depend only on the list's sizes: the norm has the same bits every run.  The
 // scaling pass walks the tiles backwards, so that what the first pass read last is still in L2.
 //
-// Measured: 48 tensors, 400 M bf16 values, clipped: 381 us; two reads and a write of 800 MB are 359
-// us at the measured copy's rate, so 94% of that (L2 keeps an eighth of the second read at best).
-// 300 tensors of either type, 60 M values, the norm: 34 us, 5.3 TB/s, 79%.  The encoder's nine
+// Measured: 48 tensors, 400 M bf16 values, clipped: 376 us; two reads and a write of 800 MB are 359
+// us at the measured copy's rate, so 95% of that (L2 keeps an eighth of the second read at best).
+// 300 tensors of either type, 60 M values, the norm: 30 us, 6.0 TB/s, 90%.  The encoder's nine
 // tensors, 341 k fp32 values, clipped: 8 us, two launches.
 #include <algorithm>
 
@@ -23,9 +23,11 @@ namespace {
 constexpr int GRAD_THREADS = 512;
 constexpr int GRAD_TILE = 16384, GRAD_TILE_MIN = 2048;  // elements
 constexpr int GRAD_BLOCKS_SM = 4;
-constexpr int GRAD_LIST = 512, GRAD_SHORT = 48;         // entries a launch; of a short list's kernel
+constexpr int GRAD_LIST = 512, GRAD_SHORT = 32;         // entries a launch; of a short list's kernel
 
-// N entries: a launch copies its parameters, so a short list has a short type.
+// N entries: a launch copies its parameters, so a short list has a short type, 1 KB and not 14: a clip of
+// 9 tensors, the GPU waited for, takes 19.1 to 20.8 us with it and 19.7 to 21.0 without; among other
+// calls, and with 48 tensors, the two do not differ.
 template <int N> struct GradListOf {
     int count;
     int tiles;
