@@ -11,7 +11,9 @@ namespace igc {
 
 // 2^x and 1/x in one instruction each (2 and 1 units in the last place; results below 2^-126
 // are 0).  The general-range forms of exp and of the quotient take about four times the
-// instructions, and the activations are most of what these kernels compute.
+// instructions, and the activations are most of what these kernels compute.  An exponential's argument
+// is a rounded product here, so exp(-z) is also off by up to |z| 2^-24 of itself: below 2e-6 as far as
+// the sigmoid has 2^-40 of its value left.
 __device__ __forceinline__ float fast_exp2(float x)
 {
     float r;
@@ -41,7 +43,10 @@ __device__ __forceinline__ float2 sigmoid2(float2 z)
 
 // Phi(z) and e = exp(-z^2 / 2).  Phi from Abramowitz & Stegun 7.1.26, Handbook of Mathematical
 // Functions: erf(x) = 1 - (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), x >= 0,
-// to 1.5e-7 (so Phi to 0.75e-7, near fp32's own rounding); its exponential is the density's.
+// to 1.5e-7 (so Phi to 0.75e-7); its exponential is the density's.  With its roundings in fp32 Phi is
+// off by up to 3.1e-7, and over z ~ N(0, 1) GELU by 8.5e-8 and its slope by 1.0e-7 of their norms, twice
+// what a correctly rounded erf leaves (3.8e-8 and 4.1e-8; for z in [-4, 0] at most 2.1e-7 against
+// 0.6e-7): a choice for fewer instructions.  A bf16 result shows nothing of it.
 __device__ __forceinline__ float2 normal_cdf2(float2 z, float2& e)
 {
     constexpr float c = 0.3275911f * 0.70710678118654752f;

@@ -12,12 +12,13 @@
 // results through distributed shared memory, with one cluster barrier.
 //
 // Measured (us; of the rate of the measured copy for one read of each input and one write):
-//   24 x 320 x 72x72 bf16, 32 groups of 10, SiLU, channels last, forward: 53, 45%; NCHW 41, 58%;
-//     fp32 82 and 61.
-//   12 x 192 x 95x101 bf16, 24 groups of 8, GELU, channels last, backward: 65, 30% (ReLU 53).
-// Bound by latency: an instruction is issued in 0.50 (forward) or 0.47 slots, from 22 warps an SM.  They wait for the activation's steps (its 2^x and 1/x), for shared memory and, a fifth of
-// the backward's time, at the barriers around a sample's sums.  In bf16 the backward's 48
-// instructions a value (the activation is computed twice) alone would take 28 us.
+//   24 x 320 x 72x72 bf16, 32 groups of 10, SiLU, channels last, forward: 48, 49%; NCHW 41, 58%;
+//     fp32 84 and 60.
+//   12 x 192 x 95x101 bf16, 24 groups of 8, GELU, channels last, backward: 63, 32% (ReLU 12 less).
+// Bound by latency: an instruction is issued in 0.51 (forward) or 0.47 slots, from 20 warps an SM.
+// They wait for the activation's steps (its 2^x and 1/x), for shared memory and, a fifth of the
+// backward's time, at the barriers around a sample's sums.  In bf16 the backward's 48 instructions a
+// value (the activation is computed twice) alone would take 28 us.
 // Beside two passes over memory (24 x 320 x 5184, SiLU): forward bf16 41 / 78, channels last 53 / 80,
 // fp32 61 / 98 and 82 / 139; backward bf16 102 / 144 and 108 / 152, fp32 141 / 157 and 149 / 188.
 #include <atomic>

@@ -79,7 +79,7 @@ GnPieces gn_pieces(const GnParams& p, int dt, const DevInfo& d)
 namespace {
 
 // ---- small groups ----------------------------------------------------------------------------
-// 32768 x 128 x 12, 16 groups, bf16, SiLU: 45 us, 4.6 TB/s, 68% of the measured copy's; bound by
+// 32768 x 128 x 12, 16 groups, bf16, SiLU: 41 us, 5.1 TB/s, 76% of the measured copy's; bound by
 // instructions (22 a value, of which the activation takes 4, at 0.71 an issue slot), as two
 // samples read ahead instead of one change nothing.  fp32, 8192 x 128 x 12: 22 us, 4.5 TB/s.
 // 256 x 128 x 2, 8 groups: 5 to 6 us, a launch.  Groups of up to 384 (bf16: 512) values; beside a

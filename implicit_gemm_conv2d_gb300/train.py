@@ -222,7 +222,8 @@ def conv_grad_clip(grads, count: int, max_norm: float, norm, workspace, stream=N
 
 
 def grad_norm(grads, stream=None):
-    """The 2-norm over all gradients (a list or tuple), a 0-dim fp32 tensor (nothing waits for it)."""
+    """The 2-norm over all gradients (a list or tuple, not empty), a 0-dim fp32 tensor (nothing waits
+    for it)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return grad_norm(grads)
@@ -231,7 +232,8 @@ def grad_norm(grads, stream=None):
 
 def clip_grads(grads, max_norm: float, out=None, stream=None):
     """Scales the gradients by min(1, max_norm / (norm + 1e-6)), in place or into the tensors of
-    ``out``; returns the norm before."""
+    ``out``; returns the norm before.  max_norm is finite (grad_norm gives the norm alone), and no
+    output may overlap another entry: a tensor is in the list once."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return clip_grads(grads, max_norm, out)

@@ -41,8 +41,9 @@ extern "C" {
  * dtype; mean and rstd are fp32, (B, G).
  * With CONV_ACT_RELU, xhat and z are computed by separate, individually rounded fp32 operations
  * in both directions: with the forward's mean and rstd the backward's z has the forward's bits
- * and its ReLU mask is exactly y > 0 of the fp32 forward.  The other activations, whose
- * derivatives have no jump, take z = (x - mean) * (rstd * gamma) + beta with one rounding less.
+ * and its ReLU mask is exactly y > 0 of the fp32 forward.  For the other activations, whose
+ * derivatives have no jump, only z's value is fixed: how its operations are joined and rounded
+ * depends on the sizes.  GELU's Phi is within 3.1e-7 (fp32).
  * A value that is infinite or NaN makes its whole group NaN and leaves the others alone. */
 typedef enum { CONV_LAYOUT_NCHW = 0, CONV_LAYOUT_NHWC = 1 } conv_layout_t;
 typedef enum { CONV_ACT_NONE = 0, CONV_ACT_RELU = 1, CONV_ACT_SILU = 2, CONV_ACT_GELU = 3 } conv_act_t;
