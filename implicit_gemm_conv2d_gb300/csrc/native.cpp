@@ -131,6 +131,14 @@ PyObject* wrap(const at::Tensor& t)
     if (t.defined()) return THPVariable_Wrap(t);
     Py_RETURN_NONE;
 }
+PyObject* wrap(const at::Tensor& a, const at::Tensor& b)
+{
+    PyObject* t = PyTuple_New(2);
+    if (!t) throw Raised();
+    PyTuple_SET_ITEM(t, 0, wrap(a));
+    PyTuple_SET_ITEM(t, 1, wrap(b));
+    return t;
+}
 PyObject* wrap(const at::Tensor& a, const at::Tensor& b, const at::Tensor& c)
 {
     PyObject* t = PyTuple_New(3);
@@ -262,6 +270,101 @@ PyObject* embed_bwd(PyObject* const* a)
     return wrap(dtable);
 }
 
+// (batch, time, channels), the channels one behind the other; the two other distances are the tensor's own.
+conv_rows_t rows_of(const at::Tensor& t, const char* name, at::IntArrayRef sizes, at::ScalarType dtype,
+                    const at::Device& device)
+{
+    if (t.sizes() != sizes || t.scalar_type() != dtype || t.device() != device) {
+        PyErr_Format(PyExc_ValueError, "%s: another size, dtype or device than the call's other tensors give it", name);
+        throw Raised();
+    }
+    if (t.size(2) > 1 && t.stride(2) != 1 && t.numel() > 0) {
+        PyErr_Format(PyExc_ValueError, "%s: a step's channels have to lie one behind the other", name);
+        throw Raised();
+    }
+    return {t.size(0) > 1 ? t.stride(0) : 0, t.size(1) > 1 ? t.stride(1) : 0};
+}
+
+const float* states(PyObject* o, const char* name, const at::Tensor& x)
+{
+    const at::Tensor* t = optional(o, name);
+    if (!t) return nullptr;
+    return static_cast<const float*>(same(*t, name, {x.size(0), x.size(2)}, at::kFloat, x.device()).data_ptr());
+}
+
+const uint8_t* flags(PyObject* o, const at::Tensor& x)
+{
+    const at::Tensor* t = optional(o, "reset");
+    if (!t) return nullptr;
+    if (t->scalar_type() != at::kBool && t->scalar_type() != at::kByte) value_error("reset: bool or uint8");
+    return static_cast<const uint8_t*>(
+        same(*t, "reset", {x.size(0), x.size(1)}, t->scalar_type(), x.device()).data_ptr());
+}
+
+const int32_t* row_lengths(PyObject* o, const at::Tensor& x)
+{
+    const at::Tensor* t = optional(o, "lengths");
+    return t ? static_cast<const int32_t*>(same(*t, "lengths", {x.size(0)}, at::kInt, x.device()).data_ptr()) : nullptr;
+}
+
+conv_scan_desc_t scan_desc(const at::Tensor& x, const at::Tensor& gate)
+{
+    conv_scan_desc_t d = {};
+    d.dtype = dtype_code(x, "x");
+    if (x.dim() != 3) value_error("x: (batch, time, channels)");
+    if (!x.is_cuda()) value_error("tensors must be CUDA tensors");
+    on_current(x);
+    d.B = size32(x.size(0));
+    d.T = size32(x.size(1));
+    d.D = size32(x.size(2));
+    d.x = rows_of(x, "x", x.sizes(), x.scalar_type(), x.device());
+    d.gate = rows_of(gate, "gate", x.sizes(), x.scalar_type(), x.device());
+    return d;
+}
+
+// x, gate, h0, reset, lengths, out, last
+PyObject* gated_scan(PyObject* const* a)
+{
+    const at::Tensor &x = tensor(a[0], "x"), &gate = tensor(a[1], "gate");
+    conv_scan_desc_t d = scan_desc(x, gate);
+    const float* h0 = states(a[2], "h0", x);
+    const uint8_t* reset = flags(a[3], x);
+    const int32_t* lengths = row_lengths(a[4], x);
+    const at::Tensor *out = optional(a[5], "out"), *into = optional(a[6], "last");
+    states(a[6], "last", x);
+    const at::Tensor h = out ? *out : at::empty(x.sizes(), x.options());
+    d.h = rows_of(h, "out", x.sizes(), x.scalar_type(), x.device());
+    const at::Tensor last = into ? *into : at::empty({d.B, d.D}, x.options().dtype(at::kFloat));
+    check(conv_scan_fwd(&d, x.data_ptr(), gate.data_ptr(), h0, reset, lengths, h.data_ptr(),
+                        static_cast<float*>(last.data_ptr()), stream_of(x)),
+          "conv_scan_fwd");
+    return wrap(h, last);
+}
+
+// x, gate, h, dh, h0, dlast, reset, lengths, dx, dgate
+PyObject* gated_scan_bwd(PyObject* const* a)
+{
+    const at::Tensor &x = tensor(a[0], "x"), &gate = tensor(a[1], "gate"), &h = tensor(a[2], "h"),
+                     &dh = tensor(a[3], "dh");
+    conv_scan_desc_t d = scan_desc(x, gate);
+    d.h = rows_of(h, "h", x.sizes(), x.scalar_type(), x.device());
+    d.dh = rows_of(dh, "dh", x.sizes(), x.scalar_type(), x.device());
+    const float *h0 = states(a[4], "h0", x), *dlast = states(a[5], "dlast", x);
+    const uint8_t* reset = flags(a[6], x);
+    const int32_t* lengths = row_lengths(a[7], x);
+    const at::Tensor *ox = optional(a[8], "dx"), *og = optional(a[9], "dgate");
+    const at::Tensor dx = ox ? *ox : at::empty(x.sizes(), x.options());
+    const at::Tensor dgate = og ? *og : at::empty(x.sizes(), x.options());
+    d.dx = rows_of(dx, "dx", x.sizes(), x.scalar_type(), x.device());
+    d.dgate = rows_of(dgate, "dgate", x.sizes(), x.scalar_type(), x.device());
+    at::Tensor dh0;
+    if (h0) dh0 = at::empty({d.B, d.D}, x.options().dtype(at::kFloat));
+    check(conv_scan_bwd(&d, x.data_ptr(), gate.data_ptr(), h.data_ptr(), dh.data_ptr(), h0, dlast, reset, lengths,
+                        dx.data_ptr(), dgate.data_ptr(), static_cast<float*>(address(dh0)), stream_of(x)),
+          "conv_scan_bwd");
+    return wrap(dx, dgate, dh0);
+}
+
 // grads, out (None: in place), max_norm (None: the norm only).  The sequences are tuples or lists.
 PyObject* grads_call(PyObject* const* a)
 {
@@ -337,6 +440,8 @@ PyMethodDef methods[] = {ENTRY("group_norm", group_norm, 8),
                          ENTRY("group_norm_bwd", group_norm_bwd, 10),
                          ENTRY("embed", embed, 4),
                          ENTRY("embed_bwd", embed_bwd, 5),
+                         ENTRY("gated_scan", gated_scan, 7),
+                         ENTRY("gated_scan_bwd", gated_scan_bwd, 10),
                          ENTRY("grads", grads_call, 3),
                          ENTRY("set_errors", set_errors, 2),
                          {nullptr, nullptr, 0, nullptr}};

@@ -200,6 +200,10 @@ __device__ __forceinline__ float4 ld_dsmem_f4(uint32_t addr)
                  : "memory");
     return v;
 }
+__device__ __forceinline__ void st_dsmem_f2(uint32_t addr, float a, float b)
+{
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
+}
 __device__ __forceinline__ float ld_dsmem_f32(uint32_t addr)
 {
     float v;

@@ -45,6 +45,38 @@ int embed_check(const conv_embed_desc_t* d)
     return CONV_OK;
 }
 
+// The last element's offset is one that 64 bits hold in bytes.
+bool rows_near(const conv_rows_t& r, int64_t B, int64_t T, int64_t D)
+{
+    const __int128 top = __int128(B > 0 ? B - 1 : 0) * r.batch + __int128(T > 0 ? T - 1 : 0) * r.step + D;
+    return top < __int128(1) << 60;
+}
+
+// An output's rows do not overlap, whichever of the two dimensions is the outer one (rows_near holds).
+bool rows_apart(const conv_rows_t& r, int64_t B, int64_t T, int64_t D)
+{
+    if (B <= 1 || T <= 1) return (B <= 1 || T < 1 || r.batch >= D) && (T <= 1 || B < 1 || r.step >= D);
+    if (r.step < D || r.batch < D) return false;
+    return r.batch >= (T - 1) * r.step + D || r.step >= (B - 1) * r.batch + D;
+}
+
+int scan_check(const conv_scan_desc_t* d, bool bwd)
+{
+    if (!d) return CONV_ERR_NULL;
+    if (d->B < 0 || d->T < 0 || d->D < 1 || (d->dtype != CONV_F32 && d->dtype != CONV_BF16)) return CONV_ERR_DESC;
+    const conv_rows_t* rows[] = {&d->x, &d->gate, &d->h, &d->dh, &d->dx, &d->dgate};
+    const int used = bwd ? 6 : 3;
+    for (int i = 0; i < used; ++i)
+        if (rows[i]->batch < 0 || rows[i]->step < 0) return CONV_ERR_DESC;
+    for (int i = 0; i < used; ++i)
+        if (!rows_near(*rows[i], d->B, d->T, d->D)) return CONV_ERR_UNSUPPORTED;
+    for (int i = bwd ? 4 : 2; i < used; ++i)
+        if (!rows_apart(*rows[i], d->B, d->T, d->D)) return CONV_ERR_DESC;
+    const int64_t most = kMax32 - (1 << 20);
+    if (d->B > most || d->T > most || d->D > most || int64_t(d->B) * d->D >= int64_t(1) << 40) return CONV_ERR_UNSUPPORTED;
+    return CONV_OK;
+}
+
 // `clip`: out is checked too.
 int grads_check(const conv_grad_t* g, int32_t count, bool clip)
 {
@@ -169,6 +201,42 @@ int conv_embed_bwd(const conv_embed_desc_t* desc, const void* idx, const void* d
     const size_t need = embed_bwd_workspace(*desc, d);
     if (need > 0 && (!workspace || workspace_bytes < need)) return CONV_ERR_WORKSPACE;
     return cuda_status(run_embed_bwd(*desc, d, idx, dy, dtable, workspace, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int conv_scan_fwd(const conv_scan_desc_t* desc, const void* x, const void* gate, const float* h0, const uint8_t* reset,
+                  const int32_t* lengths, void* h, float* last, conv_stream_t stream)
+{
+    int rc = scan_check(desc, false);
+    if (rc != CONV_OK) return rc;
+    if (desc->B == 0) return CONV_OK;
+    if (desc->T > 0 && (!x || !gate || !h)) return CONV_ERR_NULL;
+    const size_t a = desc->dtype == CONV_F32 ? 4 : 2;
+    if (!aligned_to(x, a) || !aligned_to(gate, a) || !aligned_to(h, a) || !aligned_to(h0, 4) || !aligned_to(last, 4) ||
+        !aligned_to(lengths, 4))
+        return CONV_ERR_ALIGN;
+    DevInfo d;
+    if ((rc = device_info(d)) != CONV_OK) return rc;
+    return cuda_status(
+        run_scan_fwd(*desc, d, x, gate, h0, reset, lengths, h, last, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int conv_scan_bwd(const conv_scan_desc_t* desc, const void* x, const void* gate, const void* h, const void* dh,
+                  const float* h0, const float* dlast, const uint8_t* reset, const int32_t* lengths, void* dx,
+                  void* dgate, float* dh0, conv_stream_t stream)
+{
+    int rc = scan_check(desc, true);
+    if (rc != CONV_OK) return rc;
+    if (desc->B == 0) return CONV_OK;
+    if (desc->T > 0 && (!x || !gate || !h || !dh || !dx || !dgate)) return CONV_ERR_NULL;
+    const size_t a = desc->dtype == CONV_F32 ? 4 : 2;
+    if (!aligned_to(x, a) || !aligned_to(gate, a) || !aligned_to(h, a) || !aligned_to(dh, a) || !aligned_to(dx, a) ||
+        !aligned_to(dgate, a) || !aligned_to(h0, 4) || !aligned_to(dlast, 4) || !aligned_to(dh0, 4) ||
+        !aligned_to(lengths, 4))
+        return CONV_ERR_ALIGN;
+    DevInfo d;
+    if ((rc = device_info(d)) != CONV_OK) return rc;
+    return cuda_status(run_scan_bwd(*desc, d, x, gate, h, dh, h0, dlast, reset, lengths, dx, dgate, dh0,
+                                    reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t conv_grad_norm_workspace_size(const conv_grad_t* grads, int32_t count)

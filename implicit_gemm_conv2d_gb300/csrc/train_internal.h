@@ -119,4 +119,21 @@ size_t grad_workspace(const conv_grad_t* g, int count, const DevInfo& d);
 cudaError_t run_grad_norm(const conv_grad_t* g, int count, bool clip, float max_norm, const DevInfo& d, float* norm,
                           void* ws, cudaStream_t s);
 
+// ---- gated scan (kernels_scan.cu) -----------------------------------------------------------
+struct ScanPlan {
+    int B, T, D;
+    conv_rows_t x, gate, h, dh, dx, dgate;
+    int V, L;                    // channels and steps of a thread
+    int lx_log, ty_log, by_log;  // a block's lanes over channels, stretches over time, batch rows
+    int cluster, tiles, threads; // blocks along time; blocks over the channels
+    int64_t blocks;
+};
+// pairs: two bf16 values may be read and written at once.
+ScanPlan scan_plan(const conv_scan_desc_t& e, const DevInfo& d, bool bwd, bool pairs);
+cudaError_t run_scan_fwd(const conv_scan_desc_t& e, const DevInfo& d, const void* x, const void* gate, const float* h0,
+                         const uint8_t* reset, const int32_t* lengths, void* h, float* last, cudaStream_t s);
+cudaError_t run_scan_bwd(const conv_scan_desc_t& e, const DevInfo& d, const void* x, const void* gate, const void* h,
+                         const void* dh, const float* h0, const float* dlast, const uint8_t* reset,
+                         const int32_t* lengths, void* dx, void* dgate, float* dh0, cudaStream_t s);
+
 }  // namespace igc

@@ -30,6 +30,7 @@ _IDX = {torch.int32: 0, torch.int64: 1}
 
 EXPORTS = ["conv_gn_fwd_workspace_size", "conv_gn_fwd", "conv_gn_bwd_workspace_size", "conv_gn_bwd",
            "conv_embed_fwd", "conv_embed_bwd_workspace_size", "conv_embed_bwd",
+           "conv_scan_fwd", "conv_scan_bwd",
            "conv_grad_norm_workspace_size", "conv_grad_norm", "conv_grad_clip"]
 
 
@@ -41,6 +42,15 @@ class GnDesc(ctypes.Structure):
 class EmbedDesc(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64)] + \
         [(n, ctypes.c_int32) for n in ("V", "D", "padding_idx", "index_dtype", "dtype")] + [("scale", ctypes.c_float)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("step", ctypes.c_int64)]
+
+
+class ScanDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "D", "dtype")] + \
+        [(n, Rows) for n in ("x", "gate", "h", "dh", "dx", "dgate")]
 
 
 class Grad(ctypes.Structure):
@@ -68,6 +78,8 @@ def lib():
             L.conv_embed_bwd_workspace_size.argtypes = [vp]
             L.conv_embed_bwd_workspace_size.restype = sz
             L.conv_embed_bwd.argtypes = [vp] * 5 + [sz, vp]
+            L.conv_scan_fwd.argtypes = [vp] * 9
+            L.conv_scan_bwd.argtypes = [vp] * 13
             L.conv_grad_norm_workspace_size.argtypes = [vp, i32]
             L.conv_grad_norm_workspace_size.restype = sz
             L.conv_grad_norm.argtypes = [vp, i32, vp, vp, sz, vp]
@@ -193,6 +205,68 @@ def embed_bwd(idx, dy, V: int, scale: float = 1.0, padding_idx: int = -1, stream
         with torch.cuda.stream(stream):
             return embed_bwd(idx, dy, V, scale, padding_idx)
     return _native().embed_bwd(idx, dy, V, scale, padding_idx)
+
+
+# ---- gated scan over time --------------------------------------------------------------------
+def _row_distances(t) -> Rows:
+    return Rows(t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def _rows_ptr(t):
+    """The address of a (batch, time, channels) tensor whose channels lie one behind the other."""
+    if t is None:
+        return None
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1 and t.numel() > 0):
+        raise ValueError("(batch, time, channels), a step's channels one behind the other")
+    return _ptr(t[:1, :1]) if t.numel() else _ptr(torch.empty_strided((0,), (1,), dtype=t.dtype, device=t.device))
+
+
+def make_scan_desc(x, gate, h, dh=None, dx=None, dgate=None) -> ScanDesc:
+    """Sizes, type and distances of the call's arrays, each (batch, time, channels)."""
+    d = ScanDesc(*x.shape, _DT[x.dtype])
+    for name, t in (("x", x), ("gate", gate), ("h", h), ("dh", dh), ("dx", dx), ("dgate", dgate)):
+        if t is not None:
+            if t.shape != x.shape or t.dtype != x.dtype:
+                raise ValueError(f"{name}: x's sizes and dtype")
+            setattr(d, name, _row_distances(t))
+    return d
+
+
+def conv_scan_fwd(desc: ScanDesc, x, gate, h0, reset, lengths, h, last, stream=None) -> None:
+    """h0, reset, lengths and last may be None."""
+    _check(lib().conv_scan_fwd(_ref(desc), _rows_ptr(x), _rows_ptr(gate), _ptr(h0), _ptr(reset), _ptr(lengths),
+                               _rows_ptr(h), _ptr(last), _stream(stream)), "conv_scan_fwd")
+
+
+def conv_scan_bwd(desc: ScanDesc, x, gate, h, dh, h0, dlast, reset, lengths, dx, dgate, dh0, stream=None) -> None:
+    """h0, dlast, reset, lengths and dh0 may be None."""
+    _check(lib().conv_scan_bwd(_ref(desc), _rows_ptr(x), _rows_ptr(gate), _rows_ptr(h), _rows_ptr(dh), _ptr(h0),
+                               _ptr(dlast), _ptr(reset), _ptr(lengths), _rows_ptr(dx), _rows_ptr(dgate), _ptr(dh0),
+                               _stream(stream)), "conv_scan_bwd")
+
+
+def gated_scan(x, gate, h0=None, reset=None, lengths=None, out=None, last=None, stream=None):
+    """h, last of h[t] = h[t-1] + sigmoid(gate[t]) * (x[t] - h[t-1]) over (batch, time, channels): every
+    step's state, and the one behind each row's last step (fp32, (batch, channels)).
+
+    x and gate may be views (halves of one projection, time first) as long as a step's channels lie
+    one behind the other.  h0: the states that the rows begin with (fp32).  reset (batch, time), bool
+    or uint8: steps where a new sequence begins with a state of 0.  lengths (batch), int32: the steps
+    that each row has; h is 0 behind them.  out and last: tensors to write to; last may be h0, so that
+    a rollout keeps its states in one place."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gated_scan(x, gate, h0, reset, lengths, out, last)
+    return _native().gated_scan(x, gate, h0, reset, lengths, out, last)
+
+
+def gated_scan_bwd(x, gate, h, dh, h0=None, dlast=None, reset=None, lengths=None, dx=None, dgate=None, stream=None):
+    """dx, dgate, dh0 (None where h0 is) from gated_scan's inputs, its h, and the gradients of h and
+    (dlast, fp32) of last.  dx and dgate: tensors to write to, such as the halves of one gradient."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gated_scan_bwd(x, gate, h, dh, h0, dlast, reset, lengths, dx, dgate)
+    return _native().gated_scan_bwd(x, gate, h, dh, h0, dlast, reset, lengths, dx, dgate)
 
 
 # ---- gradient norm and clipping --------------------------------------------------------------

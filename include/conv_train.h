@@ -98,6 +98,54 @@ size_t conv_embed_bwd_workspace_size(const conv_embed_desc_t* desc);
 int conv_embed_bwd(const conv_embed_desc_t* desc, const void* idx, const void* dy, void* dtable, void* workspace,
                    size_t workspace_bytes, conv_stream_t stream);
 
+/* ---- gated scan over time --------------------------------------------------------------------
+ * For each row b of a batch and each channel, over the steps t = 0 .. T-1:
+ *
+ *   z = 1 / (1 + exp(-gate[b,t]))      h[b,t] = h[b,t-1] + z * (x[b,t] - h[b,t-1])
+ *
+ * with h[b,-1] = h0[b] (fp32; NULL: 0).  last[b] is the state behind the row's last step, in
+ * fp32: one call with T = 1 is one step of a rollout, and `last` may be h0.
+ * reset (B, T), bytes: where it is not 0, h[b,t-1] counts as 0: a new sequence begins at t, and
+ * nothing of the old one, not even a NaN, goes beyond.
+ * lengths (B), int32: row b has its first lengths[b] steps only (0 .. T; less counts as 0, more as
+ * T).  Behind them nothing is read and h is 0.
+ *
+ * Backward, from dh (the gradient that reaches h from outside the scan) and dlast (that reaches
+ * last, fp32; NULL: 0):
+ *
+ *   s[t] = dh[t] + (1 - z[t+1]) * s[t+1]     (no second term across a reset; dlast enters
+ *                                             at the row's last step)
+ *   dx = s * z     dgate = s * (x - h[t-1]) * z * (1 - z)     dh0 = (1 - z[0]) * s[0]
+ *
+ * (dh0 = 0 where step 0 is a reset; dh0 = dlast for a row without steps.)  dx and dgate are 0 behind
+ * a row's length.  h is the forward's output as it is kept: rounded, where it is bf16.
+ *
+ * The states, and every product along the time axis, are fp32.  Time is cut into parts that are
+ * joined in an order that the sizes fix.  A state that is infinite or NaN makes what follows it in
+ * its row and channel, up to the next reset, infinite or NaN.
+ *
+ * x, gate, h, dh, dx and dgate have the descriptor's dtype and lie anywhere: an array's element
+ * (b, t, d) is batch * b + step * t + d elements behind its address, which is a multiple of the
+ * element's size.  So x and gate may be halves of one array, and time may be the outer dimension.
+ * Distances are >= 0, and an output's rows do not overlap.  h0, last, dlast, dh0: fp32, (B, D)
+ * dense. */
+typedef struct { int64_t batch, step; } conv_rows_t;
+
+typedef struct {
+    int32_t B, T, D;        /* B, T >= 0; D >= 1                                           */
+    int32_t dtype;          /* conv_dtype_t                                                */
+    conv_rows_t x, gate, h; /* the backward's h too                                        */
+    conv_rows_t dh, dx, dgate;  /* backward only                                           */
+} conv_scan_desc_t;
+
+/* Limits: B, T, D < 2^31 - 2^20, B * D < 2^40.  B = 0 does nothing.  lengths or reset may be NULL. */
+int conv_scan_fwd(const conv_scan_desc_t* desc, const void* x, const void* gate, const float* h0, const uint8_t* reset,
+                  const int32_t* lengths, void* h, float* last, conv_stream_t stream);
+/* dh0: written, or NULL. */
+int conv_scan_bwd(const conv_scan_desc_t* desc, const void* x, const void* gate, const void* h, const void* dh,
+                  const float* h0, const float* dlast, const uint8_t* reset, const int32_t* lengths, void* dx,
+                  void* dgate, float* dh0, conv_stream_t stream);
+
 /* ---- global gradient norm and clipping ------------------------------------------------------
  *   norm = sqrt(sum over every tensor and element of g^2)
  *   out  = g * min(1, max_norm / (norm + 1e-6))

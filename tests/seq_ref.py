@@ -1,0 +1,69 @@
+"""fp64 references of the sequence operators (numpy), from their definitions, and bounds of the error
+that fp32 arithmetic in any order of the products may leave (the tests' tolerances)."""
+import numpy as np
+
+U = 2.0 ** -24                                   # half a step of fp32
+HALF_STEP = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}  # of a result as it is kept
+
+
+def sigmoid(g):
+    return 0.5 * (1.0 + np.tanh(0.5 * g))
+
+
+def _steps(x, lengths):
+    B, T, _ = x.shape
+    n = np.full(B, T) if lengths is None else np.clip(lengths, 0, T)
+    return np.arange(T)[None, :] < n[:, None]
+
+
+def scan_fwd(x, gate, h0=None, reset=None, lengths=None):
+    """h, last, and a bound of each one's error.
+
+    A step rounds x - h (U), its product with z, whose own error is that of exp and of the quotient
+    ((4 + 1.5 |gate|) U relative), and the sum (U of it); what a step leaves decays with the state, by
+    1 - z a step.  Joining stretches rounds as often again, so all of it counts twice."""
+    B, T, D = x.shape
+    inside = _steps(x, lengths)
+    s = np.zeros((B, D)) if h0 is None else h0.astype(np.float64)
+    e = np.zeros((B, D))
+    h, eh = np.zeros((B, T, D)), np.zeros((B, T, D))
+    for t in range(T):
+        z = sigmoid(gate[:, t])
+        there = inside[:, t][:, None]
+        if reset is not None:
+            fresh = (reset[:, t] != 0)[:, None] & there
+            s, e = np.where(fresh, 0.0, s), np.where(fresh, 0.0, e)
+        new = s + z * (x[:, t] - s)
+        err = (1 - z) * e + 2 * U * (z * (6 + 1.5 * np.abs(gate[:, t])) * (np.abs(x[:, t]) + np.abs(s)) + np.abs(s)
+                                     + np.abs(new))
+        s, e = np.where(there, new, s), np.where(there, err, e)
+        h[:, t], eh[:, t] = np.where(there, s, 0.0), np.where(there, e, 0.0)
+    return h, s, eh, e
+
+
+def scan_bwd(x, gate, h, dh, h0=None, dlast=None, reset=None, lengths=None):
+    """(dx, bound), (dgate, bound), (dh0, bound)."""
+    B, T, D = x.shape
+    inside = _steps(x, lengths)
+    flow = np.zeros((B, D)) if dlast is None else dlast.astype(np.float64)
+    e = np.zeros((B, D))
+    dx, dg, ex, eg = (np.zeros((B, T, D)) for _ in range(4))
+    for t in range(T - 1, -1, -1):
+        z = sigmoid(gate[:, t])
+        there = inside[:, t][:, None]
+        old = h[:, t - 1] if t > 0 else (np.zeros((B, D)) if h0 is None else h0)
+        fresh = np.zeros((B, 1), bool) if reset is None else (reset[:, t] != 0)[:, None]
+        old = np.where(fresh, 0.0, old)
+        lam = dh[:, t] + flow
+        el = e + 2 * U * (np.abs(dh[:, t]) + np.abs(flow))
+        rel = (8 + 3 * np.abs(gate[:, t])) * U   # of z and of z (1 - z)
+        dx[:, t] = np.where(there, z * lam, 0.0)
+        ex[:, t] = np.where(there, z * (el + rel * np.abs(lam)), 0.0)
+        slope, d = z * (1 - z), x[:, t] - old
+        dg[:, t] = np.where(there, lam * d * slope, 0.0)
+        eg[:, t] = np.where(there, slope * (el * np.abs(d) + np.abs(lam) * (rel + 4 * U) * (np.abs(x[:, t]) + np.abs(old))),
+                            0.0)
+        back = np.where(fresh, 0.0, lam - z * lam)
+        eb = np.where(fresh, 0.0, (1 - z) * el + 2 * U * (2 + z * (8 + 3 * np.abs(gate[:, t]))) * np.abs(lam))
+        flow, e = np.where(there, back, flow), np.where(there, eb, e)
+    return (dx, ex), (dg, eg), (flow, e)
