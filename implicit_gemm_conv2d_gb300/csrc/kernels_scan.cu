@@ -1,16 +1,20 @@
 // kernels_scan.cu -- the gated scan over time, h[t] = h[t-1] + z[t] (x[t] - h[t-1]) with
 // z = 1 / (1 + exp(-gate)), and its backward s[t] = dh[t] + (1 - z[t+1]) s[t+1].
 //
-// A stretch of steps acts on the state that enters it as state -> A * state + H, with A the product
-// of its 1 - z and H what it makes of 0; stretches are joined by (A2 A1, A2 H1 + H2).  A thread takes
-// L consecutive steps of V channels: it finds its stretch's (A, H), the block joins those of its
-// threads along time in shared memory, a cluster those of its blocks through distributed shared
-// memory, and the thread walks its steps again from registers with the state it now knows.  So
-// each input is read once, whatever the length, and a long sequence is worked on by many blocks.
-// A block's rows of time (TY), its channels (LX * V) and its batch rows (BY) follow from the sizes.
+// Two ways through time.  Where rows times channels fill the GPU, or there are few steps, a thread walks
+// all steps of two channels, reading a few steps ahead ("walk").  Else time is cut ("parts"):
+// a stretch of steps acts on the state that enters it as state -> A * state + H, with A the product
+// of its 1 - z and H what it makes of 0; stretches are joined by (A2 A1, A2 H1 + H2).  A lane takes
+// L consecutive steps of two channels, a warp 8 such stretches of 8 channels: the warp joins them by
+// shuffles, the warps of a cluster's blocks, which share a sequence's round, through distributed shared
+// memory, and each lane walks its steps again, from registers, with the state it now knows.  So each
+// input is read once, whatever the length, and a long sequence is worked on by many blocks.
+// Rounds travel through shared memory in both directions, whole rows at a time: inputs by
+// asynchronous copies (16 bytes where the rows allow it) that run a round or two ahead, results in
+// the places of the inputs.
 //
-// z (x - h) + h instead of (1 - z) h + z x, and A - z A: where z is small, a long memory, z's own
-// relative error is all that enters, not the rounding of 1 - z.  State, A and H are fp32.
+// State, A and H are fp32, and so is 1 - z, taken from z: where z is small, a long memory, z's error is
+// small beside the rounding of 1 - z, which is that of one more operation a step.
 // A stretch with a reset in it has A = -1: what enters it, be it NaN, is left out and not multiplied by 0.
 #include <algorithm>
 #include <cfloat>
@@ -23,17 +27,35 @@ namespace igc {
 
 namespace {
 
-constexpr int SCAN_THREADS = 256;
+constexpr int SCAN_THREADS = 256, SCAN_WARPS = 8;
+constexpr int SCAN_SEGS = 8;                 // stretches of a warp
+constexpr int SCAN_LENS = 128;               // bytes for the batch rows' lengths
+constexpr int WALK_THREADS = 128;
 
-// e = exp(-gate), infinite where the gate is far below 0, and z = 1 / (1 + e), which is 0 there.
-template <typename T> __device__ __forceinline__ float scan_gate(float g, float& e)
+__device__ unsigned g_scan_status = 0;       // CONV_STATUS_SCAN: a bounded wait ran out
+
+__device__ __forceinline__ float2 one_minus(float2 a) { return fma2(a, both(-1.f), both(1.f)); }
+
+// e = exp(-gate), infinite where the gate is far below 0, and z = 1 / (1 + e), which is 0 there.  fp32 takes
+// expf; for bf16 a rounded argument of 2^x, up to |gate| 2^-24 off, is far below the rounding of h.
+template <typename T> __device__ __forceinline__ float2 scan_gate(float2 g, float2& e)
 {
-    if constexpr (sizeof(T) == 4) e = expf(-g);
-    else e = fast_exp2(g * -kLog2e);
-    return fast_rcp(1.f + e);
+    if constexpr (sizeof(T) == 4) {
+        e = make_float2(expf(-g.x), expf(-g.y));
+    } else {
+        e = mul2(g, both(-kLog2e));
+        e = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+    }
+    const float2 w = add2(e, both(1.f));
+    return make_float2(fast_rcp(w.x), fast_rcp(w.y));
+}
+// z (1 - z) = e z z, also 0 where e is infinite
+__device__ __forceinline__ float2 scan_slope(float2 e, float2 z)
+{
+    return mul2(mul2(make_float2(fminf(e.x, FLT_MAX), fminf(e.y, FLT_MAX)), z), z);
 }
 
-// (A, H) followed by (a, h).
+// (A, H) followed by (a, h), and a state that enters.
 __device__ __forceinline__ void scan_join(float& A, float& H, float a, float h)
 {
     H = a < 0.f ? h : fmaf(a, H, h);
@@ -41,342 +63,653 @@ __device__ __forceinline__ void scan_join(float& A, float& H, float a, float h)
 }
 __device__ __forceinline__ float scan_enter(float A, float H, float state) { return A < 0.f ? H : fmaf(A, state, H); }
 
-// One side's place in the work.
-struct ScanAt {
-    int lx, seg, by;       // thread: lane over channels, stretch, batch row
-    int LX, TY, NC;        // NC: columns (batch row, channel) of the block
-    int C, rank;
-    int b0, c0;            // block: first batch row, first channel
-    __device__ __forceinline__ ScanAt(const ScanPlan& p, int V)
-    {
-        LX = 1 << p.lx_log;
-        TY = 1 << p.ty_log;
-        C = p.cluster;
-        lx = int(threadIdx.x) & (LX - 1);
-        seg = (int(threadIdx.x) >> p.lx_log) & (TY - 1);
-        by = int(threadIdx.x) >> (p.lx_log + p.ty_log);
-        NC = (LX * V) << p.by_log;
-        rank = int(blockIdx.x) % C;
-        const int unit = int(blockIdx.x) / C;
-        b0 = (unit / p.tiles) << p.by_log;
-        c0 = (unit % p.tiles) * LX * V;
-    }
-};
-
 __device__ __forceinline__ int scan_length(const ScanPlan& p, const int32_t* lengths, int b)
 {
     return lengths ? min(max(lengths[b], 0), p.T) : p.T;
 }
 
-// The block's shared memory: (A, H) of each thread's stretch, then of what lies in front of it; the
-// state that enters the block's and the next blocks' steps; the blocks' (A, H), twice in turn.
-struct ScanShared {
-    float *A, *H, *enter, *state, *total;
-    __device__ __forceinline__ ScanShared(float* sm, const ScanAt& q)
-    {
-        const int n = q.TY * q.NC;
-        A = sm;
-        H = A + n;
-        enter = H + n;
-        state = enter + q.NC;
-        total = state + q.NC;
-    }
-};
-
-// Joins the stretches of the block and the cluster along time.  On entry A, H hold each thread's stretch; on
-// return what lies in front of it within the block, `enter` the state that enters the block, `state` the one
-// behind the cluster.  Every thread of the cluster takes part.
-__device__ __forceinline__ void scan_block(const ScanAt& q, const ScanShared& s, int round)
+// ---- walk: a thread takes all steps of V channels -------------------------------------------
+template <typename T, int V> __device__ __forceinline__ float2 widen(const Vec<T, V>& r)
 {
-    __syncthreads();
-    for (int c = int(threadIdx.x); c < q.NC; c += int(blockDim.x)) {
-        float A = 1.f, H = 0.f;
-        for (int k = 0; k < q.TY; ++k) {
-            const float a = s.A[k * q.NC + c], h = s.H[k * q.NC + c];
-            s.A[k * q.NC + c] = A;
-            s.H[k * q.NC + c] = H;
-            scan_join(A, H, a, h);
-        }
-        if (q.C == 1) {
-            const float v = s.state[c];
-            s.enter[c] = v;
-            s.state[c] = scan_enter(A, H, v);
-        } else {
-            const uint32_t at = tc::smem_u32(s.total + (((round & 1) * q.C + q.rank) * q.NC + c) * 2);
-            for (int r = 0; r < q.C; ++r) tc::st_dsmem_f2(tc::dsmem_addr(at, uint32_t(r)), A, H);
-        }
-    }
-    if (q.C > 1) {
-        tc::cluster_sync();
-        for (int c = int(threadIdx.x); c < q.NC; c += int(blockDim.x)) {
-            float v = s.state[c];
-            for (int r = 0; r < q.C; ++r) {
-                if (r == q.rank) s.enter[c] = v;
-                const float2 t = reinterpret_cast<const float2*>(s.total)[((round & 1) * q.C + r) * q.NC + c];
-                v = scan_enter(t.x, t.y, v);
-            }
-            s.state[c] = v;
-        }
-    }
-    __syncthreads();
+    return make_float2(r.get(0), V == 2 ? r.get(V - 1) : 0.f);
 }
-
-// Bit i is set where step t0 + dir * i, i < L, is one of the row's (below len) and a reset.  The lanes of a
-// group of LX, which have the steps in common, read one each.
-template <int L>
-__device__ __forceinline__ uint32_t scan_flags(const ScanAt& q, const uint8_t* row, int64_t t0, int dir, int len)
+template <typename T, int V> __device__ __forceinline__ void put(T* o, float2 v)
 {
-    uint32_t mask = 0;
-    const int group = int(threadIdx.x) & 31 & ~(q.LX - 1);
-    for (int i0 = 0; i0 < L; i0 += q.LX) {
-        const int64_t t = t0 + dir * (i0 + q.lx);
-        const bool set = i0 + q.lx < L && t >= 0 && t < len && row[t] != 0;
-        const uint32_t all = __ballot_sync(0xFFFFFFFFu, set) >> group;
-        mask |= (q.LX == 32 ? all : all & ((1u << q.LX) - 1u)) << i0;
+    Vec<T, V> r;
+    if constexpr (V == 2) {
+        const float f[2] = {v.x, v.y};
+        r.set(f);
+    } else {
+        const float f[1] = {v.x};
+        r.set(f);
     }
-    return mask;
+    r.store(o);
+}
+template <int V> __device__ __forceinline__ float2 walk_state(const float* from, int64_t at)
+{
+    return from ? make_float2(from[at], V == 2 ? from[at + V - 1] : 0.f) : both(0.f);
+}
+template <int V> __device__ __forceinline__ void walk_store(float* to, int64_t at, float2 v)
+{
+    if (!to) return;
+    to[at] = v.x;
+    if constexpr (V == 2) to[at + 1] = v.y;
 }
 
 template <typename T, int V, int L, bool RESET>
-__global__ void __launch_bounds__(SCAN_THREADS)
-scan_fwd_kernel(const __grid_constant__ ScanPlan p, const T* x, const T* gate, const float* h0, const uint8_t* reset,
-                const int32_t* lengths, T* h, float* last)
+__global__ void __launch_bounds__(WALK_THREADS)
+scan_walk_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, const float* h0, const uint8_t* reset,
+              const int32_t* lengths, T* h, float* last)
 {
-    extern __shared__ __align__(16) float sm[];
-    const ScanAt q(p, V);
-    const ScanShared s(sm, q);
-    const int b = q.b0 + q.by, c = q.c0 + q.lx * V;
-    const bool row_in = b < p.B, mine = row_in && c < p.D;
     tc::grid_dep_wait();
     tc::grid_dep_launch();
-    const int row_len = row_in ? scan_length(p, lengths, b) : 0, len = mine ? row_len : 0;
-    for (int k = int(threadIdx.x); k < q.NC; k += int(blockDim.x)) {
-        const int kb = q.b0 + k / (q.LX * V), kc = q.c0 + k % (q.LX * V);
-        s.state[k] = h0 && kb < p.B && kc < p.D ? h0[int64_t(kb) * p.D + kc] : 0.f;
-    }
-    if (q.C > 1) tc::cluster_sync();  // every block of the cluster is there, and has read its h0
-
-    const int first = (q.rank * q.TY + q.seg) * L, span = q.C * q.TY * L;
-    const int64_t xs = p.x.step, gs = p.gate.step, hs = p.h.step;
-    const T* px = x + (mine ? int64_t(b) * p.x.batch + c : 0);
-    const T* pg = gate + (mine ? int64_t(b) * p.gate.batch + c : 0);
-    T* ph = h + (mine ? int64_t(b) * p.h.batch + c : 0);
-    const uint8_t* pr = RESET && row_in ? reset + int64_t(b) * p.T : nullptr;
-
+    const int64_t unit = int64_t(blockIdx.x) * WALK_THREADS + threadIdx.x, b = unit / p.cols, c = unit % p.cols * V;
+    if (b >= p.B) return;
+    const int len = scan_length(p, lengths, int(b));
+    const T *px = x + b * p.x.batch + c, *pg = gate + b * p.gate.batch + c;
+    T* ph = h + b * p.h.batch + c;
+    const uint8_t* pr = RESET ? reset + b * p.T : nullptr;
+    float2 st = walk_state<V>(h0, b * p.D + c);
     Vec<T, V> rx[L], rg[L];
-    uint32_t flags = 0;
-    auto load = [&](int64_t t0) {
-        const int n = t0 >= len ? 0 : int(min(int64_t(L), len - t0));
+    uint8_t rr[L];
+    auto load = [&](int n) {
+        if (n >= L) {
+#pragma unroll
+            for (int i = 0; i < L; ++i, px += p.x.step, pg += p.gate.step) {
+                rx[i].load(px);
+                rg[i].load(pg);
+                if (RESET) rr[i] = pr[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < L; ++i)
+                if (i < n) {
+                    rx[i].load(px + i * p.x.step);
+                    rg[i].load(pg + i * p.gate.step);
+                    if (RESET) rr[i] = pr[i];
+                }
+        }
+        if (RESET) pr += L;
+    };
+    load(len);
+    for (int t = 0; t < len; t += L) {
+        float2 keep[L], in[L];
+        uint32_t cut = 0;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            float2 e;
+            const float2 z = scan_gate<T>(widen(rg[i]), e);
+            keep[i] = one_minus(z);
+            in[i] = mul2(z, widen(rx[i]));
+            if (RESET && rr[i] != 0) cut |= 1u << i;
+        }
+        load(len - t - L);
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            if (t + i < len) {
+                if (RESET && (cut >> i & 1u)) st = both(0.f);
+                st = fma2(keep[i], st, in[i]);
+                put<T, V>(ph, st);
+                ph += p.h.step;
+            }
+        }
+    }
+    for (int t = len; t < p.T; ++t, ph += p.h.step) put<T, V>(ph, both(0.f));
+    walk_store<V>(last, b * p.D + c, st);
+}
+
+template <typename T, int V, int L, bool RESET>
+__global__ void __launch_bounds__(WALK_THREADS)
+scan_walk_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, const T* h, const T* dh, const float* h0,
+              const float* dlast, const uint8_t* reset, const int32_t* lengths, T* dx, T* dgate, float* dh0)
+{
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
+    const int64_t unit = int64_t(blockIdx.x) * WALK_THREADS + threadIdx.x, b = unit / p.cols, c = unit % p.cols * V;
+    if (b >= p.B) return;
+    const int len = scan_length(p, lengths, int(b));
+    const int64_t end = len - 1;  // the pointers are at the next step to read, and the next one to write
+    const T *px = x + b * p.x.batch + c + end * p.x.step, *pg = gate + b * p.gate.batch + c + end * p.gate.step;
+    const T *ph = h + b * p.h.batch + c + (end - 1) * p.h.step, *pd = dh + b * p.dh.batch + c + end * p.dh.step;
+    T *ox = dx + b * p.dx.batch + c + end * p.dx.step, *og = dgate + b * p.dgate.batch + c + end * p.dgate.step;
+    for (int t = len; t < p.T; ++t) {
+        put<T, V>(ox + (t - end) * p.dx.step, both(0.f));
+        put<T, V>(og + (t - end) * p.dgate.step, both(0.f));
+    }
+    const uint8_t* pr = RESET ? reset + b * p.T + end : nullptr;
+    float2 st = walk_state<V>(dlast, b * p.D + c);
+    Vec<T, V> rx[L], rg[L], rh[L], rd[L];
+    uint8_t rr[L];
+    auto load = [&](int n) {  // n steps are left, the last of them step 0, with nothing kept before it
+        if (n > L) {
+#pragma unroll
+            for (int i = 0; i < L; ++i, px -= p.x.step, pg -= p.gate.step, ph -= p.h.step, pd -= p.dh.step) {
+                rx[i].load(px);
+                rg[i].load(pg);
+                rd[i].load(pd);
+                rh[i].load(ph);
+                if (RESET) rr[i] = *(pr - i);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < L; ++i)
+                if (i < n) {
+                    rx[i].load(px - i * p.x.step);
+                    rg[i].load(pg - i * p.gate.step);
+                    rd[i].load(pd - i * p.dh.step);
+                    if (i < n - 1) rh[i].load(ph - i * p.h.step);
+                    if (RESET) rr[i] = *(pr - i);
+                }
+        }
+        if (RESET) pr -= L;
+    };
+    load(len);
+    for (int n = len; n > 0; n -= L) {
+        float2 z[L], d[L], w[L];
+        uint32_t cut = 0;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            float2 e;
+            z[i] = scan_gate<T>(widen(rg[i]), e);
+            d[i] = widen(rd[i]);
+            float2 before = widen(rh[i]);
+            if (i == n - 1) before = walk_state<V>(h0, b * p.D + c);
+            if (RESET && rr[i] != 0) {
+                cut |= 1u << i;
+                before = both(0.f);
+            }
+            w[i] = mul2(scan_slope(e, z[i]), fma2(before, both(-1.f), widen(rx[i])));
+        }
+        load(n - L);
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             if (i < n) {
-                rx[i].load(px + (t0 + i) * xs);
-                rg[i].load(pg + (t0 + i) * gs);
-            }
-        }
-        if constexpr (RESET) flags = scan_flags<L>(q, pr, t0, 1, row_len);
-    };
-    load(first);
-    int round = 0;
-    for (int64_t base = 0; base < p.T; base += span, ++round) {
-        const int64_t t0 = base + first;
-        const int n = t0 >= len ? 0 : int(min(int64_t(L), len - t0));
-        float z[L][V], xv[L][V];
-        const uint32_t cut = flags;
-#pragma unroll
-        for (int i = 0; i < L; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float e;
-                z[i][v] = 0.f;
-                xv[i][v] = 0.f;
-                if (i < n) {
-                    z[i][v] = scan_gate<T>(rg[i].get(v), e);
-                    xv[i][v] = rx[i].get(v);
-                }
-            }
-        if (base + span < p.T) load(t0 + span);
-        float A[V], H[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            A[v] = 1.f;
-            H[v] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < L; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (RESET && (cut >> i & 1u)) H[v] = 0.f;
-                if (i < n) H[v] = fmaf(z[i][v], xv[i][v] - H[v], H[v]);
-                if (i < n) A[v] = fmaf(-z[i][v], A[v], A[v]);
-            }
-        const int col = (q.by * q.LX + q.lx) * V, slot = q.seg * q.NC + col;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            s.A[slot + v] = RESET && cut != 0 ? -1.f : A[v];
-            s.H[slot + v] = H[v];
-        }
-        scan_block(q, s, round);
-        float st[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) st[v] = scan_enter(s.A[slot + v], s.H[slot + v], s.enter[col + v]);
-        if (mine) {
-#pragma unroll
-            for (int i = 0; i < L; ++i) {
-                float out[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    if (RESET && (cut >> i & 1u)) st[v] = 0.f;
-                    if (i < n) st[v] = fmaf(z[i][v], xv[i][v] - st[v], st[v]);
-                    out[v] = i < n ? st[v] : 0.f;
-                }
-                if (t0 + i < p.T) {
-                    Vec<T, V> o;
-                    o.set(out);
-                    o.store(ph + (t0 + i) * hs);
-                }
+                const float2 f = add2(d[i], st);
+                put<T, V>(ox, mul2(z[i], f));
+                put<T, V>(og, mul2(w[i], f));
+                ox -= p.dx.step;
+                og -= p.dgate.step;
+                st = mul2(one_minus(z[i]), f);
+                if (RESET && (cut >> i & 1u)) st = both(0.f);
             }
         }
     }
-    if (last && q.rank == 0) {
-        __syncthreads();
-        for (int k = int(threadIdx.x); k < q.NC; k += int(blockDim.x)) {
-            const int kb = q.b0 + k / (q.LX * V), kc = q.c0 + k % (q.LX * V);
-            if (kb < p.B && kc < p.D) last[int64_t(kb) * p.D + kc] = s.state[k];
+    walk_store<V>(dh0, b * p.D + c, st);
+}
+
+// ---- parts: warps of 8 stretches of 8 channels ------------------------------------------------
+// A block has 8 warps: WX of them side by side over the channels, BY batch rows.  A round of a block is
+// RT = 8 L steps, of a cluster C of those, one behind the other.
+//
+// Shared memory of a stage: [array][step][warp][8 channels], where the 16-byte pieces of a step's row
+// are permuted by the step's stretch, so that the 8 stretches that a warp reads at once lie in
+// different banks.
+template <typename T, int L> struct ScanTile {
+    static constexpr int ES = int(sizeof(T)), ROW = 64 * ES, RT = SCAN_SEGS * L, ARRAY = RT * ROW;
+    // Byte `at` of the row of step u.
+    static __device__ __forceinline__ uint32_t place(int u, int at)
+    {
+        const int seg = u / L;
+        return uint32_t(u * ROW + (at ^ (seg * (ES * 8) & (ROW - 16))));
+    }
+};
+
+struct ScanAt {
+    int warp, pair, seg;   // a lane's pair of channels (of the warp's 8) and stretch
+    int C, rank;
+    int b0, c0;            // block: first batch row, first channel
+    int b, c;              // lane: batch row and first channel
+    __device__ __forceinline__ ScanAt(const ScanPlan& p)
+    {
+        warp = int(threadIdx.x) >> 5;
+        pair = int(threadIdx.x) & 3;
+        seg = (int(threadIdx.x) & 31) >> 2;
+        C = p.cluster;
+        rank = int(blockIdx.x) % C;
+        const int unit = int(blockIdx.x) / C, WX = 1 << p.wx_log;
+        b0 = (unit / p.tiles) << p.by_log;
+        c0 = (unit % p.tiles) * WX * 8;
+        b = b0 + (warp >> p.wx_log);
+        c = c0 + (warp & (WX - 1)) * 8 + pair * 2;
+    }
+};
+
+// An array between memory and a stage.
+template <typename T, int L, int CB> struct ScanCopy {
+    using Tile = ScanTile<T, L>;
+    static constexpr int ES = Tile::ES, CPR = Tile::ROW / CB, ROWS = SCAN_THREADS / CPR, N = Tile::RT / ROWS;
+    static constexpr int UNROLL = N <= 4 || CB == 2 ? std::min(N, 4) : 2;  // (more spills)
+    int at, u0;        // byte in a step's row, first step
+    bool in;           // the channels are there
+    int64_t column;    // elements from the block's first row and channel
+    const int* len;    // of the batch row
+    bool row_in;
+    int by;
+    __device__ __forceinline__ ScanCopy(const ScanPlan& p, const ScanAt& q, const int* lens)
+    {
+        at = int(threadIdx.x) % CPR * CB;
+        u0 = int(threadIdx.x) / CPR;
+        const int el = at / ES, w = el >> 3, c = ((w & ((1 << p.wx_log) - 1)) << 3) + (el & 7);
+        by = w >> p.wx_log;
+        in = q.c0 + c < p.D;
+        row_in = q.b0 + by < p.B;
+        column = c;
+        len = lens + by;
+    }
+    // Steps first + u (BACK: last - u) of the arrays, `shift` steps earlier; those that the row has not are zeros.
+    template <bool BACK>
+    __device__ __forceinline__ void fill(const T* from, const conv_rows_t& r, uint32_t to, int64_t first, int shift) const
+    {
+        const int64_t stride = (BACK ? -1 : 1) * r.step;
+        const T* src = from + by * r.batch + column + (first - shift) * r.step + u0 * stride;
+        const int n = *len;
+        // a thread's steps are ROWS apart
+#pragma unroll UNROLL
+        for (int k = 0; k < N; ++k) {
+            const int u = u0 + k * ROWS;
+            const int64_t t = BACK ? first - u : first + u;
+            const bool there = in && t < n && t >= shift;
+            const T* s = there ? src + k * ROWS * stride : from;
+            const uint32_t dst = to + Tile::place(u, at);
+            if constexpr (CB == 16)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(s), "r"(there ? 16 : 0) : "memory");
+            else if constexpr (CB == 4)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(s), "r"(there ? 4 : 0) : "memory");
+            else
+                tc::sts16(dst, there ? *reinterpret_cast<const uint16_t*>(s) : 0u);
         }
+    }
+    // Back to memory.
+    template <bool BACK>
+    __device__ __forceinline__ void drain(T* to, const conv_rows_t& r, uint32_t from, int64_t first, int T_) const
+    {
+        const int64_t stride = (BACK ? -1 : 1) * r.step;
+        T* dst = to + by * r.batch + column + first * r.step + u0 * stride;
+        if (!in || !row_in) return;
+#pragma unroll UNROLL
+        for (int k = 0; k < N; ++k) {
+            const int u = u0 + k * ROWS;
+            const int64_t t = BACK ? first - u : first + u;
+            if (t < 0 || t >= T_) continue;
+            const uint32_t src = from + Tile::place(u, at);
+            T* d = dst + k * ROWS * stride;
+            if constexpr (CB == 16) *reinterpret_cast<int4*>(d) = tc::lds128(src);
+            else if constexpr (CB == 4) *reinterpret_cast<uint32_t*>(d) = tc::lds32(src);
+            else *reinterpret_cast<uint16_t*>(d) = uint16_t(tc::lds16(src));
+        }
+    }
+};
+
+// A lane's two channels of its stretch's steps.
+template <typename T, int L> struct ScanLane {
+    using Tile = ScanTile<T, L>;
+    uint32_t at;
+    __device__ __forceinline__ explicit ScanLane(const ScanAt& q)
+        : at(Tile::place(q.seg * L, q.warp * 8 * Tile::ES + q.pair * 2 * Tile::ES)) {}
+    __device__ __forceinline__ float2 read(uint32_t stage, int array, int i) const
+    {
+        const uint32_t a = stage + at + uint32_t(array * Tile::ARRAY + i * Tile::ROW);
+        if constexpr (sizeof(T) == 4) {
+            const uint2 u = tc::lds64(a);
+            return make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+        } else {
+            const uint32_t u = tc::lds32(a);
+            return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+        }
+    }
+    __device__ __forceinline__ void write(uint32_t stage, int array, int i, float2 v) const
+    {
+        const uint32_t a = stage + at + uint32_t(array * Tile::ARRAY + i * Tile::ROW);
+        if constexpr (sizeof(T) == 4) {
+            tc::sts64(a, __float_as_uint(v.x), __float_as_uint(v.y));
+        } else {
+            const __nv_bfloat162 r = __floats2bfloat162_rn(v.x, v.y);
+            tc::sts32(a, *reinterpret_cast<const uint32_t*>(&r));
+        }
+    }
+};
+
+// The warp's stretches joined along time, and with those of the same warp in the cluster's other blocks.
+struct ScanExchange {
+    uint32_t bars, slots;  // two mbarriers a warp; [parity][rank][warp][pair] of (A, H) twice
+    bool dead = false;
+
+    __device__ __forceinline__ void init(const ScanAt& q, uint32_t sm)
+    {
+        bars = sm + uint32_t(q.warp * 16);
+        slots = sm + SCAN_WARPS * 16;
+        if (q.C > 1 && (threadIdx.x & 31) == 0) {
+            tc::mbar_init(bars, 1);
+            tc::mbar_init(bars + 8, 1);
+            tc::fence_mbar_init();
+        }
+    }
+    // Behind a barrier of the cluster: the first two rounds may come in.
+    __device__ __forceinline__ void arm(const ScanAt& q, int parity) const
+    {
+        if ((threadIdx.x & 31) == 0) tc::mbar_arrive_expect_tx(bars + uint32_t(parity) * 8, uint32_t(q.C) * 64u);
+    }
+    // (A, H): the lane's stretch.  state: in, what enters the round; out, what enters the next one.  Returns what
+    // enters the lane's stretch.
+    template <bool RESET>
+    __device__ __forceinline__ float2 run(const ScanAt& q, int round, float2 A, float2 H, float2& state)
+    {
+        constexpr unsigned ALL = 0xFFFFFFFFu;
+        // inclusive over the stretches
+#pragma unroll
+        for (int o = 4; o < 32; o *= 2) {
+            const float2 a = make_float2(__shfl_up_sync(ALL, A.x, o), __shfl_up_sync(ALL, A.y, o));
+            const float2 h = make_float2(__shfl_up_sync(ALL, H.x, o), __shfl_up_sync(ALL, H.y, o));
+            if (int(threadIdx.x & 31) >= o) {
+                if constexpr (RESET) {
+                    H.x = scan_enter(A.x, H.x, h.x);
+                    H.y = scan_enter(A.y, H.y, h.y);
+                    A.x = A.x < 0.f || a.x < 0.f ? -1.f : A.x * a.x;
+                    A.y = A.y < 0.f || a.y < 0.f ? -1.f : A.y * a.y;
+                } else {
+                    H = fma2(A, h, H);
+                    A = mul2(A, a);
+                }
+            }
+        }
+        float2 enter = state;
+        if (q.C > 1) {
+            const int parity = round & 1;
+            const uint32_t base = slots + uint32_t((parity * q.C * SCAN_WARPS + q.warp) * 64 + q.pair * 16);
+            if (q.seg == SCAN_SEGS - 1 && !dead) {
+                const uint32_t mine = base + uint32_t(q.rank * SCAN_WARPS * 64), bar = bars + uint32_t(parity) * 8;
+                for (int r = 0; r < q.C; ++r)
+                    tc::st_async_f4(tc::dsmem_addr(mine, uint32_t(r)), tc::dsmem_addr(bar, uint32_t(r)), A.x, A.y, H.x, H.y);
+            }
+            if (!dead && !tc::mbar_wait(bars + uint32_t(parity) * 8, uint32_t(round >> 1) & 1u)) {
+                dead = true;  // the results are wrong and the status says so; every later wait is skipped
+                atomicOr(&g_scan_status, CONV_STATUS_SCAN);
+            }
+            if (!dead) arm(q, parity);  // of the round after the next
+            float2 s = state;
+            for (int r = 0; r < q.C; ++r) {
+                if (r == q.rank) enter = s;
+                const float4 v = tc::lds_f4(base + uint32_t(r * SCAN_WARPS * 64));
+                s = make_float2(scan_enter(v.x, v.z, s.x), scan_enter(v.y, v.w, s.y));
+            }
+            state = s;
+            __syncwarp();  // read by all before the next round but one is announced
+        } else {
+            const float2 s = make_float2(scan_enter(A.x, H.x, state.x), scan_enter(A.y, H.y, state.y));
+            const int from = 28 + q.pair;
+            state = make_float2(__shfl_sync(ALL, s.x, from), __shfl_sync(ALL, s.y, from));
+        }
+        // what the stretches in front of this one make of it
+        const float2 s = make_float2(scan_enter(A.x, H.x, enter.x), scan_enter(A.y, H.y, enter.y));
+        const float2 f = make_float2(__shfl_up_sync(ALL, s.x, 4), __shfl_up_sync(ALL, s.y, 4));
+        return q.seg == 0 ? enter : f;
+    }
+};
+
+// The reset flags of a lane's stretch, a bit a step.  The four lanes of a stretch read a step each, a round ahead.
+template <int L, int DIR> struct ScanFlags {
+    const uint8_t* row = nullptr;
+    int len = 0;
+    uint32_t next = 0;
+    __device__ __forceinline__ void fetch(const ScanAt& q, int64_t t0)
+    {
+        next = 0;
+#pragma unroll
+        for (int k = 0; k < L / 4; ++k) {
+            const int64_t t = t0 + DIR * (q.pair + 4 * k);
+            if (row && t >= 0 && t < len && row[t] != 0) next |= 1u << (4 * k);
+        }
+    }
+    __device__ __forceinline__ uint32_t take(const ScanAt& q) const
+    {
+        uint32_t m = next << q.pair;
+        m |= __shfl_xor_sync(0xFFFFFFFFu, m, 1);
+        return m | __shfl_xor_sync(0xFFFFFFFFu, m, 2);
+    }
+};
+
+__device__ __forceinline__ void scan_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void scan_arrived(int stages)
+{
+    if (stages == 3) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+}
+
+// Lengths of the block's batch rows, the exchange; returns the address of the stages.
+__device__ __forceinline__ uint32_t scan_setup(const ScanPlan& p, const ScanAt& q, const int32_t* lengths, int* lens,
+                                               uint32_t exchange, ScanExchange& ex)
+{
+    if (int(threadIdx.x) < 1 << p.by_log) {
+        const int b = q.b0 + int(threadIdx.x);
+        lens[threadIdx.x] = b < p.B ? scan_length(p, lengths, b) : 0;
+    }
+    ex.init(q, exchange);
+    if (q.C > 1) {
+        tc::cluster_sync();  // every block of the cluster is there
+        ex.arm(q, 0);
+        ex.arm(q, 1);
+    } else {
+        __syncthreads();
+    }
+    return exchange + (q.C > 1 ? SCAN_WARPS * 16 + 2 * q.C * SCAN_WARPS * 64 : 0);
+}
+
+__device__ __forceinline__ float2 scan_state(const ScanPlan& p, const ScanAt& q, const float* from)
+{
+    float2 s = both(0.f);
+    if (from && q.b < p.B && q.c < p.D) {
+        s.x = from[int64_t(q.b) * p.D + q.c];
+        if (q.c + 1 < p.D) s.y = from[int64_t(q.b) * p.D + q.c + 1];
+    }
+    return s;
+}
+__device__ __forceinline__ void scan_store(const ScanPlan& p, const ScanAt& q, float* to, float2 s)
+{
+    if (to && q.rank == 0 && q.seg == 0 && q.b < p.B && q.c < p.D) {
+        to[int64_t(q.b) * p.D + q.c] = s.x;
+        if (q.c + 1 < p.D) to[int64_t(q.b) * p.D + q.c + 1] = s.y;
     }
 }
 
-// Time runs backwards: a thread's stretch is the steps t = T - 1 - u, u = u0 .. u0 + L - 1, and the state is what
-// flows from step t into t - 1, (1 - z[t]) s[t].
-template <typename T, int V, int L, bool RESET>
-__global__ void __launch_bounds__(SCAN_THREADS)
-scan_bwd_kernel(const __grid_constant__ ScanPlan p, const T* x, const T* gate, const T* h, const T* dh, const float* h0,
-                const float* dlast, const uint8_t* reset, const int32_t* lengths, T* dx, T* dgate, float* dh0)
+template <typename T, int L, int CB, bool RESET>
+__global__ void __launch_bounds__(SCAN_THREADS, 3)
+scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, const float* h0, const uint8_t* reset,
+              const int32_t* lengths, T* h, float* last)
 {
-    extern __shared__ __align__(16) float sm[];
-    const ScanAt q(p, V);
-    const ScanShared s(sm, q);
-    const int b = q.b0 + q.by, c = q.c0 + q.lx * V;
-    const bool row_in = b < p.B, mine = row_in && c < p.D;
+    extern __shared__ __align__(128) uint8_t sm[];
+    int* const lens = reinterpret_cast<int*>(sm);
+    using Tile = ScanTile<T, L>;
+    constexpr int STAGE = 2 * Tile::ARRAY;
+    const ScanAt q(p);
+    ScanExchange ex;
     tc::grid_dep_wait();
     tc::grid_dep_launch();
-    const int row_len = row_in ? scan_length(p, lengths, b) : 0, len = mine ? row_len : 0;
-    for (int k = int(threadIdx.x); k < q.NC; k += int(blockDim.x)) {
-        const int kb = q.b0 + k / (q.LX * V), kc = q.c0 + k % (q.LX * V);
-        s.state[k] = dlast && kb < p.B && kc < p.D ? dlast[int64_t(kb) * p.D + kc] : 0.f;
+    float2 state = scan_state(p, q, h0);
+    const uint32_t stages = scan_setup(p, q, lengths, lens, tc::smem_u32(sm) + SCAN_LENS, ex);
+    const int len = lens[q.warp >> p.wx_log];
+    const ScanCopy<T, L, CB> copy(p, q, lens);
+    const ScanLane<T, L> lane(q);
+    const T *bx = x + q.b0 * p.x.batch + q.c0, *bg = gate + q.b0 * p.gate.batch + q.c0;
+    T* bh = h + q.b0 * p.h.batch + q.c0;
+    const int64_t span = int64_t(q.C) * Tile::RT, rank0 = int64_t(q.rank) * Tile::RT;
+    ScanFlags<L, 1> flags;
+    if (RESET && q.b < p.B) {
+        flags.row = reset + int64_t(q.b) * p.T;
+        flags.len = len;
+        flags.fetch(q, rank0 + q.seg * L);
     }
-    if (q.C > 1) tc::cluster_sync();
-
-    const int first = (q.rank * q.TY + q.seg) * L, span = q.C * q.TY * L;
-    const int64_t row = mine ? b : 0, ch = mine ? c : 0;
-    const T* px = x + row * p.x.batch + ch;
-    const T* pg = gate + row * p.gate.batch + ch;
-    const T* ph = h + row * p.h.batch + ch;
-    const T* pd = dh + row * p.dh.batch + ch;
-    T* ox = dx + row * p.dx.batch + ch;
-    T* og = dgate + row * p.dgate.batch + ch;
-    const uint8_t* pr = RESET && row_in ? reset + int64_t(b) * p.T : nullptr;
-
-    Vec<T, V> rx[L], rg[L], rh[L], rd[L];
-    uint32_t flags = 0;
-    auto load = [&](int64_t u0) {
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            const int64_t t = p.T - 1 - u0 - i;
-            if (t >= 0 && t < len) {
-                rx[i].load(px + t * p.x.step);
-                rg[i].load(pg + t * p.gate.step);
-                rd[i].load(pd + t * p.dh.step);
-                if (t > 0) rh[i].load(ph + (t - 1) * p.h.step);
-            }
+    auto fill = [&](int slot, int64_t base) {
+        if (base < p.T) {
+            copy.template fill<false>(bx, p.x, stages + slot * STAGE, base + rank0, 0);
+            copy.template fill<false>(bg, p.gate, stages + slot * STAGE + Tile::ARRAY, base + rank0, 0);
         }
-        if constexpr (RESET) flags = scan_flags<L>(q, pr, p.T - 1 - u0, -1, row_len);
+        scan_commit();
     };
-    load(first);
-    int round = 0;
+    for (int k = 0; k < p.stages - 1; ++k) fill(k, k * span);
+    int now = 0, round = 0;
     for (int64_t base = 0; base < p.T; base += span, ++round) {
-        const int64_t u0 = base + first;
-        float z[L][V], zz[L][V], d[L][V], xh[L][V];
-        const uint32_t cut = flags;
-        uint32_t has = 0;
+        const int prev = now == 0 ? p.stages - 1 : now - 1;
+        scan_arrived(p.stages);
+        if (round > 0) copy.template drain<false>(bh, p.h, stages + prev * STAGE, base - span + rank0, p.T);
+        fill(prev, base + (p.stages - 1) * span);
+        const uint32_t stage = stages + now * STAGE;
+        const int64_t t0 = base + rank0 + q.seg * L;
+        uint32_t cut = 0;
+        if (RESET) {
+            cut = flags.take(q);
+            flags.fetch(q, t0 + span);
+        }
+        // a step is h -> keep h + in; one that the row does not have keeps it as it is
+        float2 keep[L], in[L];
 #pragma unroll
         for (int i = 0; i < L; ++i) {
-            const int64_t t = p.T - 1 - u0 - i;
-            if (t >= 0 && t < len) has |= 1u << i;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                z[i][v] = zz[i][v] = d[i][v] = xh[i][v] = 0.f;
-                if (has >> i & 1u) {
-                    float e;
-                    z[i][v] = scan_gate<T>(rg[i].get(v), e);
-                    zz[i][v] = fminf(e, FLT_MAX) * z[i][v] * z[i][v];  // z (1 - z); 0 where e is infinite
-                    d[i][v] = rd[i].get(v);
-                    float before = t > 0 ? rh[i].get(v) : (h0 ? h0[row * p.D + ch + v] : 0.f);
-                    if (RESET && (cut >> i & 1u)) before = 0.f;
-                    xh[i][v] = rx[i].get(v) - before;
-                }
-            }
+            float2 e;
+            const float2 z = scan_gate<T>(lane.read(stage, 1, i), e);
+            keep[i] = one_minus(z);
+            in[i] = mul2(z, lane.read(stage, 0, i));
         }
-        if (base + span < p.T) load(u0 + span);
-        float A[V], H[V];
+        const bool full = t0 + L <= len;
+        if (!full) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            A[v] = 1.f;
-            H[v] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < L; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (has >> i & 1u) {
-                    const float f = d[i][v] + H[v];
-                    H[v] = RESET && (cut >> i & 1u) ? 0.f : fmaf(-z[i][v], f, f);
-                    A[v] = fmaf(-z[i][v], A[v], A[v]);
+            for (int i = 0; i < L; ++i)
+                if (t0 + i >= len) {
+                    keep[i] = both(1.f);
+                    in[i] = both(0.f);
                 }
-            }
-        const int col = (q.by * q.LX + q.lx) * V, slot = q.seg * q.NC + col;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            s.A[slot + v] = RESET && cut != 0 ? -1.f : A[v];
-            s.H[slot + v] = H[v];
         }
-        scan_block(q, s, round);
-        float st[V];
+        float2 A = both(1.f), H = both(0.f);
 #pragma unroll
-        for (int v = 0; v < V; ++v) st[v] = scan_enter(s.A[slot + v], s.H[slot + v], s.enter[col + v]);
-        if (mine) {
-#pragma unroll
-            for (int i = 0; i < L; ++i) {
-                float a[V], g[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    a[v] = g[v] = 0.f;
-                    if (has >> i & 1u) {
-                        const float f = d[i][v] + st[v];
-                        a[v] = z[i][v] * f;
-                        g[v] = f * xh[i][v] * zz[i][v];
-                        st[v] = RESET && (cut >> i & 1u) ? 0.f : fmaf(-z[i][v], f, f);
-                    }
-                }
-                const int64_t t = p.T - 1 - u0 - i;
-                if (t >= 0) {
-                    Vec<T, V> o;
-                    o.set(a);
-                    o.store(ox + t * p.dx.step);
-                    o.set(g);
-                    o.store(og + t * p.dgate.step);
-                }
-            }
+        for (int i = 0; i < L; ++i) {
+            if (RESET && (cut >> i & 1u)) H = both(0.f);
+            H = fma2(keep[i], H, in[i]);
+            A = mul2(A, keep[i]);
         }
+        if (RESET && cut != 0) A = both(-1.f);
+        float2 st = ex.run<RESET>(q, round, A, H, state);
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            if (RESET && (cut >> i & 1u)) st = both(0.f);
+            st = fma2(keep[i], st, in[i]);
+            lane.write(stage, 0, i, full || t0 + i < len ? st : both(0.f));
+        }
+        now = now + 1 == p.stages ? 0 : now + 1;
     }
-    if (dh0 && q.rank == 0) {
+    if (round > 0) {
         __syncthreads();
-        for (int k = int(threadIdx.x); k < q.NC; k += int(blockDim.x)) {
-            const int kb = q.b0 + k / (q.LX * V), kc = q.c0 + k % (q.LX * V);
-            if (kb < p.B && kc < p.D) dh0[int64_t(kb) * p.D + kc] = s.state[k];
-        }
+        copy.template drain<false>(bh, p.h, stages + (now == 0 ? p.stages - 1 : now - 1) * STAGE,
+                                   (round - 1) * span + rank0, p.T);
     }
+    scan_store(p, q, last, state);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (q.C > 1) tc::cluster_sync();  // nothing is sent to a block that has ended
+}
+
+// Time runs backwards: a lane's stretch is the steps t = T - 1 - u, u = u0 .. u0 + L - 1, and the state is what
+// flows from step t into t - 1, (1 - z[t]) s[t].
+template <typename T, int L, int CB, bool RESET>
+__global__ void __launch_bounds__(SCAN_THREADS, 3)
+scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, const T* h, const T* dh, const float* h0,
+              const float* dlast, const uint8_t* reset, const int32_t* lengths, T* dx, T* dgate, float* dh0)
+{
+    extern __shared__ __align__(128) uint8_t sm[];
+    int* const lens = reinterpret_cast<int*>(sm);
+    using Tile = ScanTile<T, L>;
+    constexpr int STAGE = 4 * Tile::ARRAY;
+    const ScanAt q(p);
+    ScanExchange ex;
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
+    float2 state = scan_state(p, q, dlast);
+    const uint32_t stages = scan_setup(p, q, lengths, lens, tc::smem_u32(sm) + SCAN_LENS, ex);
+    const int len = lens[q.warp >> p.wx_log];
+    const ScanCopy<T, L, CB> copy(p, q, lens);
+    const ScanLane<T, L> lane(q);
+    const T *bx = x + q.b0 * p.x.batch + q.c0, *bg = gate + q.b0 * p.gate.batch + q.c0;
+    const T *bh = h + q.b0 * p.h.batch + q.c0, *bd = dh + q.b0 * p.dh.batch + q.c0;
+    T *ox = dx + q.b0 * p.dx.batch + q.c0, *og = dgate + q.b0 * p.dgate.batch + q.c0;
+    const int64_t span = int64_t(q.C) * Tile::RT, last0 = int64_t(p.T) - 1 - int64_t(q.rank) * Tile::RT;
+    ScanFlags<L, -1> flags;
+    if (RESET && q.b < p.B) {
+        flags.row = reset + int64_t(q.b) * p.T;
+        flags.len = len;
+        flags.fetch(q, last0 - q.seg * L);
+    }
+    auto fill = [&](int slot, int64_t base) {
+        if (base < p.T) {
+            const uint32_t to = stages + slot * STAGE;
+            copy.template fill<true>(bx, p.x, to, last0 - base, 0);
+            copy.template fill<true>(bg, p.gate, to + Tile::ARRAY, last0 - base, 0);
+            copy.template fill<true>(bd, p.dh, to + 2 * Tile::ARRAY, last0 - base, 0);
+            copy.template fill<true>(bh, p.h, to + 3 * Tile::ARRAY, last0 - base, 1);
+        }
+        scan_commit();
+    };
+    auto drain = [&](int slot, int64_t base) {
+        copy.template drain<true>(ox, p.dx, stages + slot * STAGE, last0 - base, p.T);
+        copy.template drain<true>(og, p.dgate, stages + slot * STAGE + Tile::ARRAY, last0 - base, p.T);
+    };
+    for (int k = 0; k < p.stages - 1; ++k) fill(k, k * span);
+    int now = 0, round = 0;
+    for (int64_t base = 0; base < p.T; base += span, ++round) {
+        const int prev = now == 0 ? p.stages - 1 : now - 1;
+        scan_arrived(p.stages);
+        if (round > 0) drain(prev, base - span);
+        fill(prev, base + (p.stages - 1) * span);
+        const uint32_t stage = stages + now * STAGE;
+        const int64_t t0 = last0 - base - q.seg * L;
+        uint32_t cut = 0;
+        if (RESET) {
+            cut = flags.take(q);
+            flags.fetch(q, t0 - span);
+        }
+        const bool full = t0 < len && t0 - L + 1 > 0;  // the row has all of the steps, and one before them
+        // s = d + state, state -> (1 - z) s; dx = z s, dgate = w s
+        float2 z[L], d[L], w[L];
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            float2 e;
+            z[i] = scan_gate<T>(lane.read(stage, 1, i), e);
+            d[i] = lane.read(stage, 2, i);
+            float2 before = lane.read(stage, 3, i);
+            if (!full && t0 == i) before = scan_state(p, q, h0);
+            if (RESET && (cut >> i & 1u)) before = both(0.f);
+            w[i] = mul2(scan_slope(e, z[i]), fma2(before, both(-1.f), lane.read(stage, 0, i)));
+        }
+        if (!full) {
+#pragma unroll
+            for (int i = 0; i < L; ++i)
+                if (t0 - i < 0 || t0 - i >= len) z[i] = d[i] = w[i] = both(0.f);
+        }
+        float2 A = both(1.f), H = both(0.f);
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            const float2 keep = one_minus(z[i]);
+            H = mul2(keep, add2(d[i], H));
+            if (RESET && (cut >> i & 1u)) H = both(0.f);
+            A = mul2(A, keep);
+        }
+        if (RESET && cut != 0) A = both(-1.f);
+        float2 st = ex.run<RESET>(q, round, A, H, state);
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            const float2 f = add2(d[i], st);
+            float2 a = mul2(z[i], f), g = mul2(w[i], f);
+            st = mul2(one_minus(z[i]), f);
+            if (RESET && (cut >> i & 1u)) st = both(0.f);
+            if (!full && t0 - i >= len) a = g = both(0.f);
+            lane.write(stage, 0, i, a);
+            lane.write(stage, 1, i, g);
+        }
+        now = now + 1 == p.stages ? 0 : now + 1;
+    }
+    if (round > 0) {
+        __syncthreads();
+        drain(now == 0 ? p.stages - 1 : now - 1, (round - 1) * span);
+    }
+    scan_store(p, q, dh0, state);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (q.C > 1) tc::cluster_sync();
 }
 
 int log2_up(int64_t n)
@@ -388,91 +721,144 @@ int log2_up(int64_t n)
 
 }  // namespace
 
-// V channels a thread: two bf16 where every row begins at a multiple of 4 bytes.
-ScanPlan scan_plan(const conv_scan_desc_t& e, const DevInfo& d, bool bwd, bool pairs)
+// `chunk`: bytes that every row begins at a multiple of, 16 at most.
+ScanPlan scan_plan(const conv_scan_desc_t& e, const DevInfo& d, bool bwd, int chunk)
 {
     ScanPlan p = {};
+    const int es = e.dtype == CONV_F32 ? 4 : 2;
     p.B = e.B; p.T = e.T; p.D = e.D;
     p.x = e.x; p.gate = e.gate; p.h = e.h; p.dh = e.dh; p.dx = e.dx; p.dgate = e.dgate;
-    p.V = e.dtype == CONV_BF16 && pairs && e.D % 2 == 0 ? 2 : 1;
-    p.L = e.T <= 8 ? 4 : bwd ? 8 : 16;
-    const int64_t cols = (int64_t(e.D) + p.V - 1) / p.V, segs = std::max<int64_t>(1, (int64_t(e.T) + p.L - 1) / p.L);
-    const int all = log2_up(SCAN_THREADS);
-    int log_c = 0;
-    int64_t blocks = 0;
-    p.lx_log = std::min(5, log2_up(cols));
-    for (;;) {
-        p.ty_log = std::min(all - p.lx_log, log2_up(segs));
-        p.by_log = std::max(std::min(all - p.lx_log - p.ty_log, log2_up(std::max(1, e.B))), 5 - p.lx_log - p.ty_log);
-        p.tiles = int((cols + (1 << p.lx_log) - 1) >> p.lx_log);
-        blocks = int64_t(p.tiles) * ((int64_t(e.B) + (1 << p.by_log) - 1) >> p.by_log);
-        log_c = 0;
-        while (log_c < 3 && (blocks << log_c) < 2 * d.sms && (int64_t(1) << (log_c + p.ty_log)) < segs) ++log_c;
-        if ((blocks << log_c) >= d.sms || p.lx_log <= 3 || (int64_t(1) << (log_c + p.ty_log)) >= segs) break;
-        --p.lx_log;
+    const bool pairs = chunk >= 2 * es && e.D % 2 == 0;
+    p.V = pairs ? 2 : 1;
+    p.cols = (e.D + p.V - 1) / p.V;
+    const int64_t walkers = int64_t(e.B) * ((int64_t(e.D) + 1) / 2);
+    p.walk = e.T <= 16 || walkers >= int64_t(d.sms) * 384;
+    if (p.walk) {
+        p.L = e.T == 1 ? 1 : 8;
+        p.threads = WALK_THREADS;
+        p.cluster = 1;
+        p.blocks = (int64_t(e.B) * p.cols + WALK_THREADS - 1) / WALK_THREADS;
+        return p;
     }
+    p.CB = chunk >= 16 && e.D % (16 / es) == 0 ? 16 : es == 4 || (chunk >= 4 && e.D % 2 == 0) ? 4 : 2;
+    p.L = bwd && es == 4 ? 4 : 8;
+    p.wx_log = std::min(3, log2_up((int64_t(e.D) + 7) / 8));
+    p.by_log = 3 - p.wx_log;
+    p.tiles = int((int64_t(e.D) + (8 << p.wx_log) - 1) / (8 << p.wx_log));
+    const int64_t blocks = int64_t(p.tiles) * ((int64_t(e.B) + (1 << p.by_log) - 1) >> p.by_log);
+    const int64_t rounds = (int64_t(e.T) + SCAN_SEGS * p.L - 1) / (SCAN_SEGS * p.L);
+    int log_c = 0;
+    while (log_c < 3 && (blocks << log_c) < 2 * d.sms && (int64_t(1) << log_c) < rounds) ++log_c;
     p.cluster = 1 << log_c;
+    p.threads = SCAN_THREADS;
     p.blocks = blocks << log_c;
-    p.threads = 1 << (p.lx_log + p.ty_log + p.by_log);
+    p.stages = es == 2 && !bwd ? 3 : 2;
     return p;
 }
 
 namespace {
 
-int scan_smem(const ScanPlan& p)
+int scan_smem(const ScanPlan& p, int es, bool bwd)
 {
-    const int nc = (p.V << p.lx_log) << p.by_log, n = nc << p.ty_log;
-    return 4 * (2 * n + 2 * nc + (p.cluster > 1 ? 4 * p.cluster * nc : 0));
+    if (p.walk) return 0;
+    return SCAN_LENS + (p.cluster > 1 ? SCAN_WARPS * 16 + 2 * p.cluster * SCAN_WARPS * 64 : 0) +
+           p.stages * (bwd ? 4 : 2) * SCAN_SEGS * p.L * 64 * es;
 }
 
-// Calls f(T(), V, L, RESET), the last three as types, for the plan; LONG: the larger L.
-template <int LONG, class F> cudaError_t scan_with(const ScanPlan& p, int dt, bool reset, F&& f)
+template <int N> using Int = std::integral_constant<int, N>;
+
+// Calls f(T(), L, CB, RESET), the last three as types, for the plan of a call in parts, and g(T(), V, L, RESET) for one
+// that walks.
+template <bool BWD, class F, class G> cudaError_t scan_with(const ScanPlan& p, int dt, bool reset, F&& f, G&& g)
 {
-    auto on_reset = [&](auto t, auto v, auto l) {
-        return reset ? f(t, v, l, std::true_type()) : f(t, v, l, std::false_type());
+    auto parts = [&](auto t, auto r) {
+        using L = Int<BWD && sizeof(t) == 4 ? 4 : 8>;
+        if (p.CB == 16) return f(t, L(), Int<16>(), r);
+        if constexpr (sizeof(t) == 2)
+            if (p.CB == 2) return f(t, L(), Int<2>(), r);
+        return f(t, L(), Int<4>(), r);
     };
-    auto on_steps = [&](auto t, auto v) {
-        return p.L == 4 ? on_reset(t, v, std::integral_constant<int, 4>())
-                        : on_reset(t, v, std::integral_constant<int, LONG>());
+    auto walk = [&](auto t, auto r) {
+        if (p.L == 1) return p.V == 2 ? g(t, Int<2>(), Int<1>(), r) : g(t, Int<1>(), Int<1>(), r);
+        return p.V == 2 ? g(t, Int<2>(), Int<8>(), r) : g(t, Int<1>(), Int<8>(), r);
     };
-    if (dt == DT_F32) return on_steps(float(), std::integral_constant<int, 1>());
-    if (p.V == 2) return on_steps(__nv_bfloat16(), std::integral_constant<int, 2>());
-    return on_steps(__nv_bfloat16(), std::integral_constant<int, 1>());
+    auto on_reset = [&](auto t) {
+        if (p.walk) return reset ? walk(t, std::true_type()) : walk(t, std::false_type());
+        return reset ? parts(t, std::true_type()) : parts(t, std::false_type());
+    };
+    return dt == DT_F32 ? on_reset(float()) : on_reset(__nv_bfloat16());
 }
 
-bool rows_even(const conv_rows_t& r) { return r.batch % 2 == 0 && r.step % 2 == 0; }
-bool at_pair(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// What every row of the array begins at a multiple of, in bytes: 16, 8, 4 or 2.
+int rows_chunk(const void* p, const conv_rows_t& r, int es)
+{
+    const uint64_t all = reinterpret_cast<uintptr_t>(p) | uint64_t(r.batch) * es | uint64_t(r.step) * es;
+    return all % 16 == 0 ? 16 : all % 8 == 0 ? 8 : all % 4 == 0 ? 4 : 2;
+}
 
 }  // namespace
 
 cudaError_t run_scan_fwd(const conv_scan_desc_t& e, const DevInfo& d, const void* x, const void* gate, const float* h0,
                          const uint8_t* reset, const int32_t* lengths, void* h, float* last, cudaStream_t s)
 {
-    const bool pairs = rows_even(e.x) && rows_even(e.gate) && rows_even(e.h) && at_pair(x) && at_pair(gate) && at_pair(h);
-    const ScanPlan p = scan_plan(e, d, false, pairs);
-    return scan_with<16>(p, e.dtype, reset != nullptr, [&](auto t, auto v, auto l, auto r) {
+    const int es = e.dtype == CONV_F32 ? 4 : 2;
+    const int chunk = std::min({rows_chunk(x, e.x, es), rows_chunk(gate, e.gate, es), rows_chunk(h, e.h, es)});
+    const ScanPlan p = scan_plan(e, d, false, chunk);
+    const int smem = scan_smem(p, es, false);
+    auto launch = [&](auto kern, auto t) {
         using T = decltype(t);
-        return launch_ex(scan_fwd_kernel<T, decltype(v)::value, decltype(l)::value, decltype(r)::value>, dim3(unsigned(p.blocks)), dim3(p.threads), scan_smem(p), s,
-                         p.cluster, true, p, static_cast<const T*>(x), static_cast<const T*>(gate), h0, reset, lengths,
-                         static_cast<T*>(h), last);
-    });
+        return launch_ex(kern, dim3(unsigned(p.blocks)), dim3(p.threads), smem, s, p.cluster, true, p,
+                         static_cast<const T*>(x), static_cast<const T*>(gate), h0, reset, lengths, static_cast<T*>(h),
+                         last);
+    };
+    return scan_with<false>(
+        p, e.dtype, reset != nullptr,
+        [&](auto t, auto l, auto cb, auto r) {
+            constexpr auto kern = scan_part_fwd<decltype(t), decltype(l)::value, decltype(cb)::value, decltype(r)::value>;
+            const cudaError_t err = ensure_smem<kern>(smem);
+            return err != cudaSuccess ? err : launch(kern, t);
+        },
+        [&](auto t, auto v, auto l, auto r) {
+            return launch(scan_walk_fwd<decltype(t), decltype(v)::value, decltype(l)::value, decltype(r)::value>, t);
+        });
 }
 
 cudaError_t run_scan_bwd(const conv_scan_desc_t& e, const DevInfo& d, const void* x, const void* gate, const void* h,
                          const void* dh, const float* h0, const float* dlast, const uint8_t* reset,
                          const int32_t* lengths, void* dx, void* dgate, float* dh0, cudaStream_t s)
 {
-    const bool pairs = rows_even(e.x) && rows_even(e.gate) && rows_even(e.h) && rows_even(e.dh) && rows_even(e.dx) &&
-                       rows_even(e.dgate) && at_pair(x) && at_pair(gate) && at_pair(h) && at_pair(dh) && at_pair(dx) &&
-                       at_pair(dgate);
-    const ScanPlan p = scan_plan(e, d, true, pairs);
-    return scan_with<8>(p, e.dtype, reset != nullptr, [&](auto t, auto v, auto l, auto r) {
+    const int es = e.dtype == CONV_F32 ? 4 : 2;
+    const int chunk = std::min({rows_chunk(x, e.x, es), rows_chunk(gate, e.gate, es), rows_chunk(h, e.h, es),
+                                rows_chunk(dh, e.dh, es), rows_chunk(dx, e.dx, es), rows_chunk(dgate, e.dgate, es)});
+    const ScanPlan p = scan_plan(e, d, true, chunk);
+    const int smem = scan_smem(p, es, true);
+    auto launch = [&](auto kern, auto t) {
         using T = decltype(t);
-        return launch_ex(scan_bwd_kernel<T, decltype(v)::value, decltype(l)::value, decltype(r)::value>, dim3(unsigned(p.blocks)), dim3(p.threads), scan_smem(p), s,
-                         p.cluster, true, p, static_cast<const T*>(x), static_cast<const T*>(gate),
-                         static_cast<const T*>(h), static_cast<const T*>(dh), h0, dlast, reset, lengths,
-                         static_cast<T*>(dx), static_cast<T*>(dgate), dh0);
-    });
+        return launch_ex(kern, dim3(unsigned(p.blocks)), dim3(p.threads), smem, s, p.cluster, true, p,
+                         static_cast<const T*>(x), static_cast<const T*>(gate), static_cast<const T*>(h),
+                         static_cast<const T*>(dh), h0, dlast, reset, lengths, static_cast<T*>(dx),
+                         static_cast<T*>(dgate), dh0);
+    };
+    return scan_with<true>(
+        p, e.dtype, reset != nullptr,
+        [&](auto t, auto l, auto cb, auto r) {
+            constexpr auto kern = scan_part_bwd<decltype(t), decltype(l)::value, decltype(cb)::value, decltype(r)::value>;
+            const cudaError_t err = ensure_smem<kern>(smem);
+            return err != cudaSuccess ? err : launch(kern, t);
+        },
+        [&](auto t, auto v, auto l, auto r) {
+            return launch(scan_walk_bwd<decltype(t), decltype(v)::value, decltype(l)::value, decltype(r)::value>, t);
+        });
+}
+
+cudaError_t scan_read_status(unsigned* out, bool reset)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_scan_status, sizeof(unsigned));
+    if (e == cudaSuccess && reset) {
+        const unsigned zero = 0;
+        e = cudaMemcpyToSymbol(g_scan_status, &zero, sizeof(unsigned));
+    }
+    return e;
 }
 
 }  // namespace igc

@@ -123,6 +123,13 @@ __device__ __forceinline__ int4 lds128(uint32_t a)
     return v;
 }
 
+__device__ __forceinline__ float4 lds_f4(uint32_t a)
+{
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+    return v;
+}
+
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
 {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
@@ -200,9 +207,13 @@ __device__ __forceinline__ float4 ld_dsmem_f4(uint32_t addr)
                  : "memory");
     return v;
 }
-__device__ __forceinline__ void st_dsmem_f2(uint32_t addr, float a, float b)
+// Store 16 bytes to a CTA of the cluster and count them on a barrier of that CTA (both addresses in
+// its shared::cluster window, see dsmem_addr).
+__device__ __forceinline__ void st_async_f4(uint32_t addr, uint32_t bar, float a, float b, float c, float d)
 {
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%2,%3,%4,%5}, [%1];" ::"r"(addr),
+                 "r"(bar), "f"(a), "f"(b), "f"(c), "f"(d)
+                 : "memory");
 }
 __device__ __forceinline__ float ld_dsmem_f32(uint32_t addr)
 {
@@ -219,6 +230,11 @@ __device__ __forceinline__ void sts32(uint32_t a, uint32_t v)
 __device__ __forceinline__ void sts16(uint32_t a, uint32_t v)
 {
     asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(static_cast<unsigned short>(v)) : "memory");
+}
+
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y)
+{
+    asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }
 
 // ---- proxies and tcgen05 ordering --------------------------------------------------------

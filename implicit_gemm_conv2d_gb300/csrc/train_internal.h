@@ -123,13 +123,15 @@ cudaError_t run_grad_norm(const conv_grad_t* g, int count, bool clip, float max_
 struct ScanPlan {
     int B, T, D;
     conv_rows_t x, gate, h, dh, dx, dgate;
-    int V, L;                    // channels and steps of a thread
-    int lx_log, ty_log, by_log;  // a block's lanes over channels, stretches over time, batch rows
-    int cluster, tiles, threads; // blocks along time; blocks over the channels
+    bool walk;                   // a thread walks all steps; else time is cut
+    int V, cols;                 // walk: channels of a thread, threads of a row
+    int L;                       // steps a thread reads at once; of a stretch
+    int CB, stages;              // parts: bytes of a copy, rounds in shared memory
+    int wx_log, by_log, tiles;   // parts: a block's warps over channels and batch rows, blocks over the channels
+    int cluster, threads;
     int64_t blocks;
 };
-// pairs: two bf16 values may be read and written at once.
-ScanPlan scan_plan(const conv_scan_desc_t& e, const DevInfo& d, bool bwd, bool pairs);
+ScanPlan scan_plan(const conv_scan_desc_t& e, const DevInfo& d, bool bwd, int chunk);
 cudaError_t run_scan_fwd(const conv_scan_desc_t& e, const DevInfo& d, const void* x, const void* gate, const float* h0,
                          const uint8_t* reset, const int32_t* lengths, void* h, float* last, cudaStream_t s);
 cudaError_t run_scan_bwd(const conv_scan_desc_t& e, const DevInfo& d, const void* x, const void* gate, const void* h,

@@ -15,7 +15,8 @@ from .gpu_cases import TORCH_DT, to_np
 pytestmark = pytest.mark.gpu
 
 SIZES = [(1, 1, 1), (3, 1, 5), (96, 1, 130), (1, 2, 2), (7, 5, 33), (300, 9, 8), (2, 17, 33), (1, 129, 64), (40, 64, 16),
-         (5, 777, 31), (1, 1000, 1), (2, 1025, 72), (1, 2500, 16), (1, 3000, 260), (3, 4099, 6), (700, 40, 3)]
+         (5, 777, 31), (1, 1000, 1), (2, 1025, 72), (1, 2500, 16), (1, 3000, 260), (3, 4099, 6), (700, 40, 3),
+         (1000, 37, 130), (20000, 21, 6), (40, 200, 520)]
 OPTIONS = {
     "plain": {},
     "state": dict(h0=True),
