@@ -18,6 +18,7 @@
 // A stretch with a reset in it has A = -1: what enters it, be it NaN, is left out and not multiplied by 0.
 #include <algorithm>
 #include <cfloat>
+#include <cmath>
 
 #include "gn_common.cuh"
 #include "tc_ptx.cuh"
@@ -55,13 +56,28 @@ __device__ __forceinline__ float2 scan_slope(float2 e, float2 z)
     return mul2(mul2(make_float2(fminf(e.x, FLT_MAX), fminf(e.y, FLT_MAX)), z), z);
 }
 
-// (A, H) followed by (a, h), and a state that enters.
-__device__ __forceinline__ void scan_join(float& A, float& H, float a, float h)
+// What a stretch (A, H) makes of the state that enters it.
+template <bool RESET> __device__ __forceinline__ float2 scan_enter(float2 A, float2 H, float2 state)
 {
-    H = a < 0.f ? h : fmaf(a, H, h);
-    A = a < 0.f || A < 0.f ? -1.f : A * a;
+    const float2 r = fma2(A, state, H);
+    if constexpr (RESET) return make_float2(A.x < 0.f ? H.x : r.x, A.y < 0.f ? H.y : r.y);
+    return r;
 }
-__device__ __forceinline__ float scan_enter(float A, float H, float state) { return A < 0.f ? H : fmaf(A, state, H); }
+// (A, H) behind (a, h).
+template <bool RESET> __device__ __forceinline__ void scan_join(float2& A, float2& H, float2 a, float2 h)
+{
+    H = scan_enter<RESET>(A, H, h);
+    const float2 r = mul2(A, a);
+    A = RESET ? make_float2(A.x < 0.f || a.x < 0.f ? -1.f : r.x, A.y < 0.f || a.y < 0.f ? -1.f : r.y) : r;
+}
+__device__ __forceinline__ float2 shfl_up(float2 v, int by)
+{
+    return make_float2(__shfl_up_sync(0xFFFFFFFFu, v.x, by), __shfl_up_sync(0xFFFFFFFFu, v.y, by));
+}
+__device__ __forceinline__ float2 shfl(float2 v, int lane)
+{
+    return make_float2(__shfl_sync(0xFFFFFFFFu, v.x, lane), __shfl_sync(0xFFFFFFFFu, v.y, lane));
+}
 
 __device__ __forceinline__ int scan_length(const ScanPlan& p, const int32_t* lengths, int b)
 {
@@ -274,69 +290,84 @@ struct ScanAt {
     }
 };
 
-// An array between memory and a stage.
-template <typename T, int L, int CB> struct ScanCopy {
+// One array on its way between memory and the stages.  A thread moves CB bytes of every ROWS-th step of a round,
+// always of the same channels; DIR = -1: the rounds and their steps run down in time.
+template <typename T, int L, int CB, int DIR> struct ScanCopy {
     using Tile = ScanTile<T, L>;
     static constexpr int ES = Tile::ES, CPR = Tile::ROW / CB, ROWS = SCAN_THREADS / CPR, N = Tile::RT / ROWS;
     static constexpr int UNROLL = N <= 4 || CB == 2 ? std::min(N, 4) : 2;  // (more spills)
-    int at, u0;        // byte in a step's row, first step
-    bool in;           // the channels are there
-    int64_t column;    // elements from the block's first row and channel
-    const int* len;    // of the batch row
-    bool row_in;
-    int by;
+    struct Cursor {
+        T* at;               // of the thread's first step of the round
+        int64_t hop, round;  // from one of its steps, and of its rounds, to the next
+    };
+    int byte, u0;      // in a step's row; first step
+    int by, column;    // batch row and channel in the block
+    int len;           // of the batch row, 0 where the thread's channels are not there
+    bool out;          // they are: results are written
+
     __device__ __forceinline__ ScanCopy(const ScanPlan& p, const ScanAt& q, const int* lens)
     {
-        at = int(threadIdx.x) % CPR * CB;
+        byte = int(threadIdx.x) % CPR * CB;
         u0 = int(threadIdx.x) / CPR;
-        const int el = at / ES, w = el >> 3, c = ((w & ((1 << p.wx_log) - 1)) << 3) + (el & 7);
+        const int el = byte / ES, w = el >> 3;
+        column = ((w & ((1 << p.wx_log) - 1)) << 3) + (el & 7);
         by = w >> p.wx_log;
-        in = q.c0 + c < p.D;
-        row_in = q.b0 + by < p.B;
-        column = c;
-        len = lens + by;
+        const bool in = q.c0 + column < p.D;
+        len = in ? lens[by] : 0;
+        out = in && q.b0 + by < p.B;
     }
-    // Steps first + u (BACK: last - u) of the arrays, `shift` steps earlier; those that the row has not are zeros.
-    template <bool BACK>
-    __device__ __forceinline__ void fill(const T* from, const conv_rows_t& r, uint32_t to, int64_t first, int shift) const
+    // first: step 0 of the block's first round.
+    __device__ __forceinline__ Cursor cursor(const ScanAt& q, const void* array, const conv_rows_t& r, int64_t first,
+                                             int64_t span) const
     {
-        const int64_t stride = (BACK ? -1 : 1) * r.step;
-        const T* src = from + by * r.batch + column + (first - shift) * r.step + u0 * stride;
-        const int n = *len;
-        // a thread's steps are ROWS apart
-#pragma unroll UNROLL
-        for (int k = 0; k < N; ++k) {
-            const int u = u0 + k * ROWS;
-            const int64_t t = BACK ? first - u : first + u;
-            const bool there = in && t < n && t >= shift;
-            const T* s = there ? src + k * ROWS * stride : from;
-            const uint32_t dst = to + Tile::place(u, at);
-            if constexpr (CB == 16)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(s), "r"(there ? 16 : 0) : "memory");
-            else if constexpr (CB == 4)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(s), "r"(there ? 4 : 0) : "memory");
-            else
-                tc::sts16(dst, there ? *reinterpret_cast<const uint16_t*>(s) : 0u);
-        }
+        T* a = static_cast<T*>(const_cast<void*>(array));
+        return {a + (q.b0 + by) * r.batch + q.c0 + column + (first + DIR * u0) * r.step, DIR * ROWS * r.step,
+                DIR * span * r.step};
     }
-    // Back to memory.
-    template <bool BACK>
-    __device__ __forceinline__ void drain(T* to, const conv_rows_t& r, uint32_t from, int64_t first, int T_) const
+    // The round that begins at step first; what the row does not have, or has not `shift` steps earlier, is zeros.
+    // any: an address to name where nothing is read.
+    __device__ __forceinline__ void fill(Cursor& c, uint32_t to, int64_t first, int shift, const T* any) const
     {
-        const int64_t stride = (BACK ? -1 : 1) * r.step;
-        T* dst = to + by * r.batch + column + first * r.step + u0 * stride;
-        if (!in || !row_in) return;
+        const T* src = c.at;
+        const int64_t last = first + DIR * (Tile::RT - 1);
+        if (CB > 2 && (DIR > 0 ? last < len : first < len && last >= shift)) {
 #pragma unroll UNROLL
-        for (int k = 0; k < N; ++k) {
-            const int u = u0 + k * ROWS;
-            const int64_t t = BACK ? first - u : first + u;
-            if (t < 0 || t >= T_) continue;
-            const uint32_t src = from + Tile::place(u, at);
-            T* d = dst + k * ROWS * stride;
-            if constexpr (CB == 16) *reinterpret_cast<int4*>(d) = tc::lds128(src);
-            else if constexpr (CB == 4) *reinterpret_cast<uint32_t*>(d) = tc::lds32(src);
-            else *reinterpret_cast<uint16_t*>(d) = uint16_t(tc::lds16(src));
+            for (int k = 0; k < N; ++k, src += c.hop) copy(to + Tile::place(u0 + k * ROWS, byte), src, true);
+        } else {
+#pragma unroll UNROLL
+            for (int k = 0; k < N; ++k, src += c.hop) {
+                const int64_t t = first + DIR * (u0 + k * ROWS);
+                const bool there = t < len && t >= shift;
+                copy(to + Tile::place(u0 + k * ROWS, byte), there ? src : any, there);
+            }
         }
+        c.at += c.round;
+    }
+    static __device__ __forceinline__ void copy(uint32_t dst, const T* src, bool there)
+    {
+        if constexpr (CB == 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+        else if constexpr (CB == 4)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+        else
+            tc::sts16(dst, there ? *reinterpret_cast<const uint16_t*>(src) : 0u);
+    }
+    // A round's results back to memory.
+    __device__ __forceinline__ void drain(Cursor& c, uint32_t from, int64_t first, int T_) const
+    {
+        T* dst = c.at;
+        if (out) {
+#pragma unroll UNROLL
+            for (int k = 0; k < N; ++k, dst += c.hop) {
+                const int64_t t = first + DIR * (u0 + k * ROWS);
+                if (t < 0 || t >= T_) continue;
+                const uint32_t src = from + Tile::place(u0 + k * ROWS, byte);
+                if constexpr (CB == 16) *reinterpret_cast<int4*>(dst) = tc::lds128(src);
+                else if constexpr (CB == 4) *reinterpret_cast<uint32_t*>(dst) = tc::lds32(src);
+                else *reinterpret_cast<uint16_t*>(dst) = uint16_t(tc::lds16(src));
+            }
+        }
+        c.at += c.round;
     }
 };
 
@@ -389,59 +420,54 @@ struct ScanExchange {
     {
         if ((threadIdx.x & 31) == 0) tc::mbar_arrive_expect_tx(bars + uint32_t(parity) * 8, uint32_t(q.C) * 64u);
     }
+    // (A, H) of each of eight neighbours, four lanes apart, joined with all before it.
+    template <bool RESET> static __device__ __forceinline__ void join_all(float2& A, float2& H)
+    {
+#pragma unroll
+        for (int o = 4; o < 32; o *= 2) {
+            const float2 a = shfl_up(A, o), h = shfl_up(H, o);
+            if (int(threadIdx.x & 31) >= o) scan_join<RESET>(A, H, a, h);
+        }
+    }
     // (A, H): the lane's stretch.  state: in, what enters the round; out, what enters the next one.  Returns what
     // enters the lane's stretch.
     template <bool RESET>
     __device__ __forceinline__ float2 run(const ScanAt& q, int round, float2 A, float2 H, float2& state)
     {
-        constexpr unsigned ALL = 0xFFFFFFFFu;
-        // inclusive over the stretches
-#pragma unroll
-        for (int o = 4; o < 32; o *= 2) {
-            const float2 a = make_float2(__shfl_up_sync(ALL, A.x, o), __shfl_up_sync(ALL, A.y, o));
-            const float2 h = make_float2(__shfl_up_sync(ALL, H.x, o), __shfl_up_sync(ALL, H.y, o));
-            if (int(threadIdx.x & 31) >= o) {
-                if constexpr (RESET) {
-                    H.x = scan_enter(A.x, H.x, h.x);
-                    H.y = scan_enter(A.y, H.y, h.y);
-                    A.x = A.x < 0.f || a.x < 0.f ? -1.f : A.x * a.x;
-                    A.y = A.y < 0.f || a.y < 0.f ? -1.f : A.y * a.y;
-                } else {
-                    H = fma2(A, h, H);
-                    A = mul2(A, a);
-                }
-            }
-        }
+        join_all<RESET>(A, H);
         float2 enter = state;
         if (q.C > 1) {
             const int parity = round & 1;
             const uint32_t base = slots + uint32_t((parity * q.C * SCAN_WARPS + q.warp) * 64 + q.pair * 16);
+            const uint32_t bar = bars + uint32_t(parity) * 8;
+            // the last stretch's lanes hold the warp's
             if (q.seg == SCAN_SEGS - 1 && !dead) {
-                const uint32_t mine = base + uint32_t(q.rank * SCAN_WARPS * 64), bar = bars + uint32_t(parity) * 8;
+                const uint32_t mine = base + uint32_t(q.rank * SCAN_WARPS * 64);
                 for (int r = 0; r < q.C; ++r)
                     tc::st_async_f4(tc::dsmem_addr(mine, uint32_t(r)), tc::dsmem_addr(bar, uint32_t(r)), A.x, A.y, H.x, H.y);
             }
-            if (!dead && !tc::mbar_wait(bars + uint32_t(parity) * 8, uint32_t(round >> 1) & 1u)) {
+            if (!dead && !tc::mbar_wait(bar, uint32_t(round >> 1) & 1u)) {
                 dead = true;  // the results are wrong and the status says so; every later wait is skipped
                 atomicOr(&g_scan_status, CONV_STATUS_SCAN);
             }
             if (!dead) arm(q, parity);  // of the round after the next
-            float2 s = state;
-            for (int r = 0; r < q.C; ++r) {
-                if (r == q.rank) enter = s;
-                const float4 v = tc::lds_f4(base + uint32_t(r * SCAN_WARPS * 64));
-                s = make_float2(scan_enter(v.x, v.z, s.x), scan_enter(v.y, v.w, s.y));
+            // lane (seg, pair) takes rank seg's
+            float2 a = both(1.f), h = both(0.f);
+            if (q.seg < q.C) {
+                const float4 v = tc::lds_f4(base + uint32_t(q.seg * SCAN_WARPS * 64));
+                a = make_float2(v.x, v.y);
+                h = make_float2(v.z, v.w);
             }
-            state = s;
-            __syncwarp();  // read by all before the next round but one is announced
+            __syncwarp();  // read by all before the round after the next is announced
+            join_all<RESET>(a, h);
+            const float2 s = scan_enter<RESET>(a, h, state);
+            if (q.rank > 0) enter = shfl(s, (q.rank - 1) * 4 + q.pair);
+            state = shfl(s, 28 + q.pair);
         } else {
-            const float2 s = make_float2(scan_enter(A.x, H.x, state.x), scan_enter(A.y, H.y, state.y));
-            const int from = 28 + q.pair;
-            state = make_float2(__shfl_sync(ALL, s.x, from), __shfl_sync(ALL, s.y, from));
+            state = shfl(scan_enter<RESET>(A, H, state), 28 + q.pair);
         }
         // what the stretches in front of this one make of it
-        const float2 s = make_float2(scan_enter(A.x, H.x, enter.x), scan_enter(A.y, H.y, enter.y));
-        const float2 f = make_float2(__shfl_up_sync(ALL, s.x, 4), __shfl_up_sync(ALL, s.y, 4));
+        const float2 f = shfl_up(scan_enter<RESET>(A, H, enter), 4);
         return q.seg == 0 ? enter : f;
     }
 };
@@ -513,7 +539,7 @@ __device__ __forceinline__ void scan_store(const ScanPlan& p, const ScanAt& q, f
 }
 
 template <typename T, int L, int CB, bool RESET>
-__global__ void __launch_bounds__(SCAN_THREADS, 3)
+__global__ void __launch_bounds__(SCAN_THREADS, sizeof(T) == 2 ? 2 : 3)
 scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, const float* h0, const uint8_t* reset,
               const int32_t* lengths, T* h, float* last)
 {
@@ -528,11 +554,12 @@ scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
     float2 state = scan_state(p, q, h0);
     const uint32_t stages = scan_setup(p, q, lengths, lens, tc::smem_u32(sm) + SCAN_LENS, ex);
     const int len = lens[q.warp >> p.wx_log];
-    const ScanCopy<T, L, CB> copy(p, q, lens);
+    using Copy = ScanCopy<T, L, CB, 1>;
+    const Copy copy(p, q, lens);
     const ScanLane<T, L> lane(q);
-    const T *bx = x + q.b0 * p.x.batch + q.c0, *bg = gate + q.b0 * p.gate.batch + q.c0;
-    T* bh = h + q.b0 * p.h.batch + q.c0;
     const int64_t span = int64_t(q.C) * Tile::RT, rank0 = int64_t(q.rank) * Tile::RT;
+    typename Copy::Cursor cx = copy.cursor(q, x, p.x, rank0, span), cg = copy.cursor(q, gate, p.gate, rank0, span);
+    typename Copy::Cursor ch = copy.cursor(q, h, p.h, rank0, span);
     ScanFlags<L, 1> flags;
     if (RESET && q.b < p.B) {
         flags.row = reset + int64_t(q.b) * p.T;
@@ -541,8 +568,8 @@ scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
     }
     auto fill = [&](int slot, int64_t base) {
         if (base < p.T) {
-            copy.template fill<false>(bx, p.x, stages + slot * STAGE, base + rank0, 0);
-            copy.template fill<false>(bg, p.gate, stages + slot * STAGE + Tile::ARRAY, base + rank0, 0);
+            copy.fill(cx, stages + slot * STAGE, base + rank0, 0, x);
+            copy.fill(cg, stages + slot * STAGE + Tile::ARRAY, base + rank0, 0, gate);
         }
         scan_commit();
     };
@@ -551,7 +578,7 @@ scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
     for (int64_t base = 0; base < p.T; base += span, ++round) {
         const int prev = now == 0 ? p.stages - 1 : now - 1;
         scan_arrived(p.stages);
-        if (round > 0) copy.template drain<false>(bh, p.h, stages + prev * STAGE, base - span + rank0, p.T);
+        if (round > 0) copy.drain(ch, stages + prev * STAGE, base - span + rank0, p.T);
         fill(prev, base + (p.stages - 1) * span);
         const uint32_t stage = stages + now * STAGE;
         const int64_t t0 = base + rank0 + q.seg * L;
@@ -591,14 +618,18 @@ scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
         for (int i = 0; i < L; ++i) {
             if (RESET && (cut >> i & 1u)) st = both(0.f);
             st = fma2(keep[i], st, in[i]);
-            lane.write(stage, 0, i, full || t0 + i < len ? st : both(0.f));
+            lane.write(stage, 0, i, st);
+        }
+        if (!full) {
+#pragma unroll
+            for (int i = 0; i < L; ++i)
+                if (t0 + i >= len) lane.write(stage, 0, i, both(0.f));
         }
         now = now + 1 == p.stages ? 0 : now + 1;
     }
     if (round > 0) {
         __syncthreads();
-        copy.template drain<false>(bh, p.h, stages + (now == 0 ? p.stages - 1 : now - 1) * STAGE,
-                                   (round - 1) * span + rank0, p.T);
+        copy.drain(ch, stages + (now == 0 ? p.stages - 1 : now - 1) * STAGE, (round - 1) * span + rank0, p.T);
     }
     scan_store(p, q, last, state);
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -608,7 +639,7 @@ scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
 // Time runs backwards: a lane's stretch is the steps t = T - 1 - u, u = u0 .. u0 + L - 1, and the state is what
 // flows from step t into t - 1, (1 - z[t]) s[t].
 template <typename T, int L, int CB, bool RESET>
-__global__ void __launch_bounds__(SCAN_THREADS, 3)
+__global__ void __launch_bounds__(SCAN_THREADS, sizeof(T) == 2 ? 2 : 3)
 scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, const T* h, const T* dh, const float* h0,
               const float* dlast, const uint8_t* reset, const int32_t* lengths, T* dx, T* dgate, float* dh0)
 {
@@ -623,12 +654,13 @@ scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
     float2 state = scan_state(p, q, dlast);
     const uint32_t stages = scan_setup(p, q, lengths, lens, tc::smem_u32(sm) + SCAN_LENS, ex);
     const int len = lens[q.warp >> p.wx_log];
-    const ScanCopy<T, L, CB> copy(p, q, lens);
+    using Copy = ScanCopy<T, L, CB, -1>;
+    const Copy copy(p, q, lens);
     const ScanLane<T, L> lane(q);
-    const T *bx = x + q.b0 * p.x.batch + q.c0, *bg = gate + q.b0 * p.gate.batch + q.c0;
-    const T *bh = h + q.b0 * p.h.batch + q.c0, *bd = dh + q.b0 * p.dh.batch + q.c0;
-    T *ox = dx + q.b0 * p.dx.batch + q.c0, *og = dgate + q.b0 * p.dgate.batch + q.c0;
     const int64_t span = int64_t(q.C) * Tile::RT, last0 = int64_t(p.T) - 1 - int64_t(q.rank) * Tile::RT;
+    typename Copy::Cursor cx = copy.cursor(q, x, p.x, last0, span), cg = copy.cursor(q, gate, p.gate, last0, span),
+                          cd = copy.cursor(q, dh, p.dh, last0, span), ch = copy.cursor(q, h, p.h, last0 - 1, span),
+                          ox = copy.cursor(q, dx, p.dx, last0, span), og = copy.cursor(q, dgate, p.dgate, last0, span);
     ScanFlags<L, -1> flags;
     if (RESET && q.b < p.B) {
         flags.row = reset + int64_t(q.b) * p.T;
@@ -638,16 +670,16 @@ scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
     auto fill = [&](int slot, int64_t base) {
         if (base < p.T) {
             const uint32_t to = stages + slot * STAGE;
-            copy.template fill<true>(bx, p.x, to, last0 - base, 0);
-            copy.template fill<true>(bg, p.gate, to + Tile::ARRAY, last0 - base, 0);
-            copy.template fill<true>(bd, p.dh, to + 2 * Tile::ARRAY, last0 - base, 0);
-            copy.template fill<true>(bh, p.h, to + 3 * Tile::ARRAY, last0 - base, 1);
+            copy.fill(cx, to, last0 - base, 0, x);
+            copy.fill(cg, to + Tile::ARRAY, last0 - base, 0, gate);
+            copy.fill(cd, to + 2 * Tile::ARRAY, last0 - base, 0, dh);
+            copy.fill(ch, to + 3 * Tile::ARRAY, last0 - base, 1, h);
         }
         scan_commit();
     };
     auto drain = [&](int slot, int64_t base) {
-        copy.template drain<true>(ox, p.dx, stages + slot * STAGE, last0 - base, p.T);
-        copy.template drain<true>(og, p.dgate, stages + slot * STAGE + Tile::ARRAY, last0 - base, p.T);
+        copy.drain(ox, stages + slot * STAGE, last0 - base, p.T);
+        copy.drain(og, stages + slot * STAGE + Tile::ARRAY, last0 - base, p.T);
     };
     for (int k = 0; k < p.stages - 1; ++k) fill(k, k * span);
     int now = 0, round = 0;
@@ -741,18 +773,29 @@ ScanPlan scan_plan(const conv_scan_desc_t& e, const DevInfo& d, bool bwd, int ch
         return p;
     }
     p.CB = chunk >= 16 && e.D % (16 / es) == 0 ? 16 : es == 4 || (chunk >= 4 && e.D % 2 == 0) ? 4 : 2;
-    p.L = bwd && es == 4 ? 4 : 8;
+    p.L = es == 2 ? (bwd ? 8 : 16) : bwd ? 4 : 8;
     p.wx_log = std::min(3, log2_up((int64_t(e.D) + 7) / 8));
     p.by_log = 3 - p.wx_log;
     p.tiles = int((int64_t(e.D) + (8 << p.wx_log) - 1) / (8 << p.wx_log));
     const int64_t blocks = int64_t(p.tiles) * ((int64_t(e.B) + (1 << p.by_log) - 1) >> p.by_log);
     const int64_t rounds = (int64_t(e.T) + SCAN_SEGS * p.L - 1) / (SCAN_SEGS * p.L);
+    // Blocks along time: fewer rounds each, as far as the blocks fit the GPU.  A round takes a block's latencies (as
+    // long as 1.5 blocks' instructions) and the instructions of all blocks of its SM.
+    const int fit = es == 2 ? 2 : 3;
     int log_c = 0;
-    while (log_c < 3 && (blocks << log_c) < 2 * d.sms && (int64_t(1) << log_c) < rounds) ++log_c;
+    double best = 0;
+    for (int k = 0; k <= 3 && (k == 0 || (int64_t(1) << (k - 1)) < rounds); ++k) {
+        const double n = double(blocks) * (1 << k), waves = std::ceil(n / (double(d.sms) * fit));
+        const double cost = waves * (std::min(std::ceil(n / d.sms), double(fit)) + 1.5) / (1 << k);
+        if (k == 0 || cost < best) {
+            best = cost;
+            log_c = k;
+        }
+    }
     p.cluster = 1 << log_c;
     p.threads = SCAN_THREADS;
     p.blocks = blocks << log_c;
-    p.stages = es == 2 && !bwd ? 3 : 2;
+    p.stages = 2;
     return p;
 }
 
@@ -772,7 +815,7 @@ template <int N> using Int = std::integral_constant<int, N>;
 template <bool BWD, class F, class G> cudaError_t scan_with(const ScanPlan& p, int dt, bool reset, F&& f, G&& g)
 {
     auto parts = [&](auto t, auto r) {
-        using L = Int<BWD && sizeof(t) == 4 ? 4 : 8>;
+        using L = Int<sizeof(t) == 2 ? (BWD ? 8 : 16) : BWD ? 4 : 8>;
         if (p.CB == 16) return f(t, L(), Int<16>(), r);
         if constexpr (sizeof(t) == 2)
             if (p.CB == 2) return f(t, L(), Int<2>(), r);
