@@ -1,0 +1,464 @@
+// kernels_distill.cu -- the loss of a row of logits z against a teacher's K named entries and its
+// gradient.  With P = softmax(z / tau) over the vocabulary and p = softmax(teacher / tau) over the row's
+// entries:
+//   loss = tau^2 sum_k p_k (log p_k - log P[id_k])        dz = w tau (P - the p_k at their ids)
+//
+// One pass over a row keeps the running maximum m and the sum of exp((z - m) / tau); a row is one warp's
+// (short ones), a block's, or that of a cluster of up to 8 blocks, each with a part of the vocabulary, whose
+// (m, sum) travel through distributed shared memory.  The loss with its gradient reads z once: a block's part
+// of the row waits in shared memory, at the threads that read it, for the row's sum, and goes out as
+// dz.  Rows begin anywhere: a row is taken by 16-byte vectors of memory, its first and last one by
+// elements.
+//
+// One warp more than those that sweep works on the teacher's entries: their softmax, the student's logits at their
+// ids, and which ids occur twice.  dz at the ids is written again, whole, behind the sweep's barrier, by
+// one thread an id: no atomic adds, and a fixed order for an id that occurs twice.
+#include <algorithm>
+
+#include "gn_common.cuh"
+#include "tc_ptx.cuh"
+#include "train_internal.h"
+
+namespace igc {
+
+namespace {
+
+enum { DISTILL_FWD = 0, DISTILL_BWD = 1, DISTILL_GRAD = 2 };
+constexpr int DISTILL_WARPS = 8;       // that sweep a row, where a block does
+constexpr int DISTILL_UNROLL = 4;      // vectors a thread has on their way
+
+struct Stat { float m, s; };
+
+// m: of both, or 0 while all values are -inf (so that nothing is subtracted from them).
+__device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.f : m; }
+__device__ __forceinline__ Stat stat_join(Stat a, Stat b, float k)
+{
+    const float m = fmaxf(a.m, b.m), f = finite_base(m);
+    return {m, a.s * fast_exp2((a.m - f) * k) + b.s * fast_exp2((b.m - f) * k)};
+}
+
+// A row's place: 16-byte vectors from `base` on; vector j holds the row's elements j * VE - off and on.
+template <typename T> struct RowAt {
+    static constexpr int VE = 16 / int(sizeof(T));
+    int64_t first;    // element of the array that vector 0 begins with (may lie before the row)
+    int off, V, vecs;
+    __device__ __forceinline__ RowAt(const T* z, int64_t n, int64_t ld, int V_) : V(V_)
+    {
+        const int64_t at = n * ld;
+        off = int((reinterpret_cast<uintptr_t>(z + at) & 15u) / sizeof(T));
+        first = at - off;
+        vecs = (off + V + VE - 1) / VE;
+    }
+    __device__ __forceinline__ bool whole(int j) const { return j * VE >= off && (j + 1) * VE <= off + V; }
+    __device__ __forceinline__ Vec<T, VE> load(const T* z, int j) const
+    {
+        Vec<T, VE> r;
+        const T* p = z + first + int64_t(j) * VE;
+        if (whole(j)) {
+            r.load(p);
+        } else {
+            float f[VE];
+#pragma unroll
+            for (int i = 0; i < VE; ++i) {
+                const int e = j * VE + i - off;
+                f[i] = e >= 0 && e < V ? Elem<T>::ld(p + i) : -INFINITY;
+            }
+            r.set(f);
+        }
+        return r;
+    }
+    __device__ __forceinline__ void store(T* dz, int j, const Vec<T, VE>& r) const
+    {
+        T* p = dz + first + int64_t(j) * VE;
+        if (whole(j)) {
+            r.store(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VE; ++i) {
+                const int e = j * VE + i - off;
+                if (e >= 0 && e < V) Elem<T>::st(p + i, r.get(i));
+            }
+        }
+    }
+};
+
+// One vector more.
+template <typename T, int VE> __device__ __forceinline__ float vec_max(const Vec<T, VE>& v)
+{
+    float m = v.get(0);
+#pragma unroll
+    for (int i = 1; i < VE; ++i) m = fmaxf(m, v.get(i));
+    return m;
+}
+template <typename T, int VE> __device__ __forceinline__ float vec_sum(const Vec<T, VE>& v, float base, float k)
+{
+    float2 t[VE / 2];
+#pragma unroll
+    for (int i = 0; i < VE / 2; ++i) {
+        const float2 d = mul2(add2(make_float2(v.get(2 * i), v.get(2 * i + 1)), both(-base)), both(k));
+        t[i] = make_float2(fast_exp2(d.x), fast_exp2(d.y));
+    }
+#pragma unroll
+    for (int n = VE / 4; n > 0; n /= 2)
+#pragma unroll
+        for (int i = 0; i < n; ++i) t[i] = add2(t[i], t[i + n]);
+    return t[0].x + t[0].y;
+}
+
+// The teacher's entries of a row, worked on by one warp.  ids: -1 where the entry names nothing; p: their
+// probabilities; zk: the student's logits; total: what is taken off dz there, or -1 where another entry
+// with the same id does it.
+struct Teacher {
+    int* id;
+    float *p, *zk, *total;
+    uint32_t* seen;  // two bitmaps
+    int bits;        // of one, a power of two
+    static __host__ __device__ int bytes(int K, int bits) { return 16 * K + bits / 4; }
+    __device__ __forceinline__ Teacher(uint8_t* sm, int K, int bits_) : bits(bits_)
+    {
+        seen = reinterpret_cast<uint32_t*>(sm);
+        id = reinterpret_cast<int*>(seen + bits / 16);
+        p = reinterpret_cast<float*>(id + K);
+        zk = p + K;
+        total = zk + K;
+    }
+    // ids and probabilities; false: the row names nothing.
+    __device__ __forceinline__ bool probabilities(const DistillParams& a, int64_t n, int lane)
+    {
+        float top = -INFINITY;
+        bool nan = false;
+        for (int k = lane; k < a.K; k += 32) {
+            const int64_t at = n * a.K + k;
+            const int64_t v = a.ids64 ? static_cast<const int64_t*>(a.ids)[at] : static_cast<const int32_t*>(a.ids)[at];
+            float q = a.teacher_bf16 ? Elem<__nv_bfloat16>::ld(static_cast<const __nv_bfloat16*>(a.teacher) + at)
+                                     : static_cast<const float*>(a.teacher)[at];
+            const bool named = v >= 0 && v < a.V;
+            if (!named) q = -INFINITY;
+            id[k] = named ? int(v) : -1;
+            p[k] = q;
+            top = fmaxf(top, q);
+            nan |= q != q;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        nan = __any_sync(0xFFFFFFFFu, nan);
+        if (top == -INFINITY && !nan) return false;
+        const float base = finite_base(top);
+        float sum = 0.f;
+        for (int k = lane; k < a.K; k += 32) {
+            zk[k] = __fdiv_rn(p[k] - base, a.tau);  // log p but for the sum
+            const float e = expf(zk[k]);
+            p[k] = e;
+            sum += e;
+        }
+        sum = warp_sum(sum);
+        const float log_sum = logf(sum);
+        for (int k = lane; k < a.K; k += 32) {
+            p[k] = __fdiv_rn(p[k], sum);
+            total[k] = zk[k] - log_sum;  // log p, until it is needed no more
+        }
+        return true;
+    }
+    // The student's logits of the entries in [lo, hi).
+    template <typename T> __device__ __forceinline__ void gather(const DistillParams& a, const T* row, int lo, int hi, int lane)
+    {
+        for (int k = lane; k < a.K; k += 32) zk[k] = id[k] >= lo && id[k] < hi ? Elem<T>::ld(row + id[k]) : 0.f;
+    }
+    __device__ __forceinline__ float loss(const DistillParams& a, float m, float log_s, int lane) const
+    {
+        float sum = 0.f;
+        for (int k = lane; k < a.K; k += 32)
+            if (!(p[k] == 0.f)) sum += p[k] * (total[k] - (__fdiv_rn(zk[k] - m, a.tau) - log_s));
+        return a.tau * a.tau * warp_sum(sum);
+    }
+    // total: the sum of p over the entries of an id, at the first of them.  Ids that share a bit of `seen` are
+    // looked at one by one, in order.
+    __device__ __forceinline__ void totals(const DistillParams& a, int lane)
+    {
+        uint32_t* twice = seen + bits / 32;
+        for (int i = lane; i < bits / 16; i += 32) seen[i] = 0;
+        __syncwarp();
+        for (int k = lane; k < a.K; k += 32) {
+            if (id[k] < 0) continue;
+            const int h = id[k] & (bits - 1);
+            if (atomicOr(&seen[h >> 5], 1u << (h & 31)) >> (h & 31) & 1u) atomicOr(&twice[h >> 5], 1u << (h & 31));
+        }
+        __syncwarp();
+        for (int k = lane; k < a.K; k += 32) {
+            float t = p[k];
+            const int me = id[k], h = me & (bits - 1);
+            if (me >= 0 && (twice[h >> 5] >> (h & 31) & 1u)) {
+                t = 0.f;
+                for (int j = 0; j < a.K; ++j) {
+                    if (id[j] != me) continue;
+                    if (j < k) {
+                        t = -1.f;
+                        break;
+                    }
+                    t += p[j];
+                }
+            }
+            total[k] = t;
+        }
+    }
+};
+
+// WARP: a warp a row; else a block of DISTILL_WARPS warps and one for the teacher, `cluster` blocks a row.
+template <typename T, int MODE, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : DISTILL_WARPS * 32 + 32)
+distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float* weight, float* zmax, float* zlog,
+               float* loss, T* dz)
+{
+    extern __shared__ __align__(16) uint8_t sm[];
+    __shared__ Stat parts[DISTILL_WARPS + 8];
+    __shared__ int none;
+    constexpr int VE = RowAt<T>::VE, U = DISTILL_UNROLL;
+    const int lane = int(threadIdx.x) & 31, warp = int(threadIdx.x) >> 5;
+    const int C = WARP ? 1 : a.cluster, rank = WARP ? 0 : int(blockIdx.x) % C;
+    const int64_t n = WARP ? int64_t(blockIdx.x) * a.rows + warp : int64_t(blockIdx.x) / C;
+    const int step = WARP ? 32 : DISTILL_WARPS * 32, me = WARP ? lane : int(threadIdx.x);
+    const bool teaches = WARP || warp == DISTILL_WARPS, sweeps = WARP || !teaches;
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
+    if (WARP && n >= a.N) return;
+    if (!WARP && MODE != DISTILL_BWD && C > 1) tc::cluster_arrive();
+
+    const RowAt<T> row(z, n, a.ld, a.V);
+    const T* zrow = z + n * a.ld;
+    const int per = (row.vecs + C - 1) / C, j0 = min(rank * per, row.vecs), j1 = min(j0 + per, row.vecs);
+    const int lo = max(0, j0 * VE - row.off), hi = min(a.V, j1 * VE - row.off);  // the block's elements
+    Teacher t(sm + (WARP ? warp * Teacher::bytes(a.K, a.bits) : 0), a.K, a.bits);
+    uint8_t* const stage = sm + (WARP ? a.rows : 1) * Teacher::bytes(a.K, a.bits) +
+                           (WARP ? warp * a.stage_bytes : 0);  // vector j - j0 at the thread that reads it
+    const bool staged = MODE == DISTILL_GRAD && a.stage_bytes > 0;
+
+    // ---- the teacher's entries, and what the first sweep finds
+    bool empty = false;
+    auto teach = [&] {
+        empty = !t.probabilities(a, n, lane);
+        if (!empty) {
+            if (MODE == DISTILL_BWD) t.gather(a, zrow, lo, hi, lane);
+            else t.gather(a, zrow, 0, a.V, lane);
+        }
+        if (!WARP && lane == 0) none = empty;
+    };
+    float m, log_s;
+    if (MODE == DISTILL_BWD) {
+        m = zmax[n];
+        log_s = zlog[n];
+        if (teaches) teach();
+        if (WARP) __syncwarp();
+        else __syncthreads();  // z may be dz
+    } else {
+        if (teaches) teach();
+        Stat st = {-INFINITY, 0.f};
+        if (sweeps) {
+            for (int j = j0 + me; j < j1; j += step * U) {
+                Vec<T, VE> v[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (j + u * step < j1) v[u] = row.load(z, j + u * step);
+                float top = st.m;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (j + u * step < j1) {
+                        top = fmaxf(top, vec_max<T, VE>(v[u]));
+                        if (staged) v[u].store(reinterpret_cast<T*>(stage + (j + u * step - j0) * 16));
+                    }
+                const float base = finite_base(top);
+                if (top > st.m) st.s *= fast_exp2((st.m - base) * a.k);
+                st.m = top;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (j + u * step < j1) st.s += vec_sum<T, VE>(v[u], base, a.k);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            st = stat_join(st, {__shfl_xor_sync(0xFFFFFFFFu, st.m, o), __shfl_xor_sync(0xFFFFFFFFu, st.s, o)}, a.k);
+        if (!WARP) {
+            if (lane == 0 && sweeps) parts[warp] = st;
+            __syncthreads();
+            st = parts[0];
+            for (int w = 1; w < DISTILL_WARPS; ++w) st = stat_join(st, parts[w], a.k);
+            if (C > 1) {
+                tc::cluster_wait();  // every block of the cluster is there
+                if (threadIdx.x < unsigned(C))
+                    tc::st_dsmem_f2(tc::dsmem_addr(tc::smem_u32(&parts[DISTILL_WARPS + rank]), threadIdx.x), st.m, st.s);
+                tc::cluster_sync();
+                st = parts[DISTILL_WARPS];
+                for (int r = 1; r < C; ++r) st = stat_join(st, parts[DISTILL_WARPS + r], a.k);
+            }
+        }
+        m = st.m;
+        log_s = logf(st.s);
+        if (teaches && rank == 0) {
+            const float l = empty ? 0.f : t.loss(a, m, log_s, lane);
+            if (lane == 0) {
+                loss[n] = l;
+                if (MODE == DISTILL_FWD) {
+                    zmax[n] = m;
+                    zlog[n] = log_s;
+                }
+            }
+        }
+    }
+    if (MODE == DISTILL_FWD) return;
+
+    // ---- the gradient
+    if (!WARP) empty = none != 0;
+    const float w = weight ? weight[n] : 1.f, c = a.scale * a.tau * w, log2_s = log_s * kLog2e;
+    const bool zeros = empty || w == 0.f;
+    if (teaches && !zeros) t.totals(a, lane);
+    if (sweeps) {
+        for (int j = j0 + me; j < j1; j += step * U) {
+            Vec<T, VE> v[U];
+            if (!zeros) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (j + u * step < j1) {
+                        if (staged) v[u].load(reinterpret_cast<const T*>(stage + (j + u * step - j0) * 16));
+                        else v[u] = row.load(z, j + u * step);
+                    }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (j + u * step >= j1) continue;
+                Vec<T, VE> r;
+                if (zeros) {
+                    r.zero();
+                } else {
+                    float f[VE];
+#pragma unroll
+                    for (int i = 0; i < VE; i += 2) {
+                        const float2 d = fma2(add2(make_float2(v[u].get(i), v[u].get(i + 1)), both(-m)), both(a.k),
+                                              both(-log2_s));
+                        f[i] = c * fast_exp2(d.x);
+                        f[i + 1] = c * fast_exp2(d.y);
+                    }
+                    r.set(f);
+                }
+                row.store(dz, j + u * step, r);
+            }
+        }
+    }
+    if (WARP) __syncwarp();
+    else __syncthreads();
+    if (zeros) return;
+    for (int k = me; k < a.K; k += WARP ? 32 : int(blockDim.x)) {
+        const int id = t.id[k];
+        if (id < lo || id >= hi || t.total[k] == -1.f) continue;
+        Elem<T>::st(dz + n * a.ld + id, c * (fast_exp2((t.zk[k] - m) * a.k - log2_s) - t.total[k]));
+    }
+}
+
+}  // namespace
+
+namespace {
+
+DistillParams distill_params(const conv_distill_desc_t& e, const void* ids, const void* teacher, float scale)
+{
+    DistillParams a = {};
+    a.N = e.N; a.V = e.V; a.K = e.K; a.ld = e.ld;
+    a.ids = ids;
+    a.ids64 = e.index_dtype == CONV_INDEX_I64;
+    a.teacher = teacher;
+    a.teacher_bf16 = e.teacher_dtype == CONV_BF16;
+    a.tau = e.temperature;
+    a.k = float(1.4426950408889634 / double(e.temperature));
+    a.scale = scale;
+    return a;
+}
+
+}  // namespace
+
+DistillPlan distill_plan(const conv_distill_desc_t& e, const DevInfo& d, int mode)
+{
+    DistillPlan p = {};
+    const int es = e.dtype == CONV_F32 ? 4 : 2, ve = 16 / es;
+    const int64_t vecs = (int64_t(e.V) + ve - 1) / ve + 1;
+    const int64_t most = d.smem_optin - 2048;  // (and the static part)
+    p.warp = vecs <= 256 && e.K <= 256;
+    if (p.warp) {
+        p.bits = 2048;
+        p.stage_bytes = mode == DISTILL_GRAD ? int(vecs) * 16 : 0;
+        const int64_t one = 16 * int64_t(e.K) + p.bits / 4 + p.stage_bytes;
+        p.rows = int(std::max<int64_t>(1, std::min<int64_t>(8, 48 * 1024 / one)));
+        p.cluster = 1;
+        p.threads = p.rows * 32;
+        p.smem = int(p.rows * one);
+        p.blocks = (e.N + p.rows - 1) / p.rows;
+        return p;
+    }
+    p.bits = 8192;
+    p.rows = 1;
+    p.threads = DISTILL_WARPS * 32 + 32;
+    const int64_t teacher = 16 * int64_t(e.K) + p.bits / 4;
+    // A row's blocks: as many as give every SM four, while a thread has four vectors and more; and as many as keep a
+    // block's part small enough for four on an SM.
+    int C = 1;
+    while (C < 8 && e.N * C < 4 * int64_t(d.sms) && vecs >= int64_t(C) * 2 * DISTILL_WARPS * 32 * 4) C *= 2;
+    if (mode == DISTILL_GRAD) {
+        while (C < 8 && (vecs + C - 1) / C * 16 + teacher > 55 * 1024) C *= 2;
+        const int64_t part = (vecs + C - 1) / C * 16;
+        p.stage_bytes = part + teacher <= most ? int(part) : 0;
+    }
+    p.cluster = C;
+    p.smem = int(teacher) + p.stage_bytes;
+    p.blocks = e.N * C;
+    return p;
+}
+
+namespace {
+
+template <typename T, int MODE>
+cudaError_t launch_distill(const DistillPlan& p, DistillParams a, const void* z, const float* weight, float* zmax,
+                           float* zlog, float* loss, void* dz, cudaStream_t s)
+{
+    a.cluster = p.cluster;
+    a.rows = p.rows;
+    a.bits = p.bits;
+    a.stage_bytes = p.stage_bytes;
+    auto go = [&](auto kern) {
+        return launch_ex(kern, dim3(unsigned(p.blocks)), dim3(p.threads), p.smem, s, p.cluster, true, a,
+                         static_cast<const T*>(z), weight, zmax, zlog, loss, static_cast<T*>(dz));
+    };
+    if (p.warp) {
+        const cudaError_t e = ensure_smem<distill_kernel<T, MODE, true>>(p.smem);
+        return e != cudaSuccess ? e : go(distill_kernel<T, MODE, true>);
+    }
+    const cudaError_t e = ensure_smem<distill_kernel<T, MODE, false>>(p.smem);
+    return e != cudaSuccess ? e : go(distill_kernel<T, MODE, false>);
+}
+
+template <int MODE>
+cudaError_t run_distill(const conv_distill_desc_t& e, const DevInfo& d, const DistillParams& a, const void* z,
+                        const float* weight, float* zmax, float* zlog, float* loss, void* dz, cudaStream_t s)
+{
+    const DistillPlan p = distill_plan(e, d, MODE);
+    return e.dtype == CONV_F32 ? launch_distill<float, MODE>(p, a, z, weight, zmax, zlog, loss, dz, s)
+                               : launch_distill<__nv_bfloat16, MODE>(p, a, z, weight, zmax, zlog, loss, dz, s);
+}
+
+}  // namespace
+
+cudaError_t run_distill_fwd(const conv_distill_desc_t& e, const DevInfo& d, const void* z, const void* ids,
+                            const void* teacher, float* loss, float* zmax, float* zlog, cudaStream_t s)
+{
+    return run_distill<DISTILL_FWD>(e, d, distill_params(e, ids, teacher, 1.f), z, nullptr, zmax, zlog, loss, nullptr, s);
+}
+cudaError_t run_distill_bwd(const conv_distill_desc_t& e, const DevInfo& d, const void* z, const void* ids,
+                            const void* teacher, const float* zmax, const float* zlog, const float* weight, float scale,
+                            void* dz, cudaStream_t s)
+{
+    return run_distill<DISTILL_BWD>(e, d, distill_params(e, ids, teacher, scale), z, weight, const_cast<float*>(zmax),
+                                    const_cast<float*>(zlog), nullptr, dz, s);
+}
+cudaError_t run_distill_grad(const conv_distill_desc_t& e, const DevInfo& d, const void* z, const void* ids,
+                             const void* teacher, const float* weight, float scale, float* loss, void* dz, cudaStream_t s)
+{
+    return run_distill<DISTILL_GRAD>(e, d, distill_params(e, ids, teacher, scale), z, weight, nullptr, nullptr, loss, dz,
+                                     s);
+}
+
+}  // namespace igc

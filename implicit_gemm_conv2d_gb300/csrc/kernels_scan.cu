@@ -295,7 +295,7 @@ struct ScanAt {
 template <typename T, int L, int CB, int DIR> struct ScanCopy {
     using Tile = ScanTile<T, L>;
     static constexpr int ES = Tile::ES, CPR = Tile::ROW / CB, ROWS = SCAN_THREADS / CPR, N = Tile::RT / ROWS;
-    static constexpr int UNROLL = N <= 4 || CB == 2 ? std::min(N, 4) : 2;  // (more spills)
+    static constexpr int UNROLL = std::min(N, CB == 2 ? 8 : 16);
     struct Cursor {
         T* at;               // of the thread's first step of the round
         int64_t hop, round;  // from one of its steps, and of its rounds, to the next
@@ -324,50 +324,54 @@ template <typename T, int L, int CB, int DIR> struct ScanCopy {
         return {a + (q.b0 + by) * r.batch + q.c0 + column + (first + DIR * u0) * r.step, DIR * ROWS * r.step,
                 DIR * span * r.step};
     }
-    // The round that begins at step first; what the row does not have, or has not `shift` steps earlier, is zeros.
-    // any: an address to name where nothing is read.
-    __device__ __forceinline__ void fill(Cursor& c, uint32_t to, int64_t first, int shift, const T* any) const
+    // The round that begins at step first: the steps that the row has, and `shift` steps earlier too.  (What is not
+    // copied is not used.)
+    __device__ __forceinline__ void fill(Cursor& c, uint32_t to, int first, int shift) const
     {
         const T* src = c.at;
-        const int64_t last = first + DIR * (Tile::RT - 1);
-        if (CB > 2 && (DIR > 0 ? last < len : first < len && last >= shift)) {
+        const int last = first + DIR * (Tile::RT - 1), low = DIR > 0 ? first : last, high = DIR > 0 ? last : first;
+        if (low >= shift && high < len) {
 #pragma unroll UNROLL
-            for (int k = 0; k < N; ++k, src += c.hop) copy(to + Tile::place(u0 + k * ROWS, byte), src, true);
-        } else {
+            for (int k = 0; k < N; ++k, src += c.hop) copy(to + Tile::place(u0 + k * ROWS, byte), src);
+        } else if (low < len) {
+            const unsigned some = unsigned(len - shift);  // len > low >= -RT: steps shift .. len - 1, none if len <= shift
 #pragma unroll UNROLL
-            for (int k = 0; k < N; ++k, src += c.hop) {
-                const int64_t t = first + DIR * (u0 + k * ROWS);
-                const bool there = t < len && t >= shift;
-                copy(to + Tile::place(u0 + k * ROWS, byte), there ? src : any, there);
-            }
+            for (int k = 0; k < N; ++k, src += c.hop)
+                if (len > shift && unsigned(first + DIR * (u0 + k * ROWS) - shift) < some)
+                    copy(to + Tile::place(u0 + k * ROWS, byte), src);
         }
         c.at += c.round;
     }
-    static __device__ __forceinline__ void copy(uint32_t dst, const T* src, bool there)
+    static __device__ __forceinline__ void copy(uint32_t dst, const T* src)
     {
         if constexpr (CB == 16)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
         else if constexpr (CB == 4)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
         else
-            tc::sts16(dst, there ? *reinterpret_cast<const uint16_t*>(src) : 0u);
+            tc::sts16(dst, *reinterpret_cast<const uint16_t*>(src));
     }
     // A round's results back to memory.
-    __device__ __forceinline__ void drain(Cursor& c, uint32_t from, int64_t first, int T_) const
+    __device__ __forceinline__ void drain(Cursor& c, uint32_t from, int first, int T_) const
     {
         T* dst = c.at;
-        if (out) {
+        const int last = first + DIR * (Tile::RT - 1);
+        if (out && first >= 0 && first < T_ && last >= 0 && last < T_) {
 #pragma unroll UNROLL
-            for (int k = 0; k < N; ++k, dst += c.hop) {
-                const int64_t t = first + DIR * (u0 + k * ROWS);
-                if (t < 0 || t >= T_) continue;
-                const uint32_t src = from + Tile::place(u0 + k * ROWS, byte);
-                if constexpr (CB == 16) *reinterpret_cast<int4*>(dst) = tc::lds128(src);
-                else if constexpr (CB == 4) *reinterpret_cast<uint32_t*>(dst) = tc::lds32(src);
-                else *reinterpret_cast<uint16_t*>(dst) = uint16_t(tc::lds16(src));
-            }
+            for (int k = 0; k < N; ++k, dst += c.hop) back(dst, from + Tile::place(u0 + k * ROWS, byte));
+        } else if (out) {
+#pragma unroll UNROLL
+            for (int k = 0; k < N; ++k, dst += c.hop)
+                if (unsigned(first + DIR * (u0 + k * ROWS)) < unsigned(T_))
+                    back(dst, from + Tile::place(u0 + k * ROWS, byte));
         }
         c.at += c.round;
+    }
+    static __device__ __forceinline__ void back(T* dst, uint32_t src)
+    {
+        if constexpr (CB == 16) *reinterpret_cast<int4*>(dst) = tc::lds128(src);
+        else if constexpr (CB == 4) *reinterpret_cast<uint32_t*>(dst) = tc::lds32(src);
+        else *reinterpret_cast<uint16_t*>(dst) = uint16_t(tc::lds16(src));
     }
 };
 
@@ -429,24 +433,31 @@ struct ScanExchange {
             if (int(threadIdx.x & 31) >= o) scan_join<RESET>(A, H, a, h);
         }
     }
-    // (A, H): the lane's stretch.  state: in, what enters the round; out, what enters the next one.  Returns what
-    // enters the lane's stretch.
-    template <bool RESET>
-    __device__ __forceinline__ float2 run(const ScanAt& q, int round, float2 A, float2 H, float2& state)
+    // Joins the warp's stretches; (A, H) become the lane's and all before it.  With a cluster, tells its blocks.
+    template <bool RESET> __device__ __forceinline__ void send(const ScanAt& q, int round, float2& A, float2& H) const
     {
         join_all<RESET>(A, H);
+        if (q.C == 1) return;
+        // the last stretch's lanes hold the warp's; lane (seg, pair) tells rank seg
+        const float2 a = shfl(A, 28 + q.pair), h = shfl(H, 28 + q.pair);
+        if (q.seg < q.C && !dead) {
+            const int parity = round & 1;
+            const uint32_t to = slots + uint32_t(((parity * q.C + q.rank) * SCAN_WARPS + q.warp) * 64 + q.pair * 16);
+            tc::st_async_f4(tc::dsmem_addr(to, uint32_t(q.seg)),
+                            tc::dsmem_addr(bars + uint32_t(parity) * 8, uint32_t(q.seg)), a.x, a.y, h.x, h.y);
+        }
+    }
+    // state: in, what enters the round; out, what enters the next one.  Returns what enters the lane's stretch.
+    template <bool RESET>
+    __device__ __forceinline__ float2 receive(const ScanAt& q, int round, float2 A, float2 H, float2& state)
+    {
         float2 enter = state;
         if (q.C > 1) {
             const int parity = round & 1;
-            const uint32_t base = slots + uint32_t((parity * q.C * SCAN_WARPS + q.warp) * 64 + q.pair * 16);
-            const uint32_t bar = bars + uint32_t(parity) * 8;
-            // the last stretch's lanes hold the warp's
-            if (q.seg == SCAN_SEGS - 1 && !dead) {
-                const uint32_t mine = base + uint32_t(q.rank * SCAN_WARPS * 64);
-                for (int r = 0; r < q.C; ++r)
-                    tc::st_async_f4(tc::dsmem_addr(mine, uint32_t(r)), tc::dsmem_addr(bar, uint32_t(r)), A.x, A.y, H.x, H.y);
-            }
-            if (!dead && !tc::mbar_wait(bar, uint32_t(round >> 1) & 1u)) {
+            const uint32_t bar = bars + uint32_t(parity) * 8, phase = uint32_t(round >> 1) & 1u;
+            bool here = dead;
+            for (int k = 0; k < 32 && !here; ++k) here = tc::mbar_test_wait(bar, phase);  // soon, mostly
+            if (!here && !tc::mbar_wait(bar, phase)) {
                 dead = true;  // the results are wrong and the status says so; every later wait is skipped
                 atomicOr(&g_scan_status, CONV_STATUS_SCAN);
             }
@@ -454,7 +465,7 @@ struct ScanExchange {
             // lane (seg, pair) takes rank seg's
             float2 a = both(1.f), h = both(0.f);
             if (q.seg < q.C) {
-                const float4 v = tc::lds_f4(base + uint32_t(q.seg * SCAN_WARPS * 64));
+                const float4 v = tc::lds_f4(slots + uint32_t(((parity * q.C + q.seg) * SCAN_WARPS + q.warp) * 64 + q.pair * 16));
                 a = make_float2(v.x, v.y);
                 h = make_float2(v.z, v.w);
             }
@@ -477,12 +488,12 @@ template <int L, int DIR> struct ScanFlags {
     const uint8_t* row = nullptr;
     int len = 0;
     uint32_t next = 0;
-    __device__ __forceinline__ void fetch(const ScanAt& q, int64_t t0)
+    __device__ __forceinline__ void fetch(const ScanAt& q, int t0)
     {
         next = 0;
 #pragma unroll
         for (int k = 0; k < L / 4; ++k) {
-            const int64_t t = t0 + DIR * (q.pair + 4 * k);
+            const int t = t0 + DIR * (q.pair + 4 * k);
             if (row && t >= 0 && t < len && row[t] != 0) next |= 1u << (4 * k);
         }
     }
@@ -557,7 +568,7 @@ scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
     using Copy = ScanCopy<T, L, CB, 1>;
     const Copy copy(p, q, lens);
     const ScanLane<T, L> lane(q);
-    const int64_t span = int64_t(q.C) * Tile::RT, rank0 = int64_t(q.rank) * Tile::RT;
+    const int span = q.C * Tile::RT, rank0 = q.rank * Tile::RT;  // (T + span is below 2^31)
     typename Copy::Cursor cx = copy.cursor(q, x, p.x, rank0, span), cg = copy.cursor(q, gate, p.gate, rank0, span);
     typename Copy::Cursor ch = copy.cursor(q, h, p.h, rank0, span);
     ScanFlags<L, 1> flags;
@@ -566,22 +577,27 @@ scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
         flags.len = len;
         flags.fetch(q, rank0 + q.seg * L);
     }
-    auto fill = [&](int slot, int64_t base) {
+    auto fill = [&](int slot, int base) {
         if (base < p.T) {
-            copy.fill(cx, stages + slot * STAGE, base + rank0, 0, x);
-            copy.fill(cg, stages + slot * STAGE + Tile::ARRAY, base + rank0, 0, gate);
+            copy.fill(cx, stages + slot * STAGE, base + rank0, 0);
+            copy.fill(cg, stages + slot * STAGE + Tile::ARRAY, base + rank0, 0);
         }
         scan_commit();
     };
     for (int k = 0; k < p.stages - 1; ++k) fill(k, k * span);
     int now = 0, round = 0;
-    for (int64_t base = 0; base < p.T; base += span, ++round) {
+    for (int base = 0; base < p.T; base += span, ++round) {
         const int prev = now == 0 ? p.stages - 1 : now - 1;
         scan_arrived(p.stages);
-        if (round > 0) copy.drain(ch, stages + prev * STAGE, base - span + rank0, p.T);
-        fill(prev, base + (p.stages - 1) * span);
+        // The stage of a round ago, which nobody reads any more: its results go out, a later round comes in.  Between
+        // send and receive, where the cluster's answers are waited for; loads that a thread waits for come first.
+        auto turn = [&] {
+            if (round > 0) copy.drain(ch, stages + prev * STAGE, base - span + rank0, p.T);
+            fill(prev, base + (p.stages - 1) * span);
+        };
+        if (CB == 2) turn();
         const uint32_t stage = stages + now * STAGE;
-        const int64_t t0 = base + rank0 + q.seg * L;
+        const int t0 = base + rank0 + q.seg * L;
         uint32_t cut = 0;
         if (RESET) {
             cut = flags.take(q);
@@ -613,7 +629,9 @@ scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
             A = mul2(A, keep[i]);
         }
         if (RESET && cut != 0) A = both(-1.f);
-        float2 st = ex.run<RESET>(q, round, A, H, state);
+        ex.send<RESET>(q, round, A, H);
+        if (CB != 2) turn();
+        float2 st = ex.receive<RESET>(q, round, A, H, state);
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             if (RESET && (cut >> i & 1u)) st = both(0.f);
@@ -657,7 +675,7 @@ scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
     using Copy = ScanCopy<T, L, CB, -1>;
     const Copy copy(p, q, lens);
     const ScanLane<T, L> lane(q);
-    const int64_t span = int64_t(q.C) * Tile::RT, last0 = int64_t(p.T) - 1 - int64_t(q.rank) * Tile::RT;
+    const int span = q.C * Tile::RT, last0 = p.T - 1 - q.rank * Tile::RT;
     typename Copy::Cursor cx = copy.cursor(q, x, p.x, last0, span), cg = copy.cursor(q, gate, p.gate, last0, span),
                           cd = copy.cursor(q, dh, p.dh, last0, span), ch = copy.cursor(q, h, p.h, last0 - 1, span),
                           ox = copy.cursor(q, dx, p.dx, last0, span), og = copy.cursor(q, dgate, p.dgate, last0, span);
@@ -667,29 +685,34 @@ scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
         flags.len = len;
         flags.fetch(q, last0 - q.seg * L);
     }
-    auto fill = [&](int slot, int64_t base) {
+    auto fill = [&](int slot, int base) {
         if (base < p.T) {
             const uint32_t to = stages + slot * STAGE;
-            copy.fill(cx, to, last0 - base, 0, x);
-            copy.fill(cg, to + Tile::ARRAY, last0 - base, 0, gate);
-            copy.fill(cd, to + 2 * Tile::ARRAY, last0 - base, 0, dh);
-            copy.fill(ch, to + 3 * Tile::ARRAY, last0 - base, 1, h);
+            copy.fill(cx, to, last0 - base, 0);
+            copy.fill(cg, to + Tile::ARRAY, last0 - base, 0);
+            copy.fill(cd, to + 2 * Tile::ARRAY, last0 - base, 0);
+            copy.fill(ch, to + 3 * Tile::ARRAY, last0 - base, 1);
         }
         scan_commit();
     };
-    auto drain = [&](int slot, int64_t base) {
+    auto drain = [&](int slot, int base) {
         copy.drain(ox, stages + slot * STAGE, last0 - base, p.T);
         copy.drain(og, stages + slot * STAGE + Tile::ARRAY, last0 - base, p.T);
     };
     for (int k = 0; k < p.stages - 1; ++k) fill(k, k * span);
     int now = 0, round = 0;
-    for (int64_t base = 0; base < p.T; base += span, ++round) {
+    for (int base = 0; base < p.T; base += span, ++round) {
         const int prev = now == 0 ? p.stages - 1 : now - 1;
         scan_arrived(p.stages);
-        if (round > 0) drain(prev, base - span);
-        fill(prev, base + (p.stages - 1) * span);
+        // The stage of a round ago, which nobody reads any more: its results go out, a later round comes in.  Between
+        // send and receive, where the cluster's answers are waited for; loads that a thread waits for come first.
+        auto turn = [&] {
+            if (round > 0) drain(prev, base - span);
+            fill(prev, base + (p.stages - 1) * span);
+        };
+        if (CB == 2) turn();
         const uint32_t stage = stages + now * STAGE;
-        const int64_t t0 = last0 - base - q.seg * L;
+        const int t0 = last0 - base - q.seg * L;
         uint32_t cut = 0;
         if (RESET) {
             cut = flags.take(q);
@@ -722,7 +745,9 @@ scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
             A = mul2(A, keep);
         }
         if (RESET && cut != 0) A = both(-1.f);
-        float2 st = ex.run<RESET>(q, round, A, H, state);
+        ex.send<RESET>(q, round, A, H);
+        if (CB != 2) turn();
+        float2 st = ex.receive<RESET>(q, round, A, H, state);
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             const float2 f = add2(d[i], st);
@@ -795,7 +820,7 @@ ScanPlan scan_plan(const conv_scan_desc_t& e, const DevInfo& d, bool bwd, int ch
     p.cluster = 1 << log_c;
     p.threads = SCAN_THREADS;
     p.blocks = blocks << log_c;
-    p.stages = 2;
+    p.stages = rounds > (int64_t(2) << log_c) ? 3 : 2;
     return p;
 }
 

@@ -365,6 +365,89 @@ PyObject* gated_scan_bwd(PyObject* const* a)
     return wrap(dx, dgate, dh0);
 }
 
+// z (rows, logits), the rows any distance apart.
+conv_distill_desc_t distill_desc(const at::Tensor& z, const at::Tensor& ids, const at::Tensor& teacher, double temperature)
+{
+    conv_distill_desc_t d;
+    d.dtype = dtype_code(z, "z");
+    d.teacher_dtype = dtype_code(teacher, "teacher");
+    if (ids.scalar_type() == at::kInt) d.index_dtype = CONV_INDEX_I32;
+    else if (ids.scalar_type() == at::kLong) d.index_dtype = CONV_INDEX_I64;
+    else value_error("ids: int32 or int64");
+    if (z.dim() != 2 || ids.dim() != 2 || ids.size(0) != z.size(0) || ids.sizes() != teacher.sizes())
+        value_error("z: (rows, logits); ids and teacher: (rows, entries)");
+    if (!z.is_cuda()) value_error("tensors must be CUDA tensors");
+    if (z.size(1) > 1 && z.stride(1) != 1) value_error("z: a row's logits have to lie one behind the other");
+    on_gpu(ids);
+    on_gpu(teacher);
+    if (ids.device() != z.device() || teacher.device() != z.device()) value_error("tensors on different devices");
+    on_current(z);
+    d.N = z.size(0);
+    d.V = size32(z.size(1));
+    d.K = size32(ids.size(1));
+    d.ld = d.N > 1 ? z.stride(0) : d.V;
+    d.temperature = float(temperature);
+    return d;
+}
+
+float* row_values(const at::Tensor* t, const char* name, const at::Tensor& z)
+{
+    return t ? static_cast<float*>(same(*t, name, {z.size(0)}, at::kFloat, z.device()).data_ptr()) : nullptr;
+}
+
+// dz with z's distances; out: the tensor to write to.
+at::Tensor logit_grads(PyObject* out, const at::Tensor& z, int64_t ld)
+{
+    const at::Tensor* t = optional(out, "out");
+    if (!t) return at::empty_strided(z.sizes(), {ld, 1}, z.options());
+    if (t->sizes() != z.sizes() || t->scalar_type() != z.scalar_type() || t->device() != z.device() ||
+        (t->size(1) > 1 && t->stride(1) != 1) || (t->size(0) > 1 && t->stride(0) != ld))
+        value_error("out: z's sizes, dtype, device and distances");
+    return *t;
+}
+
+// z, ids, teacher, temperature
+PyObject* distill(PyObject* const* a)
+{
+    const at::Tensor &z = tensor(a[0], "z"), &ids = tensor(a[1], "ids"), &teacher = tensor(a[2], "teacher");
+    const conv_distill_desc_t d = distill_desc(z, ids, teacher, number(a[3]));
+    const auto options = z.options().dtype(at::kFloat);
+    const at::Tensor loss = at::empty({d.N}, options), zmax = at::empty({d.N}, options), zlog = at::empty({d.N}, options);
+    check(conv_distill_fwd(&d, z.data_ptr(), ids.data_ptr(), teacher.data_ptr(), static_cast<float*>(loss.data_ptr()),
+                           static_cast<float*>(zmax.data_ptr()), static_cast<float*>(zlog.data_ptr()), stream_of(z)),
+          "conv_distill_fwd");
+    return wrap(loss, zmax, zlog);
+}
+
+// z, ids, teacher, zmax, zlog, weight, scale, temperature, out
+PyObject* distill_bwd(PyObject* const* a)
+{
+    const at::Tensor &z = tensor(a[0], "z"), &ids = tensor(a[1], "ids"), &teacher = tensor(a[2], "teacher");
+    const conv_distill_desc_t d = distill_desc(z, ids, teacher, number(a[7]));
+    const float *zmax = row_values(&tensor(a[3], "zmax"), "zmax", z), *zlog = row_values(&tensor(a[4], "zlog"), "zlog", z);
+    const float* weight = row_values(optional(a[5], "weight"), "weight", z);
+    const double scale = number(a[6]);
+    const at::Tensor dz = logit_grads(a[8], z, d.ld);
+    check(conv_distill_bwd(&d, z.data_ptr(), ids.data_ptr(), teacher.data_ptr(), zmax, zlog, weight, float(scale),
+                           dz.data_ptr(), stream_of(z)),
+          "conv_distill_bwd");
+    return wrap(dz);
+}
+
+// z, ids, teacher, weight, scale, temperature, out
+PyObject* distill_grad(PyObject* const* a)
+{
+    const at::Tensor &z = tensor(a[0], "z"), &ids = tensor(a[1], "ids"), &teacher = tensor(a[2], "teacher");
+    const conv_distill_desc_t d = distill_desc(z, ids, teacher, number(a[5]));
+    const float* weight = row_values(optional(a[3], "weight"), "weight", z);
+    const double scale = number(a[4]);
+    const at::Tensor loss = at::empty({d.N}, z.options().dtype(at::kFloat)), dz = logit_grads(a[6], z, d.ld);
+    check(conv_distill_grad(&d, z.data_ptr(), ids.data_ptr(), teacher.data_ptr(), weight, float(scale),
+                            static_cast<float*>(loss.data_ptr()), dz.data_ptr(), stream_of(z)),
+          "conv_distill_grad");
+    return wrap(loss, dz);
+}
+
 // grads, out (None: in place), max_norm (None: the norm only).  The sequences are tuples or lists.
 PyObject* grads_call(PyObject* const* a)
 {
@@ -442,6 +525,9 @@ PyMethodDef methods[] = {ENTRY("group_norm", group_norm, 8),
                          ENTRY("embed_bwd", embed_bwd, 5),
                          ENTRY("gated_scan", gated_scan, 7),
                          ENTRY("gated_scan_bwd", gated_scan_bwd, 10),
+                         ENTRY("distill", distill, 4),
+                         ENTRY("distill_bwd", distill_bwd, 9),
+                         ENTRY("distill_grad", distill_grad, 7),
                          ENTRY("grads", grads_call, 3),
                          ENTRY("set_errors", set_errors, 2),
                          {nullptr, nullptr, 0, nullptr}};

@@ -191,6 +191,10 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same barrier in two halves: what lies between them runs while the other CTAs arrive.  The first half
+// announces no writes.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // The shared::cluster address of the variable at shared::cta address `saddr` in CTA `rank`.
 __device__ __forceinline__ uint32_t dsmem_addr(uint32_t saddr, uint32_t rank)
 {
@@ -206,6 +210,10 @@ __device__ __forceinline__ float4 ld_dsmem_f4(uint32_t addr)
                  : "r"(addr)
                  : "memory");
     return v;
+}
+__device__ __forceinline__ void st_dsmem_f2(uint32_t addr, float a, float b)
+{
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
 }
 // Store 16 bytes to a CTA of the cluster and count them on a barrier of that CTA (both addresses in
 // its shared::cluster window, see dsmem_addr).

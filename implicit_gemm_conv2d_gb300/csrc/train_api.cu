@@ -77,6 +77,18 @@ int scan_check(const conv_scan_desc_t* d, bool bwd)
     return CONV_OK;
 }
 
+int distill_check(const conv_distill_desc_t* d)
+{
+    if (!d) return CONV_ERR_NULL;
+    if (d->N < 0 || d->V < 1 || d->K < 1 || d->ld < d->V || (d->dtype != CONV_F32 && d->dtype != CONV_BF16) ||
+        (d->teacher_dtype != CONV_F32 && d->teacher_dtype != CONV_BF16) ||
+        (d->index_dtype != CONV_INDEX_I32 && d->index_dtype != CONV_INDEX_I64) || !std::isfinite(d->temperature) ||
+        !(d->temperature > 0.f) || !std::isfinite(1.f / d->temperature))
+        return CONV_ERR_DESC;
+    if (d->N >= 1 << 27 || d->V >= 1 << 30 || d->K > 1024 || d->ld >= int64_t(1) << 32) return CONV_ERR_UNSUPPORTED;
+    return CONV_OK;
+}
+
 // `clip`: out is checked too.
 int grads_check(const conv_grad_t* g, int32_t count, bool clip)
 {
@@ -237,6 +249,57 @@ int conv_scan_bwd(const conv_scan_desc_t* desc, const void* x, const void* gate,
     if ((rc = device_info(d)) != CONV_OK) return rc;
     return cuda_status(run_scan_bwd(*desc, d, x, gate, h, dh, h0, dlast, reset, lengths, dx, dgate, dh0,
                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int conv_distill_fwd(const conv_distill_desc_t* desc, const void* z, const void* ids, const void* teacher, float* loss,
+                     float* zmax, float* zlog, conv_stream_t stream)
+{
+    int rc = distill_check(desc);
+    if (rc != CONV_OK) return rc;
+    if (desc->N == 0) return CONV_OK;
+    if (!z || !ids || !teacher || !loss || !zmax || !zlog) return CONV_ERR_NULL;
+    if (!aligned16(z) || !aligned16(ids) || !aligned16(teacher) || !aligned16(loss) || !aligned16(zmax) ||
+        !aligned16(zlog))
+        return CONV_ERR_ALIGN;
+    DevInfo d;
+    if ((rc = device_info(d)) != CONV_OK) return rc;
+    return cuda_status(
+        run_distill_fwd(*desc, d, z, ids, teacher, loss, zmax, zlog, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int conv_distill_bwd(const conv_distill_desc_t* desc, const void* z, const void* ids, const void* teacher,
+                     const float* zmax, const float* zlog, const float* weight, float scale, void* dz,
+                     conv_stream_t stream)
+{
+    int rc = distill_check(desc);
+    if (rc != CONV_OK) return rc;
+    if (!std::isfinite(scale)) return CONV_ERR_DESC;
+    if (desc->N == 0) return CONV_OK;
+    if (!z || !ids || !teacher || !zmax || !zlog || !dz) return CONV_ERR_NULL;
+    if (!aligned16(z) || !aligned16(ids) || !aligned16(teacher) || !aligned16(zmax) || !aligned16(zlog) ||
+        !aligned16(weight) || !aligned16(dz))
+        return CONV_ERR_ALIGN;
+    DevInfo d;
+    if ((rc = device_info(d)) != CONV_OK) return rc;
+    return cuda_status(run_distill_bwd(*desc, d, z, ids, teacher, zmax, zlog, weight, scale, dz,
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int conv_distill_grad(const conv_distill_desc_t* desc, const void* z, const void* ids, const void* teacher,
+                      const float* weight, float scale, float* loss, void* dz, conv_stream_t stream)
+{
+    int rc = distill_check(desc);
+    if (rc != CONV_OK) return rc;
+    if (!std::isfinite(scale)) return CONV_ERR_DESC;
+    if (desc->N == 0) return CONV_OK;
+    if (!z || !ids || !teacher || !loss || !dz) return CONV_ERR_NULL;
+    if (!aligned16(z) || !aligned16(ids) || !aligned16(teacher) || !aligned16(loss) || !aligned16(weight) ||
+        !aligned16(dz))
+        return CONV_ERR_ALIGN;
+    DevInfo d;
+    if ((rc = device_info(d)) != CONV_OK) return rc;
+    return cuda_status(
+        run_distill_grad(*desc, d, z, ids, teacher, weight, scale, loss, dz, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t conv_grad_norm_workspace_size(const conv_grad_t* grads, int32_t count)

@@ -138,4 +138,30 @@ cudaError_t run_scan_bwd(const conv_scan_desc_t& e, const DevInfo& d, const void
                          const void* dh, const float* h0, const float* dlast, const uint8_t* reset,
                          const int32_t* lengths, void* dx, void* dgate, float* dh0, cudaStream_t s);
 
+// ---- loss against a teacher's top logits (kernels_distill.cu) --------------------------------
+struct DistillParams {
+    int64_t N, ld;
+    int V, K;
+    const void *ids, *teacher;
+    bool ids64, teacher_bf16;
+    float tau, k, scale;         // k: log2(e) / tau
+    int cluster, rows, bits, stage_bytes;
+};
+struct DistillPlan {
+    bool warp;                   // a warp a row
+    int cluster, rows;           // blocks a row, rows a block
+    int bits, stage_bytes;       // of an id bitmap; of a block's (a warp's) part of a row in shared memory
+    int threads, smem;
+    int64_t blocks;
+};
+// mode: 0 forward, 1 backward, 2 both at once
+DistillPlan distill_plan(const conv_distill_desc_t& e, const DevInfo& d, int mode);
+cudaError_t run_distill_fwd(const conv_distill_desc_t& e, const DevInfo& d, const void* z, const void* ids,
+                            const void* teacher, float* loss, float* zmax, float* zlog, cudaStream_t s);
+cudaError_t run_distill_bwd(const conv_distill_desc_t& e, const DevInfo& d, const void* z, const void* ids,
+                            const void* teacher, const float* zmax, const float* zlog, const float* weight, float scale,
+                            void* dz, cudaStream_t s);
+cudaError_t run_distill_grad(const conv_distill_desc_t& e, const DevInfo& d, const void* z, const void* ids,
+                             const void* teacher, const float* weight, float scale, float* loss, void* dz, cudaStream_t s);
+
 }  // namespace igc

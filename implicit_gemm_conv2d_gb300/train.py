@@ -30,7 +30,7 @@ _IDX = {torch.int32: 0, torch.int64: 1}
 
 EXPORTS = ["conv_gn_fwd_workspace_size", "conv_gn_fwd", "conv_gn_bwd_workspace_size", "conv_gn_bwd",
            "conv_embed_fwd", "conv_embed_bwd_workspace_size", "conv_embed_bwd",
-           "conv_scan_fwd", "conv_scan_bwd",
+           "conv_scan_fwd", "conv_scan_bwd", "conv_distill_fwd", "conv_distill_bwd", "conv_distill_grad",
            "conv_grad_norm_workspace_size", "conv_grad_norm", "conv_grad_clip"]
 
 
@@ -51,6 +51,12 @@ class Rows(ctypes.Structure):
 class ScanDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "D", "dtype")] + \
         [(n, Rows) for n in ("x", "gate", "h", "dh", "dx", "dgate")]
+
+
+class DistillDesc(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("ld", ctypes.c_int64)] + \
+        [(n, ctypes.c_int32) for n in ("V", "K", "dtype", "index_dtype", "teacher_dtype")] + \
+        [("temperature", ctypes.c_float)]
 
 
 class Grad(ctypes.Structure):
@@ -80,6 +86,9 @@ def lib():
             L.conv_embed_bwd.argtypes = [vp] * 5 + [sz, vp]
             L.conv_scan_fwd.argtypes = [vp] * 9
             L.conv_scan_bwd.argtypes = [vp] * 13
+            L.conv_distill_fwd.argtypes = [vp] * 8
+            L.conv_distill_bwd.argtypes = [vp] * 7 + [ctypes.c_float, vp, vp]
+            L.conv_distill_grad.argtypes = [vp] * 5 + [ctypes.c_float, vp, vp, vp]
             L.conv_grad_norm_workspace_size.argtypes = [vp, i32]
             L.conv_grad_norm_workspace_size.restype = sz
             L.conv_grad_norm.argtypes = [vp, i32, vp, vp, sz, vp]
@@ -267,6 +276,67 @@ def gated_scan_bwd(x, gate, h, dh, h0=None, dlast=None, reset=None, lengths=None
         with torch.cuda.stream(stream):
             return gated_scan_bwd(x, gate, h, dh, h0, dlast, reset, lengths, dx, dgate)
     return _native().gated_scan_bwd(x, gate, h, dh, h0, dlast, reset, lengths, dx, dgate)
+
+
+# ---- loss against a teacher's top logits -----------------------------------------------------
+def _logits_ptr(t):
+    """The address of (rows, logits) whose rows may be any distance apart."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("(rows, logits), a row's logits one behind the other")
+    return _ptr(t[:1])
+
+
+def make_distill_desc(z, ids, teacher, temperature=1.0) -> DistillDesc:
+    return DistillDesc(z.shape[0], z.stride(0) if z.shape[0] > 1 else z.shape[1], z.shape[1], ids.shape[1], _DT[z.dtype],
+                       _IDX[ids.dtype], _DT[teacher.dtype], temperature)
+
+
+def conv_distill_fwd(desc: DistillDesc, z, ids, teacher, loss, zmax, zlog, stream=None) -> None:
+    _check(lib().conv_distill_fwd(_ref(desc), _logits_ptr(z), _ptr(ids), _ptr(teacher), _ptr(loss), _ptr(zmax), _ptr(zlog),
+                                  _stream(stream)), "conv_distill_fwd")
+
+
+def conv_distill_bwd(desc: DistillDesc, z, ids, teacher, zmax, zlog, weight, scale, dz, stream=None) -> None:
+    """weight may be None; dz has z's distances and may be z."""
+    _check(lib().conv_distill_bwd(_ref(desc), _logits_ptr(z), _ptr(ids), _ptr(teacher), _ptr(zmax), _ptr(zlog),
+                                  _ptr(weight), scale, _logits_ptr(dz), _stream(stream)), "conv_distill_bwd")
+
+
+def conv_distill_grad(desc: DistillDesc, z, ids, teacher, weight, scale, loss, dz, stream=None) -> None:
+    """weight may be None; dz has z's distances and may be z."""
+    _check(lib().conv_distill_grad(_ref(desc), _logits_ptr(z), _ptr(ids), _ptr(teacher), _ptr(weight), scale, _ptr(loss),
+                                   _logits_ptr(dz), _stream(stream)), "conv_distill_grad")
+
+
+def distill(z, ids, teacher, temperature: float = 1.0, stream=None):
+    """loss, zmax, zlog of logits z (rows, V) against a teacher's logits (rows, K) at ids (rows, K): the
+    Kullback-Leibler divergence of the teacher's distribution over the K entries from the softmax of z,
+    both at the temperature, times its square.  Entries outside [0, V) or of -inf count for nothing; a
+    row without others has loss 0.  One entry a row at temperature 1 is the cross entropy.  zmax and
+    zlog are what distill_bwd takes.  z's rows may be any distance apart."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return distill(z, ids, teacher, temperature)
+    return _native().distill(z, ids, teacher, temperature)
+
+
+def distill_bwd(z, ids, teacher, zmax, zlog, weight=None, scale: float = 1.0, temperature: float = 1.0, out=None,
+                stream=None):
+    """dz of sum over the rows of scale * weight * loss, with z's distances between the rows; out: a tensor
+    with the same to write to, which may be z."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return distill_bwd(z, ids, teacher, zmax, zlog, weight, scale, temperature, out)
+    return _native().distill_bwd(z, ids, teacher, zmax, zlog, weight, scale, temperature, out)
+
+
+def distill_grad(z, ids, teacher, weight=None, scale: float = 1.0, temperature: float = 1.0, out=None, stream=None):
+    """loss and dz (distill, then distill_bwd) in one call that reads z once, for weights known before the
+    losses; the losses are without weight and scale."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return distill_grad(z, ids, teacher, weight, scale, temperature, out)
+    return _native().distill_grad(z, ids, teacher, weight, scale, temperature, out)
 
 
 # ---- gradient norm and clipping --------------------------------------------------------------

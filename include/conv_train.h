@@ -146,6 +146,49 @@ int conv_scan_bwd(const conv_scan_desc_t* desc, const void* x, const void* gate,
                   const float* h0, const float* dlast, const uint8_t* reset, const int32_t* lengths, void* dx,
                   void* dgate, float* dh0, conv_stream_t stream);
 
+/* ---- loss against a teacher's top logits ----------------------------------------------------
+ * Row n has V logits z and a teacher's K entries: ids and the teacher's logits at them.  With the
+ * temperature tau, P = softmax(z / tau) over all V and p = softmax(teacher / tau) over the row's
+ * entries:
+ *
+ *   loss[n] = tau^2 * sum_k p_k * (log p_k - log P[id_k])
+ *   dz[n,v] = scale * weight[n] * tau * (P[v] - sum of p_k over the k with id_k = v)
+ *
+ * (the factors tau^2 and tau keep the gradients' size over temperatures).  K = 1 is the cross entropy
+ * with the label id_0 at tau = 1.  An entry whose id is outside [0, V), or whose teacher's logit is
+ * -infinity, counts for nothing; a row without entries that count has loss 0 and dz 0, and one of weight 0
+ * has dz 0, whatever z holds there.  An id may occur more than once in a row.  z may hold -infinity
+ * (P is 0 there); a row that holds nothing else, +infinity or NaN gives NaN and leaves the other rows alone.
+ *
+ * z, dz: (N, V), a row's logits one behind the other, rows ld elements apart (ld >= V; dz is
+ * written at the row's V elements only), of the descriptor's dtype.  ids, teacher: (N, K) dense,
+ * teacher of teacher_dtype.  loss, zmax, zlog, weight: fp32, (N).  zmax[n] is the largest z of the
+ * row, zlog[n] = log sum_v exp((z[v] - zmax[n]) / tau): what the backward takes. */
+typedef struct {
+    int64_t N;              /* rows, >= 0                                                  */
+    int64_t ld;             /* elements from one row of z (and dz) to the next             */
+    int32_t V, K;           /* logits and teacher's entries a row, >= 1                    */
+    int32_t dtype;          /* conv_dtype_t of z and dz                                    */
+    int32_t index_dtype;    /* conv_index_t of ids                                         */
+    int32_t teacher_dtype;  /* conv_dtype_t of teacher                                     */
+    float temperature;      /* finite, > 0; 1 / temperature finite                         */
+} conv_distill_desc_t;
+
+/* Limits: N < 2^27, V < 2^30, K <= 1024 (CONV_ERR_UNSUPPORTED beyond); N * ld may pass 2^31.  N = 0 does
+ * nothing. */
+int conv_distill_fwd(const conv_distill_desc_t* desc, const void* z, const void* ids, const void* teacher, float* loss,
+                     float* zmax, float* zlog, conv_stream_t stream);
+
+/* weight: the gradient of each loss, or NULL (1).  scale: finite.  dz may be z (in place). */
+int conv_distill_bwd(const conv_distill_desc_t* desc, const void* z, const void* ids, const void* teacher,
+                     const float* zmax, const float* zlog, const float* weight, float scale, void* dz,
+                     conv_stream_t stream);
+
+/* The losses and the gradient at once, for weights known before the losses: z is read once where a row's
+ * part fits the chip (about 800 000 bf16 values).  dz may be z (in place). */
+int conv_distill_grad(const conv_distill_desc_t* desc, const void* z, const void* ids, const void* teacher,
+                      const float* weight, float scale, float* loss, void* dz, conv_stream_t stream);
+
 /* ---- global gradient norm and clipping ------------------------------------------------------
  *   norm = sqrt(sum over every tensor and element of g^2)
  *   out  = g * min(1, max_norm / (norm + 1e-6))

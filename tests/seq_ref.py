@@ -67,3 +67,54 @@ def scan_bwd(x, gate, h, dh, h0=None, dlast=None, reset=None, lengths=None):
         eb = np.where(fresh, 0.0, (1 - z) * el + 2 * U * (2 + z * (8 + 3 * np.abs(gate[:, t]))) * np.abs(lam))
         flow, e = np.where(there, back, flow), np.where(there, eb, e)
     return (dx, ex), (dg, eg), (flow, e)
+
+
+def teacher_probabilities(ids, teacher, V, tau):
+    """p (0 where the entry counts for nothing), log p, and which rows have entries that count."""
+    with np.errstate(invalid="ignore", divide="ignore"):
+        q = np.where((ids >= 0) & (ids < V), teacher, -np.inf) / tau
+        some = (q > -np.inf).any(axis=1)
+        x = q - np.where(some, q.max(axis=1, initial=-np.inf), 0.0)[:, None]
+        e = np.where(some[:, None], np.exp(x), 0.0)
+        s = np.where(some, e.sum(axis=1), 1.0)[:, None]
+        return e / s, x - np.log(s), some, np.where(e > 0, np.abs(x), 0.0)
+
+
+def distill_fwd(z, ids, teacher, tau):
+    """(loss, bound), zmax, (zlog, bound).
+
+    exp's argument (z - m) / tau is off by 3 U of itself and 2^x by 4 U; x exp(-x) is below 1, so the terms
+    leave 8 U of the sum, and its additions (64 + V / 512) U: a tree over chains of a few hundred
+    vectors.  log p and log P are off by 4 U of their terms."""
+    N, V = z.shape
+    K = ids.shape[1]
+    m = z.max(axis=1)
+    with np.errstate(invalid="ignore", divide="ignore"):
+        log = np.log(np.exp((z - m[:, None]) / tau).sum(axis=1))
+        blog = (72 + V / 512) * U + 2 * U * np.abs(log)
+        p, logp, some, x = teacher_probabilities(ids, teacher, V, tau)
+        zk = (np.take_along_axis(z, np.clip(ids, 0, V - 1), 1) - m[:, None]) / tau
+        logs = zk - log[:, None]
+        term = np.where(p > 0, p * (logp - logs), 0.0)
+        rel = (x + K / 16 + 16) * U
+        err = np.where(p > 0, rel * np.abs(term) + p * (rel + 4 * U * (np.abs(zk) + np.abs(logp) + 1) + blog[:, None]), 0.0)
+        return (tau * tau * term.sum(axis=1), tau * tau * (err.sum(axis=1) + (K / 16 + 16) * U * np.abs(term).sum(axis=1))), \
+            m, (log, blog)
+
+
+def distill_bwd(z, ids, teacher, m, log, weight, scale, tau, blog=0.0):
+    """dz and its bound; blog: of log's own error."""
+    N, V = z.shape
+    p, _, some, x = teacher_probabilities(ids, teacher, V, tau)
+    w = np.ones(N) if weight is None else weight
+    c = (scale * tau * w * some)[:, None]
+    a = (z - m[:, None]) / tau
+    P = np.exp(a - log[:, None])
+    relP = np.where(P > 0, 3 * U * np.abs(a), 0.0) + (3 * np.abs(log)[:, None] + 10) * U + np.reshape(blog, (-1, 1))
+    t, bt = np.zeros((N, V)), np.zeros((N, V))
+    for k in range(ids.shape[1]):
+        rows = np.flatnonzero((ids[:, k] >= 0) & (ids[:, k] < V))
+        np.add.at(t, (rows, ids[rows, k]), p[rows, k])
+        np.add.at(bt, (rows, ids[rows, k]), p[rows, k] * (x[rows, k] + ids.shape[1] / 8 + 20) * U)
+    dz = np.where(c != 0, c * (P - t), 0.0)
+    return dz, np.where(c != 0, np.abs(c) * (P * relP + bt + 1.2e-38) + 4 * U * np.abs(dz), 0.0)
