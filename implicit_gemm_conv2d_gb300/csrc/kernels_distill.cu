@@ -49,7 +49,10 @@ template <typename T> struct RowAt {
         first = at - off;
         vecs = (off + V + VE - 1) / VE;
     }
-    __device__ __forceinline__ bool whole(int j) const { return j * VE >= off && (j + 1) * VE <= off + V; }
+    // Vectors that lie in the row with all their elements: [first_whole, end_whole).
+    __device__ __forceinline__ int first_whole() const { return off > 0 ? 1 : 0; }
+    __device__ __forceinline__ int end_whole() const { return (off + V) / VE; }
+    __device__ __forceinline__ bool whole(int j) const { return j >= first_whole() && j < end_whole(); }
     __device__ __forceinline__ Vec<T, VE> load(const T* z, int j) const
     {
         Vec<T, VE> r;
@@ -82,13 +85,15 @@ template <typename T> struct RowAt {
     }
 };
 
-// One vector more.
 template <typename T, int VE> __device__ __forceinline__ float vec_max(const Vec<T, VE>& v)
 {
-    float m = v.get(0);
-#pragma unroll
-    for (int i = 1; i < VE; ++i) m = fmaxf(m, v.get(i));
-    return m;
+    if constexpr (sizeof(T) == 2) {
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(v.r.w);
+        const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        return fmaxf(__low2float(m), __high2float(m));
+    } else {
+        return fmaxf(fmaxf(v.get(0), v.get(1)), fmaxf(v.get(2), v.get(3)));
+    }
 }
 template <typename T, int VE> __device__ __forceinline__ float vec_sum(const Vec<T, VE>& v, float base, float k)
 {
@@ -227,6 +232,10 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
     const T* zrow = z + n * a.ld;
     const int per = (row.vecs + C - 1) / C, j0 = min(rank * per, row.vecs), j1 = min(j0 + per, row.vecs);
     const int lo = max(0, j0 * VE - row.off), hi = min(a.V, j1 * VE - row.off);  // the block's elements
+    // whole vectors of the block's, and the one that this thread takes by elements (-1: none)
+    const int w0 = max(j0, row.first_whole()), w1 = min(j1, row.end_whole());
+    int edge = me == 0 ? 0 : me == 1 && row.vecs > 1 ? row.vecs - 1 : -1;
+    if (edge >= 0 && (edge < j0 || edge >= j1 || row.whole(edge))) edge = -1;
     Teacher t(sm + (WARP ? warp * Teacher::bytes(a.K, a.bits) : 0), a.K, a.bits);
     uint8_t* const stage = sm + (WARP ? a.rows : 1) * Teacher::bytes(a.K, a.bits) +
                            (WARP ? warp * a.stage_bytes : 0);  // vector j - j0 at the thread that reads it
@@ -252,25 +261,37 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
     } else {
         if (teaches) teach();
         Stat st = {-INFINITY, 0.f};
+        auto take = [&](auto& v, int j) {  // vectors j, j + step, ..
+            constexpr int count = int(sizeof(v) / sizeof(v[0]));
+            float top = st.m;
+#pragma unroll
+            for (int u = 0; u < count; ++u) {
+                top = fmaxf(top, vec_max<T, VE>(v[u]));
+                if (staged) v[u].store(reinterpret_cast<T*>(stage + (j + u * step - j0) * 16));
+            }
+            const float base = finite_base(top);
+            if (top > st.m) st.s *= fast_exp2((st.m - base) * a.k);
+            st.m = top;
+#pragma unroll
+            for (int u = 0; u < count; ++u) st.s += vec_sum<T, VE>(v[u], base, a.k);
+        };
         if (sweeps) {
-            for (int j = j0 + me; j < j1; j += step * U) {
+            Vec<T, VE> one[1];
+            if (edge >= 0) {
+                one[0] = row.load(z, edge);
+                take(one, edge);
+            }
+            const T* src = z + row.first + int64_t(w0 + me) * VE;
+            int j = w0 + me;
+            for (; j + (U - 1) * step < w1; j += U * step, src += U * step * VE) {
                 Vec<T, VE> v[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (j + u * step < j1) v[u] = row.load(z, j + u * step);
-                float top = st.m;
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (j + u * step < j1) {
-                        top = fmaxf(top, vec_max<T, VE>(v[u]));
-                        if (staged) v[u].store(reinterpret_cast<T*>(stage + (j + u * step - j0) * 16));
-                    }
-                const float base = finite_base(top);
-                if (top > st.m) st.s *= fast_exp2((st.m - base) * a.k);
-                st.m = top;
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (j + u * step < j1) st.s += vec_sum<T, VE>(v[u], base, a.k);
+                for (int u = 0; u < U; ++u) v[u].load(src + u * step * VE);
+                take(v, j);
+            }
+            for (; j < w1; j += step, src += step * VE) {
+                one[0].load(src);
+                take(one, j);
             }
         }
 #pragma unroll
@@ -311,35 +332,53 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
     const bool zeros = empty || w == 0.f;
     if (teaches && !zeros) t.totals(a, lane);
     if (sweeps) {
-        for (int j = j0 + me; j < j1; j += step * U) {
-            Vec<T, VE> v[U];
-            if (!zeros) {
+        auto give = [&](Vec<T, VE>& v) {
+            float f[VE];
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (j + u * step < j1) {
-                        if (staged) v[u].load(reinterpret_cast<const T*>(stage + (j + u * step - j0) * 16));
-                        else v[u] = row.load(z, j + u * step);
-                    }
+            for (int i = 0; i < VE; i += 2) {
+                const float2 d = fma2(add2(make_float2(v.get(i), v.get(i + 1)), both(-m)), both(a.k), both(-log2_s));
+                const float2 e = mul2(make_float2(fast_exp2(d.x), fast_exp2(d.y)), both(c));
+                f[i] = e.x;
+                f[i + 1] = e.y;
             }
+            v.set(f);
+            if (zeros) v.zero();
+        };
+        Vec<T, VE> one;
+        if (edge >= 0) {
+            if (staged) one.load(reinterpret_cast<const T*>(stage + (edge - j0) * 16));
+            else one = row.load(z, edge);
+            give(one);
+            row.store(dz, edge, one);
+        }
+        T* dst = dz + row.first + int64_t(w0 + me) * VE;
+        auto sweep = [&](auto&& read) {  // read(v, j): vector j
+            int j = w0 + me;
+            for (; j + (U - 1) * step < w1; j += U * step, dst += U * step * VE) {
+                Vec<T, VE> v[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (j + u * step >= j1) continue;
-                Vec<T, VE> r;
-                if (zeros) {
-                    r.zero();
-                } else {
-                    float f[VE];
+                for (int u = 0; u < U; ++u) read(v[u], j + u * step);
 #pragma unroll
-                    for (int i = 0; i < VE; i += 2) {
-                        const float2 d = fma2(add2(make_float2(v[u].get(i), v[u].get(i + 1)), both(-m)), both(a.k),
-                                              both(-log2_s));
-                        f[i] = c * fast_exp2(d.x);
-                        f[i + 1] = c * fast_exp2(d.y);
-                    }
-                    r.set(f);
+                for (int u = 0; u < U; ++u) {
+                    give(v[u]);
+                    v[u].store(dst + u * step * VE);
                 }
-                row.store(dz, j + u * step, r);
             }
+            for (; j < w1; j += step, dst += step * VE) {
+                read(one, j);
+                give(one);
+                one.store(dst);
+            }
+        };
+        if (staged) {
+            const uint32_t at = tc::smem_u32(stage) - uint32_t(j0) * 16;
+            sweep([&](Vec<T, VE>& v, int j) {
+                const int4 q = tc::lds128(at + uint32_t(j) * 16);
+                v.r.w[0] = uint32_t(q.x); v.r.w[1] = uint32_t(q.y); v.r.w[2] = uint32_t(q.z); v.r.w[3] = uint32_t(q.w);
+            });
+        } else {
+            const T* src = z + row.first;
+            sweep([&](Vec<T, VE>& v, int j) { v.load(src + int64_t(j) * VE); });
         }
     }
     if (WARP) __syncwarp();
