@@ -149,6 +149,17 @@ PyObject* wrap(const at::Tensor& a, const at::Tensor& b, const at::Tensor& c)
     return t;
 }
 
+PyObject* wrap(const at::Tensor& a, const at::Tensor& b, const at::Tensor& c, const at::Tensor& d)
+{
+    PyObject* t = PyTuple_New(4);
+    if (!t) throw Raised();
+    PyTuple_SET_ITEM(t, 0, wrap(a));
+    PyTuple_SET_ITEM(t, 1, wrap(b));
+    PyTuple_SET_ITEM(t, 2, wrap(c));
+    PyTuple_SET_ITEM(t, 3, wrap(d));
+    return t;
+}
+
 conv_gn_desc_t gn_desc(const at::Tensor& x, PyObject* groups, double eps, PyObject* act, PyObject* layout)
 {
     conv_gn_desc_t d;
@@ -268,6 +279,70 @@ PyObject* embed_bwd(PyObject* const* a)
     check(conv_embed_bwd(&d, idx.data_ptr(), dy.data_ptr(), dtable.data_ptr(), address(ws), bytes, stream_of(dy)),
           "conv_embed_bwd");
     return wrap(dtable);
+}
+
+conv_ln_desc_t ln_desc(const at::Tensor& x, double eps, bool rms)
+{
+    conv_ln_desc_t d;
+    d.dtype = dtype_code(x, "x");
+    if (x.dim() < 1) value_error("x: at least (values)");
+    on_gpu(x);
+    on_current(x);
+    d.D = size32(x.size(-1));
+    d.N = 1;
+    for (int64_t i = 0; i + 1 < x.dim(); ++i) d.N *= x.size(i);
+    d.rms = rms;
+    d.eps = float(eps);
+    return d;
+}
+
+// x, gamma, beta, residual, eps, rms, stats
+PyObject* layer_norm(PyObject* const* a)
+{
+    const at::Tensor& x = tensor(a[0], "x");
+    const conv_ln_desc_t d = ln_desc(x, number(a[4]), PyObject_IsTrue(a[5]));
+    const at::Tensor* gamma = channels(a[1], "gamma", x, d.D);
+    const at::Tensor* beta = channels(a[2], "beta", x, d.D);
+    const at::Tensor* residual = optional(a[3], "residual");
+    if (residual) same(*residual, "residual", x.sizes(), x.scalar_type(), x.device());
+    at::Tensor y = at::empty(x.sizes(), x.options()), total, mean, rstd;
+    if (residual) total = at::empty(x.sizes(), x.options());
+    if (PyObject_IsTrue(a[6])) {
+        const auto rows = x.sizes().slice(0, size_t(x.dim() - 1));
+        if (!d.rms) mean = at::empty(rows, x.options().dtype(at::kFloat));
+        rstd = at::empty(rows, x.options().dtype(at::kFloat));
+    }
+    check(conv_ln_fwd(&d, x.data_ptr(), address(residual), address(gamma), address(beta), y.data_ptr(), address(total),
+                      static_cast<float*>(address(mean)), static_cast<float*>(address(rstd)), stream_of(x)),
+          "conv_ln_fwd");
+    return wrap(y, total, mean, rstd);
+}
+
+// x, dy, gamma, mean, rstd, dtotal, param_grads
+PyObject* layer_norm_bwd(PyObject* const* a)
+{
+    const at::Tensor& x = tensor(a[0], "x");
+    const at::Tensor* mean = optional(a[3], "mean");
+    const conv_ln_desc_t d = ln_desc(x, 0.0, !mean);
+    const at::Tensor& dy = same(tensor(a[1], "dy"), "dy", x.sizes(), x.scalar_type(), x.device());
+    const at::Tensor* gamma = channels(a[2], "gamma", x, d.D);
+    const auto rows = x.sizes().slice(0, size_t(x.dim() - 1));
+    if (mean) same(*mean, "mean", rows, at::kFloat, x.device());
+    const at::Tensor& rstd = same(tensor(a[4], "rstd"), "rstd", rows, at::kFloat, x.device());
+    const at::Tensor* dtotal = optional(a[5], "dtotal");
+    if (dtotal) same(*dtotal, "dtotal", x.sizes(), x.scalar_type(), x.device());
+    at::Tensor dx = at::empty(x.sizes(), x.options()), dgamma, dbeta;
+    if (PyObject_IsTrue(a[6])) {
+        dgamma = at::empty({d.D}, x.options());
+        if (mean) dbeta = at::empty({d.D}, x.options());
+    }
+    const size_t bytes = conv_ln_bwd_workspace_size(&d);
+    const at::Tensor ws = workspace(bytes, x);
+    check(conv_ln_bwd(&d, x.data_ptr(), dy.data_ptr(), address(gamma), static_cast<const float*>(address(mean)),
+                      static_cast<const float*>(rstd.data_ptr()), address(dtotal), dx.data_ptr(), address(dgamma),
+                      address(dbeta), address(ws), bytes, stream_of(x)),
+          "conv_ln_bwd");
+    return wrap(dx, dgamma, dbeta);
 }
 
 // (batch, time, channels), the channels one behind the other; the two other distances are the tensor's own.
@@ -523,6 +598,8 @@ PyMethodDef methods[] = {ENTRY("group_norm", group_norm, 8),
                          ENTRY("group_norm_bwd", group_norm_bwd, 10),
                          ENTRY("embed", embed, 4),
                          ENTRY("embed_bwd", embed_bwd, 5),
+                         ENTRY("layer_norm", layer_norm, 7),
+                         ENTRY("layer_norm_bwd", layer_norm_bwd, 7),
                          ENTRY("gated_scan", gated_scan, 7),
                          ENTRY("gated_scan_bwd", gated_scan_bwd, 10),
                          ENTRY("distill", distill, 4),

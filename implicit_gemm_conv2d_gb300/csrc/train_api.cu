@@ -45,6 +45,16 @@ int embed_check(const conv_embed_desc_t* d)
     return CONV_OK;
 }
 
+int ln_check(const conv_ln_desc_t* d)
+{
+    if (!d) return CONV_ERR_NULL;
+    if (d->N < 0 || d->D < 1 || (d->rms != 0 && d->rms != 1) || (d->dtype != CONV_F32 && d->dtype != CONV_BF16) ||
+        !std::isfinite(d->eps) || d->eps < 0.f)
+        return CONV_ERR_DESC;
+    if (d->N > kMax32 || d->D >= 1 << 30) return CONV_ERR_UNSUPPORTED;
+    return CONV_OK;
+}
+
 // The last element's offset is one that 64 bits hold in bytes.
 bool rows_near(const conv_rows_t& r, int64_t B, int64_t T, int64_t D)
 {
@@ -213,6 +223,51 @@ int conv_embed_bwd(const conv_embed_desc_t* desc, const void* idx, const void* d
     const size_t need = embed_bwd_workspace(*desc, d);
     if (need > 0 && (!workspace || workspace_bytes < need)) return CONV_ERR_WORKSPACE;
     return cuda_status(run_embed_bwd(*desc, d, idx, dy, dtable, workspace, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int conv_ln_fwd(const conv_ln_desc_t* desc, const void* x, const void* residual, const void* gamma, const void* beta,
+                void* y, void* total, float* mean, float* rstd, conv_stream_t stream)
+{
+    int rc = ln_check(desc);
+    if (rc != CONV_OK) return rc;
+    if (desc->rms && (beta || mean)) return CONV_ERR_DESC;
+    if (desc->N == 0) return CONV_OK;
+    if (!x || !y || (!residual) != (!total) || (!desc->rms && (!mean) != (!rstd))) return CONV_ERR_NULL;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(gamma) || !aligned16(beta) || !aligned16(y) ||
+        !aligned16(total) || !aligned16(mean) || !aligned16(rstd))
+        return CONV_ERR_ALIGN;
+    DevInfo d;
+    if ((rc = device_info(d)) != CONV_OK) return rc;
+    return cuda_status(run_ln_fwd(*desc, d, x, residual, gamma, beta, y, total, mean, rstd,
+                                  reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t conv_ln_bwd_workspace_size(const conv_ln_desc_t* desc)
+{
+    DevInfo d;
+    if (ln_check(desc) != CONV_OK || device_info(d) != CONV_OK) return 0;
+    return ln_bwd_workspace(*desc, d);
+}
+
+int conv_ln_bwd(const conv_ln_desc_t* desc, const void* x, const void* dy, const void* gamma, const float* mean,
+                const float* rstd, const void* dtotal, void* dx, void* dgamma, void* dbeta, void* workspace,
+                size_t workspace_bytes, conv_stream_t stream)
+{
+    int rc = ln_check(desc);
+    if (rc != CONV_OK) return rc;
+    if (desc->rms && (mean || dbeta)) return CONV_ERR_DESC;
+    if (!desc->rms && (!dgamma) != (!dbeta)) return CONV_ERR_NULL;
+    if (desc->N > 0 && (!x || !dy || !rstd || !dx || (!desc->rms && !mean))) return CONV_ERR_NULL;
+    if (!aligned16(dgamma) || !aligned16(dbeta) || !aligned16(workspace) ||
+        (desc->N > 0 && (!aligned16(x) || !aligned16(dy) || !aligned16(gamma) || !aligned16(mean) || !aligned16(rstd) ||
+                         !aligned16(dtotal) || !aligned16(dx))))
+        return CONV_ERR_ALIGN;
+    DevInfo d;
+    if ((rc = device_info(d)) != CONV_OK) return rc;
+    const size_t need = ln_bwd_workspace(*desc, d);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return CONV_ERR_WORKSPACE;
+    return cuda_status(run_ln_bwd(*desc, d, x, dy, gamma, mean, rstd, dtotal, dx, dgamma, dbeta, workspace,
+                                  reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int conv_scan_fwd(const conv_scan_desc_t* desc, const void* x, const void* gate, const float* h0, const uint8_t* reset,

@@ -164,4 +164,21 @@ cudaError_t run_distill_bwd(const conv_distill_desc_t& e, const DevInfo& d, cons
 cudaError_t run_distill_grad(const conv_distill_desc_t& e, const DevInfo& d, const void* z, const void* ids,
                              const void* teacher, const float* weight, float scale, float* loss, void* dz, cudaStream_t s);
 
+// ---- layer norm of a residual sum (kernels_ln.cu) --------------------------------------------
+struct LnParams {
+    int64_t N;
+    int D, V, vecs, NV;          // values a vector, vectors a row and a thread (0: rows that no team holds)
+    int TL, teams, R;            // threads a team, teams a block, rows a team takes at once
+    int blocks;
+    bool rms, flush;             // flush: chains of additions are cut
+    float eps, inv_d;
+};
+LnParams ln_plan(const conv_ln_desc_t& e, const DevInfo& d, bool bwd);
+cudaError_t run_ln_fwd(const conv_ln_desc_t& e, const DevInfo& d, const void* x, const void* residual, const void* gamma,
+                       const void* beta, void* y, void* total, float* mean, float* rstd, cudaStream_t s);
+size_t ln_bwd_workspace(const conv_ln_desc_t& e, const DevInfo& d);
+cudaError_t run_ln_bwd(const conv_ln_desc_t& e, const DevInfo& d, const void* x, const void* dy, const void* gamma,
+                       const float* mean, const float* rstd, const void* dtotal, void* dx, void* dgamma, void* dbeta,
+                       void* ws, cudaStream_t s);
+
 }  // namespace igc

@@ -30,6 +30,7 @@ _IDX = {torch.int32: 0, torch.int64: 1}
 
 EXPORTS = ["conv_gn_fwd_workspace_size", "conv_gn_fwd", "conv_gn_bwd_workspace_size", "conv_gn_bwd",
            "conv_embed_fwd", "conv_embed_bwd_workspace_size", "conv_embed_bwd",
+           "conv_ln_fwd", "conv_ln_bwd_workspace_size", "conv_ln_bwd",
            "conv_scan_fwd", "conv_scan_bwd", "conv_distill_fwd", "conv_distill_bwd", "conv_distill_grad",
            "conv_grad_norm_workspace_size", "conv_grad_norm", "conv_grad_clip"]
 
@@ -42,6 +43,10 @@ class GnDesc(ctypes.Structure):
 class EmbedDesc(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64)] + \
         [(n, ctypes.c_int32) for n in ("V", "D", "padding_idx", "index_dtype", "dtype")] + [("scale", ctypes.c_float)]
+
+
+class LnDesc(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in ("D", "rms", "dtype")] + [("eps", ctypes.c_float)]
 
 
 class Rows(ctypes.Structure):
@@ -84,6 +89,10 @@ def lib():
             L.conv_embed_bwd_workspace_size.argtypes = [vp]
             L.conv_embed_bwd_workspace_size.restype = sz
             L.conv_embed_bwd.argtypes = [vp] * 5 + [sz, vp]
+            L.conv_ln_fwd.argtypes = [vp] * 10
+            L.conv_ln_bwd_workspace_size.argtypes = [vp]
+            L.conv_ln_bwd_workspace_size.restype = sz
+            L.conv_ln_bwd.argtypes = [vp] * 11 + [sz, vp]
             L.conv_scan_fwd.argtypes = [vp] * 9
             L.conv_scan_bwd.argtypes = [vp] * 13
             L.conv_distill_fwd.argtypes = [vp] * 8
@@ -214,6 +223,50 @@ def embed_bwd(idx, dy, V: int, scale: float = 1.0, padding_idx: int = -1, stream
         with torch.cuda.stream(stream):
             return embed_bwd(idx, dy, V, scale, padding_idx)
     return _native().embed_bwd(idx, dy, V, scale, padding_idx)
+
+
+# ---- layer norm of a residual sum ------------------------------------------------------------
+def make_ln_desc(N, D, dtype, eps=1e-5, rms=False) -> LnDesc:
+    return LnDesc(N, D, int(rms), _DT.get(dtype, dtype), eps)
+
+
+def conv_ln_fwd(desc: LnDesc, x, residual, gamma, beta, y, total, mean, rstd, stream=None) -> None:
+    """gamma, beta, (both together) residual, total, and (both together) mean, rstd may be None; with rms
+    beta and mean are."""
+    _check(lib().conv_ln_fwd(_ref(desc), _ptr(x), _ptr(residual), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(total),
+                             _ptr(mean), _ptr(rstd), _stream(stream)), "conv_ln_fwd")
+
+
+def conv_ln_bwd_workspace_size(desc: LnDesc) -> int:
+    return lib().conv_ln_bwd_workspace_size(_ref(desc))
+
+
+def conv_ln_bwd(desc: LnDesc, x, dy, gamma, mean, rstd, dtotal, dx, dgamma, dbeta, workspace, stream=None) -> None:
+    """gamma, dtotal, and (both together) dgamma, dbeta may be None; with rms mean and dbeta are."""
+    _check(lib().conv_ln_bwd(_ref(desc), _ptr(x), _ptr(dy), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dtotal), _ptr(dx),
+                             _ptr(dgamma), _ptr(dbeta), _ptr(workspace), _bytes(workspace), _stream(stream)),
+           "conv_ln_bwd")
+
+
+def layer_norm(x, gamma=None, beta=None, residual=None, eps: float = 1e-5, rms: bool = False, stats: bool = True,
+               stream=None):
+    """y, total, mean, rstd of the rows (..., D) of x + residual: total is the sum (None without a residual),
+    y its norm times gamma plus beta.  rms: the form without a mean (then beta and mean are None).  mean
+    and rstd (fp32) are what the backward takes, None with stats=False."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return layer_norm(x, gamma, beta, residual, eps, rms, stats)
+    return _native().layer_norm(x, gamma, beta, residual, eps, rms, stats)
+
+
+def layer_norm_bwd(x, dy, gamma, mean, rstd, dtotal=None, param_grads: bool = True, stream=None):
+    """dx, dgamma, dbeta from the forward's total (x without a residual) and stats; dx is the gradient of x
+    and of residual.  mean None: the form without a mean (dbeta is None).  dtotal: the gradient that
+    reached total beside the norm.  param_grads False: dgamma and dbeta are None."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return layer_norm_bwd(x, dy, gamma, mean, rstd, dtotal, param_grads)
+    return _native().layer_norm_bwd(x, dy, gamma, mean, rstd, dtotal, param_grads)
 
 
 # ---- gated scan over time --------------------------------------------------------------------

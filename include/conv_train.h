@@ -98,6 +98,41 @@ size_t conv_embed_bwd_workspace_size(const conv_embed_desc_t* desc);
 int conv_embed_bwd(const conv_embed_desc_t* desc, const void* idx, const void* dy, void* dtable, void* workspace,
                    size_t workspace_bytes, conv_stream_t stream);
 
+/* ---- layer norm of a residual sum -----------------------------------------------------------
+ * For each of N rows of D values:
+ *
+ *   total = x + residual (rounded to the dtype; without a residual total is x)
+ *   mean = sum total / D      rstd = 1 / sqrt(sum (total - mean)^2 / D + eps)
+ *   xhat = (total - mean) * rstd      y = xhat * gamma + beta
+ *   dx = rstd * (e - m1 - xhat * m2) + dtotal      e = dy * gamma, m1 = sum e / D, m2 = sum e * xhat / D
+ *   dgamma = sum over the rows of dy * xhat        dbeta = sum over the rows of dy
+ *
+ * dx is the gradient of x and of residual; dtotal is the gradient that reaches total by another way (a
+ * residual stream goes on beside its norm), or NULL (0).  rms: the form without a mean: mean, m1
+ * and beta are 0, and mean, beta and dbeta NULL.
+ * All arrays dense, (N, D) or (D), of the descriptor's dtype; mean and rstd fp32, (N).  A row with an
+ * infinity or NaN is NaN, and so are dgamma and dbeta with it; the other rows are not. */
+typedef struct {
+    int64_t N;              /* rows, >= 0                                                 */
+    int32_t D;              /* values a row, >= 1                                         */
+    int32_t rms;            /* 0 or 1                                                     */
+    int32_t dtype;          /* conv_dtype_t                                               */
+    float eps;              /* finite, >= 0                                               */
+} conv_ln_desc_t;
+
+/* gamma, beta: NULL counts as 1 and 0.  total: written, if and only if there is a residual.  mean and
+ * rstd: written, or NULL (an inference call; with rms: rstd).  y may be x or residual, total the other.
+ * Limits: N < 2^31, D < 2^30 (CONV_ERR_UNSUPPORTED beyond).  N = 0 does nothing. */
+int conv_ln_fwd(const conv_ln_desc_t* desc, const void* x, const void* residual, const void* gamma, const void* beta,
+                void* y, void* total, float* mean, float* rstd, conv_stream_t stream);
+
+/* x: the forward's total.  dx may be dy or dtotal.  dgamma, dbeta: written, or both NULL (rms: dgamma, or
+ * NULL).  N = 0 writes zeros to them. */
+size_t conv_ln_bwd_workspace_size(const conv_ln_desc_t* desc);
+int conv_ln_bwd(const conv_ln_desc_t* desc, const void* x, const void* dy, const void* gamma, const float* mean,
+                const float* rstd, const void* dtotal, void* dx, void* dgamma, void* dbeta, void* workspace,
+                size_t workspace_bytes, conv_stream_t stream);
+
 /* ---- gated scan over time --------------------------------------------------------------------
  * For each row b of a batch and each channel, over the steps t = 0 .. T-1:
  *

@@ -118,3 +118,56 @@ def distill_bwd(z, ids, teacher, m, log, weight, scale, tau, blog=0.0):
         np.add.at(bt, (rows, ids[rows, k]), p[rows, k] * (x[rows, k] + ids.shape[1] / 8 + 20) * U)
     dz = np.where(c != 0, c * (P - t), 0.0)
     return dz, np.where(c != 0, np.abs(c) * (P * relP + bt + 1.2e-38) + 4 * U * np.abs(dz), 0.0)
+
+
+def ln_stats(x, eps, rms):
+    mean = np.zeros(x.shape[0]) if rms else x.mean(axis=1)
+    return mean, 1.0 / np.sqrt(((x - mean[:, None]) ** 2).mean(axis=1) + eps)
+
+
+def ln_fwd(x, gamma, beta, eps, rms):
+    """(y, bound), (mean, bound), (rstd, bound) of x, the sum as it is kept.
+
+    A row's sums are trees over chains of at most 64 + D / 1024 values: n U of the sum of magnitudes.  The mean's
+    error is common to the row's deviations, and adds its square to their mean square."""
+    D = x.shape[1]
+    n = (72 + D / 512) * U
+    mean, rstd = ln_stats(x, eps, rms)
+    em = np.zeros_like(mean) if rms else (n + 2 * U) * np.abs(x).mean(axis=1) + U * np.abs(mean)
+    d = x - mean[:, None]
+    ed = em[:, None] + U * (np.abs(x) + np.abs(mean)[:, None])
+    var = (d * d).mean(axis=1)
+    ev = (2 * np.abs(d) * ed + ed * ed).mean(axis=1) + n * var
+    er = rstd * (0.51 * ev * rstd * rstd + 3 * U)
+    xh = d * rstd[:, None]
+    exh = ed * rstd[:, None] + np.abs(d) * er[:, None] + 2 * U * np.abs(xh)
+    ga = np.ones(D) if gamma is None else gamma
+    be = np.zeros(D) if beta is None else beta
+    y = xh * ga + be
+    return (y, exh * np.abs(ga) + U * (np.abs(xh * ga) + np.abs(y))), (mean, em), (rstd, er)
+
+
+def ln_bwd(x, dy, gamma, mean, rstd, dtotal, rms):
+    """(dx, bound), (dgamma, bound), (dbeta, bound), from the statistics as they are kept."""
+    N, D = x.shape
+    n = (72 + D / 512) * U
+    m, r = np.zeros((N, 1)) if rms else mean[:, None], rstd[:, None]
+    ga = np.ones(D) if gamma is None else gamma
+    xh = (x - m) * r
+    exh = (np.abs(x) + np.abs(m)) * r * 3 * U
+    e = dy * ga
+    ee = U * np.abs(e)
+    m1 = np.zeros((N, 1)) if rms else e.mean(axis=1, keepdims=True)
+    em1 = np.zeros((N, 1)) if rms else (n + 2 * U) * np.abs(e).mean(axis=1, keepdims=True)
+    m2 = (e * xh).mean(axis=1, keepdims=True)
+    em2 = (np.abs(e) * exh + (n + 4 * U) * np.abs(e * xh)).mean(axis=1, keepdims=True)
+    inner = e - m1 - xh * m2
+    t = np.zeros_like(x) if dtotal is None else dtotal
+    dx = r * inner + t
+    edx = r * (ee + em1 + np.abs(xh) * em2 + exh * np.abs(m2) + 3 * U * (np.abs(e) + np.abs(m1) + np.abs(xh * m2))) \
+        + 2 * U * (np.abs(r * inner) + np.abs(dx))
+    # the rows' sums: chains of 256, of their sums, and of the blocks'
+    c = (256 + 64 + N / 65536 + 40) * U
+    dg, db = (dy * xh).sum(axis=0), dy.sum(axis=0)
+    return (dx, edx), (dg, (np.abs(dy) * exh).sum(axis=0) + c * np.abs(dy * xh).sum(axis=0)), \
+        (db, c * np.abs(dy).sum(axis=0))
