@@ -23,11 +23,12 @@ constexpr int LN_MOST = 1024;    // threads of a team, forward
 constexpr int LN_MOST_BWD = 512; // backward: 128 registers a thread
 constexpr int LN_FLUSH = 256;    // rows that are added to each other in one chain
 
-// Rows a team of the backward takes at once: what a thread's registers hold of x, dy and dtotal, 48 of them.
+// Rows a team of the backward takes at once: what a thread's registers hold of x, dy and dtotal, 48 of them, beside
+// its columns' sums.
 constexpr int ln_rows(int es, int V, int NV)
 {
     const int regs = 3 * NV * (es == 2 && V > 1 ? V / 2 : V);
-    return regs <= 12 ? 4 : regs <= 24 ? 2 : 1;
+    return regs <= 12 ? 4 : NV * V <= 8 ? 2 : 1;
 }
 
 // A thread's place: teams of TL threads, each a row at a time.
@@ -220,6 +221,13 @@ ln_fwd_long(const __grid_constant__ LnParams p, const T* x, const T* residual, c
     }
 }
 
+// Columns c and c + 1 of a thread's NV vectors; a single column has a second one of 0.
+template <typename T, int V, int NV> __device__ __forceinline__ float2 pick(const Vec<T, V> (&a)[NV], int c)
+{
+    if constexpr (V * NV == 1) return make_float2(a[0].get(0), 0.f);
+    else return make_float2(a[c / V].get(c % V), a[(c + 1) / V].get((c + 1) % V));
+}
+
 // R rows a team at a time.  part: [block][dgamma, dbeta][D], or NULL.
 template <typename T, int V, int NV, int R>
 __global__ void __launch_bounds__(LN_MOST_BWD)
@@ -228,31 +236,34 @@ ln_bwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* dy, const
 {
     extern __shared__ __align__(16) float dyn[];  // [2 NV V][threads]: what the chains of additions have left so far
     __shared__ float sm[2][32 * 2 * R];
+    constexpr int CPT = NV * V, P = (CPT + 1) / 2;
     const LnAt q(p);
     tc::grid_dep_wait();
     tc::grid_dep_launch();
-    float dg[NV][V], db[NV][V];
+    float2 dg[P], db[P];
     Vec<T, V> g[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int j = q.lane + i * q.TL;
-        g[i].zero();
-        if (gamma && j < p.vecs) g[i].load(gamma + j * V);
+        float one[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) dg[i][v] = db[i][v] = 0.f;
+        for (int v = 0; v < V; ++v) one[v] = 1.f;
+        g[i].set(one);
+        if (gamma && j < p.vecs) g[i].load(gamma + j * V);
     }
+#pragma unroll
+    for (int c = 0; c < P; ++c) dg[c] = db[c] = both(0.f);
+    const int slot = 2 * int(blockDim.x);
     if (p.flush)
-        for (int k = 0; k < 2 * NV * V; ++k) dyn[k * blockDim.x + threadIdx.x] = 0.f;
+        for (int k = 0; k < 2 * P; ++k) reinterpret_cast<float2*>(dyn)[k * int(blockDim.x) + int(threadIdx.x)] = both(0.f);
     auto flush = [&] {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float* a = dyn + (i * V + v) * 2 * int(blockDim.x) + threadIdx.x;
-                a[0] += dg[i][v];
-                a[blockDim.x] += db[i][v];
-                dg[i][v] = db[i][v] = 0.f;
-            }
+        for (int c = 0; c < P; ++c) {
+            float2* a = reinterpret_cast<float2*>(dyn) + c * slot + threadIdx.x;
+            a[0] = add2(a[0], dg[c]);
+            a[blockDim.x] = add2(a[blockDim.x], db[c]);
+            dg[c] = db[c] = both(0.f);
+        }
     };
     const int64_t stride = int64_t(gridDim.x) * q.teams * R;
     int turn = 0, chain = 0;
@@ -270,56 +281,52 @@ ln_bwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* dy, const
                 const int j = q.lane + i * q.TL;
                 const int64_t at = (row + k) * p.D + int64_t(j) * V;
                 a[k][i].zero();
-                d[k][i].zero();
+                d[k][i].zero();  // (dy of 0: a place that is not there adds nothing)
                 t[k][i].zero();
                 if (on && j < p.vecs) {
                     a[k][i].load(x + at);
                     d[k][i].load(dy + at);
                     if (dtotal) t[k][i].load(dtotal + at);
-                } else {
-                    // (a place that is not there has xhat = 0)
-                    float z[V];
-#pragma unroll
-                    for (int v = 0; v < V; ++v) z[v] = 0.f;
-                    a[k][i].set(z);
                 }
             }
         }
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            float s1 = 0.f, s2 = 0.f;
+            float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float xh = (a[k][i].get(v) - m[k]) * r[k], y = d[k][i].get(v);
-                    const float e = gamma ? y * g[i].get(v) : y;
-                    s1 += e;
-                    s2 += e * xh;
-                    dg[i][v] += y * xh;
-                    db[i][v] += y;
-                }
-            sums[2 * k] = s1;
-            sums[2 * k + 1] = s2;
+            for (int c = 0; c < P; ++c) {
+                const float2 xh = mul2(add2(pick(a[k], 2 * c), both(-m[k])), both(r[k])), y = pick(d[k], 2 * c);
+                const float2 e = mul2(y, pick(g, 2 * c));
+                s1 = add2(s1, e);
+                s2 = fma2(e, xh, s2);
+                dg[c] = fma2(y, xh, dg[c]);
+                db[c] = add2(db[c], y);
+            }
+            sums[2 * k] = s1.x + s1.y;
+            sums[2 * k + 1] = s2.x + s2.y;
         }
         ln_sum(q, sums, sm[turn]);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const bool on = row + k < p.N;
+            if (row + k >= p.N) continue;
             const float m1 = p.rms ? 0.f : sums[2 * k] * p.inv_d, m2 = sums[2 * k + 1] * p.inv_d;
+            float o[2 * P];
+#pragma unroll
+            for (int c = 0; c < P; ++c) {
+                const float2 xh = mul2(add2(pick(a[k], 2 * c), both(-m[k])), both(r[k]));
+                const float2 e = mul2(pick(d[k], 2 * c), pick(g, 2 * c));
+                const float2 v = fma2(both(r[k]), fma2(xh, both(-m2), add2(e, both(-m1))), pick(t[k], 2 * c));
+                o[2 * c] = v.x;
+                o[2 * c + 1] = v.y;
+            }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int j = q.lane + i * q.TL;
-                if (!on || j >= p.vecs) continue;
-                float o[V];
+                float f[V];
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float xh = (a[k][i].get(v) - m[k]) * r[k], y = d[k][i].get(v);
-                    const float e = gamma ? y * g[i].get(v) : y;
-                    o[v] = fmaf(r[k], e - m1 - xh * m2, t[k][i].get(v));
-                }
-                a[k][i].set(o);
-                a[k][i].store(dx + (row + k) * p.D + int64_t(j) * V);
+                for (int v = 0; v < V; ++v) f[v] = o[i * V + v];
+                a[k][i].set(f);
+                if (j < p.vecs) a[k][i].store(dx + (row + k) * p.D + int64_t(j) * V);
             }
         }
         chain += R;
@@ -332,46 +339,32 @@ ln_bwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* dy, const
     if (p.flush) {
         flush();
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float* a = dyn + (i * V + v) * 2 * int(blockDim.x) + threadIdx.x;
-                dg[i][v] = a[0];
-                db[i][v] = a[blockDim.x];
-            }
+        for (int c = 0; c < P; ++c) {
+            const float2* a = reinterpret_cast<const float2*>(dyn) + c * slot + threadIdx.x;
+            dg[c] = a[0];
+            db[c] = a[blockDim.x];
+        }
+        __syncthreads();
     }
     float* to = part + int64_t(blockIdx.x) * 2 * p.D;
-    if (q.teams == 1) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int j = q.lane + i * q.TL;
-            if (j >= p.vecs) continue;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                to[j * V + v] = dg[i][v];
-                to[p.D + j * V + v] = db[i][v];
-            }
-        }
-        return;
-    }
-    // Teams of a warp and less: over the warp's teams by shuffles, over the warps in shared memory.
-    if (p.flush) __syncthreads();
     const int warp = int(threadIdx.x) >> 5, warps = int(blockDim.x) >> 5;
+    // Teams of a warp and less: over the warp's teams by shuffles, over the warps in shared memory.
+    float* at = q.teams > 1 ? dyn + warp * 2 * p.D : to;
+    const bool writes = q.teams == 1 || (threadIdx.x & 31) < unsigned(q.TL);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int j = q.lane + i * q.TL;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            for (int o = q.TL; o < 32; o *= 2) {
-                dg[i][v] += __shfl_xor_sync(0xFFFFFFFFu, dg[i][v], o);
-                db[i][v] += __shfl_xor_sync(0xFFFFFFFFu, db[i][v], o);
-            }
-            if ((threadIdx.x & 31) < unsigned(q.TL) && j < p.vecs) {
-                dyn[warp * 2 * p.D + j * V + v] = dg[i][v];
-                dyn[warp * 2 * p.D + p.D + j * V + v] = db[i][v];
-            }
+    for (int c = 0; c < CPT; ++c) {
+        float u = c & 1 ? dg[c / 2].y : dg[c / 2].x, w = c & 1 ? db[c / 2].y : db[c / 2].x;
+        const int j = q.lane + c / V * q.TL;
+        for (int o = q.TL; o < 32; o *= 2) {
+            u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
+            w += __shfl_xor_sync(0xFFFFFFFFu, w, o);
+        }
+        if (writes && j < p.vecs) {
+            at[j * V + c % V] = u;
+            at[p.D + j * V + c % V] = w;
         }
     }
+    if (q.teams == 1) return;
     __syncthreads();
     for (int c = int(threadIdx.x); c < 2 * p.D; c += int(blockDim.x)) {
         float s = 0.f;
@@ -517,11 +510,11 @@ LnParams ln_plan(const conv_ln_desc_t& e, const DevInfo& d, bool bwd)
     p.V = e.D % ve == 0 ? ve : e.D % 2 == 0 ? 2 : 1;
     p.vecs = e.D / p.V;
     const int64_t room = int64_t(d.sms) * 2048;  // threads
-    const int most_nv = bwd ? std::min(8, 16 / p.V) : 8;
-    // Vectors of a thread: in the backward as few as a team of 512 can do with (a thread keeps two sums a column), in
+    const int most_nv = bwd ? 16 / p.V : 8;
+    // Vectors of a thread: in the backward as few as a team of 256 can do with (a thread keeps two sums a column), in
     // the forward as many as 4, by which a row of a warp needs no barrier.
     int nv = 1;
-    while (nv < most_nv && (bwd ? p.vecs > nv * 128 : nv < 4 ? p.vecs > nv * 32 : p.vecs > nv * 256)) nv *= 2;
+    while (nv < most_nv && (bwd ? p.vecs > nv * 256 : nv < 4 ? p.vecs > nv * 32 : p.vecs > nv * 256)) nv *= 2;
     p.NV = nv;
     const int need = (p.vecs + nv - 1) / nv;
     if (need > (bwd ? LN_MOST_BWD : LN_MOST)) {
@@ -542,8 +535,9 @@ LnParams ln_plan(const conv_ln_desc_t& e, const DevInfo& d, bool bwd)
     p.R = bwd ? ln_rows(es, p.V, p.NV) : 1;
     const int threads = p.TL * p.teams;
     const int64_t blocks = (e.N + int64_t(p.teams) * p.R - 1) / (int64_t(p.teams) * p.R);
-    // The forward: as many blocks as the SMs hold threads for.  The backward: half of that, 128 registers a thread.
-    p.blocks = int(std::max<int64_t>(1, std::min(blocks, room / threads / (bwd ? 4 : 1))));
+    // The forward: as many blocks as the SMs hold threads for.  The backward: as its registers allow, 128 a thread or 64.
+    const int per_sm = std::max(1, (p.NV * p.V * p.R <= 8 ? 1024 : 512) / threads);
+    p.blocks = int(std::max<int64_t>(1, std::min(blocks, bwd ? int64_t(d.sms) * per_sm : room / threads)));
     if (bwd) p.flush = e.N > int64_t(p.blocks) * p.teams * LN_FLUSH;
     return p;
 }
@@ -553,7 +547,7 @@ namespace {
 int ln_smem(const LnParams& p)
 {
     const int threads = p.TL * p.teams;
-    return std::max(p.flush ? 2 * p.NV * p.V * threads * 4 : 0, p.teams > 1 ? threads / 32 * 2 * p.D * 4 : 0);
+    return std::max(p.flush ? 2 * (p.NV * p.V + 1) / 2 * 2 * threads * 4 : 0, p.teams > 1 ? threads / 32 * 2 * p.D * 4 : 0);
 }
 
 // The blocks of columns and rows of a long row's second kernel.
@@ -626,7 +620,8 @@ cudaError_t run_ln_bwd(const conv_ln_desc_t& e, const DevInfo& d, const void* x,
             err = p.NV == 1   ? go(Int<1>())
                   : p.NV == 2 ? go(Int<2>())
                   : p.NV == 4 ? go(Int<4>())
-                              : go(Int<8>());
+                  : p.NV == 8 ? go(Int<8>())
+                              : go(Int<16>());
         } else if (e.N > 0) {
             float2* sums = static_cast<float2*>(ws);
             part += (size_t(e.N) * 8 + 15) / 16 * 4;
