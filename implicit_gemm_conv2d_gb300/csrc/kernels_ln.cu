@@ -4,10 +4,14 @@
 //   dgamma = sum over the rows of dy xhat      dbeta = sum over the rows of dy
 // (the form without a mean: mean, m1 and beta are 0).
 //
-// Bound by memory: a row is read once and held in the registers of a team, from a few lanes to 32
+// Bound by memory: a row is read once and held in the registers of a team, from one thread to 16
 // warps; mean and squared deviations are two passes over the registers.  Blocks stay and take rows in turn.  In
 // the backward a thread keeps its columns' sums of dgamma and dbeta over all rows of its team, the
 // block's go to the workspace and a second kernel adds those: an order that the sizes fix.
+// Where D is no multiple of 16 bytes, rows begin anywhere, but every VE-th row (VE values are 16 bytes)
+// alike: a team's rows are a multiple of VE apart, so that it reads them all by the same whole vectors of memory
+// and a thread's columns stay its own.  The first and the last vector hold values of the rows beside it,
+// which are cut off as they come in and never written.
 // Rows that no team holds are read again for each pass.
 #include <algorithm>
 
@@ -19,21 +23,19 @@ namespace igc {
 
 namespace {
 
-constexpr int LN_MOST = 1024;    // threads of a team, forward
-constexpr int LN_MOST_BWD = 512; // backward: 128 registers a thread
+constexpr int LN_MOST = 512;     // threads of a team
+constexpr int LN_LONG = 1024;    // threads a row that no team holds
 constexpr int LN_FLUSH = 256;    // rows that are added to each other in one chain
 
-// Rows a team of the backward takes at once: what a thread's registers hold of x, dy and dtotal, 48 of them, beside
-// its columns' sums.
-constexpr int ln_rows(int es, int V, int NV)
-{
-    const int regs = 3 * NV * (es == 2 && V > 1 ? V / 2 : V);
-    return regs <= 12 ? 4 : NV * V <= 8 ? 2 : 1;
-}
+template <typename T> constexpr int ln_ve() { return 16 / int(sizeof(T)); }
 
-// A thread's place: teams of TL threads, each a row at a time.
+// Rows a team of the backward takes at once: as its registers allow.
+constexpr int ln_rows(int es, int NV, bool edge) { return NV * 16 / es > 8 ? 1 : es == 2 && !edge ? 4 : 2; }
+
+// A thread's place: teams of TL threads, each a row at a time, `rows` apart.
 struct LnAt {
     int lane, team, TL, teams, warps;  // warps of a team of more than one, else 1
+    int64_t first, rows;               // the team's first row; rows to its next
     __device__ __forceinline__ explicit LnAt(const LnParams& p)
     {
         TL = p.TL;
@@ -41,6 +43,94 @@ struct LnAt {
         lane = teams > 1 ? int(threadIdx.x) & (TL - 1) : int(threadIdx.x);
         team = teams > 1 ? int(threadIdx.x) / TL : 0;
         warps = TL > 32 ? TL / 32 : 1;
+        first = int64_t(blockIdx.x) * teams + team;
+        rows = int64_t(gridDim.x) * teams;
+    }
+};
+
+// A thread's NV vectors of its team's rows.  EDGE: rows do not all begin at 16 bytes; a vector's values that
+// belong to the row are the bits of `have`.
+template <typename T, int NV, bool EDGE> struct LnRow {
+    static constexpr int VE = ln_ve<T>(), FULL = (1 << VE) - 1;
+    using Vector = Vec<T, VE>;
+    int off;         // elements of vector 0 that belong to the row before
+    uint32_t have[EDGE ? NV : 1];
+    int lane, TL, vecs;
+    int64_t end;     // elements of the array
+    __device__ __forceinline__ LnRow(const LnParams& p, const LnAt& q) : lane(q.lane), TL(q.TL), end(p.N * p.D)
+    {
+        off = EDGE ? int(uint64_t(q.first) * uint64_t(p.D) % VE) : 0;
+        vecs = (off + p.D + VE - 1) / VE;
+        if constexpr (EDGE) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int at = (lane + i * TL) * VE - off;  // the vector's first column
+                const int lo = max(0, -at), hi = min(VE, p.D - at);
+                have[i] = hi > lo ? ((1u << hi) - 1u) & ~((1u << lo) - 1u) : 0u;
+            }
+        }
+    }
+    __device__ __forceinline__ bool in(int i) const { return EDGE ? have[EDGE ? i : 0] != 0 : lane + i * TL < vecs; }
+    __device__ __forceinline__ bool whole(int i) const { return !EDGE || have[EDGE ? i : 0] == FULL; }
+    __device__ __forceinline__ bool has(int i, int v) const { return !EDGE || (have[EDGE ? i : 0] >> v & 1u); }
+    __device__ __forceinline__ int column(int i) const { return (lane + i * TL) * VE - off; }
+    // Element of the array that vector i of a row begins with.
+    __device__ __forceinline__ int64_t at(int64_t row, int D, int i) const
+    {
+        return row * D - off + int64_t(lane + i * TL) * VE;
+    }
+    // Vector i with what lies beside the row in it; cut() makes that 0, once all loads are on their way.
+    __device__ __forceinline__ void load(Vector& r, const T* a, int64_t at, int i) const
+    {
+        if (whole(i) || at + VE <= end) {
+            r.load(a + at);
+        } else {  // the array's last vector
+            float f[VE];
+#pragma unroll
+            for (int v = 0; v < VE; ++v) f[v] = has(i, v) ? Elem<T>::ld(a + at + v) : 0.f;
+            r.set(f);
+        }
+    }
+    __device__ __forceinline__ void cut(Vector (&a)[NV]) const
+    {
+        if constexpr (EDGE) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (whole(i)) continue;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if constexpr (sizeof(T) == 4) a[i].r.w[k] = has(i, k) ? a[i].r.w[k] : 0u;
+                    else a[i].r.w[k] &= (has(i, 2 * k) ? 0xFFFFu : 0u) | (has(i, 2 * k + 1) ? 0xFFFF0000u : 0u);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void store(T* a, int64_t at, int i, const Vector& r) const
+    {
+        if (whole(i)) {
+            r.store(a + at);
+        } else {
+#pragma unroll
+            for (int v = 0; v < VE; ++v)
+                if (has(i, v)) Elem<T>::st(a + at + v, r.get(v));
+        }
+    }
+    // A parameter of the thread's columns, `other` where there is none.
+    __device__ __forceinline__ void params(Vector& r, const T* a, int i, float other) const
+    {
+        float f[VE];
+#pragma unroll
+        for (int v = 0; v < VE; ++v) f[v] = other;
+        r.set(f);
+        if (!a || !in(i)) return;
+        if constexpr (!EDGE) {
+            r.load(a + column(i));
+        } else {
+#pragma unroll
+            for (int v = 0; v < VE; ++v)
+                if (has(i, v)) f[v] = Elem<T>::ld(a + column(i) + v);
+            r.set(f);
+        }
     }
 };
 
@@ -68,49 +158,68 @@ template <int K> __device__ __forceinline__ void ln_sum(const LnAt& q, float (&v
         for (int k = 0; k < K; ++k) v[k] += sm[w * K + k];
 }
 
-template <typename T, int V, int NV>
-__global__ void __launch_bounds__(LN_MOST)
+template <typename T, int NV, bool EDGE>
+__global__ void __launch_bounds__(LN_MOST, 2)
 ln_fwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* residual, const T* gamma, const T* beta, T* y,
               T* total, float* mean, float* rstd)
 {
     __shared__ float sm[2][32];
+    constexpr int VE = ln_ve<T>();
+    using Vector = Vec<T, VE>;
     const LnAt q(p);
+    const LnRow<T, NV, EDGE> w(p, q);
     tc::grid_dep_wait();
     tc::grid_dep_launch();
-    for (int64_t row0 = int64_t(blockIdx.x) * q.teams; row0 < p.N; row0 += int64_t(gridDim.x) * q.teams) {
-        const int64_t row = row0 + q.team, at = row * p.D;
+    // Whole vectors of gamma and beta are read again for each row, from L1; where rows begin anywhere, from copies in
+    // shared memory that begin as the rows of the block's team, or of its VE-th team each, do.
+    extern __shared__ __align__(16) uint8_t columns[];
+    const int wide = (p.D + 2 * VE - 1) / VE * VE, copies = EDGE ? min(q.teams, VE) : 0;
+    T* const mine = reinterpret_cast<T*>(columns) + (q.team % VE) * 2 * wide;
+    if constexpr (EDGE) {
+        for (int k = int(threadIdx.x); k < copies * wide; k += int(blockDim.x)) {
+            const int copy = k / wide, e = k % wide;
+            const int c = e - int(uint64_t(int64_t(blockIdx.x) * q.teams + copy) * uint64_t(p.D) % VE);
+            T* to = reinterpret_cast<T*>(columns) + copy * 2 * wide + e;
+            const bool there = c >= 0 && c < p.D;
+            Elem<T>::st(to, there ? (gamma ? Elem<T>::ld(gamma + c) : 1.f) : 0.f);
+            Elem<T>::st(to + wide, there && beta ? Elem<T>::ld(beta + c) : 0.f);
+        }
+        __syncthreads();
+    }
+    for (int64_t row = q.first; row - q.team < p.N; row += q.rows) {
         const bool on = row < p.N;
-        Vec<T, V> a[NV];
-        float f[NV][V];
+        Vector a[NV];
+        float f[NV][VE];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int j = q.lane + i * q.TL;
             a[i].zero();
-            if (on && j < p.vecs) a[i].load(x + at + int64_t(j) * V);
+            if (on && w.in(i)) w.load(a[i], x, w.at(row, p.D, i), i);
         }
         if (residual) {
-            Vec<T, V> r[NV];
+            Vector r[NV];
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int j = q.lane + i * q.TL;
                 r[i].zero();
-                if (on && j < p.vecs) r[i].load(residual + at + int64_t(j) * V);
+                if (on && w.in(i)) w.load(r[i], residual, w.at(row, p.D, i), i);
             }
+            w.cut(a);
+            w.cut(r);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int j = q.lane + i * q.TL;
-                float s[V];
+                float s[VE];
 #pragma unroll
-                for (int v = 0; v < V; ++v) s[v] = a[i].get(v) + r[i].get(v);
+                for (int v = 0; v < VE; ++v) s[v] = a[i].get(v) + r[i].get(v);
                 a[i].set(s);
-                if (on && j < p.vecs) a[i].store(total + at + int64_t(j) * V);
+                if (on && w.in(i)) w.store(total, w.at(row, p.D, i), i, a[i]);
             }
+        } else {
+            w.cut(a);
         }
         float sum[1] = {0.f};
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
+            for (int v = 0; v < VE; ++v) {
                 f[i][v] = a[i].get(v);
                 sum[0] += f[i][v];
             }
@@ -122,11 +231,16 @@ ln_fwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* residual,
         float sq[1] = {0.f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const bool in = q.lane + i * q.TL < p.vecs;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                f[i][v] -= m;
-                if (in) sq[0] += f[i][v] * f[i][v];
+            for (int v = 0; v < VE; ++v) f[i][v] -= m;
+            if (!w.in(i)) continue;
+            if (w.whole(i)) {
+#pragma unroll
+                for (int v = 0; v < VE; ++v) sq[0] += f[i][v] * f[i][v];
+            } else {
+#pragma unroll
+                for (int v = 0; v < VE; ++v)
+                    if (w.has(i, v)) sq[0] += f[i][v] * f[i][v];
             }
         }
         if (p.rms && q.warps > 1) __syncthreads();  // the sums of the row before have been read
@@ -134,19 +248,21 @@ ln_fwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* residual,
         const float r = __frsqrt_rn(sq[0] * p.inv_d + p.eps);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int j = q.lane + i * q.TL;
-            if (!on || j >= p.vecs) continue;
-            Vec<T, V> g, b, o;
-            if (gamma) g.load(gamma + j * V);
-            if (beta) b.load(beta + j * V);
-            float out[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float h = f[i][v] * r;
-                out[v] = fmaf(h, gamma ? g.get(v) : 1.f, beta ? b.get(v) : 0.f);
+            if (!on || !w.in(i)) continue;
+            Vector gi, bi, o;
+            if constexpr (EDGE) {
+                gi.load(mine + (q.lane + i * q.TL) * VE);
+                bi.load(mine + wide + (q.lane + i * q.TL) * VE);
+            } else {
+                if (gamma) gi.load(gamma + w.column(i));
+                if (beta) bi.load(beta + w.column(i));
             }
+            float out[VE];
+#pragma unroll
+            for (int v = 0; v < VE; ++v)
+                out[v] = fmaf(f[i][v] * r, EDGE || gamma ? gi.get(v) : 1.f, EDGE || beta ? bi.get(v) : 0.f);
             o.set(out);
-            o.store(y + at + int64_t(j) * V);
+            w.store(y, w.at(row, p.D, i), i, o);
         }
         if (on && q.lane == 0) {
             if (mean) mean[row] = m;
@@ -157,7 +273,7 @@ ln_fwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* residual,
 
 // A block a row, of any length: the row is read again for each pass.
 template <typename T, int V>
-__global__ void __launch_bounds__(LN_MOST)
+__global__ void __launch_bounds__(LN_LONG)
 ln_fwd_long(const __grid_constant__ LnParams p, const T* x, const T* residual, const T* gamma, const T* beta, T* y,
             T* total, float* mean, float* rstd)
 {
@@ -221,36 +337,30 @@ ln_fwd_long(const __grid_constant__ LnParams p, const T* x, const T* residual, c
     }
 }
 
-// Columns c and c + 1 of a thread's NV vectors; a single column has a second one of 0.
-template <typename T, int V, int NV> __device__ __forceinline__ float2 pick(const Vec<T, V> (&a)[NV], int c)
+// Columns c and c + 1 of a thread's vectors, c even.
+template <typename T, int VE, int NV> __device__ __forceinline__ float2 pick(const Vec<T, VE> (&a)[NV], int c)
 {
-    if constexpr (V * NV == 1) return make_float2(a[0].get(0), 0.f);
-    else return make_float2(a[c / V].get(c % V), a[(c + 1) / V].get((c + 1) % V));
+    return make_float2(a[c / VE].get(c % VE), a[c / VE].get(c % VE + 1));
 }
 
-// R rows a team at a time.  part: [block][dgamma, dbeta][D], or NULL.
-template <typename T, int V, int NV, int R>
-__global__ void __launch_bounds__(LN_MOST_BWD)
+// R rows of a team at a time: neighbours, where rows begin at 16 bytes.  part: [block][dgamma, dbeta][D], or NULL.
+template <typename T, int NV, int R, bool EDGE>
+__global__ void __launch_bounds__(LN_MOST)
 ln_bwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* dy, const T* gamma, const float* mean,
               const float* rstd, const T* dtotal, T* dx, float* part)
 {
-    extern __shared__ __align__(16) float dyn[];  // [2 NV V][threads]: what the chains of additions have left so far
+    extern __shared__ __align__(16) float dyn[];  // [2 P][threads] pairs: what the chains of additions have left so far
     __shared__ float sm[2][32 * 2 * R];
-    constexpr int CPT = NV * V, P = (CPT + 1) / 2;
+    constexpr int VE = ln_ve<T>(), CPT = NV * VE, P = CPT / 2;
+    using Vector = Vec<T, VE>;
     const LnAt q(p);
+    const LnRow<T, NV, EDGE> w(p, q);
     tc::grid_dep_wait();
     tc::grid_dep_launch();
     float2 dg[P], db[P];
-    Vec<T, V> g[NV];
+    Vector g[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int j = q.lane + i * q.TL;
-        float one[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) one[v] = 1.f;
-        g[i].set(one);
-        if (gamma && j < p.vecs) g[i].load(gamma + j * V);
-    }
+    for (int i = 0; i < NV; ++i) w.params(g[i], gamma, i, 1.f);
 #pragma unroll
     for (int c = 0; c < P; ++c) dg[c] = db[c] = both(0.f);
     const int slot = 2 * int(blockDim.x);
@@ -265,33 +375,40 @@ ln_bwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* dy, const
             dg[c] = db[c] = both(0.f);
         }
     };
-    const int64_t stride = int64_t(gridDim.x) * q.teams * R;
     int turn = 0, chain = 0;
-    for (int64_t row0 = int64_t(blockIdx.x) * q.teams * R; row0 < p.N; row0 += stride, turn ^= 1) {
-        const int64_t row = row0 + q.team * R;
-        Vec<T, V> a[R][NV], d[R][NV], t[R][NV];
+    const int64_t next = EDGE ? q.rows : 1;  // from one of the R rows to the next
+    for (int64_t row0 = EDGE ? q.first : q.first * R; row0 - (EDGE ? 1 : R) * q.team < p.N; row0 += R * q.rows, turn ^= 1) {
+        Vector a[R][NV], d[R][NV], t[R][NV];
         float m[R], r[R], sums[2 * R];
+        const int64_t at0 = w.at(row0, p.D, 0), hop = next * p.D;
+        uint32_t on = 0;  // rows that are there
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+            if (row0 + k * next < p.N) on |= 1u << k;
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const bool on = row + k < p.N;
-            m[k] = on && mean ? mean[row + k] : 0.f;
-            r[k] = on ? rstd[row + k] : 0.f;
+            m[k] = r[k] = 0.f;
+            if (on >> k & 1u) {
+                if (mean) m[k] = mean[row0 + k * next];
+                r[k] = rstd[row0 + k * next];
+            }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int j = q.lane + i * q.TL;
-                const int64_t at = (row + k) * p.D + int64_t(j) * V;
                 a[k][i].zero();
                 d[k][i].zero();  // (dy of 0: a place that is not there adds nothing)
                 t[k][i].zero();
-                if (on && j < p.vecs) {
-                    a[k][i].load(x + at);
-                    d[k][i].load(dy + at);
-                    if (dtotal) t[k][i].load(dtotal + at);
+                if ((on >> k & 1u) && w.in(i)) {
+                    const int64_t at = at0 + k * hop + i * q.TL * VE;
+                    w.load(a[k][i], x, at, i);
+                    w.load(d[k][i], dy, at, i);
+                    if (dtotal) w.load(t[k][i], dtotal, at, i);
                 }
             }
         }
 #pragma unroll
         for (int k = 0; k < R; ++k) {
+            w.cut(a[k]);
+            w.cut(d[k]);
             float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
             for (int c = 0; c < P; ++c) {
@@ -306,27 +423,31 @@ ln_bwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* dy, const
             sums[2 * k + 1] = s2.x + s2.y;
         }
         ln_sum(q, sums, sm[turn]);
+        // What is computed of x and dy is computed again below: kept from above, it spills (32768 x 1024 bf16 66 -> 55 us).
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) asm volatile("" : "+r"(a[k][i].r.w[c]), "+r"(d[k][i].r.w[c]));
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            if (row + k >= p.N) continue;
+            if (!(on >> k & 1u)) continue;
             const float m1 = p.rms ? 0.f : sums[2 * k] * p.inv_d, m2 = sums[2 * k + 1] * p.inv_d;
-            float o[2 * P];
-#pragma unroll
-            for (int c = 0; c < P; ++c) {
-                const float2 xh = mul2(add2(pick(a[k], 2 * c), both(-m[k])), both(r[k]));
-                const float2 e = mul2(pick(d[k], 2 * c), pick(g, 2 * c));
-                const float2 v = fma2(both(r[k]), fma2(xh, both(-m2), add2(e, both(-m1))), pick(t[k], 2 * c));
-                o[2 * c] = v.x;
-                o[2 * c + 1] = v.y;
-            }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int j = q.lane + i * q.TL;
-                float f[V];
+                float o[VE];
 #pragma unroll
-                for (int v = 0; v < V; ++v) f[v] = o[i * V + v];
-                a[k][i].set(f);
-                if (j < p.vecs) a[k][i].store(dx + (row + k) * p.D + int64_t(j) * V);
+                for (int v = 0; v < VE; v += 2) {
+                    const int c = i * VE + v;
+                    const float2 xh = mul2(add2(pick(a[k], c), both(-m[k])), both(r[k]));
+                    const float2 e = mul2(pick(d[k], c), pick(g, c));
+                    const float2 u = fma2(both(r[k]), fma2(xh, both(-m2), add2(e, both(-m1))), pick(t[k], c));
+                    o[v] = u.x;
+                    o[v + 1] = u.y;
+                }
+                a[k][i].set(o);
+                if (w.in(i)) w.store(dx, at0 + k * hop + i * q.TL * VE, i, a[k][i]);
             }
         }
         chain += R;
@@ -347,35 +468,45 @@ ln_bwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* dy, const
         __syncthreads();
     }
     float* to = part + int64_t(blockIdx.x) * 2 * p.D;
-    const int warp = int(threadIdx.x) >> 5, warps = int(blockDim.x) >> 5;
-    // Teams of a warp and less: over the warp's teams by shuffles, over the warps in shared memory.
-    float* at = q.teams > 1 ? dyn + warp * 2 * p.D : to;
-    const bool writes = q.teams == 1 || (threadIdx.x & 31) < unsigned(q.TL);
+    if (q.teams == 1) {
 #pragma unroll
-    for (int c = 0; c < CPT; ++c) {
-        float u = c & 1 ? dg[c / 2].y : dg[c / 2].x, w = c & 1 ? db[c / 2].y : db[c / 2].x;
-        const int j = q.lane + c / V * q.TL;
-        for (int o = q.TL; o < 32; o *= 2) {
-            u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
-            w += __shfl_xor_sync(0xFFFFFFFFu, w, o);
+        for (int c = 0; c < CPT; ++c) {
+            const int col = w.column(c / VE) + c % VE;
+            if (w.in(c / VE) && w.has(c / VE, c % VE)) {
+                to[col] = c & 1 ? dg[c / 2].y : dg[c / 2].x;
+                to[p.D + col] = c & 1 ? db[c / 2].y : db[c / 2].x;
+            }
         }
-        if (writes && j < p.vecs) {
-            at[j * V + c % V] = u;
-            at[p.D + j * V + c % V] = w;
+        return;
+    }
+    // Teams of a warp and less: one team of each warp after the other into the warp's columns (teams begin their
+    // vectors at other columns, where rows do), then over the warps.
+    const int warp = int(threadIdx.x) >> 5, warps = int(blockDim.x) >> 5, of_warp = (int(threadIdx.x) & 31) / q.TL;
+    float* at = dyn + warp * 2 * p.D;
+    for (int c = int(threadIdx.x) & 31; c < 2 * p.D; c += 32) at[c] = 0.f;
+    for (int k = 0; k < 32 / q.TL; ++k) {
+        __syncwarp();
+        if (k != of_warp) continue;
+#pragma unroll
+        for (int c = 0; c < CPT; ++c) {
+            const int col = w.column(c / VE) + c % VE;
+            if (w.in(c / VE) && w.has(c / VE, c % VE)) {
+                at[col] += c & 1 ? dg[c / 2].y : dg[c / 2].x;
+                at[p.D + col] += c & 1 ? db[c / 2].y : db[c / 2].x;
+            }
         }
     }
-    if (q.teams == 1) return;
     __syncthreads();
     for (int c = int(threadIdx.x); c < 2 * p.D; c += int(blockDim.x)) {
         float s = 0.f;
-        for (int w = 0; w < warps; ++w) s += dyn[w * 2 * p.D + c];
+        for (int k = 0; k < warps; ++k) s += dyn[k * 2 * p.D + c];
         to[c] = s;
     }
 }
 
 // ---- rows that no team holds: the rows' sums, then columns of all rows -------------------------
 template <typename T, int V>
-__global__ void __launch_bounds__(LN_MOST)
+__global__ void __launch_bounds__(LN_LONG)
 ln_bwd_rows(const __grid_constant__ LnParams p, const T* x, const T* dy, const T* gamma, const float* mean,
             const float* rstd, float2* sums)
 {
@@ -487,8 +618,14 @@ ln_params_kernel(const float* part, int parts, int D, T* dgamma, T* dbeta)
 
 template <int N> using Int = std::integral_constant<int, N>;
 
-// Calls f(T(), V) for the plan.
-template <class F> cudaError_t ln_types(const LnParams& p, int dt, F&& f)
+// Calls f(T(), EDGE) for a plan with teams.
+template <class F> cudaError_t ln_edge(const LnParams& p, int dt, F&& f)
+{
+    if (dt == DT_F32) return p.edge ? f(float(), std::true_type()) : f(float(), std::false_type());
+    return p.edge ? f(__nv_bfloat16(), std::true_type()) : f(__nv_bfloat16(), std::false_type());
+}
+// Calls f(T(), V) for one without.
+template <class F> cudaError_t ln_long(const LnParams& p, int dt, F&& f)
 {
     if (dt == DT_F32) return p.V == 4 ? f(float(), Int<4>()) : p.V == 2 ? f(float(), Int<2>()) : f(float(), Int<1>());
     return p.V == 8   ? f(__nv_bfloat16(), Int<8>())
@@ -507,23 +644,28 @@ LnParams ln_plan(const conv_ln_desc_t& e, const DevInfo& d, bool bwd)
     p.eps = e.eps;
     p.inv_d = float(1.0 / e.D);
     p.rms = e.rms != 0;
-    p.V = e.D % ve == 0 ? ve : e.D % 2 == 0 ? 2 : 1;
-    p.vecs = e.D / p.V;
-    const int64_t room = int64_t(d.sms) * 2048;  // threads
-    const int most_nv = bwd ? 16 / p.V : 8;
-    // Vectors of a thread: in the backward as few as a team of 256 can do with (a thread keeps two sums a column), in
-    // the forward as many as 4, by which a row of a warp needs no barrier.
+    p.edge = e.D % ve != 0;
+    const int vecs = int((int64_t(e.D) + ve - 1) / ve) + (p.edge ? 1 : 0);
+    // Vectors of a thread.  Forward: four, where a row has as many, and eight for the longest.  Backward, where a thread
+    // keeps two sums a column: eight columns, sixteen for the longest rows.
     int nv = 1;
-    while (nv < most_nv && (bwd ? p.vecs > nv * 256 : nv < 4 ? p.vecs > nv * 32 : p.vecs > nv * 256)) nv *= 2;
-    p.NV = nv;
-    const int need = (p.vecs + nv - 1) / nv;
-    if (need > (bwd ? LN_MOST_BWD : LN_MOST)) {
-        p.NV = 0;
-        p.TL = LN_MOST;
+    if (!bwd) {
+        while (nv < 4 && nv * 2 <= vecs) nv *= 2;
+        if (vecs > 4 * LN_MOST) nv = 8;
+    } else {
+        nv = es == 2 || vecs < 2 ? 1 : 2;
+        if (vecs > nv * LN_MOST) nv *= 2;
+    }
+    const int need = (vecs + nv - 1) / nv;
+    if (need > LN_MOST) {
+        p.V = e.D % ve == 0 ? ve : e.D % 2 == 0 ? 2 : 1;
+        p.vecs = e.D / p.V;
+        p.TL = LN_LONG;
         p.teams = 1;
-        p.blocks = int(std::min<int64_t>(e.N, d.sms * 2));
+        p.blocks = int(std::max<int64_t>(1, std::min<int64_t>(e.N, d.sms * 2)));
         return p;
     }
+    p.NV = nv;
     if (need <= 32) {
         p.TL = 1;
         while (p.TL < need) p.TL *= 2;
@@ -532,22 +674,24 @@ LnParams ln_plan(const conv_ln_desc_t& e, const DevInfo& d, bool bwd)
         p.TL = (need + 31) / 32 * 32;
         p.teams = 1;
     }
-    p.R = bwd ? ln_rows(es, p.V, p.NV) : 1;
+    p.R = bwd ? ln_rows(es, nv, p.edge) : 1;
     const int threads = p.TL * p.teams;
-    const int64_t blocks = (e.N + int64_t(p.teams) * p.R - 1) / (int64_t(p.teams) * p.R);
-    // The forward: as many blocks as the SMs hold threads for.  The backward: as its registers allow, 128 a thread or 64.
-    const int per_sm = std::max(1, (p.NV * p.V * p.R <= 8 ? 1024 : 512) / threads);
-    p.blocks = int(std::max<int64_t>(1, std::min(blocks, bwd ? int64_t(d.sms) * per_sm : room / threads)));
+    const int64_t rows = int64_t(p.teams) * p.R, blocks = (e.N + rows - 1) / rows;
+    // Twice as many blocks as the SMs hold at once with 64 registers a thread, or as many as they do with 128 in the
+    // backward; a multiple of what makes a team's rows begin alike.
+    const int per_sm = std::max(1, (bwd ? 512 : 2048) / threads);
+    p.blocks = int(std::max<int64_t>(1, std::min<int64_t>(blocks, int64_t(d.sms) * per_sm)));
+    if (p.edge && p.teams % ve != 0) p.blocks = (p.blocks + ve - 1) / ve * ve;
     if (bwd) p.flush = e.N > int64_t(p.blocks) * p.teams * LN_FLUSH;
     return p;
 }
 
 namespace {
 
-int ln_smem(const LnParams& p)
+int ln_smem(const LnParams& p, int ve)
 {
     const int threads = p.TL * p.teams;
-    return std::max(p.flush ? 2 * (p.NV * p.V + 1) / 2 * 2 * threads * 4 : 0, p.teams > 1 ? threads / 32 * 2 * p.D * 4 : 0);
+    return std::max(p.flush ? 2 * p.NV * ve * threads * 4 : 0, p.teams > 1 ? threads / 32 * 2 * p.D * 4 : 0);
 }
 
 // The blocks of columns and rows of a long row's second kernel.
@@ -564,21 +708,25 @@ cudaError_t run_ln_fwd(const conv_ln_desc_t& e, const DevInfo& d, const void* x,
                        const void* beta, void* y, void* total, float* mean, float* rstd, cudaStream_t s)
 {
     const LnParams p = ln_plan(e, d, false);
-    return ln_types(p, e.dtype, [&](auto t, auto v) {
+    const int ve = e.dtype == CONV_F32 ? 4 : 8;
+    const int smem = p.edge && p.NV > 0 ? std::min(p.teams, ve) * 2 * ((e.D + 2 * ve - 1) / ve * ve) * (16 / ve) : 0;
+    auto go = [&](auto kern, auto t) {
         using T = decltype(t);
-        constexpr int V = decltype(v)::value;
-        auto go = [&](auto kern) {
-            return launch_ex(kern, dim3(p.blocks), dim3(p.TL * p.teams), 0, s, 1, true, p, static_cast<const T*>(x),
-                             static_cast<const T*>(residual), static_cast<const T*>(gamma), static_cast<const T*>(beta),
-                             static_cast<T*>(y), static_cast<T*>(total), mean, rstd);
+        return launch_ex(kern, dim3(p.blocks), dim3(p.TL * p.teams), smem, s, 1, true, p, static_cast<const T*>(x),
+                         static_cast<const T*>(residual), static_cast<const T*>(gamma), static_cast<const T*>(beta),
+                         static_cast<T*>(y), static_cast<T*>(total), mean, rstd);
+    };
+    if (p.NV == 0)
+        return ln_long(p, e.dtype, [&](auto t, auto v) { return go(ln_fwd_long<decltype(t), decltype(v)::value>, t); });
+    return ln_edge(p, e.dtype, [&](auto t, auto edge) {
+        using T = decltype(t);
+        constexpr bool EDGE = decltype(edge)::value;
+        auto team = [&](auto nv) {
+            constexpr auto kern = ln_fwd_kernel<T, decltype(nv)::value, EDGE>;
+            const cudaError_t bad = ensure_smem<kern>(smem);
+            return bad != cudaSuccess ? bad : go(kern, t);
         };
-        switch (p.NV) {
-            case 1: return go(ln_fwd_kernel<T, V, 1>);
-            case 2: return go(ln_fwd_kernel<T, V, 2>);
-            case 4: return go(ln_fwd_kernel<T, V, 4>);
-            case 8: return go(ln_fwd_kernel<T, V, 8>);
-            default: return go(ln_fwd_long<T, V>);
-        }
+        return p.NV == 1 ? team(Int<1>()) : p.NV == 2 ? team(Int<2>()) : p.NV == 4 ? team(Int<4>()) : team(Int<8>());
     });
 }
 
@@ -595,48 +743,51 @@ cudaError_t run_ln_bwd(const conv_ln_desc_t& e, const DevInfo& d, const void* x,
                        void* ws, cudaStream_t s)
 {
     const LnParams p = ln_plan(e, d, true);
-    return ln_types(p, e.dtype, [&](auto t, auto v) {
-        using T = decltype(t);
-        constexpr int V = decltype(v)::value;
-        const T *px = static_cast<const T*>(x), *pdy = static_cast<const T*>(dy), *pg = static_cast<const T*>(gamma);
-        const T* pt = static_cast<const T*>(dtotal);
-        T* pdx = static_cast<T*>(dx);
-        float* part = static_cast<float*>(ws);
-        int parts = e.N > 0 ? p.blocks : 0;
-        cudaError_t err = cudaSuccess;
-        if (e.N > 0 && p.NV > 0) {
+    float* part = static_cast<float*>(ws);
+    int parts = e.N > 0 ? p.blocks : 0;
+    cudaError_t err = cudaSuccess;
+    if (e.N > 0 && p.NV > 0) {
+        err = ln_edge(p, e.dtype, [&](auto t, auto edge) {
+            using T = decltype(t);
             auto go = [&](auto nv) {
-                constexpr int NV = decltype(nv)::value;
-                if constexpr (NV * V <= 16) {
-                    constexpr auto kern = ln_bwd_kernel<T, V, NV, ln_rows(sizeof(T), V, NV)>;
-                    const int smem = ln_smem(p);
-                    if (const cudaError_t bad = ensure_smem<kern>(smem); bad != cudaSuccess) return bad;
-                    return launch_ex(kern, dim3(p.blocks), dim3(p.TL * p.teams), smem, s, 1, true, p, px, pdy, pg, mean,
-                                     rstd, pt, pdx, dgamma ? part : static_cast<float*>(nullptr));
-                } else {
-                    return cudaErrorInvalidValue;
-                }
+                constexpr int NV = decltype(nv)::value, ES = int(sizeof(T));
+                constexpr auto kern = ln_bwd_kernel<T, NV, ln_rows(ES, NV, decltype(edge)::value), decltype(edge)::value>;
+                const int smem = ln_smem(p, 16 / ES);
+                if (const cudaError_t bad = ensure_smem<kern>(smem); bad != cudaSuccess) return bad;
+                return launch_ex(kern, dim3(p.blocks), dim3(p.TL * p.teams), smem, s, 1, true, p,
+                                 static_cast<const T*>(x), static_cast<const T*>(dy), static_cast<const T*>(gamma), mean,
+                                 rstd, static_cast<const T*>(dtotal), static_cast<T*>(dx),
+                                 dgamma ? part : static_cast<float*>(nullptr));
             };
-            err = p.NV == 1   ? go(Int<1>())
-                  : p.NV == 2 ? go(Int<2>())
-                  : p.NV == 4 ? go(Int<4>())
-                  : p.NV == 8 ? go(Int<8>())
-                              : go(Int<16>());
-        } else if (e.N > 0) {
-            float2* sums = static_cast<float2*>(ws);
-            part += (size_t(e.N) * 8 + 15) / 16 * 4;
-            const dim3 grid = ln_columns_grid(p, d);
-            parts = int(grid.y);
-            err = launch_ex(ln_bwd_rows<T, V>, dim3(p.blocks), dim3(p.TL), 0, s, 1, true, p, px, pdy, pg, mean, rstd, sums);
-            if (err != cudaSuccess) return err;
-            err = launch_ex(ln_bwd_columns<T, V>, grid, dim3(LN_COLUMNS), 0, s, 1, true, p, px, pdy, pg, mean, rstd, pt,
-                            static_cast<const float2*>(sums), pdx, dgamma ? part : static_cast<float*>(nullptr));
-        }
-        if (err != cudaSuccess || !dgamma) return err;
-        const int64_t columns = int64_t(e.D) * (dbeta ? 2 : 1);
-        return launch_ex(ln_params_kernel<T>, dim3(unsigned((columns + 31) / 32)), dim3(1024), 0, s, 1, true,
-                         static_cast<const float*>(part), parts, e.D, static_cast<T*>(dgamma), static_cast<T*>(dbeta));
-    });
+            if constexpr (sizeof(T) == 4)
+                if (p.NV == 4) return go(Int<4>());
+            return p.NV == 1 ? go(Int<1>()) : go(Int<2>());
+        });
+    } else if (e.N > 0) {
+        float2* sums = static_cast<float2*>(ws);
+        part += (size_t(e.N) * 8 + 15) / 16 * 4;
+        const dim3 grid = ln_columns_grid(p, d);
+        parts = int(grid.y);
+        err = ln_long(p, e.dtype, [&](auto t, auto v) {
+            using T = decltype(t);
+            constexpr int V = decltype(v)::value;
+            const T *px = static_cast<const T*>(x), *pdy = static_cast<const T*>(dy), *pg = static_cast<const T*>(gamma);
+            const cudaError_t bad = launch_ex(ln_bwd_rows<T, V>, dim3(p.blocks), dim3(p.TL), 0, s, 1, true, p, px, pdy, pg,
+                                              mean, rstd, sums);
+            if (bad != cudaSuccess) return bad;
+            return launch_ex(ln_bwd_columns<T, V>, grid, dim3(LN_COLUMNS), 0, s, 1, true, p, px, pdy, pg, mean, rstd,
+                             static_cast<const T*>(dtotal), static_cast<const float2*>(sums), static_cast<T*>(dx),
+                             dgamma ? part : static_cast<float*>(nullptr));
+        });
+    }
+    if (err != cudaSuccess || !dgamma) return err;
+    const dim3 grid(unsigned((int64_t(e.D) * (dbeta ? 2 : 1) + 31) / 32));
+    auto add = [&](auto t) {
+        using T = decltype(t);
+        return launch_ex(ln_params_kernel<T>, grid, dim3(1024), 0, s, 1, true, static_cast<const float*>(part), parts, e.D,
+                         static_cast<T*>(dgamma), static_cast<T*>(dbeta));
+    };
+    return e.dtype == CONV_F32 ? add(float()) : add(__nv_bfloat16());
 }
 
 }  // namespace igc

@@ -167,10 +167,11 @@ cudaError_t run_distill_grad(const conv_distill_desc_t& e, const DevInfo& d, con
 // ---- layer norm of a residual sum (kernels_ln.cu) --------------------------------------------
 struct LnParams {
     int64_t N;
-    int D, V, vecs, NV;          // values a vector, vectors a row and a thread (0: rows that no team holds)
+    int D, NV;                   // NV: 16-byte vectors a thread; 0: rows that no team holds
+    int V, vecs;                 // where NV is 0: values a vector, vectors a row
     int TL, teams, R;            // threads a team, teams a block, rows a team takes at once
     int blocks;
-    bool rms, flush;             // flush: chains of additions are cut
+    bool rms, edge, flush;       // edge: rows do not all begin at 16 bytes; flush: chains of additions are cut
     float eps, inv_d;
 };
 LnParams ln_plan(const conv_ln_desc_t& e, const DevInfo& d, bool bwd);
