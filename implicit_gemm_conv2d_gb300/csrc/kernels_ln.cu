@@ -25,12 +25,13 @@ namespace {
 
 constexpr int LN_MOST = 512;     // threads of a team
 constexpr int LN_LONG = 1024;    // threads a row that no team holds
+constexpr int LN_SUMS = 128;     // floats: two sums of four rows of each warp
 constexpr int LN_FLUSH = 256;    // rows that are added to each other in one chain
 
 template <typename T> constexpr int ln_ve() { return 16 / int(sizeof(T)); }
 
-// Rows a team of the backward takes at once: as its registers allow.
-constexpr int ln_rows(int es, int NV, bool edge) { return NV * 16 / es > 8 ? 1 : es == 2 && !edge ? 4 : 2; }
+// Rows a team of the backward takes at once: 192 bytes a thread of x, dy and dtotal.
+constexpr int ln_rows(int NV) { return 4 / NV; }
 
 // A thread's place: teams of TL threads, each a row at a time, `rows` apart.
 struct LnAt {
@@ -91,19 +92,27 @@ template <typename T, int NV, bool EDGE> struct LnRow {
             r.set(f);
         }
     }
+    __device__ __forceinline__ void cut(Vector& r, int i) const
+    {
+        if (whole(i)) return;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (sizeof(T) == 4) r.r.w[k] = has(i, k) ? r.r.w[k] : 0u;
+            else r.r.w[k] &= (has(i, 2 * k) ? 0xFFFFu : 0u) | (has(i, 2 * k + 1) ? 0xFFFF0000u : 0u);
+        }
+    }
     __device__ __forceinline__ void cut(Vector (&a)[NV]) const
     {
-        if constexpr (EDGE) {
+        if constexpr (EDGE)
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (whole(i)) continue;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if constexpr (sizeof(T) == 4) a[i].r.w[k] = has(i, k) ? a[i].r.w[k] : 0u;
-                    else a[i].r.w[k] &= (has(i, 2 * k) ? 0xFFFFu : 0u) | (has(i, 2 * k + 1) ? 0xFFFF0000u : 0u);
-                }
-            }
-        }
+            for (int i = 0; i < NV; ++i) cut(a[i], i);
+    }
+    // The same vector on its way to shared memory; what lies behind the array is not read.
+    __device__ __forceinline__ void copy(uint32_t to, const T* a, int64_t at, int i) const
+    {
+        int bytes = 16;
+        if (EDGE && !whole(i) && at + VE > end) bytes = int(end - at) * int(sizeof(T));
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(a + at), "r"(bytes) : "memory");
     }
     __device__ __forceinline__ void store(T* a, int64_t at, int i, const Vector& r) const
     {
@@ -337,24 +346,31 @@ ln_fwd_long(const __grid_constant__ LnParams p, const T* x, const T* residual, c
     }
 }
 
-// Columns c and c + 1 of a thread's vectors, c even.
-template <typename T, int VE, int NV> __device__ __forceinline__ float2 pick(const Vec<T, VE> (&a)[NV], int c)
+// Columns v and v + 1 of a vector.
+template <typename T, int VE> __device__ __forceinline__ float2 pick(const Vec<T, VE>& a, int v)
 {
-    return make_float2(a[c / VE].get(c % VE), a[c / VE].get(c % VE + 1));
+    return make_float2(a.get(v), a.get(v + 1));
 }
 
-// R rows of a team at a time: neighbours, where rows begin at 16 bytes.  part: [block][dgamma, dbeta][D], or NULL.
-template <typename T, int NV, int R, bool EDGE>
+// R rows of a team at a time: neighbours, where rows begin at 16 bytes.  A thread's own vectors of the next rows are on
+// their way to its own places in shared memory while these are worked on: no barrier, and few registers.  What
+// both passes need is read there twice.  part: [block][dgamma, dbeta][D], or NULL.
+template <typename T, int NV, bool EDGE>
 __global__ void __launch_bounds__(LN_MOST)
 ln_bwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* dy, const T* gamma, const float* mean,
               const float* rstd, const T* dtotal, T* dx, float* part)
 {
-    extern __shared__ __align__(16) float dyn[];  // [2 P][threads] pairs: what the chains of additions have left so far
-    __shared__ float sm[2][32 * 2 * R];
-    constexpr int VE = ln_ve<T>(), CPT = NV * VE, P = CPT / 2;
+    // the rows' sums, twice in turn; [stage][row][x, dy, dtotal][NV][thread] vectors; what the chains of additions have
+    // left so far
+    extern __shared__ __align__(16) float dyn[];
+    constexpr int VE = ln_ve<T>(), CPT = NV * VE, P = CPT / 2, R = ln_rows(NV);
+    float* const tiles = dyn + 2 * LN_SUMS;
     using Vector = Vec<T, VE>;
     const LnAt q(p);
     const LnRow<T, NV, EDGE> w(p, q);
+    const uint32_t stages = tc::smem_u32(tiles) + threadIdx.x * 16;
+    const int step = int(blockDim.x) * 16, stage_bytes = R * 3 * NV * step;
+    float2* const left = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(tiles) + 2 * stage_bytes);
     tc::grid_dep_wait();
     tc::grid_dep_launch();
     float2 dg[P], db[P];
@@ -363,91 +379,106 @@ ln_bwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* dy, const
     for (int i = 0; i < NV; ++i) w.params(g[i], gamma, i, 1.f);
 #pragma unroll
     for (int c = 0; c < P; ++c) dg[c] = db[c] = both(0.f);
-    const int slot = 2 * int(blockDim.x);
     if (p.flush)
-        for (int k = 0; k < 2 * P; ++k) reinterpret_cast<float2*>(dyn)[k * int(blockDim.x) + int(threadIdx.x)] = both(0.f);
+        for (int k = 0; k < 2 * P; ++k) left[k * int(blockDim.x) + int(threadIdx.x)] = both(0.f);
     auto flush = [&] {
 #pragma unroll
         for (int c = 0; c < P; ++c) {
-            float2* a = reinterpret_cast<float2*>(dyn) + c * slot + threadIdx.x;
+            float2* a = left + 2 * c * int(blockDim.x) + int(threadIdx.x);
             a[0] = add2(a[0], dg[c]);
             a[blockDim.x] = add2(a[blockDim.x], db[c]);
             dg[c] = db[c] = both(0.f);
         }
     };
-    int turn = 0, chain = 0;
-    const int64_t next = EDGE ? q.rows : 1;  // from one of the R rows to the next
-    for (int64_t row0 = EDGE ? q.first : q.first * R; row0 - (EDGE ? 1 : R) * q.team < p.N; row0 += R * q.rows, turn ^= 1) {
-        Vector a[R][NV], d[R][NV], t[R][NV];
-        float m[R], r[R], sums[2 * R];
-        const int64_t at0 = w.at(row0, p.D, 0), hop = next * p.D;
-        uint32_t on = 0;  // rows that are there
-#pragma unroll
-        for (int k = 0; k < R; ++k)
-            if (row0 + k * next < p.N) on |= 1u << k;
+    const int64_t next = EDGE ? q.rows : 1, hop = next * p.D;  // from one of the R rows to the next
+    float m_next[R], r_next[R];
+    auto fetch = [&](int64_t row0, uint32_t to) {
+        const int64_t at0 = w.at(row0, p.D, 0);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            m[k] = r[k] = 0.f;
-            if (on >> k & 1u) {
-                if (mean) m[k] = mean[row0 + k * next];
-                r[k] = rstd[row0 + k * next];
-            }
+            m_next[k] = r_next[k] = 0.f;
+            if (row0 + k * next >= p.N) continue;
+            if (mean) m_next[k] = mean[row0 + k * next];
+            r_next[k] = rstd[row0 + k * next];
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                a[k][i].zero();
-                d[k][i].zero();  // (dy of 0: a place that is not there adds nothing)
-                t[k][i].zero();
-                if ((on >> k & 1u) && w.in(i)) {
-                    const int64_t at = at0 + k * hop + i * q.TL * VE;
-                    w.load(a[k][i], x, at, i);
-                    w.load(d[k][i], dy, at, i);
-                    if (dtotal) w.load(t[k][i], dtotal, at, i);
-                }
+                if (!w.in(i)) continue;
+                const int64_t at = at0 + k * hop + i * q.TL * VE;
+                const uint32_t slot = to + uint32_t((k * 3 * NV + i) * step);
+                w.copy(slot, x, at, i);
+                w.copy(slot + uint32_t(NV * step), dy, at, i);
+                if (dtotal) w.copy(slot + uint32_t(2 * NV * step), dtotal, at, i);
             }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto read = [&](Vector& r, uint32_t slot, int i) {
+        const int4 u = tc::lds128(slot);
+        r.r.w[0] = uint32_t(u.x); r.r.w[1] = uint32_t(u.y); r.r.w[2] = uint32_t(u.z); r.r.w[3] = uint32_t(u.w);
+        if (EDGE) w.cut(r, i);
+    };
+    const int64_t first = EDGE ? q.first : q.first * R, ahead = R * q.rows;
+    fetch(first, stages);
+    int turn = 0, chain = 0;
+    for (int64_t row0 = first; row0 - (EDGE ? 1 : R) * q.team < p.N; row0 += ahead, turn ^= 1) {
+        const uint32_t now = stages + uint32_t(turn * stage_bytes);
+        float m[R], r[R], sums[2 * R];
+        uint32_t on = 0;  // rows that are there
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            w.cut(a[k]);
-            w.cut(d[k]);
+            m[k] = m_next[k];
+            r[k] = r_next[k];
+            if (row0 + k * next < p.N) on |= 1u << k;
+        }
+        fetch(row0 + ahead, stages + uint32_t((turn ^ 1) * stage_bytes));
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
             float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
-            for (int c = 0; c < P; ++c) {
-                const float2 xh = mul2(add2(pick(a[k], 2 * c), both(-m[k])), both(r[k])), y = pick(d[k], 2 * c);
-                const float2 e = mul2(y, pick(g, 2 * c));
-                s1 = add2(s1, e);
-                s2 = fma2(e, xh, s2);
-                dg[c] = fma2(y, xh, dg[c]);
-                db[c] = add2(db[c], y);
+            for (int i = 0; i < NV; ++i) {
+                if (!(on >> k & 1u) || !w.in(i)) continue;
+                Vector a, d;
+                read(a, now + uint32_t((k * 3 * NV + i) * step), i);
+                read(d, now + uint32_t((k * 3 * NV + NV + i) * step), i);  // (0 where the row is not)
+#pragma unroll
+                for (int v = 0; v < VE; v += 2) {
+                    const int c = (i * VE + v) / 2;
+                    const float2 xh = mul2(add2(pick(a, v), both(-m[k])), both(r[k])), y = pick(d, v);
+                    const float2 e = mul2(y, pick(g[i], v));
+                    s1 = add2(s1, e);
+                    s2 = fma2(e, xh, s2);
+                    dg[c] = fma2(y, xh, dg[c]);
+                    db[c] = add2(db[c], y);
+                }
             }
             sums[2 * k] = s1.x + s1.y;
             sums[2 * k + 1] = s2.x + s2.y;
         }
-        ln_sum(q, sums, sm[turn]);
-        // What is computed of x and dy is computed again below: kept from above, it spills (32768 x 1024 bf16 66 -> 55 us).
-#pragma unroll
-        for (int k = 0; k < R; ++k)
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) asm volatile("" : "+r"(a[k][i].r.w[c]), "+r"(d[k][i].r.w[c]));
+        ln_sum(q, sums, dyn + turn * LN_SUMS);
+        const int64_t at0 = w.at(row0, p.D, 0);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            if (!(on >> k & 1u)) continue;
             const float m1 = p.rms ? 0.f : sums[2 * k] * p.inv_d, m2 = sums[2 * k + 1] * p.inv_d;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
+                if (!(on >> k & 1u) || !w.in(i)) continue;
+                Vector a, d, t;
+                read(a, now + uint32_t((k * 3 * NV + i) * step), i);
+                read(d, now + uint32_t((k * 3 * NV + NV + i) * step), i);
+                t.zero();
+                if (dtotal) read(t, now + uint32_t((k * 3 * NV + 2 * NV + i) * step), i);
                 float o[VE];
 #pragma unroll
                 for (int v = 0; v < VE; v += 2) {
-                    const int c = i * VE + v;
-                    const float2 xh = mul2(add2(pick(a[k], c), both(-m[k])), both(r[k]));
-                    const float2 e = mul2(pick(d[k], c), pick(g, c));
-                    const float2 u = fma2(both(r[k]), fma2(xh, both(-m2), add2(e, both(-m1))), pick(t[k], c));
+                    const float2 xh = mul2(add2(pick(a, v), both(-m[k])), both(r[k]));
+                    const float2 e = mul2(pick(d, v), pick(g[i], v));
+                    const float2 u = fma2(both(r[k]), fma2(xh, both(-m2), add2(e, both(-m1))), pick(t, v));
                     o[v] = u.x;
                     o[v + 1] = u.y;
                 }
-                a[k][i].set(o);
-                if (w.in(i)) w.store(dx, at0 + k * hop + i * q.TL * VE, i, a[k][i]);
+                a.set(o);
+                w.store(dx, at0 + k * hop + i * q.TL * VE, i, a);
             }
         }
         chain += R;
@@ -456,16 +487,16 @@ ln_bwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* dy, const
             chain = 0;
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (!part) return;
     if (p.flush) {
         flush();
 #pragma unroll
         for (int c = 0; c < P; ++c) {
-            const float2* a = reinterpret_cast<const float2*>(dyn) + c * slot + threadIdx.x;
+            const float2* a = left + 2 * c * int(blockDim.x) + int(threadIdx.x);
             dg[c] = a[0];
             db[c] = a[blockDim.x];
         }
-        __syncthreads();
     }
     float* to = part + int64_t(blockIdx.x) * 2 * p.D;
     if (q.teams == 1) {
@@ -482,7 +513,8 @@ ln_bwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* dy, const
     // Teams of a warp and less: one team of each warp after the other into the warp's columns (teams begin their
     // vectors at other columns, where rows do), then over the warps.
     const int warp = int(threadIdx.x) >> 5, warps = int(blockDim.x) >> 5, of_warp = (int(threadIdx.x) & 31) / q.TL;
-    float* at = dyn + warp * 2 * p.D;
+    float* at = tiles + warp * 2 * p.D;  // over the stages
+    __syncthreads();
     for (int c = int(threadIdx.x) & 31; c < 2 * p.D; c += 32) at[c] = 0.f;
     for (int k = 0; k < 32 / q.TL; ++k) {
         __syncwarp();
@@ -499,7 +531,7 @@ ln_bwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* dy, const
     __syncthreads();
     for (int c = int(threadIdx.x); c < 2 * p.D; c += int(blockDim.x)) {
         float s = 0.f;
-        for (int k = 0; k < warps; ++k) s += dyn[k * 2 * p.D + c];
+        for (int k = 0; k < warps; ++k) s += tiles[k * 2 * p.D + c];
         to[c] = s;
     }
 }
@@ -674,11 +706,11 @@ LnParams ln_plan(const conv_ln_desc_t& e, const DevInfo& d, bool bwd)
         p.TL = (need + 31) / 32 * 32;
         p.teams = 1;
     }
-    p.R = bwd ? ln_rows(es, nv, p.edge) : 1;
+    p.R = bwd ? ln_rows(nv) : 1;
     const int threads = p.TL * p.teams;
     const int64_t rows = int64_t(p.teams) * p.R, blocks = (e.N + rows - 1) / rows;
-    // Twice as many blocks as the SMs hold at once with 64 registers a thread, or as many as they do with 128 in the
-    // backward; a multiple of what makes a team's rows begin alike.
+    // Twice as many blocks as the SMs hold at once with 64 registers a thread; in the backward as many as they do with 128.
+    // A multiple of what makes a team's rows begin alike.
     const int per_sm = std::max(1, (bwd ? 512 : 2048) / threads);
     p.blocks = int(std::max<int64_t>(1, std::min<int64_t>(blocks, int64_t(d.sms) * per_sm)));
     if (p.edge && p.teams % ve != 0) p.blocks = (p.blocks + ve - 1) / ve * ve;
@@ -690,8 +722,8 @@ namespace {
 
 int ln_smem(const LnParams& p, int ve)
 {
-    const int threads = p.TL * p.teams;
-    return std::max(p.flush ? 2 * p.NV * ve * threads * 4 : 0, p.teams > 1 ? threads / 32 * 2 * p.D * 4 : 0);
+    const int threads = p.TL * p.teams, stages = 2 * p.R * 3 * p.NV * threads * 16;
+    return 8 * LN_SUMS + std::max(stages + (p.flush ? 2 * p.NV * ve * threads * 4 : 0), p.teams > 1 ? threads / 32 * 2 * p.D * 4 : 0);
 }
 
 // The blocks of columns and rows of a long row's second kernel.
@@ -751,7 +783,7 @@ cudaError_t run_ln_bwd(const conv_ln_desc_t& e, const DevInfo& d, const void* x,
             using T = decltype(t);
             auto go = [&](auto nv) {
                 constexpr int NV = decltype(nv)::value, ES = int(sizeof(T));
-                constexpr auto kern = ln_bwd_kernel<T, NV, ln_rows(ES, NV, decltype(edge)::value), decltype(edge)::value>;
+                constexpr auto kern = ln_bwd_kernel<T, NV, decltype(edge)::value>;
                 const int smem = ln_smem(p, 16 / ES);
                 if (const cudaError_t bad = ensure_smem<kern>(smem); bad != cudaSuccess) return bad;
                 return launch_ex(kern, dim3(p.blocks), dim3(p.TL * p.teams), smem, s, 1, true, p,
