@@ -9,6 +9,8 @@
 // shuffles, the warps of a cluster's blocks, which share a sequence's round, through distributed shared
 // memory, and each lane walks its steps again, from registers, with the state it now knows.  So each
 // input is read once, whatever the length, and a long sequence is worked on by many blocks.
+// Where even a cluster of 8 blocks a sequence leaves most of the GPU idle, time is cut into pieces first: one kernel
+// finds each piece's (A, H), the other joins those in front of its own and walks it.
 // Rounds travel through shared memory in both directions, whole rows at a time: inputs by
 // asynchronous copies (16 bytes where the rows allow it) that run a round or two ahead, results in
 // the places of the inputs.
@@ -275,6 +277,7 @@ struct ScanAt {
     int C, rank;
     int b0, c0;            // block: first batch row, first channel
     int b, c;              // lane: batch row and first channel
+    int piece, begin, end; // of time, in steps from the side that the scan begins at
     __device__ __forceinline__ ScanAt(const ScanPlan& p)
     {
         warp = int(threadIdx.x) >> 5;
@@ -282,7 +285,11 @@ struct ScanAt {
         seg = (int(threadIdx.x) & 31) >> 2;
         C = p.cluster;
         rank = int(blockIdx.x) % C;
-        const int unit = int(blockIdx.x) / C, WX = 1 << p.wx_log;
+        const int WX = 1 << p.wx_log, all = int(blockIdx.x) / C;
+        piece = all % p.pieces;
+        const int unit = all / p.pieces;
+        begin = piece * p.piece;
+        end = min(p.T - begin, p.piece) + begin;
         b0 = (unit / p.tiles) << p.by_log;
         c0 = (unit % p.tiles) * WX * 8;
         b = b0 + (warp >> p.wx_log);
@@ -549,10 +556,42 @@ __device__ __forceinline__ void scan_store(const ScanPlan& p, const ScanAt& q, f
     }
 }
 
-template <typename T, int L, int CB, bool RESET>
-__global__ void __launch_bounds__(SCAN_THREADS, sizeof(T) == 2 ? 2 : 3)
-scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, const float* h0, const uint8_t* reset,
-              const int32_t* lengths, T* h, float* last)
+// (A, H) of the pieces of time: [piece][batch row][channel], and behind them, as H, the state that enters the row (it
+// may lie where the state behind it is written).
+__device__ __forceinline__ int64_t scan_piece_at(const ScanPlan& p, const ScanAt& q, int piece)
+{
+    return (int64_t(piece) * p.B + q.b) * p.D + q.c;
+}
+// What the pieces in front of this one make of the state that enters the row: each of the warp's eight groups of
+// lanes joins an eighth of them.
+template <bool RESET>
+__device__ __forceinline__ float2 scan_pieces(const ScanPlan& p, const ScanAt& q, const float2* pieces)
+{
+    float2 A = both(1.f), H = both(0.f), state = both(0.f);
+    const int each = (q.piece + SCAN_SEGS - 1) / SCAN_SEGS, stop = min(q.piece, (q.seg + 1) * each);
+    if (q.b < p.B && q.c < p.D) {
+        const bool two = q.c + 1 < p.D;
+#pragma unroll 4
+        for (int k = q.seg * each; k < stop; ++k) {
+            const float2* at = pieces + scan_piece_at(p, q, k);
+            const float2 u = at[0], v = two ? at[1] : make_float2(1.f, 0.f);
+            float2 a = make_float2(u.x, v.x), h = make_float2(u.y, v.y);
+            scan_join<RESET>(a, h, A, H);
+            A = a;
+            H = h;
+        }
+        const float2* at = pieces + scan_piece_at(p, q, p.pieces);
+        state = make_float2(at[0].y, two ? at[1].y : 0.f);
+    }
+    ScanExchange::join_all<RESET>(A, H);
+    return shfl(scan_enter<RESET>(A, H, state), 28 + q.pair);
+}
+
+// (A, H) of each piece, forward from x and gate, backward (DIR = -1) from dh and gate.
+template <typename T, int L, int CB, bool RESET, int DIR>
+__global__ void __launch_bounds__(SCAN_THREADS, 3)
+scan_part_totals(const __grid_constant__ ScanPlan p, const T* x, const T* gate, const T* dh, const float* state,
+                 const uint8_t* reset, const int32_t* lengths, float2* pieces)
 {
     extern __shared__ __align__(128) uint8_t sm[];
     int* const lens = reinterpret_cast<int*>(sm);
@@ -562,31 +601,118 @@ scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
     ScanExchange ex;
     tc::grid_dep_wait();
     tc::grid_dep_launch();
-    float2 state = scan_state(p, q, h0);
+    const uint32_t stages = scan_setup(p, q, lengths, lens, tc::smem_u32(sm) + SCAN_LENS, ex);
+    const int len = lens[q.warp >> p.wx_log];
+    using Copy = ScanCopy<T, L, CB, DIR>;
+    const Copy copy(p, q, lens);
+    const ScanLane<T, L> lane(q);
+    constexpr int span = Tile::RT;
+    const int begin = DIR > 0 ? 0 : p.T - 1;  // step u is begin + DIR * u
+    typename Copy::Cursor ca = DIR > 0 ? copy.cursor(q, x, p.x, begin + q.begin, span)
+                                       : copy.cursor(q, dh, p.dh, begin - q.begin, span);
+    typename Copy::Cursor cg = copy.cursor(q, gate, p.gate, begin + DIR * q.begin, span);
+    ScanFlags<L, DIR> flags;
+    if (RESET && q.b < p.B) {
+        flags.row = reset + int64_t(q.b) * p.T;
+        flags.len = len;
+        flags.fetch(q, begin + DIR * (q.begin + q.seg * L));
+    }
+    auto fill = [&](int slot, int base) {
+        if (base < q.end) {
+            copy.fill(ca, stages + slot * STAGE, begin + DIR * base, 0);
+            copy.fill(cg, stages + slot * STAGE + Tile::ARRAY, begin + DIR * base, 0);
+        }
+        scan_commit();
+    };
+    fill(0, q.begin);
+    float2 A = both(1.f), H = both(0.f);
+    int now = 0;
+    for (int base = q.begin; base < q.end; base += span, now ^= 1) {
+        scan_arrived(2);
+        fill(now ^ 1, base + span);
+        const uint32_t stage = stages + now * STAGE;
+        const int t0 = begin + DIR * (base + q.seg * L);
+        uint32_t cut = 0;
+        if (RESET) {
+            cut = flags.take(q);
+            flags.fetch(q, t0 + DIR * span);
+        }
+        float2 a = both(1.f), h = both(0.f);
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            const int t = t0 + DIR * i;
+            if (t < 0 || t >= len) continue;
+            float2 e;
+            const float2 z = scan_gate<T>(lane.read(stage, 1, i), e), keep = one_minus(z), v = lane.read(stage, 0, i);
+            if (DIR > 0) {
+                if (RESET && (cut >> i & 1u)) h = both(0.f);
+                h = fma2(keep, h, mul2(z, v));
+            } else {
+                h = mul2(keep, add2(v, h));
+                if (RESET && (cut >> i & 1u)) h = both(0.f);
+            }
+            a = mul2(a, keep);
+        }
+        if (RESET && cut != 0) a = both(-1.f);
+        ScanExchange::join_all<RESET>(a, h);
+        a = shfl(a, 28 + q.pair);
+        h = shfl(h, 28 + q.pair);
+        scan_join<RESET>(a, h, A, H);
+        A = a;
+        H = h;
+    }
+    if (q.seg == 0 && q.b < p.B && q.c < p.D) {
+        float2* to = pieces + scan_piece_at(p, q, q.piece);
+        to[0] = make_float2(A.x, H.x);
+        if (q.c + 1 < p.D) to[1] = make_float2(A.y, H.y);
+        if (q.piece == 0) {
+            const float2 v = scan_state(p, q, state);
+            to = pieces + scan_piece_at(p, q, p.pieces);
+            to[0] = make_float2(0.f, v.x);
+            if (q.c + 1 < p.D) to[1] = make_float2(0.f, v.y);
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+template <typename T, int L, int CB, bool RESET>
+__global__ void __launch_bounds__(SCAN_THREADS, sizeof(T) == 2 ? 2 : 3)
+scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, const float* h0, const uint8_t* reset,
+              const int32_t* lengths, const float2* pieces, T* h, float* last)
+{
+    extern __shared__ __align__(128) uint8_t sm[];
+    int* const lens = reinterpret_cast<int*>(sm);
+    using Tile = ScanTile<T, L>;
+    constexpr int STAGE = 2 * Tile::ARRAY;
+    const ScanAt q(p);
+    ScanExchange ex;
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
+    float2 state = p.pieces > 1 ? scan_pieces<RESET>(p, q, pieces) : scan_state(p, q, h0);
     const uint32_t stages = scan_setup(p, q, lengths, lens, tc::smem_u32(sm) + SCAN_LENS, ex);
     const int len = lens[q.warp >> p.wx_log];
     using Copy = ScanCopy<T, L, CB, 1>;
     const Copy copy(p, q, lens);
     const ScanLane<T, L> lane(q);
     const int span = q.C * Tile::RT, rank0 = q.rank * Tile::RT;  // (T + span is below 2^31)
-    typename Copy::Cursor cx = copy.cursor(q, x, p.x, rank0, span), cg = copy.cursor(q, gate, p.gate, rank0, span);
-    typename Copy::Cursor ch = copy.cursor(q, h, p.h, rank0, span);
+    typename Copy::Cursor cx = copy.cursor(q, x, p.x, q.begin + rank0, span), cg = copy.cursor(q, gate, p.gate, q.begin + rank0, span);
+    typename Copy::Cursor ch = copy.cursor(q, h, p.h, q.begin + rank0, span);
     ScanFlags<L, 1> flags;
     if (RESET && q.b < p.B) {
         flags.row = reset + int64_t(q.b) * p.T;
         flags.len = len;
-        flags.fetch(q, rank0 + q.seg * L);
+        flags.fetch(q, q.begin + rank0 + q.seg * L);
     }
     auto fill = [&](int slot, int base) {
-        if (base < p.T) {
+        if (base < q.end) {
             copy.fill(cx, stages + slot * STAGE, base + rank0, 0);
             copy.fill(cg, stages + slot * STAGE + Tile::ARRAY, base + rank0, 0);
         }
         scan_commit();
     };
-    for (int k = 0; k < p.stages - 1; ++k) fill(k, k * span);
+    for (int k = 0; k < p.stages - 1; ++k) fill(k, q.begin + k * span);
     int now = 0, round = 0;
-    for (int base = 0; base < p.T; base += span, ++round) {
+    for (int base = q.begin; base < q.end; base += span, ++round) {
         const int prev = now == 0 ? p.stages - 1 : now - 1;
         scan_arrived(p.stages);
         // The stage of a round ago, which nobody reads any more: its results go out, a later round comes in.  Between
@@ -647,9 +773,9 @@ scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
     }
     if (round > 0) {
         __syncthreads();
-        copy.drain(ch, stages + (now == 0 ? p.stages - 1 : now - 1) * STAGE, (round - 1) * span + rank0, p.T);
+        copy.drain(ch, stages + (now == 0 ? p.stages - 1 : now - 1) * STAGE, q.begin + (round - 1) * span + rank0, p.T);
     }
-    scan_store(p, q, last, state);
+    if (q.end == p.T) scan_store(p, q, last, state);
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (q.C > 1) tc::cluster_sync();  // nothing is sent to a block that has ended
 }
@@ -659,7 +785,8 @@ scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
 template <typename T, int L, int CB, bool RESET>
 __global__ void __launch_bounds__(SCAN_THREADS, sizeof(T) == 2 ? 2 : 3)
 scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, const T* h, const T* dh, const float* h0,
-              const float* dlast, const uint8_t* reset, const int32_t* lengths, T* dx, T* dgate, float* dh0)
+              const float* dlast, const uint8_t* reset, const int32_t* lengths, const float2* pieces, T* dx, T* dgate,
+              float* dh0)
 {
     extern __shared__ __align__(128) uint8_t sm[];
     int* const lens = reinterpret_cast<int*>(sm);
@@ -669,24 +796,24 @@ scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
     ScanExchange ex;
     tc::grid_dep_wait();
     tc::grid_dep_launch();
-    float2 state = scan_state(p, q, dlast);
+    float2 state = p.pieces > 1 ? scan_pieces<RESET>(p, q, pieces) : scan_state(p, q, dlast);
     const uint32_t stages = scan_setup(p, q, lengths, lens, tc::smem_u32(sm) + SCAN_LENS, ex);
     const int len = lens[q.warp >> p.wx_log];
     using Copy = ScanCopy<T, L, CB, -1>;
     const Copy copy(p, q, lens);
     const ScanLane<T, L> lane(q);
     const int span = q.C * Tile::RT, last0 = p.T - 1 - q.rank * Tile::RT;
-    typename Copy::Cursor cx = copy.cursor(q, x, p.x, last0, span), cg = copy.cursor(q, gate, p.gate, last0, span),
-                          cd = copy.cursor(q, dh, p.dh, last0, span), ch = copy.cursor(q, h, p.h, last0 - 1, span),
-                          ox = copy.cursor(q, dx, p.dx, last0, span), og = copy.cursor(q, dgate, p.dgate, last0, span);
+    typename Copy::Cursor cx = copy.cursor(q, x, p.x, last0 - q.begin, span), cg = copy.cursor(q, gate, p.gate, last0 - q.begin, span),
+                          cd = copy.cursor(q, dh, p.dh, last0 - q.begin, span), ch = copy.cursor(q, h, p.h, last0 - q.begin - 1, span),
+                          ox = copy.cursor(q, dx, p.dx, last0 - q.begin, span), og = copy.cursor(q, dgate, p.dgate, last0 - q.begin, span);
     ScanFlags<L, -1> flags;
     if (RESET && q.b < p.B) {
         flags.row = reset + int64_t(q.b) * p.T;
         flags.len = len;
-        flags.fetch(q, last0 - q.seg * L);
+        flags.fetch(q, last0 - q.begin - q.seg * L);
     }
     auto fill = [&](int slot, int base) {
-        if (base < p.T) {
+        if (base < q.end) {
             const uint32_t to = stages + slot * STAGE;
             copy.fill(cx, to, last0 - base, 0);
             copy.fill(cg, to + Tile::ARRAY, last0 - base, 0);
@@ -699,9 +826,9 @@ scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
         copy.drain(ox, stages + slot * STAGE, last0 - base, p.T);
         copy.drain(og, stages + slot * STAGE + Tile::ARRAY, last0 - base, p.T);
     };
-    for (int k = 0; k < p.stages - 1; ++k) fill(k, k * span);
+    for (int k = 0; k < p.stages - 1; ++k) fill(k, q.begin + k * span);
     int now = 0, round = 0;
-    for (int base = 0; base < p.T; base += span, ++round) {
+    for (int base = q.begin; base < q.end; base += span, ++round) {
         const int prev = now == 0 ? p.stages - 1 : now - 1;
         scan_arrived(p.stages);
         // The stage of a round ago, which nobody reads any more: its results go out, a later round comes in.  Between
@@ -762,9 +889,9 @@ scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
     }
     if (round > 0) {
         __syncthreads();
-        drain(now == 0 ? p.stages - 1 : now - 1, (round - 1) * span);
+        drain(now == 0 ? p.stages - 1 : now - 1, q.begin + (round - 1) * span);
     }
-    scan_store(p, q, dh0, state);
+    if (q.end == p.T) scan_store(p, q, dh0, state);
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (q.C > 1) tc::cluster_sync();
 }
@@ -793,7 +920,7 @@ ScanPlan scan_plan(const conv_scan_desc_t& e, const DevInfo& d, bool bwd, int ch
     if (p.walk) {
         p.L = e.T == 1 ? 1 : 8;
         p.threads = WALK_THREADS;
-        p.cluster = 1;
+        p.cluster = p.pieces = 1;
         p.blocks = (int64_t(e.B) * p.cols + WALK_THREADS - 1) / WALK_THREADS;
         return p;
     }
@@ -818,10 +945,29 @@ ScanPlan scan_plan(const conv_scan_desc_t& e, const DevInfo& d, bool bwd, int ch
         }
     }
     p.cluster = 1 << log_c;
+    p.pieces = 1;
+    p.piece = e.T;
     p.threads = SCAN_THREADS;
     p.blocks = blocks << log_c;
     p.stages = rounds > (int64_t(2) << log_c) ? 3 : 2;
+    // Pieces of time, as many as the GPU holds blocks for, of two rounds and more: each is read twice, and a second launch
+    // comes on top, which is worth it where a cluster's blocks have some eight rounds more than that.
+    const int64_t most = std::min<int64_t>(int64_t(d.sms) * fit / std::max<int64_t>(1, blocks), rounds / 2);
+    if (most > 8 && rounds >> log_c > 2 * ((rounds + most - 1) / most) + 8) {
+        const int64_t each = (rounds + most - 1) / most;
+        p.cluster = 1;
+        p.piece = int(each * SCAN_SEGS * p.L);
+        p.pieces = int((rounds + each - 1) / each);
+        p.blocks = blocks * p.pieces;
+        p.stages = each > 2 ? 3 : 2;
+    }
     return p;
+}
+
+size_t scan_workspace(const conv_scan_desc_t& e, const DevInfo& d, bool bwd)
+{
+    const ScanPlan p = scan_plan(e, d, bwd, 16);  // (the pieces do not go by where rows begin)
+    return p.pieces > 1 ? size_t(p.pieces + 1) * size_t(e.B) * size_t(e.D) * 8 : 0;
 }
 
 namespace {
@@ -857,6 +1003,18 @@ template <bool BWD, class F, class G> cudaError_t scan_with(const ScanPlan& p, i
     return dt == DT_F32 ? on_reset(float()) : on_reset(__nv_bfloat16());
 }
 
+template <typename T, int L, int CB, bool RESET, int DIR>
+cudaError_t launch_totals(const ScanPlan& p, const T* x, const T* gate, const T* dh, const float* state,
+                          const uint8_t* reset, const int32_t* lengths, float2* pieces, cudaStream_t s)
+{
+    constexpr auto kern = scan_part_totals<T, L, CB, RESET, DIR>;
+    const int smem = SCAN_LENS + 4 * SCAN_SEGS * L * 64 * int(sizeof(T));  // two stages of two arrays
+    const cudaError_t err = ensure_smem<kern>(smem);
+    if (err != cudaSuccess) return err;
+    return launch_ex(kern, dim3(unsigned(p.blocks)), dim3(p.threads), smem, s, 1, true, p, x, gate, dh, state, reset,
+                     lengths, pieces);
+}
+
 // What every row of the array begins at a multiple of, in bytes: 16, 8, 4 or 2.
 int rows_chunk(const void* p, const conv_rows_t& r, int es)
 {
@@ -867,55 +1025,74 @@ int rows_chunk(const void* p, const conv_rows_t& r, int es)
 }  // namespace
 
 cudaError_t run_scan_fwd(const conv_scan_desc_t& e, const DevInfo& d, const void* x, const void* gate, const float* h0,
-                         const uint8_t* reset, const int32_t* lengths, void* h, float* last, cudaStream_t s)
+                         const uint8_t* reset, const int32_t* lengths, void* h, float* last, void* ws, cudaStream_t s)
 {
     const int es = e.dtype == CONV_F32 ? 4 : 2;
     const int chunk = std::min({rows_chunk(x, e.x, es), rows_chunk(gate, e.gate, es), rows_chunk(h, e.h, es)});
     const ScanPlan p = scan_plan(e, d, false, chunk);
     const int smem = scan_smem(p, es, false);
-    auto launch = [&](auto kern, auto t) {
-        using T = decltype(t);
-        return launch_ex(kern, dim3(unsigned(p.blocks)), dim3(p.threads), smem, s, p.cluster, true, p,
-                         static_cast<const T*>(x), static_cast<const T*>(gate), h0, reset, lengths, static_cast<T*>(h),
-                         last);
-    };
+    float2* const pieces = static_cast<float2*>(ws);
+    const dim3 grid(unsigned(p.blocks)), block(p.threads);
     return scan_with<false>(
         p, e.dtype, reset != nullptr,
         [&](auto t, auto l, auto cb, auto r) {
-            constexpr auto kern = scan_part_fwd<decltype(t), decltype(l)::value, decltype(cb)::value, decltype(r)::value>;
+            using T = decltype(t);
+            constexpr int L = decltype(l)::value, CB = decltype(cb)::value;
+            constexpr bool RESET = decltype(r)::value;
+            const T *px = static_cast<const T*>(x), *pg = static_cast<const T*>(gate);
+            if (p.pieces > 1) {
+                const cudaError_t err = launch_totals<T, L, CB, RESET, 1>(p, px, pg, nullptr, h0, reset, lengths, pieces, s);
+                if (err != cudaSuccess) return err;
+            }
+            constexpr auto kern = scan_part_fwd<T, L, CB, RESET>;
             const cudaError_t err = ensure_smem<kern>(smem);
-            return err != cudaSuccess ? err : launch(kern, t);
+            if (err != cudaSuccess) return err;
+            return launch_ex(kern, grid, block, smem, s, p.cluster, true, p, px, pg, h0, reset, lengths,
+                             static_cast<const float2*>(pieces), static_cast<T*>(h), last);
         },
         [&](auto t, auto v, auto l, auto r) {
-            return launch(scan_walk_fwd<decltype(t), decltype(v)::value, decltype(l)::value, decltype(r)::value>, t);
+            using T = decltype(t);
+            return launch_ex(scan_walk_fwd<T, decltype(v)::value, decltype(l)::value, decltype(r)::value>, grid, block, 0, s,
+                             1, true, p, static_cast<const T*>(x), static_cast<const T*>(gate), h0, reset, lengths,
+                             static_cast<T*>(h), last);
         });
 }
 
 cudaError_t run_scan_bwd(const conv_scan_desc_t& e, const DevInfo& d, const void* x, const void* gate, const void* h,
                          const void* dh, const float* h0, const float* dlast, const uint8_t* reset,
-                         const int32_t* lengths, void* dx, void* dgate, float* dh0, cudaStream_t s)
+                         const int32_t* lengths, void* dx, void* dgate, float* dh0, void* ws, cudaStream_t s)
 {
     const int es = e.dtype == CONV_F32 ? 4 : 2;
     const int chunk = std::min({rows_chunk(x, e.x, es), rows_chunk(gate, e.gate, es), rows_chunk(h, e.h, es),
                                 rows_chunk(dh, e.dh, es), rows_chunk(dx, e.dx, es), rows_chunk(dgate, e.dgate, es)});
     const ScanPlan p = scan_plan(e, d, true, chunk);
     const int smem = scan_smem(p, es, true);
-    auto launch = [&](auto kern, auto t) {
-        using T = decltype(t);
-        return launch_ex(kern, dim3(unsigned(p.blocks)), dim3(p.threads), smem, s, p.cluster, true, p,
-                         static_cast<const T*>(x), static_cast<const T*>(gate), static_cast<const T*>(h),
-                         static_cast<const T*>(dh), h0, dlast, reset, lengths, static_cast<T*>(dx),
-                         static_cast<T*>(dgate), dh0);
-    };
+    float2* const pieces = static_cast<float2*>(ws);
+    const dim3 grid(unsigned(p.blocks)), block(p.threads);
     return scan_with<true>(
         p, e.dtype, reset != nullptr,
         [&](auto t, auto l, auto cb, auto r) {
-            constexpr auto kern = scan_part_bwd<decltype(t), decltype(l)::value, decltype(cb)::value, decltype(r)::value>;
+            using T = decltype(t);
+            constexpr int L = decltype(l)::value, CB = decltype(cb)::value;
+            constexpr bool RESET = decltype(r)::value;
+            const T *pg = static_cast<const T*>(gate), *pd = static_cast<const T*>(dh);
+            if (p.pieces > 1) {
+                const cudaError_t err = launch_totals<T, L, CB, RESET, -1>(p, nullptr, pg, pd, dlast, reset, lengths, pieces, s);
+                if (err != cudaSuccess) return err;
+            }
+            constexpr auto kern = scan_part_bwd<T, L, CB, RESET>;
             const cudaError_t err = ensure_smem<kern>(smem);
-            return err != cudaSuccess ? err : launch(kern, t);
+            if (err != cudaSuccess) return err;
+            return launch_ex(kern, grid, block, smem, s, p.cluster, true, p, static_cast<const T*>(x), pg,
+                             static_cast<const T*>(h), pd, h0, dlast, reset, lengths, static_cast<const float2*>(pieces),
+                             static_cast<T*>(dx), static_cast<T*>(dgate), dh0);
         },
         [&](auto t, auto v, auto l, auto r) {
-            return launch(scan_walk_bwd<decltype(t), decltype(v)::value, decltype(l)::value, decltype(r)::value>, t);
+            using T = decltype(t);
+            return launch_ex(scan_walk_bwd<T, decltype(v)::value, decltype(l)::value, decltype(r)::value>, grid, block, 0, s,
+                             1, true, p, static_cast<const T*>(x), static_cast<const T*>(gate), static_cast<const T*>(h),
+                             static_cast<const T*>(dh), h0, dlast, reset, lengths, static_cast<T*>(dx),
+                             static_cast<T*>(dgate), dh0);
         });
 }
 

@@ -410,8 +410,10 @@ PyObject* gated_scan(PyObject* const* a)
     const at::Tensor h = out ? *out : at::empty(x.sizes(), x.options());
     d.h = rows_of(h, "out", x.sizes(), x.scalar_type(), x.device());
     const at::Tensor last = into ? *into : at::empty({d.B, d.D}, x.options().dtype(at::kFloat));
+    const size_t bytes = conv_scan_fwd_workspace_size(&d);
+    const at::Tensor ws = workspace(bytes, x);
     check(conv_scan_fwd(&d, x.data_ptr(), gate.data_ptr(), h0, reset, lengths, h.data_ptr(),
-                        static_cast<float*>(last.data_ptr()), stream_of(x)),
+                        static_cast<float*>(last.data_ptr()), address(ws), bytes, stream_of(x)),
           "conv_scan_fwd");
     return wrap(h, last);
 }
@@ -434,8 +436,11 @@ PyObject* gated_scan_bwd(PyObject* const* a)
     d.dgate = rows_of(dgate, "dgate", x.sizes(), x.scalar_type(), x.device());
     at::Tensor dh0;
     if (h0) dh0 = at::empty({d.B, d.D}, x.options().dtype(at::kFloat));
+    const size_t bytes = conv_scan_bwd_workspace_size(&d);
+    const at::Tensor ws = workspace(bytes, x);
     check(conv_scan_bwd(&d, x.data_ptr(), gate.data_ptr(), h.data_ptr(), dh.data_ptr(), h0, dlast, reset, lengths,
-                        dx.data_ptr(), dgate.data_ptr(), static_cast<float*>(address(dh0)), stream_of(x)),
+                        dx.data_ptr(), dgate.data_ptr(), static_cast<float*>(address(dh0)), address(ws), bytes,
+                        stream_of(x)),
           "conv_scan_bwd");
     return wrap(dx, dgate, dh0);
 }

@@ -270,8 +270,23 @@ int conv_ln_bwd(const conv_ln_desc_t* desc, const void* x, const void* dy, const
                                   reinterpret_cast<cudaStream_t>(stream)));
 }
 
+size_t conv_scan_fwd_workspace_size(const conv_scan_desc_t* desc)
+{
+    DevInfo d;
+    if (scan_check(desc, false) != CONV_OK || device_info(d) != CONV_OK) return 0;
+    return scan_workspace(*desc, d, false);
+}
+
+size_t conv_scan_bwd_workspace_size(const conv_scan_desc_t* desc)
+{
+    DevInfo d;
+    if (scan_check(desc, true) != CONV_OK || device_info(d) != CONV_OK) return 0;
+    return scan_workspace(*desc, d, true);
+}
+
 int conv_scan_fwd(const conv_scan_desc_t* desc, const void* x, const void* gate, const float* h0, const uint8_t* reset,
-                  const int32_t* lengths, void* h, float* last, conv_stream_t stream)
+                  const int32_t* lengths, void* h, float* last, void* workspace, size_t workspace_bytes,
+                  conv_stream_t stream)
 {
     int rc = scan_check(desc, false);
     if (rc != CONV_OK) return rc;
@@ -279,17 +294,19 @@ int conv_scan_fwd(const conv_scan_desc_t* desc, const void* x, const void* gate,
     if (desc->T > 0 && (!x || !gate || !h)) return CONV_ERR_NULL;
     const size_t a = desc->dtype == CONV_F32 ? 4 : 2;
     if (!aligned_to(x, a) || !aligned_to(gate, a) || !aligned_to(h, a) || !aligned_to(h0, 4) || !aligned_to(last, 4) ||
-        !aligned_to(lengths, 4))
+        !aligned_to(lengths, 4) || !aligned16(workspace))
         return CONV_ERR_ALIGN;
     DevInfo d;
     if ((rc = device_info(d)) != CONV_OK) return rc;
-    return cuda_status(
-        run_scan_fwd(*desc, d, x, gate, h0, reset, lengths, h, last, reinterpret_cast<cudaStream_t>(stream)));
+    const size_t need = scan_workspace(*desc, d, false);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return CONV_ERR_WORKSPACE;
+    return cuda_status(run_scan_fwd(*desc, d, x, gate, h0, reset, lengths, h, last, workspace,
+                                    reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int conv_scan_bwd(const conv_scan_desc_t* desc, const void* x, const void* gate, const void* h, const void* dh,
                   const float* h0, const float* dlast, const uint8_t* reset, const int32_t* lengths, void* dx,
-                  void* dgate, float* dh0, conv_stream_t stream)
+                  void* dgate, float* dh0, void* workspace, size_t workspace_bytes, conv_stream_t stream)
 {
     int rc = scan_check(desc, true);
     if (rc != CONV_OK) return rc;
@@ -298,11 +315,13 @@ int conv_scan_bwd(const conv_scan_desc_t* desc, const void* x, const void* gate,
     const size_t a = desc->dtype == CONV_F32 ? 4 : 2;
     if (!aligned_to(x, a) || !aligned_to(gate, a) || !aligned_to(h, a) || !aligned_to(dh, a) || !aligned_to(dx, a) ||
         !aligned_to(dgate, a) || !aligned_to(h0, 4) || !aligned_to(dlast, 4) || !aligned_to(dh0, 4) ||
-        !aligned_to(lengths, 4))
+        !aligned_to(lengths, 4) || !aligned16(workspace))
         return CONV_ERR_ALIGN;
     DevInfo d;
     if ((rc = device_info(d)) != CONV_OK) return rc;
-    return cuda_status(run_scan_bwd(*desc, d, x, gate, h, dh, h0, dlast, reset, lengths, dx, dgate, dh0,
+    const size_t need = scan_workspace(*desc, d, true);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return CONV_ERR_WORKSPACE;
+    return cuda_status(run_scan_bwd(*desc, d, x, gate, h, dh, h0, dlast, reset, lengths, dx, dgate, dh0, workspace,
                                     reinterpret_cast<cudaStream_t>(stream)));
 }
 

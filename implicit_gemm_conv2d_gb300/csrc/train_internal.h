@@ -129,14 +129,16 @@ struct ScanPlan {
     int CB, stages;              // parts: bytes of a copy, rounds in shared memory
     int wx_log, by_log, tiles;   // parts: a block's warps over channels and batch rows, blocks over the channels
     int cluster, threads;
+    int pieces, piece;           // parts: of time, steps of one
     int64_t blocks;
 };
 ScanPlan scan_plan(const conv_scan_desc_t& e, const DevInfo& d, bool bwd, int chunk);
+size_t scan_workspace(const conv_scan_desc_t& e, const DevInfo& d, bool bwd);
 cudaError_t run_scan_fwd(const conv_scan_desc_t& e, const DevInfo& d, const void* x, const void* gate, const float* h0,
-                         const uint8_t* reset, const int32_t* lengths, void* h, float* last, cudaStream_t s);
+                         const uint8_t* reset, const int32_t* lengths, void* h, float* last, void* ws, cudaStream_t s);
 cudaError_t run_scan_bwd(const conv_scan_desc_t& e, const DevInfo& d, const void* x, const void* gate, const void* h,
                          const void* dh, const float* h0, const float* dlast, const uint8_t* reset,
-                         const int32_t* lengths, void* dx, void* dgate, float* dh0, cudaStream_t s);
+                         const int32_t* lengths, void* dx, void* dgate, float* dh0, void* ws, cudaStream_t s);
 
 // ---- loss against a teacher's top logits (kernels_distill.cu) --------------------------------
 struct DistillParams {

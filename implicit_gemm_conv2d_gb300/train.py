@@ -31,7 +31,8 @@ _IDX = {torch.int32: 0, torch.int64: 1}
 EXPORTS = ["conv_gn_fwd_workspace_size", "conv_gn_fwd", "conv_gn_bwd_workspace_size", "conv_gn_bwd",
            "conv_embed_fwd", "conv_embed_bwd_workspace_size", "conv_embed_bwd",
            "conv_ln_fwd", "conv_ln_bwd_workspace_size", "conv_ln_bwd",
-           "conv_scan_fwd", "conv_scan_bwd", "conv_distill_fwd", "conv_distill_bwd", "conv_distill_grad",
+           "conv_scan_fwd_workspace_size", "conv_scan_fwd", "conv_scan_bwd_workspace_size", "conv_scan_bwd",
+           "conv_distill_fwd", "conv_distill_bwd", "conv_distill_grad",
            "conv_grad_norm_workspace_size", "conv_grad_norm", "conv_grad_clip"]
 
 
@@ -93,8 +94,12 @@ def lib():
             L.conv_ln_bwd_workspace_size.argtypes = [vp]
             L.conv_ln_bwd_workspace_size.restype = sz
             L.conv_ln_bwd.argtypes = [vp] * 11 + [sz, vp]
-            L.conv_scan_fwd.argtypes = [vp] * 9
-            L.conv_scan_bwd.argtypes = [vp] * 13
+            L.conv_scan_fwd_workspace_size.argtypes = [vp]
+            L.conv_scan_fwd_workspace_size.restype = sz
+            L.conv_scan_fwd.argtypes = [vp] * 9 + [sz, vp]
+            L.conv_scan_bwd_workspace_size.argtypes = [vp]
+            L.conv_scan_bwd_workspace_size.restype = sz
+            L.conv_scan_bwd.argtypes = [vp] * 13 + [sz, vp]
             L.conv_distill_fwd.argtypes = [vp] * 8
             L.conv_distill_bwd.argtypes = [vp] * 7 + [ctypes.c_float, vp, vp]
             L.conv_distill_grad.argtypes = [vp] * 5 + [ctypes.c_float, vp, vp, vp]
@@ -294,17 +299,27 @@ def make_scan_desc(x, gate, h, dh=None, dx=None, dgate=None) -> ScanDesc:
     return d
 
 
-def conv_scan_fwd(desc: ScanDesc, x, gate, h0, reset, lengths, h, last, stream=None) -> None:
+def conv_scan_fwd_workspace_size(desc: ScanDesc) -> int:
+    return lib().conv_scan_fwd_workspace_size(_ref(desc))
+
+
+def conv_scan_fwd(desc: ScanDesc, x, gate, h0, reset, lengths, h, last, workspace, stream=None) -> None:
     """h0, reset, lengths and last may be None."""
     _check(lib().conv_scan_fwd(_ref(desc), _rows_ptr(x), _rows_ptr(gate), _ptr(h0), _ptr(reset), _ptr(lengths),
-                               _rows_ptr(h), _ptr(last), _stream(stream)), "conv_scan_fwd")
+                               _rows_ptr(h), _ptr(last), _ptr(workspace), _bytes(workspace), _stream(stream)),
+           "conv_scan_fwd")
 
 
-def conv_scan_bwd(desc: ScanDesc, x, gate, h, dh, h0, dlast, reset, lengths, dx, dgate, dh0, stream=None) -> None:
+def conv_scan_bwd_workspace_size(desc: ScanDesc) -> int:
+    return lib().conv_scan_bwd_workspace_size(_ref(desc))
+
+
+def conv_scan_bwd(desc: ScanDesc, x, gate, h, dh, h0, dlast, reset, lengths, dx, dgate, dh0, workspace,
+                  stream=None) -> None:
     """h0, dlast, reset, lengths and dh0 may be None."""
     _check(lib().conv_scan_bwd(_ref(desc), _rows_ptr(x), _rows_ptr(gate), _rows_ptr(h), _rows_ptr(dh), _ptr(h0),
                                _ptr(dlast), _ptr(reset), _ptr(lengths), _rows_ptr(dx), _rows_ptr(dgate), _ptr(dh0),
-                               _stream(stream)), "conv_scan_bwd")
+                               _ptr(workspace), _bytes(workspace), _stream(stream)), "conv_scan_bwd")
 
 
 def gated_scan(x, gate, h0=None, reset=None, lengths=None, out=None, last=None, stream=None):

@@ -173,13 +173,16 @@ typedef struct {
     conv_rows_t dh, dx, dgate;  /* backward only                                           */
 } conv_scan_desc_t;
 
-/* Limits: B, T, D < 2^31 - 2^20, B * D < 2^40.  B = 0 does nothing.  lengths or reset may be NULL. */
+/* Limits: B, T, D < 2^31 - 2^20, B * D < 2^40.  B = 0 does nothing.  h0, reset, lengths and last may be NULL. */
+size_t conv_scan_fwd_workspace_size(const conv_scan_desc_t* desc);
 int conv_scan_fwd(const conv_scan_desc_t* desc, const void* x, const void* gate, const float* h0, const uint8_t* reset,
-                  const int32_t* lengths, void* h, float* last, conv_stream_t stream);
+                  const int32_t* lengths, void* h, float* last, void* workspace, size_t workspace_bytes,
+                  conv_stream_t stream);
 /* dh0: written, or NULL. */
+size_t conv_scan_bwd_workspace_size(const conv_scan_desc_t* desc);
 int conv_scan_bwd(const conv_scan_desc_t* desc, const void* x, const void* gate, const void* h, const void* dh,
                   const float* h0, const float* dlast, const uint8_t* reset, const int32_t* lengths, void* dx,
-                  void* dgate, float* dh0, conv_stream_t stream);
+                  void* dgate, float* dh0, void* workspace, size_t workspace_bytes, conv_stream_t stream);
 
 /* ---- loss against a teacher's top logits ----------------------------------------------------
  * Row n has V logits z and a teacher's K entries: ids and the teacher's logits at them.  With the

@@ -16,7 +16,8 @@ pytestmark = pytest.mark.gpu
 
 SIZES = [(1, 1, 1), (3, 1, 5), (96, 1, 130), (1, 2, 2), (7, 5, 33), (300, 9, 8), (2, 17, 33), (1, 129, 64), (40, 64, 16),
          (5, 777, 31), (1, 1000, 1), (2, 1025, 72), (1, 2500, 16), (1, 3000, 260), (3, 4099, 6), (700, 40, 3),
-         (1000, 37, 130), (20000, 21, 6), (40, 200, 520)]
+         (1000, 37, 130), (20000, 21, 6), (40, 200, 520),
+         (1, 9001, 24), (2, 20011, 9), (1, 5000, 70)]
 OPTIONS = {
     "plain": {},
     "state": dict(h0=True),
@@ -122,7 +123,7 @@ def test_run_to_run(dtype):
     assert all(torch.equal(a, b) for r in runs[1:] for a, b in zip(runs[0], r))
 
 
-@pytest.mark.parametrize("T", [1, 30, 3000])
+@pytest.mark.parametrize("T", [1, 30, 3000, 20000])
 def test_state_in_place_and_outputs_given(T):
     dev, side = inputs((5, T, 44), "bf16", h0=True, layout="joined")
     h, last = train.gated_scan(dev["x"], dev["gate"], side["h0"])
@@ -236,6 +237,37 @@ def test_rows_beyond_32_bits():
     assert torch.equal(dx, wantb[0]) and torch.equal(back[1], wantb[1])
 
 
+def test_pieces_of_time():
+    """Few channels over many steps, in pieces: what is not finite in one stays in its sequence, and a workspace that
+    is too small is refused."""
+    B, T, D = 1, 20000, 24
+    dev, side = inputs((B, T, D), "f32", h0=True)
+    side["reset"] = torch.zeros((B, T), dtype=torch.bool, device="cuda")
+    side["reset"][:, [9000, 9001, 15000]] = True
+    d = train.make_scan_desc(dev["x"], dev["gate"], dev["x"], dev["dh"], dev["x"], dev["x"])
+    need = train.conv_scan_fwd_workspace_size(d)
+    assert need > 0 and train.conv_scan_bwd_workspace_size(d) > 0
+    clean = train.gated_scan(dev["x"], dev["gate"], side["h0"], side["reset"])
+    back = train.gated_scan_bwd(dev["x"], dev["gate"], clean[0], dev["dh"], side["h0"], side["dlast"], side["reset"])
+    bad = dev["x"].clone()
+    bad[:, 5000] = float("nan")
+    h, last = train.gated_scan(bad, dev["gate"], side["h0"], side["reset"])
+    assert torch.equal(h[:, :5000], clean[0][:, :5000]) and torch.equal(h[:, 9000:], clean[0][:, 9000:])
+    assert bool(torch.isnan(h[:, 5000:9000]).all()) and torch.equal(last, clean[1])
+    bad = dev["dh"].clone()
+    bad[:, 12000] = float("inf")
+    dx, dgate, dh0 = train.gated_scan_bwd(dev["x"], dev["gate"], clean[0], bad, side["h0"], side["dlast"], side["reset"])
+    assert torch.equal(dx[:, 12001:], back[0][:, 12001:]) and torch.equal(dx[:, :9001], back[0][:, :9001])
+    assert torch.equal(dgate[:, :9001], back[1][:, :9001]) and torch.equal(dh0, back[2])
+    assert not bool(torch.isfinite(dx[:, 9001:12001]).any())
+    out, ws = torch.empty_like(dev["x"]), torch.empty(need, dtype=torch.uint8, device="cuda")
+    for room in (None, ws[:need - 8]):
+        with pytest.raises(train.binding.ConvError, match="(?i)workspace"):
+            train.conv_scan_fwd(d, dev["x"], dev["gate"], None, None, None, out, None, room)
+    train.conv_scan_fwd(d, dev["x"], dev["gate"], side["h0"], side["reset"].view(torch.uint8), None, out, None, ws.fill_(255))
+    assert torch.equal(out, clean[0])
+
+
 def test_c_entry_points():
     dev, side = inputs((3, 90, 26), "bf16", h0=True, reset=0.05, layout="joined")
     want = train.gated_scan(dev["x"], dev["gate"], side["h0"], side["reset"])
@@ -245,9 +277,9 @@ def test_c_entry_points():
     d = train.make_scan_desc(dev["x"], dev["gate"], h, dev["dh"], dx, dgate)
     reset = side["reset"].view(torch.uint8)
     last = torch.empty_like(side["h0"])
-    train.conv_scan_fwd(d, dev["x"], dev["gate"], side["h0"], reset, None, h, last)
+    train.conv_scan_fwd(d, dev["x"], dev["gate"], side["h0"], reset, None, h, last, None)
     assert torch.equal(h, want[0]) and torch.equal(last, want[1])
-    train.conv_scan_fwd(d, dev["x"], dev["gate"], side["h0"], reset, None, h, None)
+    train.conv_scan_fwd(d, dev["x"], dev["gate"], side["h0"], reset, None, h, None, None)
     dh0 = torch.empty_like(side["h0"])
-    train.conv_scan_bwd(d, dev["x"], dev["gate"], h, dev["dh"], side["h0"], side["dlast"], reset, None, dx, dgate, dh0)
+    train.conv_scan_bwd(d, dev["x"], dev["gate"], h, dev["dh"], side["h0"], side["dlast"], reset, None, dx, dgate, dh0, None)
     assert all(torch.equal(a, b) for a, b in zip((dx, dgate, dh0), grads))

@@ -31,12 +31,12 @@ def desc(rows=None, **kw):
 
 
 # The addresses are made up: every call here has to be one that is refused.
-def fwd(L, d, x=OK, gate=OK, h0=None, lengths=None, h=OK, last=OK):
-    return L.conv_scan_fwd(ctypes.addressof(d), x, gate, h0, None, lengths, h, last, None)
+def fwd(L, d, x=OK, gate=OK, h0=None, lengths=None, h=OK, last=OK, ws=None):
+    return L.conv_scan_fwd(ctypes.addressof(d), x, gate, h0, None, lengths, h, last, ws, 0, None)
 
 
-def bwd(L, d, x=OK, gate=OK, h=OK, dh=OK, h0=None, dlast=None, lengths=None, dx=OK, dgate=OK, dh0=None):
-    return L.conv_scan_bwd(ctypes.addressof(d), x, gate, h, dh, h0, dlast, None, lengths, dx, dgate, dh0, None)
+def bwd(L, d, x=OK, gate=OK, h=OK, dh=OK, h0=None, dlast=None, lengths=None, dx=OK, dgate=OK, dh0=None, ws=None):
+    return L.conv_scan_bwd(ctypes.addressof(d), x, gate, h, dh, h0, dlast, None, lengths, dx, dgate, dh0, ws, 0, None)
 
 
 @pytest.mark.parametrize("bad,code", [(dict(B=-1), -2), (dict(T=-1), -2), (dict(D=0), -2), (dict(dtype=2), -2),
@@ -44,7 +44,10 @@ def bwd(L, d, x=OK, gate=OK, h=OK, dh=OK, h0=None, dlast=None, lengths=None, dx=
                                       (dict(rows=dict(x=(-60, 6))), -2), (dict(rows=dict(gate=(60, -6))), -2),
                                       (dict(rows=dict(x=(1 << 62, 6))), -3)])
 def test_descriptor_refused(L, bad, code):
-    assert (fwd(L, desc(**bad)), bwd(L, desc(**bad))) == (code, code)
+    d = desc(**bad)
+    assert (fwd(L, d), bwd(L, d)) == (code, code)
+    assert L.conv_scan_fwd_workspace_size(ctypes.addressof(d)) == 0
+    assert L.conv_scan_bwd_workspace_size(ctypes.addressof(d)) == 0
 
 
 @pytest.mark.parametrize("rows", [(59, 6), (60, 5), (0, 6), (6, 23), (5, 60), (60, 0)])
@@ -62,12 +65,12 @@ def test_pointers_and_alignment(L):
     for name in ("x", "gate", "h", "dh", "dx", "dgate"):
         assert bwd(L, desc(), **{name: None}) == -1
         assert bwd(L, desc(), **{name: ODD + 1}) == -4
-    for name in ("h0", "last", "lengths"):
+    for name in ("h0", "last", "lengths", "ws"):
         assert fwd(L, desc(), **{name: ODD}) == -4
-    for name in ("h0", "dlast", "dh0", "lengths"):
+    for name in ("h0", "dlast", "dh0", "lengths", "ws"):
         assert bwd(L, desc(), **{name: ODD}) == -4
-    assert L.conv_scan_fwd(None, OK, OK, None, None, None, OK, OK, None) == -1
-    assert L.conv_scan_bwd(None, OK, OK, OK, OK, None, None, None, None, OK, OK, None, None) == -1
+    assert L.conv_scan_fwd(None, OK, OK, None, None, None, OK, OK, None, 0, None) == -1
+    assert L.conv_scan_bwd(None, OK, OK, OK, OK, None, None, None, None, OK, OK, None, None, 0, None) == -1
     assert fwd(L, desc(B=0), None, None, None, None, None, None) == 0
     assert bwd(L, desc(B=0), None, None, None, None, None, None, None, None, None, None) == 0
 
