@@ -255,6 +255,177 @@ scan_walk_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
     walk_store<V>(dh0, b * p.D + c, st);
 }
 
+// The same with the steps to come in shared memory, for fewer threads: their asynchronous copies go to their own
+// places, RING groups of RING_STEPS steps ahead, and need no barrier.  [group][step][array][thread] elements of V values.
+constexpr int RING_STEPS = 8;
+template <int BYTES> __device__ __forceinline__ void ring_copy(uint32_t to, const void* from)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
+}
+template <typename T, int V> __device__ __forceinline__ float2 ring_read(uint32_t at)
+{
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t u = tc::lds32(at);
+        return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+    } else if constexpr (V == 2) {
+        const uint2 u = tc::lds64(at);
+        return make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+    } else {
+        return make_float2(__uint_as_float(tc::lds32(at)), 0.f);
+    }
+}
+
+template <typename T, int V, int RING, bool RESET>
+__global__ void __launch_bounds__(WALK_THREADS)
+scan_ring_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, const float* h0, const uint8_t* reset,
+              const int32_t* lengths, T* h, float* last)
+{
+    extern __shared__ __align__(16) uint8_t sm[];
+    constexpr int SIZE = V * int(sizeof(T)), LINE = WALK_THREADS * SIZE, GROUP = RING_STEPS * 2 * LINE;
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
+    const int64_t unit = int64_t(blockIdx.x) * WALK_THREADS + threadIdx.x, b = unit / p.cols, c = unit % p.cols * V;
+    if (b >= p.B) return;
+    const int len = scan_length(p, lengths, int(b));
+    const T *px = x + b * p.x.batch + c, *pg = gate + b * p.gate.batch + c;
+    T* ph = h + b * p.h.batch + c;
+    const uint8_t* pr = RESET ? reset + b * p.T : nullptr;
+    float2 st = walk_state<V>(h0, b * p.D + c);
+    const uint32_t ring = tc::smem_u32(sm) + threadIdx.x * SIZE;
+    int ahead = 0;
+    auto fetch = [&](uint32_t to) {
+#pragma unroll
+        for (int i = 0; i < RING_STEPS; ++i, px += p.x.step, pg += p.gate.step)
+            if (ahead + i < len) {
+                ring_copy<SIZE>(to + uint32_t(i * 2 * LINE), px);
+                ring_copy<SIZE>(to + uint32_t((i * 2 + 1) * LINE), pg);
+            }
+        ahead += RING_STEPS;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int k = 0; k < RING; ++k) fetch(ring + uint32_t(k * GROUP));
+    uint32_t at = ring;
+    uint32_t flags = 0;  // of the steps ahead, one group's
+    auto look = [&](int t) {
+        flags = 0;
+        if (RESET)
+#pragma unroll
+            for (int i = 0; i < RING_STEPS; ++i)
+                if (t + i < len && pr[t + i] != 0) flags |= 1u << i;
+    };
+    look(0);
+    for (int t = 0; t < len; t += RING_STEPS) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
+        const uint32_t cut = flags;
+        float2 keep[RING_STEPS], in[RING_STEPS];
+#pragma unroll
+        for (int i = 0; i < RING_STEPS; ++i) {
+            float2 e;
+            const float2 z = scan_gate<T>(ring_read<T, V>(at + uint32_t((i * 2 + 1) * LINE)), e);
+            keep[i] = one_minus(z);
+            in[i] = mul2(z, ring_read<T, V>(at + uint32_t(i * 2 * LINE)));
+        }
+        fetch(at);
+        look(t + RING_STEPS);
+        at = at + GROUP == ring + RING * GROUP ? ring : at + GROUP;
+#pragma unroll
+        for (int i = 0; i < RING_STEPS; ++i) {
+            if (t + i < len) {
+                if (RESET && (cut >> i & 1u)) st = both(0.f);
+                st = fma2(keep[i], st, in[i]);
+                put<T, V>(ph, st);
+                ph += p.h.step;
+            }
+        }
+    }
+    for (int t = len; t < p.T; ++t, ph += p.h.step) put<T, V>(ph, both(0.f));
+    walk_store<V>(last, b * p.D + c, st);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+template <typename T, int V, int RING, bool RESET>
+__global__ void __launch_bounds__(WALK_THREADS)
+scan_ring_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, const T* h, const T* dh, const float* h0,
+              const float* dlast, const uint8_t* reset, const int32_t* lengths, T* dx, T* dgate, float* dh0)
+{
+    extern __shared__ __align__(16) uint8_t sm[];
+    constexpr int SIZE = V * int(sizeof(T)), LINE = WALK_THREADS * SIZE, GROUP = RING_STEPS * 4 * LINE;
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
+    const int64_t unit = int64_t(blockIdx.x) * WALK_THREADS + threadIdx.x, b = unit / p.cols, c = unit % p.cols * V;
+    if (b >= p.B) return;
+    const int len = scan_length(p, lengths, int(b));
+    const int64_t end = len - 1;  // the pointers are at the next step to read, and the next one to write
+    const T *px = x + b * p.x.batch + c + end * p.x.step, *pg = gate + b * p.gate.batch + c + end * p.gate.step;
+    const T *ph = h + b * p.h.batch + c + (end - 1) * p.h.step, *pd = dh + b * p.dh.batch + c + end * p.dh.step;
+    T *ox = dx + b * p.dx.batch + c + end * p.dx.step, *og = dgate + b * p.dgate.batch + c + end * p.dgate.step;
+    for (int t = len; t < p.T; ++t) {
+        put<T, V>(ox + (t - end) * p.dx.step, both(0.f));
+        put<T, V>(og + (t - end) * p.dgate.step, both(0.f));
+    }
+    const uint8_t* pr = RESET ? reset + b * p.T : nullptr;
+    float2 st = walk_state<V>(dlast, b * p.D + c);
+    const uint32_t ring = tc::smem_u32(sm) + threadIdx.x * SIZE;
+    int ahead = len;  // steps that are not on their way yet
+    auto fetch = [&](uint32_t to) {
+#pragma unroll
+        for (int i = 0; i < RING_STEPS; ++i, px -= p.x.step, pg -= p.gate.step, ph -= p.h.step, pd -= p.dh.step)
+            if (i < ahead) {
+                const uint32_t line = to + uint32_t(i * 4 * LINE);
+                ring_copy<SIZE>(line, px);
+                ring_copy<SIZE>(line + LINE, pg);
+                ring_copy<SIZE>(line + 2 * LINE, pd);
+                if (i < ahead - 1) ring_copy<SIZE>(line + 3 * LINE, ph);
+            }
+        ahead -= RING_STEPS;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int k = 0; k < RING; ++k) fetch(ring + uint32_t(k * GROUP));
+    uint32_t at = ring;
+    uint32_t flags = 0;
+    auto look = [&](int n) {
+        flags = 0;
+        if (RESET)
+#pragma unroll
+            for (int i = 0; i < RING_STEPS; ++i)
+                if (i < n && pr[n - 1 - i] != 0) flags |= 1u << i;
+    };
+    look(len);
+    for (int n = len; n > 0; n -= RING_STEPS) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
+        const uint32_t cut = flags;
+        float2 z[RING_STEPS], d[RING_STEPS], w[RING_STEPS];
+#pragma unroll
+        for (int i = 0; i < RING_STEPS; ++i) {
+            const uint32_t line = at + uint32_t(i * 4 * LINE);
+            float2 e;
+            z[i] = scan_gate<T>(ring_read<T, V>(line + LINE), e);
+            d[i] = ring_read<T, V>(line + 2 * LINE);
+            float2 before = ring_read<T, V>(line + 3 * LINE);
+            if (i == n - 1) before = walk_state<V>(h0, b * p.D + c);
+            if (RESET && (cut >> i & 1u)) before = both(0.f);
+            w[i] = mul2(scan_slope(e, z[i]), fma2(before, both(-1.f), ring_read<T, V>(line)));
+        }
+        fetch(at);
+        look(n - RING_STEPS);
+        at = at + GROUP == ring + RING * GROUP ? ring : at + GROUP;
+#pragma unroll
+        for (int i = 0; i < RING_STEPS; ++i) {
+            if (i < n) {
+                const float2 f = add2(d[i], st);
+                put<T, V>(ox, mul2(z[i], f));
+                put<T, V>(og, mul2(w[i], f));
+                ox -= p.dx.step;
+                og -= p.dgate.step;
+                st = mul2(one_minus(z[i]), f);
+                if (RESET && (cut >> i & 1u)) st = both(0.f);
+            }
+        }
+    }
+    walk_store<V>(dh0, b * p.D + c, st);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // ---- parts: warps of 8 stretches of 8 channels ------------------------------------------------
 // A block has 8 warps: WX of them side by side over the channels, BY batch rows.  A round of a block is
 // RT = 8 L steps, of a cluster C of those, one behind the other.
@@ -915,10 +1086,22 @@ ScanPlan scan_plan(const conv_scan_desc_t& e, const DevInfo& d, bool bwd, int ch
     const bool pairs = chunk >= 2 * es && e.D % 2 == 0;
     p.V = pairs ? 2 : 1;
     p.cols = (e.D + p.V - 1) / p.V;
+    // Which way.  A walk costs a step's instructions at least, one behind the other (0.05 to 0.1 us), parts the
+    // instructions of finding (A, H) and of two trips through shared memory.  In us, walk from registers / walk from
+    // shared memory / parts:
+    //   bf16 forward   16 x 1024 x 1024 104 / 56 / 45    48 x 512 x 1024 61 / 38 / 60    452 x 129 x 188 18 / 15 / 53
+    //   bf16 backward  16 x 1024 x 1024 133 / 101 / 69   48 x 512 x 1024 81 / 79 / 136   452 x 129 x 188 31 / 36 / 85
+    //   fp32 forward   24 x 1024 x 512 112 / 58 / 41     32 x 1024 x 1024 127 / 67 / 98  1024 x 64 x 128 18 / 23 / 22
+    //   fp32 backward  24 x 1024 x 512 144 / 115 / 65    32 x 1024 x 1024 174 / 135 / 176  1024 x 64 x 128 38 / 41 / 61
+    // and with 16 channels, where a block of parts has four batch rows: 1620 x 712 x 16 bf16 76 / 42 / 70.
     const int64_t walkers = int64_t(e.B) * ((int64_t(e.D) + 1) / 2);
-    p.walk = e.T <= 16 || walkers >= int64_t(d.sms) * 384;
+    const int64_t few = int64_t(d.sms) * (es == 2 ? 104 : 72) / (e.D <= 32 ? 2 : 1);
+    p.walk = e.T <= 16 || walkers >= few;
     if (p.walk) {
-        p.L = e.T == 1 ? 1 : 8;
+        // Single bf16 values are none that an asynchronous copy takes.
+        const bool ring = e.T > 8 && (es == 4 || pairs) && walkers < int64_t(d.sms) * 256;
+        p.ring = !ring ? 0 : es == 4 && !bwd ? 4 : 2;
+        p.L = e.T > 4 ? 8 : e.T > 2 ? 4 : std::max(1, e.T);
         p.threads = WALK_THREADS;
         p.cluster = p.pieces = 1;
         p.blocks = (int64_t(e.B) * p.cols + WALK_THREADS - 1) / WALK_THREADS;
@@ -974,16 +1157,17 @@ namespace {
 
 int scan_smem(const ScanPlan& p, int es, bool bwd)
 {
-    if (p.walk) return 0;
+    if (p.walk) return p.ring * RING_STEPS * (bwd ? 4 : 2) * WALK_THREADS * p.V * es;
     return SCAN_LENS + (p.cluster > 1 ? SCAN_WARPS * 16 + 2 * p.cluster * SCAN_WARPS * 64 : 0) +
            p.stages * (bwd ? 4 : 2) * SCAN_SEGS * p.L * 64 * es;
 }
 
 template <int N> using Int = std::integral_constant<int, N>;
 
-// Calls f(T(), L, CB, RESET), the last three as types, for the plan of a call in parts, and g(T(), V, L, RESET) for one
-// that walks.
-template <bool BWD, class F, class G> cudaError_t scan_with(const ScanPlan& p, int dt, bool reset, F&& f, G&& g)
+// Calls f(T(), L, CB, RESET), the last three as types, for the plan of a call in parts, and g(T(), V, L, RESET) or
+// ring(T(), V, RING, RESET) for one that walks.
+template <bool BWD, class F, class G, class H>
+cudaError_t scan_with(const ScanPlan& p, int dt, bool reset, F&& f, G&& g, H&& ring)
 {
     auto parts = [&](auto t, auto r) {
         using L = Int<sizeof(t) == 2 ? (BWD ? 8 : 16) : BWD ? 4 : 8>;
@@ -993,8 +1177,15 @@ template <bool BWD, class F, class G> cudaError_t scan_with(const ScanPlan& p, i
         return f(t, L(), Int<4>(), r);
     };
     auto walk = [&](auto t, auto r) {
-        if (p.L == 1) return p.V == 2 ? g(t, Int<2>(), Int<1>(), r) : g(t, Int<1>(), Int<1>(), r);
-        return p.V == 2 ? g(t, Int<2>(), Int<8>(), r) : g(t, Int<1>(), Int<8>(), r);
+        auto steps = [&](auto v) {
+            if constexpr (sizeof(t) == 4 || decltype(v)::value == 2) {
+                using Ring = Int<sizeof(t) == 4 && !BWD ? 4 : 2>;
+                if (p.ring > 0) return ring(t, v, Ring(), r);
+            }
+            return p.L == 1 ? g(t, v, Int<1>(), r) : p.L == 2 ? g(t, v, Int<2>(), r) : p.L == 4 ? g(t, v, Int<4>(), r)
+                                                                                               : g(t, v, Int<8>(), r);
+        };
+        return p.V == 2 ? steps(Int<2>()) : steps(Int<1>());
     };
     auto on_reset = [&](auto t) {
         if (p.walk) return reset ? walk(t, std::true_type()) : walk(t, std::false_type());
@@ -1055,6 +1246,14 @@ cudaError_t run_scan_fwd(const conv_scan_desc_t& e, const DevInfo& d, const void
             return launch_ex(scan_walk_fwd<T, decltype(v)::value, decltype(l)::value, decltype(r)::value>, grid, block, 0, s,
                              1, true, p, static_cast<const T*>(x), static_cast<const T*>(gate), h0, reset, lengths,
                              static_cast<T*>(h), last);
+        },
+        [&](auto t, auto v, auto n, auto r) {
+            using T = decltype(t);
+            constexpr auto kern = scan_ring_fwd<T, decltype(v)::value, decltype(n)::value, decltype(r)::value>;
+            const cudaError_t err = ensure_smem<kern>(smem);
+            if (err != cudaSuccess) return err;
+            return launch_ex(kern, grid, block, smem, s, 1, true, p, static_cast<const T*>(x), static_cast<const T*>(gate),
+                             h0, reset, lengths, static_cast<T*>(h), last);
         });
 }
 
@@ -1093,6 +1292,15 @@ cudaError_t run_scan_bwd(const conv_scan_desc_t& e, const DevInfo& d, const void
                              1, true, p, static_cast<const T*>(x), static_cast<const T*>(gate), static_cast<const T*>(h),
                              static_cast<const T*>(dh), h0, dlast, reset, lengths, static_cast<T*>(dx),
                              static_cast<T*>(dgate), dh0);
+        },
+        [&](auto t, auto v, auto n, auto r) {
+            using T = decltype(t);
+            constexpr auto kern = scan_ring_bwd<T, decltype(v)::value, decltype(n)::value, decltype(r)::value>;
+            const cudaError_t err = ensure_smem<kern>(smem);
+            if (err != cudaSuccess) return err;
+            return launch_ex(kern, grid, block, smem, s, 1, true, p, static_cast<const T*>(x), static_cast<const T*>(gate),
+                             static_cast<const T*>(h), static_cast<const T*>(dh), h0, dlast, reset, lengths,
+                             static_cast<T*>(dx), static_cast<T*>(dgate), dh0);
         });
 }
 

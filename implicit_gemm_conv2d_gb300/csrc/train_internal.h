@@ -125,7 +125,7 @@ struct ScanPlan {
     conv_rows_t x, gate, h, dh, dx, dgate;
     bool walk;                   // a thread walks all steps; else time is cut
     int V, cols;                 // walk: channels of a thread, threads of a row
-    int L;                       // steps a thread reads at once; of a stretch
+    int L, ring;                 // steps a thread reads at once; of a stretch.  ring: groups of steps in shared memory
     int CB, stages;              // parts: bytes of a copy, rounds in shared memory
     int wx_log, by_log, tiles;   // parts: a block's warps over channels and batch rows, blocks over the channels
     int cluster, threads;
