@@ -582,6 +582,91 @@ template <typename T, int L> struct ScanLane {
     }
 };
 
+// Inputs whose rows begin anywhere, for blocks of one batch row: a step's row of the tile comes as the 16-byte pieces of
+// memory that it lies in, one more than it is long, and is read from where it begins in the first of them.  Where
+// that is goes by the step's place in its stretch alone: L steps are a multiple of 16 bytes apart.  Stretches begin
+// `SKEW` bytes further on each, in other banks.
+template <typename T, int L, int DIR> struct ScanWindow {
+    using Tile = ScanTile<T, L>;
+    static constexpr int ES = Tile::ES, CHUNKS = Tile::ROW / 16, ROWS = SCAN_THREADS / CHUNKS, N = Tile::RT / ROWS;
+    static constexpr int PITCH = Tile::ROW + 16, SKEW = ES == 2 ? 16 : L == 4 ? 96 : 32;
+    static constexpr int ARRAY = Tile::RT * PITCH + SCAN_SEGS * SKEW;
+    static_assert(L * ES % 16 == 0, "a stretch's steps repeat their places");
+    struct Cursor {
+        const char *at, *last;  // the row of the thread's first step, and of the one whose last piece it takes
+        const char* lowest;     // of the array
+        int64_t hop, round;
+    };
+    int chunk, u0, bytes, len;
+    static __device__ __forceinline__ uint32_t place(int u) { return uint32_t(u * PITCH + u / L * SKEW); }
+    __device__ __forceinline__ ScanWindow(const ScanPlan& p, const ScanAt& q, const int* lens)
+    {
+        chunk = int(threadIdx.x) % CHUNKS;
+        u0 = int(threadIdx.x) / CHUNKS;
+        bytes = min(64, p.D - q.c0) * ES;
+        len = lens[0];
+    }
+    __device__ __forceinline__ Cursor cursor(const ScanAt& q, const void* array, const conv_rows_t& r, int64_t first,
+                                             int64_t span) const
+    {
+        const char* a = static_cast<const char*>(array);
+        const int64_t row = q.b0 * r.batch + q.c0 + first * r.step;
+        return {a + (row + DIR * u0 * r.step) * ES, a + (row + DIR * int(threadIdx.x) * r.step) * ES, a,
+                DIR * ROWS * r.step * ES, DIR * span * r.step * ES};
+    }
+    // Where the first step of a lane's stretch begins in its first piece.
+    static __device__ __forceinline__ uint32_t begins(const ScanAt& q, const void* array, const conv_rows_t& r, int64_t first)
+    {
+        const int64_t row = q.b0 * r.batch + q.c0 + (first + DIR * q.seg * L) * r.step;
+        return uint32_t((reinterpret_cast<uintptr_t>(array) + uint64_t(row) * ES) & 15);
+    }
+    __device__ __forceinline__ void piece(uint32_t row, int k, const char* at, const char* lowest) const
+    {
+        const int off = k * 16 - int(reinterpret_cast<uintptr_t>(at) & 15);  // of the piece, from the row's first byte
+        if (off >= bytes) return;
+        const uint32_t to = row + uint32_t(k * 16);
+        if (off < 0 && at + off < lowest) {  // the array's first piece, which begins before the array does
+#pragma unroll
+            for (int e = 0; e < 16; e += ES)
+                if (off + e >= 0 && off + e < bytes) {
+                    if constexpr (ES == 4) tc::sts32(to + e, *reinterpret_cast<const uint32_t*>(at + off + e));
+                    else tc::sts16(to + e, *reinterpret_cast<const uint16_t*>(at + off + e));
+                }
+        } else {
+            const int size = min(16, bytes - off);  // (what lies behind the row's last channel may not be there)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(at + off), "r"(size) : "memory");
+        }
+    }
+    __device__ __forceinline__ void fill(Cursor& c, uint32_t to, int first, int shift) const
+    {
+        const char* src = c.at;
+        const unsigned some = unsigned(max(0, len - shift));
+#pragma unroll
+        for (int k = 0; k < N; ++k, src += c.hop)
+            if (unsigned(first + DIR * (u0 + k * ROWS) - shift) < some) piece(to + place(u0 + k * ROWS), chunk, src, c.lowest);
+        const int u = int(threadIdx.x);
+        if (u < Tile::RT && unsigned(first + DIR * u - shift) < some) piece(to + place(u), CHUNKS, c.last, c.lowest);
+        c.at += c.round;
+        c.last += c.round;
+    }
+    static __device__ __forceinline__ uint32_t lane(const ScanAt& q)
+    {
+        return place(q.seg * L) + uint32_t(q.warp * 8 * ES + q.pair * 2 * ES);
+    }
+    // Two channels of the row that begins at byte `at` and `begin` more.
+    static __device__ __forceinline__ float2 read(uint32_t at, uint32_t begin)
+    {
+        at += begin & 15u;
+        if constexpr (ES == 4) {
+            return make_float2(__uint_as_float(tc::lds32(at)), __uint_as_float(tc::lds32(at + 4)));
+        } else {
+            const uint32_t word = at & ~3u;
+            const uint32_t u = __funnelshift_r(tc::lds32(word), tc::lds32(word + 4), (at & 2u) * 8u);
+            return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+        }
+    }
+};
+
 // The warp's stretches joined along time, and with those of the same warp in the cluster's other blocks.
 struct ScanExchange {
     uint32_t bars, slots;  // two mbarriers a warp; [parity][rank][warp][pair] of (A, H) twice
@@ -846,15 +931,18 @@ scan_part_totals(const __grid_constant__ ScanPlan p, const T* x, const T* gate, 
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <typename T, int L, int CB, bool RESET>
-__global__ void __launch_bounds__(SCAN_THREADS, sizeof(T) == 2 ? 2 : 3)
+template <typename T, int L, int CB, bool WINDOW, bool RESET>
+__global__ void __launch_bounds__(SCAN_THREADS, sizeof(T) == 2 || WINDOW ? 2 : 3)
 scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, const float* h0, const uint8_t* reset,
               const int32_t* lengths, const float2* pieces, T* h, float* last)
 {
     extern __shared__ __align__(128) uint8_t sm[];
     int* const lens = reinterpret_cast<int*>(sm);
     using Tile = ScanTile<T, L>;
-    constexpr int STAGE = 2 * Tile::ARRAY;
+    using Copy = ScanCopy<T, L, CB, 1>;
+    using Window = ScanWindow<T, L, 1>;
+    using In = std::conditional_t<WINDOW, Window, Copy>;
+    constexpr int ARRAY = WINDOW ? Window::ARRAY : Tile::ARRAY, STAGE = 2 * ARRAY;
     const ScanAt q(p);
     ScanExchange ex;
     tc::grid_dep_wait();
@@ -862,12 +950,25 @@ scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
     float2 state = p.pieces > 1 ? scan_pieces<RESET>(p, q, pieces) : scan_state(p, q, h0);
     const uint32_t stages = scan_setup(p, q, lengths, lens, tc::smem_u32(sm) + SCAN_LENS, ex);
     const int len = lens[q.warp >> p.wx_log];
-    using Copy = ScanCopy<T, L, CB, 1>;
     const Copy copy(p, q, lens);
+    const In in_copy(p, q, lens);
     const ScanLane<T, L> lane(q);
     const int span = q.C * Tile::RT, rank0 = q.rank * Tile::RT;  // (T + span is below 2^31)
-    typename Copy::Cursor cx = copy.cursor(q, x, p.x, q.begin + rank0, span), cg = copy.cursor(q, gate, p.gate, q.begin + rank0, span);
+    typename In::Cursor cx = in_copy.cursor(q, x, p.x, q.begin + rank0, span);
+    typename In::Cursor cg = in_copy.cursor(q, gate, p.gate, q.begin + rank0, span);
     typename Copy::Cursor ch = copy.cursor(q, h, p.h, q.begin + rank0, span);
+    // Results wait in the places of x, or, where those are not a lane's own, behind the stages, two rounds in turn.
+    const uint32_t results = stages + p.stages * STAGE;
+    const uint32_t bx = WINDOW ? Window::begins(q, x, p.x, q.begin + rank0) : 0;
+    const uint32_t bg = WINDOW ? Window::begins(q, gate, p.gate, q.begin + rank0) : 0;
+    auto value = [&](uint32_t stage, int array, int i) {
+        if constexpr (WINDOW)
+            return Window::read(stage + Window::lane(q) + uint32_t(array * ARRAY + i * Window::PITCH),
+                                array == 0 ? bx + uint32_t(i) * uint32_t(p.x.step * Tile::ES)
+                                           : bg + uint32_t(i) * uint32_t(p.gate.step * Tile::ES));
+        else
+            return lane.read(stage, array, i);
+    };
     ScanFlags<L, 1> flags;
     if (RESET && q.b < p.B) {
         flags.row = reset + int64_t(q.b) * p.T;
@@ -876,8 +977,8 @@ scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
     }
     auto fill = [&](int slot, int base) {
         if (base < q.end) {
-            copy.fill(cx, stages + slot * STAGE, base + rank0, 0);
-            copy.fill(cg, stages + slot * STAGE + Tile::ARRAY, base + rank0, 0);
+            in_copy.fill(cx, stages + slot * STAGE, base + rank0, 0);
+            in_copy.fill(cg, stages + slot * STAGE + ARRAY, base + rank0, 0);
         }
         scan_commit();
     };
@@ -889,10 +990,10 @@ scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
         // The stage of a round ago, which nobody reads any more: its results go out, a later round comes in.  Between
         // send and receive, where the cluster's answers are waited for; loads that a thread waits for come first.
         auto turn = [&] {
-            if (round > 0) copy.drain(ch, stages + prev * STAGE, base - span + rank0, p.T);
+            if (round > 0) copy.drain(ch, WINDOW ? results + ((round - 1) & 1) * Tile::ARRAY : stages + prev * STAGE, base - span + rank0, p.T);
             fill(prev, base + (p.stages - 1) * span);
         };
-        if (CB == 2) turn();
+        if (CB == 2 && !WINDOW) turn();
         const uint32_t stage = stages + now * STAGE;
         const int t0 = base + rank0 + q.seg * L;
         uint32_t cut = 0;
@@ -905,9 +1006,9 @@ scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             float2 e;
-            const float2 z = scan_gate<T>(lane.read(stage, 1, i), e);
+            const float2 z = scan_gate<T>(value(stage, 1, i), e);
             keep[i] = one_minus(z);
-            in[i] = mul2(z, lane.read(stage, 0, i));
+            in[i] = mul2(z, value(stage, 0, i));
         }
         const bool full = t0 + L <= len;
         if (!full) {
@@ -927,24 +1028,26 @@ scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
         }
         if (RESET && cut != 0) A = both(-1.f);
         ex.send<RESET>(q, round, A, H);
-        if (CB != 2) turn();
+        if (CB != 2 || WINDOW) turn();
         float2 st = ex.receive<RESET>(q, round, A, H, state);
+        const uint32_t out = WINDOW ? results + (round & 1) * Tile::ARRAY : stage;
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             if (RESET && (cut >> i & 1u)) st = both(0.f);
             st = fma2(keep[i], st, in[i]);
-            lane.write(stage, 0, i, st);
+            lane.write(out, 0, i, st);
         }
         if (!full) {
 #pragma unroll
             for (int i = 0; i < L; ++i)
-                if (t0 + i >= len) lane.write(stage, 0, i, both(0.f));
+                if (t0 + i >= len) lane.write(out, 0, i, both(0.f));
         }
         now = now + 1 == p.stages ? 0 : now + 1;
     }
     if (round > 0) {
         __syncthreads();
-        copy.drain(ch, stages + (now == 0 ? p.stages - 1 : now - 1) * STAGE, q.begin + (round - 1) * span + rank0, p.T);
+        copy.drain(ch, WINDOW ? results + ((round - 1) & 1) * Tile::ARRAY : stages + (now == 0 ? p.stages - 1 : now - 1) * STAGE,
+                   q.begin + (round - 1) * span + rank0, p.T);
     }
     if (q.end == p.T) scan_store(p, q, last, state);
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -953,8 +1056,8 @@ scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
 
 // Time runs backwards: a lane's stretch is the steps t = T - 1 - u, u = u0 .. u0 + L - 1, and the state is what
 // flows from step t into t - 1, (1 - z[t]) s[t].
-template <typename T, int L, int CB, bool RESET>
-__global__ void __launch_bounds__(SCAN_THREADS, sizeof(T) == 2 ? 2 : 3)
+template <typename T, int L, int CB, bool WINDOW, bool RESET>
+__global__ void __launch_bounds__(SCAN_THREADS, sizeof(T) == 2 || WINDOW ? 2 : 3)
 scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, const T* h, const T* dh, const float* h0,
               const float* dlast, const uint8_t* reset, const int32_t* lengths, const float2* pieces, T* dx, T* dgate,
               float* dh0)
@@ -962,7 +1065,10 @@ scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
     extern __shared__ __align__(128) uint8_t sm[];
     int* const lens = reinterpret_cast<int*>(sm);
     using Tile = ScanTile<T, L>;
-    constexpr int STAGE = 4 * Tile::ARRAY;
+    using Copy = ScanCopy<T, L, CB, -1>;
+    using Window = ScanWindow<T, L, -1>;
+    using In = std::conditional_t<WINDOW, Window, Copy>;
+    constexpr int ARRAY = WINDOW ? Window::ARRAY : Tile::ARRAY, STAGE = 4 * ARRAY;
     const ScanAt q(p);
     ScanExchange ex;
     tc::grid_dep_wait();
@@ -970,13 +1076,30 @@ scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
     float2 state = p.pieces > 1 ? scan_pieces<RESET>(p, q, pieces) : scan_state(p, q, dlast);
     const uint32_t stages = scan_setup(p, q, lengths, lens, tc::smem_u32(sm) + SCAN_LENS, ex);
     const int len = lens[q.warp >> p.wx_log];
-    using Copy = ScanCopy<T, L, CB, -1>;
     const Copy copy(p, q, lens);
+    const In in_copy(p, q, lens);
     const ScanLane<T, L> lane(q);
     const int span = q.C * Tile::RT, last0 = p.T - 1 - q.rank * Tile::RT;
-    typename Copy::Cursor cx = copy.cursor(q, x, p.x, last0 - q.begin, span), cg = copy.cursor(q, gate, p.gate, last0 - q.begin, span),
-                          cd = copy.cursor(q, dh, p.dh, last0 - q.begin, span), ch = copy.cursor(q, h, p.h, last0 - q.begin - 1, span),
-                          ox = copy.cursor(q, dx, p.dx, last0 - q.begin, span), og = copy.cursor(q, dgate, p.dgate, last0 - q.begin, span);
+    const int first = last0 - q.begin;
+    typename In::Cursor cx = in_copy.cursor(q, x, p.x, first, span), cg = in_copy.cursor(q, gate, p.gate, first, span),
+                        cd = in_copy.cursor(q, dh, p.dh, first, span), ch = in_copy.cursor(q, h, p.h, first - 1, span);
+    typename Copy::Cursor ox = copy.cursor(q, dx, p.dx, first, span), og = copy.cursor(q, dgate, p.dgate, first, span);
+    // (as in the forward)
+    const uint32_t results = stages + p.stages * STAGE;
+    const uint32_t bx = WINDOW ? Window::begins(q, x, p.x, first) : 0, bg = WINDOW ? Window::begins(q, gate, p.gate, first) : 0;
+    const uint32_t bd = WINDOW ? Window::begins(q, dh, p.dh, first) : 0, bh = WINDOW ? Window::begins(q, h, p.h, first - 1) : 0;
+    auto value = [&](uint32_t stage, int array, int i) {
+        if constexpr (WINDOW) {
+            const uint32_t n = uint32_t(i), es = Tile::ES;
+            const uint32_t begin = array == 0   ? bx - n * uint32_t(p.x.step) * es
+                                   : array == 1 ? bg - n * uint32_t(p.gate.step) * es
+                                   : array == 2 ? bd - n * uint32_t(p.dh.step) * es
+                                                : bh - n * uint32_t(p.h.step) * es;
+            return Window::read(stage + Window::lane(q) + uint32_t(array * ARRAY + i * Window::PITCH), begin);
+        } else {
+            return lane.read(stage, array, i);
+        }
+    };
     ScanFlags<L, -1> flags;
     if (RESET && q.b < p.B) {
         flags.row = reset + int64_t(q.b) * p.T;
@@ -986,16 +1109,17 @@ scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
     auto fill = [&](int slot, int base) {
         if (base < q.end) {
             const uint32_t to = stages + slot * STAGE;
-            copy.fill(cx, to, last0 - base, 0);
-            copy.fill(cg, to + Tile::ARRAY, last0 - base, 0);
-            copy.fill(cd, to + 2 * Tile::ARRAY, last0 - base, 0);
-            copy.fill(ch, to + 3 * Tile::ARRAY, last0 - base, 1);
+            in_copy.fill(cx, to, last0 - base, 0);
+            in_copy.fill(cg, to + ARRAY, last0 - base, 0);
+            in_copy.fill(cd, to + 2 * ARRAY, last0 - base, 0);
+            in_copy.fill(ch, to + 3 * ARRAY, last0 - base, 1);
         }
         scan_commit();
     };
-    auto drain = [&](int slot, int base) {
-        copy.drain(ox, stages + slot * STAGE, last0 - base, p.T);
-        copy.drain(og, stages + slot * STAGE + Tile::ARRAY, last0 - base, p.T);
+    auto drain = [&](int slot, int round, int base) {
+        const uint32_t from = WINDOW ? results + (round & 1) * 2 * Tile::ARRAY : stages + slot * STAGE;
+        copy.drain(ox, from, last0 - base, p.T);
+        copy.drain(og, from + Tile::ARRAY, last0 - base, p.T);
     };
     for (int k = 0; k < p.stages - 1; ++k) fill(k, q.begin + k * span);
     int now = 0, round = 0;
@@ -1005,10 +1129,10 @@ scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
         // The stage of a round ago, which nobody reads any more: its results go out, a later round comes in.  Between
         // send and receive, where the cluster's answers are waited for; loads that a thread waits for come first.
         auto turn = [&] {
-            if (round > 0) drain(prev, base - span);
+            if (round > 0) drain(prev, round - 1, base - span);
             fill(prev, base + (p.stages - 1) * span);
         };
-        if (CB == 2) turn();
+        if (CB == 2 && !WINDOW) turn();
         const uint32_t stage = stages + now * STAGE;
         const int t0 = last0 - base - q.seg * L;
         uint32_t cut = 0;
@@ -1022,12 +1146,12 @@ scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             float2 e;
-            z[i] = scan_gate<T>(lane.read(stage, 1, i), e);
-            d[i] = lane.read(stage, 2, i);
-            float2 before = lane.read(stage, 3, i);
+            z[i] = scan_gate<T>(value(stage, 1, i), e);
+            d[i] = value(stage, 2, i);
+            float2 before = value(stage, 3, i);
             if (!full && t0 == i) before = scan_state(p, q, h0);
             if (RESET && (cut >> i & 1u)) before = both(0.f);
-            w[i] = mul2(scan_slope(e, z[i]), fma2(before, both(-1.f), lane.read(stage, 0, i)));
+            w[i] = mul2(scan_slope(e, z[i]), fma2(before, both(-1.f), value(stage, 0, i)));
         }
         if (!full) {
 #pragma unroll
@@ -1044,8 +1168,9 @@ scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
         }
         if (RESET && cut != 0) A = both(-1.f);
         ex.send<RESET>(q, round, A, H);
-        if (CB != 2) turn();
+        if (CB != 2 || WINDOW) turn();
         float2 st = ex.receive<RESET>(q, round, A, H, state);
+        const uint32_t out = WINDOW ? results + (round & 1) * 2 * Tile::ARRAY : stage;
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             const float2 f = add2(d[i], st);
@@ -1053,14 +1178,14 @@ scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
             st = mul2(one_minus(z[i]), f);
             if (RESET && (cut >> i & 1u)) st = both(0.f);
             if (!full && t0 - i >= len) a = g = both(0.f);
-            lane.write(stage, 0, i, a);
-            lane.write(stage, 1, i, g);
+            lane.write(out, 0, i, a);
+            lane.write(out, 1, i, g);
         }
         now = now + 1 == p.stages ? 0 : now + 1;
     }
     if (round > 0) {
         __syncthreads();
-        drain(now == 0 ? p.stages - 1 : now - 1, q.begin + (round - 1) * span);
+        drain(now == 0 ? p.stages - 1 : now - 1, round - 1, q.begin + (round - 1) * span);
     }
     if (q.end == p.T) scan_store(p, q, dh0, state);
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -1111,12 +1236,15 @@ ScanPlan scan_plan(const conv_scan_desc_t& e, const DevInfo& d, bool bwd, int ch
     p.L = es == 2 ? (bwd ? 8 : 16) : bwd ? 4 : 8;
     p.wx_log = std::min(3, log2_up((int64_t(e.D) + 7) / 8));
     p.by_log = 3 - p.wx_log;
+    // Whole pieces of memory or copies of single values (5 x 2048, us): fp32, 777 channels, backward 60 / 91, forward
+    // 30 / 38; bf16, 777, backward 60 / 70, forward 21 / 35.  Pairs of bf16 values stay copies: 778, backward 58 / 40.
+    p.window = p.by_log == 0 && p.CB == es;
     p.tiles = int((int64_t(e.D) + (8 << p.wx_log) - 1) / (8 << p.wx_log));
     const int64_t blocks = int64_t(p.tiles) * ((int64_t(e.B) + (1 << p.by_log) - 1) >> p.by_log);
     const int64_t rounds = (int64_t(e.T) + SCAN_SEGS * p.L - 1) / (SCAN_SEGS * p.L);
     // Blocks along time: fewer rounds each, as far as the blocks fit the GPU.  A round takes a block's latencies (as
     // long as 1.5 blocks' instructions) and the instructions of all blocks of its SM.
-    const int fit = es == 2 ? 2 : 3;
+    const int fit = es == 2 || p.window ? 2 : 3;
     int log_c = 0;
     double best = 0;
     for (int k = 0; k <= 3 && (k == 0 || (int64_t(1) << (k - 1)) < rounds); ++k) {
@@ -1132,17 +1260,18 @@ ScanPlan scan_plan(const conv_scan_desc_t& e, const DevInfo& d, bool bwd, int ch
     p.piece = e.T;
     p.threads = SCAN_THREADS;
     p.blocks = blocks << log_c;
-    p.stages = rounds > (int64_t(2) << log_c) ? 3 : 2;
+    p.stages = !p.window && rounds > (int64_t(2) << log_c) ? 3 : 2;
     // Pieces of time, as many as the GPU holds blocks for, of two rounds and more: each is read twice, and a second launch
     // comes on top, which is worth it where a cluster's blocks have some eight rounds more than that.
-    const int64_t most = std::min<int64_t>(int64_t(d.sms) * fit / std::max<int64_t>(1, blocks), rounds / 2);
-    if (most > 8 && rounds >> log_c > 2 * ((rounds + most - 1) / most) + 8) {
+    // (The number of pieces, and so the workspace, does not go by where rows begin.)
+    const int64_t most = std::min<int64_t>(int64_t(d.sms) * 2 / std::max<int64_t>(1, blocks), rounds / 2);
+    if (most > 8 && rounds >> 3 > 2 * ((rounds + most - 1) / most) + 8) {
         const int64_t each = (rounds + most - 1) / most;
         p.cluster = 1;
         p.piece = int(each * SCAN_SEGS * p.L);
         p.pieces = int((rounds + each - 1) / each);
         p.blocks = blocks * p.pieces;
-        p.stages = each > 2 ? 3 : 2;
+        p.stages = !p.window && each > 2 ? 3 : 2;
     }
     return p;
 }
@@ -1158,23 +1287,26 @@ namespace {
 int scan_smem(const ScanPlan& p, int es, bool bwd)
 {
     if (p.walk) return p.ring * RING_STEPS * (bwd ? 4 : 2) * WALK_THREADS * p.V * es;
+    const int rt = SCAN_SEGS * p.L, row = 64 * es, inputs = p.stages * (bwd ? 4 : 2), results = 2 * (bwd ? 2 : 1);
+    const int skew = es == 2 ? 16 : p.L == 4 ? 96 : 32;  // (ScanWindow's)
     return SCAN_LENS + (p.cluster > 1 ? SCAN_WARPS * 16 + 2 * p.cluster * SCAN_WARPS * 64 : 0) +
-           p.stages * (bwd ? 4 : 2) * SCAN_SEGS * p.L * 64 * es;
+           (p.window ? inputs * (rt * (row + 16) + SCAN_SEGS * skew) + results * rt * row : inputs * rt * row);
 }
 
 template <int N> using Int = std::integral_constant<int, N>;
 
-// Calls f(T(), L, CB, RESET), the last three as types, for the plan of a call in parts, and g(T(), V, L, RESET) or
+// Calls f(T(), L, CB, WINDOW, RESET), the last four as types, for the plan of a call in parts, and g(T(), V, L, RESET) or
 // ring(T(), V, RING, RESET) for one that walks.
 template <bool BWD, class F, class G, class H>
 cudaError_t scan_with(const ScanPlan& p, int dt, bool reset, F&& f, G&& g, H&& ring)
 {
     auto parts = [&](auto t, auto r) {
         using L = Int<sizeof(t) == 2 ? (BWD ? 8 : 16) : BWD ? 4 : 8>;
-        if (p.CB == 16) return f(t, L(), Int<16>(), r);
+        if (p.CB == 16) return f(t, L(), Int<16>(), std::false_type(), r);
+        if (p.window) return f(t, L(), Int<sizeof(t)>(), std::true_type(), r);
         if constexpr (sizeof(t) == 2)
-            if (p.CB == 2) return f(t, L(), Int<2>(), r);
-        return f(t, L(), Int<4>(), r);
+            if (p.CB == 2) return f(t, L(), Int<2>(), std::false_type(), r);
+        return f(t, L(), Int<4>(), std::false_type(), r);
     };
     auto walk = [&](auto t, auto r) {
         auto steps = [&](auto v) {
@@ -1226,7 +1358,7 @@ cudaError_t run_scan_fwd(const conv_scan_desc_t& e, const DevInfo& d, const void
     const dim3 grid(unsigned(p.blocks)), block(p.threads);
     return scan_with<false>(
         p, e.dtype, reset != nullptr,
-        [&](auto t, auto l, auto cb, auto r) {
+        [&](auto t, auto l, auto cb, auto window, auto r) {
             using T = decltype(t);
             constexpr int L = decltype(l)::value, CB = decltype(cb)::value;
             constexpr bool RESET = decltype(r)::value;
@@ -1235,7 +1367,7 @@ cudaError_t run_scan_fwd(const conv_scan_desc_t& e, const DevInfo& d, const void
                 const cudaError_t err = launch_totals<T, L, CB, RESET, 1>(p, px, pg, nullptr, h0, reset, lengths, pieces, s);
                 if (err != cudaSuccess) return err;
             }
-            constexpr auto kern = scan_part_fwd<T, L, CB, RESET>;
+            constexpr auto kern = scan_part_fwd<T, L, CB, decltype(window)::value, RESET>;
             const cudaError_t err = ensure_smem<kern>(smem);
             if (err != cudaSuccess) return err;
             return launch_ex(kern, grid, block, smem, s, p.cluster, true, p, px, pg, h0, reset, lengths,
@@ -1270,7 +1402,7 @@ cudaError_t run_scan_bwd(const conv_scan_desc_t& e, const DevInfo& d, const void
     const dim3 grid(unsigned(p.blocks)), block(p.threads);
     return scan_with<true>(
         p, e.dtype, reset != nullptr,
-        [&](auto t, auto l, auto cb, auto r) {
+        [&](auto t, auto l, auto cb, auto window, auto r) {
             using T = decltype(t);
             constexpr int L = decltype(l)::value, CB = decltype(cb)::value;
             constexpr bool RESET = decltype(r)::value;
@@ -1279,7 +1411,7 @@ cudaError_t run_scan_bwd(const conv_scan_desc_t& e, const DevInfo& d, const void
                 const cudaError_t err = launch_totals<T, L, CB, RESET, -1>(p, nullptr, pg, pd, dlast, reset, lengths, pieces, s);
                 if (err != cudaSuccess) return err;
             }
-            constexpr auto kern = scan_part_bwd<T, L, CB, RESET>;
+            constexpr auto kern = scan_part_bwd<T, L, CB, decltype(window)::value, RESET>;
             const cudaError_t err = ensure_smem<kern>(smem);
             if (err != cudaSuccess) return err;
             return launch_ex(kern, grid, block, smem, s, p.cluster, true, p, static_cast<const T*>(x), pg,

@@ -127,6 +127,7 @@ struct ScanPlan {
     int V, cols;                 // walk: channels of a thread, threads of a row
     int L, ring;                 // steps a thread reads at once; of a stretch.  ring: groups of steps in shared memory
     int CB, stages;              // parts: bytes of a copy, rounds in shared memory
+    bool window;                 // parts: rows that begin anywhere, read by whole pieces of memory
     int wx_log, by_log, tiles;   // parts: a block's warps over channels and batch rows, blocks over the channels
     int cluster, threads;
     int pieces, piece;           // parts: of time, steps of one
