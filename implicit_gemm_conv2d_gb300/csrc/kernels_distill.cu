@@ -462,11 +462,12 @@ cudaError_t launch_distill(const DistillPlan& p, DistillParams a, const void* z,
         return launch_ex(kern, dim3(unsigned(p.blocks)), dim3(p.threads), p.smem, s, p.cluster, true, a,
                          static_cast<const T*>(z), weight, zmax, zlog, loss, static_cast<T*>(dz));
     };
+    const int room = p.smem + 1024;  // (the static part comes on top of the dynamic one)
     if (p.warp) {
-        const cudaError_t e = ensure_smem<distill_kernel<T, MODE, true>>(p.smem);
+        const cudaError_t e = ensure_smem<distill_kernel<T, MODE, true>>(room);
         return e != cudaSuccess ? e : go(distill_kernel<T, MODE, true>);
     }
-    const cudaError_t e = ensure_smem<distill_kernel<T, MODE, false>>(p.smem);
+    const cudaError_t e = ensure_smem<distill_kernel<T, MODE, false>>(room);
     return e != cudaSuccess ? e : go(distill_kernel<T, MODE, false>);
 }
 

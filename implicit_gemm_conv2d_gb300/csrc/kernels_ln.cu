@@ -361,7 +361,7 @@ ln_bwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* dy, const
               const float* rstd, const T* dtotal, T* dx, float* part)
 {
     // the rows' sums, twice in turn; [stage][row][x, dy, dtotal][NV][thread] vectors; what the chains of additions have
-    // left so far
+    // left so far, where a block has several teams (one team's goes to the workspace)
     extern __shared__ __align__(16) float dyn[];
     constexpr int VE = ln_ve<T>(), CPT = NV * VE, P = CPT / 2, R = ln_rows(NV);
     float* const tiles = dyn + 2 * LN_SUMS;
@@ -379,9 +379,28 @@ ln_bwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* dy, const
     for (int i = 0; i < NV; ++i) w.params(g[i], gamma, i, 1.f);
 #pragma unroll
     for (int c = 0; c < P; ++c) dg[c] = db[c] = both(0.f);
-    if (p.flush)
+    float* const to = part + int64_t(blockIdx.x) * 2 * p.D;
+    if (p.flush && q.teams > 1)
         for (int k = 0; k < 2 * P; ++k) left[k * int(blockDim.x) + int(threadIdx.x)] = both(0.f);
+    bool begun = false;  // there are sums in the workspace
+    auto hand_over = [&] {
+#pragma unroll
+        for (int c = 0; c < CPT; ++c) {
+            if (!w.in(c / VE) || !w.has(c / VE, c % VE)) continue;
+            float *a = to + w.column(c / VE) + c % VE, *b = a + p.D;
+            const float u = c & 1 ? dg[c / 2].y : dg[c / 2].x, v = c & 1 ? db[c / 2].y : db[c / 2].x;
+            *a = begun ? *a + u : u;
+            *b = begun ? *b + v : v;
+        }
+        begun = true;
+    };
     auto flush = [&] {
+        if (q.teams == 1) {
+            hand_over();
+#pragma unroll
+            for (int c = 0; c < P; ++c) dg[c] = db[c] = both(0.f);
+            return;
+        }
 #pragma unroll
         for (int c = 0; c < P; ++c) {
             float2* a = left + 2 * c * int(blockDim.x) + int(threadIdx.x);
@@ -482,13 +501,17 @@ ln_bwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* dy, const
             }
         }
         chain += R;
-        if (p.flush && chain >= LN_FLUSH) {
+        if (p.flush && part && chain >= LN_FLUSH) {
             flush();
             chain = 0;
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (!part) return;
+    if (q.teams == 1) {
+        hand_over();
+        return;
+    }
     if (p.flush) {
         flush();
 #pragma unroll
@@ -497,18 +520,6 @@ ln_bwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* dy, const
             dg[c] = a[0];
             db[c] = a[blockDim.x];
         }
-    }
-    float* to = part + int64_t(blockIdx.x) * 2 * p.D;
-    if (q.teams == 1) {
-#pragma unroll
-        for (int c = 0; c < CPT; ++c) {
-            const int col = w.column(c / VE) + c % VE;
-            if (w.in(c / VE) && w.has(c / VE, c % VE)) {
-                to[col] = c & 1 ? dg[c / 2].y : dg[c / 2].x;
-                to[p.D + col] = c & 1 ? db[c / 2].y : db[c / 2].x;
-            }
-        }
-        return;
     }
     // Teams of a warp and less: one team of each warp after the other into the warp's columns (teams begin their
     // vectors at other columns, where rows do), then over the warps.
@@ -723,7 +734,7 @@ namespace {
 int ln_smem(const LnParams& p, int ve)
 {
     const int threads = p.TL * p.teams, stages = 2 * p.R * 3 * p.NV * threads * 16;
-    return 8 * LN_SUMS + std::max(stages + (p.flush ? 2 * p.NV * ve * threads * 4 : 0), p.teams > 1 ? threads / 32 * 2 * p.D * 4 : 0);
+    return 8 * LN_SUMS + std::max(stages + (p.flush && p.teams > 1 ? 2 * p.NV * ve * threads * 4 : 0), p.teams > 1 ? threads / 32 * 2 * p.D * 4 : 0);
 }
 
 // The blocks of columns and rows of a long row's second kernel.
@@ -755,7 +766,7 @@ cudaError_t run_ln_fwd(const conv_ln_desc_t& e, const DevInfo& d, const void* x,
         constexpr bool EDGE = decltype(edge)::value;
         auto team = [&](auto nv) {
             constexpr auto kern = ln_fwd_kernel<T, decltype(nv)::value, EDGE>;
-            const cudaError_t bad = ensure_smem<kern>(smem);
+            const cudaError_t bad = ensure_smem<kern>(smem > 0 ? smem + 1024 : 0);  // (and the static part)
             return bad != cudaSuccess ? bad : go(kern, t);
         };
         return p.NV == 1 ? team(Int<1>()) : p.NV == 2 ? team(Int<2>()) : p.NV == 4 ? team(Int<4>()) : team(Int<8>());

@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(WALK_THREADS)
 scan_ring_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, const float* h0, const uint8_t* reset,
               const int32_t* lengths, T* h, float* last)
 {
-    extern __shared__ __align__(16) uint8_t sm[];
+    extern __shared__ __align__(128) uint8_t sm[];
     constexpr int SIZE = V * int(sizeof(T)), LINE = WALK_THREADS * SIZE, GROUP = RING_STEPS * 2 * LINE;
     tc::grid_dep_wait();
     tc::grid_dep_launch();
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(WALK_THREADS)
 scan_ring_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, const T* h, const T* dh, const float* h0,
               const float* dlast, const uint8_t* reset, const int32_t* lengths, T* dx, T* dgate, float* dh0)
 {
-    extern __shared__ __align__(16) uint8_t sm[];
+    extern __shared__ __align__(128) uint8_t sm[];
     constexpr int SIZE = V * int(sizeof(T)), LINE = WALK_THREADS * SIZE, GROUP = RING_STEPS * 4 * LINE;
     tc::grid_dep_wait();
     tc::grid_dep_launch();

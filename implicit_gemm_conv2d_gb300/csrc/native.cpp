@@ -9,6 +9,7 @@
 #include <vector>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -122,6 +123,11 @@ conv_stream_t stream_of(const at::Tensor& t)
 at::Tensor workspace(size_t bytes, const at::Tensor& like)
 {
     return bytes ? at::empty({int64_t(bytes)}, like.options().dtype(at::kByte)) : at::Tensor();
+}
+// An output on x's device, past the dispatcher: 0.4 us less each, and a small norm has four.
+at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType dtype, const at::Tensor& x)
+{
+    return at::Tensor(at::detail::empty_cuda(sizes, dtype, x.device(), std::nullopt));
 }
 void* address(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 const void* address(const at::Tensor* t) { return t ? t->data_ptr() : nullptr; }
@@ -305,12 +311,12 @@ PyObject* layer_norm(PyObject* const* a)
     const at::Tensor* beta = channels(a[2], "beta", x, d.D);
     const at::Tensor* residual = optional(a[3], "residual");
     if (residual) same(*residual, "residual", x.sizes(), x.scalar_type(), x.device());
-    at::Tensor y = at::empty(x.sizes(), x.options()), total, mean, rstd;
-    if (residual) total = at::empty(x.sizes(), x.options());
+    at::Tensor y = fresh(x.sizes(), x.scalar_type(), x), total, mean, rstd;
+    if (residual) total = fresh(x.sizes(), x.scalar_type(), x);
     if (PyObject_IsTrue(a[6])) {
         const auto rows = x.sizes().slice(0, size_t(x.dim() - 1));
-        if (!d.rms) mean = at::empty(rows, x.options().dtype(at::kFloat));
-        rstd = at::empty(rows, x.options().dtype(at::kFloat));
+        if (!d.rms) mean = fresh(rows, at::kFloat, x);
+        rstd = fresh(rows, at::kFloat, x);
     }
     check(conv_ln_fwd(&d, x.data_ptr(), address(residual), address(gamma), address(beta), y.data_ptr(), address(total),
                       static_cast<float*>(address(mean)), static_cast<float*>(address(rstd)), stream_of(x)),
@@ -331,13 +337,13 @@ PyObject* layer_norm_bwd(PyObject* const* a)
     const at::Tensor& rstd = same(tensor(a[4], "rstd"), "rstd", rows, at::kFloat, x.device());
     const at::Tensor* dtotal = optional(a[5], "dtotal");
     if (dtotal) same(*dtotal, "dtotal", x.sizes(), x.scalar_type(), x.device());
-    at::Tensor dx = at::empty(x.sizes(), x.options()), dgamma, dbeta;
+    at::Tensor dx = fresh(x.sizes(), x.scalar_type(), x), dgamma, dbeta;
     if (PyObject_IsTrue(a[6])) {
-        dgamma = at::empty({d.D}, x.options());
-        if (mean) dbeta = at::empty({d.D}, x.options());
+        dgamma = fresh({d.D}, x.scalar_type(), x);
+        if (mean) dbeta = fresh({d.D}, x.scalar_type(), x);
     }
     const size_t bytes = conv_ln_bwd_workspace_size(&d);
-    const at::Tensor ws = workspace(bytes, x);
+    const at::Tensor ws = bytes ? fresh({int64_t(bytes)}, at::kByte, x) : at::Tensor();
     check(conv_ln_bwd(&d, x.data_ptr(), dy.data_ptr(), address(gamma), static_cast<const float*>(address(mean)),
                       static_cast<const float*>(rstd.data_ptr()), address(dtotal), dx.data_ptr(), address(dgamma),
                       address(dbeta), address(ws), bytes, stream_of(x)),
@@ -407,11 +413,11 @@ PyObject* gated_scan(PyObject* const* a)
     const int32_t* lengths = row_lengths(a[4], x);
     const at::Tensor *out = optional(a[5], "out"), *into = optional(a[6], "last");
     states(a[6], "last", x);
-    const at::Tensor h = out ? *out : at::empty(x.sizes(), x.options());
+    const at::Tensor h = out ? *out : fresh(x.sizes(), x.scalar_type(), x);
     d.h = rows_of(h, "out", x.sizes(), x.scalar_type(), x.device());
-    const at::Tensor last = into ? *into : at::empty({d.B, d.D}, x.options().dtype(at::kFloat));
+    const at::Tensor last = into ? *into : fresh({d.B, d.D}, at::kFloat, x);
     const size_t bytes = conv_scan_fwd_workspace_size(&d);
-    const at::Tensor ws = workspace(bytes, x);
+    const at::Tensor ws = bytes ? fresh({int64_t(bytes)}, at::kByte, x) : at::Tensor();
     check(conv_scan_fwd(&d, x.data_ptr(), gate.data_ptr(), h0, reset, lengths, h.data_ptr(),
                         static_cast<float*>(last.data_ptr()), address(ws), bytes, stream_of(x)),
           "conv_scan_fwd");
@@ -430,14 +436,14 @@ PyObject* gated_scan_bwd(PyObject* const* a)
     const uint8_t* reset = flags(a[6], x);
     const int32_t* lengths = row_lengths(a[7], x);
     const at::Tensor *ox = optional(a[8], "dx"), *og = optional(a[9], "dgate");
-    const at::Tensor dx = ox ? *ox : at::empty(x.sizes(), x.options());
-    const at::Tensor dgate = og ? *og : at::empty(x.sizes(), x.options());
+    const at::Tensor dx = ox ? *ox : fresh(x.sizes(), x.scalar_type(), x);
+    const at::Tensor dgate = og ? *og : fresh(x.sizes(), x.scalar_type(), x);
     d.dx = rows_of(dx, "dx", x.sizes(), x.scalar_type(), x.device());
     d.dgate = rows_of(dgate, "dgate", x.sizes(), x.scalar_type(), x.device());
     at::Tensor dh0;
-    if (h0) dh0 = at::empty({d.B, d.D}, x.options().dtype(at::kFloat));
+    if (h0) dh0 = fresh({d.B, d.D}, at::kFloat, x);
     const size_t bytes = conv_scan_bwd_workspace_size(&d);
-    const at::Tensor ws = workspace(bytes, x);
+    const at::Tensor ws = bytes ? fresh({int64_t(bytes)}, at::kByte, x) : at::Tensor();
     check(conv_scan_bwd(&d, x.data_ptr(), gate.data_ptr(), h.data_ptr(), dh.data_ptr(), h0, dlast, reset, lengths,
                         dx.data_ptr(), dgate.data_ptr(), static_cast<float*>(address(dh0)), address(ws), bytes,
                         stream_of(x)),
@@ -479,7 +485,7 @@ float* row_values(const at::Tensor* t, const char* name, const at::Tensor& z)
 at::Tensor logit_grads(PyObject* out, const at::Tensor& z, int64_t ld)
 {
     const at::Tensor* t = optional(out, "out");
-    if (!t) return at::empty_strided(z.sizes(), {ld, 1}, z.options());
+    if (!t) return at::Tensor(at::detail::empty_strided_cuda(z.sizes(), {ld, 1}, z.scalar_type(), z.device()));
     if (t->sizes() != z.sizes() || t->scalar_type() != z.scalar_type() || t->device() != z.device() ||
         (t->size(1) > 1 && t->stride(1) != 1) || (t->size(0) > 1 && t->stride(0) != ld))
         value_error("out: z's sizes, dtype, device and distances");
@@ -491,8 +497,7 @@ PyObject* distill(PyObject* const* a)
 {
     const at::Tensor &z = tensor(a[0], "z"), &ids = tensor(a[1], "ids"), &teacher = tensor(a[2], "teacher");
     const conv_distill_desc_t d = distill_desc(z, ids, teacher, number(a[3]));
-    const auto options = z.options().dtype(at::kFloat);
-    const at::Tensor loss = at::empty({d.N}, options), zmax = at::empty({d.N}, options), zlog = at::empty({d.N}, options);
+    const at::Tensor loss = fresh({d.N}, at::kFloat, z), zmax = fresh({d.N}, at::kFloat, z), zlog = fresh({d.N}, at::kFloat, z);
     check(conv_distill_fwd(&d, z.data_ptr(), ids.data_ptr(), teacher.data_ptr(), static_cast<float*>(loss.data_ptr()),
                            static_cast<float*>(zmax.data_ptr()), static_cast<float*>(zlog.data_ptr()), stream_of(z)),
           "conv_distill_fwd");
@@ -521,7 +526,7 @@ PyObject* distill_grad(PyObject* const* a)
     const conv_distill_desc_t d = distill_desc(z, ids, teacher, number(a[5]));
     const float* weight = row_values(optional(a[3], "weight"), "weight", z);
     const double scale = number(a[4]);
-    const at::Tensor loss = at::empty({d.N}, z.options().dtype(at::kFloat)), dz = logit_grads(a[6], z, d.ld);
+    const at::Tensor loss = fresh({d.N}, at::kFloat, z), dz = logit_grads(a[6], z, d.ld);
     check(conv_distill_grad(&d, z.data_ptr(), ids.data_ptr(), teacher.data_ptr(), weight, float(scale),
                             static_cast<float*>(loss.data_ptr()), dz.data_ptr(), stream_of(z)),
           "conv_distill_grad");

@@ -83,7 +83,7 @@ int scan_check(const conv_scan_desc_t* d, bool bwd)
     for (int i = bwd ? 4 : 2; i < used; ++i)
         if (!rows_apart(*rows[i], d->B, d->T, d->D)) return CONV_ERR_DESC;
     const int64_t most = kMax32 - (1 << 20);
-    if (d->B > most || d->T > most || d->D > most || int64_t(d->B) * d->D >= int64_t(1) << 40) return CONV_ERR_UNSUPPORTED;
+    if (d->B > most || d->T > most || d->D > most || int64_t(d->B) * d->D >= int64_t(1) << 37) return CONV_ERR_UNSUPPORTED;
     return CONV_OK;
 }
 

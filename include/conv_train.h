@@ -162,8 +162,8 @@ int conv_ln_bwd(const conv_ln_desc_t* desc, const void* x, const void* dy, const
  * x, gate, h, dh, dx and dgate have the descriptor's dtype and lie anywhere: an array's element
  * (b, t, d) is batch * b + step * t + d elements behind its address, which is a multiple of the
  * element's size.  So x and gate may be halves of one array, and time may be the outer dimension.
- * Distances are >= 0, and an output's rows do not overlap.  h0, last, dlast, dh0: fp32, (B, D)
- * dense. */
+ * Distances are >= 0; an output's rows do not overlap one another, nor any input.  h0, last, dlast,
+ * dh0: fp32, (B, D) dense. */
 typedef struct { int64_t batch, step; } conv_rows_t;
 
 typedef struct {
@@ -173,7 +173,7 @@ typedef struct {
     conv_rows_t dh, dx, dgate;  /* backward only                                           */
 } conv_scan_desc_t;
 
-/* Limits: B, T, D < 2^31 - 2^20, B * D < 2^40.  B = 0 does nothing.  h0, reset, lengths and last may be NULL. */
+/* Limits: B, T, D < 2^31 - 2^20, B * D < 2^37.  B = 0 does nothing.  h0, reset, lengths and last may be NULL. */
 size_t conv_scan_fwd_workspace_size(const conv_scan_desc_t* desc);
 int conv_scan_fwd(const conv_scan_desc_t* desc, const void* x, const void* gate, const float* h0, const uint8_t* reset,
                   const int32_t* lengths, void* h, float* last, void* workspace, size_t workspace_bytes,
@@ -196,7 +196,8 @@ int conv_scan_bwd(const conv_scan_desc_t* desc, const void* x, const void* gate,
  * with the label id_0 at tau = 1.  An entry whose id is outside [0, V), or whose teacher's logit is
  * -infinity, counts for nothing; a row without entries that count has loss 0 and dz 0, and one of weight 0
  * has dz 0, whatever z holds there.  An id may occur more than once in a row.  z may hold -infinity
- * (P is 0 there); a row that holds nothing else, +infinity or NaN gives NaN and leaves the other rows alone.
+ * (P is 0 there); a row that holds nothing else, +infinity or NaN gives NaN and leaves the other rows alone,
+ * and so does a teacher's logit of +infinity or NaN, in the loss and in dz at the row's ids.
  *
  * z, dz: (N, V), a row's logits one behind the other, rows ld elements apart (ld >= V; dz is
  * written at the row's V elements only), of the descriptor's dtype.  ids, teacher: (N, K) dense,

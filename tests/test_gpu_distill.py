@@ -73,6 +73,28 @@ def test_types_of_the_teacher(size, index, teacher):
     all_ways(z, ids, q, w, 1.0, "bf16", f"{size} {index} {teacher}")
 
 
+@pytest.mark.parametrize("size", [(40, 796, 152), (700, 11516, 64), (700, 11500, 65), (9, 23000, 33)], ids=str)
+def test_blocks_of_48_kilobytes(size):
+    """Rows whose part in shared memory ends at what a launch may ask for without opting in."""
+    z, ids, q, w = inputs(size, "f32", 11)
+    all_ways(z, ids, q, w, 1.0, "f32", str(size))
+
+
+def test_a_teacher_that_is_not_finite():
+    z, ids, q, w = inputs((6, 900, 5), "f32", 12, pad=0.0)
+    ids = torch.arange(5, device="cuda", dtype=torch.int32).repeat(6, 1) * 100
+    clean = train.distill_grad(z, ids, q, w)
+    q[1, 2], q[4, 0] = float("nan"), float("inf")
+    loss, dz = train.distill_grad(z, ids, q, w)
+    keep = [0, 2, 3, 5]
+    assert torch.equal(loss[keep], clean[0][keep]) and torch.equal(dz[keep], clean[1][keep])
+    assert bool(torch.isnan(loss[[1, 4]]).all())
+    named = torch.zeros(900, dtype=torch.bool, device="cuda")
+    named[::100][:5] = True
+    for row in (1, 4):
+        assert bool(torch.isnan(dz[row][named]).all()) and bool(torch.isfinite(dz[row][~named]).all())
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("V", [130, 4099, 60001])
 def test_rows_apart_and_in_place(V, dtype):

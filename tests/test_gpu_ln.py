@@ -18,7 +18,7 @@ EPS = 1e-5
 
 #     rows, values
 SIZES = [(1, 1), (5, 2), (3, 16), (1000, 16), (257, 33), (96, 512), (130, 100), (70, 1024), (9, 1430), (33, 1023),
-         (12, 2048), (5, 3001), (4, 4094), (3, 8192), (2, 8193), (3, 12000), (2, 70001), (1, 131072), (20011, 24)]
+         (12, 2048), (5, 3001), (4, 4094), (3, 8192), (2, 8193), (3, 12000), (3, 12275), (3, 6140), (2, 70001), (1, 131072), (20011, 24)]
 
 
 def inputs(size, dtype, seed=0, residual=True, offset=0.0):
@@ -78,6 +78,31 @@ def test_against_the_reference(rms, size, dtype):
 @pytest.mark.parametrize("size", [(300_001, 16), (400_000, 24), (150_000, 7), (100_003, 130)], ids=str)
 def test_many_rows(size, dtype):
     both_ways(size, dtype, False)
+
+
+@pytest.mark.parametrize("D", [4104, 6001, 8192])
+def test_many_long_rows(D):
+    """Rows of one team a block, so many that a thread's sums are handed over in between."""
+    N = 45_000
+    g = torch.Generator(device="cuda").manual_seed(D)
+    x, dy = (torch.empty((N, D), device="cuda", dtype=torch.bfloat16).normal_(generator=g) for _ in range(2))
+    gamma = 1 + 0.2 * torch.randn(D, device="cuda", generator=g).bfloat16()
+    _, _, mean, rstd = train.layer_norm(x, gamma)
+    dx, dgamma, dbeta = train.layer_norm_bwd(x, dy, gamma, mean, rstd)
+    dg, db, mg, mb = (torch.zeros(D, dtype=torch.float64, device="cuda") for _ in range(4))
+    for a in range(0, N, 5000):
+        xh = (x[a:a + 5000].double() - mean[a:a + 5000, None]) * rstd[a:a + 5000, None]
+        y = dy[a:a + 5000].double()
+        dg += (y * xh).sum(0)
+        db += y.sum(0)
+        mg += (y * xh).abs().sum(0)
+        mb += y.abs().sum(0)
+    # chains of 256, of 2 of those and of the blocks' sums, and xhat's three roundings
+    for got, want, size in ((dgamma, dg, mg), (dbeta, db, mb)):
+        room = (256 + 2 + 152 + 16) * seq_ref.U * size + seq_ref.HALF_STEP["bf16"] * want.abs()
+        assert bool(((got.double() - want).abs() <= room).all())
+    refs = seq_ref.ln_bwd(to_np(x[-3:]), to_np(dy[-3:]), to_np(gamma), to_np(mean[-3:]), to_np(rstd[-3:]), None, False)
+    within(dx[-3:], *refs[0], "bf16", "dx")
 
 
 def test_sums_over_equal_rows():

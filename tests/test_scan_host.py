@@ -41,6 +41,7 @@ def bwd(L, d, x=OK, gate=OK, h=OK, dh=OK, h0=None, dlast=None, lengths=None, dx=
 
 @pytest.mark.parametrize("bad,code", [(dict(B=-1), -2), (dict(T=-1), -2), (dict(D=0), -2), (dict(dtype=2), -2),
                                       (dict(B=2 ** 31 - 1), -3), (dict(T=2 ** 31 - 1, B=1), -3),
+                                      (dict(B=1 << 20, D=1 << 17, rows={n: (1 << 21, 1 << 17) for n in ARRAYS}), -3),
                                       (dict(rows=dict(x=(-60, 6))), -2), (dict(rows=dict(gate=(60, -6))), -2),
                                       (dict(rows=dict(x=(1 << 62, 6))), -3)])
 def test_descriptor_refused(L, bad, code):
