@@ -630,13 +630,13 @@ uint64_t conv_fastdivmod_check(uint32_t d, uint32_t lo, uint32_t hi)
 int conv_device_status(uint32_t* status, int reset)
 {
     if (!status) return CONV_ERR_NULL;
-    unsigned v = 0, w = 0, u = 0;
+    unsigned v = 0, w = 0, u = 0, t = 0;
     if (tc_read_status(&v, reset != 0) != cudaSuccess || diag_read_status(&w, reset != 0) != cudaSuccess ||
-        scan_read_status(&u, reset != 0) != cudaSuccess) {
+        scan_read_status(&u, reset != 0) != cudaSuccess || distill_read_status(&t, reset != 0) != cudaSuccess) {
         cudaGetLastError();
         return CONV_ERR_CUDA;
     }
-    *status = v | w | u;
+    *status = v | w | u | t;
     return CONV_OK;
 }
 

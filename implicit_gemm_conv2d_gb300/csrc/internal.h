@@ -185,8 +185,10 @@ cudaError_t tc_read_status(unsigned* out, bool reset);
 // mbarrier runs out and sets CONV_STATUS_WAIT_SELFTEST in its own status word.
 cudaError_t run_wait_selftest(unsigned max_sleeps, cudaStream_t s);
 cudaError_t diag_read_status(unsigned* out, bool reset);
-// The same of the gated scan's waits along a cluster (kernels_scan.cu).
+// The same of the gated scan's waits along a cluster (kernels_scan.cu), and of the loss's for its copies
+// (kernels_distill.cu).
 cudaError_t scan_read_status(unsigned* out, bool reset);
+cudaError_t distill_read_status(unsigned* out, bool reset);
 
 __host__ __device__ inline int round_up(int a, int b) { return (a + b - 1) / b * b; }
 // (on the host for every a >= 0, b > 0; on the device a + b stays below 2^31)

@@ -6,7 +6,7 @@
 // One pass over a row keeps the running maximum m and the sum of exp((z - m) / tau); a row is one warp's
 // (short ones), a block's, or that of a cluster of up to 8 blocks, each with a part of the vocabulary, whose
 // (m, sum) travel through distributed shared memory.  The loss with its gradient reads z once: a block's part
-// of the row waits in shared memory, at the threads that read it, for the row's sum, and goes out as
+// of the row comes to shared memory in a few large copies, waits there for the row's sum, and goes out as
 // dz.  Rows begin anywhere: a row is taken by 16-byte vectors of memory, its first and last one by
 // elements.
 //
@@ -26,15 +26,22 @@ namespace {
 enum { DISTILL_FWD = 0, DISTILL_BWD = 1, DISTILL_GRAD = 2 };
 constexpr int DISTILL_WARPS = 8;       // that sweep a row, where a block does
 constexpr int DISTILL_UNROLL = 4;      // vectors a thread has on their way
+constexpr int DISTILL_COPIES = 4;      // of a block's part of a row, one behind the other
+
+__device__ unsigned g_distill_status = 0;  // CONV_STATUS_DISTILL: a bounded wait ran out
 
 struct Stat { float m, s; };
 
 // m: of both, or 0 while all values are -inf (so that nothing is subtracted from them).
 __device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.f : m; }
-__device__ __forceinline__ Stat stat_join(Stat a, Stat b, float k)
+// Over groups of `lanes` lanes (a power of two): the largest m, and the sums brought to it.
+__device__ __forceinline__ Stat stat_join(Stat a, int lanes, float k)
 {
-    const float m = fmaxf(a.m, b.m), f = finite_base(m);
-    return {m, a.s * fast_exp2((a.m - f) * k) + b.s * fast_exp2((b.m - f) * k)};
+    float m = a.m;
+    for (int o = lanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    float s = a.s * fast_exp2((a.m - finite_base(m)) * k);
+    for (int o = lanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    return {m, s};
 }
 
 // A row's place: 16-byte vectors from `base` on; vector j holds the row's elements j * VE - off and on.
@@ -151,15 +158,15 @@ struct Teacher {
         const float base = finite_base(top);
         float sum = 0.f;
         for (int k = lane; k < a.K; k += 32) {
-            zk[k] = __fdiv_rn(p[k] - base, a.tau);  // log p but for the sum
+            zk[k] = (p[k] - base) * a.inv_tau;  // log p but for the sum
             const float e = expf(zk[k]);
             p[k] = e;
             sum += e;
         }
         sum = warp_sum(sum);
-        const float log_sum = logf(sum);
+        const float log_sum = logf(sum), over = __fdiv_rn(1.f, sum);
         for (int k = lane; k < a.K; k += 32) {
-            p[k] = __fdiv_rn(p[k], sum);
+            p[k] *= over;
             total[k] = zk[k] - log_sum;  // log p, until it is needed no more
         }
         return true;
@@ -173,7 +180,7 @@ struct Teacher {
     {
         float sum = 0.f;
         for (int k = lane; k < a.K; k += 32)
-            if (!(p[k] == 0.f)) sum += p[k] * (total[k] - (__fdiv_rn(zk[k] - m, a.tau) - log_s));
+            if (!(p[k] == 0.f)) sum += p[k] * (total[k] - ((zk[k] - m) * a.inv_tau - log_s));
         return a.tau * a.tau * warp_sum(sum);
     }
     // total: the sum of p over the entries of an id, at the first of them.  Ids that share a bit of `seen` are
@@ -217,6 +224,7 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
     extern __shared__ __align__(16) uint8_t sm[];
     __shared__ Stat parts[DISTILL_WARPS + 8];
     __shared__ int none;
+    __shared__ __align__(8) uint64_t bars[DISTILL_COPIES];
     constexpr int VE = RowAt<T>::VE, U = DISTILL_UNROLL;
     const int lane = int(threadIdx.x) & 31, warp = int(threadIdx.x) >> 5;
     const int C = WARP ? 1 : a.cluster, rank = WARP ? 0 : int(blockIdx.x) % C;
@@ -240,6 +248,28 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
     uint8_t* const stage = sm + (WARP ? a.rows : 1) * Teacher::bytes(a.K, a.bits) +
                            (WARP ? warp * a.stage_bytes : 0);  // vector j - j0 at the thread that reads it
     const bool staged = MODE == DISTILL_GRAD && a.stage_bytes > 0;
+    // A block's part of the row comes in a few large copies; `copy` vectors each.
+    const int copy = (max(0, w1 - w0) + DISTILL_COPIES * step - 1) / (DISTILL_COPIES * step) * step;
+    if (!WARP && staged) {
+        if (threadIdx.x == 0) {
+            for (int k = 0; k < DISTILL_COPIES; ++k) tc::mbar_init(tc::smem_u32(&bars[k]), 1);
+            tc::fence_mbar_init();
+            for (int k = 0; k < DISTILL_COPIES; ++k) {
+                const int from = w0 + k * copy, n = min(copy, w1 - from);
+                if (n <= 0) break;
+                tc::mbar_arrive_expect_tx(tc::smem_u32(&bars[k]), uint32_t(n) * 16u);
+                tc::bulk_g2s(tc::smem_u32(stage) + uint32_t(from - j0) * 16u, z + row.first + int64_t(from) * VE,
+                             uint32_t(n) * 16u, tc::smem_u32(&bars[k]));
+            }
+        }
+        __syncthreads();
+    }
+
+    const uint32_t staged_at = tc::smem_u32(stage) - uint32_t(j0) * 16;
+    auto waiting = [&](Vec<T, VE>& v, int j) {  // vector j, in shared memory
+        const int4 q = tc::lds128(staged_at + uint32_t(j) * 16);
+        v.r.w[0] = uint32_t(q.x); v.r.w[1] = uint32_t(q.y); v.r.w[2] = uint32_t(q.z); v.r.w[3] = uint32_t(q.w);
+    };
 
     // ---- the teacher's entries, and what the first sweep finds
     bool empty = false;
@@ -261,13 +291,14 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
     } else {
         if (teaches) teach();
         Stat st = {-INFINITY, 0.f};
+        bool edged = false;  // the vector is one that no copy brought
         auto take = [&](auto& v, int j) {  // vectors j, j + step, ..
             constexpr int count = int(sizeof(v) / sizeof(v[0]));
             float top = st.m;
 #pragma unroll
             for (int u = 0; u < count; ++u) {
                 top = fmaxf(top, vec_max<T, VE>(v[u]));
-                if (staged) v[u].store(reinterpret_cast<T*>(stage + (j + u * step - j0) * 16));
+                if (staged && (WARP || edged)) v[u].store(reinterpret_cast<T*>(stage + (j + u * step - j0) * 16));
             }
             const float base = finite_base(top);
             if (top > st.m) st.s *= fast_exp2((st.m - base) * a.k);
@@ -279,36 +310,45 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
             Vec<T, VE> one[1];
             if (edge >= 0) {
                 one[0] = row.load(z, edge);
+                edged = true;
                 take(one, edge);
+                edged = false;
             }
-            const T* src = z + row.first + int64_t(w0 + me) * VE;
-            int j = w0 + me;
-            for (; j + (U - 1) * step < w1; j += U * step, src += U * step * VE) {
-                Vec<T, VE> v[U];
+            auto all = [&](int from, int to, auto&& read) {
+                int j = from + me;
+                for (; j + (U - 1) * step < to; j += U * step) {
+                    Vec<T, VE> v[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u) v[u].load(src + u * step * VE);
-                take(v, j);
-            }
-            for (; j < w1; j += step, src += step * VE) {
-                one[0].load(src);
-                take(one, j);
+                    for (int u = 0; u < U; ++u) read(v[u], j + u * step);
+                    take(v, j);
+                }
+                for (; j < to; j += step) {
+                    read(one[0], j);
+                    take(one, j);
+                }
+            };
+            if (!WARP && staged) {
+                for (int k = 0; k < DISTILL_COPIES && w0 + k * copy < w1; ++k) {
+                    if (!tc::mbar_wait(tc::smem_u32(&bars[k]), 0u))
+                        atomicOr(&g_distill_status, CONV_STATUS_DISTILL);  // the results are wrong, and the status says so
+                    all(w0 + k * copy, min(w1, w0 + (k + 1) * copy), waiting);
+                }
+            } else {
+                const T* src = z + row.first;
+                all(w0, w1, [&](Vec<T, VE>& v, int j) { v.load(src + int64_t(j) * VE); });
             }
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            st = stat_join(st, {__shfl_xor_sync(0xFFFFFFFFu, st.m, o), __shfl_xor_sync(0xFFFFFFFFu, st.s, o)}, a.k);
+        st = stat_join(st, 32, a.k);
         if (!WARP) {
             if (lane == 0 && sweeps) parts[warp] = st;
             __syncthreads();
-            st = parts[0];
-            for (int w = 1; w < DISTILL_WARPS; ++w) st = stat_join(st, parts[w], a.k);
+            st = stat_join(parts[lane & (DISTILL_WARPS - 1)], DISTILL_WARPS, a.k);
             if (C > 1) {
                 tc::cluster_wait();  // every block of the cluster is there
                 if (threadIdx.x < unsigned(C))
                     tc::st_dsmem_f2(tc::dsmem_addr(tc::smem_u32(&parts[DISTILL_WARPS + rank]), threadIdx.x), st.m, st.s);
                 tc::cluster_sync();
-                st = parts[DISTILL_WARPS];
-                for (int r = 1; r < C; ++r) st = stat_join(st, parts[DISTILL_WARPS + r], a.k);
+                st = stat_join(parts[DISTILL_WARPS + (lane & (C - 1))], C, a.k);
             }
         }
         m = st.m;
@@ -371,11 +411,7 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
             }
         };
         if (staged) {
-            const uint32_t at = tc::smem_u32(stage) - uint32_t(j0) * 16;
-            sweep([&](Vec<T, VE>& v, int j) {
-                const int4 q = tc::lds128(at + uint32_t(j) * 16);
-                v.r.w[0] = uint32_t(q.x); v.r.w[1] = uint32_t(q.y); v.r.w[2] = uint32_t(q.z); v.r.w[3] = uint32_t(q.w);
-            });
+            sweep(waiting);
         } else {
             const T* src = z + row.first;
             sweep([&](Vec<T, VE>& v, int j) { v.load(src + int64_t(j) * VE); });
@@ -404,6 +440,7 @@ DistillParams distill_params(const conv_distill_desc_t& e, const void* ids, cons
     a.teacher = teacher;
     a.teacher_bf16 = e.teacher_dtype == CONV_BF16;
     a.tau = e.temperature;
+    a.inv_tau = float(1.0 / double(e.temperature));
     a.k = float(1.4426950408889634 / double(e.temperature));
     a.scale = scale;
     return a;
@@ -499,6 +536,16 @@ cudaError_t run_distill_grad(const conv_distill_desc_t& e, const DevInfo& d, con
 {
     return run_distill<DISTILL_GRAD>(e, d, distill_params(e, ids, teacher, scale), z, weight, nullptr, nullptr, loss, dz,
                                      s);
+}
+
+cudaError_t distill_read_status(unsigned* out, bool reset)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_distill_status, sizeof(unsigned));
+    if (e == cudaSuccess && reset) {
+        const unsigned zero = 0;
+        e = cudaMemcpyToSymbol(g_distill_status, &zero, sizeof(unsigned));
+    }
+    return e;
 }
 
 }  // namespace igc

@@ -147,7 +147,7 @@ struct DistillParams {
     int V, K;
     const void *ids, *teacher;
     bool ids64, teacher_bf16;
-    float tau, k, scale;         // k: log2(e) / tau
+    float tau, inv_tau, k, scale;  // k: log2(e) / tau
     int cluster, rows, bits, stage_bytes;
 };
 struct DistillPlan {

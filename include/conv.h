@@ -340,9 +340,9 @@ int conv_set_algo(int op, int algo);
  * differ from '/' and '%'; (uint64_t)-1 if d is outside [1, 2^31). */
 uint64_t conv_fastdivmod_check(uint32_t d, uint32_t lo, uint32_t hi);
 
-/* Diagnostics: the tensor-core kernels, and the gated scan of conv_train.h where it works
- * on a sequence with a cluster, bound every wait on an mbarrier; a wait
- * that runs out makes the kernel set a bit here (the scan: CONV_STATUS_SCAN), free its
+/* Diagnostics: the tensor-core kernels, and of conv_train.h the gated scan where it works on
+ * a sequence with a cluster and conv_distill_grad, bound every wait on an mbarrier; a wait
+ * that runs out makes the kernel set a bit here (those two CONV_STATUS_SCAN and _DISTILL), free its
  * tensor memory and return (its output is then unspecified).  Reads the word into *status
  * (0 = no timeout since the last reset), and clears it if reset != 0.
  * Synchronises the device. */
@@ -356,6 +356,7 @@ int conv_device_status(uint32_t* status, int reset);
  * usable.  max_sleeps must be in [1, 10^6] (CONV_ERR_UNSUPPORTED otherwise). */
 #define CONV_STATUS_WAIT_SELFTEST (1u << 30)
 #define CONV_STATUS_SCAN (1u << 29)
+#define CONV_STATUS_DISTILL (1u << 28)
 int conv_wait_selftest(uint32_t max_sleeps, conv_stream_t stream);
 
 /* Write `bytes` bytes of `buf` (device memory, 16-byte aligned, bytes a
