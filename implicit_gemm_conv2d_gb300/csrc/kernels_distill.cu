@@ -123,6 +123,7 @@ template <typename T, int VE> __device__ __forceinline__ float vec_sum(const Vec
 struct Teacher {
     int* id;
     float *p, *zk, *total;
+    float top;       // the largest of the teacher's logits
     uint32_t* seen;  // two bitmaps
     int bits;        // of one, a power of two
     static __host__ __device__ int bytes(int K, int bits) { return 16 * K + bits / 4; }
@@ -134,10 +135,10 @@ struct Teacher {
         zk = p + K;
         total = zk + K;
     }
-    // ids and probabilities; false: the row names nothing.
-    __device__ __forceinline__ bool probabilities(const DistillParams& a, int64_t n, int lane)
+    // ids and the teacher's logits; false: the row names nothing.
+    __device__ __forceinline__ bool entries(const DistillParams& a, int64_t n, int lane)
     {
-        float top = -INFINITY;
+        top = -INFINITY;
         bool nan = false;
         for (int k = lane; k < a.K; k += 32) {
             const int64_t at = n * a.K + k;
@@ -154,12 +155,15 @@ struct Teacher {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
         nan = __any_sync(0xFFFFFFFFu, nan);
-        if (top == -INFINITY && !nan) return false;
+        return !(top == -INFINITY && !nan);
+    }
+    __device__ __forceinline__ void probabilities(const DistillParams& a, int lane)
+    {
         const float base = finite_base(top);
         float sum = 0.f;
         for (int k = lane; k < a.K; k += 32) {
-            zk[k] = (p[k] - base) * a.inv_tau;  // log p but for the sum
-            const float e = expf(zk[k]);
+            total[k] = (p[k] - base) * a.inv_tau;  // log p but for the sum, until it is needed no more
+            const float e = expf(total[k]);
             p[k] = e;
             sum += e;
         }
@@ -167,9 +171,17 @@ struct Teacher {
         const float log_sum = logf(sum), over = __fdiv_rn(1.f, sum);
         for (int k = lane; k < a.K; k += 32) {
             p[k] *= over;
-            total[k] = zk[k] - log_sum;  // log p, until it is needed no more
+            total[k] -= log_sum;
         }
-        return true;
+    }
+    // Asks for the entries' lines, which are read later.
+    __device__ __forceinline__ void announce(const DistillParams& a, int64_t n, int lane) const
+    {
+        const int64_t ids = a.K * (a.ids64 ? 8 : 4), qs = a.K * (a.teacher_bf16 ? 2 : 4);
+        for (int64_t k = lane * 128; k < ids + 128; k += 4096)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a.ids) + n * ids + min(k, ids - 1)));
+        for (int64_t k = lane * 128; k < qs + 128; k += 4096)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a.teacher) + n * qs + min(k, qs - 1)));
     }
     // The student's logits of the entries in [lo, hi).
     template <typename T> __device__ __forceinline__ void gather(const DistillParams& a, const T* row, int lo, int hi, int lane)
@@ -187,6 +199,22 @@ struct Teacher {
     // looked at one by one, in order.
     __device__ __forceinline__ void totals(const DistillParams& a, int lane)
     {
+        if (a.K <= 32) {
+            const int me = lane < a.K ? id[lane] : -1;
+            const float mine = lane < a.K ? p[lane] : 0.f;
+            const unsigned same = __match_any_sync(0xFFFFFFFFu, me < 0 ? -1 - lane : me);
+            float t = mine;
+            if (__any_sync(0xFFFFFFFFu, (same & (same - 1)) != 0)) {
+                t = 0.f;
+                for (int j = 0; j < a.K; ++j) {
+                    const float q = __shfl_sync(0xFFFFFFFFu, p[min(lane, a.K - 1)], j);
+                    if (same >> j & 1u) t += q;
+                }
+                if (same & ((1u << lane) - 1u)) t = -1.f;
+            }
+            if (lane < a.K) total[lane] = t;
+            return;
+        }
         uint32_t* twice = seen + bits / 32;
         for (int i = lane; i < bits / 16; i += 32) seen[i] = 0;
         __syncwarp();
@@ -215,7 +243,8 @@ struct Teacher {
     }
 };
 
-// WARP: a warp a row; else a block of DISTILL_WARPS warps and one for the teacher, `cluster` blocks a row.
+// WARP: a warp a row; else a block of `warps` warps, DISTILL_WARPS at most and a power of two, and one for the teacher,
+// `cluster` blocks a row.
 template <typename T, int MODE, bool WARP>
 __global__ void __launch_bounds__(WARP ? 256 : DISTILL_WARPS * 32 + 32)
 distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float* weight, float* zmax, float* zlog,
@@ -229,8 +258,8 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
     const int lane = int(threadIdx.x) & 31, warp = int(threadIdx.x) >> 5;
     const int C = WARP ? 1 : a.cluster, rank = WARP ? 0 : int(blockIdx.x) % C;
     const int64_t n = WARP ? int64_t(blockIdx.x) * a.rows + warp : int64_t(blockIdx.x) / C;
-    const int step = WARP ? 32 : DISTILL_WARPS * 32, me = WARP ? lane : int(threadIdx.x);
-    const bool teaches = WARP || warp == DISTILL_WARPS, sweeps = WARP || !teaches;
+    const int warps = a.warps, step = WARP ? 32 : warps * 32, me = WARP ? lane : int(threadIdx.x);
+    const bool teaches = WARP || warp == warps, sweeps = WARP || !teaches;
     tc::grid_dep_wait();
     tc::grid_dep_launch();
     if (WARP && n >= a.N) return;
@@ -273,23 +302,46 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
 
     // ---- the teacher's entries, and what the first sweep finds
     bool empty = false;
-    auto teach = [&] {
-        empty = !t.probabilities(a, n, lane);
-        if (!empty) {
-            if (MODE == DISTILL_BWD) t.gather(a, zrow, lo, hi, lane);
-            else t.gather(a, zrow, 0, a.V, lane);
-        }
-        if (!WARP && lane == 0) none = empty;
-    };
+    const float w = MODE != DISTILL_FWD && weight ? weight[n] : 1.f;
     float m, log_s;
     if (MODE == DISTILL_BWD) {
         m = zmax[n];
         log_s = zlog[n];
-        if (teaches) teach();
+        const bool in_place = z == dz;
+        if (teaches) {
+            empty = !t.entries(a, n, lane);
+            if (!WARP && lane == 0) none = empty;
+            if (in_place && !empty) t.gather(a, zrow, lo, hi, lane);
+        }
         if (WARP) __syncwarp();
-        else __syncthreads();  // z may be dz
+        else __syncthreads();
+        if (teaches && !empty) {
+            t.probabilities(a, lane);
+            if (!in_place) t.gather(a, zrow, lo, hi, lane);
+        }
+        if (WARP) __syncwarp();
     } else {
-        if (teaches) teach();
+        auto teach = [&](bool here) {  // the row is in the stage
+            empty = !t.entries(a, n, lane);
+            if (!WARP && lane == 0) none = empty;
+            if (empty) return;
+            t.probabilities(a, lane);
+            if (here && staged) t.gather(a, reinterpret_cast<const T*>(stage) + row.off, 0, a.V, lane);
+            else t.gather(a, zrow, 0, a.V, lane);
+        };
+        // A warp that does both begins with the row where that is long (29605 x 1568 bf16 at once 59 / 52 us, 4344 x 197
+        // 7.5 / 9.6).
+        const bool row_first = WARP && row.vecs > 64;
+        Vec<T, VE> early[2];  // a short row's vectors, all on their way beside the teacher's entries
+        if (row_first) {
+            t.announce(a, n, lane);
+        } else {
+            if (WARP)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    if (lane + u * 32 < row.vecs) early[u] = row.load(z, lane + u * 32);
+            if (teaches) teach(false);
+        }
         Stat st = {-INFINITY, 0.f};
         bool edged = false;  // the vector is one that no copy brought
         auto take = [&](auto& v, int j) {  // vectors j, j + step, ..
@@ -306,7 +358,12 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
 #pragma unroll
             for (int u = 0; u < count; ++u) st.s += vec_sum<T, VE>(v[u], base, a.k);
         };
-        if (sweeps) {
+        if (WARP && !row_first) {
+            edged = true;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (lane + u * 32 < row.vecs) take(reinterpret_cast<Vec<T, VE>(&)[1]>(early[u]), lane + u * 32);
+        } else if (sweeps) {
             Vec<T, VE> one[1];
             if (edge >= 0) {
                 one[0] = row.load(z, edge);
@@ -338,11 +395,15 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
                 all(w0, w1, [&](Vec<T, VE>& v, int j) { v.load(src + int64_t(j) * VE); });
             }
         }
+        if (row_first) {
+            __syncwarp();
+            teach(true);
+        }
         st = stat_join(st, 32, a.k);
         if (!WARP) {
             if (lane == 0 && sweeps) parts[warp] = st;
             __syncthreads();
-            st = stat_join(parts[lane & (DISTILL_WARPS - 1)], DISTILL_WARPS, a.k);
+            st = stat_join(parts[lane & (warps - 1)], warps, a.k);
             if (C > 1) {
                 tc::cluster_wait();  // every block of the cluster is there
                 if (threadIdx.x < unsigned(C))
@@ -368,7 +429,7 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
 
     // ---- the gradient
     if (!WARP) empty = none != 0;
-    const float w = weight ? weight[n] : 1.f, c = a.scale * a.tau * w, log2_s = log_s * kLog2e;
+    const float c = a.scale * a.tau * w, log2_s = log_s * kLog2e;
     const bool zeros = empty || w == 0.f;
     if (teaches && !zeros) t.totals(a, lane);
     if (sweeps) {
@@ -468,7 +529,6 @@ DistillPlan distill_plan(const conv_distill_desc_t& e, const DevInfo& d, int mod
     }
     p.bits = 8192;
     p.rows = 1;
-    p.threads = DISTILL_WARPS * 32 + 32;
     const int64_t teacher = 16 * int64_t(e.K) + p.bits / 4;
     // A row's blocks: as many as give every SM four, while a thread has four vectors and more; and as many as keep a
     // block's part small enough for four on an SM.
@@ -476,9 +536,14 @@ DistillPlan distill_plan(const conv_distill_desc_t& e, const DevInfo& d, int mod
     while (C < 8 && e.N * C < 4 * int64_t(d.sms) && vecs >= int64_t(C) * 2 * DISTILL_WARPS * 32 * 4) C *= 2;
     if (mode == DISTILL_GRAD) {
         while (C < 8 && (vecs + C - 1) / C * 16 + teacher > 55 * 1024) C *= 2;
-        const int64_t part = (vecs + C - 1) / C * 16;
-        p.stage_bytes = part + teacher <= most ? int(part) : 0;
+        const int64_t bytes = (vecs + C - 1) / C * 16;
+        p.stage_bytes = bytes + teacher <= most ? int(bytes) : 0;
     }
+    // Warps that sweep: a thread has eight vectors and more (6319 x 8978 bf16 backward 88 us with 8 warps, 62 with 4; 20000 x
+    // 3000 bf16 at once 136 with 8, 88 with 4, 59 with 2).
+    const int64_t part = (vecs + C - 1) / C;
+    p.warps = part > 2048 ? 8 : part > 512 ? 4 : 2;
+    p.threads = p.warps * 32 + 32;
     p.cluster = C;
     p.smem = int(teacher) + p.stage_bytes;
     p.blocks = e.N * C;
@@ -493,6 +558,7 @@ cudaError_t launch_distill(const DistillPlan& p, DistillParams a, const void* z,
 {
     a.cluster = p.cluster;
     a.rows = p.rows;
+    a.warps = p.warps;
     a.bits = p.bits;
     a.stage_bytes = p.stage_bytes;
     auto go = [&](auto kern) {

@@ -148,11 +148,11 @@ struct DistillParams {
     const void *ids, *teacher;
     bool ids64, teacher_bf16;
     float tau, inv_tau, k, scale;  // k: log2(e) / tau
-    int cluster, rows, bits, stage_bytes;
+    int cluster, rows, warps, bits, stage_bytes;
 };
 struct DistillPlan {
     bool warp;                   // a warp a row
-    int cluster, rows;           // blocks a row, rows a block
+    int cluster, rows, warps;    // blocks a row, rows a block, a block's warps that sweep
     int bits, stage_bytes;       // of an id bitmap; of a block's (a warp's) part of a row in shared memory
     int threads, smem;
     int64_t blocks;
