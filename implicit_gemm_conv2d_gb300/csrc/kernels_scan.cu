@@ -305,18 +305,22 @@ scan_ring_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
     };
     for (int k = 0; k < RING; ++k) fetch(ring + uint32_t(k * GROUP));
     uint32_t at = ring;
-    uint32_t flags = 0;  // of the steps ahead, one group's
+    uint8_t flags[RING_STEPS];  // of the steps ahead, one group's
     auto look = [&](int t) {
-        flags = 0;
         if (RESET)
 #pragma unroll
-            for (int i = 0; i < RING_STEPS; ++i)
-                if (t + i < len && pr[t + i] != 0) flags |= 1u << i;
+            for (int i = 0; i < RING_STEPS; ++i) {
+                flags[i] = 0;
+                if (t + i < len) flags[i] = pr[t + i];
+            }
     };
     look(0);
     for (int t = 0; t < len; t += RING_STEPS) {
         asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
-        const uint32_t cut = flags;
+        uint32_t cut = 0;
+        if (RESET)
+#pragma unroll
+            for (int i = 0; i < RING_STEPS; ++i) cut |= flags[i] != 0 ? 1u << i : 0u;
         float2 keep[RING_STEPS], in[RING_STEPS];
 #pragma unroll
         for (int i = 0; i < RING_STEPS; ++i) {
@@ -382,18 +386,22 @@ scan_ring_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
     };
     for (int k = 0; k < RING; ++k) fetch(ring + uint32_t(k * GROUP));
     uint32_t at = ring;
-    uint32_t flags = 0;
+    uint8_t flags[RING_STEPS];
     auto look = [&](int n) {
-        flags = 0;
         if (RESET)
 #pragma unroll
-            for (int i = 0; i < RING_STEPS; ++i)
-                if (i < n && pr[n - 1 - i] != 0) flags |= 1u << i;
+            for (int i = 0; i < RING_STEPS; ++i) {
+                flags[i] = 0;
+                if (i < n) flags[i] = pr[n - 1 - i];
+            }
     };
     look(len);
     for (int n = len; n > 0; n -= RING_STEPS) {
         asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
-        const uint32_t cut = flags;
+        uint32_t cut = 0;
+        if (RESET)
+#pragma unroll
+            for (int i = 0; i < RING_STEPS; ++i) cut |= flags[i] != 0 ? 1u << i : 0u;
         float2 z[RING_STEPS], d[RING_STEPS], w[RING_STEPS];
 #pragma unroll
         for (int i = 0; i < RING_STEPS; ++i) {
@@ -746,23 +754,27 @@ struct ScanExchange {
     }
 };
 
-// The reset flags of a lane's stretch, a bit a step.  The four lanes of a stretch read a step each, a round ahead.
+// The reset flags of a lane's stretch, a bit a step.  The four lanes of a stretch read a step each, a round ahead; what
+// they read is looked at when it is needed.
 template <int L, int DIR> struct ScanFlags {
     const uint8_t* row = nullptr;
     int len = 0;
-    uint32_t next = 0;
+    uint8_t next[L / 4];
     __device__ __forceinline__ void fetch(const ScanAt& q, int t0)
     {
-        next = 0;
 #pragma unroll
         for (int k = 0; k < L / 4; ++k) {
             const int t = t0 + DIR * (q.pair + 4 * k);
-            if (row && t >= 0 && t < len && row[t] != 0) next |= 1u << (4 * k);
+            next[k] = 0;
+            if (row && t >= 0 && t < len) next[k] = row[t];
         }
     }
     __device__ __forceinline__ uint32_t take(const ScanAt& q) const
     {
-        uint32_t m = next << q.pair;
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < L / 4; ++k) m |= next[k] != 0 ? 1u << (4 * k) : 0u;
+        m <<= q.pair;
         m |= __shfl_xor_sync(0xFFFFFFFFu, m, 1);
         return m | __shfl_xor_sync(0xFFFFFFFFu, m, 2);
     }
