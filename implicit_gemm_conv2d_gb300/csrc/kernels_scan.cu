@@ -704,13 +704,40 @@ struct ScanExchange {
             if (int(threadIdx.x & 31) >= o) scan_join<RESET>(A, H, a, h);
         }
     }
-    // Joins the warp's stretches; (A, H) become the lane's and all before it.  With a cluster, tells its blocks.
-    template <bool RESET> __device__ __forceinline__ void send(const ScanAt& q, int round, float2& A, float2& H) const
+    // The same where some have a reset in them: not by their A, but by a vote, as bits 28 to 31 for the lane's own, 24 to
+    // 27 for the one before it and so on.  Two instructions a step less for each of four values.
+    static __device__ __forceinline__ void join_all(float2& A, float2& H, uint32_t cuts)
     {
-        join_all<RESET>(A, H);
+#pragma unroll
+        for (int o = 4; o < 32; o *= 2) {
+            const float2 a = shfl_up(A, o), h = shfl_up(H, o);
+            if (int(threadIdx.x & 31) >= o) {
+                if (cuts < 1u << (32 - o)) H = fma2(A, h, H);  // none among those that are joined already
+                A = mul2(A, a);
+            }
+        }
+    }
+    static __device__ __forceinline__ uint32_t vote(const ScanAt& q, bool cut)
+    {
+        return __ballot_sync(0xFFFFFFFFu, cut) << (28 - 4 * q.seg);
+    }
+    template <bool RESET> static __device__ __forceinline__ float2 enter(float2 A, float2 H, uint32_t cuts, float2 state)
+    {
+        return RESET && cuts != 0 ? H : fma2(A, state, H);
+    }
+    // Joins the warp's stretches; (A, H) become the lane's and all before it, cuts the resets among them.  With a
+    // cluster, tells its blocks.
+    template <bool RESET>
+    __device__ __forceinline__ void send(const ScanAt& q, int round, float2& A, float2& H, bool cut, uint32_t& cuts) const
+    {
+        cuts = RESET ? vote(q, cut) : 0u;
+        if constexpr (RESET) join_all(A, H, cuts);
+        else join_all<false>(A, H);
         if (q.C == 1) return;
         // the last stretch's lanes hold the warp's; lane (seg, pair) tells rank seg
-        const float2 a = shfl(A, 28 + q.pair), h = shfl(H, 28 + q.pair);
+        float2 a = shfl(A, 28 + q.pair);
+        const float2 h = shfl(H, 28 + q.pair);
+        if (RESET && __any_sync(0xFFFFFFFFu, cut)) a = both(-1.f);
         if (q.seg < q.C && !dead) {
             const int parity = round & 1;
             const uint32_t to = slots + uint32_t(((parity * q.C + q.rank) * SCAN_WARPS + q.warp) * 64 + q.pair * 16);
@@ -720,9 +747,9 @@ struct ScanExchange {
     }
     // state: in, what enters the round; out, what enters the next one.  Returns what enters the lane's stretch.
     template <bool RESET>
-    __device__ __forceinline__ float2 receive(const ScanAt& q, int round, float2 A, float2 H, float2& state)
+    __device__ __forceinline__ float2 receive(const ScanAt& q, int round, float2 A, float2 H, uint32_t cuts, float2& state)
     {
-        float2 enter = state;
+        float2 in = state;
         if (q.C > 1) {
             const int parity = round & 1;
             const uint32_t bar = bars + uint32_t(parity) * 8, phase = uint32_t(round >> 1) & 1u;
@@ -741,16 +768,18 @@ struct ScanExchange {
                 h = make_float2(v.z, v.w);
             }
             __syncwarp();  // read by all before the round after the next is announced
-            join_all<RESET>(a, h);
-            const float2 s = scan_enter<RESET>(a, h, state);
-            if (q.rank > 0) enter = shfl(s, (q.rank - 1) * 4 + q.pair);
+            const uint32_t theirs = RESET ? vote(q, a.x < 0.f) : 0u;
+            if constexpr (RESET) join_all(a, h, theirs);
+            else join_all<false>(a, h);
+            const float2 s = enter<RESET>(a, h, theirs, state);
+            if (q.rank > 0) in = shfl(s, (q.rank - 1) * 4 + q.pair);
             state = shfl(s, 28 + q.pair);
         } else {
-            state = shfl(scan_enter<RESET>(A, H, state), 28 + q.pair);
+            state = shfl(enter<RESET>(A, H, cuts, state), 28 + q.pair);
         }
         // what the stretches in front of this one make of it
-        const float2 f = shfl_up(scan_enter<RESET>(A, H, enter), 4);
-        return q.seg == 0 ? enter : f;
+        const float2 f = shfl_up(enter<RESET>(A, H, cuts, in), 4);
+        return q.seg == 0 ? in : f;
     }
 };
 
@@ -1038,10 +1067,10 @@ scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
             H = fma2(keep[i], H, in[i]);
             A = mul2(A, keep[i]);
         }
-        if (RESET && cut != 0) A = both(-1.f);
-        ex.send<RESET>(q, round, A, H);
+        uint32_t cuts;
+        ex.send<RESET>(q, round, A, H, cut != 0, cuts);
         if (CB != 2 || WINDOW) turn();
-        float2 st = ex.receive<RESET>(q, round, A, H, state);
+        float2 st = ex.receive<RESET>(q, round, A, H, cuts, state);
         const uint32_t out = WINDOW ? results + (round & 1) * Tile::ARRAY : stage;
 #pragma unroll
         for (int i = 0; i < L; ++i) {
@@ -1178,10 +1207,10 @@ scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
             if (RESET && (cut >> i & 1u)) H = both(0.f);
             A = mul2(A, keep);
         }
-        if (RESET && cut != 0) A = both(-1.f);
-        ex.send<RESET>(q, round, A, H);
+        uint32_t cuts;
+        ex.send<RESET>(q, round, A, H, cut != 0, cuts);
         if (CB != 2 || WINDOW) turn();
-        float2 st = ex.receive<RESET>(q, round, A, H, state);
+        float2 st = ex.receive<RESET>(q, round, A, H, cuts, state);
         const uint32_t out = WINDOW ? results + (round & 1) * 2 * Tile::ARRAY : stage;
 #pragma unroll
         for (int i = 0; i < L; ++i) {
