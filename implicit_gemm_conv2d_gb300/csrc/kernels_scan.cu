@@ -1190,7 +1190,6 @@ scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
             z[i] = scan_gate<T>(value(stage, 1, i), e);
             d[i] = value(stage, 2, i);
             float2 before = value(stage, 3, i);
-            if (!full && t0 == i) before = scan_state(p, q, h0);
             if (RESET && (cut >> i & 1u)) before = both(0.f);
             w[i] = mul2(scan_slope(e, z[i]), fma2(before, both(-1.f), value(stage, 0, i)));
         }
@@ -1198,6 +1197,15 @@ scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
 #pragma unroll
             for (int i = 0; i < L; ++i)
                 if (t0 - i < 0 || t0 - i >= len) z[i] = d[i] = w[i] = both(0.f);
+            // step 0 comes behind h0
+#pragma unroll
+            for (int i = 0; i < L; ++i)
+                if (t0 == i && len > 0) {
+                    float2 e;
+                    const float2 g = scan_gate<T>(value(stage, 1, i), e);
+                    const float2 before = RESET && (cut >> i & 1u) ? both(0.f) : scan_state(p, q, h0);
+                    w[i] = mul2(scan_slope(e, g), fma2(before, both(-1.f), value(stage, 0, i)));
+                }
         }
         float2 A = both(1.f), H = both(0.f);
 #pragma unroll
