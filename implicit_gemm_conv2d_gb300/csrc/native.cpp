@@ -108,6 +108,13 @@ int32_t size32(int64_t v)
     return int32_t(v);
 }
 
+bool truth(PyObject* o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Raised();
+    return v != 0;
+}
+
 double number(PyObject* o)
 {
     const double v = PyFloat_AsDouble(o);
@@ -201,7 +208,7 @@ PyObject* group_norm(PyObject* const* a)
     const at::Tensor* gamma = channels(a[2], "gamma", x, d.C);
     const at::Tensor* beta = channels(a[3], "beta", x, d.C);
     at::Tensor y = at::empty(x.sizes(), x.options()), mean, rstd;
-    if (PyObject_IsTrue(a[7])) {
+    if (truth(a[7])) {
         mean = at::empty({d.B, d.G}, x.options().dtype(at::kFloat));
         rstd = at::empty({d.B, d.G}, x.options().dtype(at::kFloat));
     }
@@ -226,7 +233,7 @@ PyObject* group_norm_bwd(PyObject* const* a)
     const at::Tensor& mean = same(tensor(a[5], "mean"), "mean", stat, at::kFloat, x.device());
     const at::Tensor& rstd = same(tensor(a[6], "rstd"), "rstd", stat, at::kFloat, x.device());
     at::Tensor dx = at::empty(x.sizes(), x.options()), dgamma, dbeta;
-    if (PyObject_IsTrue(a[9])) {
+    if (truth(a[9])) {
         dgamma = at::empty({d.C}, x.options());
         dbeta = at::empty({d.C}, x.options());
     }
@@ -306,14 +313,14 @@ conv_ln_desc_t ln_desc(const at::Tensor& x, double eps, bool rms)
 PyObject* layer_norm(PyObject* const* a)
 {
     const at::Tensor& x = tensor(a[0], "x");
-    const conv_ln_desc_t d = ln_desc(x, number(a[4]), PyObject_IsTrue(a[5]));
+    const conv_ln_desc_t d = ln_desc(x, number(a[4]), truth(a[5]));
     const at::Tensor* gamma = channels(a[1], "gamma", x, d.D);
     const at::Tensor* beta = channels(a[2], "beta", x, d.D);
     const at::Tensor* residual = optional(a[3], "residual");
     if (residual) same(*residual, "residual", x.sizes(), x.scalar_type(), x.device());
     at::Tensor y = fresh(x.sizes(), x.scalar_type(), x), total, mean, rstd;
     if (residual) total = fresh(x.sizes(), x.scalar_type(), x);
-    if (PyObject_IsTrue(a[6])) {
+    if (truth(a[6])) {
         const auto rows = x.sizes().slice(0, size_t(x.dim() - 1));
         if (!d.rms) mean = fresh(rows, at::kFloat, x);
         rstd = fresh(rows, at::kFloat, x);
@@ -338,7 +345,7 @@ PyObject* layer_norm_bwd(PyObject* const* a)
     const at::Tensor* dtotal = optional(a[5], "dtotal");
     if (dtotal) same(*dtotal, "dtotal", x.sizes(), x.scalar_type(), x.device());
     at::Tensor dx = fresh(x.sizes(), x.scalar_type(), x), dgamma, dbeta;
-    if (PyObject_IsTrue(a[6])) {
+    if (truth(a[6])) {
         dgamma = fresh({d.D}, x.scalar_type(), x);
         if (mean) dbeta = fresh({d.D}, x.scalar_type(), x);
     }

@@ -92,8 +92,8 @@ int distill_check(const conv_distill_desc_t* d)
     if (!d) return CONV_ERR_NULL;
     if (d->N < 0 || d->V < 1 || d->K < 1 || d->ld < d->V || (d->dtype != CONV_F32 && d->dtype != CONV_BF16) ||
         (d->teacher_dtype != CONV_F32 && d->teacher_dtype != CONV_BF16) ||
-        (d->index_dtype != CONV_INDEX_I32 && d->index_dtype != CONV_INDEX_I64) || !std::isfinite(d->temperature) ||
-        !(d->temperature > 0.f) || !std::isfinite(1.f / d->temperature))
+        (d->index_dtype != CONV_INDEX_I32 && d->index_dtype != CONV_INDEX_I64) || 
+        !(d->temperature >= 0x1p-60f && d->temperature <= 0x1p60f))  // its square and 1 / it are normal numbers
         return CONV_ERR_DESC;
     if (d->N >= 1 << 27 || d->V >= 1 << 30 || d->K > 1024 || d->ld >= int64_t(1) << 32) return CONV_ERR_UNSUPPORTED;
     return CONV_OK;
@@ -236,6 +236,7 @@ int conv_ln_fwd(const conv_ln_desc_t* desc, const void* x, const void* residual,
     if (!aligned16(x) || !aligned16(residual) || !aligned16(gamma) || !aligned16(beta) || !aligned16(y) ||
         !aligned16(total) || !aligned16(mean) || !aligned16(rstd))
         return CONV_ERR_ALIGN;
+    if (y == total) return CONV_ERR_DESC;
     DevInfo d;
     if ((rc = device_info(d)) != CONV_OK) return rc;
     return cuda_status(run_ln_fwd(*desc, d, x, residual, gamma, beta, y, total, mean, rstd,
@@ -262,6 +263,7 @@ int conv_ln_bwd(const conv_ln_desc_t* desc, const void* x, const void* dy, const
         (desc->N > 0 && (!aligned16(x) || !aligned16(dy) || !aligned16(gamma) || !aligned16(mean) || !aligned16(rstd) ||
                          !aligned16(dtotal) || !aligned16(dx))))
         return CONV_ERR_ALIGN;
+    if (desc->N > 0 && dx == x) return CONV_ERR_DESC;
     DevInfo d;
     if ((rc = device_info(d)) != CONV_OK) return rc;
     const size_t need = ln_bwd_workspace(*desc, d);
@@ -296,6 +298,7 @@ int conv_scan_fwd(const conv_scan_desc_t* desc, const void* x, const void* gate,
     if (!aligned_to(x, a) || !aligned_to(gate, a) || !aligned_to(h, a) || !aligned_to(h0, 4) || !aligned_to(last, 4) ||
         !aligned_to(lengths, 4) || !aligned16(workspace))
         return CONV_ERR_ALIGN;
+    if (desc->T > 0 && (h == x || h == gate)) return CONV_ERR_DESC;
     DevInfo d;
     if ((rc = device_info(d)) != CONV_OK) return rc;
     const size_t need = scan_workspace(*desc, d, false);
@@ -317,6 +320,9 @@ int conv_scan_bwd(const conv_scan_desc_t* desc, const void* x, const void* gate,
         !aligned_to(dgate, a) || !aligned_to(h0, 4) || !aligned_to(dlast, 4) || !aligned_to(dh0, 4) ||
         !aligned_to(lengths, 4) || !aligned16(workspace))
         return CONV_ERR_ALIGN;
+    const void* inputs[] = {x, gate, h, dh};
+    for (const void* in : inputs)
+        if (desc->T > 0 && (dx == in || dgate == in || dx == dgate)) return CONV_ERR_DESC;
     DevInfo d;
     if ((rc = device_info(d)) != CONV_OK) return rc;
     const size_t need = scan_workspace(*desc, d, true);

@@ -1,11 +1,13 @@
 """Python side of include/conv_train.h: the operators a training step runs around the conv
-layers -- group norm with an activation, embedding lookup and its gradient, the global gradient
-norm and clipping.
+layers -- group norm with an activation, embedding lookup and its gradient, layer norm of a
+residual sum, the gated scan over time, the loss against a teacher's top logits, the global
+gradient norm and clipping.
 
 The functions named like the C entry points (conv_gn_fwd, conv_embed_bwd, conv_grad_clip, ...)
 take a descriptor and already-allocated CUDA tensors, like those of ``binding``.  group_norm,
-group_norm_bwd, embed, embed_bwd, grad_norm and clip_grads check shapes and types and allocate
-outputs and workspaces with torch first.  Everything is enqueued on the current torch stream (or
+group_norm_bwd, embed, embed_bwd, layer_norm, layer_norm_bwd, gated_scan, gated_scan_bwd, distill,
+distill_bwd, distill_grad, grad_norm and clip_grads check shapes and types and allocate outputs and
+workspaces with torch first.  Everything is enqueued on the current torch stream (or
 the stream given) and nothing waits for the GPU; tensors made on another stream have to be
 ordered by the caller (``stream.wait_stream``), as for any torch operation.  What the allocating
 functions allocate belongs to the stream they run on.  A call runs on the current device, and
@@ -329,8 +331,8 @@ def gated_scan(x, gate, h0=None, reset=None, lengths=None, out=None, last=None, 
     x and gate may be views (halves of one projection, time first) as long as a step's channels lie
     one behind the other.  h0: the states that the rows begin with (fp32).  reset (batch, time), bool
     or uint8: steps where a new sequence begins with a state of 0.  lengths (batch), int32: the steps
-    that each row has; h is 0 behind them.  out and last: tensors to write to; last may be h0, so that
-    a rollout keeps its states in one place."""
+    that each row has; h is 0 behind them.  out and last: tensors to write to, out apart from the inputs;
+    last may be h0, so that a rollout keeps its states in one place."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return gated_scan(x, gate, h0, reset, lengths, out, last)
@@ -339,7 +341,8 @@ def gated_scan(x, gate, h0=None, reset=None, lengths=None, out=None, last=None, 
 
 def gated_scan_bwd(x, gate, h, dh, h0=None, dlast=None, reset=None, lengths=None, dx=None, dgate=None, stream=None):
     """dx, dgate, dh0 (None where h0 is) from gated_scan's inputs, its h, and the gradients of h and
-    (dlast, fp32) of last.  dx and dgate: tensors to write to, such as the halves of one gradient."""
+    (dlast, fp32) of last.  dx and dgate: tensors to write to, such as the halves of one gradient, apart
+    from the inputs and one another."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return gated_scan_bwd(x, gate, h, dh, h0, dlast, reset, lengths, dx, dgate)

@@ -1,7 +1,8 @@
 /*
  * conv_train.h -- C ABI of the operators a training step runs around the conv layers of
- * conv.h: group normalisation with an activation, the embedding lookup with its gradient, and
- * the global gradient norm with clipping.
+ * conv.h: group normalisation with an activation, the embedding lookup with its gradient, layer
+ * normalisation of a residual sum, the gated scan over time, the loss against a teacher's top
+ * logits, and the global gradient norm with clipping.
  *
  * The conventions are conv.h's: device pointers owned by the caller, no allocation inside the
  * library (workspaces are sized by a query and passed in), calls that are asynchronous on
@@ -111,7 +112,8 @@ int conv_embed_bwd(const conv_embed_desc_t* desc, const void* idx, const void* d
  * residual stream goes on beside its norm), or NULL (0).  rms: the form without a mean: mean, m1
  * and beta are 0, and mean, beta and dbeta NULL.
  * All arrays dense, (N, D) or (D), of the descriptor's dtype; mean and rstd fp32, (N).  A row with an
- * infinity or NaN is NaN, and so are dgamma and dbeta with it; the other rows are not. */
+ * infinity or NaN is NaN, and so are dgamma and dbeta with it; the other rows are not.
+ * Squares are fp32: deviations from 1.8e19 on make rstd 0. */
 typedef struct {
     int64_t N;              /* rows, >= 0                                                 */
     int32_t D;              /* values a row, >= 1                                         */
@@ -121,12 +123,13 @@ typedef struct {
 } conv_ln_desc_t;
 
 /* gamma, beta: NULL counts as 1 and 0.  total: written, if and only if there is a residual.  mean and
- * rstd: written, or NULL (an inference call; with rms: rstd).  y may be x or residual, total the other.
+ * rstd: written, or NULL (an inference call; with rms: rstd).  y may be x or residual, total the other;
+ * y is not total.
  * Limits: N < 2^31, D < 2^30 (CONV_ERR_UNSUPPORTED beyond).  N = 0 does nothing. */
 int conv_ln_fwd(const conv_ln_desc_t* desc, const void* x, const void* residual, const void* gamma, const void* beta,
                 void* y, void* total, float* mean, float* rstd, conv_stream_t stream);
 
-/* x: the forward's total.  dx may be dy or dtotal.  dgamma, dbeta: written, or both NULL (rms: dgamma, or
+/* x: the forward's total.  dx may be dy or dtotal, not x.  dgamma, dbeta: written, or both NULL (rms: dgamma, or
  * NULL).  N = 0 writes zeros to them. */
 size_t conv_ln_bwd_workspace_size(const conv_ln_desc_t* desc);
 int conv_ln_bwd(const conv_ln_desc_t* desc, const void* x, const void* dy, const void* gamma, const float* mean,
@@ -162,7 +165,8 @@ int conv_ln_bwd(const conv_ln_desc_t* desc, const void* x, const void* dy, const
  * x, gate, h, dh, dx and dgate have the descriptor's dtype and lie anywhere: an array's element
  * (b, t, d) is batch * b + step * t + d elements behind its address, which is a multiple of the
  * element's size.  So x and gate may be halves of one array, and time may be the outer dimension.
- * Distances are >= 0; an output's rows do not overlap one another, nor any input.  h0, last, dlast,
+ * Distances are >= 0; an output's rows do not overlap one another, nor another output's or an input's
+ * (CONV_ERR_DESC where the first elements coincide; the rest is the caller's to see to).  h0, last, dlast,
  * dh0: fp32, (B, D) dense. */
 typedef struct { int64_t batch, step; } conv_rows_t;
 
@@ -210,7 +214,7 @@ typedef struct {
     int32_t dtype;          /* conv_dtype_t of z and dz                                    */
     int32_t index_dtype;    /* conv_index_t of ids                                         */
     int32_t teacher_dtype;  /* conv_dtype_t of teacher                                     */
-    float temperature;      /* finite, > 0; 1 / temperature finite                         */
+    float temperature;      /* 2^-60 to 2^60                                               */
 } conv_distill_desc_t;
 
 /* Limits: N < 2^27, V < 2^30, K <= 1024 (CONV_ERR_UNSUPPORTED beyond); N * ld may pass 2^31.  N = 0 does

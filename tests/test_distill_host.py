@@ -45,7 +45,8 @@ def calls(L, d, at=None, value=None, scale=1.0):
                                       (dict(dtype=2), -2), (dict(teacher_dtype=2), -2), (dict(index_dtype=2), -2),
                                       (dict(temperature=0.0), -2), (dict(temperature=-1.0), -2),
                                       (dict(temperature=float("nan")), -2), (dict(temperature=float("inf")), -2),
-                                      (dict(temperature=1e-45), -2), (dict(N=1 << 27), -3),
+                                      (dict(temperature=1e-45), -2), (dict(temperature=2.0 ** -61), -2),
+                                      (dict(temperature=2.0 ** 61), -2), (dict(N=1 << 27), -3),
                                       (dict(V=1 << 30, ld=1 << 30), -3), (dict(K=1025), -3), (dict(ld=1 << 32), -3)])
 def test_descriptor_refused(L, bad, code):
     assert calls(L, desc(**bad)) == {code}

@@ -199,6 +199,32 @@ def test_masked_logits(tau, V, dtype):
     within(train.distill_bwd(z, ids, q, zmax, zlog, w, 1.0, tau), ref, bound, dtype, "dz")
 
 
+@pytest.mark.parametrize("size", [(5, 130, 7), (5, 4099, 40), (3, 60001, 64)], ids=str)
+def test_ids_whose_low_half_is_in_range(size):
+    """64-bit ids beyond 32 bits are outside of the vocabulary, whatever their low half says."""
+    z, _, q, w = inputs(size, "bf16", 15)
+    ids = torch.arange(size[2], device="cuda").repeat(size[0], 1)
+    far = ids.clone()
+    far[:, ::3] += 1 << 32
+    far[:, 1::3] -= 1 << 32
+    out = ids.clone()
+    out[:, ::3], out[:, 1::3] = -1, size[1]
+    for a, b in zip(train.distill_grad(z, far, q, w), train.distill_grad(z, out, q, w)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("tau", [2.0 ** -60, 2.0 ** 60])
+def test_temperatures_at_their_limits(tau):
+    """The largest logit takes all of P, or every logit the same: the losses and gradients stay finite."""
+    z, ids, q, w = inputs((4, 5003, 6), "f32", 16, pad=0.0)
+    ids = torch.arange(6, device="cuda", dtype=torch.int32).repeat(4, 1)
+    loss, dz = train.distill_grad(z, ids, q, w, temperature=tau)
+    assert bool(torch.isfinite(loss).all()) and bool(torch.isfinite(dz).all())
+    if tau > 1:  # P = 1 / V, p = 1 / K
+        want = tau * tau * np.log(5003 / 6)
+        assert float((loss / want - 1).abs().max()) <= 1e-5
+
+
 def test_no_rows_and_refusals():
     z = torch.zeros((0, 10), device="cuda")
     ids, q = torch.zeros((0, 2), dtype=torch.int32, device="cuda"), torch.zeros((0, 2), device="cuda")

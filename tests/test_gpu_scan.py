@@ -137,6 +137,36 @@ def test_state_in_place_and_outputs_given(T):
     assert torch.equal(grad[..., :44], dx) and torch.equal(grad[..., 44:88], dgate) and bool((grad[..., 88] == 7).all())
 
 
+@pytest.mark.parametrize("size", [(300, 9, 8), (1000, 37, 130), (40, 200, 520), (5, 777, 31), (2, 1025, 72), (1, 9001, 24)],
+                         ids=str)
+def test_side_arrays_anywhere(size):
+    """States, lengths and flags at addresses that are only their elements'; flags of any value but 0."""
+    dev, side, (h, last, dx, dgate) = both_ways(size, "bf16", h0=True, reset=0.05, lengths=True)
+
+    def moved(t):
+        room = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        room[1:] = t.reshape(-1)
+        return room[1:].view(t.shape)
+
+    flags = side["reset"].to(torch.uint8) * torch.randint(1, 256, side["reset"].shape, device="cuda").to(torch.uint8)
+    h0, lengths, dlast = moved(side["h0"]), moved(side["lengths"]), moved(side["dlast"])
+    h2, last2 = train.gated_scan(dev["x"], dev["gate"], h0, moved(flags), lengths, last=moved(side["h0"]))
+    assert torch.equal(h2, h) and torch.equal(last2, last)
+    got = train.gated_scan_bwd(dev["x"], dev["gate"], h, dev["dh"], h0, dlast, moved(flags), lengths)
+    assert torch.equal(got[0], dx) and torch.equal(got[1], dgate)
+
+
+def test_outputs_over_inputs_are_refused():
+    dev, side = inputs((3, 20, 8), "f32")
+    h, _ = train.gated_scan(dev["x"], dev["gate"])
+    for bad in (lambda: train.gated_scan(dev["x"], dev["gate"], out=dev["x"]),
+                lambda: train.gated_scan(dev["x"], dev["gate"], out=dev["gate"]),
+                lambda: train.gated_scan_bwd(dev["x"], dev["gate"], h, dev["dh"], dx=dev["dh"]),
+                lambda: train.gated_scan_bwd(dev["x"], dev["gate"], h, dev["dh"], dgate=h)):
+        with pytest.raises(train.binding.ConvError):
+            bad()
+
+
 def test_steps_one_by_one_are_the_sequence():
     """A rollout's steps with the state kept in place: step t's state is the sequence's, within both bounds."""
     dev, side = inputs((6, 50, 20), "f32", h0=True)

@@ -60,6 +60,11 @@ def test_pointers_and_alignment(L):
     assert bwd(L, empty, *[None] * 7, OK, None) == -1
 
 
+def test_outputs_over_what_is_still_read(L):
+    assert fwd(L, desc(), y=OK + 16, total=OK + 16) == -2
+    assert bwd(L, desc(), x=OK + 16, dx=OK + 16) == -2
+
+
 def test_python_checks_before_the_library():
     torch = pytest.importorskip("torch")
     x = torch.zeros((2, 8))

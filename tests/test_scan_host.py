@@ -76,6 +76,17 @@ def test_pointers_and_alignment(L):
     assert bwd(L, desc(B=0), None, None, None, None, None, None, None, None, None, None) == 0
 
 
+def test_outputs_over_inputs_are_refused(L):
+    a, b, c, e, f, g = (OK + 0x1000 * i for i in range(6))
+    for name in ("x", "gate"):
+        assert fwd(L, desc(), **{**dict(x=a, gate=b, h=c), name: c}) == -2
+    for out in ("dx", "dgate"):
+        for name in ("x", "gate", "h", "dh", "dx", "dgate"):
+            if name != out:
+                args = dict(x=a, gate=b, h=c, dh=e, dx=f, dgate=g)
+                assert bwd(L, desc(), **{**args, out: args[name]}) == -2
+
+
 def test_python_checks_before_the_library():
     torch = pytest.importorskip("torch")
     x = torch.zeros((2, 8, 3))
