@@ -13,6 +13,11 @@
 // One warp more than those that sweep works on the teacher's entries: their softmax, the student's logits at their
 // ids, and which ids occur twice.  dz at the ids is written again, whole, behind the sweep's barrier, by
 // one thread an id: no atomic adds, and a fixed order for an id that occurs twice.
+//
+// Floor: z once, and dz.  Measured, with the share of that floor at the measured copy's bandwidth: 1024 x 50021 fp32
+// backward 69.7 us (87 %), 8192 x 50021 bf16 both at once 299 (81 %), 24 x 131071 fp32 forward 5.9 (a launch and two
+// trips along a cluster).  Bound by memory, bf16 both at once also by instructions (0.62 issued a slot); rows of a few
+// hundred logits by the teacher's entries (32768 x 128 fp32 both at once 28.8 against 5.3).
 #include <algorithm>
 
 #include "gn_common.cuh"

@@ -13,6 +13,10 @@
 // and a thread's columns stay its own.  The first and the last vector hold values of the rows beside it,
 // which are cut off as they come in and never written.
 // Rows that no team holds are read again for each pass.
+//
+// Measured, with the share of the floor (each array once) at the measured copy's bandwidth: 32768 x 1024 bf16
+// forward 46.6 us (85 %), backward 48.3 (82 %, of it 7 the columns' sums), 6001 x 1430 fp32 backward without a mean
+// 25.0 (61 %: a third of it are the sums, and three waves of rows), 2000 x 16384 bf16 backward 94 (42 %: read twice).
 #include <algorithm>
 
 #include "gn_common.cuh"

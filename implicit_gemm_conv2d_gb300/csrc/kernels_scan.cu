@@ -7,7 +7,8 @@
 // of its 1 - z and H what it makes of 0; stretches are joined by (A2 A1, A2 H1 + H2).  A lane takes
 // L consecutive steps of two channels, a warp 8 such stretches of 8 channels: the warp joins them by
 // shuffles, the warps of a cluster's blocks, which share a sequence's round, through distributed shared
-// memory, and each lane walks its steps again, from registers, with the state it now knows.  So each
+// memory (stores that count on a barrier), and each lane walks its steps again, from registers, with the state it now
+// knows.  So each
 // input is read once, whatever the length, and a long sequence is worked on by many blocks.
 // Where even a cluster of 8 blocks a sequence leaves most of the GPU idle, time is cut into pieces first: one kernel
 // finds each piece's (A, H), the other joins those in front of its own and walks it.
@@ -17,7 +18,14 @@
 //
 // State, A and H are fp32, and so is 1 - z, taken from z: where z is small, a long memory, z's error is
 // small beside the rounding of 1 - z, which is that of one more operation a step.
-// A stretch with a reset in it has A = -1: what enters it, be it NaN, is left out and not multiplied by 0.
+// What enters a stretch with a reset in it, be it NaN, is left out and not multiplied by 0: a warp votes on its
+// stretches' resets; where a stretch travels further, A = -1 says it.
+//
+// Floor: 3 values an element are read and written (backward 6).  Measured, with the share of that floor at the
+// measured copy's bandwidth: 1024 x 64 x 128 fp32 forward 18.2 us (82 %, walk), 2 x 32768 x 1024 bf16 forward 79.5
+// (75 %), 8 x 4096 x 1024 bf16 backward 76.1 (78 %), with resets 88.5 (67 %), 5 x 1999 x 777 fp32 padded backward 55 (41 %).
+// Bound by instructions and the latency between a round's phases at two or three blocks an SM (0.44 to 0.57 issued a
+// slot); a step of few rows by its launch.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
