@@ -699,6 +699,10 @@ LnParams ln_plan(const conv_ln_desc_t& e, const DevInfo& d, bool bwd)
     if (!bwd) {
         while (nv < 4 && nv * 2 <= vecs) nv *= 2;
         if (vecs > 4 * LN_MOST) nv = 8;
+        // Teams of several warps that begin anywhere: two spill nothing in bf16, and more threads share a block's copies of
+        // gamma and beta (8001 x 1431 30.4 us with four, 26.4 with two; 4001 x 5001 46.0 and 42.7; one warp, 20000 x 770, 36.3 and
+        // 38.5; fp32 3001 x 2750 29.3 and 35.4).
+        if (p.edge && es == 2 && vecs > 4 * 32 && vecs <= 2 * LN_MOST) nv = 2;
     } else {
         nv = es == 2 || vecs < 2 ? 1 : 2;
         if (vecs > nv * LN_MOST) nv *= 2;
@@ -725,8 +729,9 @@ LnParams ln_plan(const conv_ln_desc_t& e, const DevInfo& d, bool bwd)
     const int threads = p.TL * p.teams;
     const int64_t rows = int64_t(p.teams) * p.R, blocks = (e.N + rows - 1) / rows;
     // Twice as many blocks as the SMs hold at once with 64 registers a thread; in the backward as many as they do with 128.
-    // A multiple of what makes a team's rows begin alike.
-    const int per_sm = std::max(1, (bwd ? 512 : 2048) / threads);
+    // Where rows begin anywhere, each makes its copies of gamma and beta first: as many as the SMs hold (6001 x 1430 fp32
+    // 32.6 us with twice as many, 29.5 with these, 37.8 with half of them).  A multiple of what makes a team's rows begin alike.
+    const int per_sm = std::max(1, (bwd ? 512 : p.edge ? 1024 : 2048) / threads);
     p.blocks = int(std::max<int64_t>(1, std::min<int64_t>(blocks, int64_t(d.sms) * per_sm)));
     if (p.edge && p.teams % ve != 0) p.blocks = (p.blocks + ve - 1) / ve * ve;
     if (bwd) p.flush = e.N > int64_t(p.blocks) * p.teams * LN_FLUSH;
