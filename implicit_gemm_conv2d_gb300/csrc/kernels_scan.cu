@@ -1268,27 +1268,9 @@ ScanPlan scan_plan(const conv_scan_desc_t& e, const DevInfo& d, bool bwd, int ch
     const bool pairs = chunk >= 2 * es && e.D % 2 == 0;
     p.V = pairs ? 2 : 1;
     p.cols = (e.D + p.V - 1) / p.V;
-    // Which way.  A walk costs a step's instructions at least, one behind the other (0.05 to 0.1 us), parts the
-    // instructions of finding (A, H) and of two trips through shared memory.  In us, walk from registers / walk from
-    // shared memory / parts:
-    //   bf16 forward   16 x 1024 x 1024 104 / 56 / 45    48 x 512 x 1024 61 / 38 / 60    452 x 129 x 188 18 / 15 / 53
-    //   bf16 backward  16 x 1024 x 1024 133 / 101 / 69   48 x 512 x 1024 81 / 79 / 136   452 x 129 x 188 31 / 36 / 85
-    //   fp32 forward   24 x 1024 x 512 112 / 58 / 41     32 x 1024 x 1024 127 / 67 / 98  1024 x 64 x 128 18 / 23 / 22
-    //   fp32 backward  24 x 1024 x 512 144 / 115 / 65    32 x 1024 x 1024 174 / 135 / 176  1024 x 64 x 128 38 / 41 / 61
-    // and with 16 channels, where a block of parts has four batch rows: 1620 x 712 x 16 bf16 76 / 42 / 70.
-    const int64_t walkers = int64_t(e.B) * ((int64_t(e.D) + 1) / 2);
-    const int64_t few = int64_t(d.sms) * (es == 2 ? 104 : 72) / (e.D <= 32 ? 2 : 1);
-    p.walk = e.T <= 16 || walkers >= few;
-    if (p.walk) {
-        // Single bf16 values are none that an asynchronous copy takes.
-        const bool ring = e.T > 8 && (es == 4 || pairs) && walkers < int64_t(d.sms) * 256;
-        p.ring = !ring ? 0 : es == 4 && !bwd ? 4 : 2;
-        p.L = e.T > 4 ? 8 : e.T > 2 ? 4 : std::max(1, e.T);
-        p.threads = WALK_THREADS;
-        p.cluster = p.pieces = 1;
-        p.blocks = (int64_t(e.B) * p.cols + WALK_THREADS - 1) / WALK_THREADS;
-        return p;
-    }
+    p.pieces = 1;
+    p.piece = e.T;
+    // Parts: rounds, and blocks without their number along time.
     p.CB = chunk >= 16 && e.D % (16 / es) == 0 ? 16 : es == 4 || (chunk >= 4 && e.D % 2 == 0) ? 4 : 2;
     p.L = es == 2 ? (bwd ? 8 : 16) : bwd ? 4 : 8;
     p.wx_log = std::min(3, log2_up((int64_t(e.D) + 7) / 8));
@@ -1299,30 +1281,58 @@ ScanPlan scan_plan(const conv_scan_desc_t& e, const DevInfo& d, bool bwd, int ch
     p.tiles = int((int64_t(e.D) + (8 << p.wx_log) - 1) / (8 << p.wx_log));
     const int64_t blocks = int64_t(p.tiles) * ((int64_t(e.B) + (1 << p.by_log) - 1) >> p.by_log);
     const int64_t rounds = (int64_t(e.T) + SCAN_SEGS * p.L - 1) / (SCAN_SEGS * p.L);
-    // Blocks along time: fewer rounds each, as far as the blocks fit the GPU.  A round takes a block's latencies (as
-    // long as 1.5 blocks' instructions) and the instructions of all blocks of its SM.
-    const int fit = es == 2 || p.window ? 2 : 3;
-    int log_c = 0;
-    double best = 0;
-    for (int k = 0; k <= 3 && (k == 0 || (int64_t(1) << (k - 1)) < rounds); ++k) {
-        const double n = double(blocks) * (1 << k), waves = std::ceil(n / (double(d.sms) * fit));
-        const double cost = waves * (std::min(std::ceil(n / d.sms), double(fit)) + 1.5) / (1 << k);
-        if (k == 0 || cost < best) {
-            best = cost;
-            log_c = k;
-        }
-    }
-    p.cluster = 1 << log_c;
-    p.pieces = 1;
-    p.piece = e.T;
-    p.threads = SCAN_THREADS;
-    p.blocks = blocks << log_c;
-    p.stages = !p.window && rounds > (int64_t(2) << log_c) ? 3 : 2;
     // Pieces of time, as many as the GPU holds blocks for, of two rounds and more: each is read twice, and a second launch
     // comes on top, which is worth it where a cluster's blocks have some eight rounds more than that.
     // (The number of pieces, and so the workspace, does not go by where rows begin.)
     const int64_t most = std::min<int64_t>(int64_t(d.sms) * 2 / std::max<int64_t>(1, blocks), rounds / 2);
-    if (most > 8 && rounds >> 3 > 2 * ((rounds + most - 1) / most) + 8) {
+    const bool pieces = most > 8 && rounds >> 3 > 2 * ((rounds + most - 1) / most) + 8;
+    // Blocks along time: fewer rounds each, as far as the blocks fit the GPU.  A round takes 2.5 units with one block an SM,
+    // 3.8 with two, 7.5 with three, a wave of blocks 5 us (the first 3) and with exchanges along a cluster 6 (bf16 backward, 1024
+    // channels, clusters of 1, 2, 4, 8 blocks, us: 16 x 300 15 / 22 / 31 / 43, 16 x 2500 82 / 95 / 93 / 111, 8 x 1000 25 / 24 / 28 / 35,
+    // 4 x 1000 23 / 17 / 15 / 18, 20 x 2500 132 / 122 / 117 / 137).
+    const double unit = p.CB == 16 ? 0.44 : p.window ? (es == 4 ? 0.72 : bwd ? 1.8 : 0.9) : 0.65;
+    const int fit = es == 2 || p.window ? 2 : 3;
+    const double round_cost[] = {0, 2.5, 3.8, 7.5};
+    const int64_t wave = int64_t(d.sms) * fit;
+    int log_c = 0;
+    double parts = 0;
+    for (int k = 0; k <= 3 && (k == 0 || (int64_t(1) << (k - 1)) < rounds); ++k) {
+        const int64_t n = blocks << k, full = n / wave, rest = n % wave, each = (rounds + (int64_t(1) << k) - 1) >> k;
+        const double one = double(full) * round_cost[fit] + round_cost[(rest + d.sms - 1) / d.sms];
+        const double time = unit * one * double(each) + double(full + (rest > 0)) * (k == 0 ? 5 : 6) - 2;
+        if (k == 0 || time < parts) {
+            parts = time;
+            log_c = k;
+        }
+    }
+    // Or a walk, whose steps come one behind the other: a step's latency at least, with the steps to come in registers or
+    // in shared memory (single bf16 values are none that an asynchronous copy takes), and its bytes.  In us, walk from
+    // registers / from shared memory / parts:
+    //   bf16 forward   64 x 300 x 328 31 / 18 / 15   48 x 300 x 1024 37 / 23 / 24   452 x 300 x 188 42 / 41 / 50
+    //   bf16 backward  64 x 300 x 328 40 / 32 / 22   48 x 100 x 1024 17 / 17 / 20   452 x 300 x 188 64 / 64 / 77
+    //   fp32 forward   16 x 300 x 1024 33 / 19 / 13  64 x 300 x 328 36 / 20 / 21    452 x 300 x 188 58 / 58 / 61
+    //   fp32 backward  16 x 300 x 1024 47 / 36 / 23  28 x 300 x 1024 53 / 40 / 40   300 x 300 x 130 60 / 68 / 94
+    const int64_t threads = int64_t(e.B) * p.cols;
+    const bool ring = e.T > 8 && (es == 4 || pairs) && threads < int64_t(d.sms) * (bwd ? 128 : 256);
+    // (fp32's expf: a second warp a scheduler doubles a step of the forward from shared memory)
+    const double latency = !ring ? (!bwd ? 0.105 : es == 2 ? 0.13 : 0.145)
+                           : bwd ? (es == 2 ? 0.098 : 0.113) : es == 4 && threads > int64_t(d.sms) * 128 ? 0.11 : 0.056;
+    const double channel = es == 2 ? (bwd ? 2.65e-6 : 1.5e-6) : bwd ? 4e-6 : 2.15e-6;
+    const double step = std::max(latency, channel * double(e.B) * double(e.D));
+    p.walk = e.T <= 16 || (!pieces && step * e.T <= parts);
+    if (p.walk) {
+        p.ring = !ring ? 0 : es == 4 && !bwd ? 4 : 2;
+        p.L = e.T > 4 ? 8 : e.T > 2 ? 4 : std::max(1, e.T);
+        p.threads = WALK_THREADS;
+        p.cluster = 1;
+        p.blocks = (threads + WALK_THREADS - 1) / WALK_THREADS;
+        return p;
+    }
+    p.cluster = 1 << log_c;
+    p.threads = SCAN_THREADS;
+    p.blocks = blocks << log_c;
+    p.stages = !p.window && rounds > (int64_t(2) << log_c) ? 3 : 2;
+    if (pieces) {
         const int64_t each = (rounds + most - 1) / most;
         p.cluster = 1;
         p.piece = int(each * SCAN_SEGS * p.L);
