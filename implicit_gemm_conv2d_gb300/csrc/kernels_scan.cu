@@ -540,8 +540,8 @@ template <typename T, int L, int CB, int DIR> struct ScanCopy {
     {
         if constexpr (CB == 16)
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-        else if constexpr (CB == 4)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+        else if constexpr (CB >= 4)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(CB) : "memory");
         else
             tc::sts16(dst, *reinterpret_cast<const uint16_t*>(src));
     }
@@ -564,6 +564,7 @@ template <typename T, int L, int CB, int DIR> struct ScanCopy {
     static __device__ __forceinline__ void back(T* dst, uint32_t src)
     {
         if constexpr (CB == 16) *reinterpret_cast<int4*>(dst) = tc::lds128(src);
+        else if constexpr (CB == 8) *reinterpret_cast<uint2*>(dst) = tc::lds64(src);
         else if constexpr (CB == 4) *reinterpret_cast<uint32_t*>(dst) = tc::lds32(src);
         else *reinterpret_cast<uint16_t*>(dst) = uint16_t(tc::lds16(src));
     }
@@ -601,8 +602,8 @@ template <typename T, int L> struct ScanLane {
 // Inputs whose rows begin anywhere, for blocks of one batch row: a step's row of the tile comes as the 16-byte pieces of
 // memory that it lies in, one more than it is long, and is read from where it begins in the first of them.  Where
 // that is goes by the step's place in its stretch alone: L steps are a multiple of 16 bytes apart.  Stretches begin
-// `SKEW` bytes further on each, in other banks.
-template <typename T, int L, int DIR> struct ScanWindow {
+// `SKEW` bytes further on each, in other banks.  Rows begin at multiples of CB bytes.
+template <typename T, int L, int CB, int DIR> struct ScanWindow {
     using Tile = ScanTile<T, L>;
     static constexpr int ES = Tile::ES, CHUNKS = Tile::ROW / 16, ROWS = SCAN_THREADS / CHUNKS, N = Tile::RT / ROWS;
     static constexpr int PITCH = Tile::ROW + 16, SKEW = ES == 2 ? 16 : L == 4 ? 96 : 32;
@@ -673,11 +674,15 @@ template <typename T, int L, int DIR> struct ScanWindow {
     static __device__ __forceinline__ float2 read(uint32_t at, uint32_t begin)
     {
         at += begin & 15u;
-        if constexpr (ES == 4) {
+        if constexpr (ES == 4 && CB == 8) {
+            const uint2 u = tc::lds64(at);
+            return make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+        } else if constexpr (ES == 4) {
             return make_float2(__uint_as_float(tc::lds32(at)), __uint_as_float(tc::lds32(at + 4)));
         } else {
             const uint32_t word = at & ~3u;
-            const uint32_t u = __funnelshift_r(tc::lds32(word), tc::lds32(word + 4), (at & 2u) * 8u);
+            const uint32_t u = CB == 4 ? tc::lds32(at)
+                                       : __funnelshift_r(tc::lds32(word), tc::lds32(word + 4), (at & 2u) * 8u);
             return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
         }
     }
@@ -989,7 +994,7 @@ scan_part_fwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
     int* const lens = reinterpret_cast<int*>(sm);
     using Tile = ScanTile<T, L>;
     using Copy = ScanCopy<T, L, CB, 1>;
-    using Window = ScanWindow<T, L, 1>;
+    using Window = ScanWindow<T, L, CB, 1>;
     using In = std::conditional_t<WINDOW, Window, Copy>;
     constexpr int ARRAY = WINDOW ? Window::ARRAY : Tile::ARRAY, STAGE = 2 * ARRAY;
     const ScanAt q(p);
@@ -1115,7 +1120,7 @@ scan_part_bwd(const __grid_constant__ ScanPlan p, const T* x, const T* gate, con
     int* const lens = reinterpret_cast<int*>(sm);
     using Tile = ScanTile<T, L>;
     using Copy = ScanCopy<T, L, CB, -1>;
-    using Window = ScanWindow<T, L, -1>;
+    using Window = ScanWindow<T, L, CB, -1>;
     using In = std::conditional_t<WINDOW, Window, Copy>;
     constexpr int ARRAY = WINDOW ? Window::ARRAY : Tile::ARRAY, STAGE = 4 * ARRAY;
     const ScanAt q(p);
@@ -1275,9 +1280,6 @@ ScanPlan scan_plan(const conv_scan_desc_t& e, const DevInfo& d, bool bwd, int ch
     p.L = es == 2 ? (bwd ? 8 : 16) : bwd ? 4 : 8;
     p.wx_log = std::min(3, log2_up((int64_t(e.D) + 7) / 8));
     p.by_log = 3 - p.wx_log;
-    // Whole pieces of memory or copies of single values (5 x 2048, us): fp32, 777 channels, backward 60 / 91, forward
-    // 30 / 38; bf16, 777, backward 60 / 70, forward 21 / 35.  Pairs of bf16 values stay copies: 778, backward 58 / 40.
-    p.window = p.by_log == 0 && p.CB == es;
     p.tiles = int((int64_t(e.D) + (8 << p.wx_log) - 1) / (8 << p.wx_log));
     const int64_t blocks = int64_t(p.tiles) * ((int64_t(e.B) + (1 << p.by_log) - 1) >> p.by_log);
     const int64_t rounds = (int64_t(e.T) + SCAN_SEGS * p.L - 1) / (SCAN_SEGS * p.L);
@@ -1286,17 +1288,25 @@ ScanPlan scan_plan(const conv_scan_desc_t& e, const DevInfo& d, bool bwd, int ch
     // (The number of pieces, and so the workspace, does not go by where rows begin.)
     const int64_t most = std::min<int64_t>(int64_t(d.sms) * 2 / std::max<int64_t>(1, blocks), rounds / 2);
     const bool pieces = most > 8 && rounds >> 3 > 2 * ((rounds + most - 1) / most) + 8;
+    // Whole pieces of memory or copies of what rows begin at multiples of, in us: fp32 forward 2 x 16384 x 1023 107 / 136,
+    // 2 x 16384 x 1022 100 / 136, backward 5 x 2048 x 777 58 / 87, 2 x 16384 x 1022 293 / 326; bf16 forward 2 x 16384 x 1023 72 / 119,
+    // 2 x 16384 x 1022 64 / 75; not the bf16 backward, which has no registers for it (2 x 16384 x 1023 431 / 239, 1022
+    // 370 / 155), and not where time is cut into pieces of a few rounds (1 x 30001 x 333 fp32 79 / 67, but bf16 59 / 68).
+    p.window = p.by_log == 0 && p.CB < 16 && !(es == 2 && bwd) && (!pieces || p.CB == 2);
+    if (p.window && es == 4 && pairs) p.CB = 8;
     // Blocks along time: fewer rounds each, as far as the blocks fit the GPU.  A round takes 2.5 units with one block an SM,
     // 3.8 with two, 7.5 with three, a wave of blocks 5 us (the first 3) and with exchanges along a cluster 6 (bf16 backward, 1024
     // channels, clusters of 1, 2, 4, 8 blocks, us: 16 x 300 15 / 22 / 31 / 43, 16 x 2500 82 / 95 / 93 / 111, 8 x 1000 25 / 24 / 28 / 35,
     // 4 x 1000 23 / 17 / 15 / 18, 20 x 2500 132 / 122 / 117 / 137).
-    const double unit = p.CB == 16 ? 0.44 : p.window ? (es == 4 ? 0.72 : bwd ? 1.8 : 0.9) : 0.65;
+    const double unit = p.CB == 16 ? 0.44 : es == 4 ? 0.72 : p.CB == 4 ? 0.62 : bwd ? 1.8 : 0.9;
     const int fit = es == 2 || p.window ? 2 : 3;
     const double round_cost[] = {0, 2.5, 3.8, 7.5};
     const int64_t wave = int64_t(d.sms) * fit;
     int log_c = 0;
     double parts = 0;
-    for (int k = 0; k <= 3 && (k == 0 || (int64_t(1) << (k - 1)) < rounds); ++k) {
+    // (Where the backward takes whole pieces of memory, a cluster of 8 has no shared memory for a second block an SM.)
+    const int most_c = p.window && bwd ? 2 : 3;
+    for (int k = 0; k <= most_c && (k == 0 || (int64_t(1) << (k - 1)) < rounds); ++k) {
         const int64_t n = blocks << k, full = n / wave, rest = n % wave, each = (rounds + (int64_t(1) << k) - 1) >> k;
         const double one = double(full) * round_cost[fit] + round_cost[(rest + d.sms - 1) / d.sms];
         const double time = unit * one * double(each) + double(full + (rest > 0)) * (k == 0 ? 5 : 6) - 2;
@@ -1370,7 +1380,10 @@ cudaError_t scan_with(const ScanPlan& p, int dt, bool reset, F&& f, G&& g, H&& r
     auto parts = [&](auto t, auto r) {
         using L = Int<sizeof(t) == 2 ? (BWD ? 8 : 16) : BWD ? 4 : 8>;
         if (p.CB == 16) return f(t, L(), Int<16>(), std::false_type(), r);
-        if (p.window) return f(t, L(), Int<sizeof(t)>(), std::true_type(), r);
+        if constexpr (sizeof(t) == 4 || !BWD)
+            if (p.window)
+                return p.CB == sizeof(t) ? f(t, L(), Int<sizeof(t)>(), std::true_type(), r)
+                                         : f(t, L(), Int<2 * sizeof(t)>(), std::true_type(), r);
         if constexpr (sizeof(t) == 2)
             if (p.CB == 2) return f(t, L(), Int<2>(), std::false_type(), r);
         return f(t, L(), Int<4>(), std::false_type(), r);

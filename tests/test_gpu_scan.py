@@ -100,7 +100,7 @@ def test_against_the_reference(options, size, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("size", [(140, 150, 260), (250, 33, 75), (60, 700, 70), (30, 700, 70), (330, 65, 64), (3, 700, 1030)], ids=str)
+@pytest.mark.parametrize("size", [(140, 150, 260), (250, 33, 75), (60, 700, 70), (30, 700, 70), (330, 65, 64), (3, 700, 1030), (2, 900, 778), (1, 9000, 70)], ids=str)
 @pytest.mark.parametrize("options", ["plain", "everything"])
 def test_walks_from_shared_memory_and_clusters_of_each_size(options, size, dtype):
     both_ways(size, dtype, **OPTIONS[options])
