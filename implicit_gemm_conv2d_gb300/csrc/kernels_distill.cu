@@ -17,7 +17,8 @@
 // Floor: z once, and dz.  Measured, with the share of that floor at the measured copy's bandwidth: 1024 x 50021 fp32
 // backward 69.7 us (87 %), 8192 x 50021 bf16 both at once 299 (81 %), 24 x 131071 fp32 forward 5.9 (a launch and two
 // trips along a cluster).  Bound by memory, bf16 both at once also by instructions (0.62 issued a slot); rows of a few
-// hundred logits by the teacher's entries (32768 x 128 fp32 both at once 28.8 against 5.3).
+// hundred logits by the teacher's entries (32768 x 128 both at once, bf16 with 8 of them 27 against 2.8, fp32 with 100 of
+// them 59 against 8.9).
 #include <algorithm>
 
 #include "gn_common.cuh"
@@ -179,15 +180,6 @@ struct Teacher {
             total[k] -= log_sum;
         }
     }
-    // Asks for the entries' lines, which are read later.
-    __device__ __forceinline__ void announce(const DistillParams& a, int64_t n, int lane) const
-    {
-        const int64_t ids = a.K * (a.ids64 ? 8 : 4), qs = a.K * (a.teacher_bf16 ? 2 : 4);
-        for (int64_t k = lane * 128; k < ids + 128; k += 4096)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a.ids) + n * ids + min(k, ids - 1)));
-        for (int64_t k = lane * 128; k < qs + 128; k += 4096)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a.teacher) + n * qs + min(k, qs - 1)));
-    }
     // The student's logits of the entries in [lo, hi).
     template <typename T> __device__ __forceinline__ void gather(const DistillParams& a, const T* row, int lo, int hi, int lane)
     {
@@ -248,13 +240,21 @@ struct Teacher {
     }
 };
 
-// WARP: a warp a row; else a block of `warps` warps, DISTILL_WARPS at most and a power of two, and one for the teacher,
+// Blocks an SM for whose number of registers a kernel is compiled (0: the compiler's choice).
+constexpr int distill_blocks(int mode, int NV)
+{
+    return NV == 0 || NV == 2 ? 5 : mode == DISTILL_BWD ? 0 : mode == DISTILL_GRAD && NV == 8 ? 3 : 4;
+}
+
+// NV > 0: a warp a row, which it keeps in registers, NV vectors a lane (but for the gradient alone, which reads it
+// once anyway); else a block of `warps` warps, DISTILL_WARPS at most and a power of two, and one for the teacher,
 // `cluster` blocks a row.
-template <typename T, int MODE, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : DISTILL_WARPS * 32 + 32)
+template <typename T, int MODE, int NV>
+__global__ void __launch_bounds__(NV > 0 ? 256 : DISTILL_WARPS * 32 + 32, distill_blocks(MODE, NV))
 distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float* weight, float* zmax, float* zlog,
                float* loss, T* dz)
 {
+    constexpr bool WARP = NV > 0, HELD = WARP && MODE != DISTILL_BWD;
     extern __shared__ __align__(16) uint8_t sm[];
     __shared__ Stat parts[DISTILL_WARPS + 8];
     __shared__ int none;
@@ -279,9 +279,8 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
     int edge = me == 0 ? 0 : me == 1 && row.vecs > 1 ? row.vecs - 1 : -1;
     if (edge >= 0 && (edge < j0 || edge >= j1 || row.whole(edge))) edge = -1;
     Teacher t(sm + (WARP ? warp * Teacher::bytes(a.K, a.bits) : 0), a.K, a.bits);
-    uint8_t* const stage = sm + (WARP ? a.rows : 1) * Teacher::bytes(a.K, a.bits) +
-                           (WARP ? warp * a.stage_bytes : 0);  // vector j - j0 at the thread that reads it
-    const bool staged = MODE == DISTILL_GRAD && a.stage_bytes > 0;
+    uint8_t* const stage = sm + Teacher::bytes(a.K, a.bits);  // vector j - j0 at the thread that reads it
+    const bool staged = !WARP && MODE == DISTILL_GRAD && a.stage_bytes > 0;
     // A block's part of the row comes in a few large copies; `copy` vectors each.
     const int copy = (max(0, w1 - w0) + DISTILL_COPIES * step - 1) / (DISTILL_COPIES * step) * step;
     if (!WARP && staged) {
@@ -305,6 +304,17 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
         v.r.w[0] = uint32_t(q.x); v.r.w[1] = uint32_t(q.y); v.r.w[2] = uint32_t(q.z); v.r.w[3] = uint32_t(q.w);
     };
 
+    // A warp's row, all of it on its way beside the teacher's entries.
+    Vec<T, VE> held[HELD ? NV : 1], ends;
+    auto holds = [&](int u) { return lane + u * 32 >= w0 && lane + u * 32 < w1; };
+    if constexpr (HELD) {
+        const T* src = z + row.first + lane * VE;
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+            if (holds(u)) held[u].load(src + u * 32 * VE);
+        if (edge >= 0) ends = row.load(z, edge);
+    }
+
     // ---- the teacher's entries, and what the first sweep finds
     bool empty = false;
     const float w = MODE != DISTILL_FWD && weight ? weight[n] : 1.f;
@@ -326,26 +336,13 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
         }
         if (WARP) __syncwarp();
     } else {
-        auto teach = [&](bool here) {  // the row is in the stage
+        if (teaches) {
             empty = !t.entries(a, n, lane);
             if (!WARP && lane == 0) none = empty;
-            if (empty) return;
-            t.probabilities(a, lane);
-            if (here && staged) t.gather(a, reinterpret_cast<const T*>(stage) + row.off, 0, a.V, lane);
-            else t.gather(a, zrow, 0, a.V, lane);
-        };
-        // A warp that does both begins with the row where that is long (29605 x 1568 bf16 at once 59 / 52 us, 4344 x 197
-        // 7.5 / 9.6).
-        const bool row_first = WARP && row.vecs > 64;
-        Vec<T, VE> early[2];  // a short row's vectors, all on their way beside the teacher's entries
-        if (row_first) {
-            t.announce(a, n, lane);
-        } else {
-            if (WARP)
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    if (lane + u * 32 < row.vecs) early[u] = row.load(z, lane + u * 32);
-            if (teaches) teach(false);
+            if (!empty) {
+                t.probabilities(a, lane);
+                t.gather(a, zrow, 0, a.V, lane);
+            }
         }
         Stat st = {-INFINITY, 0.f};
         bool edged = false;  // the vector is one that no copy brought
@@ -355,7 +352,7 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
 #pragma unroll
             for (int u = 0; u < count; ++u) {
                 top = fmaxf(top, vec_max<T, VE>(v[u]));
-                if (staged && (WARP || edged)) v[u].store(reinterpret_cast<T*>(stage + (j + u * step - j0) * 16));
+                if (staged && edged) v[u].store(reinterpret_cast<T*>(stage + (j + u * step - j0) * 16));
             }
             const float base = finite_base(top);
             if (top > st.m) st.s *= fast_exp2((st.m - base) * a.k);
@@ -363,11 +360,16 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
 #pragma unroll
             for (int u = 0; u < count; ++u) st.s += vec_sum<T, VE>(v[u], base, a.k);
         };
-        if (WARP && !row_first) {
-            edged = true;
+        if constexpr (WARP) {
+            if (edge >= 0) st.m = vec_max<T, VE>(ends);
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-                if (lane + u * 32 < row.vecs) take(reinterpret_cast<Vec<T, VE>(&)[1]>(early[u]), lane + u * 32);
+            for (int u = 0; u < NV; ++u)
+                if (holds(u)) st.m = fmaxf(st.m, vec_max<T, VE>(held[u]));
+            const float base = finite_base(st.m);
+            if (edge >= 0) st.s = vec_sum<T, VE>(ends, base, a.k);
+#pragma unroll
+            for (int u = 0; u < NV; ++u)
+                if (holds(u)) st.s += vec_sum<T, VE>(held[u], base, a.k);
         } else if (sweeps) {
             Vec<T, VE> one[1];
             if (edge >= 0) {
@@ -389,7 +391,7 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
                     take(one, j);
                 }
             };
-            if (!WARP && staged) {
+            if (staged) {
                 for (int k = 0; k < DISTILL_COPIES && w0 + k * copy < w1; ++k) {
                     if (!tc::mbar_wait(tc::smem_u32(&bars[k]), 0u))
                         atomicOr(&g_distill_status, CONV_STATUS_DISTILL);  // the results are wrong, and the status says so
@@ -399,10 +401,6 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
                 const T* src = z + row.first;
                 all(w0, w1, [&](Vec<T, VE>& v, int j) { v.load(src + int64_t(j) * VE); });
             }
-        }
-        if (row_first) {
-            __syncwarp();
-            teach(true);
         }
         st = stat_join(st, 32, a.k);
         if (!WARP) {
@@ -450,8 +448,21 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
             v.set(f);
             if (zeros) v.zero();
         };
+        if constexpr (HELD) {
+            if (edge >= 0) {
+                give(ends);
+                row.store(dz, edge, ends);
+            }
+            T* dst = dz + row.first + lane * VE;
+#pragma unroll
+            for (int u = 0; u < NV; ++u)
+                if (holds(u)) {
+                    give(held[u]);
+                    held[u].store(dst + u * 32 * VE);
+                }
+        }
         Vec<T, VE> one;
-        if (edge >= 0) {
+        if (!HELD && edge >= 0) {
             if (staged) one.load(reinterpret_cast<const T*>(stage + (edge - j0) * 16));
             else one = row.load(z, edge);
             give(one);
@@ -478,7 +489,7 @@ distill_kernel(const __grid_constant__ DistillParams a, const T* z, const float*
         };
         if (staged) {
             sweep(waiting);
-        } else {
+        } else if (!HELD) {
             const T* src = z + row.first;
             sweep([&](Vec<T, VE>& v, int j) { v.load(src + int64_t(j) * VE); });
         }
@@ -523,8 +534,11 @@ DistillPlan distill_plan(const conv_distill_desc_t& e, const DevInfo& d, int mod
     p.warp = vecs <= 256 && e.K <= 256;
     if (p.warp) {
         p.bits = 2048;
-        p.stage_bytes = mode == DISTILL_GRAD ? int(vecs) * 16 : 0;
-        const int64_t one = 16 * int64_t(e.K) + p.bits / 4 + p.stage_bytes;
+        // The row in registers or read by four vectors a lane, and again for dz, us: bf16 29605 x 1568 forward 35 / 40, at
+        // once 51 / 57; 32768 x 128 at once 27 / 32; fp32 29639 x 618 forward 30.4 / 29.5, at once 43.8 / 44.7.  The gradient
+        // alone has it no faster: fp32 29639 x 618 36 / 34.
+        p.held = mode == DISTILL_BWD ? 4 : vecs <= 64 ? 2 : vecs <= 128 ? 4 : 8;
+        const int64_t one = 16 * int64_t(e.K) + p.bits / 4;
         p.rows = int(std::max<int64_t>(1, std::min<int64_t>(8, 48 * 1024 / one)));
         p.cluster = 1;
         p.threads = p.rows * 32;
@@ -571,12 +585,17 @@ cudaError_t launch_distill(const DistillPlan& p, DistillParams a, const void* z,
                          static_cast<const T*>(z), weight, zmax, zlog, loss, static_cast<T*>(dz));
     };
     const int room = p.smem + 1024;  // (the static part comes on top of the dynamic one)
-    if (p.warp) {
-        const cudaError_t e = ensure_smem<distill_kernel<T, MODE, true>>(room);
-        return e != cudaSuccess ? e : go(distill_kernel<T, MODE, true>);
+    auto with = [&](auto held) {
+        constexpr auto kern = distill_kernel<T, MODE, decltype(held)::value>;
+        const cudaError_t e = ensure_smem<kern>(room);
+        return e != cudaSuccess ? e : go(kern);
+    };
+    if (!p.warp) return with(std::integral_constant<int, 0>());
+    if constexpr (MODE != DISTILL_BWD) {
+        if (p.held == 2) return with(std::integral_constant<int, 2>());
+        if (p.held == 8) return with(std::integral_constant<int, 8>());
     }
-    const cudaError_t e = ensure_smem<distill_kernel<T, MODE, false>>(room);
-    return e != cudaSuccess ? e : go(distill_kernel<T, MODE, false>);
+    return with(std::integral_constant<int, 4>());
 }
 
 template <int MODE>

@@ -153,7 +153,8 @@ struct DistillParams {
 struct DistillPlan {
     bool warp;                   // a warp a row
     int cluster, rows, warps;    // blocks a row, rows a block, a block's warps that sweep
-    int bits, stage_bytes;       // of an id bitmap; of a block's (a warp's) part of a row in shared memory
+    int held;                    // vectors of its row a lane keeps, where a warp has one
+    int bits, stage_bytes;       // of an id bitmap; of a block's part of a row in shared memory
     int threads, smem;
     int64_t blocks;
 };
