@@ -1,7 +1,9 @@
 // internal.h -- host-side plan and launcher interface between api.cu (the C
 // ABI: validation, dispatch) and the kernel translation units.
 #pragma once
+#include <atomic>
 #include <cstddef>
+#include <mutex>
 #include <utility>
 #include <cuda_runtime.h>
 
@@ -73,19 +75,29 @@ cudaError_t run_wgrad_reduce(const ConvParams&, int dt, const float* ws, int spl
                              int nbp = 0, void* db = nullptr);
 cudaError_t run_l2_flush(void* buf, size_t bytes, cudaStream_t s);
 
-// Dynamic shared memory above 48 KB needs a per-kernel opt-in on every device;
-// done once per (kernel, device) and remembered.
+// Dynamic shared memory above 48 KB needs a per-kernel opt-in on every device, which replaces the
+// one before it: done for the largest size asked for so far, by one host thread at a time, so that no
+// thread's smaller size takes away what another one's launch has been granted.
 template <auto Kern>
 cudaError_t ensure_smem(int bytes)
 {
     if (bytes <= 48 * 1024) return cudaSuccess;
-    static int configured[64] = {0};
+    constexpr int DEVICES = 64;
+    static std::atomic<int> granted[DEVICES + 1];  // the last: of any further device, opted in to again each time
+    static std::mutex opting_in;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64 && configured[dev] >= bytes) return cudaSuccess;
-    e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && dev >= 0 && dev < 64) configured[dev] = bytes;
+    const bool known = dev >= 0 && dev < DEVICES;
+    std::atomic<int>& most = granted[known ? dev : DEVICES];
+    if (known && most.load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+    const std::lock_guard<std::mutex> lock(opting_in);
+    if (most.load(std::memory_order_relaxed) < bytes) {
+        e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) most.store(bytes, std::memory_order_release);
+    } else if (!known) {
+        e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most.load(std::memory_order_relaxed));
+    }
     return e;
 }
 
