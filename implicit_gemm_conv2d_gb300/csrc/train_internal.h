@@ -155,6 +155,7 @@ struct DistillPlan {
     int cluster, rows, warps;    // blocks a row, rows a block, a block's warps that sweep
     int held;                    // vectors of its row a lane keeps, where a warp has one
     int bits, stage_bytes;       // of an id bitmap; of a block's part of a row in shared memory
+    bool chains;                 // a thread's sums are added in several chains
     int threads, smem;
     int64_t blocks;
 };
