@@ -284,8 +284,35 @@ ln_fwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* residual,
     }
 }
 
+// A thread's sums over the vectors of a row that no team holds: f(j, part) adds vector j's.  An addition may be off by
+// half a step, each the same way, so a chain has 256 vectors at most; CHAINS: where a thread has more, its chains
+// are added to each other in 64 bits.  (A row of 2^29 - 1 values alike was one of 524288, off by 0.4 %.  In one
+// kernel for both the registers of the longer form cost rows of any length: 2000 x 40000 bf16 forward 114 us, 160 so.)
+constexpr int LN_CHAIN = 256;
+template <bool CHAINS, int K, class F>
+__device__ __forceinline__ void ln_long_sums(const LnAt& q, int vecs, float (&sum)[K], F&& f)
+{
+#pragma unroll
+    for (int k = 0; k < K; ++k) sum[k] = 0.f;
+    if constexpr (!CHAINS) {
+        for (int j = q.lane; j < vecs; j += q.TL) f(j, sum);
+    } else {
+        double all[K] = {};
+        const int chain = LN_CHAIN * q.TL;
+        for (int from = q.lane; from < vecs; from += chain) {
+            float part[K] = {};
+            const int to = min(vecs, from + chain);
+            for (int j = from; j < to; j += q.TL) f(j, part);
+#pragma unroll
+            for (int k = 0; k < K; ++k) all[k] += double(part[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) sum[k] = float(all[k]);
+    }
+}
+
 // A block a row, of any length: the row is read again for each pass.
-template <typename T, int V>
+template <typename T, int V, bool CHAINS>
 __global__ void __launch_bounds__(LN_LONG)
 ln_fwd_long(const __grid_constant__ LnParams p, const T* x, const T* residual, const T* gamma, const T* beta, T* y,
             T* total, float* mean, float* rstd)
@@ -297,8 +324,8 @@ ln_fwd_long(const __grid_constant__ LnParams p, const T* x, const T* residual, c
     for (int64_t row = blockIdx.x; row < p.N; row += gridDim.x) {
         const int64_t at = row * p.D;
         const T* s = residual ? total : x;
-        float sum[1] = {0.f};
-        for (int j = q.lane; j < p.vecs; j += q.TL) {
+        float sum[1];
+        ln_long_sums<CHAINS>(q, p.vecs, sum, [&](int j, float (&part)[1]) {
             Vec<T, V> a;
             a.load(x + at + int64_t(j) * V);
             float f[V], t = 0.f;
@@ -312,22 +339,22 @@ ln_fwd_long(const __grid_constant__ LnParams p, const T* x, const T* residual, c
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) t += a.get(v);
-            sum[0] += t;
-        }
+            part[0] += t;
+        });
         float m = 0.f;
         if (!p.rms) {
             ln_sum(q, sum, sm[0]);
             m = sum[0] * p.inv_d;
         }
-        float sq[1] = {0.f};
-        for (int j = q.lane; j < p.vecs; j += q.TL) {
+        float sq[1];
+        ln_long_sums<CHAINS>(q, p.vecs, sq, [&](int j, float (&part)[1]) {
             Vec<T, V> a;
             a.load(s + at + int64_t(j) * V);
             float t = 0.f;
 #pragma unroll
             for (int v = 0; v < V; ++v) t += (a.get(v) - m) * (a.get(v) - m);
-            sq[0] += t;
-        }
+            part[0] += t;
+        });
         if (p.rms) __syncthreads();
         ln_sum(q, sq, sm[1]);
         const float r = __frsqrt_rn(sq[0] * p.inv_d + p.eps);
@@ -552,7 +579,7 @@ ln_bwd_kernel(const __grid_constant__ LnParams p, const T* x, const T* dy, const
 }
 
 // ---- rows that no team holds: the rows' sums, then columns of all rows -------------------------
-template <typename T, int V>
+template <typename T, int V, bool CHAINS>
 __global__ void __launch_bounds__(LN_LONG)
 ln_bwd_rows(const __grid_constant__ LnParams p, const T* x, const T* dy, const T* gamma, const float* mean,
             const float* rstd, float2* sums)
@@ -564,8 +591,8 @@ ln_bwd_rows(const __grid_constant__ LnParams p, const T* x, const T* dy, const T
     int turn = 0;
     for (int64_t row = blockIdx.x; row < p.N; row += gridDim.x, turn ^= 1) {
         const float m = mean ? mean[row] : 0.f, r = rstd[row];
-        float s[2] = {0.f, 0.f};
-        for (int j = q.lane; j < p.vecs; j += q.TL) {
+        float s[2];
+        ln_long_sums<CHAINS>(q, p.vecs, s, [&](int j, float (&part)[2]) {
             const int64_t at = row * p.D + int64_t(j) * V;
             Vec<T, V> a, d, g;
             a.load(x + at);
@@ -578,9 +605,9 @@ ln_bwd_rows(const __grid_constant__ LnParams p, const T* x, const T* dy, const T
                 s1 += e;
                 s2 += e * ((a.get(v) - m) * r);
             }
-            s[0] += s1;
-            s[1] += s2;
-        }
+            part[0] += s1;
+            part[1] += s2;
+        });
         ln_sum(q, s, sm[turn]);
         if (threadIdx.x == 0) sums[row] = make_float2(p.rms ? 0.f : s[0] * p.inv_d, s[1] * p.inv_d);
     }
@@ -671,7 +698,12 @@ template <class F> cudaError_t ln_edge(const LnParams& p, int dt, F&& f)
     if (dt == DT_F32) return p.edge ? f(float(), std::true_type()) : f(float(), std::false_type());
     return p.edge ? f(__nv_bfloat16(), std::true_type()) : f(__nv_bfloat16(), std::false_type());
 }
-// Calls f(T(), V) for one without.
+// Calls f(CHAINS) for a plan without.
+template <class F> cudaError_t ln_chains(const LnParams& p, F&& f)
+{
+    return p.vecs > LN_CHAIN * LN_LONG ? f(std::true_type()) : f(std::false_type());
+}
+// Calls f(T(), V) for such a plan.
 template <class F> cudaError_t ln_long(const LnParams& p, int dt, F&& f)
 {
     if (dt == DT_F32) return p.V == 4 ? f(float(), Int<4>()) : p.V == 2 ? f(float(), Int<2>()) : f(float(), Int<1>());
@@ -769,7 +801,11 @@ cudaError_t run_ln_fwd(const conv_ln_desc_t& e, const DevInfo& d, const void* x,
                          static_cast<T*>(y), static_cast<T*>(total), mean, rstd);
     };
     if (p.NV == 0)
-        return ln_long(p, e.dtype, [&](auto t, auto v) { return go(ln_fwd_long<decltype(t), decltype(v)::value>, t); });
+        return ln_long(p, e.dtype, [&](auto t, auto v) {
+            return ln_chains(p, [&](auto chains) {
+                return go(ln_fwd_long<decltype(t), decltype(v)::value, decltype(chains)::value>, t);
+            });
+        });
     return ln_edge(p, e.dtype, [&](auto t, auto edge) {
         using T = decltype(t);
         constexpr bool EDGE = decltype(edge)::value;
@@ -824,8 +860,10 @@ cudaError_t run_ln_bwd(const conv_ln_desc_t& e, const DevInfo& d, const void* x,
             using T = decltype(t);
             constexpr int V = decltype(v)::value;
             const T *px = static_cast<const T*>(x), *pdy = static_cast<const T*>(dy), *pg = static_cast<const T*>(gamma);
-            const cudaError_t bad = launch_ex(ln_bwd_rows<T, V>, dim3(p.blocks), dim3(p.TL), 0, s, 1, true, p, px, pdy, pg,
-                                              mean, rstd, sums);
+            const cudaError_t bad = ln_chains(p, [&](auto chains) {
+                return launch_ex(ln_bwd_rows<T, V, decltype(chains)::value>, dim3(p.blocks), dim3(p.TL), 0, s, 1, true, p, px,
+                                 pdy, pg, mean, rstd, sums);
+            });
             if (bad != cudaSuccess) return bad;
             return launch_ex(ln_bwd_columns<T, V>, grid, dim3(LN_COLUMNS), 0, s, 1, true, p, px, pdy, pg, mean, rstd,
                              static_cast<const T*>(dtotal), static_cast<const float2*>(sums), static_cast<T*>(dx),

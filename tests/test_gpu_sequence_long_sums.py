@@ -7,7 +7,7 @@ import torch
 
 from implicit_gemm_conv2d_gb300 import train
 
-from . import seq_ref, test_gpu_distill
+from . import seq_ref, test_gpu_distill, test_gpu_ln
 
 pytestmark = pytest.mark.gpu
 U = seq_ref.U
@@ -49,3 +49,33 @@ def test_loss_where_chains_begin(size, dtype):
     """Rows a little longer than one chain a thread."""
     z, ids, q, w = test_gpu_distill.inputs(size, dtype, 23)
     test_gpu_distill.all_ways(z, ids, q, w, 1.0, dtype, f"{size} {dtype}")
+
+
+@pytest.mark.parametrize("dtype,D", [(torch.float32, 2 ** 29 - 1), (torch.float32, 2 ** 29 - 4), (torch.bfloat16, 2 ** 30 - 8),
+                                     (torch.bfloat16, 2 ** 29 - 1), (torch.bfloat16, 2 ** 29 - 2)], ids=str)
+def test_norm_of_values_alike(dtype, D):
+    """A mean, a mean square, and the backward's two sums over one row.  A vector has up to 8 values, a chain 256
+    vectors, the tree over a block's threads 12 steps."""
+    sum_room = (8 + 256 + 12) * U
+    x = torch.full((1, D), 0.1, dtype=dtype, device="cuda")
+    value = float(x[0, 0])
+    _, _, mean, _ = train.layer_norm(x)
+    assert abs(float(mean) / value - 1) <= sum_room + 2 * U          # the division's two roundings
+    _, _, _, rstd = train.layer_norm(x, eps=0.0, rms=True)
+    assert abs(float(rstd) * value - 1) <= (sum_room + 3 * U) / 2 + 2 * U
+    dy = torch.full_like(x, 0.7)
+    e = float(dy[0, 0])
+    r = torch.full((1,), 1.0 / value, device="cuda")
+    # dx / (r e) = 1 - (mean of e) / e, and without a mean 1 - xhat (mean of e xhat) / e, xhat = 1: both 0
+    dx, _, _ = train.layer_norm_bwd(x, dy, None, r * 0 + value, r, param_grads=False)
+    assert float(dx.abs().max()) <= float(r) * e * (sum_room + 4 * U)
+    dx, _, _ = train.layer_norm_bwd(x, dy, None, None, r, param_grads=False)
+    assert float(dx.abs().max()) <= float(r) * e * (sum_room + 12 * U)
+
+
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("size,dtype", [((2, 270_001), "f32"), ((1, 530_002), "f32"), ((1, 1_050_000), "f32"),
+                                        ((2, 270_001), "bf16"), ((1, 530_002), "bf16"), ((1, 2_100_000), "bf16")], ids=str)
+def test_norm_where_chains_begin(size, dtype, rms):
+    """Rows a little longer than one chain a thread, by one, two and four or eight values a vector."""
+    test_gpu_ln.both_ways(size, dtype, rms)
