@@ -357,6 +357,13 @@ def _logits_ptr(t):
     return _ptr(t[:1])
 
 
+def _same_layout(desc: DistillDesc, dz) -> None:
+    """dz is laid out as the descriptor's logits: its rows are written at their distances, which for a contiguous dz
+    beside a view of wider rows would end behind it."""
+    if dz.dim() != 2 or tuple(dz.shape) != (desc.N, desc.V) or (desc.N > 1 and dz.stride(0) != desc.ld):
+        raise ValueError("dz: z's sizes and distances")
+
+
 def make_distill_desc(z, ids, teacher, temperature=1.0) -> DistillDesc:
     return DistillDesc(z.shape[0], z.stride(0) if z.shape[0] > 1 else z.shape[1], z.shape[1], ids.shape[1], _DT[z.dtype],
                        _IDX[ids.dtype], _DT[teacher.dtype], temperature)
@@ -368,13 +375,15 @@ def conv_distill_fwd(desc: DistillDesc, z, ids, teacher, loss, zmax, zlog, strea
 
 
 def conv_distill_bwd(desc: DistillDesc, z, ids, teacher, zmax, zlog, weight, scale, dz, stream=None) -> None:
-    """weight may be None; dz has z's distances and may be z."""
+    """weight may be None; dz has z's sizes and distances (ValueError otherwise) and may be z."""
+    _same_layout(desc, dz)
     _check(lib().conv_distill_bwd(_ref(desc), _logits_ptr(z), _ptr(ids), _ptr(teacher), _ptr(zmax), _ptr(zlog),
                                   _ptr(weight), scale, _logits_ptr(dz), _stream(stream)), "conv_distill_bwd")
 
 
 def conv_distill_grad(desc: DistillDesc, z, ids, teacher, weight, scale, loss, dz, stream=None) -> None:
-    """weight may be None; dz has z's distances and may be z."""
+    """weight may be None; dz has z's sizes and distances (ValueError otherwise) and may be z."""
+    _same_layout(desc, dz)
     _check(lib().conv_distill_grad(_ref(desc), _logits_ptr(z), _ptr(ids), _ptr(teacher), _ptr(weight), scale, _ptr(loss),
                                    _logits_ptr(dz), _stream(stream)), "conv_distill_grad")
 
