@@ -814,7 +814,9 @@ cudaError_t run_ln_fwd(const conv_ln_desc_t& e, const DevInfo& d, const void* x,
             const cudaError_t bad = ensure_smem<kern>(smem > 0 ? smem + 1024 : 0);  // (and the static part)
             return bad != cudaSuccess ? bad : go(kern, t);
         };
-        return p.NV == 1 ? team(Int<1>()) : p.NV == 2 ? team(Int<2>()) : p.NV == 4 ? team(Int<4>()) : team(Int<8>());
+        if constexpr (!EDGE)  // (rows that begin anywhere have two vectors at least)
+            if (p.NV == 1) return team(Int<1>());
+        return p.NV == 2 ? team(Int<2>()) : p.NV == 4 ? team(Int<4>()) : team(Int<8>());
     });
 }
 
@@ -849,7 +851,9 @@ cudaError_t run_ln_bwd(const conv_ln_desc_t& e, const DevInfo& d, const void* x,
             };
             if constexpr (sizeof(T) == 4)
                 if (p.NV == 4) return go(Int<4>());
-            return p.NV == 1 ? go(Int<1>()) : go(Int<2>());
+            if constexpr (sizeof(T) == 2 || !decltype(edge)::value)  // (as in the forward)
+                if (p.NV == 1) return go(Int<1>());
+            return go(Int<2>());
         });
     } else if (e.N > 0) {
         float2* sums = static_cast<float2*>(ws);

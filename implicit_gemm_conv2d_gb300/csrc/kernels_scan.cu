@@ -1406,6 +1406,9 @@ cudaError_t scan_with(const ScanPlan& p, int dt, bool reset, F&& f, G&& g, H&& r
     return dt == DT_F32 ? on_reset(float()) : on_reset(__nv_bfloat16());
 }
 
+// Time may be cut into pieces (scan_plan: with whole pieces of memory for single bf16 values alone).
+constexpr bool scan_cuts(bool window, int CB) { return !window || CB == 2; }
+
 template <typename T, int L, int CB, bool RESET, int DIR>
 cudaError_t launch_totals(const ScanPlan& p, const T* x, const T* gate, const T* dh, const float* state,
                           const uint8_t* reset, const int32_t* lengths, float2* pieces, cudaStream_t s)
@@ -1441,13 +1444,14 @@ cudaError_t run_scan_fwd(const conv_scan_desc_t& e, const DevInfo& d, const void
         [&](auto t, auto l, auto cb, auto window, auto r) {
             using T = decltype(t);
             constexpr int L = decltype(l)::value, CB = decltype(cb)::value;
-            constexpr bool RESET = decltype(r)::value;
+            constexpr bool WINDOW = decltype(window)::value, RESET = decltype(r)::value;
             const T *px = static_cast<const T*>(x), *pg = static_cast<const T*>(gate);
-            if (p.pieces > 1) {
-                const cudaError_t err = launch_totals<T, L, CB, RESET, 1>(p, px, pg, nullptr, h0, reset, lengths, pieces, s);
+            if constexpr (scan_cuts(WINDOW, CB)) {
+                cudaError_t err = cudaSuccess;
+                if (p.pieces > 1) err = launch_totals<T, L, CB, RESET, 1>(p, px, pg, nullptr, h0, reset, lengths, pieces, s);
                 if (err != cudaSuccess) return err;
             }
-            constexpr auto kern = scan_part_fwd<T, L, CB, decltype(window)::value, RESET>;
+            constexpr auto kern = scan_part_fwd<T, L, CB, WINDOW, RESET>;
             const cudaError_t err = ensure_smem<kern>(smem);
             if (err != cudaSuccess) return err;
             return launch_ex(kern, grid, block, smem, s, p.cluster, true, p, px, pg, h0, reset, lengths,
@@ -1485,13 +1489,14 @@ cudaError_t run_scan_bwd(const conv_scan_desc_t& e, const DevInfo& d, const void
         [&](auto t, auto l, auto cb, auto window, auto r) {
             using T = decltype(t);
             constexpr int L = decltype(l)::value, CB = decltype(cb)::value;
-            constexpr bool RESET = decltype(r)::value;
+            constexpr bool WINDOW = decltype(window)::value, RESET = decltype(r)::value;
             const T *pg = static_cast<const T*>(gate), *pd = static_cast<const T*>(dh);
-            if (p.pieces > 1) {
-                const cudaError_t err = launch_totals<T, L, CB, RESET, -1>(p, nullptr, pg, pd, dlast, reset, lengths, pieces, s);
+            if constexpr (scan_cuts(WINDOW, CB)) {
+                cudaError_t err = cudaSuccess;
+                if (p.pieces > 1) err = launch_totals<T, L, CB, RESET, -1>(p, nullptr, pg, pd, dlast, reset, lengths, pieces, s);
                 if (err != cudaSuccess) return err;
             }
-            constexpr auto kern = scan_part_bwd<T, L, CB, decltype(window)::value, RESET>;
+            constexpr auto kern = scan_part_bwd<T, L, CB, WINDOW, RESET>;
             const cudaError_t err = ensure_smem<kern>(smem);
             if (err != cudaSuccess) return err;
             return launch_ex(kern, grid, block, smem, s, p.cluster, true, p, static_cast<const T*>(x), pg,
