@@ -111,9 +111,13 @@ int conv_embed_bwd(const conv_embed_desc_t* desc, const void* idx, const void* d
  * dx is the gradient of x and of residual; dtotal is the gradient that reaches total by another way (a
  * residual stream goes on beside its norm), or NULL (0).  rms: the form without a mean: mean, m1
  * and beta are 0, and mean, beta and dbeta NULL.
- * All arrays dense, (N, D) or (D), of the descriptor's dtype; mean and rstd fp32, (N).  A row with an
- * infinity or NaN is NaN, and so are dgamma and dbeta with it; the other rows are not.
- * Squares are fp32: deviations from 1.8e19 on make rstd 0. */
+ * All arrays dense, (N, D) or (D), of the descriptor's dtype; mean and rstd fp32, (N).
+ * What is not finite stays in its row, but for the parameters' gradients.  A row of total with a NaN in it, or with
+ * a mean an infinity, has NaN for rstd and for all of y and dx, and makes all of dgamma NaN (not dbeta).  Without
+ * a mean, a row with an infinity has rstd 0, y NaN there and 0 elsewhere, and dx NaN; dgamma is NaN in that
+ * column alone.  A NaN in dy makes its row of dx, and its column of dgamma and dbeta, NaN.
+ * Sums and squares are fp32: deviations from 1.8e19 on make rstd 0, a sum of the row's values from 3.4e38 on makes the
+ * row NaN, and a row whose values differ by less than some 2^-22 of their mean is normed to the mean's own rounding. */
 typedef struct {
     int64_t N;              /* rows, >= 0                                                 */
     int32_t D;              /* values a row, >= 1                                         */
