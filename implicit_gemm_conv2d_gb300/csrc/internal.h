@@ -82,22 +82,18 @@ template <auto Kern>
 cudaError_t ensure_smem(int bytes)
 {
     if (bytes <= 48 * 1024) return cudaSuccess;
-    constexpr int DEVICES = 64;
-    static std::atomic<int> granted[DEVICES + 1];  // the last: of any further device, opted in to again each time
+    constexpr int DEVICES = 64;  // as many as device_info knows
+    static std::atomic<int> granted[DEVICES];
     static std::mutex opting_in;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const bool known = dev >= 0 && dev < DEVICES;
-    std::atomic<int>& most = granted[known ? dev : DEVICES];
-    if (known && most.load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+    if (dev < 0 || dev >= DEVICES) return cudaErrorInvalidDevice;
+    if (granted[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
     const std::lock_guard<std::mutex> lock(opting_in);
-    if (most.load(std::memory_order_relaxed) < bytes) {
-        e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e == cudaSuccess) most.store(bytes, std::memory_order_release);
-    } else if (!known) {
-        e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most.load(std::memory_order_relaxed));
-    }
+    if (granted[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) granted[dev].store(bytes, std::memory_order_release);
     return e;
 }
 
