@@ -15,8 +15,8 @@
 // one thread an id: no atomic adds, and a fixed order for an id that occurs twice.
 //
 // Floor: z once, and dz.  Measured, with the share of that floor at the measured copy's bandwidth: 1024 x 50021 fp32
-// backward 69.7 us (87 %), 8192 x 50021 bf16 both at once 299 (81 %), 24 x 131071 fp32 forward 5.9 (a launch and two
-// trips along a cluster).  Bound by memory, bf16 both at once also by instructions (0.62 issued a slot); rows of a few
+// backward 69 us (87 %), 8192 x 50021 bf16 both at once 299 (81 %) and forward 131 (93 %), 24 x 131071 fp32 forward 6.0 (a launch
+// and two trips along a cluster).  Bound by memory, bf16 both at once also by instructions (0.62 issued a slot); rows of a few
 // hundred logits by the teacher's entries (32768 x 128 both at once, bf16 with 8 of them 27 against 2.8, fp32 with 100 of
 // them 59 against 8.9).
 #include <algorithm>
@@ -36,7 +36,8 @@ constexpr int DISTILL_COPIES = 4;      // of a block's part of a row, one behind
 // Vectors whose sums a thread adds to one another in one chain at most, where each addition may be off by half a step
 // the same way.  CHAINS: a thread has more of them, and its chains (512 at most) are added to each other.  (In one
 // kernel for both, the registers of the longer form cost rows of any length: 8192 x 50021 bf16 forward 131 us, 138 so.
-// Rows of 10 million logits pay 4 %.  A row of 2^30 - 1 with 65536 vectors in one chain was off by up to 1e-3.)
+// Rows of 10 million logits pay 4 %.  log sum exp over 2^30 - 1 logits, in one chain a thread, was off by 9e-4 in bf16 and
+// 1.5e-3 in fp32.)
 constexpr int DISTILL_CHAIN = 256;
 
 __device__ unsigned g_distill_status = 0;  // CONV_STATUS_DISTILL: a bounded wait ran out

@@ -12,11 +12,14 @@
 // alike: a team's rows are a multiple of VE apart, so that it reads them all by the same whole vectors of memory
 // and a thread's columns stay its own.  The first and the last vector hold values of the rows beside it,
 // which are cut off as they come in and never written.
-// Rows that no team holds are read again for each pass.
+// Rows that no team holds are read again for each pass.  Forward rows that take eight vectors a thread (above
+// 8192 fp32 or 16384 bf16 values) are held in part by local memory: 64 registers spill 280 to 810 bytes a thread.
 //
 // Measured, with the share of the floor (each array once) at the measured copy's bandwidth: 32768 x 1024 bf16
 // forward 46.6 us (85 %), backward 48.3 (82 %, of it 7 the columns' sums), 6001 x 1430 fp32 backward without a mean
-// 25.0 (61 %: a third of it are the sums, and three waves of rows), 2000 x 16384 bf16 backward 94 (42 %: read twice).
+// 25.0 (61 %: 304 blocks of one team of 192 threads, 12 warps an SM at 0.57 issued a slot, then the columns' sums), 2000 x 16384
+// bf16 backward 93 (42 %: read twice), 2000 x 12288 fp32 forward 109 (53 %) and 2000 x 24576 bf16 143 (40 %: both spill), 2000 x
+// 40000 bf16 114 (83 %: read three times, mostly from L2).
 #include <algorithm>
 
 #include "gn_common.cuh"

@@ -17,7 +17,8 @@
 // the places of the inputs.
 //
 // State, A and H are fp32, and so is 1 - z, taken from z: where z is small, a long memory, z's error is
-// small beside the rounding of 1 - z, which is that of one more operation a step.
+// small beside the rounding of 1 - z, which is that of one more operation a step.  Where z is near 1, what is left of
+// the state is off by up to 2^-23 of the state, as in h + z (x - h) itself.
 // What enters a stretch with a reset in it, be it NaN, is left out and not multiplied by 0: a warp votes on its
 // stretches' resets; where a stretch travels further, A = -1 says it.
 //
@@ -1295,7 +1296,9 @@ ScanPlan scan_plan(const conv_scan_desc_t& e, const DevInfo& d, bool bwd, int ch
     p.window = p.by_log == 0 && p.CB < 16 && !(es == 2 && bwd) && (!pieces || p.CB == 2);
     if (p.window && es == 4 && pairs) p.CB = 8;
     // Blocks along time: fewer rounds each, as far as the blocks fit the GPU.  A round takes 2.5 units with one block an SM,
-    // 3.8 with two, 7.5 with three, a wave of blocks 5 us (the first 3) and with exchanges along a cluster 6 (bf16 backward, 1024
+    // 3.8 with two, 7.5 with three, a wave of blocks 5 us (the first 3) and with exchanges along a cluster 6.  The estimate
+    // counts three fp32 blocks an SM where copies are of 16 or 4 bytes, for which the kernels are compiled (80 registers);
+    // shared memory holds three only with two stages, one or two rounds a block, and with three stages two.  (bf16 backward, 1024
     // channels, clusters of 1, 2, 4, 8 blocks, us: 16 x 300 15 / 22 / 31 / 43, 16 x 2500 82 / 95 / 93 / 111, 8 x 1000 25 / 24 / 28 / 35,
     // 4 x 1000 23 / 17 / 15 / 18, 20 x 2500 132 / 122 / 117 / 137).
     const double unit = p.CB == 16 ? 0.44 : es == 4 ? 0.72 : p.CB == 4 ? 0.62 : bwd ? 1.8 : 0.9;

@@ -393,7 +393,8 @@ def distill(z, ids, teacher, temperature: float = 1.0, stream=None):
     Kullback-Leibler divergence of the teacher's distribution over the K entries from the softmax of z,
     both at the temperature, times its square.  Entries outside [0, V) or of -inf count for nothing; a
     row without others has loss 0.  One entry a row at temperature 1 is the cross entropy.  zmax and
-    zlog are what distill_bwd takes.  z's rows may be any distance apart."""
+    zlog are what distill_bwd takes.  z's rows may be any distance apart; every tensor begins at a multiple
+    of 16 bytes, which a slice from some row or entry on may not (ConvError)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return distill(z, ids, teacher, temperature)

@@ -162,9 +162,11 @@ int conv_ln_bwd(const conv_ln_desc_t* desc, const void* x, const void* dy, const
  * (dh0 = 0 where step 0 is a reset; dh0 = dlast for a row without steps.)  dx and dgate are 0 behind
  * a row's length.  h is the forward's output as it is kept: rounded, where it is bf16.
  *
- * The states, and every product along the time axis, are fp32.  Time is cut into parts that are
- * joined in an order that the sizes fix.  A state that is infinite or NaN makes what follows it in
- * its row and channel, up to the next reset, infinite or NaN.
+ * The states, and every product along the time axis, are fp32; 1 - z is taken from z, so what an open gate
+ * (above 16 or so) leaves of the state may be 0 instead of less than 2^-23 of it.  Time is cut into parts that
+ * are joined in an order that the sizes, and what the addresses and distances are multiples of (2 to 16 bytes), fix:
+ * a call gives the same bits each time, another layout of the same values may give others.  A state that
+ * is infinite or NaN makes what follows it in its row and channel, up to the next reset, infinite or NaN.
  *
  * x, gate, h, dh, dx and dgate have the descriptor's dtype and lie anywhere: an array's element
  * (b, t, d) is batch * b + step * t + d elements behind its address, which is a multiple of the
@@ -210,7 +212,8 @@ int conv_scan_bwd(const conv_scan_desc_t* desc, const void* x, const void* gate,
  * z, dz: (N, V), a row's logits one behind the other, rows ld elements apart (ld >= V; dz is
  * written at the row's V elements only), of the descriptor's dtype.  ids, teacher: (N, K) dense,
  * teacher of teacher_dtype.  loss, zmax, zlog, weight: fp32, (N).  zmax[n] is the largest z of the
- * row, zlog[n] = log sum_v exp((z[v] - zmax[n]) / tau): what the backward takes. */
+ * row, zlog[n] = log sum_v exp((z[v] - zmax[n]) / tau): what the backward takes.  Rows begin anywhere, but
+ * every array, as everywhere but in the scan, begins at a multiple of 16 bytes (CONV_ERR_ALIGN). */
 typedef struct {
     int64_t N;              /* rows, >= 0                                                  */
     int64_t ld;             /* elements from one row of z (and dz) to the next             */
